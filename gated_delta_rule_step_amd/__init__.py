@@ -48,6 +48,11 @@ _SIGS = {
                                               _P, _P, _F, _F, _I32, _I32, _P, _I64, _I64, _P,
                                               _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P,
                                               _I32, _P, _I32, _P]),
+    "kda_rmsnorm": (_c.c_int, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _F,
+                               _I32, _P, _I64, _I32, _P, _I64, _P]),
+    "kda_rmsnorm_backward_workspace_size": (_c.c_size_t, [_I64, _I32, _I32]),
+    "kda_rmsnorm_backward": (_c.c_int, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                        _P, _F, _P, _I64, _P, _I64, _P, _P, _c.c_size_t, _P]),
 }
 
 # Scratch held by the library per device for kda_prefill_varlen_noalloc
@@ -352,3 +357,130 @@ def prefill_handoff_hist(cu_seqlens_host, ring_tail: int):
     last = lens - 16 * torch.div(lens - 1, 16, rounding_mode="floor")
     return torch.where(lens > 0, torch.clamp(last, max=int(ring_tail)),
                        torch.zeros_like(lens)).to(torch.int32)
+
+
+def _same_device(first, named):
+    """Every given tensor is on the first one's GPU; returns that device."""
+    dev = first.device
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return dev
+
+
+def _launch(fn, dev, stream, *args):
+    """Call a C entry point with `dev` current, on the given stream or on that
+    device's current one (appended as the last argument)."""
+    import torch
+    if stream is not None and getattr(stream, "device", dev) != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    with torch.cuda.device(dev):
+        st = getattr(lib(), fn)(*args, _stream(stream))
+    _check(fn, st)
+
+
+def _vectors(name, t, rows, heads, width):
+    """bf16 [rows, width] or [rows, heads, width] with contiguous rows: the row
+    stride (None for None)."""
+    if t is None:
+        return 0
+    _bf16(name, t, last_contig=False)
+    return _row_stride(name, t, rows, heads, width)
+
+
+def _row_stride(name, t, rows, heads, width):
+    shape, st = tuple(t.shape), t.stride()
+    if shape != (rows, heads, width) and (heads != 1 or shape != (rows, width)):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {width}], got {list(shape)}")
+    if (width > 1 and st[-1] != 1) or (len(st) == 3 and heads > 1 and st[1] != width):
+        raise ValueError(f"{name}: a row's heads and channels must be contiguous")
+    return st[0]
+
+
+def _norm_sizes(name, x):
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows, width] or [rows, heads, width]")
+    return (x.shape[0], 1, x.shape[1]) if x.dim() == 2 else tuple(x.shape)
+
+
+def _norm_weight(name, w, width):
+    _f32(name, w)
+    if tuple(w.shape) != (width,):
+        raise ValueError(f"{name} must be [{width}], got {list(w.shape)}")
+
+
+def kda_rmsnorm(x, weight, out, residual=None, residual_out=None, gate=None, scales=None,
+                eps: float = 1e-6, stream=None) -> None:
+    """y = norm(x [+ residual]) * weight [* sigmoid(gate)] per vector of the last
+    dimension. x, residual, residual_out, gate: bf16 [rows, width] or [rows,
+    heads, width] (row-strided); weight fp32 [width]; out bf16, or
+    float8_e4m3fn holding y / scale with scales fp32 [rows, n], contiguous rows:
+    n = heads (one scale per vector) or n = heads * width / 128 (one per 128
+    channels). residual_out (may be residual) receives x + residual."""
+    import torch
+    rows, heads, width = _norm_sizes("x", x)
+    xs = _vectors("x", x, rows, heads, width)
+    rs = _vectors("residual", residual, rows, heads, width)
+    ro = _vectors("residual_out", residual_out, rows, heads, width)
+    gs = _vectors("gate", gate, rows, heads, width)
+    _norm_weight("weight", weight, width)
+    fp8 = out.dtype == torch.float8_e4m3fn
+    if not fp8:
+        _bf16("out", out, last_contig=False)
+    elif not out.is_cuda:
+        raise ValueError("out must be a GPU tensor")
+    os_ = _row_stride("out", out, rows, heads, width)
+    group = ss = 0
+    if fp8:
+        if scales is None or scales.dtype != torch.float32 or not scales.is_cuda or \
+                scales.dim() != 2 or scales.shape[0] != rows or \
+                (scales.shape[1] > 1 and scales.stride(1) != 1):
+            raise ValueError("scales must be a float32 GPU tensor [rows, n] with contiguous rows")
+        ss = scales.stride(0)
+        if scales.shape[1] != heads:
+            if width % 128 != 0 or scales.shape[1] != heads * width // 128:
+                raise ValueError(f"scales must have {heads} columns, or one per 128 channels, "
+                                 f"got {scales.shape[1]}")
+            group = 128
+    elif scales is not None:
+        raise ValueError("scales belong to an fp8 output")
+    dev = _same_device(x, (("weight", weight), ("out", out), ("residual", residual),
+                           ("residual_out", residual_out), ("gate", gate), ("scales", scales)))
+    _launch("kda_rmsnorm", dev, stream, rows, heads, width, _ptr(x), xs, _ptr(residual), rs,
+            _ptr(residual_out), ro, _ptr(gate), gs, _ptr(weight), float(eps), 1 if fp8 else 0,
+            _ptr(out), os_, group, _ptr(scales), ss)
+
+
+def kda_rmsnorm_backward_workspace_size(rows: int, heads: int, width: int) -> int:
+    return int(lib().kda_rmsnorm_backward_workspace_size(rows, heads, width))
+
+
+def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None, d_residual=None,
+                         eps: float = 1e-6, workspace=None, stream=None) -> None:
+    """Gradients of kda_rmsnorm at its input z (x, or residual_out). z, dy, dz,
+    gate, dgate, d_residual: bf16 [rows, width] or [rows, heads, width]
+    (row-strided); weight, dweight fp32 [width]. dz receives the gradient at z plus
+    d_residual, the gradient that reaches z past the norm. workspace: uint8 GPU
+    tensor of >= kda_rmsnorm_backward_workspace_size(...) bytes, or None to have
+    one allocated here for this call."""
+    import torch
+    rows, heads, width = _norm_sizes("z", z)
+    zs = _vectors("z", z, rows, heads, width)
+    ys = _vectors("dy", dy, rows, heads, width)
+    gs = _vectors("gate", gate, rows, heads, width)
+    rs = _vectors("d_residual", d_residual, rows, heads, width)
+    ds = _vectors("dz", dz, rows, heads, width)
+    dgs = _vectors("dgate", dgate, rows, heads, width)
+    _norm_weight("weight", weight, width)
+    if dweight is not None:
+        _norm_weight("dweight", dweight, width)
+    dev = _same_device(z, (("weight", weight), ("dy", dy), ("dz", dz), ("dweight", dweight),
+                           ("gate", gate), ("dgate", dgate), ("d_residual", d_residual),
+                           ("workspace", workspace)))
+    if workspace is None and dweight is not None and rows > 0:
+        need = kda_rmsnorm_backward_workspace_size(rows, heads, width)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("kda_rmsnorm_backward", dev, stream, rows, heads, width, _ptr(z), zs, _ptr(dy), ys,
+            _ptr(gate), gs, _ptr(d_residual), rs, _ptr(weight), float(eps), _ptr(dz), ds,
+            _ptr(dgate), dgs, _ptr(dweight), _ptr(workspace), ws_bytes)

@@ -1,0 +1,573 @@
+// RMS norms of a KDA layer and their gradients (gfx950): residual addition,
+// norm, sigmoid gate, bf16 or fp8 e4m3 output with scales.
+//
+// Per (row, head) vector of n channels, with z = x + residual:
+//   s = 1 / sqrt(sum z^2 / n + eps),  y = z s w [sigmoid(gate)]
+// and, for the gradient, with a = dy w [sigmoid(gate)]:
+//   dz = s (a - z s^2 (sum a z) / n) [+ d_residual]
+//   dw = sum over vectors of dy z s [sigmoid(gate)]
+//   dgate = dy z s w sig (1 - sig)
+//
+// Both are bound by HBM: every tensor passes once, and a few operations per
+// element sit far below the vector rate. So a vector is held in registers
+// between the reduction and the output (read once), by LPR lanes with NV
+// groups of 8 consecutive channels each; the lane count follows the width, so
+// that a head's 128 channels take 16 lanes (one DPP row, four vectors per
+// wave, no LDS) and a wide row one workgroup. A workgroup walks over several
+// vectors and keeps its weights in registers meanwhile.
+//
+// Rows of odd strides or widths use the same 16-byte accesses: gfx950 takes
+// unaligned vector loads and stores from global memory, and only the last,
+// partial group of 8 of a vector goes element by element.
+
+#include <stdint.h>
+
+#include "../../include/kda_norm.h"
+#include "kda_common.h"
+
+namespace kda {
+namespace {
+
+typedef u32x4 u32x4_u __attribute__((aligned(1)));
+typedef u32x2 u32x2_u __attribute__((aligned(1)));
+
+constexpr int kOutBf16 = 0;
+constexpr int kOutFp8 = 1;       // one scale per vector
+constexpr int kOutFp8Group = 2;  // one scale per 128 channels
+
+struct NormParams {
+  int64_t vecs;  // rows * heads
+  int32_t heads, width;
+  const uint16_t* x;
+  const uint16_t* res;
+  uint16_t* res_out;
+  const uint16_t* gate;
+  const float* weight;
+  float eps;
+  void* out;
+  float* scales;
+  int64_t x_stride, res_stride, res_out_stride, gate_stride, out_stride, scales_stride;
+};
+
+struct NormBwdParams {
+  int64_t vecs;
+  int32_t heads, width;
+  const uint16_t* z;
+  const uint16_t* dy;
+  const uint16_t* gate;
+  const uint16_t* dres;
+  const float* weight;
+  float eps;
+  uint16_t* dz;
+  uint16_t* dgate;
+  float* partial;  // [blocks][width], or NULL
+  int64_t z_stride, dy_stride, gate_stride, dres_stride, dz_stride, dgate_stride;
+};
+
+// 8 channels from c on; channels past the width read as zeros.
+__device__ __forceinline__ u32x4 load_ch8(const uint16_t* row, int c, int width) {
+  if (c + 8 <= width) return *reinterpret_cast<const u32x4_u*>(row + c);
+  u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (c + i < width) w[i >> 1] |= uint32_t(row[c + i]) << (16 * (i & 1));
+  return w;
+}
+__device__ __forceinline__ void store_ch8(uint16_t* row, int c, int width, u32x4 w) {
+  if (c + 8 <= width) {
+    *reinterpret_cast<u32x4_u*>(row + c) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (c + i < width) row[c + i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ void store_ch8(uint8_t* row, int c, int width, u32x2 w) {
+  if (c + 8 <= width) {
+    *reinterpret_cast<u32x2_u*>(row + c) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (c + i < width) row[c + i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+}
+__device__ __forceinline__ u32x4 pack8(const float (&y)[8]) {
+  return u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+               pack_bf16x2(y[6], y[7])};
+}
+// Saturating fp8 e4m3; a NaN stays one (the clamp would turn it into -448).
+__device__ __forceinline__ float sat8(float x) { return x != x ? x : f8_sat(x); }
+__device__ __forceinline__ uint32_t pack8_fp8x4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(sat8(a), sat8(b), 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(sat8(c), sat8(d), r, true));
+}
+
+__device__ __forceinline__ float row16_max(float x) {
+  x = fmaxf(x, dpp<0xB1>(x));
+  x = fmaxf(x, dpp<0x4E>(x));
+  x = fmaxf(x, dpp<0x141>(x));
+  return fmaxf(x, dpp<0x140>(x));
+}
+
+// Reduction over the LPR lanes of a vector; every one of them gets the result.
+// Above one wave it goes through `buf` (one float per wave and buffer) with one
+// barrier: the caller alternates `buf` between two arrays, so that a wave still
+// reading one of them is a barrier ahead of its next use.
+template <int LPR, bool MAX>
+__device__ __forceinline__ float reduce(float x, float* buf) {
+  x = MAX ? row16_max(x) : row16_sum(x);
+  if constexpr (LPR >= 64) {
+#pragma unroll
+    for (int o = 16; o < 64; o *= 2) {
+      const float y = __shfl_xor(x, o);
+      x = MAX ? fmaxf(x, y) : x + y;
+    }
+  }
+  if constexpr (LPR > 64) {
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = buf[0];
+#pragma unroll
+    for (int w = 1; w < LPR / 64; ++w) x = MAX ? fmaxf(x, buf[w]) : x + buf[w];
+  }
+  return x;
+}
+
+// Threads of a workgroup: LPR lanes per vector, at least four waves.
+template <int LPR>
+constexpr int kNormThreads = LPR > 256 ? LPR : 256;
+
+template <int LPR, int NV, bool RES, bool GATE, int OUT>
+__global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p) {
+  constexpr int T = kNormThreads<LPR>;
+  constexpr int VPB = T / LPR;  // vectors of a workgroup at a time
+  __shared__ float buf[4][T / 64];
+  const int lane = threadIdx.x % LPR;
+  const float inv_n = 1.0f / float(p.width);
+
+  float w[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LPR + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[j][i] = c + i < p.width ? p.weight[c + i] : 0.f;
+  }
+
+  int turn = 0;
+  for (int64_t v = int64_t(blockIdx.x) * VPB + threadIdx.x / LPR; v < p.vecs;
+       v += int64_t(gridDim.x) * VPB, turn ^= 1) {
+    const int64_t r = p.heads == 1 ? v : v / p.heads;
+    const int64_t h0 = p.heads == 1 ? 0 : (v - r * p.heads) * p.width;
+    u32x4 xw[NV], rw[NV], gw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LPR + lane) * 8;
+      xw[j] = load_ch8(p.x + r * p.x_stride + h0, c, p.width);
+      if constexpr (RES) rw[j] = load_ch8(p.res + r * p.res_stride + h0, c, p.width);
+      if constexpr (GATE) gw[j] = load_ch8(p.gate + r * p.gate_stride + h0, c, p.width);
+    }
+    float z[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack8_bf16(xw[j], z[j]);
+      if constexpr (RES) {
+        float t[8];
+        unpack8_bf16(rw[j], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[j][i] += t[i];
+        if (p.res_out)
+          store_ch8(p.res_out + r * p.res_out_stride + h0, (j * LPR + lane) * 8, p.width,
+                    pack8(z[j]));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(z[j][i], z[j][i], ss);
+    }
+    ss = reduce<LPR, false>(ss, buf[turn]);
+    const float s = 1.0f / sqrtf(fmaf(ss, inv_n, p.eps));
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float t[8];
+      if constexpr (GATE) unpack8_bf16(gw[j], t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float y = z[j][i] * s * w[j][i];
+        if constexpr (GATE) y *= fsigmoid(t[i]);
+        z[j][i] = y;
+        if constexpr (OUT == kOutFp8) top = fmaxf(top, fabsf(y));
+      }
+    }
+    if constexpr (OUT == kOutBf16) {
+      uint16_t* out = static_cast<uint16_t*>(p.out) + r * p.out_stride + h0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) store_ch8(out, (j * LPR + lane) * 8, p.width, pack8(z[j]));
+    } else {
+      uint8_t* out = static_cast<uint8_t*>(p.out) + r * p.out_stride + h0;
+      float* sc = p.scales + r * p.scales_stride;
+      if constexpr (OUT == kOutFp8) top = reduce<LPR, true>(top, buf[2 + turn]);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * LPR + lane) * 8;
+        if constexpr (OUT == kOutFp8Group) {  // 16 lanes hold a group's 128 channels
+          top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(z[j][i]));
+          top = row16_max(top);
+        }
+        const bool some = top >= 1e-30f;
+        const float mul = some ? 448.0f / top : 1.0f;
+        const float scale = some ? top * (1.0f / 448.0f) : 1.0f;
+        if constexpr (OUT == kOutFp8Group) {
+          if ((lane & 15) == 0 && c < p.width) sc[(h0 + c) / 128] = scale;
+        } else if (j == 0 && lane == 0) {
+          sc[p.heads == 1 ? 0 : v - r * p.heads] = scale;
+        }
+        store_ch8(out, c, p.width,
+                  u32x2{pack8_fp8x4(z[j][0] * mul, z[j][1] * mul, z[j][2] * mul, z[j][3] * mul),
+                        pack8_fp8x4(z[j][4] * mul, z[j][5] * mul, z[j][6] * mul, z[j][7] * mul)});
+      }
+    }
+  }
+}
+
+// The gradient. The weights' gradient is summed in registers over the
+// vectors a workgroup walks, then over its lane groups in LDS, and leaves as
+// one partial row per workgroup; reduce_partials adds those in index order.
+template <int LPR, int NV, bool RES, bool GATE>
+__global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_bwd_kernel(NormBwdParams p) {
+  constexpr int T = kNormThreads<LPR>;
+  constexpr int VPB = T / LPR;
+  constexpr int CAP = LPR * NV * 8;
+  __shared__ float buf[4][T / 64];
+  __shared__ float fold[VPB > 1 ? VPB * CAP : 1];
+  const int lane = threadIdx.x % LPR;
+  const float inv_n = 1.0f / float(p.width);
+
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LPR + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[j][i] = c + i < p.width ? p.weight[c + i] : 0.f;
+      dw[j][i] = 0.f;
+    }
+  }
+
+  int turn = 0;
+  for (int64_t v = int64_t(blockIdx.x) * VPB + threadIdx.x / LPR; v < p.vecs;
+       v += int64_t(gridDim.x) * VPB, turn ^= 1) {
+    const int64_t r = p.heads == 1 ? v : v / p.heads;
+    const int64_t h0 = p.heads == 1 ? 0 : (v - r * p.heads) * p.width;
+    u32x4 zw[NV], yw[NV], rw[NV], gw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LPR + lane) * 8;
+      zw[j] = load_ch8(p.z + r * p.z_stride + h0, c, p.width);
+      yw[j] = load_ch8(p.dy + r * p.dy_stride + h0, c, p.width);
+      if constexpr (GATE) gw[j] = load_ch8(p.gate + r * p.gate_stride + h0, c, p.width);
+      if constexpr (RES) rw[j] = load_ch8(p.dres + r * p.dres_stride + h0, c, p.width);
+    }
+    float ss = 0.f, sa = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float z[8], a[8], g[8];
+      unpack8_bf16(zw[j], z);
+      unpack8_bf16(yw[j], a);
+      if constexpr (GATE) unpack8_bf16(gw[j], g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (GATE) a[i] *= fsigmoid(g[i]);
+        ss = fmaf(z[i], z[i], ss);
+        sa = fmaf(a[i] * w[j][i], z[i], sa);
+      }
+    }
+    ss = reduce<LPR, false>(ss, buf[turn]);
+    sa = reduce<LPR, false>(sa, buf[2 + turn]);
+    const float s = 1.0f / sqrtf(fmaf(ss, inv_n, p.eps));
+    const float m = sa * s * s * inv_n;  // mean(a n) s, with n = z s
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LPR + lane) * 8;
+      float z[8], y[8], g[8], t[8];
+      unpack8_bf16(zw[j], z);
+      unpack8_bf16(yw[j], y);
+      if constexpr (GATE) unpack8_bf16(gw[j], g);
+      if constexpr (RES) unpack8_bf16(rw[j], t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = z[i] * s;
+        float d = y[i];
+        if constexpr (GATE) {
+          const float sig = fsigmoid(g[i]);
+          d *= sig;
+          g[i] = d * (1.0f - sig) * n * w[j][i];
+        }
+        dw[j][i] = fmaf(d, n, dw[j][i]);
+        y[i] = s * fmaf(-m, z[i], d * w[j][i]);
+        if constexpr (RES) y[i] += t[i];
+      }
+      store_ch8(p.dz + r * p.dz_stride + h0, c, p.width, pack8(y));
+      if constexpr (GATE) store_ch8(p.dgate + r * p.dgate_stride + h0, c, p.width, pack8(g));
+    }
+  }
+  if (!p.partial) return;
+  float* part = p.partial + int64_t(blockIdx.x) * p.width;
+  if constexpr (VPB > 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        fold[(threadIdx.x / LPR) * CAP + (j * LPR + lane) * 8 + i] = dw[j][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.width; c += T) {
+      float t = fold[c];
+#pragma unroll
+      for (int g = 1; g < VPB; ++g) t += fold[g * CAP + c];
+      part[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (j * LPR + lane) * 8 + i;
+        if (c < p.width) part[c] = dw[j][i];
+      }
+  }
+}
+
+// dweight[c] = sum over the partial rows: 16 waves take every 16th row of 64
+// channels, and their sums meet in LDS in wave order.
+__global__ __launch_bounds__(1024) void reduce_partials(const float* partial, int blocks,
+                                                        int width, float* dweight) {
+  __shared__ float sum[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float t = 0.f;
+  if (c < width) {
+    int b = wave;
+    for (; b + 112 < blocks; b += 128) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = partial[int64_t(b + 16 * i) * width + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += x[i];
+    }
+    for (; b < blocks; b += 16) t += partial[int64_t(b) * width + c];
+  }
+  sum[wave][lane] = t;
+  __syncthreads();
+  if (wave == 0 && c < width) {
+    t = sum[0][lane];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += sum[i][lane];
+    dweight[c] = t;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+// The lanes and groups of 8 that hold a vector of this width: the narrowest
+// shape that covers it.
+#define KDA_NORM_SHAPES(F)              \
+  if (width <= 128) return F(16, 1);    \
+  if (width <= 512) return F(64, 1);    \
+  if (width <= 1024) return F(64, 2);   \
+  if (width <= 2048) return F(256, 1);  \
+  if (width <= 4096) return F(256, 2);  \
+  if (width <= 8192) return F(256, 4);  \
+  return F(512, 4)
+
+int vecs_per_block(int width) {
+#define KDA_NORM_VPB(L, N) kNormThreads<L> / L
+  KDA_NORM_SHAPES(KDA_NORM_VPB);
+#undef KDA_NORM_VPB
+}
+
+// Workgroups: every vector at once up to `most`, which fills the chip's
+// registers; above it they walk.
+unsigned norm_blocks(int64_t vecs, int width, int64_t most) {
+  const int64_t vpb = vecs_per_block(width);
+  const int64_t b = (vecs + vpb - 1) / vpb;
+  return unsigned(b < most ? b : most);
+}
+constexpr int64_t kNormBlocks = 2048;
+constexpr int64_t kNormBwdBlocks = 512;
+
+template <int L, int N, bool RES, bool GATE>
+hipError_t launch_norm3(const NormParams& p, int out, hipStream_t stream) {
+  const dim3 grid(norm_blocks(p.vecs, p.width, kNormBlocks)), block(kNormThreads<L>);
+  switch (out) {
+    case kOutBf16:
+      hipLaunchKernelGGL((rmsnorm_kernel<L, N, RES, GATE, kOutBf16>), grid, block, 0, stream, p);
+      break;
+    case kOutFp8:
+      hipLaunchKernelGGL((rmsnorm_kernel<L, N, RES, GATE, kOutFp8>), grid, block, 0, stream, p);
+      break;
+    default:
+      hipLaunchKernelGGL((rmsnorm_kernel<L, N, RES, GATE, kOutFp8Group>), grid, block, 0, stream,
+                         p);
+  }
+  return hipGetLastError();
+}
+template <int L, int N>
+hipError_t launch_norm2(const NormParams& p, int out, hipStream_t stream) {
+  if (p.res)
+    return p.gate ? launch_norm3<L, N, true, true>(p, out, stream)
+                  : launch_norm3<L, N, true, false>(p, out, stream);
+  return p.gate ? launch_norm3<L, N, false, true>(p, out, stream)
+                : launch_norm3<L, N, false, false>(p, out, stream);
+}
+hipError_t launch_norm(const NormParams& p, int out, hipStream_t stream) {
+  const int width = p.width;
+#define KDA_NORM_GO(L, N) launch_norm2<L, N>(p, out, stream)
+  KDA_NORM_SHAPES(KDA_NORM_GO);
+#undef KDA_NORM_GO
+}
+
+template <int L, int N>
+hipError_t launch_norm_bwd2(const NormBwdParams& p, hipStream_t stream) {
+  const dim3 grid(norm_blocks(p.vecs, p.width, kNormBwdBlocks)), block(kNormThreads<L>);
+  if (p.dres && p.gate)
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<L, N, true, true>), grid, block, 0, stream, p);
+  else if (p.dres)
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<L, N, true, false>), grid, block, 0, stream, p);
+  else if (p.gate)
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<L, N, false, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<L, N, false, false>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+hipError_t launch_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  const int width = p.width;
+#define KDA_NORM_GO(L, N) launch_norm_bwd2<L, N>(p, stream)
+  KDA_NORM_SHAPES(KDA_NORM_GO);
+#undef KDA_NORM_GO
+}
+
+kda_status check_sizes(int64_t rows, int32_t heads, int32_t width, float eps) {
+  if (rows < 0 || heads < 1 || width < 1) return KDA_ERR_BAD_SHAPE;
+  if (width > KDA_NORM_MAX_WIDTH || int64_t(heads) * width > (int64_t(1) << 30))
+    return KDA_ERR_UNSUPPORTED;
+  if (rows > (int64_t(1) << 62) / (int64_t(heads) * width)) return KDA_ERR_UNSUPPORTED;
+  if (!(eps > 0.0f && eps < INFINITY)) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// Rows of `len` elements do not overlap.
+bool rows_apart(int64_t rows, int64_t stride, int64_t len) { return rows <= 1 || stride >= len; }
+
+}  // namespace
+}  // namespace kda
+
+extern "C" kda_status kda_rmsnorm(int64_t rows, int32_t heads, int32_t width, const void* x,
+                                  int64_t x_row_stride, const void* residual,
+                                  int64_t residual_row_stride, void* residual_out,
+                                  int64_t residual_out_row_stride, const void* gate,
+                                  int64_t gate_row_stride, const float* weight, float eps,
+                                  int32_t out_dtype, void* out, int64_t out_row_stride,
+                                  int32_t scale_group, float* scales, int64_t scales_row_stride,
+                                  hipStream_t stream) {
+  if (const kda_status st = kda::check_sizes(rows, heads, width, eps)) return st;
+  const bool fp8 = out_dtype == KDA_NORM_OUT_FP8;
+  if (out_dtype != KDA_NORM_OUT_BF16 && !fp8) return KDA_ERR_UNSUPPORTED;
+  const bool whole = scale_group == 0 || scale_group == width;
+  if (fp8 && !whole && (scale_group != 128 || width % 128 != 0)) return KDA_ERR_UNSUPPORTED;
+  if (residual_out && !residual) return KDA_ERR_UNSUPPORTED;
+  if (rows == 0) return KDA_OK;
+  if (!x || !weight || !out || (fp8 && !scales)) return KDA_ERR_NULL_POINTER;
+  const int64_t W = int64_t(heads) * width;
+  if (x_row_stride < 0 || out_row_stride < 0 || (residual && residual_row_stride < 0) ||
+      (residual_out && residual_out_row_stride < 0) || (gate && gate_row_stride < 0) ||
+      (fp8 && scales_row_stride < 0))
+    return KDA_ERR_BAD_STRIDE;
+  if (!kda::rows_apart(rows, out_row_stride, W) ||
+      (residual_out && !kda::rows_apart(rows, residual_out_row_stride, W)) ||
+      (fp8 && !kda::rows_apart(rows, scales_row_stride,
+                               int64_t(heads) * (whole ? 1 : width / 128))))
+    return KDA_ERR_BAD_STRIDE;
+
+  kda::NormParams p;
+  p.vecs = rows * heads;
+  p.heads = heads;
+  p.width = width;
+  p.x = static_cast<const uint16_t*>(x);
+  p.res = static_cast<const uint16_t*>(residual);
+  p.res_out = static_cast<uint16_t*>(residual_out);
+  p.gate = static_cast<const uint16_t*>(gate);
+  p.weight = weight;
+  p.eps = eps;
+  p.out = out;
+  p.scales = scales;
+  p.x_stride = x_row_stride;
+  p.res_stride = residual_row_stride;
+  p.res_out_stride = residual_out_row_stride;
+  p.gate_stride = gate_row_stride;
+  p.out_stride = out_row_stride;
+  p.scales_stride = scales_row_stride;
+  const int kind = !fp8 ? kda::kOutBf16 : whole ? kda::kOutFp8 : kda::kOutFp8Group;
+  return kda::launch_norm(p, kind, stream) == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" size_t kda_rmsnorm_backward_workspace_size(int64_t rows, int32_t heads,
+                                                      int32_t width) {
+  if (kda::check_sizes(rows, heads, width, 1.0f)) return 0;
+  return size_t(kda::norm_blocks(rows * heads, width, kda::kNormBwdBlocks)) * size_t(width) * 4;
+}
+
+extern "C" kda_status kda_rmsnorm_backward(
+    int64_t rows, int32_t heads, int32_t width, const void* z, int64_t z_row_stride,
+    const void* dy, int64_t dy_row_stride, const void* gate, int64_t gate_row_stride,
+    const void* d_residual, int64_t d_residual_row_stride, const float* weight, float eps,
+    void* dz, int64_t dz_row_stride, void* dgate, int64_t dgate_row_stride, float* dweight,
+    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (const kda_status st = kda::check_sizes(rows, heads, width, eps)) return st;
+  if (rows > 0 && (!z || !dy || !weight || !dz)) return KDA_ERR_NULL_POINTER;
+  if ((gate != nullptr) != (dgate != nullptr)) return KDA_ERR_NULL_POINTER;
+  const int64_t W = int64_t(heads) * width;
+  if (rows > 0) {
+    if (z_row_stride < 0 || dy_row_stride < 0 || dz_row_stride < 0 ||
+        (gate && (gate_row_stride < 0 || dgate_row_stride < 0)) ||
+        (d_residual && d_residual_row_stride < 0))
+      return KDA_ERR_BAD_STRIDE;
+    if (!kda::rows_apart(rows, dz_row_stride, W) ||
+        (gate && !kda::rows_apart(rows, dgate_row_stride, W)))
+      return KDA_ERR_BAD_STRIDE;
+  }
+  const int blocks = int(kda::norm_blocks(rows * heads, width, kda::kNormBwdBlocks));
+  if (dweight && rows > 0) {
+    if (workspace_bytes < size_t(blocks) * size_t(width) * 4) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace) return KDA_ERR_NULL_POINTER;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KDA_ERR_UNSUPPORTED;
+  }
+
+  kda::NormBwdParams p;
+  p.vecs = rows * heads;
+  p.heads = heads;
+  p.width = width;
+  p.z = static_cast<const uint16_t*>(z);
+  p.dy = static_cast<const uint16_t*>(dy);
+  p.gate = static_cast<const uint16_t*>(gate);
+  p.dres = static_cast<const uint16_t*>(d_residual);
+  p.weight = weight;
+  p.eps = eps;
+  p.dz = static_cast<uint16_t*>(dz);
+  p.dgate = static_cast<uint16_t*>(dgate);
+  p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  p.z_stride = z_row_stride;
+  p.dy_stride = dy_row_stride;
+  p.gate_stride = gate_row_stride;
+  p.dres_stride = d_residual_row_stride;
+  p.dz_stride = dz_row_stride;
+  p.dgate_stride = dgate_row_stride;
+  if (rows > 0 && kda::launch_norm_bwd(p, stream) != hipSuccess) return KDA_ERR_LAUNCH;
+  if (dweight) {
+    hipLaunchKernelGGL(kda::reduce_partials, dim3((width + 63) / 64), dim3(1024), 0, stream,
+                       p.partial, rows > 0 ? blocks : 0, width, dweight);
+    if (hipGetLastError() != hipSuccess) return KDA_ERR_LAUNCH;
+  }
+  return KDA_OK;
+}

@@ -1,0 +1,357 @@
+"""kda_rmsnorm and kda_rmsnorm_backward: host validation (CPU) and parity with
+the formulas in 64 bits (GPU).
+
+Tolerances. bf16 outputs: half a step of the result (2^-8 |y|) plus the fp32
+arithmetic. Each factor of y = z s w sig carries a few fp32 roundings; the sum
+of squares of n terms, added in at most 64 + log steps, is off by under
+80 * 2^-24 of itself, so y by under 60 * 2^-24 |y| < 4e-6 |y|; hardware exp adds
+2^-22 |gate| to the sigmoid. 2^-8 |y| + 2e-5 |y| + 1e-6 top covers it, `top` being the
+row's largest value. fp8 outputs: half a step, 2^-4 |q|, or half the subnormal
+spacing 2^-10 near zero, and the same again where fp32 tips a tie: the value then
+still is one of the two neighbours, so 2^-4 * 1.001 |q| + 2^-10. dz cancels between
+a and n mean(a n): its fp32 error scales with the row's largest |s a|. dweight
+sums V vectors in fp32 over fewer than 1200 sequential steps: 1200 * 2^-24 = 7e-5
+of the sum of magnitudes, in practice its root; 2e-5 of that sum.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_step_amd as kda
+
+OK, NULLP, SHAPE, STRIDE, UNSUP, SEQ, WS = range(7)
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.LIB_PATH):
+        from gated_delta_rule_step_amd import build
+        build.build()
+    return kda.lib()
+
+
+# ---------------------------------------------------------------------------
+# refusals: every call returns before anything is launched (made-up pointers)
+
+def _fwd(lib, **kw):
+    a = dict(rows=2, heads=3, width=128, x=4096, xs=384, r=0, rs=384, ro=0, ros=384, g=0, gs=384,
+             w=4096, eps=1e-6, dt=0, o=4096, os=384, grp=0, sc=0, ss=3)
+    a.update(kw)
+    P = ctypes.c_void_p
+    return lib.kda_rmsnorm(a["rows"], a["heads"], a["width"], P(a["x"]), a["xs"], P(a["r"]),
+                           a["rs"], P(a["ro"]), a["ros"], P(a["g"]), a["gs"], P(a["w"]),
+                           a["eps"], a["dt"], P(a["o"]), a["os"], a["grp"], P(a["sc"]), a["ss"],
+                           P(0))
+
+
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(rows=-1)), (SHAPE, dict(heads=0)), (SHAPE, dict(width=0)),
+    (UNSUP, dict(width=16385)), (UNSUP, dict(heads=1 << 24)), (UNSUP, dict(rows=1 << 60)),
+    (UNSUP, dict(eps=0.0)), (UNSUP, dict(eps=float("nan"))), (UNSUP, dict(eps=float("inf"))),
+    (UNSUP, dict(dt=2)), (UNSUP, dict(ro=4096)), (UNSUP, dict(dt=1, sc=4096, grp=64)),
+    (UNSUP, dict(dt=1, sc=4096, grp=128, width=200)),
+    (NULLP, dict(x=0)), (NULLP, dict(w=0)), (NULLP, dict(o=0)), (NULLP, dict(dt=1)),
+    (STRIDE, dict(xs=-1)), (STRIDE, dict(os=383)), (STRIDE, dict(r=4096, rs=-8)),
+    (STRIDE, dict(r=4096, ro=4096, ros=100)), (STRIDE, dict(g=4096, gs=-1)),
+    (STRIDE, dict(dt=1, sc=4096, ss=2)),
+    (OK, dict(rows=0, x=0, w=0, o=0)),
+])
+def test_forward_refusals(lib, want, kw):
+    assert _fwd(lib, **kw) == want
+
+
+def _bwd(lib, **kw):
+    a = dict(rows=2, heads=3, width=128, z=4096, zs=384, dy=4096, ys=384, g=0, gs=384, r=0,
+             rs=384, w=4096, eps=1e-6, dz=4096, ds=384, dg=0, dgs=384, dw=0, ws=0, wb=0)
+    a.update(kw)
+    P = ctypes.c_void_p
+    return lib.kda_rmsnorm_backward(a["rows"], a["heads"], a["width"], P(a["z"]), a["zs"],
+                                    P(a["dy"]), a["ys"], P(a["g"]), a["gs"], P(a["r"]), a["rs"],
+                                    P(a["w"]), a["eps"], P(a["dz"]), a["ds"], P(a["dg"]),
+                                    a["dgs"], P(a["dw"]), P(a["ws"]), a["wb"], P(0))
+
+
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(rows=-1)), (SHAPE, dict(heads=-2)), (UNSUP, dict(width=20000)),
+    (UNSUP, dict(eps=-1.0)), (NULLP, dict(z=0)), (NULLP, dict(dy=0)), (NULLP, dict(dz=0)),
+    (NULLP, dict(g=4096)), (NULLP, dict(dg=4096)), (STRIDE, dict(zs=-1)),
+    (STRIDE, dict(ds=5)), (STRIDE, dict(g=4096, dg=4096, dgs=5)), (STRIDE, dict(r=4096, rs=-3)),
+    (WS, dict(dw=4096, ws=4096, wb=3)), (NULLP, dict(dw=4096, wb=1 << 20)),
+    (UNSUP, dict(dw=4096, ws=4100, wb=1 << 20)),
+    (OK, dict(rows=0, z=0, dy=0, dz=0)),
+])
+def test_backward_refusals(lib, want, kw):
+    assert _bwd(lib, **kw) == want
+
+
+def test_workspace_size(lib):
+    size = kda.kda_rmsnorm_backward_workspace_size
+    assert size(1, 1, 100) == 400
+    assert size(0, 1, 100) == 0 and size(5, 0, 100) == 0 and size(5, 1, 99999) == 0
+    assert size(1 << 40, 1, 8192) == size(1 << 20, 1, 8192)  # bounded by the grid
+
+
+def test_binding_refuses(lib):
+    x = torch.zeros(4, 128, dtype=BF)
+    w = torch.ones(128)
+    with pytest.raises(ValueError):
+        kda.kda_rmsnorm(x, w, torch.empty_like(x))  # not on a GPU
+    with pytest.raises(TypeError):
+        kda.kda_rmsnorm(x.float(), w, torch.empty_like(x))
+
+
+# ---------------------------------------------------------------------------
+# GPU
+
+def _rand(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(BF)
+
+
+def _strided(t, pad, offset):
+    """The same values on the GPU with `pad` more elements per row, starting `offset`
+    elements into the allocation."""
+    rows = t.shape[0]
+    n = t[0].numel() if rows else 1
+    buf = torch.full((offset + max(rows, 1) * (n + pad),), -7.0, dtype=t.dtype, device="cuda")
+    view = buf[offset:].as_strided((rows,) + tuple(t.shape[1:]),
+                                   (n + pad,) + tuple(t.stride()[1:]))
+    view.copy_(t)
+    return view, buf
+
+
+def _ref(x, w, res, gate, eps):
+    z = x.double() if res is None else x.double() + res.double()
+    y = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps) * w.double()
+    if gate is not None:
+        y = y * torch.sigmoid(gate.double())
+    return z, y
+
+
+# odd widths, one channel, the borders between the lane shapes, head vectors
+SHAPES = [(1, 1, 1), (3, 1, 7), (5, 12, 128), (129, 3, 128), (2, 1, 129), (33, 1, 512),
+          (7, 2, 513), (4, 1, 1001), (9, 1, 1024), (2, 1, 1025), (3, 1, 2048), (5, 1, 3000),
+          (2, 1, 4096), (3, 1, 8192), (2, 1, 8193), (1, 1, 16384), (4100, 1, 1536)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("res,gated,pad,off", [(False, False, 0, 0), (True, False, 0, 0),
+                                               (False, True, 8, 8), (True, True, 3, 1)])
+def test_forward_bf16(shape, res, gated, pad, off):
+    rows, heads, width = shape
+    x, w = _rand(shape, 1), 1 + 0.1 * _rand((width,), 2).float()
+    r = _rand(shape, 3, 2.0) if res else None
+    g = _rand(shape, 4) if gated else None
+    z, y = _ref(x, w, r, g, 1e-6)
+    xd = _strided(x, pad, off)[0]
+    rd = _strided(r, pad, off)[0] if res else None
+    gd = _strided(g, pad, off)[0] if gated else None
+    out, obuf = _strided(torch.zeros(shape, dtype=BF), pad, off)
+    zo, zbuf = _strided(torch.zeros(shape, dtype=BF), pad, off)
+    kda.kda_rmsnorm(xd, w.cuda(), out, residual=rd, residual_out=zo if res else None, gate=gd)
+    torch.cuda.synchronize()
+    err = (out.double().cpu() - y).abs()
+    top = y.abs().amax(-1, keepdim=True)
+    assert (err <= (2.0 ** -8 + 2e-5) * y.abs() + 1e-6 * top).all()
+    if res:  # the sum of two bf16 is rounded once: the nearest bf16 of it
+        assert torch.equal(zo.cpu(), z.to(BF))
+    # the padding between rows and before them stays
+    for buf in (obuf, zbuf):
+        n = heads * width
+        gaps = torch.cat([buf[:off], buf[off:].reshape(-1, n + pad)[:, n:].reshape(-1)])
+        assert (gaps == -7.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,group", [((5, 12, 128), 0), ((5, 12, 128), 128), ((3, 1, 1001), 0),
+                                         ((64, 1, 1536), 128), ((2, 4, 256), 128),
+                                         ((2, 4, 256), 0), ((3, 1, 8192), 128),
+                                         ((1, 1, 16384), 0), ((2, 1, 16384), 128)], ids=str)
+@pytest.mark.parametrize("res,gated", [(True, False), (False, True)])
+def test_forward_fp8(shape, group, res, gated):
+    rows, heads, width = shape
+    x, w = _rand(shape, 5, 30.0), 1 + 0.1 * _rand((width,), 6).float()
+    x[0] = 0  # a row of zeros takes scale 1
+    r = _rand(shape, 7) if res else None
+    if res:
+        r[0] = 0
+    g = _rand(shape, 8) if gated else None
+    _, y = _ref(x, w, r, g, 1e-6)
+    cols = heads * (width // group if group else 1)
+    out = torch.empty(shape, dtype=torch.float8_e4m3fn, device="cuda")
+    sbuf = torch.full((rows, cols + 3), -1.0, device="cuda")
+    sc = sbuf[:, :cols]
+    kda.kda_rmsnorm(x.cuda(), w.cuda(), out, residual=r.cuda() if res else None,
+                    gate=g.cuda() if gated else None, scales=sc)
+    torch.cuda.synchronize()
+    yg = y.reshape(rows, cols, -1)
+    top = yg.abs().amax(-1)
+    want = torch.where(top > 0, top / 448, 1.0)
+    got = sc.double().cpu()
+    assert ((got - want).abs() <= 1e-5 * want).all()
+    assert (got[0] == 1).all() and (sbuf[:, cols:] == -1).all()
+    q = out.float().double().cpu().reshape(yg.shape)
+    exact = yg / got[..., None]
+    assert ((q - exact).abs() <= 2.0 ** -4 * 1.001 * exact.abs() + 2.0 ** -10).all()
+    assert (q.abs().amax(-1)[1:] == 448).all()  # the largest value uses the format's range
+
+
+@pytest.mark.gpu
+def test_forward_in_place_broadcast_and_specials():
+    shape = (6, 1, 1000)
+    x, r, w = _rand(shape, 9), _rand(shape, 10), torch.ones(1000)
+    z, y = _ref(x, w, r, None, 1e-6)
+    xd, rd = x.cuda(), r.cuda()
+    kda.kda_rmsnorm(xd, w.cuda(), xd, residual=rd, residual_out=rd)  # both in place
+    assert torch.equal(rd.cpu(), z.to(BF))
+    assert ((xd.double().cpu() - y).abs() <= 2.0 ** -8 * 1.01 * y.abs() + 1e-5).all()
+    # one residual row for all rows (stride 0)
+    one = _rand((1, 1, 1000), 11)
+    out = torch.empty(shape, dtype=BF, device="cuda")
+    kda.kda_rmsnorm(x.cuda(), w.cuda(), out, residual=one.cuda().expand(shape))
+    y = _ref(x, w, one.expand(shape), None, 1e-6)[1]
+    assert ((out.double().cpu() - y).abs() <= 2.0 ** -8 * 1.01 * y.abs() + 1e-5).all()
+    # a NaN spoils its row and no other; fp8 keeps it a NaN
+    x[2, 0, 5] = float("nan")
+    x[3] = 0
+    o8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(6, 1, device="cuda")
+    kda.kda_rmsnorm(x.cuda(), w.cuda(), o8, scales=sc)
+    bad = o8.float().cpu().isnan().all(-1)[:, 0]
+    assert bad.tolist() == [False, False, True, False, False, False]
+    assert (o8[3].float() == 0).all() and sc[3, 0] == 1
+    # no rows
+    kda.kda_rmsnorm(x[:0].cuda(), w.cuda(), out[:0])
+    torch.cuda.synchronize()
+
+
+def _ref_bwd(z, w, dy, gate, dres, eps):
+    z = z.double().requires_grad_()
+    w = w.double().requires_grad_()
+    g = gate.double().requires_grad_() if gate is not None else None
+    y = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps) * w
+    if g is not None:
+        y = y * torch.sigmoid(g)
+    y.backward(dy.double())
+    dz = z.grad if dres is None else z.grad + dres.double()
+    return dz, w.grad, None if g is None else g.grad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES + [(3000, 5, 128)], ids=str)
+@pytest.mark.parametrize("res,gated,pad,off", [(False, False, 0, 0), (True, False, 8, 0),
+                                               (False, True, 1, 3), (True, True, 0, 0)])
+def test_backward(shape, res, gated, pad, off):
+    rows, heads, width = shape
+    z, dy, w = _rand(shape, 12), _rand(shape, 13), 1 + 0.1 * _rand((width,), 14).float()
+    r = _rand(shape, 15) if res else None
+    g = _rand(shape, 16) if gated else None
+    dz, dw, dg = _ref_bwd(z, w, dy, g, r, 1e-6)
+    zd, yd = _strided(z, pad, off)[0], _strided(dy, pad, off)[0]
+    out, obuf = _strided(torch.zeros(shape, dtype=BF), pad, off)
+    dgo = _strided(torch.zeros(shape, dtype=BF), pad, off)[0] if gated else None
+    dwo = torch.empty(width, device="cuda")
+    kw = dict(gate=_strided(g, pad, off)[0] if gated else None, dgate=dgo,
+              d_residual=_strided(r, pad, off)[0] if res else None)
+    kda.kda_rmsnorm_backward(zd, w.cuda(), yd, out, dwo, **kw)
+    torch.cuda.synchronize()
+    s = 1 / torch.sqrt(z.double().pow(2).mean(-1, keepdim=True) + 1e-6)
+    big = (s * (dy.double() * w.double()).abs()).amax(-1, keepdim=True)
+    err = (out.double().cpu() - dz).abs()
+    assert (err <= 2.0 ** -8 * dz.abs() + 2e-5 * big).all()
+    if gated:
+        top = dg.abs().amax(-1, keepdim=True)
+        assert ((dgo.double().cpu() - dg).abs() <= (2.0 ** -8 + 2e-5) * dg.abs() + 1e-6 * top).all()
+    mags = (dy.double() * z.double() * s).abs().sum((0, 1))
+    assert ((dwo.double().cpu() - dw).abs() <= 2e-5 * mags + 1e-12).all()
+    if pad:
+        assert (obuf[off:].reshape(-1, heads * width + pad)[:, heads * width:] == -7.0).all()
+    # the same bits again, with a workspace of the caller's holding anything
+    ws = torch.full((kda.kda_rmsnorm_backward_workspace_size(rows, heads, width),), 255,
+                    dtype=torch.uint8, device="cuda")
+    again = torch.empty_like(dwo)
+    kda.kda_rmsnorm_backward(zd, w.cuda(), yd, torch.empty(shape, dtype=BF, device="cuda"), again,
+                             workspace=ws, **kw)
+    assert torch.equal(again, dwo)
+
+
+@pytest.mark.gpu
+def test_backward_against_differences():
+    """dz, dgate and dweight against central differences of the forward formula."""
+    shape, h = (2, 1, 40), 1e-5
+    z, dy, g = _rand(shape, 20), _rand(shape, 21), _rand(shape, 22)
+    w = 1 + 0.1 * _rand((40,), 23).float()
+    dz = torch.empty(shape, dtype=BF, device="cuda")
+    dg, dw = torch.empty_like(dz), torch.empty(40, device="cuda")
+    kda.kda_rmsnorm_backward(z.cuda(), w.cuda(), dy.cuda(), dz, dw, gate=g.cuda(), dgate=dg)
+
+    def loss(z, w, g):
+        return (_ref(z, w, None, g, 1e-6)[1] * dy.double()).sum()
+
+    args = [z.double(), w.double(), g.double()]
+    for k, got in ((0, dz), (1, dw), (2, dg)):
+        for i in (0, 17, 39):
+            lo, hi = [a.clone() for a in args], [a.clone() for a in args]
+            lo[k].view(-1)[i] -= h
+            hi[k].view(-1)[i] += h
+            diff = (loss(*hi) - loss(*lo)) / (2 * h)
+            # half a bf16 step, and the difference's own error of about h^2 and 1e-16 / h
+            assert abs(got.reshape(-1)[i].double().cpu() - diff) <= 2.0 ** -8 * abs(diff) + 1e-5
+
+
+@pytest.mark.gpu
+def test_backward_optional_parts():
+    shape = (10, 2, 128)
+    z, dy, w = _rand(shape, 24).cuda(), _rand(shape, 25).cuda(), torch.ones(128, device="cuda")
+    dz, dw = torch.empty_like(z), torch.full((128,), -1.0, device="cuda")
+    kda.kda_rmsnorm_backward(z, w, dy, dz, dw)
+    only = torch.empty_like(z)
+    kda.kda_rmsnorm_backward(z, w, dy, only)  # no weight gradient, no workspace
+    assert torch.equal(only, dz)
+    inplace = dy.clone()
+    kda.kda_rmsnorm_backward(z, w, inplace, inplace)
+    assert torch.equal(inplace, dz)
+    kda.kda_rmsnorm_backward(z[:0], w, dy[:0], dz[:0], dw)  # no rows: zeros
+    assert (dw == 0).all()
+
+
+@pytest.mark.gpu
+def test_captured_and_on_another_stream():
+    """Both calls in one graph, replayed with changed inputs, next to eager calls
+    between the replays on the default stream with a workspace of their own."""
+    shape = (65, 1, 2000)
+    w = 1 + 0.1 * _rand((2000,), 30).float().cuda()
+    x, r, dy = (torch.zeros(shape, dtype=BF, device="cuda") for _ in range(3))
+    ws = torch.empty(kda.kda_rmsnorm_backward_workspace_size(65, 1, 2000), dtype=torch.uint8,
+                     device="cuda")
+
+    def both(ws):
+        out = torch.empty(shape, dtype=torch.float8_e4m3fn, device="cuda")
+        sc, zr = torch.empty(65, 1, device="cuda"), torch.empty_like(x)
+        dz, dw = torch.empty_like(x), torch.empty(2000, device="cuda")
+        kda.kda_rmsnorm(x, w, out, residual=r, residual_out=zr, scales=sc)
+        kda.kda_rmsnorm_backward(zr, w, dy, dz, dw, workspace=ws)
+        return out, sc, zr, dz, dw
+
+    both(ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = both(ws)
+    own = torch.empty_like(ws)
+    for k in range(3):
+        for t, s in ((x, 40), (r, 50), (dy, 60)):
+            t.copy_(_rand(shape, s + k))
+        graph.replay()
+        eager = both(own)
+        torch.cuda.synchronize()
+        for a, b in zip(captured, eager):
+            assert np.array_equal(a.view(torch.uint8).cpu().numpy(),
+                                  b.view(torch.uint8).cpu().numpy())
