@@ -48,6 +48,13 @@ _SIGS = {
                                               _P, _P, _F, _F, _I32, _I32, _P, _I64, _I64, _P,
                                               _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P,
                                               _I32, _P, _I32, _P]),
+    "kda_prefill_backward_workspace_size": (_c.c_size_t, [_I32, _I64, _I32, _I32, _I32]),
+    "kda_prefill_varlen_backward": (_c.c_int, [_I32, _I64, _I32, _I32, _I32, _P, _P,
+                                               _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                               _P, _P, _F, _F, _I32, _I32, _P, _I64, _I64, _P,
+                                               _I32, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
+                                               _P, _I64, _P, _I64, _P, _P, _P, _P, _c.c_size_t,
+                                               _P]),
     "kda_rmsnorm": (_c.c_int, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _F,
                                _I32, _P, _I64, _I32, _P, _I64, _P]),
     "kda_rmsnorm_backward_workspace_size": (_c.c_size_t, [_I64, _I32, _I32]),
@@ -67,6 +74,7 @@ FUSED_MIN_CHAINS = 256
 # dt_bias may then be None); beta_raw holds beta itself.
 GATE_PRECOMPUTED = 1
 BETA_PRESIGMOID = 2
+GATE_PER_HEAD = 4  # one gate value (and dt_bias) per head
 
 
 class KdaError(RuntimeError):
@@ -377,6 +385,83 @@ def _launch(fn, dev, stream, *args):
     with torch.cuda.device(dev):
         st = getattr(lib(), fn)(*args, _stream(stream))
     _check(fn, st)
+
+
+def kda_prefill_backward_workspace_size(n_docs: int, total_tokens: int, H: int) -> int:
+    return int(lib().kda_prefill_backward_workspace_size(n_docs, total_tokens, H, HEAD_DIM,
+                                                         HEAD_DIM))
+
+
+def kda_prefill_varlen_backward(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, beta_raw, A_log,
+                                dt_bias, state_pool, state_indices, d_out, dq, dk, dv, dg, dbeta,
+                                dA_log=None, ddt_bias=None, d_final_state=None,
+                                d_initial_state=None, workspace=None,
+                                use_initial_state: bool = True, lower_bound: float = -5.0,
+                                scale: float = 1.0, gate_mode: int = 0, stream=None) -> None:
+    """Gradients of one kda_prefill_varlen call, from the same inputs. state_pool is
+    the pool as it was before that call (only read). d_out, dq, dk, dv: bf16
+    [Ttot, H*128] (token-strided); dg like g_raw, dbeta like beta_raw; dA_log fp32 like
+    A_log and ddt_bias fp32 like dt_bias, or None; d_final_state and d_initial_state:
+    contiguous fp32 [n_docs, H, 128, 128] (value, key), or None. workspace: uint8 GPU
+    tensor of >= kda_prefill_backward_workspace_size(...) bytes, or None to have one
+    allocated here for this call."""
+    import torch
+    if cu_seqlens_host.dtype != torch.int32 or cu_seqlens_host.is_cuda or \
+            not cu_seqlens_host.is_contiguous() or cu_seqlens_host.dim() != 1 or \
+            cu_seqlens_host.shape[0] < 1:
+        raise ValueError("cu_seqlens_host must be a contiguous int32 CPU tensor [n_docs + 1]")
+    n_docs = cu_seqlens_host.shape[0] - 1
+    T, W = q.shape
+    H = W // HEAD_DIM
+    if W != H * HEAD_DIM or H < 1:
+        raise ValueError(f"q must be [Ttot, H*128], got {list(q.shape)}")
+    gw = H if gate_mode & GATE_PER_HEAD else W
+    pre = bool(gate_mode & GATE_PRECOMPUTED)
+    for n, t, w in (("q", q, W), ("k", k, W), ("v", v, W), ("g_raw", g_raw, gw),
+                    ("beta_raw", beta_raw, H), ("d_out", d_out, W), ("dq", dq, W), ("dk", dk, W),
+                    ("dv", dv, W), ("dg", dg, gw), ("dbeta", dbeta, H)):
+        _bf16(n, t, last_contig=w > 1)
+        if tuple(t.shape) != (T, w):
+            raise ValueError(f"{n} must be [{T}, {w}], got {list(t.shape)}")
+    for n, t, w in (("A_log", A_log, H), ("dt_bias", dt_bias, gw), ("dA_log", dA_log, H),
+                    ("ddt_bias", ddt_bias, gw)):
+        if t is None and (pre or n in ("dA_log", "ddt_bias")):
+            continue
+        _f32(n, t)
+        if t.numel() != w:
+            raise ValueError(f"{n} must hold {w} values, got {t.numel()}")
+    for n, t, w in (("cu_seqlens", cu_seqlens, n_docs + 1), ("state_indices", state_indices,
+                                                             n_docs)):
+        _i32(n, t)
+        if t.numel() != w:
+            raise ValueError(f"{n} must hold {w} values, got {t.numel()}")
+    for n, t in (("d_final_state", d_final_state), ("d_initial_state", d_initial_state)):
+        _f32(n, t, optional=True)
+        if t is not None and tuple(t.shape) != (n_docs, H, HEAD_DIM, HEAD_DIM):
+            raise ValueError(f"{n} must be [{n_docs}, {H}, 128, 128], got {list(t.shape)}")
+    N, slot_stride = _pool_geometry(state_pool, H)
+    dev = _same_device(q, (("cu_seqlens", cu_seqlens), ("k", k), ("v", v), ("g_raw", g_raw),
+                           ("beta_raw", beta_raw), ("A_log", A_log), ("dt_bias", dt_bias),
+                           ("state_pool", state_pool), ("state_indices", state_indices),
+                           ("d_out", d_out), ("dq", dq), ("dk", dk), ("dv", dv), ("dg", dg),
+                           ("dbeta", dbeta), ("dA_log", dA_log), ("ddt_bias", ddt_bias),
+                           ("d_final_state", d_final_state),
+                           ("d_initial_state", d_initial_state), ("workspace", workspace)))
+    if workspace is None:
+        need = kda_prefill_backward_workspace_size(n_docs, T, H)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("kda_prefill_varlen_backward", dev, stream,
+            n_docs, T, H, HEAD_DIM, HEAD_DIM, _P(cu_seqlens_host.data_ptr()), _ptr(cu_seqlens),
+            _ptr(q), q.stride(0), _ptr(k), k.stride(0), _ptr(v), v.stride(0),
+            _ptr(g_raw), g_raw.stride(0), _ptr(beta_raw), beta_raw.stride(0),
+            _ptr(A_log), _ptr(dt_bias), float(lower_bound), float(scale), int(gate_mode),
+            _state_dtype(state_pool), _ptr(state_pool) if N else _P(0), N, slot_stride,
+            _ptr(state_indices), 1 if use_initial_state else 0, _ptr(d_out), d_out.stride(0),
+            _ptr(d_final_state), _ptr(dq), dq.stride(0), _ptr(dk), dk.stride(0),
+            _ptr(dv), dv.stride(0), _ptr(dg), dg.stride(0), _ptr(dbeta), dbeta.stride(0),
+            _ptr(dA_log), _ptr(ddt_bias), _ptr(d_initial_state), _ptr(workspace), ws_bytes)
 
 
 def _vectors(name, t, rows, heads, width):

@@ -1,0 +1,450 @@
+"""kda_prefill_varlen_backward: host validation (CPU) and parity with automatic
+differentiation of the token recurrence in 64 bits (GPU).
+
+Tolerances. The kernels compute in fp32: every product sums at most 128 terms, and a
+decay weight is an exponential of a sum of at most 16 gates within +-88, so its
+relative error stays under 100 * 2^-24 = 6e-6; a gradient passes through fewer than
+ten such factors. dq, dk and dg then subtract parts of similar size, so the error is
+relative to the largest gradient of the document and head, not to the element:
+1e-4 of it. bf16 outputs add half a step, 2^-8 of the element. fp32 outputs:
+the state gradient 1e-5 of the largest element; dA_log and ddt_bias 2e-5 of
+the sum of their terms' magnitudes.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_step_amd as kda
+
+OK, NULLP, SHAPE, STRIDE, UNSUP, SEQ, WS = range(7)
+BF, D = torch.bfloat16, 128
+PRE, PRESIG, HEAD = 1, 2, 4
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.LIB_PATH):
+        from gated_delta_rule_step_amd import build
+        build.build()
+    return kda.lib()
+
+
+# ---------------------------------------------------------------------------
+# refusals: every call returns before anything is launched (made-up pointers)
+
+def _call(lib, **kw):
+    a = dict(n=2, T=30, H=3, K=128, V=128, cu=(0, 10, 30), cud=4096, q=4096, k=4096, v=4096,
+             g=4096, b=4096, al=4096, dt=4096, lb=-5.0, sc=1.0, gm=0, sd=0, pool=4096, N=4,
+             ss=3 * 16384, idx=4096, ui=1, do=4096, df=0, dq=4096, dk=4096, dv=4096, dg=4096,
+             db=4096, da=4096, dd=4096, di=4096, ws=4096, wb=1 << 40,
+             s=(384,) * 4 + (3,), os=(384,) * 4 + (3,), dos=384)
+    a.update(kw)
+    P = ctypes.c_void_p
+    cu = (ctypes.c_int32 * len(a["cu"]))(*a["cu"]) if a["cu"] else None
+    s, o = a["s"], a["os"]
+    return lib.kda_prefill_varlen_backward(
+        a["n"], a["T"], a["H"], a["K"], a["V"], cu, P(a["cud"]), P(a["q"]), s[0], P(a["k"]), s[1],
+        P(a["v"]), s[2], P(a["g"]), s[3], P(a["b"]), s[4], P(a["al"]), P(a["dt"]), a["lb"],
+        a["sc"], a["gm"], a["sd"], P(a["pool"]), a["N"], a["ss"], P(a["idx"]), a["ui"], P(a["do"]),
+        a["dos"], P(a["df"]), P(a["dq"]), o[0], P(a["dk"]), o[1], P(a["dv"]), o[2], P(a["dg"]),
+        o[3], P(a["db"]), o[4], P(a["da"]), P(a["dd"]), P(a["di"]), P(a["ws"]), a["wb"], P(0))
+
+
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(n=-1)), (SHAPE, dict(T=-1)), (SHAPE, dict(H=0)), (SHAPE, dict(N=-1)),
+    (UNSUP, dict(K=64)), (UNSUP, dict(V=64)), (UNSUP, dict(H=70000)), (UNSUP, dict(lb=-6.0)),
+    (UNSUP, dict(lb=float("nan"))), (UNSUP, dict(gm=8)), (UNSUP, dict(gm=PRE)),
+    (UNSUP, dict(gm=PRE, da=0, dd=0, lb=1.0)), (UNSUP, dict(sd=3)), (UNSUP, dict(sd=-1)),
+    (UNSUP, dict(di=4100)), (UNSUP, dict(ws=4100)),
+    (NULLP, dict(cu=None)), (NULLP, dict(cud=0)), (NULLP, dict(q=0)), (NULLP, dict(do=0)),
+    (NULLP, dict(dbeta=0, db=0)), (NULLP, dict(al=0)), (NULLP, dict(idx=0)),
+    (NULLP, dict(pool=0)), (NULLP, dict(ws=0)),
+    (SEQ, dict(cu=(1, 10, 30))), (SEQ, dict(cu=(0, 31, 30))), (SEQ, dict(cu=(0, 10, 29))),
+    (STRIDE, dict(s=(-1, 384, 384, 384, 3))), (STRIDE, dict(dos=-1)),
+    (STRIDE, dict(os=(383, 384, 384, 384, 3))), (STRIDE, dict(os=(384, 384, 384, 384, 2))),
+    (STRIDE, dict(os=(384, 384, 384, 100, 3))), (STRIDE, dict(ss=100)),
+    (WS, dict(wb=1000)),
+    (OK, dict(n=0, T=0, cu=(0,), da=0, dd=0)),
+])
+def test_refusals(lib, want, kw):
+    assert _call(lib, **kw) == want
+
+
+def test_workspace_size(lib):
+    size = kda.kda_prefill_backward_workspace_size
+    per = size(1, 0, 1)
+    assert per > 0 and size(1, 64, 1) == 2 * per and size(3, 127, 5) == 4 * 5 * per
+    assert size(0, 0, 1) == 0 and size(-1, 5, 1) == 0 and size(1, 5, 0) == 0
+    assert lib.kda_prefill_backward_workspace_size(1, 64, 1, 64, 128) == 0
+
+
+# ---------------------------------------------------------------------------
+# the recurrence in 64 bits, token by token, and its derivative by autograd
+
+def make(lens, H, gate=0, seed=0, state=None, dfinal=False, scale=0.3, lb=-5.0, idx=None,
+         spread=False):
+    g = torch.Generator().manual_seed(seed)
+    T, W, n = sum(lens), H * D, len(lens)
+
+    def rnd(*shape):
+        return torch.randn(*shape, generator=g)
+
+    gw = H if gate & HEAD else W
+    c = dict(lens=lens, H=H, gate=gate, scale=scale, lb=lb)
+    for name in ("q", "k", "v", "do"):
+        c[name] = rnd(T, W).to(BF)
+    if gate & PRE:
+        x = torch.rand(T, gw, generator=g) * 5.6 - 5.1
+        c["g"] = torch.where(torch.rand(T, gw, generator=g) < 0.6, x * 0.03, x).to(BF)
+    else:
+        c["g"] = (rnd(T, gw) * (4.0 if spread else 1.0)).to(BF)
+    c["b"] = (torch.rand(T, H, generator=g) if gate & PRESIG else rnd(T, H)).to(BF)
+    c["A"] = torch.rand(H, generator=g) * 2 - 1
+    c["dt"] = 0.1 * rnd(gw)
+    N = n + 2
+    c["pool"] = (0.2 * rnd(N, H, D, D)).to(state or BF)
+    c["ui"] = state is not None
+    c["idx"] = torch.randperm(N, generator=g)[:n].to(torch.int32) if idx is None \
+        else torch.tensor(idx, dtype=torch.int32)
+    c["df"] = rnd(n, H, D, D) if dfinal else None
+    return c
+
+
+def forward64(c, q, k, v, g, b, A, dt, S0):
+    """Outputs [T, H, 128] and final states, differentiable."""
+    H, gate = c["H"], c["gate"]
+    T = q.shape[0]
+    q, k, v = (x.reshape(T, H, D) for x in (q, k, v))
+    q = q / torch.sqrt(q.pow(2).sum(-1, keepdim=True) + 1e-6)
+    k = k / torch.sqrt(k.pow(2).sum(-1, keepdim=True) + 1e-6)
+    g = g.reshape(T, H, -1)
+    if gate & PRE:
+        g = g.clamp(c["lb"], 0.0)
+    else:
+        x = g + dt.reshape(H, -1)
+        g = (-torch.exp(A)[:, None] * torch.where(x > 20, x, torch.log1p(torch.exp(x)))) \
+            .clamp(min=c["lb"])
+    a = torch.exp(g.expand(T, H, D))
+    b = b if gate & PRESIG else torch.sigmoid(b)
+    outs, finals, t = [], [], 0
+    for d, n in enumerate(c["lens"]):
+        S = S0[d]
+        for _ in range(n):
+            S = S * a[t][:, None]
+            u = b[t][:, None] * (v[t] - (S * k[t][:, None]).sum(-1))
+            S = S + u[:, :, None] * k[t][:, None]
+            outs.append(c["scale"] * (S * q[t][:, None]).sum(-1))
+            t += 1
+        finals.append(S)
+    return (torch.stack(outs) if outs else v.new_zeros(0, H, D)), torch.stack(finals)
+
+
+def reference(c):
+    n, H = len(c["lens"]), c["H"]
+    ins = [c[x].double().requires_grad_() for x in ("q", "k", "v", "g", "b", "A", "dt")]
+    N = c["pool"].shape[0]
+    act = [0 <= int(i) < N for i in c["idx"]]
+    S0 = torch.zeros(n, H, D, D, dtype=torch.float64)
+    if c["ui"]:
+        for d in range(n):
+            if act[d]:
+                S0[d] = c["pool"][int(c["idx"][d])].double()
+    S0.requires_grad_()
+    out, fin = forward64(c, *ins, S0)
+    w = torch.cat([torch.full((x,), float(a)) for x, a in zip(c["lens"], act)]) \
+        if sum(c["lens"]) else torch.zeros(0)
+    loss = (out * c["do"].double().reshape(out.shape) * w.reshape(-1, 1, 1)).sum()
+    if c["df"] is not None:
+        loss = loss + (fin * c["df"].double() * torch.tensor(act).double()
+                       .reshape(-1, 1, 1, 1)).sum()
+    if loss.requires_grad:
+        loss.backward()
+    gr = [x.grad if x.grad is not None else torch.zeros_like(x) for x in ins]
+    return gr, (S0.grad if S0.grad is not None else torch.zeros_like(S0))
+
+
+def run(c, pad=0, off=0, stream=None, workspace=None, want_di=True):
+    def dev(t, like=False):
+        rows, w = t.shape
+        buf = torch.full((off + max(rows, 1) * (w + pad),), -7.0, dtype=t.dtype, device="cuda")
+        view = buf[off:].as_strided((rows, w), (w + pad, 1))
+        if not like:
+            view.copy_(t)
+        return view
+
+    lens, H = c["lens"], c["H"]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    pre = bool(c["gate"] & PRE)
+    o = {n: dev(c[m], like=True) for n, m in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"),
+                                             ("db", "b"))}
+    o["dA"] = None if pre else torch.empty(H, device="cuda")
+    o["ddt"] = None if pre else torch.empty(c["dt"].numel(), device="cuda")
+    o["dS"] = torch.empty(len(lens), H, D, D, device="cuda") if want_di else None
+    kda.kda_prefill_varlen_backward(
+        cu, cu.cuda(), dev(c["q"]), dev(c["k"]), dev(c["v"]), dev(c["g"]), dev(c["b"]),
+        None if pre else c["A"].cuda(), None if pre else c["dt"].cuda(), c["pool"].cuda(),
+        c["idx"].cuda(), dev(c["do"]), o["dq"], o["dk"], o["dv"], o["dg"], o["db"],
+        dA_log=o["dA"], ddt_bias=o["ddt"],
+        d_final_state=None if c["df"] is None else c["df"].cuda(), d_initial_state=o["dS"],
+        workspace=workspace, use_initial_state=c["ui"], lower_bound=c["lb"], scale=c["scale"],
+        gate_mode=c["gate"], stream=stream)
+    return o
+
+
+def close_rows(name, got, ref, lens, H):
+    """bf16 rows: 2^-8 of the element plus 1e-4 of the document and head's largest."""
+    got, ref = got.double().cpu().reshape(ref.shape[0], H, -1), ref.reshape(ref.shape[0], H, -1)
+    t = 0
+    for d, n in enumerate(lens):
+        g, r = got[t:t + n], ref[t:t + n]
+        if n:
+            top = r.abs().amax((0, 2), keepdim=True)
+            bad = ~((g - r).abs() <= 2.0 ** -8 * r.abs() + 1e-4 * top)
+            assert not bad.any(), f"{name}, document {d}: {int(bad.sum())} of {bad.numel()}, " \
+                f"first {bad.nonzero()[0].tolist()}, worst {float((g - r).abs().max()):.3e} of " \
+                f"{float(top.max()):.3e}"
+        t += n
+
+
+def compare(c, o):
+    lens, H = c["lens"], c["H"]
+    torch.cuda.synchronize()
+    gr, dS = reference(c)
+    for name, r in zip(("dq", "dk", "dv", "dg", "db"), gr):
+        close_rows(name, o[name], r, lens, H)
+    if o["dA"] is not None:
+        # terms of dA_log: dg_t g_t; of ddt_bias: the gate logits' gradients
+        mag = gr[3].abs().reshape(-1, c["dt"].numel()).sum(0)
+        assert ((o["ddt"].double().cpu() - gr[6]).abs() <= 2e-5 * mag + 1e-30).all()
+        x = c["g"].double() + c["dt"].double()
+        ratio = torch.log1p(torch.exp(x)) / torch.sigmoid(x)
+        mag = (gr[3] * ratio).abs().reshape(-1, H, c["dt"].numel() // H).sum((0, 2))
+        assert ((o["dA"].double().cpu() - gr[5]).abs() <= 2e-5 * mag + 1e-30).all()
+    if o["dS"] is not None:
+        top = dS.abs().amax((2, 3), keepdim=True)
+        assert ((o["dS"].double().cpu() - dS).abs() <= 1e-5 * top).all()
+
+
+# lengths around the 16-token blocks and the 64-token chunks
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [(1,), (2,), (15,), (16,), (17,), (63,), (64,), (65,), (128,),
+                                  (129, 1), (20, 13), (0, 5, 0, 64, 0), (200, 64, 3)], ids=str)
+def test_lengths(lens):
+    c = make(lens, H=2, seed=sum(lens))
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", range(8))
+@pytest.mark.parametrize("state,dfinal", [(None, False), (BF, True)])
+def test_gates(gate, state, dfinal):
+    c = make((70, 9), H=3, gate=gate, seed=gate + 10, state=state, dfinal=dfinal)
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("state", [BF, torch.float16, torch.float8_e4m3fn], ids=str)
+def test_state_types_strides_and_inactive(state):
+    # slots: one shared by two documents, one below and one past the pool
+    c = make((40, 33, 70, 5), H=2, seed=3, state=state, dfinal=True, idx=(1, -1, 1, 6))
+    o = run(c, pad=3, off=1)
+    compare(c, o)
+    dead = torch.cat([o["dq"][40:73], o["dk"][143:], o["dg"][40:73]])
+    assert (dead.view(torch.int16) == 0).all()  # +0.0
+    assert (o["dS"][1] == 0).all() and (o["dS"][3] == 0).all()
+    for n in ("dq", "dk", "dv", "dg", "db"):  # the padding between rows stays
+        v = o[n]
+        rows, w = v.shape
+        gaps = v.as_strided((rows - 1, 3), (w + 3, 1), v.storage_offset() + w)
+        assert (gaps == -7.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lb,spread", [(-5.0, True), (-5.5, True), (0.0, False), (-0.01, False)])
+def test_gate_extremes(lb, spread):
+    """Gates that hit the clamp for whole runs of tokens, and hardly any decay."""
+    c = make((90, 20), H=2, seed=5, lb=lb, spread=spread)
+    compare(c, run(c))
+    c = make((90, 20), H=2, gate=PRE, seed=6, lb=lb)
+    c["g"][10:40] = -20.0   # below the bound: no gradient
+    c["g"][50:60] = 0.0     # exactly at the upper border: passes
+    c["g"][60:70] = 0.5
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+def test_gates_at_the_bound_for_whole_blocks():
+    """Every gate at -5.5: 88 per block, the largest factors."""
+    c = make((64, 30), H=1, gate=PRE, seed=7, lb=-5.5, state=BF, dfinal=True)
+    c["g"][:] = -5.5
+    c["g"][16] = 0.0  # one token that keeps the block before it
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+def test_degenerate_inputs():
+    """Zero keys and queries, beta of zero and one, a repeated key."""
+    c = make((80,), H=2, gate=PRESIG, seed=8)
+    c["q"][3] = 0
+    c["k"][5] = 0
+    c["b"][7:20] = 0.0
+    c["b"][20:30] = 1.0
+    c["k"][30:40] = c["k"][30]
+    o = run(c)
+    torch.cuda.synchronize()
+    gr, _ = reference(c)
+    # the norm of an all-zero row has the slope 1 / sqrt(1e-6) = 1000, so those rows dwarf
+    # the others: they are compared apart
+    for name, r, rows in (("dq", gr[0], [3]), ("dk", gr[1], [5])):
+        got = o[name].double().cpu()
+        keep = [t for t in range(80) if t not in rows]
+        for sel in (rows, keep):
+            close_rows(name, got[sel], r[sel], (len(sel),), 2)
+    for name, r in zip(("dv", "dg", "db"), gr[2:5]):
+        close_rows(name, o[name], r, c["lens"], 2)
+
+
+@pytest.mark.gpu
+def test_no_tokens():
+    c = make((0, 0), H=2, seed=9, state=BF, dfinal=True)
+    o = run(c)
+    torch.cuda.synchronize()
+    assert torch.equal(o["dS"].cpu(), c["df"])
+    assert (o["dA"] == 0).all() and (o["ddt"] == 0).all()
+
+
+@pytest.mark.gpu
+def test_many_documents():
+    """More documents than the ordered launch holds."""
+    lens = tuple([3, 0, 17, 1] * 70)
+    c = make(lens, H=1, seed=10)
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+def test_long_document_against_its_halves():
+    """One document of 1500 tokens equals its two parts run apart, the state passed up
+    and its gradient passed down, within the fp32 arithmetic: the parts' boundary (700)
+    is no multiple of the chunk."""
+    H, cut = 4, 700
+    c = make((1500,), H=H, seed=11, state=BF, dfinal=True)
+    whole = run(c)
+    # the state after `cut` tokens, in 64 bits, handed on through an fp16 pool
+    a = {k: (v[:cut] if k in ("q", "k", "v", "do", "g", "b") else v) for k, v in c.items()}
+    b = {k: (v[cut:] if k in ("q", "k", "v", "do", "g", "b") else v) for k, v in c.items()}
+    a["lens"], b["lens"] = (cut,), (1500 - cut,)
+    with torch.no_grad():
+        S0 = c["pool"][c["idx"].long()].double()
+        _, S = forward64(a, *(a[x].double() for x in ("q", "k", "v", "g", "b", "A", "dt")), S0)
+    b["pool"], b["idx"] = S.to(torch.float16), torch.zeros(1, dtype=torch.int32)
+    second = run(b)
+    a["df"] = second["dS"].cpu()
+    first = run(a)
+    torch.cuda.synchronize()
+    # fp16 rounds the state by 2^-11 of each element (random signs): the second
+    # part's gradients move by about that much of their size, normwise
+    for n in ("dq", "dk", "dv", "dg", "db"):
+        w = whole[n].double().cpu()
+        both = torch.cat([first[n], second[n]]).double().cpu()
+        assert (w - both).norm() <= (2.0 ** -8 + 2.0 ** -10) * w.norm()
+    assert (first["dS"] - whole["dS"]).norm() <= 2.0 ** -10 * whole["dS"].norm()
+
+
+@pytest.mark.gpu
+def test_against_differences_of_the_forward_kernel():
+    """The gradient along a random direction of v (the output is linear in v up to
+    rounding) and of the state, against kda_prefill_varlen itself."""
+    H, lens = 2, (75, 30)
+    c = make(lens, H=H, seed=12, state=torch.float16)
+    o = run(c)
+    cu = torch.tensor([0, 75, 105], dtype=torch.int32)
+
+    def out_of(v):
+        out = torch.empty(105, H * D, dtype=BF, device="cuda")
+        kda.kda_prefill_varlen(cu, cu.cuda(), c["q"].cuda(), c["k"].cuda(), v.cuda(),
+                               c["g"].cuda(), c["b"].cuda(), c["A"].cuda(), c["dt"].cuda(),
+                               c["pool"].cuda(), c["idx"].cuda(), out, lower_bound=c["lb"],
+                               scale=c["scale"])
+        return out.double().cpu()
+
+    dv = 4 * torch.randn(c["v"].shape, generator=torch.Generator().manual_seed(1))
+    up, down = (c["v"].float() + dv).to(BF), (c["v"].float() - dv).to(BF)
+    diff = (out_of(up) - out_of(down)) * c["do"].double()
+    slope = (o["dv"].double().cpu() * (up.double() - down.double())).sum()
+    # forward outputs are rounded to bf16 with up to 5e-3 of error normwise
+    assert abs(diff.sum() - slope) <= 1e-2 * diff.norm() + 1e-2 * abs(slope)
+
+
+@pytest.mark.gpu
+def test_same_bits_workspace_and_stream():
+    """Twice the same bits, on a side stream too, whatever the workspace held."""
+    c = make((300, 64, 130), H=5, seed=13, state=BF, dfinal=True)
+    need = kda.kda_prefill_backward_workspace_size(3, 494, 5)
+    a = run(c)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    b = run(c, workspace=ws)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    d = run(c, workspace=ws, stream=s)
+    s.synchronize()
+    for n, x in a.items():
+        assert torch.equal(x, b[n]) and torch.equal(x, d[n]), n
+    no = run(c, want_di=False)
+    torch.cuda.synchronize()
+    assert torch.equal(no["dq"], a["dq"])
+
+
+@pytest.mark.gpu
+def test_captured():
+    """Two captured calls with a workspace each, replayed with changed inputs and eager
+    calls between."""
+    H, T = 3, 150
+    cases = [make((100, 50), H=H, seed=20 + i) for i in range(3)]
+    cu = torch.tensor([0, 100, 150], dtype=torch.int32)
+    ins = {n: cases[0][n].cuda() for n in ("q", "k", "v", "g", "b", "do", "A", "dt", "pool", "idx")}
+    cud = cu.cuda()
+    need = kda.kda_prefill_backward_workspace_size(2, T, H)
+
+    def call(ws):
+        o = [torch.empty_like(ins[n]) for n in ("q", "k", "v", "g", "b", "A", "dt")]
+        kda.kda_prefill_varlen_backward(
+            cu, cud, ins["q"], ins["k"], ins["v"], ins["g"], ins["b"], ins["A"], ins["dt"],
+            ins["pool"], ins["idx"], ins["do"], *o[:5], dA_log=o[5], ddt_bias=o[6], workspace=ws,
+            use_initial_state=False, scale=0.3)
+        return o
+
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    call(ws[2])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(ws[i]))
+        graphs.append(g)
+    for c in cases:
+        for n, t in ins.items():
+            t.copy_(c[n])
+        for g in graphs:
+            g.replay()
+        eager = call(ws[2])
+        torch.cuda.synchronize()
+        for o in outs:
+            for x, y in zip(o, eager):
+                assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_binding_refuses():
+    c = make((10,), H=2, seed=1)
+    c["b"] = c["b"][:, :1]
+    with pytest.raises(ValueError, match="beta_raw"):
+        run(c)
+    c = make((10,), H=2, seed=1)
+    with pytest.raises(kda.KdaError):
+        run(c, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
