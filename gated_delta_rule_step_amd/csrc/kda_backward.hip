@@ -92,7 +92,7 @@ struct BwdParams {
   float* dA_log;
   float* ddt_bias;
   float* d_initial;
-  float* ops;      // [slot][h][kOps]
+  uint8_t* ops;    // [slot][h][kOps]
   float* partial;  // [slot][h][2][D]: of ddt_bias and dA_log, per channel
 };
 
@@ -101,20 +101,25 @@ struct DocOrder {
   int32_t doc[kMaxOrderedDocs];
 };
 
-// A (chunk, head)'s part of the workspace, fp32 elements. Operands that an MFMA
-// reads as its left side are in fragment order [tile][tile][lane][4].
-constexpr int kTile = C * D;
-constexpr int kOpW = 0;              // -T e^G k       [rt 4][m 8][lane][4 channels]
-constexpr int kOpKE = kTile;         // beta e^(Gl-G) k [m 8][rt 4][lane][4 tokens]
-constexpr int kOpZ = 2 * kTile;      // T^T (beta e^(Gl-G) k), as W
-constexpr int kOpKG = 3 * kTile;     // -e^G k, as KE
-constexpr int kOpQG = 4 * kTile;     // e^G q', as KE
-constexpr int kOpX = 5 * kTile;      // T V, then x [token][value]
-constexpr int kOpDV = 6 * kTile;     // T^T P^T dO, then dV [token][value]
-constexpr int kOpS = 7 * kTile;      // S [key][value] entering the chunk
-constexpr int kOpDS = kOpS + D * D;  // dS [key][value] leaving it
-constexpr int kOpEG = kOpDS + D * D; // e^Gl [key]
-constexpr int kOps = kOpEG + D;
+// A (chunk, head)'s part of the workspace, in bytes. The chains' left operands are
+// fp16 high and low parts in fragment order, 16 bytes (8 contraction indices) a lane:
+//   W, Z        [rt 4][kt 4][hi, lo][lane]  token 16 rt + lane % 16, key channels
+//               32 kt + 4 (lane / 16) + 0..3 and 16 further
+//   KE, KG, QG  [m 8][t 2][hi, lo][lane]    key channel 16 m + lane % 16, tokens
+//               32 t + 4 (lane / 16) + 0..3 and 16 further
+// X and DV are accumulator tiles [vt 8][rt 4][lane][4 tokens].
+constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales of W and Z
+constexpr int kOpW = 1024;               // T e^G k, scaled
+constexpr int kOpKE = kOpW + 32768;      // e^(Gl-G) k, times 2^12
+constexpr int kOpZ = kOpKE + 32768;      // T^T (beta e^(Gl-G) k), scaled
+constexpr int kOpKG = kOpZ + 32768;      // e^G k, times 2^12
+constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat, times 2^12
+constexpr int kOpX = kOpQG + 32768;      // T V, then x
+constexpr int kOpDV = kOpX + 32768;      // T^T P^T dO, then dV
+constexpr int kOpS = kOpDV + 32768;      // S [key][value] entering the chunk
+constexpr int kOpDS = kOpS + 65536;      // dS [key][value] leaving it
+constexpr int kOps = kOpDS + 65536;
+constexpr int kTailBeta = D, kTailUnW = D + C, kTailUnZ = D + C + 1;  // in floats
 
 __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
 #pragma unroll
@@ -129,6 +134,33 @@ __device__ __forceinline__ f32x4 col4(const float* p, int stride) {
 }
 
 typedef u32x4 u32x4_u __attribute__((aligned(2)));  // any bf16 address
+typedef __fp16 f16x8 __attribute__((__vector_size__(8 * sizeof(__fp16))));  // MFMA operand
+
+// fp32 as fp16 high + low parts: 22 bits and a sign. Three products (high high,
+// high low, low high) then leave out 2^-22 of a term, less than the fp32 additions.
+__device__ __forceinline__ void split4h(f32x4 x, u32x2& hi, u32x2& lo) {
+  hi = u32x2{pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3])};
+  lo = u32x2{pack_f16x2(x[0] - f16_lo(hi[0]), x[1] - f16_hi(hi[0])),
+             pack_f16x2(x[2] - f16_lo(hi[1]), x[3] - f16_hi(hi[1]))};
+}
+__device__ __forceinline__ f16x8 join8(u32x2 a, u32x2 b) {
+  return __builtin_bit_cast(f16x8, u32x4{a[0], a[1], b[0], b[1]});
+}
+__device__ __forceinline__ f32x4 mfma32(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// fp16 holds 2^-24 to 2^16, so operands of any size are scaled by a power of two that
+// brings their largest magnitude to 2^14 .. 2^15; `un` undoes it.
+struct Scale {
+  float up, un;
+};
+__device__ __forceinline__ Scale scale_for(float top) {
+  int e = int(__float_as_uint(top) >> 23);
+  e = e < 40 ? 40 : (e > 250 ? 250 : e);
+  return {__uint_as_float(uint32_t(268 - e) << 23), __uint_as_float(uint32_t(e - 14) << 23)};
+}
+constexpr float kFixedUp = 4096.0f, kFixedUn = 1.0f / 4096.0f;  // operands within +-1
 
 // Sum over the four 16-lane rows of a wave (lanes of equal lane % 16).
 __device__ __forceinline__ float rows_sum(float x) {
@@ -173,42 +205,49 @@ __device__ __forceinline__ Chunk chunk_of(const BwdParams& p, int64_t sigma) {
   return ch;
 }
 
+// Here and below a chunk's missing tokens read its last one and drop the value: a
+// load behind a branch would be waited for one at a time.
+
 // 1 / |q|, 1 / |k| (with the epsilon) and beta of the chunk's tokens, to LDS: 16
 // lanes per token. Padding rows get zeros.
-__device__ void token_scalars(const BwdParams& p, const Chunk& ch, int h, float* rq, float* rk,
-                              float* beta) {
+__device__ __forceinline__ void token_scalars(const BwdParams& p, const Chunk& ch, int h,
+                                              float* rq, float* rk, float* beta) {
+  constexpr int N = C / (kThreads / 16);
   const int c0 = (threadIdx.x & 15) * 8;
-  for (int t = threadIdx.x >> 4; t < C; t += kThreads / 16) {
-    float sq = 0.f, sk = 0.f;
-    if (t < ch.c) {
-      float x[8];
-      unpack8_bf16(*reinterpret_cast<const u32x4_u*>(p.q + (ch.t0 + t) * p.q_stride + h * D + c0),
-                   x);
+  u32x4 qw[N], kw[N];
+  uint16_t bw[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-      unpack8_bf16(*reinterpret_cast<const u32x4_u*>(p.k + (ch.t0 + t) * p.k_stride + h * D + c0),
-                   x);
+  for (int j = 0; j < N; ++j) {
+    const int64_t t = ch.t0 + min(int(threadIdx.x >> 4) + j * (kThreads / 16), ch.c - 1);
+    qw[j] = *reinterpret_cast<const u32x4_u*>(p.q + t * p.q_stride + h * D + c0);
+    kw[j] = *reinterpret_cast<const u32x4_u*>(p.k + t * p.k_stride + h * D + c0);
+    bw[j] = p.beta[t * p.beta_stride + h];
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sk = fmaf(x[i], x[i], sk);
-    }
+  for (int j = 0; j < N; ++j) {
+    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+    float x[8], sq = 0.f, sk = 0.f;
+    unpack8_bf16(qw[j], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+    unpack8_bf16(kw[j], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sk = fmaf(x[i], x[i], sk);
     sq = row16_sum(sq);
     sk = row16_sum(sk);
     if ((threadIdx.x & 15) == 0) {
+      float b = bf1(bw[j]);
+      if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) b = sigmoidf(b);
       rq[t] = t < ch.c ? 1.0f / sqrtf(sq + kL2Eps) : 0.f;
       rk[t] = t < ch.c ? 1.0f / sqrtf(sk + kL2Eps) : 0.f;
-      float b = 0.f;
-      if (t < ch.c) {
-        b = bf1(p.beta[(ch.t0 + t) * p.beta_stride + h]);
-        if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) b = sigmoidf(b);
-      }
-      beta[t] = b;
+      beta[t] = t < ch.c ? b : 0.f;
     }
   }
 }
 
 // A lane's share of the chunk: key channel `kc`, tokens 16 b + 4 g4 + i.
 struct Lane {
-  float k[NB][4], q[NB][4];      // k_hat, q'
+  float k[NB][4], q[NB][4];      // k_hat, q_hat
   float g[NB][4], slope[NB][4];  // log-decay and its derivative by the gate input
   float lam[NB][4];              // log-decay summed from the block's first token
   float tau[NB];                 // the block's total
@@ -222,27 +261,37 @@ __device__ __forceinline__ void load_lane(const BwdParams& p, const Chunk& ch, i
   const int64_t gch = head ? h : int64_t(h) * D + kc;
   const float ea = pre ? 0.f : expf(p.A_log[h]);
   const float dtb = pre ? 0.f : p.dt_bias[gch];
+  uint16_t kw[NB][4], qw[NB][4], gw[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = ch.t0 + min(16 * b + 4 * g4 + i, ch.c - 1);
+      kw[b][i] = p.k[t * p.k_stride + h * D + kc];
+      qw[b][i] = p.q[t * p.q_stride + h * D + kc];
+      gw[b][i] = p.g[t * p.g_stride + gch];
+    }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * b + 4 * g4 + i;
-      float k = 0.f, q = 0.f, g = 0.f, s = 0.f;
-      if (t < ch.c) {
-        k = bf1(p.k[(ch.t0 + t) * p.k_stride + h * D + kc]) * rk[t];
-        q = bf1(p.q[(ch.t0 + t) * p.q_stride + h * D + kc]) * rq[t] * p.scale;
-        const float x = bf1(p.g[(ch.t0 + t) * p.g_stride + gch]);
-        if (pre) {
-          g = gate_given(x, p.lower_bound);
-          s = x >= p.lower_bound && x <= 0.f ? 1.f : 0.f;
-        } else {
-          const float y = x + dtb;
-          const float gu = -ea * (y > 20.f ? y : log1pf(expf(y)));
-          g = fmaxf(gu, p.lower_bound);
-          if (SLOPE) s = gu >= p.lower_bound ? -ea * sigmoidf(y) : 0.f;
-        }
+      const bool valid = t < ch.c;
+      const float k = valid ? bf1(kw[b][i]) * rk[t] : 0.f;
+      const float q = valid ? bf1(qw[b][i]) * rq[t] : 0.f;
+      const float x = bf1(gw[b][i]);
+      float g, s = 0.f;
+      if (pre) {
+        g = gate_given(x, p.lower_bound);
+        s = x >= p.lower_bound && x <= 0.f ? 1.f : 0.f;
+      } else {
+        const float y = x + dtb;
+        const float gu = -ea * (y > 20.f ? y : log1pf(expf(y)));
+        g = fmaxf(gu, p.lower_bound);
+        if (SLOPE) s = gu >= p.lower_bound ? -ea * sigmoidf(y) : 0.f;
       }
+      if (!valid) g = s = 0.f;
       ln.k[b][i] = k;
       ln.q[b][i] = q;
       if constexpr (SLOPE) {
@@ -275,6 +324,7 @@ struct PrepSmem {
   float pm[C * AS];    // P
   float tm[C * AS];    // T
   float pair[NP * D];  // factor of a block pair
+  float top[2][8];     // largest magnitudes of W and Z, per wave
   float rq[C], rk[C], beta[C];
 };
 constexpr int VS = 2 * RS;  // row of V and dO in uint16: V first, dO from RS on
@@ -289,10 +339,12 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g4 = lane >> 4, n16 = lane & 15;
   const int kc = 16 * w + n16;
-  float* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
+  uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
+  float* tail = reinterpret_cast<float*>(ops + kOpTail);
 
   token_scalars(p, ch, h, s.rq, s.rk, s.beta);
   __syncthreads();
+  if (threadIdx.x < C) tail[kTailBeta + threadIdx.x] = s.beta[threadIdx.x];
 
   // ---- the decayed rows, and what depends on them channel by channel alone
   f32x4 kg[NB], ke[NB];  // e^G k, beta e^(Gl-G) k: 4 tokens of channel kc
@@ -313,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
       e += ln.tau[b];
     }
     if (g4 == 0) {
-      ops[kOpEG + kc] = expf(o);
+      tail[kc] = expf(o);
 #pragma unroll
       for (int I = 1; I < NB; ++I) {
         float mid = 0.f;
@@ -327,25 +379,33 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const float ef = expf(from[b]), et = expf(to[b]);
-      f32x4 qg;
+      f32x4 qg, kee;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * b + 4 * g4 + i;
         const float x = ln.lam[b][i] - 0.5f * ln.tau[b];
         const float up = expf(x), down = expf(-x);
-        const float km = ln.k[b][i] * up, qm = ln.q[b][i] * up;
+        const float km = ln.k[b][i] * up, qm = ln.q[b][i] * up * p.scale;
         const float kb = ln.k[b][i] * down * s.beta[t];
         s.km[t * RS + kc] = km;
         s.qm[t * RS + kc] = qm;
         s.kb[t * RS + kc] = kb;
         kg[b][i] = km * ef;
-        qg[i] = qm * ef;
+        qg[i] = ln.q[b][i] * up * ef;
+        kee[i] = ln.k[b][i] * down * et;
         ke[b][i] = kb * et;
       }
-      const int at = ((w * NB + b) * 64 + lane) * 4;
-      *reinterpret_cast<f32x4*>(ops + kOpKE + at) = ke[b];
-      *reinterpret_cast<f32x4*>(ops + kOpKG + at) = -kg[b];
-      *reinterpret_cast<f32x4*>(ops + kOpQG + at) = qg;
+      const int at = ((w * 2 + (b >> 1)) * 2 * 64 + lane) * 16 + 8 * (b & 1);
+      u32x2 hi, lo;
+      split4h(kee * kFixedUp, hi, lo);
+      *reinterpret_cast<u32x2*>(ops + kOpKE + at) = hi;
+      *reinterpret_cast<u32x2*>(ops + kOpKE + at + 1024) = lo;
+      split4h(kg[b] * kFixedUp, hi, lo);
+      *reinterpret_cast<u32x2*>(ops + kOpKG + at) = hi;
+      *reinterpret_cast<u32x2*>(ops + kOpKG + at + 1024) = lo;
+      split4h(qg * kFixedUp, hi, lo);
+      *reinterpret_cast<u32x2*>(ops + kOpQG + at) = hi;
+      *reinterpret_cast<u32x2*>(ops + kOpQG + at + 1024) = lo;
     }
   }
   __syncthreads();
@@ -400,12 +460,13 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
   {
     uint16_t* vo = reinterpret_cast<uint16_t*>(s.qm);
     const int c0 = (threadIdx.x & 15) * 8;
-    for (int t = threadIdx.x >> 4; t < C; t += kThreads / 16) {
-      u32x4 a = {0u, 0u, 0u, 0u}, b = a;
-      if (t < ch.c) {
-        a = *reinterpret_cast<const u32x4_u*>(p.v + (ch.t0 + t) * p.v_stride + h * D + c0);
-        b = *reinterpret_cast<const u32x4_u*>(p.dout + (ch.t0 + t) * p.dout_stride + h * D + c0);
-      }
+#pragma unroll
+    for (int j = 0; j < C / (kThreads / 16); ++j) {
+      const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+      const int64_t at = ch.t0 + min(t, ch.c - 1);
+      u32x4 a = *reinterpret_cast<const u32x4_u*>(p.v + at * p.v_stride + h * D + c0);
+      u32x4 b = *reinterpret_cast<const u32x4_u*>(p.dout + at * p.dout_stride + h * D + c0);
+      if (t >= ch.c) a = b = u32x4{0u, 0u, 0u, 0u};
       typedef u32x4 u32x4_8 __attribute__((aligned(8)));
       *reinterpret_cast<u32x4_8*>(vo + t * VS + c0) = a;
       *reinterpret_cast<u32x4_8*>(vo + t * VS + RS + c0) = b;
@@ -444,28 +505,42 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
       oo[b][i] = bf1(vo[t * VS + RS + kc]);
     }
   f32x4 y[NB];  // P^T dO
+  f32x4 wt[NB], z[NB];
+  float wtop = 0.f, ztop = 0.f;
+  float* X = reinterpret_cast<float*>(ops + kOpX);
+  float* DV = reinterpret_cast<float*>(ops + kOpDV);
 #pragma unroll
   for (int r = 0; r < NB; ++r) {
-    f32x4 wt = zero4(), xx = zero4(), z = zero4();
-    y[r] = zero4();
+    f32x4 xx = zero4();
+    wt[r] = z[r] = y[r] = zero4();
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if (b <= r) {
         const f32x4 t = lds4(s.tm + (16 * r + n16) * AS + 16 * b + 4 * g4);
-        wt = mfma4(kg[b], t, wt);  // transposed: rows are channels
+        wt[r] = mfma4(kg[b], t, wt[r]);  // transposed: rows are channels
         xx = mfma4(t, vv[b], xx);
       }
       if (b >= r) {
         const int at = (16 * b + 4 * g4) * AS + 16 * r + n16;
-        z = mfma4(ke[b], col4(s.tm + at, AS), z);  // transposed
+        z[r] = mfma4(ke[b], col4(s.tm + at, AS), z[r]);  // transposed
         y[r] = mfma4(col4(s.pm + at, AS), oo[b], y[r]);
       }
     }
-    const int at = ((r * 8 + w) * 64 + lane) * 4;
-    *reinterpret_cast<f32x4*>(ops + kOpW + at) = -wt;
-    *reinterpret_cast<f32x4*>(ops + kOpZ + at) = z;
+    *reinterpret_cast<f32x4*>(X + ((w * NB + r) * 64 + lane) * 4) = xx;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ops[kOpX + (16 * r + 4 * g4 + i) * D + kc] = xx[i];
+    for (int i = 0; i < 4; ++i) {
+      wtop = fmaxf(wtop, fabsf(wt[r][i]));
+      ztop = fmaxf(ztop, fabsf(z[r][i]));
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    wtop = fmaxf(wtop, __shfl_xor(wtop, o));
+    ztop = fmaxf(ztop, __shfl_xor(ztop, o));
+  }
+  if (lane == 0) {
+    s.top[0][w] = wtop;
+    s.top[1][w] = ztop;
   }
 #pragma unroll
   for (int r = 0; r < NB; ++r) {
@@ -473,18 +548,45 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
 #pragma unroll
     for (int b = r; b < NB; ++b)
       d = mfma4(col4(s.tm + (16 * b + 4 * g4) * AS + 16 * r + n16, AS), y[b], d);
+    *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d;
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ops[kOpDV + (16 * r + 4 * g4 + i) * D + kc] = d[i];
+  for (int i = 0; i < 8; ++i) {
+    wtop = fmaxf(wtop, s.top[0][i]);
+    ztop = fmaxf(ztop, s.top[1][i]);
+  }
+  const Scale sw = scale_for(wtop), sz = scale_for(ztop);
+  if (threadIdx.x == 0) {
+    tail[kTailUnW] = sw.un;
+    tail[kTailUnZ] = sz.un;
+  }
+#pragma unroll
+  for (int r = 0; r < NB; ++r) {
+    const int at = ((r * 4 + (w >> 1)) * 2 * 64 + lane) * 16 + 8 * (w & 1);
+    u32x2 hi, lo;
+    split4h(wt[r] * sw.up, hi, lo);
+    *reinterpret_cast<u32x2*>(ops + kOpW + at) = hi;
+    *reinterpret_cast<u32x2*>(ops + kOpW + at + 1024) = lo;
+    split4h(z[r] * sz.up, hi, lo);
+    *reinterpret_cast<u32x2*>(ops + kOpZ + at) = hi;
+    *reinterpret_cast<u32x2*>(ops + kOpZ + at + 1024) = lo;
   }
 }
 
 // ---------------------------------------------------------------------------
 // Chains: the states up each (document, head), and the state gradients down.
-// Value channels do not mix in either, so a wave owns 16 of them, with all 128 key
-// channels in eight accumulator tiles.
-constexpr int kChainWaves = 2;
-constexpr int kParts = D / 16 / kChainWaves;
-
+// Value channels do not mix in either, so a wave owns NT tiles of 16 of them, with
+// all 128 key channels in eight accumulator tiles each, and the chain is sequential
+// over the chunks alone. What bounds it is the latency of one chunk: two products
+// that wait for each other. They run on fp16 MFMA with both sides split into high and
+// low parts (three terms, fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides,
+// which are the state and x in accumulator layout, are scaled per value channel.
+//
+// A chunk's operands come in two tiles (W, then KE; or Z, then KG and QG) that all
+// waves share through LDS. Loads of a tile are issued two phases before it is read
+// and wait in registers in between; the barrier between the phases publishes one
+// tile and frees the other.
 __device__ __forceinline__ float pool_at(const BwdParams& p, int64_t e) {
   if (p.state_dtype == KDA_STATE_FP8)
     return f8x2_lo(static_cast<const uint8_t*>(p.pool)[e])[0];
@@ -492,15 +594,78 @@ __device__ __forceinline__ float pool_at(const BwdParams& p, int64_t e) {
   return p.state_dtype == KDA_STATE_FP16 ? f16_lo(b) : bf1(b);
 }
 
-__global__ __launch_bounds__(64 * kChainWaves) void chain_kernel(BwdParams p, DocOrder ord) {
-  const int64_t chains = int64_t(p.n_docs) * p.H;
-  const int64_t id = int64_t(blockIdx.x) / kParts;
+constexpr int kTileBytes = 32768;
+constexpr int kChainLds = 3 * kTileBytes + 2 * 1024;
+
+// N 16-byte units per thread, from global memory to registers, and on to LDS.
+template <int N, int T>
+struct Stage {
+  u32x4 u[N];
+  __device__ __forceinline__ void load(const uint8_t* src) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      u[i] = *reinterpret_cast<const u32x4*>(src + (i * T + int(threadIdx.x)) * 16);
+  }
+  __device__ __forceinline__ void store(uint8_t* dst) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<u32x4*>(dst + (i * T + int(threadIdx.x)) * 16) = u[i];
+  }
+};
+
+// The largest magnitude of a value channel over the four lanes that share it.
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+
+// Right-side fragments of N accumulator tiles (rows 16 m + 4 g4 + i): pairs of tiles
+// give 32 contraction indices.
+template <int N>
+struct Right {
+  f16x8 hi[N / 2], lo[N / 2];
+  float un;
+  __device__ __forceinline__ void set(const f32x4 (&x)[N]) {
+    float top = 0.f;
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[m][i]));
+    const Scale sc = scale_for(column_max(top));
+    un = sc.un;
+#pragma unroll
+    for (int t = 0; t < N / 2; ++t) {
+      u32x2 h0, l0, h1, l1;
+      split4h(x[2 * t] * sc.up, h0, l0);
+      split4h(x[2 * t + 1] * sc.up, h1, l1);
+      hi[t] = join8(h0, h1);
+      lo[t] = join8(l0, l1);
+    }
+  }
+};
+
+template <int NW, int NT>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, 2)))
+void chain_kernel(BwdParams p, DocOrder ord) {
+  constexpr int T = 64 * NW;
+  constexpr int PARTS = 8 / (NW * NT);
+  constexpr int NA = kTileBytes / 16 / T;
+  extern __shared__ __align__(16) float smem_raw[];
+  uint8_t* la = reinterpret_cast<uint8_t*>(smem_raw);
+  uint8_t* lb = la + kTileBytes;
+  float* tails = reinterpret_cast<float*>(lb + 2 * kTileBytes);  // of even and odd chunks
+
+  // Chain c's parts are blocks (c / 8 * PARTS + part) * 8 + c % 8: blocks go to the
+  // eight XCDs in turn, so the parts share one L2 copy of the operands.
+  const int64_t bid = blockIdx.x;
+  const int64_t id = bid / (8 * PARTS) * 8 + (bid & 7);
+  const int part = int((bid >> 3) % PARTS);
   const bool down = id & 1;
   const int64_t chain = id >> 1;
-  if (chain >= chains) return;
-  const int lane = threadIdx.x & 63;
+  if (chain >= int64_t(p.n_docs) * p.H) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g4 = lane >> 4, n16 = lane & 15;
-  const int v = 16 * (int(blockIdx.x % kParts) * kChainWaves + int(threadIdx.x >> 6)) + n16;
+  const int vt0 = (part * NW + wave) * NT;  // this wave's first value tile
   const int h = int(chain % p.H);
   const int rank = int(chain / p.H);
   const int doc = ord.n > 0 ? ord.doc[rank] : rank;
@@ -509,94 +674,287 @@ __global__ __launch_bounds__(64 * kChainWaves) void chain_kernel(BwdParams p, Do
   const int32_t slot = p.state_indices[doc];
   const bool active = slot >= 0 && int64_t(slot) < p.num_slots;
   const int64_t chunks = (len + C - 1) / C;
-  const int64_t state = (int64_t(doc) * p.H + h) * HEAD_ELEMS + v * D + 4 * g4;
-  float* ops0 = p.ops + (doc_slot0(p.cu_seqlens, doc) * p.H + h) * int64_t(kOps);
+  const int64_t state = (int64_t(doc) * p.H + h) * HEAD_ELEMS + (16 * vt0 + n16) * D + 4 * g4;
   const int64_t step = int64_t(p.H) * kOps;
+  uint8_t* ops0 = p.ops + (doc_slot0(p.cu_seqlens, doc) * p.H + h) * int64_t(kOps);
 
-  f32x4 s[8];  // [key 16 m + 4 g4 + i][value v]
+  f32x4 s[NT][8];  // [key 16 m + 4 g4 + i][value 16 (vt0 + n) + n16]
 #pragma unroll
-  for (int m = 0; m < 8; ++m) s[m] = zero4();
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < 8; ++m) s[n][m] = zero4();
+
+  const uint8_t* left = la + lane * 16;
+  const uint8_t* left2 = lb + lane * 16;
+  auto frag = [](const uint8_t* base, int unit) {
+    return *reinterpret_cast<const f16x8*>(base + unit * 1024);
+  };
+  // acc[r] = sum over keys of tile A's row block r times the state
+  auto product_a = [&](const Right<8> (&b)[NT], f32x4 (&acc)[NT][NB]) {
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+      for (int r = 0; r < NB; ++r) {
+        const f16x8 ah = frag(left, (r * 4 + kt) * 2), al = frag(left, (r * 4 + kt) * 2 + 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (kt == 0) acc[n][r] = zero4();
+          acc[n][r] = mfma32(al, b[n].hi[kt], acc[n][r]);
+          acc[n][r] = mfma32(ah, b[n].lo[kt], acc[n][r]);
+          acc[n][r] = mfma32(ah, b[n].hi[kt], acc[n][r]);
+        }
+      }
+  };
+  // s = e^Gl s + sign * (tile B's first half)^T b, or with the second half on o too
+  auto update = [&](const Right<NB> (&b)[NT], float sign, const f16x8 (*o)[2],
+                    const float* uno, const float* tail) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      f32x4 acc[NT], acc2[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n] = acc2[n] = zero4();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f16x8 ah = frag(left2, (m * 2 + t) * 2), al = frag(left2, (m * 2 + t) * 2 + 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[n] = mfma32(al, b[n].hi[t], acc[n]);
+          acc[n] = mfma32(ah, b[n].lo[t], acc[n]);
+          acc[n] = mfma32(ah, b[n].hi[t], acc[n]);
+        }
+        if (o) {
+          const f16x8 qh = frag(left2, 32 + (m * 2 + t) * 2), ql = frag(left2, 33 + (m * 2 + t) * 2);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc2[n] = mfma32(ql, o[n][t], acc2[n]);
+            acc2[n] = mfma32(qh, o[n][t], acc2[n]);
+          }
+        }
+      }
+      const f32x4 eg = lds4(tail + 16 * m + 4 * g4);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float un = b[n].un * (sign * kFixedUn);
+        s[n][m] *= eg;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][m][i] = fmaf(acc[n][i], un, s[n][m][i]);
+        if (o)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][m][i] = fmaf(acc2[n][i], uno[n], s[n][m][i]);
+      }
+    }
+  };
 
   if (!down) {
     if (!active || len == 0) return;
     if (p.use_initial) {
-      const int64_t e = int64_t(slot) * p.slot_stride + int64_t(h) * HEAD_ELEMS + v * D + 4 * g4;
 #pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[m][i] = pool_at(p, e + 16 * m + i);
-    }
-    for (int64_t n = 0; n < chunks; ++n) {
-      float* ops = ops0 + n * step;
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ops[kOpS + (16 * m + 4 * g4 + i) * D + v] = s[m][i];
-      f32x4 x[NB];
-#pragma unroll
-      for (int r = 0; r < NB; ++r) {
-        x[r] = col4(ops + kOpX + (16 * r + 4 * g4) * D + v, D);
+      for (int n = 0; n < NT; ++n) {
+        const int64_t e = int64_t(slot) * p.slot_stride + int64_t(h) * HEAD_ELEMS +
+                          (16 * (vt0 + n) + n16) * D + 4 * g4;
 #pragma unroll
         for (int m = 0; m < 8; ++m)
-          x[r] = mfma4(lds4(ops + kOpW + ((r * 8 + m) * 64 + lane) * 4), s[m], x[r]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ops[kOpX + (16 * r + 4 * g4 + i) * D + v] = x[r][i];
+          for (int i = 0; i < 4; ++i) s[n][m][i] = pool_at(p, e + 16 * m + i);
       }
-      if (n + 1 == chunks) return;  // the state after the last chunk is not needed
+    }
+    Stage<NA, T> sa, sb;
+    u32x4 st = {0u, 0u, 0u, 0u};
+    auto load_a = [&](int64_t n) {
+      sa.load(ops0 + n * step + kOpW);
+      if (threadIdx.x < 64) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + threadIdx.x * 16);
+    };
+    auto store_a = [&](int64_t n) {
+      sa.store(la);
+      if (threadIdx.x < 64) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + threadIdx.x * 4) = st;
+    };
+    f32x4 x[NT][NB];  // T V of the next chunk, asked for a phase ahead
+    auto load_x = [&](int64_t n) {
+      const float* X = reinterpret_cast<const float*>(ops0 + n * step + kOpX) +
+                       (vt0 * NB * 64 + lane) * 4;
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        s[m] *= lds4(ops + kOpEG + 16 * m + 4 * g4);
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int r = 0; r < NB; ++r)
-          s[m] = mfma4(lds4(ops + kOpKE + ((m * NB + r) * 64 + lane) * 4), x[r], s[m]);
+        for (int r = 0; r < NB; ++r) x[j][r] = lds4(X + (j * NB + r) * 256);
+    };
+    load_a(0);
+    load_x(0);
+    store_a(0);
+    sb.load(ops0 + kOpKE);
+    __syncthreads();
+    for (int64_t n = 0; n < chunks; ++n) {
+      uint8_t* ops = ops0 + n * step;
+      const bool more = n + 1 < chunks;
+      const float* tail = tails + (n & 1) * 256;
+      float* S = reinterpret_cast<float*>(ops + kOpS) + 4 * g4 * D + 16 * vt0 + n16;
+      float* X = reinterpret_cast<float*>(ops + kOpX) + (vt0 * NB * 64 + lane) * 4;
+      // ---- x = T V - W S
+      if (more) load_a(n + 1);
+      {
+        Right<8> b[NT];
+        f32x4 acc[NT][NB];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          b[j].set(s[j]);
+#pragma unroll
+          for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[(16 * m + i) * D + 16 * j] = s[j][m][i];
+        }
+        product_a(b, acc);
+        const float unw = tail[kTailUnW];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < NB; ++r) {
+            const float un = -b[j].un * unw;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][r][i] = fmaf(acc[j][r][i], un, x[j][r][i]);
+            *reinterpret_cast<f32x4*>(X + (j * NB + r) * 256) = x[j][r];
+          }
       }
+      if (!more) return;  // the state after the last chunk is not needed
+      sb.store(lb);
+      __syncthreads();
+      // ---- S = e^Gl S + KE^T (beta x)
+      {
+        Right<NB> b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+          for (int r = 0; r < NB; ++r) x[j][r] *= lds4(tail + kTailBeta + 16 * r + 4 * g4);
+          b[j].set(x[j]);
+        }
+        load_x(n + 1);
+        sb.load(ops + step + kOpKE);
+        update(b, 1.0f, nullptr, nullptr, tail);
+      }
+      store_a(n + 1);
+      __syncthreads();
     }
     return;
   }
 
   if (p.d_final && active) {
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[m][i] = p.d_final[state + 16 * m + i];
-  }
-  if (active) {
-    for (int64_t n = chunks - 1; n >= 0; --n) {
-      float* ops = ops0 + n * step;
-      const int64_t tc = t0 + n * C;
-      const int c = int(min<int64_t>(C, len - n * C));
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int m = 0; m < 8; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ops[kOpDS + (16 * m + 4 * g4 + i) * D + v] = s[m][i];
-      f32x4 x[NB], o[NB];
+        for (int i = 0; i < 4; ++i) s[n][m][i] = p.d_final[state + n * 16 * D + 16 * m + i];
+  }
+  if (active && chunks > 0) {
+    Stage<NA, T> sa;
+    Stage<2 * NA, T> sb;
+    u32x4 st = {0u, 0u, 0u, 0u};
+    auto load_a = [&](int64_t n) {
+      sa.load(ops0 + n * step + kOpZ);
+      if (threadIdx.x < 64) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + threadIdx.x * 16);
+    };
+    auto store_a = [&](int64_t n) {
+      sa.store(la);
+      if (threadIdx.x < 64) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + threadIdx.x * 4) = st;
+    };
+    f32x4 x[NT][NB];  // T^T P^T dO and dO of the next chunk
+    uint16_t ow[NT][NB][4];
+    auto load_x = [&](int64_t n) {
+      const float* DV = reinterpret_cast<const float*>(ops0 + n * step + kOpDV) +
+                        (vt0 * NB * 64 + lane) * 4;
+      const int c = int(min<int64_t>(C, len - n * C));
+      const uint16_t* o = p.dout + (t0 + n * C) * p.dout_stride + h * D + 16 * vt0 + n16;
 #pragma unroll
-      for (int r = 0; r < NB; ++r) {
-        x[r] = col4(ops + kOpDV + (16 * r + 4 * g4) * D + v, D);
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-          x[r] = mfma4(lds4(ops + kOpZ + ((r * 8 + m) * 64 + lane) * 4), s[m], x[r]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ops[kOpDV + (16 * r + 4 * g4 + i) * D + v] = x[r][i];
-          const int t = 16 * r + 4 * g4 + i;
-          o[r][i] = t < c ? bf1(p.dout[(tc + t) * p.dout_stride + h * D + v]) : 0.f;
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        s[m] *= lds4(ops + kOpEG + 16 * m + 4 * g4);
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int r = 0; r < NB; ++r) {
-          s[m] = mfma4(lds4(ops + kOpKG + ((m * NB + r) * 64 + lane) * 4), x[r], s[m]);
-          s[m] = mfma4(lds4(ops + kOpQG + ((m * NB + r) * 64 + lane) * 4), o[r], s[m]);
+          x[j][r] = lds4(DV + (j * NB + r) * 256);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ow[j][r][i] = o[min(16 * r + 4 * g4 + i, c - 1) * p.dout_stride + 16 * j];
         }
+    };
+    load_a(chunks - 1);
+    load_x(chunks - 1);
+    store_a(chunks - 1);
+    sb.load(ops0 + (chunks - 1) * step + kOpKG);
+    __syncthreads();
+    for (int64_t n = chunks - 1; n >= 0; --n) {
+      uint8_t* ops = ops0 + n * step;
+      const int c = int(min<int64_t>(C, len - n * C));
+      const float* tail = tails + (n & 1) * 256;
+      float* dS = reinterpret_cast<float*>(ops + kOpDS) + 4 * g4 * D + 16 * vt0 + n16;
+      float* DV = reinterpret_cast<float*>(ops + kOpDV) + (vt0 * NB * 64 + lane) * 4;
+      // ---- dV = T^T P^T dO + Z dS
+      if (n > 0) load_a(n - 1);
+      {
+        Right<8> b[NT];
+        f32x4 acc[NT][NB];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          b[j].set(s[j]);
+#pragma unroll
+          for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dS[(16 * m + i) * D + 16 * j] = s[j][m][i];
+        }
+        product_a(b, acc);
+        const float unz = tail[kTailUnZ];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < NB; ++r) {
+            const float un = b[j].un * unz;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][r][i] = fmaf(acc[j][r][i], un, x[j][r][i]);
+            *reinterpret_cast<f32x4*>(DV + (j * NB + r) * 256) = x[j][r];
+          }
       }
+      if (n == 0 && !p.d_initial) return;
+      sb.store(lb);
+      __syncthreads();
+      // ---- dS = e^Gl dS - KG^T dV + scale QG^T dO
+      {
+        Right<NB> b[NT];
+        f16x8 o[NT][2];
+        float uno[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          b[j].set(x[j]);
+          // dO has 8 bits: its high part alone is exact
+          f32x4 y[NB];
+          float top = 0.f;
+#pragma unroll
+          for (int r = 0; r < NB; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[r][i] = 16 * r + 4 * g4 + i < c ? bf1(ow[j][r][i]) : 0.f;
+              top = fmaxf(top, fabsf(y[r][i]));
+            }
+          const Scale sc = scale_for(column_max(top));
+          uno[j] = sc.un * (p.scale * kFixedUn);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const f32x4 a = y[2 * t] * sc.up, d = y[2 * t + 1] * sc.up;
+            o[j][t] = __builtin_bit_cast(
+                f16x8, u32x4{pack_f16x2(a[0], a[1]), pack_f16x2(a[2], a[3]),
+                             pack_f16x2(d[0], d[1]), pack_f16x2(d[2], d[3])});
+          }
+        }
+        if (n > 0) {
+          load_x(n - 1);
+          sb.load(ops - step + kOpKG);
+        }
+        update(b, -1.0f, o, uno, tail);
+      }
+      if (n > 0) store_a(n - 1);
+      __syncthreads();
     }
   }
   if (p.d_initial) {
 #pragma unroll
-    for (int m = 0; m < 8; ++m) *reinterpret_cast<f32x4*>(p.d_initial + state + 16 * m) = s[m];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        *reinterpret_cast<f32x4*>(p.d_initial + state + n * 16 * D + 16 * m) = s[n][m];
   }
 }
 
@@ -637,28 +995,45 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g4 = lane >> 4, n16 = lane & 15;
   const int kc = 16 * w + n16;
-  const float* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
+  const uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
 
   token_scalars(p, ch, h, s.rq, s.rk, s.beta);
   {
-    const int c0 = (threadIdx.x & 31) * 4;
-    for (int t = threadIdx.x >> 5; t < C; t += kThreads / 32) {
-      const f32x4 dv = lds4(ops + kOpDV + t * D + c0);
-      *reinterpret_cast<f32x4*>(s.dV + t * RS + c0) = dv;
-      *reinterpret_cast<f32x4*>(s.x + t * RS + c0) = lds4(ops + kOpX + t * D + c0);
-      f32x4 o = zero4();
-      if (t < ch.c) {
-        const uint16_t* src = p.dout + (ch.t0 + t) * p.dout_stride + h * D + c0;
-        uint16_t* dst = p.dv + (ch.t0 + t) * p.dv_stride + h * D + c0;
-        typedef u32x2 u32x2_u __attribute__((aligned(2)));
-        const u32x2 b = *reinterpret_cast<const u32x2_u*>(src);
-        o = f32x4{bf_lo(b[0]), bf_hi(b[0]), bf_lo(b[1]), bf_hi(b[1])};
-        *reinterpret_cast<u32x2_u*>(dst) = u32x2{pack_bf16x2(dv[0], dv[1]), pack_bf16x2(dv[2], dv[3])};
+    // wave w brings value tile w: accumulator tiles to rows of tokens
+    const float* X = reinterpret_cast<const float*>(ops + kOpX) + (w * NB * 64 + lane) * 4;
+    const float* DV = reinterpret_cast<const float*>(ops + kOpDV) + (w * NB * 64 + lane) * 4;
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+      const f32x4 x = lds4(X + r * 256), dv = lds4(DV + r * 256);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s.x[(16 * r + 4 * g4 + i) * RS + kc] = x[i];
+        s.dV[(16 * r + 4 * g4 + i) * RS + kc] = dv[i];
       }
-      *reinterpret_cast<f32x4*>(s.dO + t * RS + c0) = o;
+    }
+    const int c0 = (threadIdx.x & 15) * 8;
+#pragma unroll
+    for (int j = 0; j < C / (kThreads / 16); ++j) {
+      const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+      u32x4 ow = *reinterpret_cast<const u32x4_u*>(
+          p.dout + (ch.t0 + min(t, ch.c - 1)) * p.dout_stride + h * D + c0);
+      if (t >= ch.c) ow = u32x4{0u, 0u, 0u, 0u};
+      float o[8];
+      unpack8_bf16(ow, o);
+      *reinterpret_cast<f32x4*>(s.dO + t * RS + c0) = f32x4{o[0], o[1], o[2], o[3]};
+      *reinterpret_cast<f32x4*>(s.dO + t * RS + c0 + 4) = f32x4{o[4], o[5], o[6], o[7]};
     }
   }
   __syncthreads();
+  {
+    const int c0 = (threadIdx.x & 15) * 8;
+    for (int t = threadIdx.x >> 4; t < ch.c; t += kThreads / 16) {
+      const f32x4 a = lds4(s.dV + t * RS + c0), b = lds4(s.dV + t * RS + c0 + 4);
+      *reinterpret_cast<u32x4_u*>(p.dv + (ch.t0 + t) * p.dv_stride + h * D + c0) =
+          u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
+                pack_bf16x2(b[2], b[3])};
+    }
+  }
 
   // ---- DP = tril(dO x^T), DA = -tril(dV x^T, -1). A token's use of its own key has no
   // decay: DP's diagonal is kept apart, out of the sums that give dg.
@@ -687,8 +1062,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   {
 #pragma unroll
     for (int r = 0; r < NB; ++r) sq[r] = sk[r] = se[r] = zero4();
-    const float* S = ops + kOpS + kc * D + 4 * g4;
-    const float* dS = ops + kOpDS + kc * D + 4 * g4;
+    const float* S = reinterpret_cast<const float*>(ops + kOpS) + kc * D + 4 * g4;
+    const float* dS = reinterpret_cast<const float*>(ops + kOpDS) + kc * D + 4 * g4;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       const f32x4 a = lds4(S + 16 * m), b = lds4(dS + 16 * m);
@@ -702,7 +1077,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
         se[r] = mfma4(lds4(s.x + at), b, se[r]);
       }
     }
-    last = rows_sum(last) * ops[kOpEG + kc];
+    last = rows_sum(last) * reinterpret_cast<const float*>(ops + kOpTail)[kc];
   }
   Lane ln;
   load_lane<true>(p, ch, h, kc, g4, s.rq, s.rk, ln);
@@ -733,6 +1108,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
         bt[b][i] = s.beta[16 * b + 4 * g4 + i];
         up[b][i] = expf(x);
         km[b][i] = ln.k[b][i] * up[b][i];
+        ln.q[b][i] *= p.scale;  // q'
         qm[b][i] = ln.q[b][i] * up[b][i];
         kb[b][i] = ln.k[b][i] * expf(-x) * bt[b][i];
       }
@@ -908,21 +1284,34 @@ int64_t slots_of(int32_t n_docs, int64_t total_tokens) { return n_docs + total_t
 // Dynamic LDS beyond 64 KiB is allowed once per kernel.
 hipError_t allow_lds() {
   static const hipError_t e = [] {
-    const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(prep_kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(sizeof(PrepSmem)));
-    if (a != hipSuccess) return a;
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(grad_kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(GradSmem)));
+    const struct { const void* f; size_t bytes; } all[] = {
+        {reinterpret_cast<const void*>(prep_kernel), sizeof(PrepSmem)},
+        {reinterpret_cast<const void*>(grad_kernel), sizeof(GradSmem)},
+        {reinterpret_cast<const void*>(chain_kernel<2, 1>), kChainLds},
+        {reinterpret_cast<const void*>(chain_kernel<4, 1>), kChainLds},
+        {reinterpret_cast<const void*>(chain_kernel<4, 2>), kChainLds}};
+    for (const auto& k : all)
+      if (const hipError_t a = hipFuncSetAttribute(
+              k.f, hipFuncAttributeMaxDynamicSharedMemorySize, int(k.bytes)))
+        return a;
+    return hipSuccess;
   }();
   return e;
+}
+
+template <int NW, int NT>
+void launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
+  constexpr int PARTS = 8 / (NW * NT);
+  const int64_t ids = (int64_t(p.n_docs) * p.H * 2 + 7) / 8 * 8;  // both directions
+  hipLaunchKernelGGL((chain_kernel<NW, NT>), dim3(unsigned(ids * PARTS)), dim3(64 * NW), kChainLds,
+                     stream, p, ord);
 }
 
 hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32_t* cu_host,
                            hipStream_t stream) {
   if (const hipError_t e = allow_lds()) return e;
   const int64_t chains = int64_t(p.n_docs) * p.H;
-  if (p.slots > 0x7fffffff || chains * 2 * kParts > 0x7fffffff) return hipErrorInvalidValue;
+  if (p.slots > 0x7fffffff || chains > 0x7fffffff / 16) return hipErrorInvalidValue;
   DocOrder ord;
   ord.n = 0;
   if (p.n_docs <= kMaxOrderedDocs) {  // the longest documents first
@@ -941,8 +1330,10 @@ hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32
     if (const hipError_t e = hipGetLastError()) return e;
   }
   if (total_tokens > 0 || p.d_initial) {
-    hipLaunchKernelGGL(chain_kernel, dim3(unsigned(chains * 2 * kParts)), dim3(64 * kChainWaves),
-                       0, stream, p, ord);
+    // workgroups per chain and direction: as many as it takes to fill the chip
+    if (chains <= 32) launch_chain<2, 1>(p, ord, stream);
+    else if (chains <= 128) launch_chain<4, 1>(p, ord, stream);
+    else launch_chain<4, 2>(p, ord, stream);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   if (total_tokens > 0) {
@@ -966,7 +1357,7 @@ extern "C" size_t kda_prefill_backward_workspace_size(int32_t n_docs, int64_t to
   if (n_docs < 0 || total_tokens < 0 || total_tokens > INT32_MAX || H < 1 || H > 65535 ||
       K != kda::D || V != kda::D)
     return 0;
-  return size_t(kda::slots_of(n_docs, total_tokens)) * size_t(H) * (kda::kOps + 2 * kda::D) * 4;
+  return size_t(kda::slots_of(n_docs, total_tokens)) * size_t(H) * (kda::kOps + 2 * kda::D * 4);
 }
 
 extern "C" kda_status kda_prefill_varlen_backward(
@@ -1065,8 +1456,9 @@ extern "C" kda_status kda_prefill_varlen_backward(
   p.dA_log = dA_log;
   p.ddt_bias = ddt_bias;
   p.d_initial = d_initial_state;
-  p.ops = static_cast<float*>(workspace);
-  p.partial = p.ops + (total_tokens > 0 ? p.slots * int64_t(H) * kda::kOps : 0);
+  p.ops = static_cast<uint8_t*>(workspace);
+  p.partial = reinterpret_cast<float*>(
+      p.ops + (total_tokens > 0 ? p.slots * int64_t(H) * kda::kOps : 0));
   if (n_docs == 0 && !dA_log && !ddt_bias) return KDA_OK;
   return kda::launch_backward(p, total_tokens, cu_seqlens_host, stream) == hipSuccess
              ? KDA_OK : KDA_ERR_LAUNCH;
