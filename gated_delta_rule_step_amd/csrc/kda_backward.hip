@@ -25,1291 +25,36 @@
 //   col  = e^(Gl-G) (x dS^T) + sum_r (DA[r,j] k_r + DP[r,j] q'_r) e^(G_r-G_j)
 // and, with dp_r beta_r k_r added to dq'_r and dp_r q'_r to col_r,
 //   dk_hat = drow + beta col,  dbeta = k_hat . col,  dq_hat = scale dq'
-// Each weight e^(G_r-G_j) rises by dg_t for all j < t <= r, so dg is a suffix sum
-// of q' dq' + k drow - beta k col before those two (what token t uses as reader less
-// as writer),
-// to which the chunk's end adds what leaves it: e^Gl sum_v S dS + sum_t beta k
-// e^(Gl-G) (x dS^T).
+// Each weight e^(G_r-G_j) grows with dg_t for all j < t <= r, so dg_t is the sum over
+// those pairs of their part in the loss, with S as a token before all others and dS as one
+// behind them (grad_kernel says how it adds them up).
 //
-// Decays. A chunk is four 16-token blocks. With lam the log-decay summed inside a
-// block and tau the block's total, readers hold e^(lam - tau/2) and writers
-// e^(tau/2 - lam), both within e^(+-44) (|lower_bound| <= 5.5); a pair of blocks
-// I >= J then lacks e^(sum of tau from the middle of J to the middle of I), one
-// factor per pair and channel. No sum runs over more than 16 tokens before it is
-// exponentiated, which keeps the weights' relative error near 16 * 2^-24 of the
-// gates.
+// Decays. A chunk is four 16-token blocks. Inside a block the weight of a pair is a
+// reader's factor from the block's middle times a writer's factor to it, both
+// within e^(+-44) (|lower_bound| <= 5.5); pairs of different blocks take what lies between
+// the two middles, or, factored at the blocks' borders, weights of at most 1. All of them
+// are products of the a_t = e^g_t.
 //
-// Every product runs on fp32 MFMA (16x16x4). An operand tile is read as 4
-// consecutive elements along the contraction by each lane, and the four
-// instructions they feed take contraction indices 4 (lane / 16) + j, so that an
-// accumulator tile (rows 4 (lane / 16) + i) serves as the next product's right
-// operand as it is.
+// Precision. States, sums and decays are fp32. Products run either on fp32 MFMA or on
+// fp16 MFMA with both sides split into high and low parts (22 bits and a sign each, three
+// terms), which loses nothing against fp32 and takes 3/16 of its time; fp16's range is
+// met by power-of-two scales. Operand tiles are read as consecutive contraction indices
+// per lane, in an order that lets an accumulator tile (rows 4 (lane / 16) + i) serve as the
+// next product's right operand as it is.
 
 #include <math.h>
 #include <stdint.h>
 
-#include "../../include/kda_backward.h"
-#include "kda_common.h"
+#include "kda_bwd.h"
 
 namespace kda {
+namespace bwd {
 namespace {
-
-constexpr int C = 64;        // tokens per chunk
-constexpr int NB = C / 16;   // 16-token blocks per chunk
-constexpr int RS = D + 4;    // padded row (fp32) of [token][channel] LDS arrays
-constexpr int AS = C + 4;    // padded row of [token][token] LDS arrays
-constexpr int NP = NB * (NB - 1) / 2;  // pairs of different blocks
-constexpr int kThreads = 512;
-constexpr int kMaxOrderedDocs = 256;
-constexpr float kL2Eps = 1e-6f;
-
-struct BwdParams {
-  int32_t n_docs, H;
-  int64_t slots;  // chunk slots: n_docs + total_tokens / C
-  const int32_t* cu_seqlens;
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  const uint16_t* g;
-  const uint16_t* beta;
-  int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
-  const float* A_log;
-  const float* dt_bias;
-  float lower_bound, scale;
-  int32_t gate_mode, state_dtype, use_initial;
-  const void* pool;
-  int64_t num_slots, slot_stride;
-  const int32_t* state_indices;
-  const uint16_t* dout;
-  int64_t dout_stride;
-  const float* d_final;
-  uint16_t* dq;
-  uint16_t* dk;
-  uint16_t* dv;
-  uint16_t* dg;
-  uint16_t* dbeta;
-  int64_t dq_stride, dk_stride, dv_stride, dg_stride, dbeta_stride;
-  float* dA_log;
-  float* ddt_bias;
-  float* d_initial;
-  uint8_t* ops;    // [slot][h][kOps]
-  float* partial;  // [slot][h][2][D]: of ddt_bias and dA_log, per channel
-};
-
-struct DocOrder {
-  int32_t n;  // 0: natural order
-  int32_t doc[kMaxOrderedDocs];
-};
-
-// A (chunk, head)'s part of the workspace, in bytes. The chains' left operands are
-// fp16 high and low parts in fragment order, 16 bytes (8 contraction indices) a lane:
-//   W, Z        [rt 4][kt 4][hi, lo][lane]  token 16 rt + lane % 16, key channels
-//               32 kt + 4 (lane / 16) + 0..3 and 16 further
-//   KE, KG, QG  [m 8][t 2][hi, lo][lane]    key channel 16 m + lane % 16, tokens
-//               32 t + 4 (lane / 16) + 0..3 and 16 further
-// X and DV are accumulator tiles [vt 8][rt 4][lane][4 tokens].
-constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales of W and Z
-constexpr int kOpW = 1024;               // T e^G k, scaled
-constexpr int kOpKE = kOpW + 32768;      // e^(Gl-G) k, times 2^12
-constexpr int kOpZ = kOpKE + 32768;      // T^T (beta e^(Gl-G) k), scaled
-constexpr int kOpKG = kOpZ + 32768;      // e^G k, times 2^12
-constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat, times 2^12
-constexpr int kOpX = kOpQG + 32768;      // T V, then x
-constexpr int kOpDV = kOpX + 32768;      // T^T P^T dO, then dV
-constexpr int kOpS = kOpDV + 32768;      // S [key][value] entering the chunk
-constexpr int kOpDS = kOpS + 65536;      // dS [key][value] leaving it
-constexpr int kOps = kOpDS + 65536;
-constexpr int kTailBeta = D, kTailUnW = D + C, kTailUnZ = D + C + 1;  // in floats
-
-__device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
-  return c;
-}
-__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
-__device__ __forceinline__ f32x4 lds4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-// 4 elements down a column
-__device__ __forceinline__ f32x4 col4(const float* p, int stride) {
-  return f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]};
-}
-
-typedef u32x4 u32x4_u __attribute__((aligned(2)));  // any bf16 address
-typedef __fp16 f16x8 __attribute__((__vector_size__(8 * sizeof(__fp16))));  // MFMA operand
-
-// fp32 as fp16 high + low parts: 22 bits and a sign. Three products (high high,
-// high low, low high) then leave out 2^-22 of a term, less than the fp32 additions.
-__device__ __forceinline__ void split4h(f32x4 x, u32x2& hi, u32x2& lo) {
-  hi = u32x2{pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3])};
-  lo = u32x2{pack_f16x2(x[0] - f16_lo(hi[0]), x[1] - f16_hi(hi[0])),
-             pack_f16x2(x[2] - f16_lo(hi[1]), x[3] - f16_hi(hi[1]))};
-}
-__device__ __forceinline__ f16x8 join8(u32x2 a, u32x2 b) {
-  return __builtin_bit_cast(f16x8, u32x4{a[0], a[1], b[0], b[1]});
-}
-__device__ __forceinline__ f32x4 mfma32(f16x8 a, f16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-// fp16 holds 2^-24 to 2^16, so operands of any size are scaled by a power of two that
-// brings their largest magnitude to 2^14 .. 2^15; `un` undoes it.
-struct Scale {
-  float up, un;
-};
-__device__ __forceinline__ Scale scale_for(float top) {
-  int e = int(__float_as_uint(top) >> 23);
-  e = e < 40 ? 40 : (e > 250 ? 250 : e);
-  return {__uint_as_float(uint32_t(268 - e) << 23), __uint_as_float(uint32_t(e - 14) << 23)};
-}
-constexpr float kFixedUp = 4096.0f, kFixedUn = 1.0f / 4096.0f;  // operands within +-1
-
-// Sum over the four 16-lane rows of a wave (lanes of equal lane % 16).
-__device__ __forceinline__ float rows_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
-}
-
-// First chunk slot of document i; slots of a document follow each other.
-__device__ __forceinline__ int64_t doc_slot0(const int32_t* cu, int i) {
-  return int64_t(i) + int64_t(cu[i]) / C;
-}
-// The document of chunk slot sigma: the largest i <= n_docs with doc_slot0(i) <=
-// sigma (doc_slot0 rises strictly from 0).
-__device__ int find_doc(const int32_t* cu, int n_docs, int64_t sigma) {
-  int lo = 0, hi = n_docs + 1;
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (doc_slot0(cu, mid) <= sigma) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
-struct Chunk {
-  int doc;
-  int64_t t0;  // first token
-  int c;       // tokens; 0: a slot between documents
-  bool active;
-};
-__device__ __forceinline__ Chunk chunk_of(const BwdParams& p, int64_t sigma) {
-  Chunk ch = {0, 0, 0, false};
-  ch.doc = find_doc(p.cu_seqlens, p.n_docs, sigma);
-  if (ch.doc >= p.n_docs) return ch;
-  const int64_t start = p.cu_seqlens[ch.doc];
-  const int64_t len = int64_t(p.cu_seqlens[ch.doc + 1]) - start;
-  const int64_t off = (sigma - doc_slot0(p.cu_seqlens, ch.doc)) * C;
-  if (off >= len) return ch;
-  ch.t0 = start + off;
-  ch.c = int(min<int64_t>(C, len - off));
-  const int32_t slot = p.state_indices[ch.doc];
-  ch.active = slot >= 0 && int64_t(slot) < p.num_slots;
-  return ch;
-}
-
-// Here and below a chunk's missing tokens read its last one and drop the value: a
-// load behind a branch would be waited for one at a time.
-
-// 1 / |q|, 1 / |k| (with the epsilon) and beta of the chunk's tokens, to LDS: 16
-// lanes per token. Padding rows get zeros.
-__device__ __forceinline__ void token_scalars(const BwdParams& p, const Chunk& ch, int h,
-                                              float* rq, float* rk, float* beta) {
-  constexpr int N = C / (kThreads / 16);
-  const int c0 = (threadIdx.x & 15) * 8;
-  u32x4 qw[N], kw[N];
-  uint16_t bw[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int64_t t = ch.t0 + min(int(threadIdx.x >> 4) + j * (kThreads / 16), ch.c - 1);
-    qw[j] = *reinterpret_cast<const u32x4_u*>(p.q + t * p.q_stride + h * D + c0);
-    kw[j] = *reinterpret_cast<const u32x4_u*>(p.k + t * p.k_stride + h * D + c0);
-    bw[j] = p.beta[t * p.beta_stride + h];
-  }
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
-    float x[8], sq = 0.f, sk = 0.f;
-    unpack8_bf16(qw[j], x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-    unpack8_bf16(kw[j], x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sk = fmaf(x[i], x[i], sk);
-    sq = row16_sum(sq);
-    sk = row16_sum(sk);
-    if ((threadIdx.x & 15) == 0) {
-      float b = bf1(bw[j]);
-      if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) b = sigmoidf(b);
-      rq[t] = t < ch.c ? 1.0f / sqrtf(sq + kL2Eps) : 0.f;
-      rk[t] = t < ch.c ? 1.0f / sqrtf(sk + kL2Eps) : 0.f;
-      beta[t] = t < ch.c ? b : 0.f;
-    }
-  }
-}
-
-// A lane's share of the chunk: key channel `kc`, tokens 16 b + 4 g4 + i.
-struct Lane {
-  float k[NB][4], q[NB][4];      // k_hat, q_hat
-  float g[NB][4], slope[NB][4];  // log-decay and its derivative by the gate input
-  float lam[NB][4];              // log-decay summed from the block's first token
-  float tau[NB];                 // the block's total
-};
-
-template <bool SLOPE>
-__device__ __forceinline__ void load_lane(const BwdParams& p, const Chunk& ch, int h, int kc,
-                                          int g4, const float* rq, const float* rk, Lane& ln) {
-  const bool pre = p.gate_mode & KDA_GATE_PRECOMPUTED;
-  const bool head = p.gate_mode & KDA_GATE_PER_HEAD;
-  const int64_t gch = head ? h : int64_t(h) * D + kc;
-  const float ea = pre ? 0.f : expf(p.A_log[h]);
-  const float dtb = pre ? 0.f : p.dt_bias[gch];
-  uint16_t kw[NB][4], qw[NB][4], gw[NB][4];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = ch.t0 + min(16 * b + 4 * g4 + i, ch.c - 1);
-      kw[b][i] = p.k[t * p.k_stride + h * D + kc];
-      qw[b][i] = p.q[t * p.q_stride + h * D + kc];
-      gw[b][i] = p.g[t * p.g_stride + gch];
-    }
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * b + 4 * g4 + i;
-      const bool valid = t < ch.c;
-      const float k = valid ? bf1(kw[b][i]) * rk[t] : 0.f;
-      const float q = valid ? bf1(qw[b][i]) * rq[t] : 0.f;
-      const float x = bf1(gw[b][i]);
-      float g, s = 0.f;
-      if (pre) {
-        g = gate_given(x, p.lower_bound);
-        s = x >= p.lower_bound && x <= 0.f ? 1.f : 0.f;
-      } else {
-        const float y = x + dtb;
-        const float gu = -ea * (y > 20.f ? y : log1pf(expf(y)));
-        g = fmaxf(gu, p.lower_bound);
-        if (SLOPE) s = gu >= p.lower_bound ? -ea * sigmoidf(y) : 0.f;
-      }
-      if (!valid) g = s = 0.f;
-      ln.k[b][i] = k;
-      ln.q[b][i] = q;
-      if constexpr (SLOPE) {
-        ln.g[b][i] = g;
-        ln.slope[b][i] = s;
-      }
-      sum += g;
-      ln.lam[b][i] = sum;
-    }
-    // the sums of the lanes with earlier tokens, then the block's total
-    const float s1 = __shfl_xor(sum, 16);
-    const float pair = sum + s1;
-    const float other = __shfl_xor(pair, 32);
-    const float before = ((g4 & 1) ? s1 : 0.f) + ((g4 & 2) ? other : 0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ln.lam[b][i] += before;
-    ln.tau[b] = pair + other;
-  }
-}
-
-__host__ __device__ constexpr int pair_index(int I, int J) { return I * (I - 1) / 2 + J; }
-
-// ---------------------------------------------------------------------------
-// Preparation: one workgroup per (chunk, head); a wave owns 16 channels.
-struct PrepSmem {
-  float km[C * RS];    // e^(lam - tau/2) k
-  float kb[C * RS];    // beta e^(tau/2 - lam) k
-  float qm[C * RS];    // e^(lam - tau/2) q', then V and dO (bf16)
-  float am[C * AS];    // A
-  float pm[C * AS];    // P
-  float tm[C * AS];    // T
-  float pair[NP * D];  // factor of a block pair
-  float top[2][8];     // largest magnitudes of W and Z, per wave
-  float rq[C], rk[C], beta[C];
-};
-constexpr int VS = 2 * RS;  // row of V and dO in uint16: V first, dO from RS on
-
-__global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
-  extern __shared__ __align__(16) float smem_raw[];
-  PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
-  const int64_t sigma = blockIdx.x;
-  const int h = blockIdx.y;
-  const Chunk ch = chunk_of(p, sigma);
-  if (ch.c == 0 || !ch.active) return;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int g4 = lane >> 4, n16 = lane & 15;
-  const int kc = 16 * w + n16;
-  uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
-  float* tail = reinterpret_cast<float*>(ops + kOpTail);
-
-  token_scalars(p, ch, h, s.rq, s.rk, s.beta);
-  __syncthreads();
-  if (threadIdx.x < C) tail[kTailBeta + threadIdx.x] = s.beta[threadIdx.x];
-
-  // ---- the decayed rows, and what depends on them channel by channel alone
-  f32x4 kg[NB], ke[NB];  // e^G k, beta e^(Gl-G) k: 4 tokens of channel kc
-  {
-    Lane ln;
-    load_lane<false>(p, ch, h, kc, g4, s.rq, s.rk, ln);
-    float from[NB], to[NB];  // middle of the block from the chunk's start, to its end
-    float o = 0.f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      from[b] = o + 0.5f * ln.tau[b];
-      o += ln.tau[b];
-    }
-    float e = 0.f;
-#pragma unroll
-    for (int b = NB - 1; b >= 0; --b) {
-      to[b] = e + 0.5f * ln.tau[b];
-      e += ln.tau[b];
-    }
-    if (g4 == 0) {
-      tail[kc] = expf(o);
-#pragma unroll
-      for (int I = 1; I < NB; ++I) {
-        float mid = 0.f;
-#pragma unroll
-        for (int J = I - 1; J >= 0; --J) {
-          s.pair[pair_index(I, J) * D + kc] = expf(0.5f * (ln.tau[I] + ln.tau[J]) + mid);
-          mid += ln.tau[J];
-        }
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float ef = expf(from[b]), et = expf(to[b]);
-      f32x4 qg, kee;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * b + 4 * g4 + i;
-        const float x = ln.lam[b][i] - 0.5f * ln.tau[b];
-        const float up = expf(x), down = expf(-x);
-        const float km = ln.k[b][i] * up, qm = ln.q[b][i] * up * p.scale;
-        const float kb = ln.k[b][i] * down * s.beta[t];
-        s.km[t * RS + kc] = km;
-        s.qm[t * RS + kc] = qm;
-        s.kb[t * RS + kc] = kb;
-        kg[b][i] = km * ef;
-        qg[i] = ln.q[b][i] * up * ef;
-        kee[i] = ln.k[b][i] * down * et;
-        ke[b][i] = kb * et;
-      }
-      const int at = ((w * 2 + (b >> 1)) * 2 * 64 + lane) * 16 + 8 * (b & 1);
-      u32x2 hi, lo;
-      split4h(kee * kFixedUp, hi, lo);
-      *reinterpret_cast<u32x2*>(ops + kOpKE + at) = hi;
-      *reinterpret_cast<u32x2*>(ops + kOpKE + at + 1024) = lo;
-      split4h(kg[b] * kFixedUp, hi, lo);
-      *reinterpret_cast<u32x2*>(ops + kOpKG + at) = hi;
-      *reinterpret_cast<u32x2*>(ops + kOpKG + at + 1024) = lo;
-      split4h(qg * kFixedUp, hi, lo);
-      *reinterpret_cast<u32x2*>(ops + kOpQG + at) = hi;
-      *reinterpret_cast<u32x2*>(ops + kOpQG + at + 1024) = lo;
-    }
-  }
-  __syncthreads();
-
-  // ---- A and P, block by block (10 each on and below the diagonal)
-  for (int task = w; task < NB * (NB + 1); task += kThreads / 64) {
-    const bool is_p = task >= NB * (NB + 1) / 2;
-    int I = 0, J = is_p ? task - NB * (NB + 1) / 2 : task;
-    while (J > I) J -= ++I;
-    const float* left = (is_p ? s.qm : s.km) + (16 * I + n16) * RS + 4 * g4;
-    const float* right = s.kb + (16 * J + n16) * RS + 4 * g4;
-    f32x4 acc = zero4();
-#pragma unroll
-    for (int m = 0; m < D / 16; ++m) {
-      f32x4 a = lds4(left + 16 * m);
-      if (I != J) a *= lds4(s.pair + pair_index(I, J) * D + 16 * m + 4 * g4);
-      acc = mfma4(a, lds4(right + 16 * m), acc);
-    }
-    float* dst = (is_p ? s.pm : s.am) + (16 * I + 4 * g4) * AS + 16 * J + n16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int over = I == J ? n16 - (4 * g4 + i) : -1;  // column beyond the row
-      dst[i * AS] = over < 0 || (is_p && over == 0) ? acc[i] : 0.f;
-    }
-  }
-  __syncthreads();
-
-  // ---- T = (1 + A)^-1. Diagonal blocks: N = -A is strictly lower, N^16 = 0, so
-  // the inverse is (1 + N)(1 + N^2)(1 + N^4)(1 + N^8). A product X Y takes X^T as
-  // its left fragment, so every power is kept with its transpose.
-  if (w < NB) {
-    const float* a = s.am + 16 * w * AS + 16 * w;
-    f32x4 n = -col4(a + 4 * g4 * AS + n16, AS), nt = -lds4(a + n16 * AS + 4 * g4);
-    f32x4 r = n, rt = nt;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float one = 4 * g4 + i == n16 ? 1.f : 0.f;
-      r[i] += one;
-      rt[i] += one;
-    }
-#pragma unroll
-    for (int step = 0; step < 3; ++step) {
-      const f32x4 n2 = mfma4(nt, n, zero4()), n2t = mfma4(n, nt, zero4());
-      const f32x4 r2 = mfma4(rt, n2, r), r2t = mfma4(n2, rt, rt);
-      n = n2, nt = n2t, r = r2, rt = r2t;
-    }
-    float* dst = s.tm + (16 * w + 4 * g4) * AS + 16 * w + n16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i * AS] = r[i];
-  }
-  // V and dO (bf16) take the place of e^(lam - tau/2) q'
-  {
-    uint16_t* vo = reinterpret_cast<uint16_t*>(s.qm);
-    const int c0 = (threadIdx.x & 15) * 8;
-#pragma unroll
-    for (int j = 0; j < C / (kThreads / 16); ++j) {
-      const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
-      const int64_t at = ch.t0 + min(t, ch.c - 1);
-      u32x4 a = *reinterpret_cast<const u32x4_u*>(p.v + at * p.v_stride + h * D + c0);
-      u32x4 b = *reinterpret_cast<const u32x4_u*>(p.dout + at * p.dout_stride + h * D + c0);
-      if (t >= ch.c) a = b = u32x4{0u, 0u, 0u, 0u};
-      typedef u32x4 u32x4_8 __attribute__((aligned(8)));
-      *reinterpret_cast<u32x4_8*>(vo + t * VS + c0) = a;
-      *reinterpret_cast<u32x4_8*>(vo + t * VS + RS + c0) = b;
-    }
-  }
-  __syncthreads();
-  // T_IJ = -T_II sum_K A_IK T_KJ, one wave per block column
-  if (w < NB - 1) {
-    f32x4 t[NB];
-    t[0] = col4(s.tm + (16 * w + 4 * g4) * AS + 16 * w + n16, AS);
-    for (int I = w + 1; I < NB; ++I) {
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int d = 0; d < NB - 1; ++d)
-        if (w + d < I) acc = mfma4(lds4(s.am + (16 * I + n16) * AS + 16 * (w + d) + 4 * g4), t[d], acc);
-      acc = mfma4(lds4(s.tm + (16 * I + n16) * AS + 16 * I + 4 * g4), -acc, zero4());
-#pragma unroll
-      for (int d = 1; d < NB; ++d)
-        if (w + d == I) t[d] = acc;
-      float* dst = s.tm + (16 * I + 4 * g4) * AS + 16 * w + n16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i * AS] = acc[i];
-    }
-  }
-  __syncthreads();
-
-  // ---- products with T for the wave's 16 channels
-  const uint16_t* vo = reinterpret_cast<const uint16_t*>(s.qm);
-  f32x4 vv[NB], oo[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * b + 4 * g4 + i;
-      vv[b][i] = bf1(vo[t * VS + kc]);
-      oo[b][i] = bf1(vo[t * VS + RS + kc]);
-    }
-  f32x4 y[NB];  // P^T dO
-  f32x4 wt[NB], z[NB];
-  float wtop = 0.f, ztop = 0.f;
-  float* X = reinterpret_cast<float*>(ops + kOpX);
-  float* DV = reinterpret_cast<float*>(ops + kOpDV);
-#pragma unroll
-  for (int r = 0; r < NB; ++r) {
-    f32x4 xx = zero4();
-    wt[r] = z[r] = y[r] = zero4();
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (b <= r) {
-        const f32x4 t = lds4(s.tm + (16 * r + n16) * AS + 16 * b + 4 * g4);
-        wt[r] = mfma4(kg[b], t, wt[r]);  // transposed: rows are channels
-        xx = mfma4(t, vv[b], xx);
-      }
-      if (b >= r) {
-        const int at = (16 * b + 4 * g4) * AS + 16 * r + n16;
-        z[r] = mfma4(ke[b], col4(s.tm + at, AS), z[r]);  // transposed
-        y[r] = mfma4(col4(s.pm + at, AS), oo[b], y[r]);
-      }
-    }
-    *reinterpret_cast<f32x4*>(X + ((w * NB + r) * 64 + lane) * 4) = xx;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      wtop = fmaxf(wtop, fabsf(wt[r][i]));
-      ztop = fmaxf(ztop, fabsf(z[r][i]));
-    }
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    wtop = fmaxf(wtop, __shfl_xor(wtop, o));
-    ztop = fmaxf(ztop, __shfl_xor(ztop, o));
-  }
-  if (lane == 0) {
-    s.top[0][w] = wtop;
-    s.top[1][w] = ztop;
-  }
-#pragma unroll
-  for (int r = 0; r < NB; ++r) {
-    f32x4 d = zero4();
-#pragma unroll
-    for (int b = r; b < NB; ++b)
-      d = mfma4(col4(s.tm + (16 * b + 4 * g4) * AS + 16 * r + n16, AS), y[b], d);
-    *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wtop = fmaxf(wtop, s.top[0][i]);
-    ztop = fmaxf(ztop, s.top[1][i]);
-  }
-  const Scale sw = scale_for(wtop), sz = scale_for(ztop);
-  if (threadIdx.x == 0) {
-    tail[kTailUnW] = sw.un;
-    tail[kTailUnZ] = sz.un;
-  }
-#pragma unroll
-  for (int r = 0; r < NB; ++r) {
-    const int at = ((r * 4 + (w >> 1)) * 2 * 64 + lane) * 16 + 8 * (w & 1);
-    u32x2 hi, lo;
-    split4h(wt[r] * sw.up, hi, lo);
-    *reinterpret_cast<u32x2*>(ops + kOpW + at) = hi;
-    *reinterpret_cast<u32x2*>(ops + kOpW + at + 1024) = lo;
-    split4h(z[r] * sz.up, hi, lo);
-    *reinterpret_cast<u32x2*>(ops + kOpZ + at) = hi;
-    *reinterpret_cast<u32x2*>(ops + kOpZ + at + 1024) = lo;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Chains: the states up each (document, head), and the state gradients down.
-// Value channels do not mix in either, so a wave owns NT tiles of 16 of them, with
-// all 128 key channels in eight accumulator tiles each, and the chain is sequential
-// over the chunks alone. What bounds it is the latency of one chunk: two products
-// that wait for each other. They run on fp16 MFMA with both sides split into high and
-// low parts (three terms, fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides,
-// which are the state and x in accumulator layout, are scaled per value channel.
-//
-// A chunk's operands come in two tiles (W, then KE; or Z, then KG and QG) that all
-// waves share through LDS. Loads of a tile are issued two phases before it is read
-// and wait in registers in between; the barrier between the phases publishes one
-// tile and frees the other.
-__device__ __forceinline__ float pool_at(const BwdParams& p, int64_t e) {
-  if (p.state_dtype == KDA_STATE_FP8)
-    return f8x2_lo(static_cast<const uint8_t*>(p.pool)[e])[0];
-  const uint16_t b = static_cast<const uint16_t*>(p.pool)[e];
-  return p.state_dtype == KDA_STATE_FP16 ? f16_lo(b) : bf1(b);
-}
-
-constexpr int kTileBytes = 32768;
-constexpr int kChainLds = 3 * kTileBytes + 2 * 1024;
-
-// N 16-byte units per thread, from global memory to registers, and on to LDS.
-template <int N, int T>
-struct Stage {
-  u32x4 u[N];
-  __device__ __forceinline__ void load(const uint8_t* src) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      u[i] = *reinterpret_cast<const u32x4*>(src + (i * T + int(threadIdx.x)) * 16);
-  }
-  __device__ __forceinline__ void store(uint8_t* dst) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      *reinterpret_cast<u32x4*>(dst + (i * T + int(threadIdx.x)) * 16) = u[i];
-  }
-};
-
-// The largest magnitude of a value channel over the four lanes that share it.
-__device__ __forceinline__ float column_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
-}
-
-// Right-side fragments of N accumulator tiles (rows 16 m + 4 g4 + i): pairs of tiles
-// give 32 contraction indices.
-template <int N>
-struct Right {
-  f16x8 hi[N / 2], lo[N / 2];
-  float un;
-  __device__ __forceinline__ void set(const f32x4 (&x)[N]) {
-    float top = 0.f;
-#pragma unroll
-    for (int m = 0; m < N; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[m][i]));
-    const Scale sc = scale_for(column_max(top));
-    un = sc.un;
-#pragma unroll
-    for (int t = 0; t < N / 2; ++t) {
-      u32x2 h0, l0, h1, l1;
-      split4h(x[2 * t] * sc.up, h0, l0);
-      split4h(x[2 * t + 1] * sc.up, h1, l1);
-      hi[t] = join8(h0, h1);
-      lo[t] = join8(l0, l1);
-    }
-  }
-};
-
-template <int NW, int NT>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, 2)))
-void chain_kernel(BwdParams p, DocOrder ord) {
-  constexpr int T = 64 * NW;
-  constexpr int PARTS = 8 / (NW * NT);
-  constexpr int NA = kTileBytes / 16 / T;
-  extern __shared__ __align__(16) float smem_raw[];
-  uint8_t* la = reinterpret_cast<uint8_t*>(smem_raw);
-  uint8_t* lb = la + kTileBytes;
-  float* tails = reinterpret_cast<float*>(lb + 2 * kTileBytes);  // of even and odd chunks
-
-  // Chain c's parts are blocks (c / 8 * PARTS + part) * 8 + c % 8: blocks go to the
-  // eight XCDs in turn, so the parts share one L2 copy of the operands.
-  const int64_t bid = blockIdx.x;
-  const int64_t id = bid / (8 * PARTS) * 8 + (bid & 7);
-  const int part = int((bid >> 3) % PARTS);
-  const bool down = id & 1;
-  const int64_t chain = id >> 1;
-  if (chain >= int64_t(p.n_docs) * p.H) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g4 = lane >> 4, n16 = lane & 15;
-  const int vt0 = (part * NW + wave) * NT;  // this wave's first value tile
-  const int h = int(chain % p.H);
-  const int rank = int(chain / p.H);
-  const int doc = ord.n > 0 ? ord.doc[rank] : rank;
-  const int64_t t0 = p.cu_seqlens[doc];
-  const int64_t len = int64_t(p.cu_seqlens[doc + 1]) - t0;
-  const int32_t slot = p.state_indices[doc];
-  const bool active = slot >= 0 && int64_t(slot) < p.num_slots;
-  const int64_t chunks = (len + C - 1) / C;
-  const int64_t state = (int64_t(doc) * p.H + h) * HEAD_ELEMS + (16 * vt0 + n16) * D + 4 * g4;
-  const int64_t step = int64_t(p.H) * kOps;
-  uint8_t* ops0 = p.ops + (doc_slot0(p.cu_seqlens, doc) * p.H + h) * int64_t(kOps);
-
-  f32x4 s[NT][8];  // [key 16 m + 4 g4 + i][value 16 (vt0 + n) + n16]
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int m = 0; m < 8; ++m) s[n][m] = zero4();
-
-  const uint8_t* left = la + lane * 16;
-  const uint8_t* left2 = lb + lane * 16;
-  auto frag = [](const uint8_t* base, int unit) {
-    return *reinterpret_cast<const f16x8*>(base + unit * 1024);
-  };
-  // acc[r] = sum over keys of tile A's row block r times the state
-  auto product_a = [&](const Right<8> (&b)[NT], f32x4 (&acc)[NT][NB]) {
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-      for (int r = 0; r < NB; ++r) {
-        const f16x8 ah = frag(left, (r * 4 + kt) * 2), al = frag(left, (r * 4 + kt) * 2 + 1);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (kt == 0) acc[n][r] = zero4();
-          acc[n][r] = mfma32(al, b[n].hi[kt], acc[n][r]);
-          acc[n][r] = mfma32(ah, b[n].lo[kt], acc[n][r]);
-          acc[n][r] = mfma32(ah, b[n].hi[kt], acc[n][r]);
-        }
-      }
-  };
-  // s = e^Gl s + sign * (tile B's first half)^T b, or with the second half on o too
-  auto update = [&](const Right<NB> (&b)[NT], float sign, const f16x8 (*o)[2],
-                    const float* uno, const float* tail) {
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      f32x4 acc[NT], acc2[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n] = acc2[n] = zero4();
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const f16x8 ah = frag(left2, (m * 2 + t) * 2), al = frag(left2, (m * 2 + t) * 2 + 1);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n] = mfma32(al, b[n].hi[t], acc[n]);
-          acc[n] = mfma32(ah, b[n].lo[t], acc[n]);
-          acc[n] = mfma32(ah, b[n].hi[t], acc[n]);
-        }
-        if (o) {
-          const f16x8 qh = frag(left2, 32 + (m * 2 + t) * 2), ql = frag(left2, 33 + (m * 2 + t) * 2);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc2[n] = mfma32(ql, o[n][t], acc2[n]);
-            acc2[n] = mfma32(qh, o[n][t], acc2[n]);
-          }
-        }
-      }
-      const f32x4 eg = lds4(tail + 16 * m + 4 * g4);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float un = b[n].un * (sign * kFixedUn);
-        s[n][m] *= eg;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][m][i] = fmaf(acc[n][i], un, s[n][m][i]);
-        if (o)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][m][i] = fmaf(acc2[n][i], uno[n], s[n][m][i]);
-      }
-    }
-  };
-
-  if (!down) {
-    if (!active || len == 0) return;
-    if (p.use_initial) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int64_t e = int64_t(slot) * p.slot_stride + int64_t(h) * HEAD_ELEMS +
-                          (16 * (vt0 + n) + n16) * D + 4 * g4;
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][m][i] = pool_at(p, e + 16 * m + i);
-      }
-    }
-    Stage<NA, T> sa, sb;
-    u32x4 st = {0u, 0u, 0u, 0u};
-    auto load_a = [&](int64_t n) {
-      sa.load(ops0 + n * step + kOpW);
-      if (threadIdx.x < 64) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + threadIdx.x * 16);
-    };
-    auto store_a = [&](int64_t n) {
-      sa.store(la);
-      if (threadIdx.x < 64) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + threadIdx.x * 4) = st;
-    };
-    f32x4 x[NT][NB];  // T V of the next chunk, asked for a phase ahead
-    auto load_x = [&](int64_t n) {
-      const float* X = reinterpret_cast<const float*>(ops0 + n * step + kOpX) +
-                       (vt0 * NB * 64 + lane) * 4;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < NB; ++r) x[j][r] = lds4(X + (j * NB + r) * 256);
-    };
-    load_a(0);
-    load_x(0);
-    store_a(0);
-    sb.load(ops0 + kOpKE);
-    __syncthreads();
-    for (int64_t n = 0; n < chunks; ++n) {
-      uint8_t* ops = ops0 + n * step;
-      const bool more = n + 1 < chunks;
-      const float* tail = tails + (n & 1) * 256;
-      float* S = reinterpret_cast<float*>(ops + kOpS) + 4 * g4 * D + 16 * vt0 + n16;
-      float* X = reinterpret_cast<float*>(ops + kOpX) + (vt0 * NB * 64 + lane) * 4;
-      // ---- x = T V - W S
-      if (more) load_a(n + 1);
-      {
-        Right<8> b[NT];
-        f32x4 acc[NT][NB];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j].set(s[j]);
-#pragma unroll
-          for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[(16 * m + i) * D + 16 * j] = s[j][m][i];
-        }
-        product_a(b, acc);
-        const float unw = tail[kTailUnW];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int r = 0; r < NB; ++r) {
-            const float un = -b[j].un * unw;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[j][r][i] = fmaf(acc[j][r][i], un, x[j][r][i]);
-            *reinterpret_cast<f32x4*>(X + (j * NB + r) * 256) = x[j][r];
-          }
-      }
-      if (!more) return;  // the state after the last chunk is not needed
-      sb.store(lb);
-      __syncthreads();
-      // ---- S = e^Gl S + KE^T (beta x)
-      {
-        Right<NB> b[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-          for (int r = 0; r < NB; ++r) x[j][r] *= lds4(tail + kTailBeta + 16 * r + 4 * g4);
-          b[j].set(x[j]);
-        }
-        load_x(n + 1);
-        sb.load(ops + step + kOpKE);
-        update(b, 1.0f, nullptr, nullptr, tail);
-      }
-      store_a(n + 1);
-      __syncthreads();
-    }
-    return;
-  }
-
-  if (p.d_final && active) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][m][i] = p.d_final[state + n * 16 * D + 16 * m + i];
-  }
-  if (active && chunks > 0) {
-    Stage<NA, T> sa;
-    Stage<2 * NA, T> sb;
-    u32x4 st = {0u, 0u, 0u, 0u};
-    auto load_a = [&](int64_t n) {
-      sa.load(ops0 + n * step + kOpZ);
-      if (threadIdx.x < 64) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + threadIdx.x * 16);
-    };
-    auto store_a = [&](int64_t n) {
-      sa.store(la);
-      if (threadIdx.x < 64) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + threadIdx.x * 4) = st;
-    };
-    f32x4 x[NT][NB];  // T^T P^T dO and dO of the next chunk
-    uint16_t ow[NT][NB][4];
-    auto load_x = [&](int64_t n) {
-      const float* DV = reinterpret_cast<const float*>(ops0 + n * step + kOpDV) +
-                        (vt0 * NB * 64 + lane) * 4;
-      const int c = int(min<int64_t>(C, len - n * C));
-      const uint16_t* o = p.dout + (t0 + n * C) * p.dout_stride + h * D + 16 * vt0 + n16;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < NB; ++r) {
-          x[j][r] = lds4(DV + (j * NB + r) * 256);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            ow[j][r][i] = o[min(16 * r + 4 * g4 + i, c - 1) * p.dout_stride + 16 * j];
-        }
-    };
-    load_a(chunks - 1);
-    load_x(chunks - 1);
-    store_a(chunks - 1);
-    sb.load(ops0 + (chunks - 1) * step + kOpKG);
-    __syncthreads();
-    for (int64_t n = chunks - 1; n >= 0; --n) {
-      uint8_t* ops = ops0 + n * step;
-      const int c = int(min<int64_t>(C, len - n * C));
-      const float* tail = tails + (n & 1) * 256;
-      float* dS = reinterpret_cast<float*>(ops + kOpDS) + 4 * g4 * D + 16 * vt0 + n16;
-      float* DV = reinterpret_cast<float*>(ops + kOpDV) + (vt0 * NB * 64 + lane) * 4;
-      // ---- dV = T^T P^T dO + Z dS
-      if (n > 0) load_a(n - 1);
-      {
-        Right<8> b[NT];
-        f32x4 acc[NT][NB];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j].set(s[j]);
-#pragma unroll
-          for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dS[(16 * m + i) * D + 16 * j] = s[j][m][i];
-        }
-        product_a(b, acc);
-        const float unz = tail[kTailUnZ];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int r = 0; r < NB; ++r) {
-            const float un = b[j].un * unz;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[j][r][i] = fmaf(acc[j][r][i], un, x[j][r][i]);
-            *reinterpret_cast<f32x4*>(DV + (j * NB + r) * 256) = x[j][r];
-          }
-      }
-      if (n == 0 && !p.d_initial) return;
-      sb.store(lb);
-      __syncthreads();
-      // ---- dS = e^Gl dS - KG^T dV + scale QG^T dO
-      {
-        Right<NB> b[NT];
-        f16x8 o[NT][2];
-        float uno[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j].set(x[j]);
-          // dO has 8 bits: its high part alone is exact
-          f32x4 y[NB];
-          float top = 0.f;
-#pragma unroll
-          for (int r = 0; r < NB; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[r][i] = 16 * r + 4 * g4 + i < c ? bf1(ow[j][r][i]) : 0.f;
-              top = fmaxf(top, fabsf(y[r][i]));
-            }
-          const Scale sc = scale_for(column_max(top));
-          uno[j] = sc.un * (p.scale * kFixedUn);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const f32x4 a = y[2 * t] * sc.up, d = y[2 * t + 1] * sc.up;
-            o[j][t] = __builtin_bit_cast(
-                f16x8, u32x4{pack_f16x2(a[0], a[1]), pack_f16x2(a[2], a[3]),
-                             pack_f16x2(d[0], d[1]), pack_f16x2(d[2], d[3])});
-          }
-        }
-        if (n > 0) {
-          load_x(n - 1);
-          sb.load(ops - step + kOpKG);
-        }
-        update(b, -1.0f, o, uno, tail);
-      }
-      if (n > 0) store_a(n - 1);
-      __syncthreads();
-    }
-  }
-  if (p.d_initial) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-        *reinterpret_cast<f32x4*>(p.d_initial + state + n * 16 * D + 16 * m) = s[n][m];
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Gradients: one workgroup per (chunk, head); a wave owns 16 key channels of all
-// tokens, so that the decays and the sums over tokens stay in its registers.
-struct GradSmem {
-  float dO[C * RS], dV[C * RS], x[C * RS];
-  float dp[C * AS], da[C * AS];
-  float red[4][8][C];  // sums over a wave's 16 channels, per token
-  float diag[C];       // DP's diagonal
-  float rq[C], rk[C], beta[C];
-};
-
-__device__ __forceinline__ void zero_row(uint16_t* p, int64_t t, int64_t stride, int64_t at, int n) {
-  for (int e = threadIdx.x; e < n; e += kThreads) p[t * stride + at + e] = 0;
-}
-
-__global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
-  extern __shared__ __align__(16) float smem_raw[];
-  GradSmem& s = *reinterpret_cast<GradSmem*>(smem_raw);
-  const int64_t sigma = blockIdx.x;
-  const int h = blockIdx.y;
-  const Chunk ch = chunk_of(p, sigma);
-  float* partial = p.partial + (sigma * p.H + h) * int64_t(2 * D);
-  const bool per_head = p.gate_mode & KDA_GATE_PER_HEAD;
-  if (ch.c == 0 || !ch.active) {
-    if (threadIdx.x < 2 * D) partial[threadIdx.x] = 0.f;
-    for (int t = 0; t < ch.c; ++t) {
-      zero_row(p.dq, ch.t0 + t, p.dq_stride, int64_t(h) * D, D);
-      zero_row(p.dk, ch.t0 + t, p.dk_stride, int64_t(h) * D, D);
-      zero_row(p.dv, ch.t0 + t, p.dv_stride, int64_t(h) * D, D);
-      zero_row(p.dg, ch.t0 + t, p.dg_stride, per_head ? h : int64_t(h) * D, per_head ? 1 : D);
-      zero_row(p.dbeta, ch.t0 + t, p.dbeta_stride, h, 1);
-    }
-    return;
-  }
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int g4 = lane >> 4, n16 = lane & 15;
-  const int kc = 16 * w + n16;
-  const uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
-
-  token_scalars(p, ch, h, s.rq, s.rk, s.beta);
-  {
-    // wave w brings value tile w: accumulator tiles to rows of tokens
-    const float* X = reinterpret_cast<const float*>(ops + kOpX) + (w * NB * 64 + lane) * 4;
-    const float* DV = reinterpret_cast<const float*>(ops + kOpDV) + (w * NB * 64 + lane) * 4;
-#pragma unroll
-    for (int r = 0; r < NB; ++r) {
-      const f32x4 x = lds4(X + r * 256), dv = lds4(DV + r * 256);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s.x[(16 * r + 4 * g4 + i) * RS + kc] = x[i];
-        s.dV[(16 * r + 4 * g4 + i) * RS + kc] = dv[i];
-      }
-    }
-    const int c0 = (threadIdx.x & 15) * 8;
-#pragma unroll
-    for (int j = 0; j < C / (kThreads / 16); ++j) {
-      const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
-      u32x4 ow = *reinterpret_cast<const u32x4_u*>(
-          p.dout + (ch.t0 + min(t, ch.c - 1)) * p.dout_stride + h * D + c0);
-      if (t >= ch.c) ow = u32x4{0u, 0u, 0u, 0u};
-      float o[8];
-      unpack8_bf16(ow, o);
-      *reinterpret_cast<f32x4*>(s.dO + t * RS + c0) = f32x4{o[0], o[1], o[2], o[3]};
-      *reinterpret_cast<f32x4*>(s.dO + t * RS + c0 + 4) = f32x4{o[4], o[5], o[6], o[7]};
-    }
-  }
-  __syncthreads();
-  {
-    const int c0 = (threadIdx.x & 15) * 8;
-    for (int t = threadIdx.x >> 4; t < ch.c; t += kThreads / 16) {
-      const f32x4 a = lds4(s.dV + t * RS + c0), b = lds4(s.dV + t * RS + c0 + 4);
-      *reinterpret_cast<u32x4_u*>(p.dv + (ch.t0 + t) * p.dv_stride + h * D + c0) =
-          u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
-                pack_bf16x2(b[2], b[3])};
-    }
-  }
-
-  // ---- DP = tril(dO x^T), DA = -tril(dV x^T, -1). A token's use of its own key has no
-  // decay: DP's diagonal is kept apart, out of the sums that give dg.
-  for (int task = w; task < NB * (NB + 1); task += kThreads / 64) {
-    const bool is_p = task >= NB * (NB + 1) / 2;
-    int I = 0, J = is_p ? task - NB * (NB + 1) / 2 : task;
-    while (J > I) J -= ++I;
-    const float* left = (is_p ? s.dO : s.dV) + (16 * I + n16) * RS + 4 * g4;
-    const float* right = s.x + (16 * J + n16) * RS + 4 * g4;
-    f32x4 acc = zero4();
-#pragma unroll
-    for (int m = 0; m < D / 16; ++m) acc = mfma4(lds4(left + 16 * m), lds4(right + 16 * m), acc);
-    if (!is_p) acc = -acc;
-    float* dst = (is_p ? s.dp : s.da) + (16 * I + 4 * g4) * AS + 16 * J + n16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int over = I == J ? n16 - (4 * g4 + i) : -1;
-      dst[i * AS] = over < 0 ? acc[i] : 0.f;
-      if (is_p && over == 0) s.diag[16 * I + n16] = acc[i];
-    }
-  }
-
-  // ---- dO S^T, dV S^T, x dS^T for the wave's channels
-  f32x4 sq[NB], sk[NB], se[NB];
-  float last = 0.f;  // e^Gl sum_v S dS, later with the writers' part
-  {
-#pragma unroll
-    for (int r = 0; r < NB; ++r) sq[r] = sk[r] = se[r] = zero4();
-    const float* S = reinterpret_cast<const float*>(ops + kOpS) + kc * D + 4 * g4;
-    const float* dS = reinterpret_cast<const float*>(ops + kOpDS) + kc * D + 4 * g4;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const f32x4 a = lds4(S + 16 * m), b = lds4(dS + 16 * m);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) last = fmaf(a[i], b[i], last);
-#pragma unroll
-      for (int r = 0; r < NB; ++r) {
-        const int at = (16 * r + n16) * RS + 16 * m + 4 * g4;
-        sq[r] = mfma4(lds4(s.dO + at), a, sq[r]);
-        sk[r] = mfma4(lds4(s.dV + at), a, sk[r]);
-        se[r] = mfma4(lds4(s.x + at), b, se[r]);
-      }
-    }
-    last = rows_sum(last) * reinterpret_cast<const float*>(ops + kOpTail)[kc];
-  }
-  Lane ln;
-  load_lane<true>(p, ch, h, kc, g4, s.rq, s.rk, ln);
-  __syncthreads();
-
-  // ---- inside the chunk: readers' rows and writers' columns
-  f32x4 up[NB], km[NB], qm[NB], kb[NB];
-  float bt[NB][4];
-  float fI[NB], tJ[NB];  // e^(from the chunk's start to the block's middle), (to the end)
-  {
-    float o = 0.f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      fI[b] = expf(o + 0.5f * ln.tau[b]);
-      o += ln.tau[b];
-    }
-    o = 0.f;
-#pragma unroll
-    for (int b = NB - 1; b >= 0; --b) {
-      tJ[b] = expf(o + 0.5f * ln.tau[b]);
-      o += ln.tau[b];
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = ln.lam[b][i] - 0.5f * ln.tau[b];
-        bt[b][i] = s.beta[16 * b + 4 * g4 + i];
-        up[b][i] = expf(x);
-        km[b][i] = ln.k[b][i] * up[b][i];
-        ln.q[b][i] *= p.scale;  // q'
-        qm[b][i] = ln.q[b][i] * up[b][i];
-        kb[b][i] = ln.k[b][i] * expf(-x) * bt[b][i];
-      }
-  }
-  f32x4 cq[NB], ck[NB], cc[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) cq[b] = ck[b] = cc[b] = zero4();
-#pragma unroll
-  for (int I = 0; I < NB; ++I) {
-    float mid = 0.f;
-#pragma unroll
-    for (int J = I; J >= 0; --J) {
-      f32x4 kj = kb[J], ki = km[I], qi = qm[I];
-      if (J < I) {
-        const float f = expf(0.5f * (ln.tau[I] + ln.tau[J]) + mid);
-        mid += ln.tau[J];
-        kj *= f;
-        ki *= f;
-        qi *= f;
-      }
-      const int row = (16 * I + n16) * AS + 16 * J + 4 * g4;
-      const int col = (16 * I + 4 * g4) * AS + 16 * J + n16;
-      cq[I] = mfma4(lds4(s.dp + row), kj, cq[I]);
-      ck[I] = mfma4(lds4(s.da + row), kj, ck[I]);
-      cc[J] = mfma4(col4(s.dp + col, AS), qi, cc[J]);
-      cc[J] = mfma4(col4(s.da + col, AS), ki, cc[J]);
-    }
-  }
-
-  // ---- put together; sums over the channels per token through LDS
-  float dG[NB][4];
-  float ends = 0.f;
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = up[b][i];
-      const float down = expf(0.5f * ln.tau[b] - ln.lam[b][i]);
-      const float end = down * tJ[b] * se[b][i];
-      const float self = s.diag[16 * b + 4 * g4 + i];
-      float dq = e * fmaf(fI[b], sq[b][i], cq[b][i]);         // dq'
-      const float dr = e * fmaf(-fI[b], sk[b][i], ck[b][i]);  // drow
-      float col = fmaf(down, cc[b][i], end);
-      const float kbeta = ln.k[b][i] * bt[b][i];
-      ends = fmaf(kbeta, end, ends);
-      dG[b][i] = ln.q[b][i] * dq + ln.k[b][i] * dr - kbeta * col;
-      dq = fmaf(self, kbeta, dq);
-      col = fmaf(self, ln.q[b][i], col);
-      cq[b][i] = dq * p.scale;
-      ck[b][i] = fmaf(bt[b][i], col, dr);
-      const float a0 = row16_sum(ln.q[b][i] * dq);  // q_hat . dq_hat
-      const float a1 = row16_sum(ln.k[b][i] * ck[b][i]);
-      const float a2 = row16_sum(ln.k[b][i] * col);
-      if (n16 == 0) {
-        const int t = 16 * b + 4 * g4 + i;
-        s.red[0][w][t] = a0;
-        s.red[1][w][t] = a1;
-        s.red[2][w][t] = a2;
-      }
-    }
-  // dg: the suffix sums over the chunk's tokens
-  float sum_b = 0.f, sum_a = 0.f;  // of ddt_bias, dA_log
-  {
-    float after = last + rows_sum(ends);
-#pragma unroll
-    for (int b = NB - 1; b >= 0; --b) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 3; i >= 0; --i) {
-        sum += dG[b][i];
-        dG[b][i] = sum;
-      }
-      const float s1 = __shfl_xor(sum, 16);
-      const float pair = sum + s1;
-      const float other = __shfl_xor(pair, 32);
-      const float later = after + ((g4 & 1) ? 0.f : s1) + ((g4 & 2) ? 0.f : other);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float dg = dG[b][i] + later;
-        dG[b][i] = dg;
-        const float inside = ln.slope[b][i] != 0.f ? ln.g[b][i] : 0.f;
-        sum_b = fmaf(dg, ln.slope[b][i], sum_b);
-        sum_a = fmaf(dg, inside, sum_a);
-        if (per_head) {
-          const float a3 = row16_sum(dg);
-          if (n16 == 0) s.red[3][w][16 * b + 4 * g4 + i] = a3;
-        }
-      }
-      after += pair + other;
-    }
-  }
-  sum_b = rows_sum(sum_b);
-  sum_a = rows_sum(sum_a);
-  if (g4 == 0) {
-    partial[kc] = sum_b;
-    partial[D + kc] = sum_a;
-  }
-  __syncthreads();
-  if (threadIdx.x < C * 4) {  // add the eight waves' sums
-    const int which = threadIdx.x / C, t = threadIdx.x % C;
-    if (which < 3 || per_head) {
-      float x = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x += s.red[which][i][t];
-      s.red[which][0][t] = x;
-      if (which == 2 && t < ch.c) {
-        if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) x *= s.beta[t] * (1.f - s.beta[t]);
-        p.dbeta[(ch.t0 + t) * p.dbeta_stride + h] = to_bf16(x);
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * b + 4 * g4 + i;
-      if (t < ch.c) {
-        // q' = scale q_hat: q_hat (q_hat . dq_hat) from q' and its dot product
-        const float rq = s.rq[t], rk = s.rk[t];
-        const float qhat = bf1(p.q[(ch.t0 + t) * p.q_stride + h * D + kc]) * rq;
-        const float dq = rq * fmaf(-qhat, s.red[0][0][t], cq[b][i]);
-        const float dk = rk * fmaf(-ln.k[b][i], s.red[1][0][t], ck[b][i]);
-        p.dq[(ch.t0 + t) * p.dq_stride + h * D + kc] = to_bf16(dq);
-        p.dk[(ch.t0 + t) * p.dk_stride + h * D + kc] = to_bf16(dk);
-        if (!per_head)
-          p.dg[(ch.t0 + t) * p.dg_stride + h * D + kc] = to_bf16(dG[b][i] * ln.slope[b][i]);
-        else if (w == 0 && n16 == 0)
-          p.dg[(ch.t0 + t) * p.dg_stride + h] = to_bf16(s.red[3][0][t] * ln.slope[b][i]);
-      }
-    }
-}
-
-// dA_log and ddt_bias: the partial sums of a head, added in the order of the chunk
-// slots by 8 groups of 128 lanes (a channel each), then group by group.
-__global__ __launch_bounds__(1024) void param_kernel(BwdParams p) {
-  __shared__ float sum[2][8][D];
-  __shared__ float half[4];
-  const int h = blockIdx.x;
-  const int c = threadIdx.x & (D - 1), grp = threadIdx.x / D;
-  float b = 0.f, a = 0.f;
-  for (int64_t n = grp; n < p.slots; n += 8) {
-    const float* x = p.partial + (n * p.H + h) * int64_t(2 * D);
-    b += x[c];
-    a += x[D + c];
-  }
-  sum[0][grp][c] = b;
-  sum[1][grp][c] = a;
-  __syncthreads();
-  const bool per_head = p.gate_mode & KDA_GATE_PER_HEAD;
-  float t = 0.f;
-  if (grp < 2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += sum[grp][i][c];
-    if (grp == 0 && !per_head && p.ddt_bias) p.ddt_bias[h * D + c] = t;
-    // a head's one value: the sum over its channels
-    t = rows_sum(row16_sum(t));
-    if ((threadIdx.x & 63) == 0) half[threadIdx.x >> 6] = t;
-  }
-  __syncthreads();
-  if (grp < 2 && c == 0) {
-    t = half[2 * grp] + half[2 * grp + 1];
-    if (grp == 1 && p.dA_log) p.dA_log[h] = t;
-    if (grp == 0 && per_head && p.ddt_bias) p.ddt_bias[h] = t;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// host
 
 int64_t slots_of(int32_t n_docs, int64_t total_tokens) { return n_docs + total_tokens / C; }
 
-// Dynamic LDS beyond 64 KiB is allowed once per kernel.
-hipError_t allow_lds() {
-  static const hipError_t e = [] {
-    const struct { const void* f; size_t bytes; } all[] = {
-        {reinterpret_cast<const void*>(prep_kernel), sizeof(PrepSmem)},
-        {reinterpret_cast<const void*>(grad_kernel), sizeof(GradSmem)},
-        {reinterpret_cast<const void*>(chain_kernel<2, 1>), kChainLds},
-        {reinterpret_cast<const void*>(chain_kernel<4, 1>), kChainLds},
-        {reinterpret_cast<const void*>(chain_kernel<4, 2>), kChainLds}};
-    for (const auto& k : all)
-      if (const hipError_t a = hipFuncSetAttribute(
-              k.f, hipFuncAttributeMaxDynamicSharedMemorySize, int(k.bytes)))
-        return a;
-    return hipSuccess;
-  }();
-  return e;
-}
-
-template <int NW, int NT>
-void launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
-  constexpr int PARTS = 8 / (NW * NT);
-  const int64_t ids = (int64_t(p.n_docs) * p.H * 2 + 7) / 8 * 8;  // both directions
-  hipLaunchKernelGGL((chain_kernel<NW, NT>), dim3(unsigned(ids * PARTS)), dim3(64 * NW), kChainLds,
-                     stream, p, ord);
-}
-
 hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32_t* cu_host,
                            hipStream_t stream) {
-  if (const hipError_t e = allow_lds()) return e;
   const int64_t chains = int64_t(p.n_docs) * p.H;
   if (p.slots > 0x7fffffff || chains > 0x7fffffff / 16) return hipErrorInvalidValue;
   DocOrder ord;
@@ -1324,32 +69,22 @@ hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32
     }
     ord.n = p.n_docs;
   }
-  if (total_tokens > 0) {
-    hipLaunchKernelGGL(prep_kernel, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
-                       sizeof(PrepSmem), stream, p);
-    if (const hipError_t e = hipGetLastError()) return e;
-  }
-  if (total_tokens > 0 || p.d_initial) {
-    // workgroups per chain and direction: as many as it takes to fill the chip
-    if (chains <= 32) launch_chain<2, 1>(p, ord, stream);
-    else if (chains <= 128) launch_chain<4, 1>(p, ord, stream);
-    else launch_chain<4, 2>(p, ord, stream);
-    if (const hipError_t e = hipGetLastError()) return e;
-  }
-  if (total_tokens > 0) {
-    hipLaunchKernelGGL(grad_kernel, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
-                       sizeof(GradSmem), stream, p);
-    if (const hipError_t e = hipGetLastError()) return e;
-  }
+  if (total_tokens > 0)
+    if (const hipError_t e = launch_prep(p, stream)) return e;
+  if (total_tokens > 0 || p.d_initial)
+    if (const hipError_t e = launch_chains(p, ord, stream)) return e;
+  if (total_tokens > 0)
+    if (const hipError_t e = launch_grads(p, stream)) return e;
   if (p.dA_log || p.ddt_bias) {
     BwdParams all = p;
     if (total_tokens == 0) all.slots = 0;  // nothing was written: the sums are zero
-    hipLaunchKernelGGL(param_kernel, dim3(unsigned(p.H)), dim3(1024), 0, stream, all);
+    return launch_params(all, stream);
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace
+}  // namespace bwd
 }  // namespace kda
 
 extern "C" size_t kda_prefill_backward_workspace_size(int32_t n_docs, int64_t total_tokens,
@@ -1357,7 +92,7 @@ extern "C" size_t kda_prefill_backward_workspace_size(int32_t n_docs, int64_t to
   if (n_docs < 0 || total_tokens < 0 || total_tokens > INT32_MAX || H < 1 || H > 65535 ||
       K != kda::D || V != kda::D)
     return 0;
-  return size_t(kda::slots_of(n_docs, total_tokens)) * size_t(H) * (kda::kOps + 2 * kda::D * 4);
+  return size_t(kda::bwd::slots_of(n_docs, total_tokens)) * size_t(H) * (kda::bwd::kOps + 2 * kda::D * 4);
 }
 
 extern "C" kda_status kda_prefill_varlen_backward(
@@ -1376,11 +111,11 @@ extern "C" kda_status kda_prefill_varlen_backward(
   using kda::D;
   if (n_docs < 0 || total_tokens < 0 || H < 1 || num_slots < 0) return KDA_ERR_BAD_SHAPE;
   if (K != D || V != D || H > 65535) return KDA_ERR_UNSUPPORTED;
-  if (!(lower_bound >= -5.5f && lower_bound <= 5.5f)) return KDA_ERR_UNSUPPORTED;
+  if (!(lower_bound >= -5.5f && lower_bound <= 0.0f)) return KDA_ERR_UNSUPPORTED;
   if (gate_mode & ~(KDA_GATE_PRECOMPUTED | KDA_BETA_PRESIGMOID | KDA_GATE_PER_HEAD))
     return KDA_ERR_UNSUPPORTED;
   const bool pre = gate_mode & KDA_GATE_PRECOMPUTED;
-  if (pre && (lower_bound > 0.0f || dA_log || ddt_bias)) return KDA_ERR_UNSUPPORTED;
+  if (pre && (dA_log || ddt_bias)) return KDA_ERR_UNSUPPORTED;
   if (state_dtype < KDA_STATE_BF16 || state_dtype > KDA_STATE_FP8) return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens_host) return KDA_ERR_NULL_POINTER;
   if (cu_seqlens_host[0] != 0) return KDA_ERR_BAD_SEQLENS;
@@ -1400,10 +135,16 @@ extern "C" kda_status kda_prefill_varlen_backward(
                           beta_tok_stride, d_out_tok_stride, slot_stride};
     for (const int64_t s : in)
       if (s < 0) return KDA_ERR_BAD_STRIDE;
+    // a chunk's rows are addressed by 32-bit offsets
+    constexpr int64_t kMaxStride = int64_t(1) << 25;
+    for (int i = 0; i < 6; ++i)
+      if (in[i] > kMaxStride) return KDA_ERR_UNSUPPORTED;
     const int64_t out[][2] = {{dq_tok_stride, W}, {dk_tok_stride, W}, {dv_tok_stride, W},
                               {dg_tok_stride, gw}, {dbeta_tok_stride, H}};
     for (const auto& s : out)
       if (s[0] < 0 || (total_tokens > 1 && s[0] < s[1])) return KDA_ERR_BAD_STRIDE;
+    for (const auto& s : out)
+      if (s[0] > kMaxStride) return KDA_ERR_UNSUPPORTED;
     if (use_initial_state && num_slots > 1 && slot_stride < W * D) return KDA_ERR_BAD_STRIDE;
     if (reinterpret_cast<uintptr_t>(d_initial_state) & 15u) return KDA_ERR_UNSUPPORTED;
     if (total_tokens > 0) {
@@ -1414,10 +155,10 @@ extern "C" kda_status kda_prefill_varlen_backward(
     }
   }
 
-  kda::BwdParams p;
+  kda::bwd::BwdParams p;
   p.n_docs = n_docs;
   p.H = H;
-  p.slots = kda::slots_of(n_docs, total_tokens);
+  p.slots = kda::bwd::slots_of(n_docs, total_tokens);
   p.cu_seqlens = cu_seqlens;
   p.q = static_cast<const uint16_t*>(q);
   p.k = static_cast<const uint16_t*>(k);
@@ -1458,8 +199,8 @@ extern "C" kda_status kda_prefill_varlen_backward(
   p.d_initial = d_initial_state;
   p.ops = static_cast<uint8_t*>(workspace);
   p.partial = reinterpret_cast<float*>(
-      p.ops + (total_tokens > 0 ? p.slots * int64_t(H) * kda::kOps : 0));
+      p.ops + (total_tokens > 0 ? p.slots * int64_t(H) * kda::bwd::kOps : 0));
   if (n_docs == 0 && !dA_log && !ddt_bias) return KDA_OK;
-  return kda::launch_backward(p, total_tokens, cu_seqlens_host, stream) == hipSuccess
+  return kda::bwd::launch_backward(p, total_tokens, cu_seqlens_host, stream) == hipSuccess
              ? KDA_OK : KDA_ERR_LAUNCH;
 }

@@ -1,0 +1,336 @@
+// Parameter block, workspace layout and device helpers of the prefill gradient's
+// kernels (gfx950). The method is described in kda_backward.hip.
+#pragma once
+
+#include <stdint.h>
+
+#include "../../include/kda_backward.h"
+#include "kda_common.h"
+
+namespace kda {
+namespace bwd {
+
+constexpr int C = 64;        // tokens per chunk
+constexpr int NB = C / 16;   // 16-token blocks per chunk
+constexpr int NP = NB * (NB - 1) / 2;
+constexpr int kThreads = 512;
+constexpr int kMaxOrderedDocs = 256;
+constexpr float kL2Eps = 1e-6f;
+
+struct BwdParams {
+  int32_t n_docs, H;
+  int64_t slots;  // chunk slots: n_docs + total_tokens / C
+  const int32_t* cu_seqlens;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* g;
+  const uint16_t* beta;
+  int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+  const float* A_log;
+  const float* dt_bias;
+  float lower_bound, scale;
+  int32_t gate_mode, state_dtype, use_initial;
+  const void* pool;
+  int64_t num_slots, slot_stride;
+  const int32_t* state_indices;
+  const uint16_t* dout;
+  int64_t dout_stride;
+  const float* d_final;
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* dv;
+  uint16_t* dg;
+  uint16_t* dbeta;
+  int64_t dq_stride, dk_stride, dv_stride, dg_stride, dbeta_stride;
+  float* dA_log;
+  float* ddt_bias;
+  float* d_initial;
+  uint8_t* ops;    // [slot][h][kOps]
+  float* partial;  // [slot][h][2][D]: of ddt_bias and dA_log, per channel
+};
+
+struct DocOrder {
+  int32_t n;  // 0: natural order
+  int32_t doc[kMaxOrderedDocs];
+};
+
+// A (chunk, head)'s part of the workspace, in bytes. The chains' left operands are
+// fp16 high and low parts in fragment order, 16 bytes (8 contraction indices) a lane:
+//   W, Z        [rt 4][kt 4][hi, lo][lane]  token 16 rt + lane % 16, key channels
+//               32 kt + 4 (lane / 16) + 0..3 and 16 further
+//   KE, KG, QG  [m 8][t 2][hi, lo][lane]    key channel 16 m + lane % 16, tokens
+//               32 t + 4 (lane / 16) + 0..3 and 16 further
+// X0 and DV0 are accumulator tiles [vt 8][rt 4][lane][4 tokens], X and DV rows
+// [token][value], S and dS rows [key][value], all fp32.
+constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales of W and Z
+constexpr int kOpW = 1024;               // T e^G k, scaled
+constexpr int kOpKE = kOpW + 32768;      // e^(Gl-G) k, times 2^12
+constexpr int kOpZ = kOpKE + 32768;      // T^T (beta e^(Gl-G) k), scaled
+constexpr int kOpKG = kOpZ + 32768;      // e^G k, times 2^12
+constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat, times 2^12
+constexpr int kOpX0 = kOpQG + 32768;     // T V
+constexpr int kOpDV0 = kOpX0 + 32768;    // T^T P^T dO
+constexpr int kOpX = kOpDV0 + 32768;     // x
+constexpr int kOpDV = kOpX + 32768;      // dV
+constexpr int kOpS = kOpDV + 32768;      // S entering the chunk
+constexpr int kOpDS = kOpS + 65536;      // dS leaving it
+constexpr int kOps = kOpDS + 65536;
+constexpr int kTailBeta = D, kTailUnW = D + C, kTailUnZ = D + C + 1;  // in floats
+
+__device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+__device__ __forceinline__ f32x4 lds4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+// 4 elements down a column
+__device__ __forceinline__ f32x4 col4(const float* p, int stride) {
+  return f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]};
+}
+
+typedef u32x4 u32x4_u __attribute__((aligned(2)));  // any bf16 address
+typedef __fp16 f16x8 __attribute__((__vector_size__(8 * sizeof(__fp16))));  // MFMA operand
+
+// fp32 as fp16 high + low parts: 22 bits and a sign. Three products (high high,
+// high low, low high) then leave out 2^-22 of a term, less than the fp32 additions.
+__device__ __forceinline__ void split4h(f32x4 x, u32x2& hi, u32x2& lo) {
+  hi = u32x2{pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3])};
+  lo = u32x2{pack_f16x2(x[0] - f16_lo(hi[0]), x[1] - f16_hi(hi[0])),
+             pack_f16x2(x[2] - f16_lo(hi[1]), x[3] - f16_hi(hi[1]))};
+}
+__device__ __forceinline__ f16x8 join8(u32x2 a, u32x2 b) {
+  return __builtin_bit_cast(f16x8, u32x4{a[0], a[1], b[0], b[1]});
+}
+__device__ __forceinline__ f32x4 mfma32(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// fp16 holds 2^-24 to 2^16, so operands of any size are scaled by a power of two that
+// brings their largest magnitude to 2^14 .. 2^15; `un` undoes it.
+struct Scale {
+  float up, un;
+};
+__device__ __forceinline__ Scale scale_for(float top) {
+  int e = int(__float_as_uint(top) >> 23);
+  e = e < 40 ? 40 : (e > 250 ? 250 : e);
+  return {__uint_as_float(uint32_t(268 - e) << 23), __uint_as_float(uint32_t(e - 14) << 23)};
+}
+constexpr float kFixedUp = 4096.0f, kFixedUn = 1.0f / 4096.0f;  // operands within +-1
+
+// Sum over the four 16-lane rows of a wave (lanes of equal lane % 16).
+__device__ __forceinline__ float rows_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// First chunk slot of document i; slots of a document follow each other.
+__device__ __forceinline__ int64_t doc_slot0(const int32_t* cu, int i) {
+  return int64_t(i) + int64_t(cu[i]) / C;
+}
+// The document of chunk slot sigma: the largest i <= n_docs with doc_slot0(i) <=
+// sigma (doc_slot0 rises strictly from 0). A wave asks for 64 documents at a time.
+__device__ __forceinline__ int find_doc(const int32_t* cu, int n_docs, int64_t sigma) {
+  int lo = 0, len = n_docs + 1;
+  while (len > 1) {
+    const int stride = (len + 63) / 64;
+    const int off = int(threadIdx.x & 63) * stride;
+    const bool le = off < len && doc_slot0(cu, lo + off) <= sigma;
+    lo += (__builtin_popcountll(__ballot(le)) - 1) * stride;
+    len = min(stride, n_docs + 1 - lo);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+struct Chunk {
+  int doc;
+  int64_t t0;  // first token
+  int c;       // tokens; 0: a slot between documents
+  bool active;
+};
+__device__ __forceinline__ Chunk chunk_of(const BwdParams& p, int64_t sigma) {
+  Chunk ch = {0, 0, 0, false};
+  ch.doc = find_doc(p.cu_seqlens, p.n_docs, sigma);
+  if (ch.doc >= p.n_docs) return ch;
+  const int64_t start = p.cu_seqlens[ch.doc];
+  const int64_t len = int64_t(p.cu_seqlens[ch.doc + 1]) - start;
+  const int64_t off = (sigma - doc_slot0(p.cu_seqlens, ch.doc)) * C;
+  if (off >= len) return ch;
+  ch.t0 = start + off;
+  ch.c = int(min<int64_t>(C, len - off));
+  const int32_t slot = p.state_indices[ch.doc];
+  ch.active = slot >= 0 && int64_t(slot) < p.num_slots;
+  return ch;
+}
+
+// A chunk's rows of a bf16 tensor from channel `col` on: one scalar base and 32-bit lane
+// offsets (the host keeps strides within 2^25 elements, so 64 rows span less than 2^32
+// bytes).
+struct Rows {
+  uint16_t* base;
+  uint32_t stride;
+  __device__ __forceinline__ uint16_t* at(int t, int col) const {
+    return reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(base) +
+                                       (uint32_t(t) * stride + uint32_t(col) * 2u));
+  }
+};
+__device__ __forceinline__ Rows rows_of(const uint16_t* x, const Chunk& ch, int64_t stride,
+                                        int64_t col) {
+  return {const_cast<uint16_t*>(x) + ch.t0 * stride + col, uint32_t(stride * 2)};
+}
+
+// Here and below a chunk's missing tokens read its last one and drop the value: a
+// load behind a branch would be waited for one at a time.
+
+// 1 / |q|, 1 / |k| (with the epsilon) and beta of the chunk's tokens, to LDS: 16
+// lanes per token. Padding rows get zeros.
+__device__ __forceinline__ void token_scalars(const BwdParams& p, const Chunk& ch, int h,
+                                              float* rq, float* rk, float* beta) {
+  constexpr int N = C / (kThreads / 16);
+  const int c0 = (threadIdx.x & 15) * 8;
+  const Rows qr = rows_of(p.q, ch, p.q_stride, int64_t(h) * D);
+  const Rows kr = rows_of(p.k, ch, p.k_stride, int64_t(h) * D);
+  const Rows br = rows_of(p.beta, ch, p.beta_stride, h);
+  u32x4 qw[N], kw[N];
+  uint16_t bw[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int t = min(int(threadIdx.x >> 4) + j * (kThreads / 16), ch.c - 1);
+    qw[j] = *reinterpret_cast<const u32x4_u*>(qr.at(t, c0));
+    kw[j] = *reinterpret_cast<const u32x4_u*>(kr.at(t, c0));
+    bw[j] = *br.at(t, 0);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+    float x[8], sq = 0.f, sk = 0.f;
+    unpack8_bf16(qw[j], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+    unpack8_bf16(kw[j], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sk = fmaf(x[i], x[i], sk);
+    sq = row16_sum(sq);
+    sk = row16_sum(sk);
+    if ((threadIdx.x & 15) == 0) {
+      float b = bf1(bw[j]);
+      if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) b = sigmoidf(b);
+      rq[t] = t < ch.c ? 1.0f / sqrtf(sq + kL2Eps) : 0.f;
+      rk[t] = t < ch.c ? 1.0f / sqrtf(sk + kL2Eps) : 0.f;
+      beta[t] = t < ch.c ? b : 0.f;
+    }
+  }
+}
+
+// A lane's share of the chunk: key channel `kc`, tokens 16 b + 4 g4 + i.
+struct RawLane {
+  uint16_t k[NB][4], q[NB][4], g[NB][4];
+};
+__device__ __forceinline__ int64_t gate_channel(const BwdParams& p, int h, int kc) {
+  return (p.gate_mode & KDA_GATE_PER_HEAD) ? h : int64_t(h) * D + kc;
+}
+__device__ __forceinline__ void load_lane(const BwdParams& p, const Chunk& ch, int h, int kc,
+                                          int g4, RawLane& raw) {
+  const bool head = p.gate_mode & KDA_GATE_PER_HEAD;
+  const Rows qr = rows_of(p.q, ch, p.q_stride, int64_t(h) * D);
+  const Rows kr = rows_of(p.k, ch, p.k_stride, int64_t(h) * D);
+  const Rows gr = rows_of(p.g, ch, p.g_stride, head ? h : int64_t(h) * D);
+  const int gc = head ? 0 : kc;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = min(16 * b + 4 * g4 + i, ch.c - 1);
+      raw.k[b][i] = *kr.at(t, kc);
+      raw.q[b][i] = *qr.at(t, kc);
+      raw.g[b][i] = *gr.at(t, gc);
+    }
+}
+
+// Decays are products of a_t = e^g_t, never exponentials of sums: 16 factors keep a
+// relative error of a few 2^-24 where a sum of 16 gates of size 5 would lose ten times
+// that. `up` reaches from the middle of the token's block (after its 8th token)
+// to the token, its inverse back; both lie within e^(+-44). head and tail are the
+// block's two halves.
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
+
+struct Lane {
+  float k[NB][4], q[NB][4];  // k_hat, q_hat
+  float up[NB][4];
+  float head[NB], tail[NB];
+};
+// With SLOPE, `keep` takes each token's log-decay and its derivative by the gate input:
+// 2 x 16 floats per thread, kThreads apart.
+template <bool SLOPE>
+__device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, int h, int kc,
+                                          int g4, const RawLane& raw, const float* rq,
+                                          const float* rk, Lane& ln, float* keep) {
+  const bool pre = p.gate_mode & KDA_GATE_PRECOMPUTED;
+  const float ea = pre ? 0.f : expf(p.A_log[h]);
+  const float dtb = pre ? 0.f : p.dt_bias[gate_channel(p, h, kc)];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    __builtin_amdgcn_sched_barrier(0);  // a block at a time: the raw values make room
+    const f32x4 rq4 = lds4(rq + 16 * b + 4 * g4), rk4 = lds4(rk + 16 * b + 4 * g4);
+    float a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * b + 4 * g4 + i;
+      const bool valid = t < ch.c;
+      ln.k[b][i] = valid ? bf1(raw.k[b][i]) * rk4[i] : 0.f;
+      ln.q[b][i] = valid ? bf1(raw.q[b][i]) * rq4[i] : 0.f;
+      const float x = bf1(raw.g[b][i]);
+      float g, s = 0.f;
+      if (pre) {
+        g = gate_given(x, p.lower_bound);
+        s = x >= p.lower_bound && x <= 0.f ? 1.f : 0.f;
+      } else {
+        // softplus and sigmoid from one exponential (hardware exp2, log2, rcp)
+        const float y = x + dtb;
+        const float e = fexp(y);
+        const bool far = y > 20.f;
+        const float gu = -ea * (far ? y : LN2 * __builtin_amdgcn_logf(1.0f + e));
+        g = fmaxf(gu, p.lower_bound);
+        if (SLOPE)
+          s = gu >= p.lower_bound ? -ea * (far ? 1.f : e * __builtin_amdgcn_rcpf(1.0f + e)) : 0.f;
+      }
+      a[i] = valid ? fexp(g) : 1.f;
+      if constexpr (SLOPE) {
+        keep[(4 * b + i) * kThreads] = g;
+        keep[(16 + 4 * b + i) * kThreads] = valid ? s : 0.f;
+      }
+    }
+    // A lane's four tokens, the lanes between them and the middle, and the other half.
+    const float all = (a[0] * a[1]) * (a[2] * a[3]);
+    const float near = __shfl_xor(all, 16);
+    const float half = all * near;
+    const float other = __shfl_xor(half, 32);
+    ln.head[b] = g4 < 2 ? half : other;
+    ln.tail[b] = g4 < 2 ? other : half;
+    // upper half: from the middle to the token; lower: from behind it to the middle
+    const float base = g4 == 0 || g4 == 3 ? near : 1.f;
+    float w[4];
+    if (g4 < 2) {
+      w[3] = base;
+      w[2] = w[3] * a[3];
+      w[1] = w[2] * a[2];
+      w[0] = w[1] * a[1];
+    } else {
+      w[0] = base * a[0];
+      w[1] = w[0] * a[1];
+      w[2] = w[1] * a[2];
+      w[3] = w[2] * a[3];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ln.up[b][i] = g4 < 2 ? inverse(w[i]) : w[i];
+  }
+}
+
+hipError_t launch_prep(const BwdParams& p, hipStream_t stream);
+hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream);
+hipError_t launch_grads(const BwdParams& p, hipStream_t stream);
+hipError_t launch_params(const BwdParams& p, hipStream_t stream);  // dA_log, ddt_bias
+
+}  // namespace bwd
+}  // namespace kda

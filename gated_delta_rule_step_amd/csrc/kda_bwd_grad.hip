@@ -1,0 +1,581 @@
+// Prefill gradient, gradients (gfx950): those of every input from the states, the state
+// gradients, x and dV that the chains left, for all chunks and heads at once. The method
+// is described in kda_backward.hip.
+
+#include "kda_bwd.h"
+
+namespace kda {
+namespace bwd {
+namespace {
+
+// Gradients: one workgroup per (chunk, head); a wave owns 16 key channels of all
+// tokens, so that the decays and the sums over tokens stay in its registers.
+//
+// The products with S and dS and those between blocks of tokens run on fp16 MFMA, both
+// sides split into high and low parts (dO's 8 bits fit the high one); a token tile (dO,
+// dV, x) has one scale, S and dS one per key. Between blocks the decays factor at a block's
+// border into two weights of at most 1. Inside a block they reach e^(+-44), beyond fp16,
+// and the four diagonal blocks run on fp32 MFMA.
+//
+// dg without cancellation: what crosses token t from before its block or to behind it is
+// added up from the readers' side (a suffix sum over the block) or the writers' (a prefix
+// sum), and what passes the whole block from one of the two. Only pairs inside one
+// block are taken as readers less writers.
+constexpr int HS = D + 8;   // row (fp16) of dO, dV, x: 16-byte rows, 4 banks apart
+constexpr int PS = C + 8;   // row (fp16) of DP, DA
+constexpr int GS = 20;      // row (fp32) of the diagonal blocks
+constexpr int kRows = 48;   // DP, DA: readers 16..63; their transposes: writers 0..47
+
+struct GradSmem {
+  uint16_t oh[C * HS], vh[C * HS], vl[C * HS], xh[C * HS], xl[C * HS];
+  // off-diagonal blocks, zero elsewhere, columns in the order of the right fragments:
+  // [hi, lo]
+  uint16_t pr[2][kRows * PS], ar[2][kRows * PS];  // DP, DA: [reader - 16][writer]
+  uint16_t pt[2][kRows * PS], at[2][kRows * PS];  // transposed: [writer][reader]
+  float dp[NB][16 * GS], da[NB][16 * GS];         // diagonal blocks, strictly lower
+  float diag[C];                                  // DP's diagonal
+  float top[3][8];
+  alignas(16) float beta[C];
+  alignas(16) float rq[C], rk[C];
+};
+// In the place of dO, dV and x once they are read out: sums over a wave's 16 channels per
+// token, and every lane's log-decays and gate slopes.
+struct RedSmem {
+  float red[4][8][C];
+  float keep[2 * 16 * kThreads];
+};
+static_assert(sizeof(RedSmem) <= sizeof(uint16_t) * C * HS * 5, "the sums fit");
+
+// Column of token t in DP and DA: a right fragment holds, for lane group g, tokens
+// 4 g .. 4 g + 3 of a block and of the next one.
+__device__ __forceinline__ int perm32(int t) {
+  return (t & 32) + 8 * ((t & 15) >> 2) + 4 * ((t >> 4) & 1) + (t & 3);
+}
+
+__device__ __forceinline__ void zero_row(uint16_t* p, int64_t t, int64_t stride, int64_t at, int n) {
+  for (int e = threadIdx.x; e < n; e += kThreads) p[t * stride + at + e] = 0;
+}
+
+// 8 values to fp16 high and low parts, 16 bytes each.
+__device__ __forceinline__ void put8(uint16_t* hi, uint16_t* lo, f32x4 a, f32x4 b) {
+  u32x2 h0, l0, h1, l1;
+  split4h(a, h0, l0);
+  split4h(b, h1, l1);
+  *reinterpret_cast<u32x4*>(hi) = u32x4{h0[0], h0[1], h1[0], h1[1]};
+  *reinterpret_cast<u32x4*>(lo) = u32x4{l0[0], l0[1], l1[0], l1[1]};
+}
+__device__ __forceinline__ f16x8 frag8(const uint16_t* p) {
+  return *reinterpret_cast<const f16x8*>(p);
+}
+__device__ __forceinline__ float max8(f32x4 a, f32x4 b) {
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(fabsf(a[i]), fabsf(b[i])));
+  return t;
+}
+__device__ __forceinline__ f32x4 mfma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4 c) {
+  c = mfma32(al, bh, c);
+  c = mfma32(ah, bl, c);
+  return mfma32(ah, bh, c);
+}
+
+// Keeps the compiler from moving work of one stage into another: it would fetch the
+// fragments of several stages at once and run out of registers.
+__device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+
+__global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
+  extern __shared__ __align__(16) float smem_raw[];
+  GradSmem& s = *reinterpret_cast<GradSmem*>(smem_raw);
+  RedSmem& sr = *reinterpret_cast<RedSmem*>(smem_raw);
+  const int64_t sigma = blockIdx.x;
+  const int h = blockIdx.y;
+  const Chunk ch = chunk_of(p, sigma);
+  float* partial = p.partial + (sigma * p.H + h) * int64_t(2 * D);
+  const bool per_head = p.gate_mode & KDA_GATE_PER_HEAD;
+  if (ch.c == 0 || !ch.active) {
+    if (threadIdx.x < 2 * D) partial[threadIdx.x] = 0.f;
+    for (int t = 0; t < ch.c; ++t) {
+      zero_row(p.dq, ch.t0 + t, p.dq_stride, int64_t(h) * D, D);
+      zero_row(p.dk, ch.t0 + t, p.dk_stride, int64_t(h) * D, D);
+      zero_row(p.dv, ch.t0 + t, p.dv_stride, int64_t(h) * D, D);
+      zero_row(p.dg, ch.t0 + t, p.dg_stride, per_head ? h : int64_t(h) * D, per_head ? 1 : D);
+      zero_row(p.dbeta, ch.t0 + t, p.dbeta_stride, h, 1);
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int g4 = lane >> 4, n16 = lane & 15;
+  const int kc = 16 * w + n16;
+  const uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
+
+  // ---- everything is asked for at once: token tiles (a token's 128 values by 16
+  // lanes), rows of S and dS (a key's values by the four lanes that share it), q, k, g
+  constexpr int NR = C / (kThreads / 16);
+  const int c0 = (threadIdx.x & 15) * 8;
+  const Rows orow = rows_of(p.dout, ch, p.dout_stride, int64_t(h) * D);
+  const Rows dvr = rows_of(p.dv, ch, p.dv_stride, int64_t(h) * D);
+  u32x4 ow[NR];
+  f32x4 xv[NR][2], dv[NR][2];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+    ow[j] = *reinterpret_cast<const u32x4_u*>(orow.at(min(t, ch.c - 1), c0));
+    const float* X = reinterpret_cast<const float*>(ops + kOpX) + t * D + c0;
+    const float* DV = reinterpret_cast<const float*>(ops + kOpDV) + t * D + c0;
+    xv[j][0] = lds4(X);
+    xv[j][1] = lds4(X + 4);
+    dv[j][0] = lds4(DV);
+    dv[j][1] = lds4(DV + 4);
+  }
+  token_scalars(p, ch, h, s.rq, s.rk, s.beta);
+  f32x4 Sv[8], dSv[8];
+  {
+    const float* S = reinterpret_cast<const float*>(ops + kOpS) + kc * D + 8 * g4;
+    const float* dS = reinterpret_cast<const float*>(ops + kOpDS) + kc * D + 8 * g4;
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      Sv[2 * kt] = lds4(S + 32 * kt);
+      Sv[2 * kt + 1] = lds4(S + 32 * kt + 4);
+      dSv[2 * kt] = lds4(dS + 32 * kt);
+      dSv[2 * kt + 1] = lds4(dS + 32 * kt + 4);
+    }
+  }
+  const float eg = reinterpret_cast<const float*>(ops + kOpTail)[kc];
+
+  float top[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+    if (t >= ch.c) ow[j] = u32x4{0u, 0u, 0u, 0u};
+    else
+      *reinterpret_cast<u32x4_u*>(dvr.at(t, c0)) =
+          u32x4{pack_bf16x2(dv[j][0][0], dv[j][0][1]), pack_bf16x2(dv[j][0][2], dv[j][0][3]),
+                pack_bf16x2(dv[j][1][0], dv[j][1][1]), pack_bf16x2(dv[j][1][2], dv[j][1][3])};
+    float o[8];
+    unpack8_bf16(ow[j], o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[0] = fmaxf(top[0], fabsf(o[i]));
+    top[1] = fmaxf(top[1], max8(dv[j][0], dv[j][1]));
+    top[2] = fmaxf(top[2], max8(xv[j][0], xv[j][1]));
+  }
+#pragma unroll
+  for (int a = 0; a < 3; ++a) {
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) top[a] = fmaxf(top[a], __shfl_xor(top[a], o));
+    if (lane == 0) s.top[a][w] = top[a];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < 3; ++a)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[a] = fmaxf(top[a], s.top[a][i]);
+  const Scale so = scale_for(top[0]), sv = scale_for(top[1]), sx = scale_for(top[2]);
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const int at = ((threadIdx.x >> 4) + j * (kThreads / 16)) * HS + c0;
+    float o[8];
+    unpack8_bf16(ow[j], o);
+    u32x4 oh;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) oh[i] = pack_f16x2(o[2 * i] * so.up, o[2 * i + 1] * so.up);
+    *reinterpret_cast<u32x4*>(s.oh + at) = oh;
+    put8(s.vh + at, s.vl + at, dv[j][0] * sv.up, dv[j][1] * sv.up);
+    put8(s.xh + at, s.xl + at, xv[j][0] * sx.up, xv[j][1] * sx.up);
+  }
+  // the blocks that a 32-token contraction takes along and that hold nothing
+  for (int e = threadIdx.x; e < 2 * kRows * PS / 8; e += kThreads) {
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    reinterpret_cast<u32x4*>(&s.pr[0][0])[e] = z;
+    reinterpret_cast<u32x4*>(&s.ar[0][0])[e] = z;
+    reinterpret_cast<u32x4*>(&s.pt[0][0])[e] = z;
+    reinterpret_cast<u32x4*>(&s.at[0][0])[e] = z;
+  }
+  __syncthreads();
+  RawLane raw;
+  load_lane(p, ch, h, kc, g4, raw);
+
+  // ---- DP = tril(dO x^T, -1) and its diagonal, DA = -tril(dV x^T, -1). Both factors
+  // are below 2^15, so 128 terms are below 2^37, and 2^-22 of that fits fp16.
+  constexpr float kDown = 1.0f / 4194304.0f, kUp = 4194304.0f;
+  for (int task = w; task < NB * (NB + 1); task += kThreads / 64) {
+    const bool is_p = task >= NB * (NB + 1) / 2;
+    int I = 0, J = is_p ? task - NB * (NB + 1) / 2 : task;
+    while (J > I) J -= ++I;
+    const int left = (16 * I + n16) * HS + 8 * g4, right = (16 * J + n16) * HS + 8 * g4;
+    f32x4 acc = zero4();
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      const f16x8 bh = frag8(s.xh + right + 32 * kt), bl = frag8(s.xl + right + 32 * kt);
+      if (is_p) {
+        const f16x8 a = frag8(s.oh + left + 32 * kt);
+        acc = mfma32(a, bl, acc);
+        acc = mfma32(a, bh, acc);
+      } else {
+        acc = mfma_split(frag8(s.vh + left + 32 * kt), frag8(s.vl + left + 32 * kt), bh, bl, acc);
+      }
+    }
+    if (!is_p) acc = -acc;
+    if (I == J) {
+      acc *= (is_p ? so.un : sv.un) * sx.un;
+      float* dst = is_p ? s.dp[I] : s.da[I];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * g4 + i;
+        dst[r * GS + n16] = n16 < r ? acc[i] : 0.f;
+        if (is_p && n16 == r) s.diag[16 * I + n16] = acc[i];
+      }
+    } else {
+      u32x2 hi, lo;
+      split4h(acc * kDown, hi, lo);
+      uint16_t(*row)[kRows * PS] = is_p ? s.pr : s.ar;
+      uint16_t(*col)[kRows * PS] = is_p ? s.pt : s.at;
+      const int at = perm32(16 * J + n16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        row[0][(16 * (I - 1) + 4 * g4 + i) * PS + at] = uint16_t(hi[i >> 1] >> (16 * (i & 1)));
+        row[1][(16 * (I - 1) + 4 * g4 + i) * PS + at] = uint16_t(lo[i >> 1] >> (16 * (i & 1)));
+      }
+      const int to = (16 * J + n16) * PS + perm32(16 * I + 4 * g4);
+      *reinterpret_cast<u32x2*>(col[0] + to) = hi;
+      *reinterpret_cast<u32x2*>(col[1] + to) = lo;
+    }
+  }
+
+  stage();
+  // ---- dO S^T, dV S^T, x dS^T for the wave's channels
+  f32x4 sq[NB], sk[NB], se[NB];
+  float flow = 0.f;  // e^Gl sum_v S dS: what passes the whole chunk
+  {
+    float ts = 0.f, td = 0.f;
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        flow = fmaf(Sv[m][i], dSv[m][i], flow);
+        ts = fmaxf(ts, fabsf(Sv[m][i]));
+        td = fmaxf(td, fabsf(dSv[m][i]));
+      }
+    ts = fmaxf(ts, __shfl_xor(ts, 16));
+    td = fmaxf(td, __shfl_xor(td, 16));
+    const Scale ss = scale_for(fmaxf(ts, __shfl_xor(ts, 32)));
+    const Scale sd = scale_for(fmaxf(td, __shfl_xor(td, 32)));
+    flow = rows_sum(flow) * eg;
+#pragma unroll
+    for (int r = 0; r < NB; ++r) sq[r] = sk[r] = se[r] = zero4();
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      stage();
+      u32x2 h0, l0, h1, l1;
+      split4h(Sv[2 * kt] * ss.up, h0, l0);
+      split4h(Sv[2 * kt + 1] * ss.up, h1, l1);
+      const f16x8 Sh = join8(h0, h1), Sl = join8(l0, l1);
+      split4h(dSv[2 * kt] * sd.up, h0, l0);
+      split4h(dSv[2 * kt + 1] * sd.up, h1, l1);
+      const f16x8 Dh = join8(h0, h1), Dl = join8(l0, l1);
+#pragma unroll
+      for (int r = 0; r < NB; ++r) {
+        const int at = (16 * r + n16) * HS + 32 * kt + 8 * g4;
+        const f16x8 o = frag8(s.oh + at);
+        sq[r] = mfma32(o, Sl, sq[r]);
+        sq[r] = mfma32(o, Sh, sq[r]);
+        sk[r] = mfma_split(frag8(s.vh + at), frag8(s.vl + at), Sh, Sl, sk[r]);
+        se[r] = mfma_split(frag8(s.xh + at), frag8(s.xl + at), Dh, Dl, se[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+      sq[r] *= so.un * ss.un;
+      sk[r] *= sv.un * ss.un;
+      se[r] *= sx.un * sd.un;
+    }
+  }
+  stage();
+  __syncthreads();
+  Lane ln;
+  float* keep = sr.keep + threadIdx.x;
+  make_lane<true>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, keep);
+  stage();
+
+  // ---- between blocks: readers from the block's start, writers to its end
+  f32x4 cq[NB], ck[NB], cc[NB];  // readers' sums, q and k; writers'
+  f32x4 tq, tk, tc;  // block 3's readers of blocks 0 and 1; block 0's writers for 2 and 3
+  float T[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    T[b] = ln.head[b] * ln.tail[b];
+    cq[b] = ck[b] = cc[b] = zero4();
+  }
+  {
+    constexpr float kW = 16.0f;  // writers' scale: leaves room for a beta beyond 1
+    auto frags = [](f32x4 a, f32x4 b, f16x8& hi, f16x8& lo) {
+      u32x2 h0, l0, h1, l1;
+      split4h(a, h0, l0);
+      split4h(b, h1, l1);
+      hi = join8(h0, h1);
+      lo = join8(l0, l1);
+    };
+    f32x4 kw[3], kr[3], qr[3];  // writers 0..2, readers 1..3
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+      const f32x4 bt = lds4(s.beta + 16 * b + 4 * g4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kw[b][i] = ln.k[b][i] * bt[i] * (inverse(ln.up[b][i]) * ln.tail[b]) * kW;
+        const float rd = ln.up[b + 1][i] * ln.head[b + 1] * kFixedUp;
+        kr[b][i] = ln.k[b + 1][i] * rd;
+        qr[b][i] = ln.q[b + 1][i] * rd;
+      }
+    }
+    const float un = kUp * sx.un / kW;
+    f16x8 bh, bl;
+    // readers: block 1 of 0; block 2 of 0, 1; block 3 of 0, 1 and of 2
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      stage();
+      const int I = n < 2 ? n + 1 : 3, t = n == 3 ? 1 : 0;
+      if (n == 0) frags(kw[0], zero4(), bh, bl);
+      else if (n == 1) frags(kw[0] * T[1], kw[1], bh, bl);
+      else if (n == 2) frags(kw[0] * (T[1] * T[2]), kw[1] * T[2], bh, bl);
+      else frags(kw[2], zero4(), bh, bl);
+      const int at = (16 * (I - 1) + n16) * PS + 32 * t + 8 * g4;
+      const f32x4 q = mfma_split(frag8(s.pr[0] + at), frag8(s.pr[1] + at), bh, bl, zero4());
+      const f32x4 k = mfma_split(frag8(s.ar[0] + at), frag8(s.ar[1] + at), bh, bl, zero4());
+      if (n == 2) tq = q * (so.un * un), tk = k * (sv.un * un);
+      cq[I] += q * (so.un * un);
+      ck[I] += k * (sv.un * un);
+    }
+    // writers: block 0 for 1 and for 2, 3; block 1 for 2, 3; block 2 for 3
+    const float uk = kUp * sx.un * kFixedUn * sv.un, uq = kUp * sx.un * kFixedUn * so.un * p.scale;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      stage();
+      const int J = n < 2 ? 0 : n - 1, t = n == 0 ? 0 : 1;
+      const int at = (16 * J + n16) * PS + 32 * t + 8 * g4;
+      f32x4 c;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const f32x4* x = which ? qr : kr;
+        if (n == 0) frags(zero4(), x[0], bh, bl);
+        else if (n == 1) frags(x[1] * T[1], x[2] * (T[1] * T[2]), bh, bl);
+        else if (n == 2) frags(x[1], x[2] * T[2], bh, bl);
+        else frags(zero4(), x[2], bh, bl);
+        const uint16_t(*m)[kRows * PS] = which ? s.pt : s.at;
+        const f32x4 a = mfma_split(frag8(m[0] + at), frag8(m[1] + at), bh, bl, zero4());
+        if (which == 0) c = a * uk;
+        else c += a * uq;
+      }
+      if (n == 1) tc = c;
+      cc[J] += c;
+    }
+  }
+
+  // Hidden from the compiler, so that it forms the weights again below instead of keeping
+  // all of them from above.
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("" : "+v"(ln.up[b][i]), "+v"(ln.k[b][i]), "+v"(ln.q[b][i]));
+
+  // ---- block by block: the diagonal block, the sums, and the tokens' gradients
+  float dg[NB][4];           // first what the block itself adds to dg
+  float reads[NB], ends[NB]; // block sums: readers of S; writers into dS
+  float pass1 = 0.f, pass2 = 0.f;  // pairs across block 1, across block 2
+  float F = 1.f;                   // from the chunk's start
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    stage();
+    const f32x4 bt = lds4(s.beta + 16 * b + 4 * g4);
+    f32x4 dq = zero4(), dk = zero4(), dc = zero4();  // inside the block
+    {
+      f32x4 kb, km, qm;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kb[i] = ln.k[b][i] * bt[i] * inverse(ln.up[b][i]);
+        km[i] = ln.k[b][i] * ln.up[b][i];
+        qm[i] = ln.q[b][i] * ln.up[b][i] * p.scale;
+      }
+      dq = mfma4(lds4(s.dp[b] + n16 * GS + 4 * g4), kb, dq);
+      dk = mfma4(lds4(s.da[b] + n16 * GS + 4 * g4), kb, dk);
+      dc = mfma4(col4(s.dp[b] + 4 * g4 * GS + n16, GS), qm, dc);
+      dc = mfma4(col4(s.da[b] + 4 * g4 * GS + n16, GS), km, dc);
+    }
+    float E = 1.f;  // to the chunk's end
+#pragma unroll
+    for (int m = b + 1; m < NB; ++m) E *= T[m];
+    float rsum = 0.f, esum = 0.f, fromq = 0.f, before = 0.f;
+    float suf[4], pre[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float k = ln.k[b][i], q = ln.q[b][i] * p.scale, kb = k * bt[i];
+      const float dn = inverse(ln.up[b][i]);
+      const float rd = ln.up[b][i] * ln.head[b], wr = dn * ln.tail[b];
+      const float self = s.diag[16 * b + 4 * g4 + i];
+      // by state, by other blocks, inside
+      const float rs = F * (q * sq[b][i] - k * sk[b][i]) * rd;
+      const float ro = (q * cq[b][i] + k * ck[b][i]) * rd;
+      const float end = wr * E * se[b][i];
+      const float wo = wr * cc[b][i];
+      const float in = ln.up[b][i] * (q * dq[i] + k * dk[i]) - kb * (dn * dc[i]);
+      rsum += rs;
+      esum = fmaf(kb, end, esum);
+      suf[i] = rs + ro + in;
+      pre[i] = kb * (end + wo);
+      if (b == 3) fromq += (q * tq[i] + k * tk[i]) * rd;
+      if (b == 0) before += kb * wr * tc[i];
+      const float dqi = fmaf(rd, fmaf(F, sq[b][i], cq[b][i]), fmaf(ln.up[b][i], dq[i], self * kb));
+      const float dri = fmaf(rd, fmaf(-F, sk[b][i], ck[b][i]), ln.up[b][i] * dk[i]);
+      const float col = end + wo + fmaf(dn, dc[i], self * q);
+      cq[b][i] = dqi * p.scale;
+      ck[b][i] = fmaf(bt[i], col, dri);
+      // q_hat . dq_hat, k_hat . dk_hat, k_hat . col over the wave's channels
+      const float a0 = row16_sum(ln.q[b][i] * cq[b][i]);
+      const float a1 = row16_sum(k * ck[b][i]);
+      const float a2 = row16_sum(k * col);
+      if (n16 == 0) {
+        const int t = 16 * b + 4 * g4 + i;
+        sr.red[0][w][t] = a0;
+        sr.red[1][w][t] = a1;
+        sr.red[2][w][t] = a2;
+      }
+    }
+    reads[b] = rows_sum(rsum);
+    ends[b] = rows_sum(esum);
+    if (b == 3) pass2 = rows_sum(fromq);
+    if (b == 0) pass1 = rows_sum(before);
+    // suffix sums (from the token on) and prefix sums (before it) over the block
+    const float stot = (suf[0] + suf[1]) + (suf[2] + suf[3]);
+    const float ptot = (pre[0] + pre[1]) + (pre[2] + pre[3]);
+    const float s1 = __shfl_xor(stot, 16), p1 = __shfl_xor(ptot, 16);
+    const float s2 = __shfl_xor(stot + s1, 32), p2 = __shfl_xor(ptot + p1, 32);
+    float sacc = ((g4 & 1) ? 0.f : s1) + ((g4 & 2) ? 0.f : s2);
+    float pacc = ((g4 & 1) ? p1 : 0.f) + ((g4 & 2) ? p2 : 0.f);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      sacc += suf[i];
+      dg[b][i] = sacc;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dg[b][i] += pacc;
+      pacc += pre[i];
+    }
+    F *= T[b];
+  }
+  stage();
+  // what passes each block as a whole
+  const float across[NB] = {reads[1] + reads[2] + reads[3], reads[2] + reads[3] + ends[0] + pass1,
+                            reads[3] + ends[0] + ends[1] + pass2, ends[0] + ends[1] + ends[2]};
+  float sum_b = 0.f, sum_a = 0.f;  // of ddt_bias, dA_log
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = dg[b][i] + (across[b] + flow);
+      dg[b][i] = x;
+      const float slope = keep[(16 + 4 * b + i) * kThreads];
+      sum_b = fmaf(x, slope, sum_b);
+      sum_a = fmaf(x, slope != 0.f ? keep[(4 * b + i) * kThreads] : 0.f, sum_a);
+      if (per_head) {
+        const float a3 = row16_sum(x);
+        if (n16 == 0) sr.red[3][w][16 * b + 4 * g4 + i] = a3;
+      }
+    }
+  sum_b = rows_sum(sum_b);
+  sum_a = rows_sum(sum_a);
+  if (g4 == 0) {
+    partial[kc] = sum_b;
+    partial[D + kc] = sum_a;
+  }
+  __syncthreads();
+  if (threadIdx.x < C * 4) {  // add the eight waves' sums
+    const int which = threadIdx.x / C, t = threadIdx.x % C;
+    if (which < 3 || per_head) {
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x += sr.red[which][i][t];
+      sr.red[which][0][t] = x;
+      if (which == 2 && t < ch.c) {
+        if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) x *= s.beta[t] * (1.f - s.beta[t]);
+        p.dbeta[(ch.t0 + t) * p.dbeta_stride + h] = to_bf16(x);
+      }
+    }
+  }
+  __syncthreads();
+  const Rows dqr = rows_of(p.dq, ch, p.dq_stride, int64_t(h) * D);
+  const Rows dkr = rows_of(p.dk, ch, p.dk_stride, int64_t(h) * D);
+  const Rows dgr = rows_of(p.dg, ch, p.dg_stride, per_head ? h : int64_t(h) * D);
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * b + 4 * g4 + i;
+      if (t < ch.c) {
+        const float rq = s.rq[t], rk = s.rk[t];
+        const float slope = keep[(16 + 4 * b + i) * kThreads];
+        const float dq = rq * fmaf(-ln.q[b][i], sr.red[0][0][t], cq[b][i]);
+        const float dk = rk * fmaf(-ln.k[b][i], sr.red[1][0][t], ck[b][i]);
+        *dqr.at(t, kc) = to_bf16(dq);
+        *dkr.at(t, kc) = to_bf16(dk);
+        if (!per_head)
+          *dgr.at(t, kc) = to_bf16(dg[b][i] * slope);
+        else if (w == 0 && n16 == 0)
+          *dgr.at(t, 0) = to_bf16(sr.red[3][0][t] * slope);
+      }
+    }
+}
+
+// dA_log and ddt_bias: the partial sums of a head, added in the order of the chunk
+// slots by 8 groups of 128 lanes (a channel each), then group by group.
+__global__ __launch_bounds__(1024) void param_kernel(BwdParams p) {
+  __shared__ float sum[2][8][D];
+  __shared__ float half[4];
+  const int h = blockIdx.x;
+  const int c = threadIdx.x & (D - 1), grp = threadIdx.x / D;
+  float b = 0.f, a = 0.f;
+  for (int64_t n = grp; n < p.slots; n += 8) {
+    const float* x = p.partial + (n * p.H + h) * int64_t(2 * D);
+    b += x[c];
+    a += x[D + c];
+  }
+  sum[0][grp][c] = b;
+  sum[1][grp][c] = a;
+  __syncthreads();
+  const bool per_head = p.gate_mode & KDA_GATE_PER_HEAD;
+  float t = 0.f;
+  if (grp < 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += sum[grp][i][c];
+    if (grp == 0 && !per_head && p.ddt_bias) p.ddt_bias[h * D + c] = t;
+    // a head's one value: the sum over its channels
+    t = rows_sum(row16_sum(t));
+    if ((threadIdx.x & 63) == 0) half[threadIdx.x >> 6] = t;
+  }
+  __syncthreads();
+  if (grp < 2 && c == 0) {
+    t = half[2 * grp] + half[2 * grp + 1];
+    if (grp == 1 && p.dA_log) p.dA_log[h] = t;
+    if (grp == 0 && per_head && p.ddt_bias) p.ddt_bias[h] = t;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_grads(const BwdParams& p, hipStream_t stream) {
+  static const hipError_t lds = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(grad_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+      int(sizeof(GradSmem)));
+  if (lds != hipSuccess) return lds;
+  static_assert(sizeof(GradSmem) <= 160 * 1024, "LDS of a CU");
+  hipLaunchKernelGGL(grad_kernel, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
+                     sizeof(GradSmem), stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_params(const BwdParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL(param_kernel, dim3(unsigned(p.H)), dim3(1024), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace bwd
+}  // namespace kda

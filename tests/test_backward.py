@@ -60,7 +60,9 @@ def _call(lib, **kw):
     (UNSUP, dict(K=64)), (UNSUP, dict(V=64)), (UNSUP, dict(H=70000)), (UNSUP, dict(lb=-6.0)),
     (UNSUP, dict(lb=float("nan"))), (UNSUP, dict(gm=8)), (UNSUP, dict(gm=PRE)),
     (UNSUP, dict(gm=PRE, da=0, dd=0, lb=1.0)), (UNSUP, dict(sd=3)), (UNSUP, dict(sd=-1)),
-    (UNSUP, dict(di=4100)), (UNSUP, dict(ws=4100)),
+    (UNSUP, dict(di=4100)), (UNSUP, dict(ws=4100)), (UNSUP, dict(lb=0.5)),
+    (UNSUP, dict(s=(384, 384, (1 << 25) + 1, 384, 3))), (UNSUP, dict(dos=1 << 26)),
+    (UNSUP, dict(os=(384, 384, 384, 384, 1 << 26))),
     (NULLP, dict(cu=None)), (NULLP, dict(cud=0)), (NULLP, dict(q=0)), (NULLP, dict(do=0)),
     (NULLP, dict(dbeta=0, db=0)), (NULLP, dict(al=0)), (NULLP, dict(idx=0)),
     (NULLP, dict(pool=0)), (NULLP, dict(ws=0)),
