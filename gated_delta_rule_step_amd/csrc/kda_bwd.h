@@ -153,13 +153,14 @@ __device__ __forceinline__ Chunk chunk_of(const BwdParams& p, int64_t sigma) {
   Chunk ch = {0, 0, 0, false};
   ch.doc = find_doc(p.cu_seqlens, p.n_docs, sigma);
   if (ch.doc >= p.n_docs) return ch;
-  const int64_t start = p.cu_seqlens[ch.doc];
-  const int64_t len = int64_t(p.cu_seqlens[ch.doc + 1]) - start;
-  const int64_t off = (sigma - doc_slot0(p.cu_seqlens, ch.doc)) * C;
-  if (off >= len) return ch;
+  // the same in every lane: kept in scalar registers, addresses with them
+  const int32_t start = __builtin_amdgcn_readfirstlane(p.cu_seqlens[ch.doc]);
+  const int32_t end = __builtin_amdgcn_readfirstlane(p.cu_seqlens[ch.doc + 1]);
+  const int32_t slot = __builtin_amdgcn_readfirstlane(p.state_indices[ch.doc]);
+  const int64_t off = (sigma - (int64_t(ch.doc) + start / C)) * C;
+  if (off >= end - start) return ch;
   ch.t0 = start + off;
-  ch.c = int(min<int64_t>(C, len - off));
-  const int32_t slot = p.state_indices[ch.doc];
+  ch.c = int(min<int64_t>(C, end - start - off));
   ch.active = slot >= 0 && int64_t(slot) < p.num_slots;
   return ch;
 }
@@ -170,10 +171,19 @@ __device__ __forceinline__ Chunk chunk_of(const BwdParams& p, int64_t sigma) {
 struct Rows {
   uint16_t* base;
   uint32_t stride;
-  __device__ __forceinline__ uint16_t* at(int t, int col) const {
-    return reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(base) +
-                                       (uint32_t(t) * stride + uint32_t(col) * 2u));
+  __device__ __forceinline__ uint32_t offset(int t, int col) const {
+    return uint32_t(t) * stride + uint32_t(col) * 2u;
   }
+  // `t` more rows (the same for all lanes) after a lane's offset
+  __device__ __forceinline__ uint16_t* from(uint32_t off, int t) const {
+    return reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(base) +
+                                       (off + uint32_t(t) * stride));
+  }
+  // the same, but no further than offset `last`
+  __device__ __forceinline__ uint16_t* upto(uint32_t off, int t, uint32_t last) const {
+    return from(min(off + uint32_t(t) * stride, last), 0);
+  }
+  __device__ __forceinline__ uint16_t* at(int t, int col) const { return from(offset(t, col), 0); }
 };
 __device__ __forceinline__ Rows rows_of(const uint16_t* x, const Chunk& ch, int64_t stride,
                                         int64_t col) {
@@ -237,14 +247,16 @@ __device__ __forceinline__ void load_lane(const BwdParams& p, const Chunk& ch, i
   const Rows kr = rows_of(p.k, ch, p.k_stride, int64_t(h) * D);
   const Rows gr = rows_of(p.g, ch, p.g_stride, head ? h : int64_t(h) * D);
   const int gc = head ? 0 : kc;
+  const uint32_t k0 = kr.offset(4 * g4, kc), q0 = qr.offset(4 * g4, kc), g0 = gr.offset(4 * g4, gc);
+  const uint32_t kl = kr.offset(ch.c - 1, kc), ql = qr.offset(ch.c - 1, kc),
+                 gl = gr.offset(ch.c - 1, gc);
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = min(16 * b + 4 * g4 + i, ch.c - 1);
-      raw.k[b][i] = *kr.at(t, kc);
-      raw.q[b][i] = *qr.at(t, kc);
-      raw.g[b][i] = *gr.at(t, gc);
+      raw.k[b][i] = *kr.upto(k0, 16 * b + i, kl);
+      raw.q[b][i] = *qr.upto(q0, 16 * b + i, ql);
+      raw.g[b][i] = *gr.upto(g0, 16 * b + i, gl);
     }
 }
 

@@ -33,7 +33,7 @@ struct GradSmem {
   uint16_t pr[2][kRows * PS], ar[2][kRows * PS];  // DP, DA: [reader - 16][writer]
   uint16_t pt[2][kRows * PS], at[2][kRows * PS];  // transposed: [writer][reader]
   float dp[NB][16 * GS], da[NB][16 * GS];         // diagonal blocks, strictly lower
-  float diag[C];                                  // DP's diagonal
+  alignas(16) float diag[C];                      // DP's diagonal
   float top[3][8];
   alignas(16) float beta[C];
   alignas(16) float rq[C], rk[C];
@@ -82,6 +82,17 @@ __device__ __forceinline__ f32x4 mfma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 
 // Keeps the compiler from moving work of one stage into another: it would fetch the
 // fragments of several stages at once and run out of registers.
 __device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+
+// Sums of four values over a DPP row: lane n of the row ends with that of value n % 4.
+// Two exchanges that halve the values, then two rotations over the lanes of equal n % 4.
+__device__ __forceinline__ float row16_sums(const float (&v)[4], int n16) {
+  const bool b0 = n16 & 1, b1 = n16 & 2;
+  const float x = (b0 ? v[1] : v[0]) + dpp<0xB1>(b0 ? v[0] : v[1]);
+  const float y = (b0 ? v[3] : v[2]) + dpp<0xB1>(b0 ? v[2] : v[3]);
+  float t = (b1 ? y : x) + dpp<0x4E>(b1 ? x : y);
+  t += dpp<0x124>(t);         // row_ror:4
+  return t + dpp<0x128>(t);   // row_ror:8
+}
 
 __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   extern __shared__ __align__(16) float smem_raw[];
@@ -197,6 +208,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   // ---- DP = tril(dO x^T, -1) and its diagonal, DA = -tril(dV x^T, -1). Both factors
   // are below 2^15, so 128 terms are below 2^37, and 2^-22 of that fits fp16.
   constexpr float kDown = 1.0f / 4194304.0f, kUp = 4194304.0f;
+  constexpr float kW = 16.0f;  // writers' scale: leaves room for a beta beyond 1
+  const float uo = so.un * p.scale;  // from here on dO stands for scale dO
   for (int task = w; task < NB * (NB + 1); task += kThreads / 64) {
     const bool is_p = task >= NB * (NB + 1) / 2;
     int I = 0, J = is_p ? task - NB * (NB + 1) / 2 : task;
@@ -216,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
     }
     if (!is_p) acc = -acc;
     if (I == J) {
-      acc *= (is_p ? so.un : sv.un) * sx.un;
+      acc *= (is_p ? uo : sv.un) * sx.un;
       float* dst = is_p ? s.dp[I] : s.da[I];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -244,6 +257,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   stage();
   // ---- dO S^T, dV S^T, x dS^T for the wave's channels
   f32x4 sq[NB], sk[NB], se[NB];
+  float uq, uk, ue;  // their scales
   float flow = 0.f;  // e^Gl sum_v S dS: what passes the whole chunk
   {
     float ts = 0.f, td = 0.f;
@@ -282,12 +296,9 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
         se[r] = mfma_split(frag8(s.xh + at), frag8(s.xl + at), Dh, Dl, se[r]);
       }
     }
-#pragma unroll
-    for (int r = 0; r < NB; ++r) {
-      sq[r] *= so.un * ss.un;
-      sk[r] *= sv.un * ss.un;
-      se[r] *= sx.un * sd.un;
-    }
+    uq = uo * ss.un;
+    uk = sv.un * ss.un;
+    ue = sx.un * sd.un;
   }
   stage();
   __syncthreads();
@@ -296,153 +307,163 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   make_lane<true>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, keep);
   stage();
 
-  // ---- between blocks: readers from the block's start, writers to its end
-  f32x4 cq[NB], ck[NB], cc[NB];  // readers' sums, q and k; writers'
-  f32x4 tq, tk, tc;  // block 3's readers of blocks 0 and 1; block 0's writers for 2 and 3
+  // ---- between blocks: readers from the block's start, writers to its end. A pair two
+  // blocks apart also takes the whole blocks between, a factor per channel: on the operand
+  // where one product holds pairs of both kinds, else on the result.
+  const float uqr = kUp * uo * sx.un / kW, ukr = kUp * sv.un * sx.un / kW;
+  const float uboth = fmaxf(fabsf(uo), sv.un);  // writers add up DA^T k and DP^T q
+  const float uw = kUp * sx.un * uboth * kFixedUn;
   float T[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    T[b] = ln.head[b] * ln.tail[b];
-    cq[b] = ck[b] = cc[b] = zero4();
-  }
+  for (int b = 0; b < NB; ++b) T[b] = ln.head[b] * ln.tail[b];
+  auto frags = [](f32x4 a, f32x4 b, f16x8& hi, f16x8& lo) {
+    u32x2 h0, l0, h1, l1;
+    split4h(a, h0, l0);
+    split4h(b, h1, l1);
+    hi = join8(h0, h1);
+    lo = join8(l0, l1);
+  };
+  auto row = [&](const uint16_t(*m)[kRows * PS], int blk, int t, f16x8 bh, f16x8 bl, f32x4 c) {
+    const int at = (16 * blk + n16) * PS + 32 * t + 8 * g4;
+    return mfma_split(frag8(m[0] + at), frag8(m[1] + at), bh, bl, c);
+  };
+  auto writer = [&](int b) {  // beta k of block b's tokens, to its end
+    const f32x4 bt = lds4(s.beta + 16 * b + 4 * g4) * (ln.tail[b] * kW);
+    f32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = ln.k[b][i] * (bt[i] * inverse(ln.up[b][i]));
+    return x;
+  };
+  f32x4 c0a, c0b, c1, c2;  // writers of block 0 (for 1; for 2, 3), 1 and 2
   {
-    constexpr float kW = 16.0f;  // writers' scale: leaves room for a beta beyond 1
-    auto frags = [](f32x4 a, f32x4 b, f16x8& hi, f16x8& lo) {
-      u32x2 h0, l0, h1, l1;
-      split4h(a, h0, l0);
-      split4h(b, h1, l1);
-      hi = join8(h0, h1);
-      lo = join8(l0, l1);
-    };
-    f32x4 kw[3], kr[3], qr[3];  // writers 0..2, readers 1..3
-#pragma unroll
-    for (int b = 0; b < 3; ++b) {
-      const f32x4 bt = lds4(s.beta + 16 * b + 4 * g4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kw[b][i] = ln.k[b][i] * bt[i] * (inverse(ln.up[b][i]) * ln.tail[b]) * kW;
-        const float rd = ln.up[b + 1][i] * ln.head[b + 1] * kFixedUp;
-        kr[b][i] = ln.k[b + 1][i] * rd;
-        qr[b][i] = ln.q[b + 1][i] * rd;
-      }
-    }
-    const float un = kUp * sx.un / kW;
     f16x8 bh, bl;
-    // readers: block 1 of 0; block 2 of 0, 1; block 3 of 0, 1 and of 2
+    c0a = c0b = c1 = c2 = zero4();
+    // brought to one scale, the larger of the two, so that both stay within fp16
+    const float cq = kFixedUp * (uo / uboth), ck = kFixedUp * (sv.un / uboth);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int which = 0; which < 2; ++which) {
       stage();
-      const int I = n < 2 ? n + 1 : 3, t = n == 3 ? 1 : 0;
-      if (n == 0) frags(kw[0], zero4(), bh, bl);
-      else if (n == 1) frags(kw[0] * T[1], kw[1], bh, bl);
-      else if (n == 2) frags(kw[0] * (T[1] * T[2]), kw[1] * T[2], bh, bl);
-      else frags(kw[2], zero4(), bh, bl);
-      const int at = (16 * (I - 1) + n16) * PS + 32 * t + 8 * g4;
-      const f32x4 q = mfma_split(frag8(s.pr[0] + at), frag8(s.pr[1] + at), bh, bl, zero4());
-      const f32x4 k = mfma_split(frag8(s.ar[0] + at), frag8(s.ar[1] + at), bh, bl, zero4());
-      if (n == 2) tq = q * (so.un * un), tk = k * (sv.un * un);
-      cq[I] += q * (so.un * un);
-      ck[I] += k * (sv.un * un);
-    }
-    // writers: block 0 for 1 and for 2, 3; block 1 for 2, 3; block 2 for 3
-    const float uk = kUp * sx.un * kFixedUn * sv.un, uq = kUp * sx.un * kFixedUn * so.un * p.scale;
+      const uint16_t(*m)[kRows * PS] = which ? s.pt : s.at;
+      f32x4 x[3];  // readers 1..3
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      stage();
-      const int J = n < 2 ? 0 : n - 1, t = n == 0 ? 0 : 1;
-      const int at = (16 * J + n16) * PS + 32 * t + 8 * g4;
-      f32x4 c;
+      for (int b = 0; b < 3; ++b) {
+        const float hd = ln.head[b + 1] * (which ? cq : ck);
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const f32x4* x = which ? qr : kr;
-        if (n == 0) frags(zero4(), x[0], bh, bl);
-        else if (n == 1) frags(x[1] * T[1], x[2] * (T[1] * T[2]), bh, bl);
-        else if (n == 2) frags(x[1], x[2] * T[2], bh, bl);
-        else frags(zero4(), x[2], bh, bl);
-        const uint16_t(*m)[kRows * PS] = which ? s.pt : s.at;
-        const f32x4 a = mfma_split(frag8(m[0] + at), frag8(m[1] + at), bh, bl, zero4());
-        if (which == 0) c = a * uk;
-        else c += a * uq;
+        for (int i = 0; i < 4; ++i)
+          x[b][i] = (which ? ln.q[b + 1][i] : ln.k[b + 1][i]) * (ln.up[b + 1][i] * hd);
       }
-      if (n == 1) tc = c;
-      cc[J] += c;
+      frags(zero4(), x[0], bh, bl);
+      c0a = row(m, 0, 0, bh, bl, c0a);
+      frags(x[1], x[2] * T[2], bh, bl);
+      c0b = row(m, 0, 1, bh, bl, c0b);
+      c1 = row(m, 1, 1, bh, bl, c1);
+      frags(zero4(), x[2], bh, bl);
+      c2 = row(m, 2, 1, bh, bl, c2);
     }
   }
-
-  // Hidden from the compiler, so that it forms the weights again below instead of keeping
-  // all of them from above.
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("" : "+v"(ln.up[b][i]), "+v"(ln.k[b][i]), "+v"(ln.q[b][i]));
 
   // ---- block by block: the diagonal block, the sums, and the tokens' gradients
-  float dg[NB][4];           // first what the block itself adds to dg
-  float reads[NB], ends[NB]; // block sums: readers of S; writers into dS
+  float dg[NB][4];                 // first what the block itself adds to dg
+  f32x4 gq[NB], gk[NB];            // dq_hat, dk_hat
+  float reads[NB], ends[NB];       // block sums: readers of S; writers into dS
   float pass1 = 0.f, pass2 = 0.f;  // pairs across block 1, across block 2
   float F = 1.f;                   // from the chunk's start
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     stage();
-    const f32x4 bt = lds4(s.beta + 16 * b + 4 * g4);
-    f32x4 dq = zero4(), dk = zero4(), dc = zero4();  // inside the block
-    {
-      f32x4 kb, km, qm;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kb[i] = ln.k[b][i] * bt[i] * inverse(ln.up[b][i]);
-        km[i] = ln.k[b][i] * ln.up[b][i];
-        qm[i] = ln.q[b][i] * ln.up[b][i] * p.scale;
+    // what the block's readers get from earlier ones; of block 3 apart from 0, 1 and from 2
+    f32x4 rq = zero4(), rk = zero4(), rqa = zero4(), rka = zero4();
+    if (b > 0) {
+      f16x8 bh, bl;
+      if (b == 1) frags(writer(0), zero4(), bh, bl);
+      if (b >= 2) frags(writer(0) * T[1], writer(1), bh, bl);
+      rq = row(s.pr, b - 1, 0, bh, bl, zero4());
+      rk = row(s.ar, b - 1, 0, bh, bl, zero4());
+      if (b == 3) {
+        rqa = rq;
+        rka = rk;
+        frags(writer(2), zero4(), bh, bl);
+        rq = row(s.pr, 2, 1, bh, bl, zero4());
+        rk = row(s.ar, 2, 1, bh, bl, zero4());
       }
-      dq = mfma4(lds4(s.dp[b] + n16 * GS + 4 * g4), kb, dq);
-      dk = mfma4(lds4(s.da[b] + n16 * GS + 4 * g4), kb, dk);
-      dc = mfma4(col4(s.dp[b] + 4 * g4 * GS + n16, GS), qm, dc);
-      dc = mfma4(col4(s.da[b] + 4 * g4 * GS + n16, GS), km, dc);
     }
-    float E = 1.f;  // to the chunk's end
-#pragma unroll
-    for (int m = b + 1; m < NB; ++m) E *= T[m];
-    float rsum = 0.f, esum = 0.f, fromq = 0.f, before = 0.f;
-    float suf[4], pre[4];
+    stage();
+    const f32x4 bt = lds4(s.beta + 16 * b + 4 * g4), self = lds4(s.diag + 16 * b + 4 * g4);
+    f32x4 kb, km, qm, dn;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float k = ln.k[b][i], q = ln.q[b][i] * p.scale, kb = k * bt[i];
-      const float dn = inverse(ln.up[b][i]);
-      const float rd = ln.up[b][i] * ln.head[b], wr = dn * ln.tail[b];
-      const float self = s.diag[16 * b + 4 * g4 + i];
-      // by state, by other blocks, inside
-      const float rs = F * (q * sq[b][i] - k * sk[b][i]) * rd;
-      const float ro = (q * cq[b][i] + k * ck[b][i]) * rd;
-      const float end = wr * E * se[b][i];
-      const float wo = wr * cc[b][i];
-      const float in = ln.up[b][i] * (q * dq[i] + k * dk[i]) - kb * (dn * dc[i]);
-      rsum += rs;
-      esum = fmaf(kb, end, esum);
-      suf[i] = rs + ro + in;
-      pre[i] = kb * (end + wo);
-      if (b == 3) fromq += (q * tq[i] + k * tk[i]) * rd;
-      if (b == 0) before += kb * wr * tc[i];
-      const float dqi = fmaf(rd, fmaf(F, sq[b][i], cq[b][i]), fmaf(ln.up[b][i], dq[i], self * kb));
-      const float dri = fmaf(rd, fmaf(-F, sk[b][i], ck[b][i]), ln.up[b][i] * dk[i]);
-      const float col = end + wo + fmaf(dn, dc[i], self * q);
-      cq[b][i] = dqi * p.scale;
-      ck[b][i] = fmaf(bt[i], col, dri);
-      // q_hat . dq_hat, k_hat . dk_hat, k_hat . col over the wave's channels
-      const float a0 = row16_sum(ln.q[b][i] * cq[b][i]);
-      const float a1 = row16_sum(k * ck[b][i]);
-      const float a2 = row16_sum(k * col);
-      if (n16 == 0) {
-        const int t = 16 * b + 4 * g4 + i;
-        sr.red[0][w][t] = a0;
-        sr.red[1][w][t] = a1;
-        sr.red[2][w][t] = a2;
-      }
+      // hidden from the compiler, which would keep what it has formed above of these
+      asm volatile("" : "+v"(ln.up[b][i]), "+v"(ln.k[b][i]), "+v"(ln.q[b][i]));
+      dn[i] = inverse(ln.up[b][i]);
+      kb[i] = ln.k[b][i] * bt[i] * dn[i];
+      km[i] = ln.k[b][i] * ln.up[b][i];
+      qm[i] = ln.q[b][i] * ln.up[b][i];
     }
-    reads[b] = rows_sum(rsum);
-    ends[b] = rows_sum(esum);
-    if (b == 3) pass2 = rows_sum(fromq);
-    if (b == 0) pass1 = rows_sum(before);
+    const f32x4 dq = mfma4(lds4(s.dp[b] + n16 * GS + 4 * g4), kb, zero4());
+    const f32x4 dk = mfma4(lds4(s.da[b] + n16 * GS + 4 * g4), kb, zero4());
+    f32x4 dc = mfma4(col4(s.dp[b] + 4 * g4 * GS + n16, GS), qm, zero4());
+    dc = mfma4(col4(s.da[b] + 4 * g4 * GS + n16, GS), km, dc);
+    float E = ue;  // to the chunk's end
+#pragma unroll
+    for (int m = b + 1; m < NB; ++m) E *= T[m];
+    const float Fq = F * uq, Fk = F * uk, qT = uqr * T[2], kT = ukr * T[2], cT = uw * T[1];
+    float rsum = 0.f, esum = 0.f, across = 0.f;
+    float suf[4], pre[4], a0[4], a1[4], a2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float k = ln.k[b][i], q = ln.q[b][i], kbeta = k * bt[i];
+      const float rd = ln.up[b][i] * ln.head[b], wr = dn[i] * ln.tail[b];
+      const float kwr = kbeta * wr;
+      // readers: of the state, then of earlier blocks too
+      const float fs = Fq * sq[b][i], fk = Fk * sk[b][i];
+      float A = fs, B = -fk;
+      if (b > 0) {
+        A = fmaf(uqr, rq[i], A);
+        B = fmaf(ukr, rk[i], B);
+      }
+      if (b == 3) {
+        const float fq = qT * rqa[i], fr = kT * rka[i];
+        A += fq;
+        B += fr;
+        across = fmaf(fmaf(k, fr, q * fq), rd, across);
+      }
+      if (b > 0) rsum = fmaf(fmaf(-k, fk, q * fs), rd, rsum);
+      // writers: into dS, then for later blocks too
+      const float we = E * se[b][i];
+      float W = we;
+      if (b == 0) {
+        const float far = cT * c0b[i];
+        W = fmaf(uw, c0a[i], W + far);
+        across = fmaf(kwr, far, across);
+      }
+      if (b == 1) W = fmaf(uw, c1[i], W);
+      if (b == 2) W = fmaf(uw, c2[i], W);
+      if (b < 3) esum = fmaf(kwr, we, esum);
+      // with the block's own pairs, and at last the token's own
+      const float in = dn[i] * dc[i];
+      const float dqt = fmaf(rd, A, ln.up[b][i] * dq[i]);
+      const float dkt = fmaf(rd, B, ln.up[b][i] * dk[i]);
+      suf[i] = fmaf(-kbeta, in, fmaf(k, dkt, q * dqt));
+      pre[i] = kwr * W;
+      const float col = fmaf(self[i], q, fmaf(wr, W, in));
+      gq[b][i] = fmaf(self[i], kbeta, dqt);
+      gk[b][i] = fmaf(bt[i], col, dkt);
+      a0[i] = q * gq[b][i];
+      a1[i] = k * gk[b][i];
+      a2[i] = k * col;
+    }
+    // q_hat . dq_hat, k_hat . dk_hat, k_hat . col over the wave's channels
+    const float r0 = row16_sums(a0, n16), r1 = row16_sums(a1, n16), r2 = row16_sums(a2, n16);
+    if (n16 < 4) {
+      const int t = 16 * b + 4 * g4 + n16;
+      sr.red[0][w][t] = r0;
+      sr.red[1][w][t] = r1;
+      sr.red[2][w][t] = r2;
+    }
+    reads[b] = b > 0 ? rows_sum(rsum) : 0.f;
+    ends[b] = b < 3 ? rows_sum(esum) : 0.f;
+    if (b == 3) pass2 = rows_sum(across);
+    if (b == 0) pass1 = rows_sum(across);
     // suffix sums (from the token on) and prefix sums (before it) over the block
     const float stot = (suf[0] + suf[1]) + (suf[2] + suf[3]);
     const float ptot = (pre[0] + pre[1]) + (pre[2] + pre[3]);
@@ -505,6 +526,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   const Rows dqr = rows_of(p.dq, ch, p.dq_stride, int64_t(h) * D);
   const Rows dkr = rows_of(p.dk, ch, p.dk_stride, int64_t(h) * D);
   const Rows dgr = rows_of(p.dg, ch, p.dg_stride, per_head ? h : int64_t(h) * D);
+  const uint32_t dq0 = dqr.offset(4 * g4, kc), dk0 = dkr.offset(4 * g4, kc);
+  const uint32_t dg0 = dgr.offset(4 * g4, per_head ? 0 : kc);
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -513,14 +536,14 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
       if (t < ch.c) {
         const float rq = s.rq[t], rk = s.rk[t];
         const float slope = keep[(16 + 4 * b + i) * kThreads];
-        const float dq = rq * fmaf(-ln.q[b][i], sr.red[0][0][t], cq[b][i]);
-        const float dk = rk * fmaf(-ln.k[b][i], sr.red[1][0][t], ck[b][i]);
-        *dqr.at(t, kc) = to_bf16(dq);
-        *dkr.at(t, kc) = to_bf16(dk);
+        const float dq = rq * fmaf(-ln.q[b][i], sr.red[0][0][t], gq[b][i]);
+        const float dk = rk * fmaf(-ln.k[b][i], sr.red[1][0][t], gk[b][i]);
+        *dqr.from(dq0, 16 * b + i) = to_bf16(dq);
+        *dkr.from(dk0, 16 * b + i) = to_bf16(dk);
         if (!per_head)
-          *dgr.at(t, kc) = to_bf16(dg[b][i] * slope);
+          *dgr.from(dg0, 16 * b + i) = to_bf16(dg[b][i] * slope);
         else if (w == 0 && n16 == 0)
-          *dgr.at(t, 0) = to_bf16(sr.red[3][0][t] * slope);
+          *dgr.from(dg0, 16 * b + i) = to_bf16(sr.red[3][0][t] * slope);
       }
     }
 }
