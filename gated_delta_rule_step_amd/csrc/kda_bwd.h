@@ -61,6 +61,7 @@ struct DocOrder {
 //               32 kt + 4 (lane / 16) + 0..3 and 16 further
 //   KE, KG, QG  [m 8][t 2][hi, lo][lane]    key channel 16 m + lane % 16, tokens
 //               32 t + 4 (lane / 16) + 0..3 and 16 further
+//   O           [vt 8][t 2][lane]           value channel 16 vt + lane % 16, tokens as in KE
 // X0 and DV0 are accumulator tiles [vt 8][rt 4][lane][4 tokens], X and DV rows
 // [token][value], S and dS rows [key][value], all fp32.
 constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales of W and Z
@@ -71,7 +72,8 @@ constexpr int kOpKG = kOpZ + 32768;      // e^G k, times 2^12
 constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat, times 2^12
 constexpr int kOpX0 = kOpQG + 32768;     // T V
 constexpr int kOpDV0 = kOpX0 + 32768;    // T^T P^T dO
-constexpr int kOpX = kOpDV0 + 32768;     // x
+constexpr int kOpO = kOpDV0 + 32768;     // dO (bf16)
+constexpr int kOpX = kOpO + 16384;       // x
 constexpr int kOpDV = kOpX + 32768;      // dV
 constexpr int kOpS = kOpDV + 32768;      // S entering the chunk
 constexpr int kOpDS = kOpS + 65536;      // dS leaving it
@@ -118,6 +120,18 @@ __device__ __forceinline__ Scale scale_for(float top) {
   return {__uint_as_float(uint32_t(268 - e) << 23), __uint_as_float(uint32_t(e - 14) << 23)};
 }
 constexpr float kFixedUp = 4096.0f, kFixedUn = 1.0f / 4096.0f;  // operands within +-1
+
+__device__ __forceinline__ f32x4 mfma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4 c) {
+  c = mfma32(al, bh, c);
+  c = mfma32(ah, bl, c);
+  return mfma32(ah, bh, c);
+}
+
+// The largest magnitude over the four lanes that share a column of an accumulator tile.
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
 
 // Sum over the four 16-lane rows of a wave (lanes of equal lane % 16).
 __device__ __forceinline__ float rows_sum(float x) {

@@ -10,17 +10,22 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Chains: the states up each (document, head), and the state gradients down.
-// Value channels do not mix in either, so a wave owns NT tiles of 16 of them, with
-// all 128 key channels in eight accumulator tiles each, and the chain is sequential
-// over the chunks alone. What bounds it is the latency of one chunk: two products
-// that wait for each other. They run on fp16 MFMA with both sides split into high and
-// low parts (three terms, fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides,
-// which are the state and x in accumulator layout, are scaled per value channel.
+// Value channels do not mix in either, so a chain splits into tiles of 16 of them, and
+// it is sequential over the chunks alone. What bounds it is the latency of one chunk:
+// two products that wait for each other, with a handful of waves per CU to hide it. A tile
+// therefore belongs to two waves that hold 64 key channels each (four accumulator tiles):
+// both form their keys' part of the first product, exchange it through LDS, and then hold the
+// same x for the second. (One wave per tile: 8191 tokens, 12 heads, 616 us instead of 500;
+// six documents at 64 heads as fast.)
 //
-// A chunk's operands come in two tiles (W, then KE; or Z, then KG and QG) that all
-// waves share through LDS. Loads of a tile are issued two phases before it is read
-// and wait in registers in between; the barrier between the phases publishes one
-// tile and frees the other.
+// The products run on fp16 MFMA, both sides split into high and low parts (three terms,
+// fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides, the state and x in
+// accumulator layout, are scaled per value channel.
+//
+// A chunk's left operands come in two tiles (W, then KE; or Z, then KG and QG) that all
+// waves share through LDS. Loads of a tile are issued two phases before it is read and
+// wait in registers in between; the barrier between the phases publishes one tile, frees
+// the other, and publishes the exchanged parts too.
 __device__ __forceinline__ float pool_at(const BwdParams& p, int64_t e) {
   if (p.state_dtype == KDA_STATE_FP8)
     return f8x2_lo(static_cast<const uint8_t*>(p.pool)[e])[0];
@@ -29,7 +34,6 @@ __device__ __forceinline__ float pool_at(const BwdParams& p, int64_t e) {
 }
 
 constexpr int kTileBytes = 32768;
-constexpr int kChainLds = 3 * kTileBytes + 2 * 1024;
 
 // N 16-byte units per thread, from global memory to registers, and on to LDS.
 template <int N, int T>
@@ -37,8 +41,19 @@ struct Stage {
   u32x4 u[N];
   __device__ __forceinline__ void load(const uint8_t* src) {
 #pragma unroll
+    for (int i = 0; i < N; ++i) load_one(src, i);
+  }
+  // share `part` of `parts`: a CU takes in some 32 bytes a cycle, so a whole tile asked
+  // for at once would hold up the wave that asks; in shares it hides between products
+  template <int PARTS>
+  __device__ __forceinline__ void load_share(const uint8_t* src, int part) {
+#pragma unroll
     for (int i = 0; i < N; ++i)
-      u[i] = *reinterpret_cast<const u32x4*>(src + (i * T + int(threadIdx.x)) * 16);
+      if (i * PARTS / N == part) load_one(src, i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ __forceinline__ void load_one(const uint8_t* src, int i) {
+    u[i] = *reinterpret_cast<const u32x4*>(src + (i * T + int(threadIdx.x)) * 16);
   }
   __device__ __forceinline__ void store(uint8_t* dst) const {
 #pragma unroll
@@ -46,12 +61,6 @@ struct Stage {
       *reinterpret_cast<u32x4*>(dst + (i * T + int(threadIdx.x)) * 16) = u[i];
   }
 };
-
-// The largest magnitude of a value channel over the four lanes that share it.
-__device__ __forceinline__ float column_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
-}
 
 // Right-side fragments of N accumulator tiles (rows 16 m + 4 g4 + i): pairs of tiles
 // give 32 contraction indices.
@@ -78,16 +87,30 @@ struct Right {
   }
 };
 
-template <int NW, int NT>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(1, 2)))
-void chain_kernel(BwdParams p, DocOrder ord) {
-  constexpr int T = 64 * NW;
-  constexpr int PARTS = 8 / (NW * NT);
+constexpr int KS = 2;        // waves of a value tile
+constexpr int NM = 8 / KS;   // state tiles of a wave
+constexpr int NX = NB / KS;  // token blocks of x whose start and result a wave moves
+
+// Workgroups of TW value tiles.
+template <int TW>
+struct ChainShape {
+  static constexpr int kThreads = 64 * KS * TW;
+  static constexpr int kParts = 8 / TW;
+  static constexpr int kXch = KS * TW * 4096;  // each wave's part of x
+  static constexpr int kLds = 3 * kTileBytes + 2 * 1024 + kXch;
+};
+
+template <int TW>
+__global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdParams p,
+                                                                         DocOrder ord) {
+  constexpr int T = ChainShape<TW>::kThreads;
+  constexpr int PARTS = ChainShape<TW>::kParts;
   constexpr int NA = kTileBytes / 16 / T;
   extern __shared__ __align__(16) float smem_raw[];
   uint8_t* la = reinterpret_cast<uint8_t*>(smem_raw);
   uint8_t* lb = la + kTileBytes;
   float* tails = reinterpret_cast<float*>(lb + 2 * kTileBytes);  // of even and odd chunks
+  float* xch = tails + 512;                                      // [wave][rt][lane][4]
 
   // Chain c's parts are blocks (c / 8 * PARTS + part) * 8 + c % 8: blocks go to the
   // eight XCDs in turn, so the parts share one L2 copy of the operands.
@@ -97,173 +120,149 @@ void chain_kernel(BwdParams p, DocOrder ord) {
   const bool down = id & 1;
   const int64_t chain = id >> 1;
   if (chain >= int64_t(p.n_docs) * p.H) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kh = wave % KS;
   const int g4 = lane >> 4, n16 = lane & 15;
-  const int vt0 = (part * NW + wave) * NT;  // this wave's first value tile
+  const int v = 16 * (part * TW + wave / KS) + n16;  // this lane's value channel
+  const int k0 = 64 * kh + 4 * g4;                   // its first key channel
   const int h = int(chain % p.H);
   const int rank = int(chain / p.H);
   const int doc = ord.n > 0 ? ord.doc[rank] : rank;
-  const int64_t t0 = p.cu_seqlens[doc];
-  const int64_t len = int64_t(p.cu_seqlens[doc + 1]) - t0;
-  const int32_t slot = p.state_indices[doc];
+  const int32_t t0 = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc]);
+  const int32_t len = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc + 1]) - t0;
+  const int32_t slot = __builtin_amdgcn_readfirstlane(p.state_indices[doc]);
   const bool active = slot >= 0 && int64_t(slot) < p.num_slots;
-  const int64_t chunks = (len + C - 1) / C;
-  const int64_t state = (int64_t(doc) * p.H + h) * HEAD_ELEMS + (16 * vt0 + n16) * D + 4 * g4;
+  const int chunks = (len + C - 1) / C;
+  const int64_t state = (int64_t(doc) * p.H + h) * HEAD_ELEMS + v * D + k0;
   const int64_t step = int64_t(p.H) * kOps;
-  uint8_t* ops0 = p.ops + (doc_slot0(p.cu_seqlens, doc) * p.H + h) * int64_t(kOps);
+  uint8_t* ops0 = p.ops + ((int64_t(doc) + t0 / C) * p.H + h) * int64_t(kOps);
 
-  f32x4 s[NT][8];  // [key 16 m + 4 g4 + i][value 16 (vt0 + n) + n16]
+  f32x4 s[NM];  // [key k0 + 16 m + i][value v]
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int m = 0; m < 8; ++m) s[n][m] = zero4();
+  for (int m = 0; m < NM; ++m) s[m] = zero4();
 
-  const uint8_t* left = la + lane * 16;
-  const uint8_t* left2 = lb + lane * 16;
+  // tile A's fragments of this wave's keys, tile B's of its state tiles
+  const uint8_t* fa = la + kh * 4096 + lane * 16;
+  const uint8_t* fb = lb + kh * 16384 + lane * 16;
   auto frag = [](const uint8_t* base, int unit) {
     return *reinterpret_cast<const f16x8*>(base + unit * 1024);
   };
-  // acc[r] = sum over keys of tile A's row block r times the state
-  auto product_a = [&](const Right<8> (&b)[NT], f32x4 (&acc)[NT][NB]) {
+  Stage<NA, T> sa;  // the next tile A, and its chunk's tail
+  u32x4 st = {0u, 0u, 0u, 0u};
+  // this wave's part of x: the sum over its keys of tile A times the state
+  auto product = [&](const Right<NM>& b, f32x4 (&acc)[NB], const uint8_t* next) {
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
+    for (int r = 0; r < NB; ++r) {
+      acc[r] = zero4();
 #pragma unroll
-      for (int r = 0; r < NB; ++r) {
-        const f16x8 ah = frag(left, (r * 4 + kt) * 2), al = frag(left, (r * 4 + kt) * 2 + 1);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (kt == 0) acc[n][r] = zero4();
-          acc[n][r] = mfma32(al, b[n].hi[kt], acc[n][r]);
-          acc[n][r] = mfma32(ah, b[n].lo[kt], acc[n][r]);
-          acc[n][r] = mfma32(ah, b[n].hi[kt], acc[n][r]);
-        }
+      for (int t = 0; t < NM / 2; ++t) {
+        const f16x8 ah = frag(fa, r * 8 + t * 2), al = frag(fa, r * 8 + t * 2 + 1);
+        acc[r] = mfma32(al, b.hi[t], acc[r]);
+        acc[r] = mfma32(ah, b.lo[t], acc[r]);
+        acc[r] = mfma32(ah, b.hi[t], acc[r]);
       }
-  };
-  // s = e^Gl s + sign * (tile B's first half)^T b, or with the second half on o too
-  auto update = [&](const Right<NB> (&b)[NT], float sign, const f16x8 (*o)[2],
-                    const float* uno, const float* tail) {
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      f32x4 acc[NT], acc2[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n] = acc2[n] = zero4();
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const f16x8 ah = frag(left2, (m * 2 + t) * 2), al = frag(left2, (m * 2 + t) * 2 + 1);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n] = mfma32(al, b[n].hi[t], acc[n]);
-          acc[n] = mfma32(ah, b[n].lo[t], acc[n]);
-          acc[n] = mfma32(ah, b[n].hi[t], acc[n]);
-        }
-        if (o) {
-          const f16x8 qh = frag(left2, 32 + (m * 2 + t) * 2), ql = frag(left2, 33 + (m * 2 + t) * 2);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc2[n] = mfma32(ql, o[n][t], acc2[n]);
-            acc2[n] = mfma32(qh, o[n][t], acc2[n]);
-          }
-        }
-      }
-      const f32x4 eg = lds4(tail + 16 * m + 4 * g4);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float un = b[n].un * (sign * kFixedUn);
-        s[n][m] *= eg;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][m][i] = fmaf(acc[n][i], un, s[n][m][i]);
-        if (o)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][m][i] = fmaf(acc2[n][i], uno[n], s[n][m][i]);
-      }
+      sa.template load_share<NB>(next, r);
     }
+  };
+  // x = x0 + un * (what `product` left), rows written: the two waves of a tile add up their
+  // parts (x0 and the rows are shared between them, a part of the blocks each).
+  auto exchange_out = [&](f32x4 (&x)[NB], const f32x4 (&acc)[NB], float un, const f32x4 (&x0)[NX]) {
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+      x[r] = acc[r] * un;
+      if (r / NX == kh) x[r] += x0[r % NX];
+      *reinterpret_cast<f32x4*>(xch + ((wave * NB + r) * 64 + lane) * 4) = x[r];
+    }
+  };
+  auto exchange_in = [&](f32x4 (&x)[NB], float* rows) {
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+      x[r] += lds4(xch + (((wave ^ 1) * NB + r) * 64 + lane) * 4);
+      if (r / NX == kh)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[(16 * r + 4 * g4 + i) * D + v] = x[r][i];
+    }
+  };
+  auto store_state = [&](float* rows) {
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows[(k0 + 16 * m + i) * D + v] = s[m][i];
+  };
+  // the start of x of chunk n, this wave's token blocks
+  auto load_x0 = [&](f32x4 (&x0)[NX], int n, int op) {
+    const float* src = reinterpret_cast<const float*>(ops0 + n * step + op) +
+                       ((v >> 4) * NB * 64 + lane) * 4;
+#pragma unroll
+    for (int r = 0; r < NX; ++r) x0[r] = lds4(src + (NX * kh + r) * 256);
+  };
+  auto load_tail = [&](int n) {
+    if (wave == 0) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + lane * 16);
+  };
+  auto store_a = [&](int n) {
+    sa.store(la);
+    if (wave == 0) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + lane * 4) = st;
   };
 
   if (!down) {
     if (!active || len == 0) return;
     if (p.use_initial) {
+      const int64_t e = int64_t(slot) * p.slot_stride + int64_t(h) * HEAD_ELEMS + v * D + k0;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int64_t e = int64_t(slot) * p.slot_stride + int64_t(h) * HEAD_ELEMS +
-                          (16 * (vt0 + n) + n16) * D + 4 * g4;
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][m][i] = pool_at(p, e + 16 * m + i);
-      }
+        for (int i = 0; i < 4; ++i) s[m][i] = pool_at(p, e + 16 * m + i);
     }
-    Stage<NA, T> sa, sb;
-    u32x4 st = {0u, 0u, 0u, 0u};
-    auto load_a = [&](int64_t n) {
-      sa.load(ops0 + n * step + kOpW);
-      if (threadIdx.x < 64) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + threadIdx.x * 16);
-    };
-    auto store_a = [&](int64_t n) {
-      sa.store(la);
-      if (threadIdx.x < 64) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + threadIdx.x * 4) = st;
-    };
-    f32x4 x[NT][NB];  // T V of the next chunk, asked for a phase ahead
-    auto load_x = [&](int64_t n) {
-      const float* X = reinterpret_cast<const float*>(ops0 + n * step + kOpX0) +
-                       (vt0 * NB * 64 + lane) * 4;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < NB; ++r) x[j][r] = lds4(X + (j * NB + r) * 256);
-    };
-    load_a(0);
-    load_x(0);
+    Stage<NA, T> sb;
+    f32x4 x0[NX];  // of the next chunk, asked for a phase ahead
+    sa.load(ops0 + kOpW);
+    load_tail(0);
+    load_x0(x0, 0, kOpX0);
     store_a(0);
     sb.load(ops0 + kOpKE);
     __syncthreads();
-    for (int64_t n = 0; n < chunks; ++n) {
+    for (int n = 0; n < chunks; ++n) {
       uint8_t* ops = ops0 + n * step;
       const bool more = n + 1 < chunks;
+      const uint8_t* after = more ? ops + step : ops;  // (the last chunk asks for itself again)
       const float* tail = tails + (n & 1) * 256;
-      float* S = reinterpret_cast<float*>(ops + kOpS) + 4 * g4 * D + 16 * vt0 + n16;
-      float* X = reinterpret_cast<float*>(ops + kOpX) + 4 * g4 * D + 16 * vt0 + n16;
+      f32x4 x[NB];
       // ---- x = T V - W S
-      if (more) load_a(n + 1);
+      load_tail(more ? n + 1 : n);
       {
-        Right<8> b[NT];
-        f32x4 acc[NT][NB];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j].set(s[j]);
-#pragma unroll
-          for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[(16 * m + i) * D + 16 * j] = s[j][m][i];
-        }
-        product_a(b, acc);
-        const float unw = tail[kTailUnW];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int r = 0; r < NB; ++r) {
-            const float un = -b[j].un * unw;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[j][r][i] = fmaf(acc[j][r][i], un, x[j][r][i]);
-              X[(16 * r + i) * D + 16 * j] = x[j][r][i];
-            }
-          }
+        Right<NM> b;
+        f32x4 acc[NB];
+        b.set(s);
+        product(b, acc, after + kOpW);
+        store_state(reinterpret_cast<float*>(ops + kOpS));
+        exchange_out(x, acc, -b.un * tail[kTailUnW], x0);
       }
-      if (!more) return;  // the state after the last chunk is not needed
-      sb.store(lb);
+      if (more) sb.store(lb);
       __syncthreads();
+      exchange_in(x, reinterpret_cast<float*>(ops + kOpX));
+      if (!more) return;  // the state after the last chunk is not needed
       // ---- S = e^Gl S + KE^T (beta x)
-      {
-        Right<NB> b[NT];
+      Right<NB> b;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+      for (int r = 0; r < NB; ++r) x[r] *= lds4(tail + kTailBeta + 16 * r + 4 * g4);
+      b.set(x);
+      load_x0(x0, n + 1, kOpX0);
+      const float un = b.un * kFixedUn;
 #pragma unroll
-          for (int r = 0; r < NB; ++r) x[j][r] *= lds4(tail + kTailBeta + 16 * r + 4 * g4);
-          b[j].set(x[j]);
+      for (int m = 0; m < NM; ++m) {
+        f32x4 acc = zero4();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f16x8 ah = frag(fb, m * 4 + t * 2), al = frag(fb, m * 4 + t * 2 + 1);
+          acc = mfma32(al, b.hi[t], acc);
+          acc = mfma32(ah, b.lo[t], acc);
+          acc = mfma32(ah, b.hi[t], acc);
         }
-        load_x(n + 1);
-        sb.load(ops + step + kOpKE);
-        update(b, 1.0f, nullptr, nullptr, tail);
+        sb.template load_share<NM>(after + kOpKE, m);
+        s[m] *= lds4(tail + k0 + 16 * m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[m][i] = fmaf(acc[i], un, s[m][i]);
       }
       store_a(n + 1);
       __syncthreads();
@@ -273,115 +272,85 @@ void chain_kernel(BwdParams p, DocOrder ord) {
 
   if (p.d_final && active) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
-      for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][m][i] = p.d_final[state + n * 16 * D + 16 * m + i];
+      for (int i = 0; i < 4; ++i) s[m][i] = p.d_final[state + 16 * m + i];
   }
   if (active && chunks > 0) {
-    Stage<NA, T> sa;
     Stage<2 * NA, T> sb;
-    u32x4 st = {0u, 0u, 0u, 0u};
-    auto load_a = [&](int64_t n) {
-      sa.load(ops0 + n * step + kOpZ);
-      if (threadIdx.x < 64) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + threadIdx.x * 16);
-    };
-    auto store_a = [&](int64_t n) {
-      sa.store(la);
-      if (threadIdx.x < 64) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + threadIdx.x * 4) = st;
-    };
-    f32x4 x[NT][NB];  // T^T P^T dO and dO of the next chunk
-    uint16_t ow[NT][NB][4];
-    auto load_x = [&](int64_t n) {
-      const float* DV = reinterpret_cast<const float*>(ops0 + n * step + kOpDV0) +
-                        (vt0 * NB * 64 + lane) * 4;
-      const int c = int(min<int64_t>(C, len - n * C));
-      const Rows o = rows_of(p.dout, Chunk{doc, t0 + n * C, c, true}, p.dout_stride, int64_t(h) * D);
+    f32x4 x0[NX];
+    u32x4 ow[2];  // dO: 64 tokens of this lane's value, in the order of a right fragment
+    auto load_o = [&](int n) {
+      const uint8_t* src = ops0 + n * step + kOpO + ((v >> 4) * 2 * 64 + lane) * 16;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < NB; ++r) {
-          x[j][r] = lds4(DV + (j * NB + r) * 256);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            ow[j][r][i] = *o.at(min(16 * r + 4 * g4 + i, c - 1), 16 * (vt0 + j) + n16);
-        }
+      for (int t = 0; t < 2; ++t) ow[t] = *reinterpret_cast<const u32x4*>(src + t * 1024);
     };
-    load_a(chunks - 1);
-    load_x(chunks - 1);
+    sa.load(ops0 + (chunks - 1) * step + kOpZ);
+    load_tail(chunks - 1);
+    load_x0(x0, chunks - 1, kOpDV0);
+    load_o(chunks - 1);
     store_a(chunks - 1);
     sb.load(ops0 + (chunks - 1) * step + kOpKG);
     __syncthreads();
-    for (int64_t n = chunks - 1; n >= 0; --n) {
+    for (int n = chunks - 1; n >= 0; --n) {
       uint8_t* ops = ops0 + n * step;
-      const int c = int(min<int64_t>(C, len - n * C));
+      const uint8_t* after = n > 0 ? ops - step : ops;
       const float* tail = tails + (n & 1) * 256;
-      float* dS = reinterpret_cast<float*>(ops + kOpDS) + 4 * g4 * D + 16 * vt0 + n16;
-      float* DV = reinterpret_cast<float*>(ops + kOpDV) + 4 * g4 * D + 16 * vt0 + n16;
+      f32x4 x[NB];
       // ---- dV = T^T P^T dO + Z dS
-      if (n > 0) load_a(n - 1);
+      load_tail(n > 0 ? n - 1 : 0);
       {
-        Right<8> b[NT];
-        f32x4 acc[NT][NB];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j].set(s[j]);
-#pragma unroll
-          for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dS[(16 * m + i) * D + 16 * j] = s[j][m][i];
-        }
-        product_a(b, acc);
-        const float unz = tail[kTailUnZ];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int r = 0; r < NB; ++r) {
-            const float un = b[j].un * unz;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[j][r][i] = fmaf(acc[j][r][i], un, x[j][r][i]);
-              DV[(16 * r + i) * D + 16 * j] = x[j][r][i];
-            }
-          }
+        Right<NM> b;
+        f32x4 acc[NB];
+        b.set(s);
+        product(b, acc, after + kOpZ);
+        store_state(reinterpret_cast<float*>(ops + kOpDS));
+        exchange_out(x, acc, b.un * tail[kTailUnZ], x0);
       }
-      if (n == 0 && !p.d_initial) return;
-      sb.store(lb);
+      const bool more = n > 0 || p.d_initial;
+      if (more) sb.store(lb);
       __syncthreads();
-      // ---- dS = e^Gl dS - KG^T dV + scale QG^T dO
-      {
-        Right<NB> b[NT];
-        f16x8 o[NT][2];
-        float uno[NT];
+      exchange_in(x, reinterpret_cast<float*>(ops + kOpDV));
+      if (!more) return;
+      // ---- dS = e^Gl dS - KG^T dV + scale QG^T dO. dO has 8 bits: its high part is exact.
+      Right<NB> b;
+      b.set(x);
+      f16x8 o[2];
+      float y[2][8], top = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j].set(x[j]);
-          // dO has 8 bits: its high part alone is exact
-          f32x4 y[NB];
-          float top = 0.f;
+      for (int t = 0; t < 2; ++t) {
+        unpack8_bf16(ow[t], y[t]);
 #pragma unroll
-          for (int r = 0; r < NB; ++r)
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[t][i]));
+      }
+      const Scale sc = scale_for(column_max(top));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[r][i] = 16 * r + 4 * g4 + i < c ? bf1(ow[j][r][i]) : 0.f;
-              top = fmaxf(top, fabsf(y[r][i]));
-            }
-          const Scale sc = scale_for(column_max(top));
-          uno[j] = sc.un * (p.scale * kFixedUn);
+      for (int t = 0; t < 2; ++t) {
+        u32x4 w;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const f32x4 a = y[2 * t] * sc.up, d = y[2 * t + 1] * sc.up;
-            o[j][t] = __builtin_bit_cast(
-                f16x8, u32x4{pack_f16x2(a[0], a[1]), pack_f16x2(a[2], a[3]),
-                             pack_f16x2(d[0], d[1]), pack_f16x2(d[2], d[3])});
-          }
+        for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(y[t][2 * i] * sc.up, y[t][2 * i + 1] * sc.up);
+        o[t] = __builtin_bit_cast(f16x8, w);
+      }
+      load_x0(x0, n > 0 ? n - 1 : 0, kOpDV0);
+      load_o(n > 0 ? n - 1 : 0);
+      const float un = -b.un * kFixedUn, uno = sc.un * (p.scale * kFixedUn);
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        f32x4 acc = zero4(), acc2 = zero4();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f16x8 ah = frag(fb, m * 4 + t * 2), al = frag(fb, m * 4 + t * 2 + 1);
+          const f16x8 qh = frag(fb, 32 + m * 4 + t * 2), ql = frag(fb, 33 + m * 4 + t * 2);
+          acc = mfma32(al, b.hi[t], acc);
+          acc2 = mfma32(ql, o[t], acc2);
+          acc = mfma32(ah, b.lo[t], acc);
+          acc2 = mfma32(qh, o[t], acc2);
+          acc = mfma32(ah, b.hi[t], acc);
         }
-        if (n > 0) {
-          load_x(n - 1);
-          sb.load(ops - step + kOpKG);
-        }
-        update(b, -1.0f, o, uno, tail);
+        sb.template load_share<NM>(after + kOpKG, m);
+        s[m] *= lds4(tail + k0 + 16 * m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[m][i] = fmaf(acc2[i], uno, fmaf(acc[i], un, s[m][i]));
       }
       if (n > 0) store_a(n - 1);
       __syncthreads();
@@ -389,41 +358,30 @@ void chain_kernel(BwdParams p, DocOrder ord) {
   }
   if (p.d_initial) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-        *reinterpret_cast<f32x4*>(p.d_initial + state + n * 16 * D + 16 * m) = s[n][m];
+    for (int m = 0; m < NM; ++m) *reinterpret_cast<f32x4*>(p.d_initial + state + 16 * m) = s[m];
   }
 }
 
-template <int NW, int NT>
-void launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
-  constexpr int PARTS = 8 / (NW * NT);
+template <int TW>
+hipError_t launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
+  using Shape = ChainShape<TW>;
+  static const hipError_t lds =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(chain_kernel<TW>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, Shape::kLds);
+  if (lds != hipSuccess) return lds;
   const int64_t ids = (int64_t(p.n_docs) * p.H * 2 + 7) / 8 * 8;  // both directions
-  hipLaunchKernelGGL((chain_kernel<NW, NT>), dim3(unsigned(ids * PARTS)), dim3(64 * NW), kChainLds,
-                     stream, p, ord);
+  hipLaunchKernelGGL(chain_kernel<TW>, dim3(unsigned(ids * Shape::kParts)), dim3(Shape::kThreads),
+                     Shape::kLds, stream, p, ord);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
-  static const hipError_t lds = [] {
-    const void* all[] = {reinterpret_cast<const void*>(chain_kernel<2, 1>),
-                         reinterpret_cast<const void*>(chain_kernel<4, 1>),
-                         reinterpret_cast<const void*>(chain_kernel<4, 2>)};
-    for (const void* f : all)
-      if (const hipError_t e = hipFuncSetAttribute(
-              f, hipFuncAttributeMaxDynamicSharedMemorySize, kChainLds))
-        return e;
-    return hipSuccess;
-  }();
-  if (lds != hipSuccess) return lds;
-  const int64_t chains = int64_t(p.n_docs) * p.H;
-  // workgroups per chain and direction: as many as it takes to fill the chip
-  if (chains <= 32) launch_chain<2, 1>(p, ord, stream);
-  else if (chains <= 128) launch_chain<4, 1>(p, ord, stream);
-  else launch_chain<4, 2>(p, ord, stream);
-  return hipGetLastError();
+  // Two value tiles per workgroup where the chains alone would leave most CUs idle (12 chains
+  // of 8191 tokens: 500 us against 575 with four), else four (156 chains: 400 against 470).
+  return int64_t(p.n_docs) * p.H <= 32 ? launch_chain<2>(p, ord, stream)
+                                       : launch_chain<4>(p, ord, stream);
 }
 
 }  // namespace bwd

@@ -73,12 +73,6 @@ __device__ __forceinline__ float max8(f32x4 a, f32x4 b) {
   for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(fabsf(a[i]), fabsf(b[i])));
   return t;
 }
-__device__ __forceinline__ f32x4 mfma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4 c) {
-  c = mfma32(al, bh, c);
-  c = mfma32(ah, bl, c);
-  return mfma32(ah, bh, c);
-}
-
 // Keeps the compiler from moving work of one stage into another: it would fetch the
 // fragments of several stages at once and run out of registers.
 __device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
@@ -556,7 +550,22 @@ __global__ __launch_bounds__(1024) void param_kernel(BwdParams p) {
   const int h = blockIdx.x;
   const int c = threadIdx.x & (D - 1), grp = threadIdx.x / D;
   float b = 0.f, a = 0.f;
-  for (int64_t n = grp; n < p.slots; n += 8) {
+  int64_t n = grp;
+  for (; n + 56 < p.slots; n += 64) {  // eight loads in flight, added in the same order
+    float xb[8], xa[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float* x = p.partial + ((n + 8 * i) * p.H + h) * int64_t(2 * D);
+      xb[i] = x[c];
+      xa[i] = x[D + c];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      b += xb[i];
+      a += xa[i];
+    }
+  }
+  for (; n < p.slots; n += 8) {
     const float* x = p.partial + (n * p.H + h) * int64_t(2 * D);
     b += x[c];
     a += x[D + c];
