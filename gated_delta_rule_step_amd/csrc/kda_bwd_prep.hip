@@ -9,35 +9,56 @@ namespace bwd {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Preparation: one workgroup per (chunk, head); a wave owns 16 channels.
-constexpr int RS = D + 4;  // padded row (fp32) of [token][channel] LDS arrays
-constexpr int AS = C + 4;  // padded row of [token][token] LDS arrays
+// Preparation: one workgroup per (chunk, head); a wave owns 16 channels. Its phases are
+// bound by different things (loads and gates, fp32 MFMA, latency, stores), so LDS and
+// registers are kept to half a CU and two workgroups overlap theirs.
+constexpr int HC = D / 2;   // channels whose rows are in LDS at a time
+constexpr int RS = HC + 4;  // padded row (fp32) of [token][channel]
+constexpr int GS = 20;      // row (fp32) of a 16 x 16 block
+constexpr int PS = C + 8;   // row (fp16) of T and P as MFMA operands
+constexpr int kBlocks = NB * (NB + 1) / 2;
 
-// Pairs of different blocks, I > J.
+// Blocks on and below the diagonal, I >= J, and strictly below it.
+__host__ __device__ constexpr int block_index(int I, int J) { return I * (I + 1) / 2 + J; }
 __host__ __device__ constexpr int pair_index(int I, int J) { return I * (I - 1) / 2 + J; }
 
-constexpr int PS = C + 8;  // row (fp16) of T and P as MFMA operands
-
+// First the decayed rows of half the channels, from which A and P are formed.
+struct Rows64 {
+  float km[C * RS];     // readers: up k
+  float kw[C * RS];     // writers: dn k
+  float qm[C * RS];     // readers: up q_hat
+  float pair[NP * HC];  // factor of a block pair
+};
+// Then A, P and T, and T and P as operands: high and low parts, [row][the other index in
+// the order of a right fragment]; blocks that a 32-index contraction takes along and that
+// hold nothing are zeros.
+struct Blocks {
+  float pm[kBlocks][16 * GS];  // P / (scale beta)
+  float tm[kBlocks][16 * GS];  // T
+  union {
+    struct {
+      float am[kBlocks][16 * GS];  // A
+      uint16_t v[C * D], o[C * D];  // V, dO
+    };
+    struct {
+      uint16_t t[2][C * PS];   // T
+      uint16_t tt[2][C * PS];  // beta T, transposed
+      uint16_t pt[2][C * PS];  // P^T / (scale beta)
+    };
+  };
+};
 struct PrepSmem {
-  float km[C * RS];    // readers: up k; then T and P as operands
-  float kb[C * RS];    // writers: beta dn k
-  float qm[C * RS];    // up q', then V and dO (bf16)
-  float am[C * AS];    // A
-  float pm[C * AS];    // P
-  float tm[C * AS];    // T
-  float pair[NP * D];  // factor of a block pair
-  float top[2][8];     // largest magnitudes of W and Z, per wave
-  uint32_t ttop, ptop; // of T and P (as bits)
-  alignas(16) float rq[C], rk[C], beta[C];
+  union {
+    Rows64 rows;
+    Blocks b;
+  };
+  alignas(16) float beta[C];
+  alignas(16) float rq[C], rk[C];
+  float top[2][8];      // largest magnitudes of W and Z, per wave
+  uint32_t ttop, ptop;  // of T and P (as bits)
 };
-// High and low parts, [row][the other index in the order of a right fragment]; blocks
-// that a 32-index contraction takes along and that hold nothing are zeros.
-struct TPlanes {
-  uint16_t t[2][C * PS];   // T
-  uint16_t tt[2][C * PS];  // T^T
-  uint16_t pt[2][C * PS];  // P^T
-};
-static_assert(sizeof(TPlanes) <= sizeof(float) * 2 * C * RS, "they fit over km and kb");
+static_assert(sizeof(PrepSmem) <= 80 * 1024, "two workgroups per CU");
+
 // Position of index t among 32: a fragment holds, for lane group g, 4 g .. 4 g + 3 of a
 // block of 16 and of the next one.
 __device__ __forceinline__ int perm32(int t) {
@@ -51,8 +72,11 @@ __device__ __forceinline__ float wave_max(float x) {
 __device__ __forceinline__ float max4(f32x4 x) {
   return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 }
-
-constexpr int VS = 2 * RS;  // row of V and dO in uint16: V first, dO from RS on
+// Block row and column of the n-th block on or below the diagonal.
+__device__ __forceinline__ void block_of(int n, int& I, int& J) {
+  I = 0, J = n;
+  while (J > I) J -= ++I;
+}
 
 // 64 tokens of a bf16 column as right fragments, scaled by the column's largest magnitude.
 __device__ __forceinline__ void bf16_fragments(const u32x4 (&w)[2], f16x8 (&f)[2], float& un) {
@@ -74,10 +98,7 @@ __device__ __forceinline__ void bf16_fragments(const u32x4 (&w)[2], f16x8 (&f)[2
   }
 }
 
-// Writers' operands carry beta, which may exceed 1 where it is given: a smaller scale.
-constexpr float kBetaUp = 16.0f;
-
-__global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
+__global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   extern __shared__ __align__(16) float smem_raw[];
   PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int64_t sigma = blockIdx.x;
@@ -94,27 +115,16 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
   RawLane raw;
   load_lane(p, ch, h, kc, g4, raw);
   token_scalars(p, ch, h, s.rq, s.rk, s.beta);
-  u32x4 vw[C / (kThreads / 16)], ow[C / (kThreads / 16)];  // V and dO, written to LDS below
-  const Rows vr = rows_of(p.v, ch, p.v_stride, int64_t(h) * D);
-  const Rows orow = rows_of(p.dout, ch, p.dout_stride, int64_t(h) * D);
-#pragma unroll
-  for (int j = 0; j < C / (kThreads / 16); ++j) {
-    const int t = min(int(threadIdx.x >> 4) + j * (kThreads / 16), ch.c - 1);
-    vw[j] = *reinterpret_cast<const u32x4_u*>(vr.at(t, (threadIdx.x & 15) * 8));
-    ow[j] = *reinterpret_cast<const u32x4_u*>(orow.at(t, (threadIdx.x & 15) * 8));
-  }
-  __syncthreads();
   if (threadIdx.x == 0) s.ttop = s.ptop = 0;
+  __syncthreads();
   if (threadIdx.x < C) tail[kTailBeta + threadIdx.x] = s.beta[threadIdx.x];
 
   // ---- the decayed rows, and what depends on them channel by channel alone
-  // left fragments of e^G k and beta e^(Gl-G) k: channel kc, pairs of token blocks
-  f16x8 kgh[2], kgl[2], keh[2], kel[2];
+  Lane ln;
+  make_lane<false>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, nullptr);
   {
-    Lane ln;
-    make_lane<false>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, nullptr);
     float from[NB], to[NB];  // from the chunk's start to the block's middle, to its end
-    float o = 1.f, e = 1.f;
+    float o = kFixedUp, e = kFixedUp;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       from[b] = o * ln.head[b];
@@ -125,85 +135,123 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
       to[b] = e * ln.tail[b];
       e *= ln.head[b] * ln.tail[b];
     }
-    if (g4 == 0) {
-      tail[kc] = o;
+    if (g4 == 0) tail[kc] = o * kFixedUn;
 #pragma unroll
-      for (int I = 1; I < NB; ++I) {
-        float mid = ln.head[I];
+    for (int t = 0; t < 2; ++t) {
+      u32x2 gh[2], gl[2], eh[2], el[2], qh[2], ql[2];
 #pragma unroll
-        for (int J = I - 1; J >= 0; --J) {
-          s.pair[pair_index(I, J) * D + kc] = mid * ln.tail[J];
-          mid *= ln.head[J] * ln.tail[J];
+      for (int u = 0; u < 2; ++u) {
+        const int b = 2 * t + u;
+        f32x4 qg, kg, ke;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float uf = ln.up[b][i] * from[b];
+          kg[i] = ln.k[b][i] * uf;
+          qg[i] = ln.q[b][i] * uf;
+          ke[i] = ln.k[b][i] * (inverse(ln.up[b][i]) * to[b]);
+        }
+        split4h(kg, gh[u], gl[u]);
+        split4h(ke, eh[u], el[u]);
+        split4h(qg, qh[u], ql[u]);
+      }
+      uint8_t* at = ops + ((w * 2 + t) * 2 * 64 + lane) * 16;
+      *reinterpret_cast<f16x8*>(at + kOpKE) = join8(eh[0], eh[1]);
+      *reinterpret_cast<f16x8*>(at + kOpKE + 1024) = join8(el[0], el[1]);
+      *reinterpret_cast<f16x8*>(at + kOpKG) = join8(gh[0], gh[1]);
+      *reinterpret_cast<f16x8*>(at + kOpKG + 1024) = join8(gl[0], gl[1]);
+      *reinterpret_cast<f16x8*>(at + kOpQG) = join8(qh[0], qh[1]);
+      *reinterpret_cast<f16x8*>(at + kOpQG + 1024) = join8(ql[0], ql[1]);
+    }
+  }
+
+  // ---- A and P, block by block (10 each on and below the diagonal), half the channels
+  // at a time: the waves that own them write their rows, then all take their blocks
+  constexpr int kTasks = 2 * kBlocks, kRounds = (kTasks + 7) / 8;
+  f32x4 acc[kRounds];
+#pragma unroll
+  for (int n = 0; n < kRounds; ++n) acc[n] = zero4();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (half) __syncthreads();
+    if (w / 4 == half) {
+      const int c = kc - HC * half;
+      if (g4 == 0) {
+#pragma unroll
+        for (int I = 1; I < NB; ++I) {
+          float mid = ln.head[I];
+#pragma unroll
+          for (int J = I - 1; J >= 0; --J) {
+            s.rows.pair[pair_index(I, J) * HC + c] = mid * ln.tail[J];
+            mid *= ln.head[J] * ln.tail[J];
+          }
         }
       }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = (16 * b + 4 * g4 + i) * RS + c;
+          s.rows.km[at] = ln.k[b][i] * ln.up[b][i];
+          s.rows.qm[at] = ln.q[b][i] * ln.up[b][i];
+          s.rows.kw[at] = ln.k[b][i] * inverse(ln.up[b][i]);
+        }
     }
-    u32x2 half[4];  // of the even block
+    __syncthreads();
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float ef = from[b], et = to[b];
-      f32x4 qg, kee, kg, ke;
+    for (int n = 0; n < kRounds; ++n) {
+      const int task = w + 8 * n;
+      if (task >= kTasks) continue;
+      int I, J;
+      block_of(task % kBlocks, I, J);
+      const float* left = (task >= kBlocks ? s.rows.qm : s.rows.km) + (16 * I + n16) * RS + 4 * g4;
+      const float* right = s.rows.kw + (16 * J + n16) * RS + 4 * g4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * b + 4 * g4 + i;
-        const float up = ln.up[b][i], down = inverse(up);
-        const float km = ln.k[b][i] * up, qm = ln.q[b][i] * up * p.scale;
-        const float kb = ln.k[b][i] * down * s.beta[t];
-        s.km[t * RS + kc] = km;
-        s.qm[t * RS + kc] = qm;
-        s.kb[t * RS + kc] = kb;
-        kg[i] = km * ef;
-        qg[i] = ln.q[b][i] * up * ef;
-        kee[i] = ln.k[b][i] * down * et;
-        ke[i] = kb * et;
+      for (int m = 0; m < HC / 16; ++m) {
+        f32x4 a = lds4(left + 16 * m);
+        if (I != J) a *= lds4(s.rows.pair + pair_index(I, J) * HC + 16 * m + 4 * g4);
+        acc[n] = mfma4(a, lds4(right + 16 * m), acc[n]);
       }
-      const int at = ((w * 2 + (b >> 1)) * 2 * 64 + lane) * 16 + 8 * (b & 1);
-      u32x2 hi, lo;
-      split4h(kee * kFixedUp, hi, lo);
-      *reinterpret_cast<u32x2*>(ops + kOpKE + at) = hi;
-      *reinterpret_cast<u32x2*>(ops + kOpKE + at + 1024) = lo;
-      split4h(kg * kFixedUp, hi, lo);
-      *reinterpret_cast<u32x2*>(ops + kOpKG + at) = hi;
-      *reinterpret_cast<u32x2*>(ops + kOpKG + at + 1024) = lo;
-      u32x2 eh, el;
-      split4h(ke * kBetaUp, eh, el);
-      if (b & 1) {
-        kgh[b >> 1] = join8(half[0], hi), kgl[b >> 1] = join8(half[1], lo);
-        keh[b >> 1] = join8(half[2], eh), kel[b >> 1] = join8(half[3], el);
-      } else {
-        half[0] = hi, half[1] = lo, half[2] = eh, half[3] = el;
-      }
-      split4h(qg * kFixedUp, hi, lo);
-      *reinterpret_cast<u32x2*>(ops + kOpQG + at) = hi;
-      *reinterpret_cast<u32x2*>(ops + kOpQG + at + 1024) = lo;
+    }
+  }
+  // V and dO on their way to LDS
+  u32x4 vw[C / (kThreads / 16)], ow[C / (kThreads / 16)];
+  {
+    const Rows vr = rows_of(p.v, ch, p.v_stride, int64_t(h) * D);
+    const Rows orow = rows_of(p.dout, ch, p.dout_stride, int64_t(h) * D);
+#pragma unroll
+    for (int j = 0; j < C / (kThreads / 16); ++j) {
+      const int t = min(int(threadIdx.x >> 4) + j * (kThreads / 16), ch.c - 1);
+      vw[j] = *reinterpret_cast<const u32x4_u*>(vr.at(t, (threadIdx.x & 15) * 8));
+      ow[j] = *reinterpret_cast<const u32x4_u*>(orow.at(t, (threadIdx.x & 15) * 8));
     }
   }
   __syncthreads();
-
-  // ---- A and P, block by block (10 each on and below the diagonal)
-  for (int task = w; task < NB * (NB + 1); task += kThreads / 64) {
-    const bool is_p = task >= NB * (NB + 1) / 2;
-    int I = 0, J = is_p ? task - NB * (NB + 1) / 2 : task;
-    while (J > I) J -= ++I;
-    const float* left = (is_p ? s.qm : s.km) + (16 * I + n16) * RS + 4 * g4;
-    const float* right = s.kb + (16 * J + n16) * RS + 4 * g4;
-    f32x4 acc = zero4();
 #pragma unroll
-    for (int m = 0; m < D / 16; ++m) {
-      f32x4 a = lds4(left + 16 * m);
-      if (I != J) a *= lds4(s.pair + pair_index(I, J) * D + 16 * m + 4 * g4);
-      acc = mfma4(a, lds4(right + 16 * m), acc);
-    }
-    float* dst = (is_p ? s.pm : s.am) + (16 * I + 4 * g4) * AS + 16 * J + n16;
+  for (int n = 0; n < kRounds; ++n) {
+    const int task = w + 8 * n;
+    if (task >= kTasks) continue;
+    const bool is_p = task >= kBlocks;
+    int I, J;
+    block_of(task % kBlocks, I, J);
+    if (!is_p) acc[n] *= s.beta[16 * J + n16];
+    float* dst = (is_p ? s.b.pm : s.b.am)[task % kBlocks] + 4 * g4 * GS + n16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int over = I == J ? n16 - (4 * g4 + i) : -1;  // column beyond the row
-      if (!(over < 0 || (is_p && over == 0))) acc[i] = 0.f;
-      dst[i * AS] = acc[i];
+      if (!(over < 0 || (is_p && over == 0))) acc[n][i] = 0.f;
+      dst[i * GS] = acc[n][i];
     }
     if (is_p) {
-      const float top = wave_max(max4(acc));
+      const float top = wave_max(max4(acc[n]));
       if (lane == 0) atomicMax(&s.ptop, __float_as_uint(top));
     }
+  }
+#pragma unroll
+  for (int j = 0; j < C / (kThreads / 16); ++j) {
+    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
+    if (t >= ch.c) vw[j] = ow[j] = u32x4{0u, 0u, 0u, 0u};
+    *reinterpret_cast<u32x4*>(s.b.v + t * D + (threadIdx.x & 15) * 8) = vw[j];
+    *reinterpret_cast<u32x4*>(s.b.o + t * D + (threadIdx.x & 15) * 8) = ow[j];
   }
   __syncthreads();
 
@@ -211,8 +259,8 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
   // the inverse is (1 + N)(1 + N^2)(1 + N^4)(1 + N^8). A product X Y takes X^T as
   // its left fragment, so every power is kept with its transpose.
   if (w < NB) {
-    const float* a = s.am + 16 * w * AS + 16 * w;
-    f32x4 n = -col4(a + 4 * g4 * AS + n16, AS), nt = -lds4(a + n16 * AS + 4 * g4);
+    const float* a = s.b.am[block_index(w, w)];
+    f32x4 n = -col4(a + 4 * g4 * GS + n16, GS), nt = -lds4(a + n16 * GS + 4 * g4);
     f32x4 r = n, rt = nt;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -226,79 +274,15 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
       const f32x4 r2 = mfma4(rt, n2, r), r2t = mfma4(n2, rt, rt);
       n = n2, nt = n2t, r = r2, rt = r2t;
     }
-    float* dst = s.tm + (16 * w + 4 * g4) * AS + 16 * w + n16;
+    float* dst = s.b.tm[block_index(w, w)] + 4 * g4 * GS + n16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dst[i * AS] = r[i];
+    for (int i = 0; i < 4; ++i) dst[i * GS] = r[i];
     const float top = wave_max(max4(r));
     if (lane == 0) atomicMax(&s.ttop, __float_as_uint(top));
   }
-  // V and dO (bf16) take the place of up q'
-  {
-    uint16_t* vo = reinterpret_cast<uint16_t*>(s.qm);
-    const int c0 = (threadIdx.x & 15) * 8;
-#pragma unroll
-    for (int j = 0; j < C / (kThreads / 16); ++j) {
-      const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
-      if (t >= ch.c) vw[j] = ow[j] = u32x4{0u, 0u, 0u, 0u};
-      typedef u32x4 u32x4_8 __attribute__((aligned(8)));
-      *reinterpret_cast<u32x4_8*>(vo + t * VS + c0) = vw[j];
-      *reinterpret_cast<u32x4_8*>(vo + t * VS + RS + c0) = ow[j];
-    }
-  }
-  __syncthreads();
-  // T_IJ = -T_II sum_K A_IK T_KJ, one wave per block column
-  if (w < NB - 1) {
-    f32x4 t[NB];
-    t[0] = col4(s.tm + (16 * w + 4 * g4) * AS + 16 * w + n16, AS);
-    for (int I = w + 1; I < NB; ++I) {
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int d = 0; d < NB - 1; ++d)
-        if (w + d < I) acc = mfma4(lds4(s.am + (16 * I + n16) * AS + 16 * (w + d) + 4 * g4), t[d], acc);
-      acc = mfma4(lds4(s.tm + (16 * I + n16) * AS + 16 * I + 4 * g4), -acc, zero4());
-#pragma unroll
-      for (int d = 1; d < NB; ++d)
-        if (w + d == I) t[d] = acc;
-      float* dst = s.tm + (16 * I + 4 * g4) * AS + 16 * w + n16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i * AS] = acc[i];
-      const float top = wave_max(max4(acc));
-      if (lane == 0) atomicMax(&s.ttop, __float_as_uint(top));
-    }
-  }
-  __syncthreads();
-
-  // ---- T, T^T and P^T as operands, over km and kb
-  TPlanes& tp = *reinterpret_cast<TPlanes*>(smem_raw);
-  const Scale st = scale_for(__uint_as_float(s.ttop)), sp = scale_for(__uint_as_float(s.ptop));
-  for (int task = w; task < 30; task += kThreads / 64) {
-    const int kind = task / 10;  // T, T^T, P^T
-    int I = 0, J = task % 10;
-    while (J > I) J -= ++I;
-    const float* src = kind == 2 ? s.pm : s.tm;
-    const f32x4 x = kind == 0 ? lds4(src + (16 * I + n16) * AS + 16 * J + 4 * g4)
-                              : col4(src + (16 * I + 4 * g4) * AS + 16 * J + n16, AS);
-    uint16_t(*dst)[C * PS] = kind == 0 ? tp.t : kind == 1 ? tp.tt : tp.pt;
-    const int row = 16 * (kind == 0 ? I : J) + n16;
-    const int other = 16 * (kind == 0 ? J : I) + 4 * g4;
-    u32x2 hi, lo;
-    split4h(x * (kind == 2 ? sp.up : st.up), hi, lo);
-    *reinterpret_cast<u32x2*>(dst[0] + row * PS + perm32(other)) = hi;
-    *reinterpret_cast<u32x2*>(dst[1] + row * PS + perm32(other)) = lo;
-    if (I == J) {  // the pair's other block: right of T's even ones, left of the odd transposed
-      const bool empty = kind == 0 ? !(I & 1) : (I & 1);
-      if (empty) {
-        const int at = row * PS + perm32(other ^ 16);
-        *reinterpret_cast<u32x2*>(dst[0] + at) = u32x2{0u, 0u};
-        *reinterpret_cast<u32x2*>(dst[1] + at) = u32x2{0u, 0u};
-      }
-    }
-  }
-  __syncthreads();
-
-  // ---- products with T for the wave's 16 channels
-  const uint16_t* vo = reinterpret_cast<const uint16_t*>(s.qm);
-  f16x8 vf[2], of[2];  // V and dO: 8 bits, so their high parts are exact
+  // V and dO as fragments of the wave's 16 value channels: 8 bits, so their high parts are
+  // exact
+  f16x8 vf[2], of[2];
   float unv, uno;
   {
     u32x4 vb[2], ob[2];
@@ -306,9 +290,9 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = (32 * t + 16 * (i >> 1) + 4 * g4 + 2 * (i & 1)) * VS + kc;
-        vb[t][i] = uint32_t(vo[at]) | uint32_t(vo[at + VS]) << 16;
-        ob[t][i] = uint32_t(vo[at + RS]) | uint32_t(vo[at + VS + RS]) << 16;
+        const int at = (32 * t + 16 * (i >> 1) + 4 * g4 + 2 * (i & 1)) * D + kc;
+        vb[t][i] = uint32_t(s.b.v[at]) | uint32_t(s.b.v[at + D]) << 16;
+        ob[t][i] = uint32_t(s.b.o[at]) | uint32_t(s.b.o[at + D]) << 16;
       }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -316,10 +300,71 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
     bf16_fragments(vb, vf, unv);
     bf16_fragments(ob, of, uno);
   }
+  __syncthreads();
+  // T_IJ = -T_II sum_K A_IK T_KJ, one wave per block column
+  if (w < NB - 1) {
+    f32x4 t[NB];
+    t[0] = col4(s.b.tm[block_index(w, w)] + 4 * g4 * GS + n16, GS);
+    for (int I = w + 1; I < NB; ++I) {
+      f32x4 x = zero4();
+#pragma unroll
+      for (int d = 0; d < NB - 1; ++d)
+        if (w + d < I) x = mfma4(lds4(s.b.am[block_index(I, w + d)] + n16 * GS + 4 * g4), t[d], x);
+      x = mfma4(lds4(s.b.tm[block_index(I, I)] + n16 * GS + 4 * g4), -x, zero4());
+#pragma unroll
+      for (int d = 1; d < NB; ++d)
+        if (w + d == I) t[d] = x;
+      float* dst = s.b.tm[block_index(I, w)] + 4 * g4 * GS + n16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i * GS] = x[i];
+      const float top = wave_max(max4(x));
+      if (lane == 0) atomicMax(&s.ttop, __float_as_uint(top));
+    }
+  }
+  __syncthreads();
+
+  // left fragments of e^G k and e^(Gl-G) k, as this lane has stored them
+  f16x8 kgh[2], kgl[2], keh[2], kel[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const uint8_t* at = ops + ((w * 2 + t) * 2 * 64 + lane) * 16;
+    kgh[t] = *reinterpret_cast<const f16x8*>(at + kOpKG);
+    kgl[t] = *reinterpret_cast<const f16x8*>(at + kOpKG + 1024);
+    keh[t] = *reinterpret_cast<const f16x8*>(at + kOpKE);
+    kel[t] = *reinterpret_cast<const f16x8*>(at + kOpKE + 1024);
+  }
+
+  // ---- T, T^T (with beta of the token that writes) and P^T as operands, over A, V and dO
+  const float ttop = __uint_as_float(s.ttop);
+  const Scale st = scale_for(ttop), sp = scale_for(__uint_as_float(s.ptop));
+  const Scale stt = scale_for(ttop * wave_max(fabsf(s.beta[lane])));
+  for (int task = w; task < 3 * kBlocks; task += 8) {
+    const int kind = task / kBlocks;  // T, T^T, P^T
+    int I, J;
+    block_of(task % kBlocks, I, J);
+    const float* src = (kind == 2 ? s.b.pm : s.b.tm)[task % kBlocks];
+    f32x4 x = kind == 0 ? lds4(src + n16 * GS + 4 * g4) : col4(src + 4 * g4 * GS + n16, GS);
+    if (kind == 1) x *= lds4(s.beta + 16 * I + 4 * g4);
+    uint16_t(*dst)[C * PS] = kind == 0 ? s.b.t : kind == 1 ? s.b.tt : s.b.pt;
+    const int row = 16 * (kind == 0 ? I : J) + n16;
+    const int other = 16 * (kind == 0 ? J : I) + 4 * g4;
+    u32x2 hi, lo;
+    split4h(x * (kind == 0 ? st.up : kind == 1 ? stt.up : sp.up), hi, lo);
+    *reinterpret_cast<u32x2*>(dst[0] + row * PS + perm32(other)) = hi;
+    *reinterpret_cast<u32x2*>(dst[1] + row * PS + perm32(other)) = lo;
+    if (I == J && (kind == 0 ? !(I & 1) : (I & 1))) {  // nothing beside this one
+      const int at = row * PS + perm32(other ^ 16);
+      *reinterpret_cast<u32x2*>(dst[0] + at) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(dst[1] + at) = u32x2{0u, 0u};
+    }
+  }
+  __syncthreads();
+
+  // ---- products with T for the wave's 16 channels
   auto frag = [&](const uint16_t* plane, int r, int t) {
     return *reinterpret_cast<const f16x8*>(plane + (16 * r + n16) * PS + 32 * t + 8 * g4);
   };
-  f32x4 y[NB];  // P^T dO
+  f32x4 y[NB];  // P^T dO / (scale beta)
   f32x4 wt[NB], z[NB];
   float wtop = 0.f, ztop = 0.f;
   float* X = reinterpret_cast<float*>(ops + kOpX0);
@@ -331,15 +376,15 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (t <= r / 2) {
-        const f16x8 h = frag(tp.t[0], r, t), l = frag(tp.t[1], r, t);
+        const f16x8 h = frag(s.b.t[0], r, t), l = frag(s.b.t[1], r, t);
         wt[r] = mfma_split(kgh[t], kgl[t], h, l, wt[r]);  // transposed: rows are channels
         xx = mfma32(l, vf[t], xx);
         xx = mfma32(h, vf[t], xx);
       }
       if (t >= r / 2) {
-        z[r] = mfma_split(keh[t], kel[t], frag(tp.tt[0], r, t), frag(tp.tt[1], r, t), z[r]);
-        y[r] = mfma32(frag(tp.pt[1], r, t), of[t], y[r]);
-        y[r] = mfma32(frag(tp.pt[0], r, t), of[t], y[r]);
+        z[r] = mfma_split(keh[t], kel[t], frag(s.b.tt[0], r, t), frag(s.b.tt[1], r, t), z[r]);
+        y[r] = mfma32(frag(s.b.pt[1], r, t), of[t], y[r]);
+        y[r] = mfma32(frag(s.b.pt[0], r, t), of[t], y[r]);
       }
     }
     *reinterpret_cast<f32x4*>(X + ((w * NB + r) * 64 + lane) * 4) = xx * (unv * st.un);
@@ -366,13 +411,13 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
       yh[t] = join8(h0, h1);
       yl[t] = join8(l0, l1);
     }
-    const float un = (sp.un * uno) * (st.un * sy.un);
+    const float un = (sp.un * uno) * (stt.un * sy.un) * p.scale;
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
       f32x4 d = zero4();
 #pragma unroll
       for (int t = r / 2; t < 2; ++t)
-        d = mfma_split(frag(tp.tt[0], r, t), frag(tp.tt[1], r, t), yh[t], yl[t], d);
+        d = mfma_split(frag(s.b.tt[0], r, t), frag(s.b.tt[1], r, t), yh[t], yl[t], d);
       *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d * un;
     }
   }
@@ -385,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(BwdParams p) {
   const Scale sw = scale_for(wtop), sz = scale_for(ztop);
   if (threadIdx.x == 0) {
     tail[kTailUnW] = sw.un * (st.un * kFixedUn);
-    tail[kTailUnZ] = sz.un * (st.un / kBetaUp);
+    tail[kTailUnZ] = sz.un * (stt.un * kFixedUn);
   }
 #pragma unroll
   for (int r = 0; r < NB; ++r) {
