@@ -304,8 +304,8 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * b + 4 * g4 + i;
       const bool valid = t < ch.c;
-      ln.k[b][i] = valid ? bf1(raw.k[b][i]) * rk4[i] : 0.f;
-      ln.q[b][i] = valid ? bf1(raw.q[b][i]) * rq4[i] : 0.f;
+      ln.k[b][i] = bf1(raw.k[b][i]) * rk4[i];  // missing tokens: rk, rq are zeros
+      ln.q[b][i] = bf1(raw.q[b][i]) * rq4[i];
       const float x = bf1(raw.g[b][i]);
       float g, s = 0.f;
       if (pre) {
@@ -321,7 +321,7 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
         if (SLOPE)
           s = gu >= p.lower_bound ? -ea * (far ? 1.f : e * __builtin_amdgcn_rcpf(1.0f + e)) : 0.f;
       }
-      a[i] = valid ? fexp(g) : 1.f;
+      a[i] = fexp(valid ? g : 0.f);
       if constexpr (SLOPE) {
         keep[(4 * b + i) * kThreads] = g;
         keep[(16 + 4 * b + i) * kThreads] = valid ? s : 0.f;

@@ -113,8 +113,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   const int kc = 16 * w + n16;
   const uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
 
-  // ---- everything is asked for at once: token tiles (a token's 128 values by 16
-  // lanes), rows of S and dS (a key's values by the four lanes that share it), q, k, g
+  // ---- token tiles: a token's 128 values by 16 lanes
   constexpr int NR = C / (kThreads / 16);
   const int c0 = (threadIdx.x & 15) * 8;
   const Rows orow = rows_of(p.dout, ch, p.dout_stride, int64_t(h) * D);
@@ -133,6 +132,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
     dv[j][1] = lds4(DV + 4);
   }
   token_scalars(p, ch, h, s.rq, s.rk, s.beta);
+  // rows of S and dS: a key's values by the four lanes that share it
   f32x4 Sv[8], dSv[8];
   {
     const float* S = reinterpret_cast<const float*>(ops + kOpS) + kc * D + 8 * g4;
