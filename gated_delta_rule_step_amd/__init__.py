@@ -370,20 +370,34 @@ def prefill_handoff_hist(cu_seqlens_host, ring_tail: int):
 def _same_device(first, named):
     """Every given tensor is on the first one's GPU; returns that device."""
     dev = first.device
+    at = first.get_device()
     for name, t in named:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
     return dev
+
+
+def _adr(t):
+    """A tensor's address for a void* argument (None: NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 def _launch(fn, dev, stream, *args):
     """Call a C entry point with `dev` current, on the given stream or on that
     device's current one (appended as the last argument)."""
     import torch
-    if stream is not None and getattr(stream, "device", dev) != dev:
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif getattr(stream, "device", dev) != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-    with torch.cuda.device(dev):
-        st = getattr(lib(), fn)(*args, _stream(stream))
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    call = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        st = call(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, raw)
     _check(fn, st)
 
 
@@ -453,20 +467,20 @@ def kda_prefill_varlen_backward(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, bet
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch("kda_prefill_varlen_backward", dev, stream,
-            n_docs, T, H, HEAD_DIM, HEAD_DIM, _P(cu_seqlens_host.data_ptr()), _ptr(cu_seqlens),
-            _ptr(q), q.stride(0), _ptr(k), k.stride(0), _ptr(v), v.stride(0),
-            _ptr(g_raw), g_raw.stride(0), _ptr(beta_raw), beta_raw.stride(0),
-            _ptr(A_log), _ptr(dt_bias), float(lower_bound), float(scale), int(gate_mode),
-            _state_dtype(state_pool), _ptr(state_pool) if N else _P(0), N, slot_stride,
-            _ptr(state_indices), 1 if use_initial_state else 0, _ptr(d_out), d_out.stride(0),
-            _ptr(d_final_state), _ptr(dq), dq.stride(0), _ptr(dk), dk.stride(0),
-            _ptr(dv), dv.stride(0), _ptr(dg), dg.stride(0), _ptr(dbeta), dbeta.stride(0),
-            _ptr(dA_log), _ptr(ddt_bias), _ptr(d_initial_state), _ptr(workspace), ws_bytes)
+            n_docs, T, H, HEAD_DIM, HEAD_DIM, cu_seqlens_host.data_ptr(), _adr(cu_seqlens),
+            _adr(q), q.stride(0), _adr(k), k.stride(0), _adr(v), v.stride(0),
+            _adr(g_raw), g_raw.stride(0), _adr(beta_raw), beta_raw.stride(0),
+            _adr(A_log), _adr(dt_bias), float(lower_bound), float(scale), int(gate_mode),
+            _state_dtype(state_pool), _adr(state_pool) if N else None, N, slot_stride,
+            _adr(state_indices), 1 if use_initial_state else 0, _adr(d_out), d_out.stride(0),
+            _adr(d_final_state), _adr(dq), dq.stride(0), _adr(dk), dk.stride(0),
+            _adr(dv), dv.stride(0), _adr(dg), dg.stride(0), _adr(dbeta), dbeta.stride(0),
+            _adr(dA_log), _adr(ddt_bias), _adr(d_initial_state), _adr(workspace), ws_bytes)
 
 
 def _vectors(name, t, rows, heads, width):
     """bf16 [rows, width] or [rows, heads, width] with contiguous rows: the row
-    stride (None for None)."""
+    stride (0 for None)."""
     if t is None:
         return 0
     _bf16(name, t, last_contig=False)
@@ -531,9 +545,9 @@ def kda_rmsnorm(x, weight, out, residual=None, residual_out=None, gate=None, sca
         raise ValueError("scales belong to an fp8 output")
     dev = _same_device(x, (("weight", weight), ("out", out), ("residual", residual),
                            ("residual_out", residual_out), ("gate", gate), ("scales", scales)))
-    _launch("kda_rmsnorm", dev, stream, rows, heads, width, _ptr(x), xs, _ptr(residual), rs,
-            _ptr(residual_out), ro, _ptr(gate), gs, _ptr(weight), float(eps), 1 if fp8 else 0,
-            _ptr(out), os_, group, _ptr(scales), ss)
+    _launch("kda_rmsnorm", dev, stream, rows, heads, width, _adr(x), xs, _adr(residual), rs,
+            _adr(residual_out), ro, _adr(gate), gs, _adr(weight), float(eps), 1 if fp8 else 0,
+            _adr(out), os_, group, _adr(scales), ss)
 
 
 def kda_rmsnorm_backward_workspace_size(rows: int, heads: int, width: int) -> int:
@@ -566,6 +580,6 @@ def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None,
         need = kda_rmsnorm_backward_workspace_size(rows, heads, width)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch("kda_rmsnorm_backward", dev, stream, rows, heads, width, _ptr(z), zs, _ptr(dy), ys,
-            _ptr(gate), gs, _ptr(d_residual), rs, _ptr(weight), float(eps), _ptr(dz), ds,
-            _ptr(dgate), dgs, _ptr(dweight), _ptr(workspace), ws_bytes)
+    _launch("kda_rmsnorm_backward", dev, stream, rows, heads, width, _adr(z), zs, _adr(dy), ys,
+            _adr(gate), gs, _adr(d_residual), rs, _adr(weight), float(eps), _adr(dz), ds,
+            _adr(dgate), dgs, _adr(dweight), _adr(workspace), ws_bytes)

@@ -91,6 +91,19 @@ __device__ __forceinline__ void store_ch8(uint8_t* row, int c, int width, u32x2 
   for (int i = 0; i < 7; ++i)
     if (c + i < width) row[c + i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
 }
+// 8 weights from c on, zeros past the width.
+__device__ __forceinline__ void load_w8(const float* w, int c, int width, float (&x)[8]) {
+  typedef f32x4 f32x4_u __attribute__((aligned(4)));
+  if (c + 8 <= width) {
+    const f32x4 a = *reinterpret_cast<const f32x4_u*>(w + c);
+    const f32x4 b = *reinterpret_cast<const f32x4_u*>(w + c + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = c + i < width ? w[c + i] : 0.f;
+}
 __device__ __forceinline__ u32x4 pack8(const float (&y)[8]) {
   return u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                pack_bf16x2(y[6], y[7])};
@@ -147,11 +160,7 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p
 
   float w[NV][8];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * LPR + lane) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[j][i] = c + i < p.width ? p.weight[c + i] : 0.f;
-  }
+  for (int j = 0; j < NV; ++j) load_w8(p.weight, (j * LPR + lane) * 8, p.width, w[j]);
 
   int turn = 0;
   for (int64_t v = int64_t(blockIdx.x) * VPB + threadIdx.x / LPR; v < p.vecs;
@@ -247,12 +256,9 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_bwd_kernel(NormBwdP
   float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * LPR + lane) * 8;
+    load_w8(p.weight, (j * LPR + lane) * 8, p.width, w[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[j][i] = c + i < p.width ? p.weight[c + i] : 0.f;
-      dw[j][i] = 0.f;
-    }
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
 
   int turn = 0;
@@ -370,18 +376,26 @@ __global__ __launch_bounds__(1024) void reduce_partials(const float* partial, in
 // ---------------------------------------------------------------------------
 // host
 
-// The lanes and groups of 8 that hold a vector of this width: the narrowest
-// shape that covers it.
-#define KDA_NORM_SHAPES(F)              \
-  if (width <= 128) return F(16, 1);    \
-  if (width <= 512) return F(64, 1);    \
-  if (width <= 1024) return F(64, 2);   \
-  if (width <= 2048) return F(256, 1);  \
-  if (width <= 4096) return F(256, 2);  \
-  if (width <= 8192) return F(256, 4);  \
+// The lanes and groups of 8 that hold a vector: the narrowest shape that covers its
+// width, or, where there are too few vectors to fill the chip (below four per CU), the one
+// with the most lanes, so that a vector's loads are all in flight at once.
+constexpr int64_t kFewVecs = 1024;
+#define KDA_NORM_SHAPES(F)                      \
+  if (width <= 128) return F(16, 1);            \
+  if (width <= 512) return F(64, 1);            \
+  if (vecs <= kFewVecs) {                       \
+    if (width <= 2048) return F(256, 1);        \
+    if (width <= 4096) return F(512, 1);        \
+    if (width <= 8192) return F(1024, 1);       \
+    return F(1024, 2);                          \
+  }                                             \
+  if (width <= 1024) return F(64, 2);           \
+  if (width <= 2048) return F(256, 1);          \
+  if (width <= 4096) return F(256, 2);          \
+  if (width <= 8192) return F(256, 4);          \
   return F(512, 4)
 
-int vecs_per_block(int width) {
+int vecs_per_block(int64_t vecs, int width) {
 #define KDA_NORM_VPB(L, N) kNormThreads<L> / L
   KDA_NORM_SHAPES(KDA_NORM_VPB);
 #undef KDA_NORM_VPB
@@ -390,7 +404,7 @@ int vecs_per_block(int width) {
 // Workgroups: every vector at once up to `most`, which fills the chip's
 // registers; above it they walk.
 unsigned norm_blocks(int64_t vecs, int width, int64_t most) {
-  const int64_t vpb = vecs_per_block(width);
+  const int64_t vpb = vecs_per_block(vecs, width);
   const int64_t b = (vecs + vpb - 1) / vpb;
   return unsigned(b < most ? b : most);
 }
@@ -423,6 +437,7 @@ hipError_t launch_norm2(const NormParams& p, int out, hipStream_t stream) {
 }
 hipError_t launch_norm(const NormParams& p, int out, hipStream_t stream) {
   const int width = p.width;
+  const int64_t vecs = p.vecs;
 #define KDA_NORM_GO(L, N) launch_norm2<L, N>(p, out, stream)
   KDA_NORM_SHAPES(KDA_NORM_GO);
 #undef KDA_NORM_GO
@@ -443,6 +458,7 @@ hipError_t launch_norm_bwd2(const NormBwdParams& p, hipStream_t stream) {
 }
 hipError_t launch_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   const int width = p.width;
+  const int64_t vecs = p.vecs;
 #define KDA_NORM_GO(L, N) launch_norm_bwd2<L, N>(p, stream)
   KDA_NORM_SHAPES(KDA_NORM_GO);
 #undef KDA_NORM_GO
