@@ -108,11 +108,17 @@ __device__ __forceinline__ u32x4 pack8(const float (&y)[8]) {
   return u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                pack_bf16x2(y[6], y[7])};
 }
-// Saturating fp8 e4m3; a NaN stays one (the clamp would turn it into -448).
-__device__ __forceinline__ float sat8(float x) { return x != x ? x : f8_sat(x); }
-__device__ __forceinline__ uint32_t pack8_fp8x4(float a, float b, float c, float d) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(sat8(a), sat8(b), 0, false);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(sat8(c), sat8(d), r, true));
+// Four values scaled so that the largest of their group is 448: within the format up to a
+// rounding of fp32, which the conversion rounds away, so nothing needs to be clamped and a
+// NaN stays one.
+__device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
+  const int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true));
+}
+// With the hardware reciprocal (1 ulp): the per-head norm is bound by vector instructions
+// as much as by HBM, and a division takes ten of them.
+__device__ __forceinline__ float sigmoid_rcp(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + fexp(-x));
 }
 
 __device__ __forceinline__ float row16_max(float x) {
@@ -193,7 +199,7 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p
       for (int i = 0; i < 8; ++i) ss = fmaf(z[j][i], z[j][i], ss);
     }
     ss = reduce<LPR, false>(ss, buf[turn]);
-    const float s = 1.0f / sqrtf(fmaf(ss, inv_n, p.eps));
+    const float s = __builtin_amdgcn_rsqf(fmaf(ss, inv_n, p.eps));
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -202,7 +208,7 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float y = z[j][i] * s * w[j][i];
-        if constexpr (GATE) y *= fsigmoid(t[i]);
+        if constexpr (GATE) y *= sigmoid_rcp(t[i]);
         z[j][i] = y;
         if constexpr (OUT == kOutFp8) top = fmaxf(top, fabsf(y));
       }
@@ -233,8 +239,8 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p
           sc[p.heads == 1 ? 0 : v - r * p.heads] = scale;
         }
         store_ch8(out, c, p.width,
-                  u32x2{pack8_fp8x4(z[j][0] * mul, z[j][1] * mul, z[j][2] * mul, z[j][3] * mul),
-                        pack8_fp8x4(z[j][4] * mul, z[j][5] * mul, z[j][6] * mul, z[j][7] * mul)});
+                  u32x2{pack_fp8(z[j][0] * mul, z[j][1] * mul, z[j][2] * mul, z[j][3] * mul),
+                        pack_fp8(z[j][4] * mul, z[j][5] * mul, z[j][6] * mul, z[j][7] * mul)});
       }
     }
   }
@@ -284,14 +290,14 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_bwd_kernel(NormBwdP
       if constexpr (GATE) unpack8_bf16(gw[j], g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (GATE) a[i] *= fsigmoid(g[i]);
+        if constexpr (GATE) a[i] *= sigmoid_rcp(g[i]);
         ss = fmaf(z[i], z[i], ss);
         sa = fmaf(a[i] * w[j][i], z[i], sa);
       }
     }
     ss = reduce<LPR, false>(ss, buf[turn]);
     sa = reduce<LPR, false>(sa, buf[2 + turn]);
-    const float s = 1.0f / sqrtf(fmaf(ss, inv_n, p.eps));
+    const float s = __builtin_amdgcn_rsqf(fmaf(ss, inv_n, p.eps));
     const float m = sa * s * s * inv_n;  // mean(a n) s, with n = z s
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -306,7 +312,7 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_bwd_kernel(NormBwdP
         const float n = z[i] * s;
         float d = y[i];
         if constexpr (GATE) {
-          const float sig = fsigmoid(g[i]);
+          const float sig = sigmoid_rcp(g[i]);
           d *= sig;
           g[i] = d * (1.0f - sig) * n * w[j][i];
         }
