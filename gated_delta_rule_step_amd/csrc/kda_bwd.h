@@ -286,15 +286,15 @@ struct Lane {
   float up[NB][4];
   float head[NB], tail[NB];
 };
-// With SLOPE, `keep` takes each token's log-decay and its derivative by the gate input:
-// 2 x 16 floats per thread, kThreads apart.
-template <bool SLOPE>
+// PRE: the gate input is the log-decay itself (KDA_GATE_PRECOMPUTED). With SLOPE, `keep`
+// takes each token's log-decay and its derivative by the gate input: 2 x 16 floats per
+// thread, kThreads apart.
+template <bool PRE, bool SLOPE>
 __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, int h, int kc,
                                           int g4, const RawLane& raw, const float* rq,
                                           const float* rk, Lane& ln, float* keep) {
-  const bool pre = p.gate_mode & KDA_GATE_PRECOMPUTED;
-  const float ea = pre ? 0.f : expf(p.A_log[h]);
-  const float dtb = pre ? 0.f : p.dt_bias[gate_channel(p, h, kc)];
+  const float ea = PRE ? 0.f : expf(p.A_log[h]);
+  const float dtb = PRE ? 0.f : p.dt_bias[gate_channel(p, h, kc)];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     __builtin_amdgcn_sched_barrier(0);  // a block at a time: the raw values make room
@@ -302,24 +302,22 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
     float a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = 16 * b + 4 * g4 + i;
-      const bool valid = t < ch.c;
+      const bool valid = 16 * b + 4 * g4 + i < ch.c;
       ln.k[b][i] = bf1(raw.k[b][i]) * rk4[i];  // missing tokens: rk, rq are zeros
       ln.q[b][i] = bf1(raw.q[b][i]) * rq4[i];
       const float x = bf1(raw.g[b][i]);
       float g, s = 0.f;
-      if (pre) {
+      if constexpr (PRE) {
         g = gate_given(x, p.lower_bound);
         s = x >= p.lower_bound && x <= 0.f ? 1.f : 0.f;
       } else {
-        // softplus and sigmoid from one exponential (hardware exp2, log2, rcp)
+        // softplus and sigmoid from one exponential (hardware exp2, log2, rcp), which is
+        // kept finite: log(1 + e^y) is y long before
         const float y = x + dtb;
-        const float e = fexp(y);
-        const bool far = y > 20.f;
-        const float gu = -ea * (far ? y : LN2 * __builtin_amdgcn_logf(1.0f + e));
+        const float e = fexp(fminf(y, 80.f));
+        const float gu = -ea * fmaxf(y, LN2 * __builtin_amdgcn_logf(1.0f + e));
         g = fmaxf(gu, p.lower_bound);
-        if (SLOPE)
-          s = gu >= p.lower_bound ? -ea * (far ? 1.f : e * __builtin_amdgcn_rcpf(1.0f + e)) : 0.f;
+        if (SLOPE) s = gu >= p.lower_bound ? -ea * (e * __builtin_amdgcn_rcpf(1.0f + e)) : 0.f;
       }
       a[i] = fexp(valid ? g : 0.f);
       if constexpr (SLOPE) {
@@ -327,29 +325,22 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
         keep[(16 + 4 * b + i) * kThreads] = valid ? s : 0.f;
       }
     }
-    // A lane's four tokens, the lanes between them and the middle, and the other half.
-    const float all = (a[0] * a[1]) * (a[2] * a[3]);
+    // From the lane's first token on; then the lanes between it and the block's middle, and
+    // the block's other half.
+    const float a1 = a[0] * a[1], a2 = a1 * a[2], all = a2 * a[3];
     const float near = __shfl_xor(all, 16);
     const float half = all * near;
     const float other = __shfl_xor(half, 32);
     ln.head[b] = g4 < 2 ? half : other;
     ln.tail[b] = g4 < 2 ? other : half;
-    // upper half: from the middle to the token; lower: from behind it to the middle
+    // from the middle to the lane's first token: back over its own and the next lane's
+    // tokens (lanes 0; 1 only its own), or over the lane before (3; none for 2)
     const float base = g4 == 0 || g4 == 3 ? near : 1.f;
-    float w[4];
-    if (g4 < 2) {
-      w[3] = base;
-      w[2] = w[3] * a[3];
-      w[1] = w[2] * a[2];
-      w[0] = w[1] * a[1];
-    } else {
-      w[0] = base * a[0];
-      w[1] = w[0] * a[1];
-      w[2] = w[1] * a[2];
-      w[3] = w[2] * a[3];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ln.up[b][i] = g4 < 2 ? inverse(w[i]) : w[i];
+    const float from = g4 < 2 ? inverse(all * base) : base;
+    ln.up[b][0] = from * a[0];
+    ln.up[b][1] = from * a1;
+    ln.up[b][2] = from * a2;
+    ln.up[b][3] = from * all;
   }
 }
 

@@ -379,8 +379,9 @@ hipError_t launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t str
 
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
   // Two value tiles per workgroup where the chains alone would leave most CUs idle (12 chains
-  // of 8191 tokens: 500 us against 575 with four), else four (156 chains: 400 against 470).
-  return int64_t(p.n_docs) * p.H <= 32 ? launch_chain<2>(p, ord, stream)
+  // of 8191 tokens: 550 us against 620 with four; 80 chains: 3 % of the whole call), else four
+  // (168 chains: 5 % of the call).
+  return int64_t(p.n_docs) * p.H <= 96 ? launch_chain<2>(p, ord, stream)
                                        : launch_chain<4>(p, ord, stream);
 }
 

@@ -88,6 +88,7 @@ __device__ __forceinline__ float row16_sums(const float (&v)[4], int n16) {
   return t + dpp<0x128>(t);   // row_ror:8
 }
 
+template <bool PRE>
 __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   extern __shared__ __align__(16) float smem_raw[];
   GradSmem& s = *reinterpret_cast<GradSmem*>(smem_raw);
@@ -298,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   __syncthreads();
   Lane ln;
   float* keep = sr.keep + threadIdx.x;
-  make_lane<true>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, keep);
+  make_lane<PRE, true>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, keep);
   stage();
 
   // ---- between blocks: readers from the block's start, writers to its end. A pair two
@@ -593,15 +594,21 @@ __global__ __launch_bounds__(1024) void param_kernel(BwdParams p) {
 
 }  // namespace
 
-hipError_t launch_grads(const BwdParams& p, hipStream_t stream) {
+template <bool PRE>
+static hipError_t launch_grad(const BwdParams& p, hipStream_t stream) {
+  static_assert(sizeof(GradSmem) <= 160 * 1024, "LDS of a CU");
   static const hipError_t lds = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(grad_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+      reinterpret_cast<const void*>(grad_kernel<PRE>), hipFuncAttributeMaxDynamicSharedMemorySize,
       int(sizeof(GradSmem)));
   if (lds != hipSuccess) return lds;
-  static_assert(sizeof(GradSmem) <= 160 * 1024, "LDS of a CU");
-  hipLaunchKernelGGL(grad_kernel, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
+  hipLaunchKernelGGL(grad_kernel<PRE>, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
                      sizeof(GradSmem), stream, p);
   return hipGetLastError();
+}
+
+hipError_t launch_grads(const BwdParams& p, hipStream_t stream) {
+  return (p.gate_mode & KDA_GATE_PRECOMPUTED) ? launch_grad<true>(p, stream)
+                                              : launch_grad<false>(p, stream);
 }
 
 hipError_t launch_params(const BwdParams& p, hipStream_t stream) {

@@ -98,6 +98,7 @@ __device__ __forceinline__ void bf16_fragments(const u32x4 (&w)[2], f16x8 (&f)[2
   }
 }
 
+template <bool PRE>
 __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   extern __shared__ __align__(16) float smem_raw[];
   PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
@@ -121,7 +122,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 
   // ---- the decayed rows, and what depends on them channel by channel alone
   Lane ln;
-  make_lane<false>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, nullptr);
+  make_lane<PRE, false>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, nullptr);
   {
     float from[NB], to[NB];  // from the chunk's start to the block's middle, to its end
     float o = kFixedUp, e = kFixedUp;
@@ -447,14 +448,20 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 
 }  // namespace
 
-hipError_t launch_prep(const BwdParams& p, hipStream_t stream) {
+template <bool PRE>
+static hipError_t launch_prep(const BwdParams& p, hipStream_t stream) {
   static const hipError_t lds = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(prep_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+      reinterpret_cast<const void*>(prep_kernel<PRE>), hipFuncAttributeMaxDynamicSharedMemorySize,
       int(sizeof(PrepSmem)));
   if (lds != hipSuccess) return lds;
-  hipLaunchKernelGGL(prep_kernel, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
+  hipLaunchKernelGGL(prep_kernel<PRE>, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
                      sizeof(PrepSmem), stream, p);
   return hipGetLastError();
+}
+
+hipError_t launch_prep(const BwdParams& p, hipStream_t stream) {
+  return (p.gate_mode & KDA_GATE_PRECOMPUTED) ? launch_prep<true>(p, stream)
+                                              : launch_prep<false>(p, stream);
 }
 
 }  // namespace bwd
