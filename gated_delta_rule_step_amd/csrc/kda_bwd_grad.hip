@@ -27,7 +27,7 @@ constexpr int GS = 20;      // row (fp32) of the diagonal blocks
 constexpr int kRows = 48;   // DP, DA: readers 16..63; their transposes: writers 0..47
 
 struct GradSmem {
-  uint16_t oh[C * HS], vh[C * HS], vl[C * HS], xh[C * HS], xl[C * HS];
+  uint16_t oh[C * HS], vh[C * HS], vl[C * HS], xh[C * HS], xl[C * HS];  // perm32 order
   // off-diagonal blocks, zero elsewhere, columns in the order of the right fragments:
   // [hi, lo]
   uint16_t pr[2][kRows * PS], ar[2][kRows * PS];  // DP, DA: [reader - 16][writer]
@@ -46,32 +46,25 @@ struct RedSmem {
 };
 static_assert(sizeof(RedSmem) <= sizeof(uint16_t) * C * HS * 5, "the sums fit");
 
-// Column of token t in DP and DA: a right fragment holds, for lane group g, tokens
-// 4 g .. 4 g + 3 of a block and of the next one.
+// Position of contraction index t: a fragment holds, for lane group g, 4 g .. 4 g + 3 of
+// a run of 16 and of the next one.
 __device__ __forceinline__ int perm32(int t) {
-  return (t & 32) + 8 * ((t & 15) >> 2) + 4 * ((t >> 4) & 1) + (t & 3);
+  return (t & ~31) + 8 * ((t & 15) >> 2) + 4 * ((t >> 4) & 1) + (t & 3);
 }
 
 __device__ __forceinline__ void zero_row(uint16_t* p, int64_t t, int64_t stride, int64_t at, int n) {
   for (int e = threadIdx.x; e < n; e += kThreads) p[t * stride + at + e] = 0;
 }
 
-// 8 values to fp16 high and low parts, 16 bytes each.
-__device__ __forceinline__ void put8(uint16_t* hi, uint16_t* lo, f32x4 a, f32x4 b) {
-  u32x2 h0, l0, h1, l1;
-  split4h(a, h0, l0);
-  split4h(b, h1, l1);
-  *reinterpret_cast<u32x4*>(hi) = u32x4{h0[0], h0[1], h1[0], h1[1]};
-  *reinterpret_cast<u32x4*>(lo) = u32x4{l0[0], l0[1], l1[0], l1[1]};
+typedef u32x2 u32x2_u __attribute__((aligned(2)));
+__device__ __forceinline__ f32x4 widen4(u32x2 w) {
+  return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+}
+__device__ __forceinline__ float max4(f32x4 x) {
+  return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 }
 __device__ __forceinline__ f16x8 frag8(const uint16_t* p) {
   return *reinterpret_cast<const f16x8*>(p);
-}
-__device__ __forceinline__ float max8(f32x4 a, f32x4 b) {
-  float t = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) t = fmaxf(t, fmaxf(fabsf(a[i]), fabsf(b[i])));
-  return t;
 }
 // Keeps the compiler from moving work of one stage into another: it would fetch the
 // fragments of several stages at once and run out of registers.
@@ -114,36 +107,30 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   const int kc = 16 * w + n16;
   const uint8_t* ops = p.ops + (sigma * p.H + h) * int64_t(kOps);
 
-  // ---- token tiles: a token's 128 values by 16 lanes
-  constexpr int NR = C / (kThreads / 16);
-  const int c0 = (threadIdx.x & 15) * 8;
+  // ---- token tiles: a token's 128 values by 32 lanes
+  constexpr int NR = C / (kThreads / 32);
+  const int c0 = (threadIdx.x & 31) * 4;
   const Rows orow = rows_of(p.dout, ch, p.dout_stride, int64_t(h) * D);
   const Rows dvr = rows_of(p.dv, ch, p.dv_stride, int64_t(h) * D);
-  u32x4 ow[NR];
-  f32x4 xv[NR][2], dv[NR][2];
+  u32x2 ow[NR];
+  f32x4 xv[NR], dv[NR];
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
-    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
-    ow[j] = *reinterpret_cast<const u32x4_u*>(orow.at(min(t, ch.c - 1), c0));
-    const float* X = reinterpret_cast<const float*>(ops + kOpX) + t * D + c0;
-    const float* DV = reinterpret_cast<const float*>(ops + kOpDV) + t * D + c0;
-    xv[j][0] = lds4(X);
-    xv[j][1] = lds4(X + 4);
-    dv[j][0] = lds4(DV);
-    dv[j][1] = lds4(DV + 4);
+    const int t = (threadIdx.x >> 5) + j * (kThreads / 32);
+    ow[j] = *reinterpret_cast<const u32x2_u*>(orow.at(min(t, ch.c - 1), c0));
+    xv[j] = lds4(reinterpret_cast<const float*>(ops + kOpX) + t * D + c0);
+    dv[j] = lds4(reinterpret_cast<const float*>(ops + kOpDV) + t * D + c0);
   }
   token_scalars(p, ch, h, s.rq, s.rk, s.beta);
-  // rows of S and dS: a key's values by the four lanes that share it
+  // rows of S and dS: a key's values by the four lanes that share it, in perm32 order
   f32x4 Sv[8], dSv[8];
   {
-    const float* S = reinterpret_cast<const float*>(ops + kOpS) + kc * D + 8 * g4;
-    const float* dS = reinterpret_cast<const float*>(ops + kOpDS) + kc * D + 8 * g4;
+    const float* S = reinterpret_cast<const float*>(ops + kOpS) + kc * D + 4 * g4;
+    const float* dS = reinterpret_cast<const float*>(ops + kOpDS) + kc * D + 4 * g4;
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-      Sv[2 * kt] = lds4(S + 32 * kt);
-      Sv[2 * kt + 1] = lds4(S + 32 * kt + 4);
-      dSv[2 * kt] = lds4(dS + 32 * kt);
-      dSv[2 * kt + 1] = lds4(dS + 32 * kt + 4);
+    for (int m = 0; m < 8; ++m) {
+      Sv[m] = lds4(S + 16 * m);
+      dSv[m] = lds4(dS + 16 * m);
     }
   }
   const float eg = reinterpret_cast<const float*>(ops + kOpTail)[kc];
@@ -151,18 +138,14 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   float top[3] = {0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
-    const int t = (threadIdx.x >> 4) + j * (kThreads / 16);
-    if (t >= ch.c) ow[j] = u32x4{0u, 0u, 0u, 0u};
+    const int t = (threadIdx.x >> 5) + j * (kThreads / 32);
+    if (t >= ch.c) ow[j] = u32x2{0u, 0u};
     else
-      *reinterpret_cast<u32x4_u*>(dvr.at(t, c0)) =
-          u32x4{pack_bf16x2(dv[j][0][0], dv[j][0][1]), pack_bf16x2(dv[j][0][2], dv[j][0][3]),
-                pack_bf16x2(dv[j][1][0], dv[j][1][1]), pack_bf16x2(dv[j][1][2], dv[j][1][3])};
-    float o[8];
-    unpack8_bf16(ow[j], o);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top[0] = fmaxf(top[0], fabsf(o[i]));
-    top[1] = fmaxf(top[1], max8(dv[j][0], dv[j][1]));
-    top[2] = fmaxf(top[2], max8(xv[j][0], xv[j][1]));
+      *reinterpret_cast<u32x2_u*>(dvr.at(t, c0)) =
+          u32x2{pack_bf16x2(dv[j][0], dv[j][1]), pack_bf16x2(dv[j][2], dv[j][3])};
+    top[0] = fmaxf(top[0], max4(widen4(ow[j])));
+    top[1] = fmaxf(top[1], max4(dv[j]));
+    top[2] = fmaxf(top[2], max4(xv[j]));
   }
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
@@ -178,15 +161,16 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   const Scale so = scale_for(top[0]), sv = scale_for(top[1]), sx = scale_for(top[2]);
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
-    const int at = ((threadIdx.x >> 4) + j * (kThreads / 16)) * HS + c0;
-    float o[8];
-    unpack8_bf16(ow[j], o);
-    u32x4 oh;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) oh[i] = pack_f16x2(o[2 * i] * so.up, o[2 * i + 1] * so.up);
-    *reinterpret_cast<u32x4*>(s.oh + at) = oh;
-    put8(s.vh + at, s.vl + at, dv[j][0] * sv.up, dv[j][1] * sv.up);
-    put8(s.xh + at, s.xl + at, xv[j][0] * sx.up, xv[j][1] * sx.up);
+    const int at = ((threadIdx.x >> 5) + j * (kThreads / 32)) * HS + perm32(c0);
+    const f32x4 o = widen4(ow[j]) * so.up;
+    *reinterpret_cast<u32x2*>(s.oh + at) = u32x2{pack_f16x2(o[0], o[1]), pack_f16x2(o[2], o[3])};
+    u32x2 hi, lo;
+    split4h(dv[j] * sv.up, hi, lo);
+    *reinterpret_cast<u32x2*>(s.vh + at) = hi;
+    *reinterpret_cast<u32x2*>(s.vl + at) = lo;
+    split4h(xv[j] * sx.up, hi, lo);
+    *reinterpret_cast<u32x2*>(s.xh + at) = hi;
+    *reinterpret_cast<u32x2*>(s.xl + at) = lo;
   }
   // the blocks that a 32-token contraction takes along and that hold nothing
   for (int e = threadIdx.x; e < 2 * kRows * PS / 8; e += kThreads) {
