@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kda_backward.h"
 #include "kda_common.h"
 
@@ -64,12 +66,12 @@ struct DocOrder {
 //   O           [vt 8][t 2][lane]           value channel 16 vt + lane % 16, tokens as in KE
 // X0 and DV0 are accumulator tiles [vt 8][rt 4][lane][4 tokens], X and DV rows
 // [token][value], S and dS rows [key][value], all fp32.
-constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales of W and Z
-constexpr int kOpW = 1024;               // T e^G k, scaled
-constexpr int kOpKE = kOpW + 32768;      // e^(Gl-G) k, times 2^12
-constexpr int kOpZ = kOpKE + 32768;      // T^T (beta e^(Gl-G) k), scaled
-constexpr int kOpKG = kOpZ + 32768;      // e^G k, times 2^12
-constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat, times 2^12
+constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales (below)
+constexpr int kOpW = 1024;               // T e^G k
+constexpr int kOpKE = kOpW + 32768;      // e^(Gl-G) k
+constexpr int kOpZ = kOpKE + 32768;      // T^T (beta e^(Gl-G) k)
+constexpr int kOpKG = kOpZ + 32768;      // e^G k
+constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat
 constexpr int kOpX0 = kOpQG + 32768;     // T V
 constexpr int kOpDV0 = kOpX0 + 32768;    // T^T P^T dO
 constexpr int kOpO = kOpDV0 + 32768;     // dO (bf16)
@@ -78,7 +80,11 @@ constexpr int kOpDV = kOpX + 32768;      // dV
 constexpr int kOpS = kOpDV + 32768;      // S entering the chunk
 constexpr int kOpDS = kOpS + 65536;      // dS leaving it
 constexpr int kOps = kOpDS + 65536;
-constexpr int kTailBeta = D, kTailUnW = D + C, kTailUnZ = D + C + 1;  // in floats
+// In floats. A token block of each operand has a scale of its own, a power of two: decays
+// over a chunk span far more than fp16. What undoes it: of W and Z on the product's rows, of
+// KG (and QG) and KE on the right side's.
+constexpr int kTailBeta = D, kTailUnW = D + C, kTailUnZ = kTailUnW + NB,
+              kTailDnKG = kTailUnZ + NB, kTailDnKE = kTailDnKG + NB;
 
 __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {
 #pragma unroll
@@ -119,8 +125,32 @@ __device__ __forceinline__ Scale scale_for(float top) {
   e = e < 40 ? 40 : (e > 250 ? 250 : e);
   return {__uint_as_float(uint32_t(268 - e) << 23), __uint_as_float(uint32_t(e - 14) << 23)};
 }
+// The power of two that brings x into [1, 2), and its inverse.
+__device__ __forceinline__ Scale unit_scale(float x) {
+  int e = int(__float_as_uint(x) >> 23);
+  e = e < 40 ? 40 : (e > 214 ? 214 : e);
+  return {__uint_as_float(uint32_t(254 - e) << 23), __uint_as_float(uint32_t(e) << 23)};
+}
 constexpr float kFixedUp = 4096.0f, kFixedUn = 1.0f / 4096.0f;  // operands within +-1
 
+typedef __fp16 f16x4 __attribute__((__vector_size__(4 * sizeof(__fp16))));
+// The same over one block of 16: half `u` of the fragments.
+__device__ __forceinline__ f16x4 half8(f16x8 x, int u) {
+  const u32x4 w = __builtin_bit_cast(u32x4, x);
+  return __builtin_bit_cast(f16x4, u32x2{w[2 * u], w[2 * u + 1]});
+}
+__device__ __forceinline__ f32x4 mfma_split16(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, int u) {
+  f32x4 c = zero4();
+  c = __builtin_amdgcn_mfma_f32_16x16x16f16(half8(al, u), half8(bh, u), c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x16f16(half8(ah, u), half8(bl, u), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x16f16(half8(ah, u), half8(bh, u), c, 0, 0, 0);
+}
+// With a right side that its high part holds exactly.
+__device__ __forceinline__ f32x4 mfma_high16(f16x8 ah, f16x8 al, f16x8 b, int u) {
+  f32x4 c = zero4();
+  c = __builtin_amdgcn_mfma_f32_16x16x16f16(half8(al, u), half8(b, u), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x16f16(half8(ah, u), half8(b, u), c, 0, 0, 0);
+}
 __device__ __forceinline__ f32x4 mfma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4 c) {
   c = mfma32(al, bh, c);
   c = mfma32(ah, bl, c);
@@ -131,6 +161,13 @@ __device__ __forceinline__ f32x4 mfma_split(f16x8 ah, f16x8 al, f16x8 bh, f16x8 
 __device__ __forceinline__ float column_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
+}
+
+__device__ __forceinline__ float row16_max(float x) {
+  x = fmaxf(x, dpp<0xB1>(x));
+  x = fmaxf(x, dpp<0x4E>(x));
+  x = fmaxf(x, dpp<0x141>(x));
+  return fmaxf(x, dpp<0x140>(x));
 }
 
 // Sum over the four 16-lane rows of a wave (lanes of equal lane % 16).
@@ -342,6 +379,21 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
     ln.up[b][2] = from * a2;
     ln.up[b][3] = from * all;
   }
+}
+
+// Dynamic LDS beyond 64 KiB is allowed once per kernel and device, before its first launch
+// there. The device's entry in `done` is only ever set, so calls from several threads at
+// worst allow it twice.
+constexpr int kMaxDevices = 64;
+inline hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<bool> (&done)[kMaxDevices]) {
+  int dev = -1;
+  if (const hipError_t e = hipGetDevice(&dev)) return e;
+  if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_relaxed)) return hipSuccess;
+  const hipError_t e =
+      hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == hipSuccess) done[dev].store(true, std::memory_order_relaxed);
+  return e;
 }
 
 hipError_t launch_prep(const BwdParams& p, hipStream_t stream);

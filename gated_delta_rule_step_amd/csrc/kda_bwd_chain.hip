@@ -167,10 +167,11 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
   };
   // x = x0 + un * (what `product` left), rows written: the two waves of a tile add up their
   // parts (x0 and the rows are shared between them, a part of the blocks each).
-  auto exchange_out = [&](f32x4 (&x)[NB], const f32x4 (&acc)[NB], float un, const f32x4 (&x0)[NX]) {
+  auto exchange_out = [&](f32x4 (&x)[NB], const f32x4 (&acc)[NB], float un, f32x4 unr,
+                          const f32x4 (&x0)[NX]) {
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
-      x[r] = acc[r] * un;
+      x[r] = acc[r] * (un * unr[r]);
       if (r / NX == kh) x[r] += x0[r % NX];
       *reinterpret_cast<f32x4*>(xch + ((wave * NB + r) * 64 + lane) * 4) = x[r];
     }
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
         b.set(s);
         product(b, acc, after + kOpW);
         store_state(reinterpret_cast<float*>(ops + kOpS));
-        exchange_out(x, acc, -b.un * tail[kTailUnW], x0);
+        exchange_out(x, acc, -b.un, lds4(tail + kTailUnW), x0);
       }
       if (more) sb.store(lb);
       __syncthreads();
@@ -245,7 +246,8 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
       // ---- S = e^Gl S + KE^T (beta x)
       Right<NB> b;
 #pragma unroll
-      for (int r = 0; r < NB; ++r) x[r] *= lds4(tail + kTailBeta + 16 * r + 4 * g4);
+      for (int r = 0; r < NB; ++r)
+        x[r] *= lds4(tail + kTailBeta + 16 * r + 4 * g4) * tail[kTailDnKE + r];
       b.set(x);
       load_x0(x0, n + 1, kOpX0);
       const float un = b.un * kFixedUn;
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
         b.set(s);
         product(b, acc, after + kOpZ);
         store_state(reinterpret_cast<float*>(ops + kOpDS));
-        exchange_out(x, acc, b.un * tail[kTailUnZ], x0);
+        exchange_out(x, acc, b.un, lds4(tail + kTailUnZ), x0);
       }
       const bool more = n > 0 || p.d_initial;
       if (more) sb.store(lb);
@@ -314,6 +316,9 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
       if (!more) return;
       // ---- dS = e^Gl dS - KG^T dV + scale QG^T dO. dO has 8 bits: its high part is exact.
       Right<NB> b;
+      const f32x4 dn = lds4(tail + kTailDnKG);
+#pragma unroll
+      for (int r = 0; r < NB; ++r) x[r] *= dn[r];
       b.set(x);
       f16x8 o[2];
       float y[2][8], top = 0.f;
@@ -321,7 +326,10 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
       for (int t = 0; t < 2; ++t) {
         unpack8_bf16(ow[t], y[t]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[t][i]));
+        for (int i = 0; i < 8; ++i) {
+          y[t][i] *= dn[2 * t + i / 4];
+          top = fmaxf(top, fabsf(y[t][i]));
+        }
       }
       const Scale sc = scale_for(column_max(top));
 #pragma unroll
@@ -365,10 +373,9 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
 template <int TW>
 hipError_t launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
   using Shape = ChainShape<TW>;
-  static const hipError_t lds =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(chain_kernel<TW>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, Shape::kLds);
-  if (lds != hipSuccess) return lds;
+  static std::atomic<bool> allowed[kMaxDevices];
+  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(chain_kernel<TW>), Shape::kLds, allowed))
+    return e;
   const int64_t ids = (int64_t(p.n_docs) * p.H * 2 + 7) / 8 * 8;  // both directions
   hipLaunchKernelGGL(chain_kernel<TW>, dim3(unsigned(ids * Shape::kParts)), dim3(Shape::kThreads),
                      Shape::kLds, stream, p, ord);

@@ -581,10 +581,9 @@ __global__ __launch_bounds__(1024) void param_kernel(BwdParams p) {
 template <bool PRE>
 static hipError_t launch_grad(const BwdParams& p, hipStream_t stream) {
   static_assert(sizeof(GradSmem) <= 160 * 1024, "LDS of a CU");
-  static const hipError_t lds = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(grad_kernel<PRE>), hipFuncAttributeMaxDynamicSharedMemorySize,
-      int(sizeof(GradSmem)));
-  if (lds != hipSuccess) return lds;
+  static std::atomic<bool> allowed[kMaxDevices];
+  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(grad_kernel<PRE>), sizeof(GradSmem), allowed))
+    return e;
   hipLaunchKernelGGL(grad_kernel<PRE>, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
                      sizeof(GradSmem), stream, p);
   return hipGetLastError();

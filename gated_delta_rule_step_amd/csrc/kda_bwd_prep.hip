@@ -30,8 +30,8 @@ struct Rows64 {
   float pair[NP * HC];  // factor of a block pair
 };
 // Then A, P and T, and T and P as operands: high and low parts, [row][the other index in
-// the order of a right fragment]; blocks that a 32-index contraction takes along and that
-// hold nothing are zeros.
+// the order of a right fragment]. T's blocks have a scale each and are contracted one at a
+// time; P's are taken in pairs, the second of which may hold nothing and be zeros.
 struct Blocks {
   float pm[kBlocks][16 * GS];  // P / (scale beta)
   float tm[kBlocks][16 * GS];  // T
@@ -54,9 +54,13 @@ struct PrepSmem {
   };
   alignas(16) float beta[C];
   alignas(16) float rq[C], rk[C];
-  float top[2][8];      // largest magnitudes of W and Z, per wave
-  uint32_t ttop, ptop;  // of T and P (as bits)
+  uint32_t top[4 * NB + 1 + kBlocks];  // largest magnitudes (as bits), see kTop...
 };
+// Of W's and Z's token blocks, of the decays from the chunk's start to a block and behind it
+// to the end, of P, of T's blocks (far ones are smaller by the decay between them, which may
+// exceed what fp16 spans).
+constexpr int kTopW = 0, kTopZ = NB, kTopPre = 2 * NB, kTopPost = 3 * NB, kTopP = 4 * NB,
+              kTopT = kTopP + 1;
 static_assert(sizeof(PrepSmem) <= 80 * 1024, "two workgroups per CU");
 
 // Position of index t among 32: a fragment holds, for lane group g, 4 g .. 4 g + 3 of a
@@ -116,7 +120,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   RawLane raw;
   load_lane(p, ch, h, kc, g4, raw);
   token_scalars(p, ch, h, s.rq, s.rk, s.beta);
-  if (threadIdx.x == 0) s.ttop = s.ptop = 0;
+  if (threadIdx.x < 4 * NB + 1 + kBlocks) s.top[threadIdx.x] = 0;
   __syncthreads();
   if (threadIdx.x < C) tail[kTailBeta + threadIdx.x] = s.beta[threadIdx.x];
 
@@ -124,45 +128,18 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   Lane ln;
   make_lane<PRE, false>(p, ch, h, kc, g4, raw, s.rq, s.rk, ln, nullptr);
   {
-    float from[NB], to[NB];  // from the chunk's start to the block's middle, to its end
-    float o = kFixedUp, e = kFixedUp;
+    float o = 1.f, e = 1.f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      from[b] = o * ln.head[b];
-      o *= ln.head[b] * ln.tail[b];
-    }
-#pragma unroll
-    for (int b = NB - 1; b >= 0; --b) {
-      to[b] = e * ln.tail[b];
-      e *= ln.head[b] * ln.tail[b];
-    }
-    if (g4 == 0) tail[kc] = o * kFixedUn;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      u32x2 gh[2], gl[2], eh[2], el[2], qh[2], ql[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int b = 2 * t + u;
-        f32x4 qg, kg, ke;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float uf = ln.up[b][i] * from[b];
-          kg[i] = ln.k[b][i] * uf;
-          qg[i] = ln.q[b][i] * uf;
-          ke[i] = ln.k[b][i] * (inverse(ln.up[b][i]) * to[b]);
-        }
-        split4h(kg, gh[u], gl[u]);
-        split4h(ke, eh[u], el[u]);
-        split4h(qg, qh[u], ql[u]);
+      const float pre = row16_max(o), post = row16_max(e);
+      if (lane == 0) {
+        atomicMax(&s.top[kTopPre + b], __float_as_uint(pre));
+        atomicMax(&s.top[kTopPost + NB - 1 - b], __float_as_uint(post));
       }
-      uint8_t* at = ops + ((w * 2 + t) * 2 * 64 + lane) * 16;
-      *reinterpret_cast<f16x8*>(at + kOpKE) = join8(eh[0], eh[1]);
-      *reinterpret_cast<f16x8*>(at + kOpKE + 1024) = join8(el[0], el[1]);
-      *reinterpret_cast<f16x8*>(at + kOpKG) = join8(gh[0], gh[1]);
-      *reinterpret_cast<f16x8*>(at + kOpKG + 1024) = join8(gl[0], gl[1]);
-      *reinterpret_cast<f16x8*>(at + kOpQG) = join8(qh[0], qh[1]);
-      *reinterpret_cast<f16x8*>(at + kOpQG + 1024) = join8(ql[0], ql[1]);
+      o *= ln.head[b] * ln.tail[b];
+      e *= ln.head[NB - 1 - b] * ln.tail[NB - 1 - b];
     }
+    if (g4 == 0) tail[kc] = o;
   }
 
   // ---- A and P, block by block (10 each on and below the diagonal), half the channels
@@ -198,6 +175,57 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         }
     }
     __syncthreads();
+    // the chains' operands; the decays' maxima are in by now
+    if (half == 0) {
+      float from[NB], to[NB];  // from the chunk's start to the block's middle, to its end
+      float o = kFixedUp, e = kFixedUp;
+      Scale su[NB], sd[NB];
+  #pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        su[b] = unit_scale(__uint_as_float(s.top[kTopPre + b]));
+        sd[b] = unit_scale(__uint_as_float(s.top[kTopPost + b]));
+        if (threadIdx.x == 0) {
+          tail[kTailDnKG + b] = su[b].un;
+          tail[kTailDnKE + b] = sd[b].un;
+        }
+      }
+  #pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        from[b] = o * ln.head[b] * su[b].up;
+        o *= ln.head[b] * ln.tail[b];
+      }
+  #pragma unroll
+      for (int b = NB - 1; b >= 0; --b) {
+        to[b] = e * ln.tail[b] * sd[b].up;
+        e *= ln.head[b] * ln.tail[b];
+      }
+  #pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        u32x2 gh[2], gl[2], eh[2], el[2], qh[2], ql[2];
+  #pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int b = 2 * t + u;
+          f32x4 qg, kg, ke;
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float uf = ln.up[b][i] * from[b];
+            kg[i] = ln.k[b][i] * uf;
+            qg[i] = ln.q[b][i] * uf;
+            ke[i] = ln.k[b][i] * (inverse(ln.up[b][i]) * to[b]);
+          }
+          split4h(kg, gh[u], gl[u]);
+          split4h(ke, eh[u], el[u]);
+          split4h(qg, qh[u], ql[u]);
+        }
+        uint8_t* at = ops + ((w * 2 + t) * 2 * 64 + lane) * 16;
+        *reinterpret_cast<f16x8*>(at + kOpKE) = join8(eh[0], eh[1]);
+        *reinterpret_cast<f16x8*>(at + kOpKE + 1024) = join8(el[0], el[1]);
+        *reinterpret_cast<f16x8*>(at + kOpKG) = join8(gh[0], gh[1]);
+        *reinterpret_cast<f16x8*>(at + kOpKG + 1024) = join8(gl[0], gl[1]);
+        *reinterpret_cast<f16x8*>(at + kOpQG) = join8(qh[0], qh[1]);
+        *reinterpret_cast<f16x8*>(at + kOpQG + 1024) = join8(ql[0], ql[1]);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < kRounds; ++n) {
       const int task = w + 8 * n;
@@ -244,7 +272,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
     }
     if (is_p) {
       const float top = wave_max(max4(acc[n]));
-      if (lane == 0) atomicMax(&s.ptop, __float_as_uint(top));
+      if (lane == 0) atomicMax(&s.top[kTopP], __float_as_uint(top));
     }
   }
 #pragma unroll
@@ -279,7 +307,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) dst[i * GS] = r[i];
     const float top = wave_max(max4(r));
-    if (lane == 0) atomicMax(&s.ttop, __float_as_uint(top));
+    if (lane == 0) s.top[kTopT + block_index(w, w)] = __float_as_uint(top);
   }
   // V and dO as fragments of the wave's 16 value channels: 8 bits, so their high parts are
   // exact
@@ -319,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) dst[i * GS] = x[i];
       const float top = wave_max(max4(x));
-      if (lane == 0) atomicMax(&s.ttop, __float_as_uint(top));
+      if (lane == 0) s.top[kTopT + block_index(I, w)] = __float_as_uint(top);
     }
   }
   __syncthreads();
@@ -336,9 +364,9 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   }
 
   // ---- T, T^T (with beta of the token that writes) and P^T as operands, over A, V and dO
-  const float ttop = __uint_as_float(s.ttop);
-  const Scale st = scale_for(ttop), sp = scale_for(__uint_as_float(s.ptop));
-  const Scale stt = scale_for(ttop * wave_max(fabsf(s.beta[lane])));
+  const float btop = wave_max(fabsf(s.beta[lane]));
+  const Scale sp = scale_for(__uint_as_float(s.top[kTopP]));
+  auto t_scale = [&](int n, float f) { return scale_for(__uint_as_float(s.top[kTopT + n]) * f); };
   for (int task = w; task < 3 * kBlocks; task += 8) {
     const int kind = task / kBlocks;  // T, T^T, P^T
     int I, J;
@@ -350,10 +378,10 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
     const int row = 16 * (kind == 0 ? I : J) + n16;
     const int other = 16 * (kind == 0 ? J : I) + 4 * g4;
     u32x2 hi, lo;
-    split4h(x * (kind == 0 ? st.up : kind == 1 ? stt.up : sp.up), hi, lo);
+    split4h(x * (kind == 2 ? sp.up : t_scale(task % kBlocks, kind == 0 ? 1.f : btop).up), hi, lo);
     *reinterpret_cast<u32x2*>(dst[0] + row * PS + perm32(other)) = hi;
     *reinterpret_cast<u32x2*>(dst[1] + row * PS + perm32(other)) = lo;
-    if (I == J && (kind == 0 ? !(I & 1) : (I & 1))) {  // nothing beside this one
+    if (kind == 2 && I == J && (I & 1)) {  // nothing beside this one
       const int at = row * PS + perm32(other ^ 16);
       *reinterpret_cast<u32x2*>(dst[0] + at) = u32x2{0u, 0u};
       *reinterpret_cast<u32x2*>(dst[1] + at) = u32x2{0u, 0u};
@@ -367,7 +395,12 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   };
   f32x4 y[NB];  // P^T dO / (scale beta)
   f32x4 wt[NB], z[NB];
-  float wtop = 0.f, ztop = 0.f;
+  float tail_dn[2 * NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    tail_dn[b] = unit_scale(__uint_as_float(s.top[kTopPre + b])).un;
+    tail_dn[NB + b] = unit_scale(__uint_as_float(s.top[kTopPost + b])).un;
+  }
   float* X = reinterpret_cast<float*>(ops + kOpX0);
   float* DV = reinterpret_cast<float*>(ops + kOpDV0);
 #pragma unroll
@@ -378,25 +411,32 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
     for (int t = 0; t < 2; ++t) {
       if (t <= r / 2) {
         const f16x8 h = frag(s.b.t[0], r, t), l = frag(s.b.t[1], r, t);
-        wt[r] = mfma_split(kgh[t], kgl[t], h, l, wt[r]);  // transposed: rows are channels
-        xx = mfma32(l, vf[t], xx);
-        xx = mfma32(h, vf[t], xx);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)  // transposed: rows are channels
+          if (2 * t + u <= r)
+          {
+            const float un = t_scale(block_index(r, 2 * t + u), 1.f).un;
+            wt[r] += mfma_split16(kgh[t], kgl[t], h, l, u) * (un * tail_dn[2 * t + u]);
+            xx += mfma_high16(h, l, vf[t], u) * (un * unv);
+          }
       }
       if (t >= r / 2) {
-        z[r] = mfma_split(keh[t], kel[t], frag(s.b.tt[0], r, t), frag(s.b.tt[1], r, t), z[r]);
+        const f16x8 h = frag(s.b.tt[0], r, t), l = frag(s.b.tt[1], r, t);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (2 * t + u >= r)
+            z[r] += mfma_split16(keh[t], kel[t], h, l, u) *
+                    (t_scale(block_index(2 * t + u, r), btop).un * tail_dn[NB + 2 * t + u]);
         y[r] = mfma32(frag(s.b.pt[1], r, t), of[t], y[r]);
         y[r] = mfma32(frag(s.b.pt[0], r, t), of[t], y[r]);
       }
     }
-    *reinterpret_cast<f32x4*>(X + ((w * NB + r) * 64 + lane) * 4) = xx * (unv * st.un);
-    wtop = fmaxf(wtop, max4(wt[r]));
-    ztop = fmaxf(ztop, max4(z[r]));
-  }
-  wtop = wave_max(wtop);
-  ztop = wave_max(ztop);
-  if (lane == 0) {
-    s.top[0][w] = wtop;
-    s.top[1][w] = ztop;
+    *reinterpret_cast<f32x4*>(X + ((w * NB + r) * 64 + lane) * 4) = xx;
+    const float wtop = wave_max(max4(wt[r])), ztop = wave_max(max4(z[r]));
+    if (lane == 0) {
+      atomicMax(&s.top[kTopW + r], __float_as_uint(wtop));
+      atomicMax(&s.top[kTopZ + r], __float_as_uint(ztop));
+    }
   }
   {
     float top = 0.f;
@@ -412,29 +452,31 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
       yh[t] = join8(h0, h1);
       yl[t] = join8(l0, l1);
     }
-    const float un = (sp.un * uno) * (stt.un * sy.un) * p.scale;
+    const float un = (sp.un * uno) * sy.un * p.scale;
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
       f32x4 d = zero4();
 #pragma unroll
-      for (int t = r / 2; t < 2; ++t)
-        d = mfma_split(frag(s.b.tt[0], r, t), frag(s.b.tt[1], r, t), yh[t], yl[t], d);
-      *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d * un;
+      for (int t = r / 2; t < 2; ++t) {
+        const f16x8 h = frag(s.b.tt[0], r, t), l = frag(s.b.tt[1], r, t);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (2 * t + u >= r)
+            d += mfma_split16(h, l, yh[t], yl[t], u) *
+                 (t_scale(block_index(2 * t + u, r), btop).un * un);
+      }
+      *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wtop = fmaxf(wtop, s.top[0][i]);
-    ztop = fmaxf(ztop, s.top[1][i]);
-  }
-  const Scale sw = scale_for(wtop), sz = scale_for(ztop);
-  if (threadIdx.x == 0) {
-    tail[kTailUnW] = sw.un * (st.un * kFixedUn);
-    tail[kTailUnZ] = sz.un * (stt.un * kFixedUn);
-  }
-#pragma unroll
   for (int r = 0; r < NB; ++r) {
+    const Scale sw = scale_for(__uint_as_float(s.top[kTopW + r]));
+    const Scale sz = scale_for(__uint_as_float(s.top[kTopZ + r]));
+    if (threadIdx.x == 0) {
+      tail[kTailUnW + r] = sw.un * kFixedUn;
+      tail[kTailUnZ + r] = sz.un * kFixedUn;
+    }
     const int at = ((r * 4 + (w >> 1)) * 2 * 64 + lane) * 16 + 8 * (w & 1);
     u32x2 hi, lo;
     split4h(wt[r] * sw.up, hi, lo);
@@ -450,10 +492,9 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 
 template <bool PRE>
 static hipError_t launch_prep(const BwdParams& p, hipStream_t stream) {
-  static const hipError_t lds = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(prep_kernel<PRE>), hipFuncAttributeMaxDynamicSharedMemorySize,
-      int(sizeof(PrepSmem)));
-  if (lds != hipSuccess) return lds;
+  static std::atomic<bool> allowed[kMaxDevices];
+  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(prep_kernel<PRE>), sizeof(PrepSmem), allowed))
+    return e;
   hipLaunchKernelGGL(prep_kernel<PRE>, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
                      sizeof(PrepSmem), stream, p);
   return hipGetLastError();

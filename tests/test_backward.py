@@ -312,6 +312,39 @@ def test_degenerate_inputs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("do,v,state", [(1e-8, 1.0, 0.2), (1e4, 1e-3, 1e-6), (1e-3, 300.0, 50.0),
+                                        (1e20, 1e-20, 1e-20), (0.0, 1.0, 1.0)])
+def test_magnitudes(do, v, state):
+    """Loss scales and value sizes far from 1: the products' operands are scaled to fp16's
+    range, so the errors stay relative to the results. (The state gradient at the end has
+    the size of do.)"""
+    c = make((150, 20), H=2, seed=30, state=BF, dfinal=True)
+    for n, f in (("do", do), ("v", v)):
+        c[n] = (c[n].float() * f).to(BF)
+    c["pool"] = (c["pool"].float() * (state / 0.2)).to(BF)
+    c["df"] = c["df"] * do
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+def test_beta_as_given():
+    """Given betas need not lie in (0, 1): zero, negative and beyond 1 (up to 2 the
+    recurrence is stable; a few beyond grow it)."""
+    c = make((130,), H=2, gate=PRESIG | PRE, seed=31, state=BF, dfinal=True)
+    c["b"] = (c["b"].float() * 2.4 - 0.2).to(BF)
+    c["b"][40:44] = 3.0
+    c["b"][60:63] = -1.5
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.7, 25.0])
+def test_scale(scale):
+    c = make((70,), H=2, seed=32, scale=scale, dfinal=True)
+    compare(c, run(c))
+
+
+@pytest.mark.gpu
 def test_no_tokens():
     c = make((0, 0), H=2, seed=9, state=BF, dfinal=True)
     o = run(c)
@@ -439,6 +472,79 @@ def test_captured():
         for o in outs:
             for x, y in zip(o, eager):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_a_layer_forward_and_backward():
+    """The calls of a training step together: residual norm, prefill, gated norm per
+    head, and their gradients back to the residual stream; q, k and v are the normed stream
+    itself (as if the projections were the identity), so its gradient is the sum of three.
+    Each call is held to its formula in 64 bits on what it was given: a bound on the whole
+    would have to follow every bf16 value in between through the divisions of the norms.
+    A bf16 result is off by 2^-8 of each element and the fp32 arithmetic, so normwise by
+    at most 2^-8 + 2e-4."""
+    H, lens = 2, (75, 20)
+    T, W = sum(lens), H * D
+    c = make(lens, H=H, seed=40, scale=D ** -0.5)
+    g = torch.Generator().manual_seed(41)
+    x, r, og = (torch.randn(T, W, generator=g).to(BF) for _ in range(3))
+    dy, dr = (torch.randn(T, W, generator=g).to(BF) for _ in range(2))
+    w1, w2 = 1 + 0.1 * torch.randn(W, generator=g), 1 + 0.1 * torch.randn(D, generator=g)
+    cu = torch.tensor([0, 75, 95], dtype=torch.int32)
+    dev = {n: t.cuda() for n, t in dict(x=x, r=r, og=og, dy=dy, dr=dr, w1=w1, w2=w2, g=c["g"],
+                                       b=c["b"], A=c["A"], dt=c["dt"], cu=cu,
+                                       idx=c["idx"]).items()}
+    new = lambda *s: torch.empty(*s, dtype=BF, device="cuda")  # noqa: E731
+    z, u, o, y = new(T, W), new(T, W), new(T, W), new(T, H, D)
+    kda.kda_rmsnorm(dev["x"], dev["w1"], u, residual=dev["r"], residual_out=z)
+    pool = c["pool"].cuda()
+    kda.kda_prefill_varlen(cu, dev["cu"], u, u, u, dev["g"], dev["b"], dev["A"], dev["dt"], pool,
+                           dev["idx"], o, use_initial_state=False, scale=c["scale"])
+    kda.kda_rmsnorm(o.view(T, H, D), dev["w2"], y, gate=dev["og"].view(T, H, D))
+    do, dog, dw2 = new(T, H, D), new(T, H, D), torch.empty(D, device="cuda")
+    kda.kda_rmsnorm_backward(o.view(T, H, D), dev["w2"], dev["dy"].view(T, H, D), do, dw2,
+                             gate=dev["og"].view(T, H, D), dgate=dog)
+    dq, dk, dv, dg, db = new(T, W), new(T, W), new(T, W), new(T, W), new(T, H)
+    dA, ddt = torch.empty(H, device="cuda"), torch.empty(W, device="cuda")
+    kda.kda_prefill_varlen_backward(cu, dev["cu"], u, u, u, dev["g"], dev["b"], dev["A"],
+                                    dev["dt"], pool, dev["idx"], do.view(T, W), dq, dk, dv, dg,
+                                    db, dA_log=dA, ddt_bias=ddt, use_initial_state=False,
+                                    scale=c["scale"])
+    dz, dw1 = new(T, W), torch.empty(W, device="cuda")
+    kda.kda_rmsnorm_backward(z, dev["w1"], dq + dk + dv, dz, dw1, d_residual=dev["dr"])
+    torch.cuda.synchronize()
+
+    from tests.helpers import OUT_NORM_PREFILL
+
+    def far(got, ref):
+        return float((got.double().cpu().reshape(ref.shape) - ref).norm() / ref.norm())
+
+    def norm(z, w, gate=None):
+        n = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + 1e-6) * w
+        return n if gate is None else n * torch.sigmoid(gate)
+
+    def grads(out, dy, *leaves):
+        return torch.autograd.grad((out * dy).sum(), leaves)
+
+    bf = 2.0 ** -8 + 2e-4
+    back = {n: t.double().cpu() for n, t in dict(z=z, u=u, o=o, do=do).items()}
+    Z = x.double() + r.double()
+    assert torch.equal(z.cpu(), Z.to(BF)) and far(u, norm(Z, w1.double())) <= bf
+    zeros = torch.zeros(2, H, D, D, dtype=torch.float64)
+    O, _ = forward64(c, back["u"], back["u"], back["u"], *(c[n].double() for n in
+                                                           ("g", "b", "A", "dt")), zeros)
+    assert far(o, O) <= OUT_NORM_PREFILL
+    ol, wl, gl = (t.requires_grad_() for t in (back["o"].reshape(T, H, D), w2.double(),
+                                               og.double().reshape(T, H, D)))
+    Y = norm(ol, wl, gl)
+    assert far(y, Y.detach()) <= bf
+    for got, ref in zip((do, dw2, dog), grads(Y, dy.double().reshape(T, H, D), ol, wl, gl)):
+        assert far(got, ref) <= bf
+    step = dict(c, q=u.cpu(), k=u.cpu(), v=u.cpu(), do=do.cpu().view(T, W))
+    compare(step, dict(dq=dq, dk=dk, dv=dv, dg=dg, db=db, dA=dA, ddt=ddt, dS=None))
+    zl, wl = back["z"].requires_grad_(), w1.double().requires_grad_()
+    dZ, dW = grads(norm(zl, wl), (dq + dk + dv).double().cpu(), zl, wl)
+    assert far(dz, dZ + dr.double()) <= bf and far(dw1, dW) <= 1e-5
 
 
 @pytest.mark.gpu
