@@ -55,6 +55,7 @@ struct PrepSmem {
   alignas(16) float beta[C];
   alignas(16) float rq[C], rk[C];
   uint32_t top[4 * NB + 1 + kBlocks];  // largest magnitudes (as bits), see kTop...
+  float un[2][kBlocks];                // what undoes the scales of T's blocks, of beta T's
 };
 // Of W's and Z's token blocks, of the decays from the chunk's start to a block and behind it
 // to the end, of P, of T's blocks (far ones are smaller by the decay between them, which may
@@ -366,7 +367,6 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   // ---- T, T^T (with beta of the token that writes) and P^T as operands, over A, V and dO
   const float btop = wave_max(fabsf(s.beta[lane]));
   const Scale sp = scale_for(__uint_as_float(s.top[kTopP]));
-  auto t_scale = [&](int n, float f) { return scale_for(__uint_as_float(s.top[kTopT + n]) * f); };
   for (int task = w; task < 3 * kBlocks; task += 8) {
     const int kind = task / kBlocks;  // T, T^T, P^T
     int I, J;
@@ -378,7 +378,12 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
     const int row = 16 * (kind == 0 ? I : J) + n16;
     const int other = 16 * (kind == 0 ? J : I) + 4 * g4;
     u32x2 hi, lo;
-    split4h(x * (kind == 2 ? sp.up : t_scale(task % kBlocks, kind == 0 ? 1.f : btop).up), hi, lo);
+    Scale sc = sp;
+    if (kind < 2) {
+      sc = scale_for(__uint_as_float(s.top[kTopT + task % kBlocks]) * (kind == 0 ? 1.f : btop));
+      if (lane == 0) s.un[kind][task % kBlocks] = sc.un;
+    }
+    split4h(x * sc.up, hi, lo);
     *reinterpret_cast<u32x2*>(dst[0] + row * PS + perm32(other)) = hi;
     *reinterpret_cast<u32x2*>(dst[1] + row * PS + perm32(other)) = lo;
     if (kind == 2 && I == J && (I & 1)) {  // nothing beside this one
@@ -415,7 +420,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         for (int u = 0; u < 2; ++u)  // transposed: rows are channels
           if (2 * t + u <= r)
           {
-            const float un = t_scale(block_index(r, 2 * t + u), 1.f).un;
+            const float un = s.un[0][block_index(r, 2 * t + u)];
             wt[r] += mfma_split16(kgh[t], kgl[t], h, l, u) * (un * tail_dn[2 * t + u]);
             xx += mfma_high16(h, l, vf[t], u) * (un * unv);
           }
@@ -426,7 +431,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         for (int u = 0; u < 2; ++u)
           if (2 * t + u >= r)
             z[r] += mfma_split16(keh[t], kel[t], h, l, u) *
-                    (t_scale(block_index(2 * t + u, r), btop).un * tail_dn[NB + 2 * t + u]);
+                    (s.un[1][block_index(2 * t + u, r)] * tail_dn[NB + 2 * t + u]);
         y[r] = mfma32(frag(s.b.pt[1], r, t), of[t], y[r]);
         y[r] = mfma32(frag(s.b.pt[0], r, t), of[t], y[r]);
       }
@@ -463,7 +468,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         for (int u = 0; u < 2; ++u)
           if (2 * t + u >= r)
             d += mfma_split16(h, l, yh[t], yl[t], u) *
-                 (t_scale(block_index(2 * t + u, r), btop).un * un);
+                 (s.un[1][block_index(2 * t + u, r)] * un);
       }
       *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d;
     }
