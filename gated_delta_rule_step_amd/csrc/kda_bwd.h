@@ -170,6 +170,16 @@ __device__ __forceinline__ float row16_max(float x) {
   return fmaxf(x, dpp<0x140>(x));
 }
 
+// The largest of a wave, in every lane.
+__device__ __forceinline__ float wave_max(float x) { return column_max(row16_max(x)); }
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+__device__ __forceinline__ float uniform_bits(uint32_t x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(x));
+}
+
 // Sum over the four 16-lane rows of a wave (lanes of equal lane % 16).
 __device__ __forceinline__ float rows_sum(float x) {
   x += __shfl_xor(x, 16);

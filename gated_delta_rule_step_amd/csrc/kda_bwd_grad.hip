@@ -149,15 +149,14 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
   }
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) top[a] = fmaxf(top[a], __shfl_xor(top[a], o));
+    top[a] = wave_max(top[a]);
     if (lane == 0) s.top[a][w] = top[a];
   }
   __syncthreads();
 #pragma unroll
   for (int a = 0; a < 3; ++a)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top[a] = fmaxf(top[a], s.top[a][i]);
+    for (int i = 0; i < 8; ++i) top[a] = fmaxf(top[a], uniform(s.top[a][i]));
   const Scale so = scale_for(top[0]), sv = scale_for(top[1]), sx = scale_for(top[2]);
 #pragma unroll
   for (int j = 0; j < NR; ++j) {

@@ -69,11 +69,6 @@ static_assert(sizeof(PrepSmem) <= 80 * 1024, "two workgroups per CU");
 __device__ __forceinline__ int perm32(int t) {
   return (t & 32) + 8 * ((t & 15) >> 2) + 4 * ((t >> 4) & 1) + (t & 3);
 }
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) x = fmaxf(x, __shfl_xor(x, o));
-  return x;
-}
 __device__ __forceinline__ float max4(f32x4 x) {
   return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 }
@@ -183,8 +178,8 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
       Scale su[NB], sd[NB];
   #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        su[b] = unit_scale(__uint_as_float(s.top[kTopPre + b]));
-        sd[b] = unit_scale(__uint_as_float(s.top[kTopPost + b]));
+        su[b] = unit_scale(uniform_bits(s.top[kTopPre + b]));
+        sd[b] = unit_scale(uniform_bits(s.top[kTopPost + b]));
         if (threadIdx.x == 0) {
           tail[kTailDnKG + b] = su[b].un;
           tail[kTailDnKE + b] = sd[b].un;
@@ -366,7 +361,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 
   // ---- T, T^T (with beta of the token that writes) and P^T as operands, over A, V and dO
   const float btop = wave_max(fabsf(s.beta[lane]));
-  const Scale sp = scale_for(__uint_as_float(s.top[kTopP]));
+  const Scale sp = scale_for(uniform_bits(s.top[kTopP]));
   for (int task = w; task < 3 * kBlocks; task += 8) {
     const int kind = task / kBlocks;  // T, T^T, P^T
     int I, J;
@@ -380,7 +375,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
     u32x2 hi, lo;
     Scale sc = sp;
     if (kind < 2) {
-      sc = scale_for(__uint_as_float(s.top[kTopT + task % kBlocks]) * (kind == 0 ? 1.f : btop));
+      sc = scale_for(uniform_bits(s.top[kTopT + task % kBlocks]) * (kind == 0 ? 1.f : btop));
       if (lane == 0) s.un[kind][task % kBlocks] = sc.un;
     }
     split4h(x * sc.up, hi, lo);
@@ -403,8 +398,8 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   float tail_dn[2 * NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    tail_dn[b] = unit_scale(__uint_as_float(s.top[kTopPre + b])).un;
-    tail_dn[NB + b] = unit_scale(__uint_as_float(s.top[kTopPost + b])).un;
+    tail_dn[b] = unit_scale(uniform_bits(s.top[kTopPre + b])).un;
+    tail_dn[NB + b] = unit_scale(uniform_bits(s.top[kTopPost + b])).un;
   }
   float* X = reinterpret_cast<float*>(ops + kOpX0);
   float* DV = reinterpret_cast<float*>(ops + kOpDV0);
@@ -420,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         for (int u = 0; u < 2; ++u)  // transposed: rows are channels
           if (2 * t + u <= r)
           {
-            const float un = s.un[0][block_index(r, 2 * t + u)];
+            const float un = uniform(s.un[0][block_index(r, 2 * t + u)]);
             wt[r] += mfma_split16(kgh[t], kgl[t], h, l, u) * (un * tail_dn[2 * t + u]);
             xx += mfma_high16(h, l, vf[t], u) * (un * unv);
           }
@@ -431,7 +426,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         for (int u = 0; u < 2; ++u)
           if (2 * t + u >= r)
             z[r] += mfma_split16(keh[t], kel[t], h, l, u) *
-                    (s.un[1][block_index(2 * t + u, r)] * tail_dn[NB + 2 * t + u]);
+                    (uniform(s.un[1][block_index(2 * t + u, r)]) * tail_dn[NB + 2 * t + u]);
         y[r] = mfma32(frag(s.b.pt[1], r, t), of[t], y[r]);
         y[r] = mfma32(frag(s.b.pt[0], r, t), of[t], y[r]);
       }
@@ -468,7 +463,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         for (int u = 0; u < 2; ++u)
           if (2 * t + u >= r)
             d += mfma_split16(h, l, yh[t], yl[t], u) *
-                 (s.un[1][block_index(2 * t + u, r)] * un);
+                 (uniform(s.un[1][block_index(2 * t + u, r)]) * un);
       }
       *reinterpret_cast<f32x4*>(DV + ((w * NB + r) * 64 + lane) * 4) = d;
     }
@@ -476,8 +471,8 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < NB; ++r) {
-    const Scale sw = scale_for(__uint_as_float(s.top[kTopW + r]));
-    const Scale sz = scale_for(__uint_as_float(s.top[kTopZ + r]));
+    const Scale sw = scale_for(uniform_bits(s.top[kTopW + r]));
+    const Scale sz = scale_for(uniform_bits(s.top[kTopZ + r]));
     if (threadIdx.x == 0) {
       tail[kTailUnW + r] = sw.un * kFixedUn;
       tail[kTailUnZ + r] = sz.un * kFixedUn;
