@@ -58,7 +58,7 @@ hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32
   const int64_t chains = int64_t(p.n_docs) * p.H;
   if (p.slots > 0x7fffffff || chains > 0x7fffffff / 16) return hipErrorInvalidValue;
   DocOrder ord;
-  ord.n = 0;
+  ord.n = ord.deep = 0;
   if (p.n_docs <= kMaxOrderedDocs) {  // the longest documents first
     for (int d = 0; d < p.n_docs; ++d) {
       const int len = cu_host[d + 1] - cu_host[d];
@@ -68,6 +68,10 @@ hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32
       ord.doc[at] = d;
     }
     ord.n = p.n_docs;
+    const int64_t deep = deep_chain_len(total_tokens, p.H);
+    while (ord.deep < ord.n &&
+           cu_host[ord.doc[ord.deep] + 1] - cu_host[ord.doc[ord.deep]] > deep)
+      ++ord.deep;
   }
   if (total_tokens > 0)
     if (const hipError_t e = launch_prep(p, stream)) return e;

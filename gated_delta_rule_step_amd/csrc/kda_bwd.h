@@ -17,6 +17,7 @@ constexpr int NB = C / 16;   // 16-token blocks per chunk
 constexpr int NP = NB * (NB - 1) / 2;
 constexpr int kThreads = 512;
 constexpr int kMaxOrderedDocs = 256;
+constexpr int kCus = 256;
 constexpr float kL2Eps = 1e-6f;
 
 struct BwdParams {
@@ -54,6 +55,7 @@ struct BwdParams {
 
 struct DocOrder {
   int32_t n;  // 0: natural order
+  int32_t deep;  // the first of them, whose chains take the form of least latency
   int32_t doc[kMaxOrderedDocs];
 };
 
@@ -408,6 +410,8 @@ inline hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<bool> 
 
 hipError_t launch_prep(const BwdParams& p, hipStream_t stream);
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream);
+// Length from which a document's chains bound the launch.
+int64_t deep_chain_len(int64_t total_tokens, int H);
 hipError_t launch_grads(const BwdParams& p, hipStream_t stream);
 hipError_t launch_params(const BwdParams& p, hipStream_t stream);  // dA_log, ddt_bias
 

@@ -87,24 +87,24 @@ struct Right {
   }
 };
 
-constexpr int KS = 2;        // waves of a value tile
-constexpr int NM = 8 / KS;   // state tiles of a wave
-constexpr int NX = NB / KS;  // token blocks of x whose start and result a wave moves
-
-// Workgroups of TW value tiles.
-template <int TW>
+// Workgroups of TW value tiles, KS waves each.
+template <int KS, int TW>
 struct ChainShape {
+  static constexpr int NM = 8 / KS;   // state tiles of a wave
+  static constexpr int NX = NB / KS;  // token blocks of x whose start and result a wave moves
   static constexpr int kThreads = 64 * KS * TW;
   static constexpr int kParts = 8 / TW;
   static constexpr int kXch = KS * TW * 4096;  // each wave's part of x
   static constexpr int kLds = 3 * kTileBytes + 2 * 1024 + kXch;
 };
 
-template <int TW>
-__global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdParams p,
-                                                                         DocOrder ord) {
-  constexpr int T = ChainShape<TW>::kThreads;
-  constexpr int PARTS = ChainShape<TW>::kParts;
+// Part `part` of the chain of (doc, h), up the document or down.
+template <int KS, int TW>
+__device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool down, int part) {
+  using Shape = ChainShape<KS, TW>;
+  constexpr int T = Shape::kThreads;
+  constexpr int NM = Shape::NM;
+  constexpr int NX = Shape::NX;
   constexpr int NA = kTileBytes / 16 / T;
   extern __shared__ __align__(16) float smem_raw[];
   uint8_t* la = reinterpret_cast<uint8_t*>(smem_raw);
@@ -112,23 +112,12 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
   float* tails = reinterpret_cast<float*>(lb + 2 * kTileBytes);  // of even and odd chunks
   float* xch = tails + 512;                                      // [wave][rt][lane][4]
 
-  // Chain c's parts are blocks (c / 8 * PARTS + part) * 8 + c % 8: blocks go to the
-  // eight XCDs in turn, so the parts share one L2 copy of the operands.
-  const int64_t bid = blockIdx.x;
-  const int64_t id = bid / (8 * PARTS) * 8 + (bid & 7);
-  const int part = int((bid >> 3) % PARTS);
-  const bool down = id & 1;
-  const int64_t chain = id >> 1;
-  if (chain >= int64_t(p.n_docs) * p.H) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kh = wave % KS;
   const int g4 = lane >> 4, n16 = lane & 15;
   const int v = 16 * (part * TW + wave / KS) + n16;  // this lane's value channel
-  const int k0 = 64 * kh + 4 * g4;                   // its first key channel
-  const int h = int(chain % p.H);
-  const int rank = int(chain / p.H);
-  const int doc = ord.n > 0 ? ord.doc[rank] : rank;
+  const int k0 = 16 * NM * kh + 4 * g4;                   // its first key channel
   const int32_t t0 = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc]);
   const int32_t len = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc + 1]) - t0;
   const int32_t slot = __builtin_amdgcn_readfirstlane(p.state_indices[doc]);
@@ -143,8 +132,8 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
   for (int m = 0; m < NM; ++m) s[m] = zero4();
 
   // tile A's fragments of this wave's keys, tile B's of its state tiles
-  const uint8_t* fa = la + kh * 4096 + lane * 16;
-  const uint8_t* fb = lb + kh * 16384 + lane * 16;
+  const uint8_t* fa = la + kh * (NM * 1024) + lane * 16;
+  const uint8_t* fb = lb + kh * (NM * 4096) + lane * 16;
   auto frag = [](const uint8_t* base, int unit) {
     return *reinterpret_cast<const f16x8*>(base + unit * 1024);
   };
@@ -180,6 +169,9 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
       x[r] += lds4(xch + (((wave ^ 1) * NB + r) * 64 + lane) * 4);
+      if constexpr (KS == 4)  // (pairs first: the same sum in all four)
+        x[r] += lds4(xch + (((wave ^ 2) * NB + r) * 64 + lane) * 4) +
+                lds4(xch + (((wave ^ 3) * NB + r) * 64 + lane) * 4);
       if (r / NX == kh)
 #pragma unroll
         for (int i = 0; i < 4; ++i) rows[(16 * r + 4 * g4 + i) * D + v] = x[r][i];
@@ -370,26 +362,65 @@ __global__ __launch_bounds__(ChainShape<TW>::kThreads) void chain_kernel(BwdPara
   }
 }
 
-template <int TW>
-hipError_t launch_chain(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
-  using Shape = ChainShape<TW>;
-  static std::atomic<bool> allowed[kMaxDevices];
-  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(chain_kernel<TW>), Shape::kLds, allowed))
-    return e;
-  const int64_t ids = (int64_t(p.n_docs) * p.H * 2 + 7) / 8 * 8;  // both directions
-  hipLaunchKernelGGL(chain_kernel<TW>, dim3(unsigned(ids * Shape::kParts)), dim3(Shape::kThreads),
-                     Shape::kLds, stream, p, ord);
-  return hipGetLastError();
+// Of `docs` documents from the order's `first` on, the chain and part of block `bid`. Chain
+// c's parts are blocks (c / 8 * PARTS + part) * 8 + c % 8: blocks go to the eight XCDs in
+// turn, so the parts share one L2 copy of the operands.
+template <int KS, int TW>
+__device__ __forceinline__ void chain_of_block(const BwdParams& p, const DocOrder& ord, int64_t bid,
+                                               int first, int docs) {
+  constexpr int PARTS = ChainShape<KS, TW>::kParts;
+  const int64_t id = bid / (8 * PARTS) * 8 + (bid & 7);
+  const int64_t c = id >> 1;
+  if (c >= int64_t(docs) * p.H) return;
+  const int rank = first + int(c / p.H);
+  const int doc = ord.n > 0 ? ord.doc[rank] : rank;
+  chain<KS, TW>(p, doc, int(c % p.H), id & 1, int((bid >> 3) % PARTS));
+}
+template <int KS, int TW>
+__host__ __device__ int64_t blocks_of(int64_t docs, int H) {
+  return (docs * H * 2 + 7) / 8 * 8 * ChainShape<KS, TW>::kParts;
+}
+
+using Few = ChainShape<4, 1>;
+using Deep = ChainShape<4, 2>;
+using Wide = ChainShape<2, 4>;
+
+__global__ __launch_bounds__(Few::kThreads) void chain_few_kernel(BwdParams p, DocOrder ord) {
+  chain_of_block<4, 1>(p, ord, blockIdx.x, 0, p.n_docs);
+}
+
+static_assert(Deep::kThreads == Wide::kThreads && Deep::kLds == Wide::kLds, "one launch for both");
+
+__global__ __launch_bounds__(Wide::kThreads) void chain_kernel(BwdParams p, DocOrder ord) {
+  const int64_t bid = int64_t(blockIdx.x) - blocks_of<4, 2>(ord.deep, p.H);
+  if (bid < 0)
+    chain_of_block<4, 2>(p, ord, blockIdx.x, 0, ord.deep);
+  else
+    chain_of_block<2, 4>(p, ord, bid, ord.deep, p.n_docs - ord.deep);
 }
 
 }  // namespace
 
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
-  // Two value tiles per workgroup where the chains alone would leave most CUs idle (12 chains
-  // of 8191 tokens: 550 us against 620 with four; 80 chains: 3 % of the whole call), else four
-  // (168 chains: 5 % of the call).
-  return int64_t(p.n_docs) * p.H <= 96 ? launch_chain<2>(p, ord, stream)
-                                       : launch_chain<4>(p, ord, stream);
+  if (blocks_of<4, 1>(p.n_docs, p.H) <= kCus) {
+    static std::atomic<bool> allowed[kMaxDevices];
+    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(chain_few_kernel), Few::kLds, allowed))
+      return e;
+    hipLaunchKernelGGL(chain_few_kernel, dim3(unsigned(blocks_of<4, 1>(p.n_docs, p.H))),
+                       dim3(Few::kThreads), Few::kLds, stream, p, ord);
+    return hipGetLastError();
+  }
+  static std::atomic<bool> allowed[kMaxDevices];
+  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(chain_kernel), Wide::kLds, allowed))
+    return e;
+  const int64_t blocks = blocks_of<4, 2>(ord.deep, p.H) + blocks_of<2, 4>(p.n_docs - ord.deep, p.H);
+  hipLaunchKernelGGL(chain_kernel, dim3(unsigned(blocks)), dim3(Wide::kThreads), Wide::kLds, stream,
+                     p, ord);
+  return hipGetLastError();
+}
+
+int64_t deep_chain_len(int64_t total_tokens, int H) {
+  return total_tokens * H * 2 * Wide::kParts / kCus;
 }
 
 }  // namespace bwd
