@@ -94,8 +94,10 @@ struct ChainShape {
   static constexpr int NX = NB / KS;  // token blocks of x whose start and result a wave moves
   static constexpr int kThreads = 64 * KS * TW;
   static constexpr int kParts = 8 / TW;
+  // With one value tile, every fragment has one reader, and goes to its registers directly.
+  static constexpr bool kOwn = TW == 1;
   static constexpr int kXch = KS * TW * 4096;  // each wave's part of x
-  static constexpr int kLds = 3 * kTileBytes + 2 * 1024 + kXch;
+  static constexpr int kLds = kOwn ? 3 * 1024 + 2 * kXch : 3 * kTileBytes + 2 * 1024 + kXch;
 };
 
 // Part `part` of the chain of (doc, h), up the document or down.
@@ -106,11 +108,14 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   constexpr int NM = Shape::NM;
   constexpr int NX = Shape::NX;
   constexpr int NA = kTileBytes / 16 / T;
+  constexpr bool OWN = Shape::kOwn;
   extern __shared__ __align__(16) float smem_raw[];
   uint8_t* la = reinterpret_cast<uint8_t*>(smem_raw);
   uint8_t* lb = la + kTileBytes;
-  float* tails = reinterpret_cast<float*>(lb + 2 * kTileBytes);  // of even and odd chunks
-  float* xch = tails + 512;                                      // [wave][rt][lane][4]
+  // Those of even and odd chunks; OWN, whose one barrier a chunk lets a wave run further
+  // ahead: of every third, and the parts of x of even and odd chunks.
+  float* tails = reinterpret_cast<float*>(OWN ? la : lb + 2 * kTileBytes);
+  float* xch0 = tails + (OWN ? 768 : 512);  // [wave][rt][lane][4]
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -132,13 +137,47 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   for (int m = 0; m < NM; ++m) s[m] = zero4();
 
   // tile A's fragments of this wave's keys, tile B's of its state tiles
-  const uint8_t* fa = la + kh * (NM * 1024) + lane * 16;
-  const uint8_t* fb = lb + kh * (NM * 4096) + lane * 16;
+  const int at_a = kh * (NM * 1024) + lane * 16, at_b = kh * (NM * 4096) + lane * 16;
   auto frag = [](const uint8_t* base, int unit) {
     return *reinterpret_cast<const f16x8*>(base + unit * 1024);
   };
+  constexpr int OA = OWN ? NB * NM : 1, OB = OWN ? NM * 4 : 1;
+  f16x8 own_a[OA], own_b[OB], own_q[OB];
+  auto frag_a = [&](int r, int t, int low) {
+    if constexpr (OWN) return own_a[r * NM + t * 2 + low];
+    else return frag(la + at_a, r * 8 + t * 2 + low);
+  };
+  auto frag_b = [&](int m, int t, int low) {
+    if constexpr (OWN) return own_b[m * 4 + t * 2 + low];
+    else return frag(lb + at_b, m * 4 + t * 2 + low);
+  };
+  auto frag_q = [&](int m, int t, int low) {
+    if constexpr (OWN) return own_q[m * 4 + t * 2 + low];
+    else return frag(lb + at_b, 32 + m * 4 + t * 2 + low);
+  };
+  auto load_own_a = [&](const uint8_t* src, int r) {
+#pragma unroll
+    for (int i = 0; i < NM; ++i)
+      if constexpr (OWN) own_a[r * NM + i] = frag(src + at_a, r * 8 + i);
+  };
+  auto load_own_b = [&](f16x8 (&b)[OB], const uint8_t* src, int m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if constexpr (OWN) b[m * 4 + i] = frag(src + at_b, m * 4 + i);
+  };
   Stage<NA, T> sa;  // the next tile A, and its chunk's tail
   u32x4 st = {0u, 0u, 0u, 0u};
+  auto tail_of = [&](int n) { return tails + (OWN ? n % 3 : n & 1) * 256; };
+  auto xch_of = [&](int n) { return xch0 + (OWN ? (n & 1) * (Shape::kXch / 4) : 0); };
+  // tile A of chunk n, and of the next one a share per token block
+  auto load_a = [&](const uint8_t* src) {
+    if constexpr (OWN) {
+#pragma unroll
+      for (int r = 0; r < NB; ++r) load_own_a(src, r);
+    } else {
+      sa.load(src);
+    }
+  };
   // this wave's part of x: the sum over its keys of tile A times the state
   auto product = [&](const Right<NM>& b, f32x4 (&acc)[NB], const uint8_t* next) {
 #pragma unroll
@@ -146,18 +185,23 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
       acc[r] = zero4();
 #pragma unroll
       for (int t = 0; t < NM / 2; ++t) {
-        const f16x8 ah = frag(fa, r * 8 + t * 2), al = frag(fa, r * 8 + t * 2 + 1);
+        const f16x8 ah = frag_a(r, t, 0), al = frag_a(r, t, 1);
         acc[r] = mfma32(al, b.hi[t], acc[r]);
         acc[r] = mfma32(ah, b.lo[t], acc[r]);
         acc[r] = mfma32(ah, b.hi[t], acc[r]);
       }
-      sa.template load_share<NB>(next, r);
+      if constexpr (OWN) {
+        load_own_a(next, r);
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        sa.template load_share<NB>(next, r);
+      }
     }
   };
   // x = x0 + un * (what `product` left), rows written: the two waves of a tile add up their
   // parts (x0 and the rows are shared between them, a part of the blocks each).
   auto exchange_out = [&](f32x4 (&x)[NB], const f32x4 (&acc)[NB], float un, f32x4 unr,
-                          const f32x4 (&x0)[NX]) {
+                          const f32x4 (&x0)[NX], float* xch) {
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
       x[r] = acc[r] * (un * unr[r]);
@@ -165,7 +209,7 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
       *reinterpret_cast<f32x4*>(xch + ((wave * NB + r) * 64 + lane) * 4) = x[r];
     }
   };
-  auto exchange_in = [&](f32x4 (&x)[NB], float* rows) {
+  auto exchange_in = [&](f32x4 (&x)[NB], float* rows, const float* xch) {
 #pragma unroll
     for (int r = 0; r < NB; ++r) {
       x[r] += lds4(xch + (((wave ^ 1) * NB + r) * 64 + lane) * 4);
@@ -193,9 +237,12 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   auto load_tail = [&](int n) {
     if (wave == 0) st = *reinterpret_cast<const u32x4*>(ops0 + n * step + lane * 16);
   };
+  auto store_tail = [&](int n) {
+    if (wave == 0) *reinterpret_cast<u32x4*>(tail_of(n) + lane * 4) = st;
+  };
   auto store_a = [&](int n) {
     sa.store(la);
-    if (wave == 0) *reinterpret_cast<u32x4*>(tails + (n & 1) * 256 + lane * 4) = st;
+    store_tail(n);
   };
 
   if (!down) {
@@ -209,17 +256,23 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
     }
     Stage<NA, T> sb;
     f32x4 x0[NX];  // of the next chunk, asked for a phase ahead
-    sa.load(ops0 + kOpW);
+    load_a(ops0 + kOpW);
     load_tail(0);
     load_x0(x0, 0, kOpX0);
-    store_a(0);
-    sb.load(ops0 + kOpKE);
+    if constexpr (OWN) {
+      store_tail(0);
+#pragma unroll
+      for (int m = 0; m < NM; ++m) load_own_b(own_b, ops0 + kOpKE, m);
+    } else {
+      store_a(0);
+      sb.load(ops0 + kOpKE);
+    }
     __syncthreads();
     for (int n = 0; n < chunks; ++n) {
       uint8_t* ops = ops0 + n * step;
       const bool more = n + 1 < chunks;
       const uint8_t* after = more ? ops + step : ops;  // (the last chunk asks for itself again)
-      const float* tail = tails + (n & 1) * 256;
+      const float* tail = tail_of(n);
       f32x4 x[NB];
       // ---- x = T V - W S
       load_tail(more ? n + 1 : n);
@@ -229,11 +282,14 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
         b.set(s);
         product(b, acc, after + kOpW);
         store_state(reinterpret_cast<float*>(ops + kOpS));
-        exchange_out(x, acc, -b.un, lds4(tail + kTailUnW), x0);
+        exchange_out(x, acc, -b.un, lds4(tail + kTailUnW), x0, xch_of(n));
       }
-      if (more) sb.store(lb);
+      if constexpr (OWN)
+        store_tail(n + 1);
+      else if (more)
+        sb.store(lb);
       __syncthreads();
-      exchange_in(x, reinterpret_cast<float*>(ops + kOpX));
+      exchange_in(x, reinterpret_cast<float*>(ops + kOpX), xch_of(n));
       if (!more) return;  // the state after the last chunk is not needed
       // ---- S = e^Gl S + KE^T (beta x)
       Right<NB> b;
@@ -248,18 +304,25 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
         f32x4 acc = zero4();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const f16x8 ah = frag(fb, m * 4 + t * 2), al = frag(fb, m * 4 + t * 2 + 1);
+          const f16x8 ah = frag_b(m, t, 0), al = frag_b(m, t, 1);
           acc = mfma32(al, b.hi[t], acc);
           acc = mfma32(ah, b.lo[t], acc);
           acc = mfma32(ah, b.hi[t], acc);
         }
-        sb.template load_share<NM>(after + kOpKE, m);
+        if constexpr (OWN) {
+          load_own_b(own_b, after + kOpKE, m);
+          __builtin_amdgcn_sched_barrier(0);
+        } else {
+          sb.template load_share<NM>(after + kOpKE, m);
+        }
         s[m] *= lds4(tail + k0 + 16 * m);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[m][i] = fmaf(acc[i], un, s[m][i]);
       }
-      store_a(n + 1);
-      __syncthreads();
+      if constexpr (!OWN) {
+        store_a(n + 1);
+        __syncthreads();
+      }
     }
     return;
   }
@@ -279,17 +342,26 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
 #pragma unroll
       for (int t = 0; t < 2; ++t) ow[t] = *reinterpret_cast<const u32x4*>(src + t * 1024);
     };
-    sa.load(ops0 + (chunks - 1) * step + kOpZ);
+    load_a(ops0 + (chunks - 1) * step + kOpZ);
     load_tail(chunks - 1);
     load_x0(x0, chunks - 1, kOpDV0);
     load_o(chunks - 1);
-    store_a(chunks - 1);
-    sb.load(ops0 + (chunks - 1) * step + kOpKG);
+    if constexpr (OWN) {
+      store_tail(chunks - 1);
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        load_own_b(own_b, ops0 + (chunks - 1) * step + kOpKG, m);
+        load_own_b(own_q, ops0 + (chunks - 1) * step + kOpQG, m);
+      }
+    } else {
+      store_a(chunks - 1);
+      sb.load(ops0 + (chunks - 1) * step + kOpKG);
+    }
     __syncthreads();
     for (int n = chunks - 1; n >= 0; --n) {
       uint8_t* ops = ops0 + n * step;
       const uint8_t* after = n > 0 ? ops - step : ops;
-      const float* tail = tails + (n & 1) * 256;
+      const float* tail = tail_of(n);
       f32x4 x[NB];
       // ---- dV = T^T P^T dO + Z dS
       load_tail(n > 0 ? n - 1 : 0);
@@ -299,12 +371,16 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
         b.set(s);
         product(b, acc, after + kOpZ);
         store_state(reinterpret_cast<float*>(ops + kOpDS));
-        exchange_out(x, acc, b.un, lds4(tail + kTailUnZ), x0);
+        exchange_out(x, acc, b.un, lds4(tail + kTailUnZ), x0, xch_of(n));
       }
       const bool more = n > 0 || p.d_initial;
-      if (more) sb.store(lb);
+      if constexpr (OWN) {
+        if (n > 0) store_tail(n - 1);
+      } else if (more) {
+        sb.store(lb);
+      }
       __syncthreads();
-      exchange_in(x, reinterpret_cast<float*>(ops + kOpDV));
+      exchange_in(x, reinterpret_cast<float*>(ops + kOpDV), xch_of(n));
       if (!more) return;
       // ---- dS = e^Gl dS - KG^T dV + scale QG^T dO. dO has 8 bits: its high part is exact.
       Right<NB> b;
@@ -339,21 +415,29 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
         f32x4 acc = zero4(), acc2 = zero4();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const f16x8 ah = frag(fb, m * 4 + t * 2), al = frag(fb, m * 4 + t * 2 + 1);
-          const f16x8 qh = frag(fb, 32 + m * 4 + t * 2), ql = frag(fb, 33 + m * 4 + t * 2);
+          const f16x8 ah = frag_b(m, t, 0), al = frag_b(m, t, 1);
+          const f16x8 qh = frag_q(m, t, 0), ql = frag_q(m, t, 1);
           acc = mfma32(al, b.hi[t], acc);
           acc2 = mfma32(ql, o[t], acc2);
           acc = mfma32(ah, b.lo[t], acc);
           acc2 = mfma32(qh, o[t], acc2);
           acc = mfma32(ah, b.hi[t], acc);
         }
-        sb.template load_share<NM>(after + kOpKG, m);
+        if constexpr (OWN) {
+          load_own_b(own_b, after + kOpKG, m);
+          load_own_b(own_q, after + kOpQG, m);
+          __builtin_amdgcn_sched_barrier(0);
+        } else {
+          sb.template load_share<NM>(after + kOpKG, m);
+        }
         s[m] *= lds4(tail + k0 + 16 * m);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[m][i] = fmaf(acc2[i], uno, fmaf(acc[i], un, s[m][i]));
       }
-      if (n > 0) store_a(n - 1);
-      __syncthreads();
+      if constexpr (!OWN) {
+        if (n > 0) store_a(n - 1);
+        __syncthreads();
+      }
     }
   }
   if (p.d_initial) {
