@@ -68,9 +68,9 @@ hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32
       ord.doc[at] = d;
     }
     ord.n = p.n_docs;
-    const int64_t deep = deep_chain_len(total_tokens, p.H);
     while (ord.deep < ord.n &&
-           cu_host[ord.doc[ord.deep] + 1] - cu_host[ord.doc[ord.deep]] > deep)
+           deep_chains(total_tokens, p.H, ord.deep,
+                       cu_host[ord.doc[ord.deep] + 1] - cu_host[ord.doc[ord.deep]]))
       ++ord.deep;
   }
   if (total_tokens > 0)

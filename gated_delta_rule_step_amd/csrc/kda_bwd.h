@@ -410,8 +410,8 @@ inline hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<bool> 
 
 hipError_t launch_prep(const BwdParams& p, hipStream_t stream);
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream);
-// Length from which a document's chains bound the launch.
-int64_t deep_chain_len(int64_t total_tokens, int H);
+// Whether the chains of the document that is `rank`th in length take the form of least latency.
+bool deep_chains(int64_t total_tokens, int H, int rank, int len);
 hipError_t launch_grads(const BwdParams& p, hipStream_t stream);
 hipError_t launch_params(const BwdParams& p, hipStream_t stream);  // dA_log, ddt_bias
 

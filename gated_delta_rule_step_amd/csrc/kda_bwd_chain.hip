@@ -503,8 +503,8 @@ hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t st
   return hipGetLastError();
 }
 
-int64_t deep_chain_len(int64_t total_tokens, int H) {
-  return total_tokens * H * 2 * Wide::kParts / kCus;
+bool deep_chains(int64_t total_tokens, int H, int rank, int len) {
+  return len > total_tokens * H * 2 * Wide::kParts / kCus && blocks_of<4, 2>(rank + 1, H) <= kCus;
 }
 
 }  // namespace bwd
