@@ -353,6 +353,17 @@ def test_no_tokens():
     assert (o["dA"] == 0).all() and (o["ddt"] == 0).all()
 
 
+# the chains' forms: four long documents in the one of least latency and the rest in the
+# wide one; all in the first; all in the second; a document count that leaves blocks over
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,H", [((65, 0, 200, 7, 130, 64, 71, 1), 8), ((200,), 20),
+                                    ((129, 70), 40), ((193, 3, 80, 66, 5, 64, 1), 3)], ids=str)
+@pytest.mark.parametrize("state,dfinal", [(None, False), (BF, True)])
+def test_chain_forms(lens, H, state, dfinal):
+    c = make(lens, H=H, seed=50 + H, state=state, dfinal=dfinal)
+    compare(c, run(c))
+
+
 @pytest.mark.gpu
 def test_many_documents():
     """More documents than the ordered launch holds."""
