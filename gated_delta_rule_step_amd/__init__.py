@@ -3,7 +3,9 @@
 Argument marshalling only: every function takes torch tensors that already
 live on the GPU, checks dtype/device/contiguity of the innermost dimension,
 and passes raw pointers, element strides and the current HIP stream to the C
-ABI declared in include/kda.h. All arithmetic runs in the library's kernels;
+ABI declared in include/kda.h (the recurrence: decode, verify, prefill),
+kda_backward.h (the prefill's gradients) and kda_norm.h (the layer's RMS norms
+and their gradients). All arithmetic runs in the library's kernels;
 there is no fallback. If libkda.so is missing the first call raises.
 
 bf16 tensors are torch.bfloat16; A_log and dt_bias are float32; indices and

@@ -11,21 +11,30 @@ namespace {
 // ---------------------------------------------------------------------------
 // Chains: the states up each (document, head), and the state gradients down.
 // Value channels do not mix in either, so a chain splits into tiles of 16 of them, and
-// it is sequential over the chunks alone. What bounds it is the latency of one chunk:
-// two products that wait for each other, with a handful of waves per CU to hide it. A tile
-// therefore belongs to two waves that hold 64 key channels each (four accumulator tiles):
-// both form their keys' part of the first product, exchange it through LDS, and then hold the
-// same x for the second. (One wave per tile: 8191 tokens, 12 heads, 616 us instead of 500;
-// six documents at 64 heads as fast.)
+// it is sequential over the chunks alone. What bounds it is the latency of one chunk: two
+// products that wait for each other, with a handful of waves per CU to hide it. A tile
+// therefore belongs to KS waves that hold 128 / KS key channels each: all form their keys'
+// part of the first product, exchange the parts through LDS, and then hold the same x for the
+// second. Times of the whole call, us; 12 heads of 8191 tokens | 14 documents, 12 heads | 64
+// heads, 8208 tokens in six documents:
+//   two waves, four tiles (wide)           951 | 1084 | 2510
+//   four waves, two tiles (deep)           832 | 1126 | 2790
+//   four waves, one tile, operands by LDS  802 | 1412 | 3588
+//   the same, operands to registers (few)  722 | 1199 | 2963
+//   two waves, two tiles                   884 | 1162 | 2895
+//   two waves, one tile                    844 | 1470 | 3806
+// so the first, second and fourth are taken where each is best, see launch_chains.
 //
 // The products run on fp16 MFMA, both sides split into high and low parts (three terms,
 // fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides, the state and x in
 // accumulator layout, are scaled per value channel.
 //
-// A chunk's left operands come in two tiles (W, then KE; or Z, then KG and QG) that all
-// waves share through LDS. Loads of a tile are issued two phases before it is read and
-// wait in registers in between; the barrier between the phases publishes one tile, frees
-// the other, and publishes the exchanged parts too.
+// A chunk's left operands come in two tiles (W, then KE; or Z, then KG and QG). With several
+// value tiles all waves share them through LDS: loads of a tile are issued two phases before
+// it is read and wait in registers in between; the barrier between the phases publishes one
+// tile, frees the other, and publishes the exchanged parts too. With one value tile every
+// fragment has a single reader: it goes to that wave's registers a chunk ahead, LDS holds the
+// exchanged parts alone, and one barrier a chunk is left.
 __device__ __forceinline__ float pool_at(const BwdParams& p, int64_t e) {
   if (p.state_dtype == KDA_STATE_FP8)
     return f8x2_lo(static_cast<const uint8_t*>(p.pool)[e])[0];
@@ -485,6 +494,11 @@ __global__ __launch_bounds__(Wide::kThreads) void chain_kernel(BwdParams p, DocO
 
 }  // namespace
 
+// One tile per workgroup as long as all of them run at once, one per CU (8191 tokens, us:
+// 12 heads 722 against 832 with two tiles; 4096 tokens, 24 heads 670 against 618). Beyond that four
+// tiles, which read the operands least often; but the longest documents' chains, where one
+// of them would outlast its share of all the work, two tiles of four waves
+// (14 documents, 12 heads: 1056 against 1086).
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
   if (blocks_of<4, 1>(p.n_docs, p.H) <= kCus) {
     static std::atomic<bool> allowed[kMaxDevices];
@@ -503,6 +517,8 @@ hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t st
   return hipGetLastError();
 }
 
+// Deep chains' blocks run at once, one per CU (48 heads of 4096 tokens, all of them too long
+// for their share: 1194 us with twice as many blocks as fit, 1040 wide).
 bool deep_chains(int64_t total_tokens, int H, int rank, int len) {
   return len > total_tokens * H * 2 * Wide::kParts / kCus && blocks_of<4, 2>(rank + 1, H) <= kCus;
 }

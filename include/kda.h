@@ -1,5 +1,6 @@
 /*
  * kda.h -- C ABI of the MI355X (gfx950) KDA gated delta-rule step library.
+ * (kda_backward.h: the prefill's gradients; kda_norm.h: a KDA layer's norms.)
  *
  * The method (Kimi Delta Attention): per head h, a state S that maps 128 key
  * channels to 128 value channels is updated for every token by

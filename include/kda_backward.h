@@ -30,7 +30,7 @@ extern "C" {
 /*
  * kda_prefill_backward_workspace_size -- bytes of device workspace
  * kda_prefill_varlen_backward needs for these sizes (0 when K or V is not 128 or
- * a size is invalid). Pure host arithmetic: about 6.7 KB per token and head (per
+ * a size is invalid). Pure host arithmetic: about 6.9 KB per token and head (per
  * 64-token chunk and head: the state that enters it, the state gradient that
  * leaves it, and the chunk's operands, fp32).
  */
@@ -75,9 +75,10 @@ size_t kda_prefill_backward_workspace_size(int32_t n_docs, int64_t total_tokens,
  * gradient (they pass it on unchanged). States, their gradients, sums and decays
  * are fp32. Statuses as for kda_prefill_varlen; KDA_ERR_UNSUPPORTED for a
  * lower_bound outside [-5.5, 0], for dA_log or ddt_bias with KDA_GATE_PRECOMPUTED, for
- * more than 65535 heads and for a token stride beyond 2^25 elements. Any 2-byte-aligned bf16 pointer (fp32: 4-byte; fp8
- * states: any) and any stride is accepted. total_tokens = 0 writes zeros to dA_log
- * and ddt_bias and passes d_final_state on to d_initial_state.
+ * more than 65535 heads and for a token stride beyond 2^25 elements. Any
+ * 2-byte-aligned bf16 pointer (fp32: 4-byte; fp8 states: any) and any stride is
+ * accepted. total_tokens = 0 writes zeros to dA_log and ddt_bias and passes
+ * d_final_state on to d_initial_state.
  */
 kda_status kda_prefill_varlen_backward(
     int32_t n_docs, int64_t total_tokens, int32_t H, int32_t K, int32_t V,
