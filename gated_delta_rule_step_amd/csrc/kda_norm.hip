@@ -383,9 +383,11 @@ __global__ __launch_bounds__(1024) void reduce_partials(const float* partial, in
 // host
 
 // The lanes and groups of 8 that hold a vector: the narrowest shape that covers its
-// width, or, where there are too few vectors to fill the chip (below four per CU), the one
-// with the most lanes, so that a vector's loads are all in flight at once.
-constexpr int64_t kFewVecs = 1024;
+// width, or, where there are too few vectors to fill the chip (up to two per CU), the one
+// with the most lanes, so that a vector's loads are all in flight at once. (8192 channels, us,
+// most lanes against fewer; 1 row 3.1 and 3.6, 512 rows 6.1 and 6.5, their gradient 22.3 and
+// 24.5; 1024 rows 12.3 and 12.0, their gradient 27.6 and 24.3.)
+constexpr int64_t kFewVecs = 512;
 #define KDA_NORM_SHAPES(F)                      \
   if (width <= 128) return F(16, 1);            \
   if (width <= 512) return F(64, 1);            \
@@ -415,7 +417,19 @@ unsigned norm_blocks(int64_t vecs, int width, int64_t most) {
   return unsigned(b < most ? b : most);
 }
 constexpr int64_t kNormBlocks = 2048;
-constexpr int64_t kNormBwdBlocks = 512;
+// A workgroup of the gradient leaves a partial row, as much traffic as a vector, so it walks
+// at least eight vectors as long as every CU has one (8192 channels, us, 512 workgroups
+// against this rule: 512 rows 22.2 and 16.2, 2048 rows 31.0 and 28.4). Wide rows fill the chip
+// with two per CU (8208 rows: 1024 workgroups 94.0, 512 86.5); narrow ones take four where
+// each lane group still walks 16 vectors (16384 rows, with two and with four: of 1536 38.5 and
+// 32.8, of 2500 91.4 and 65.3, of 4096 78.0 and 87.1).
+int64_t most_bwd_blocks(int width) { return width <= 2560 ? 1024 : 512; }
+unsigned norm_bwd_blocks(int64_t vecs, int width) {
+  const int64_t walk = vecs / vecs_per_block(vecs, width) / 16;
+  int64_t most = vecs / 8 < 256 ? 256 : vecs / 8 > 512 ? 512 : vecs / 8;
+  if (walk > most) most = walk < most_bwd_blocks(width) ? walk : most_bwd_blocks(width);
+  return norm_blocks(vecs, width, most);
+}
 
 template <int L, int N, bool RES, bool GATE>
 hipError_t launch_norm3(const NormParams& p, int out, hipStream_t stream) {
@@ -451,7 +465,7 @@ hipError_t launch_norm(const NormParams& p, int out, hipStream_t stream) {
 
 template <int L, int N>
 hipError_t launch_norm_bwd2(const NormBwdParams& p, hipStream_t stream) {
-  const dim3 grid(norm_blocks(p.vecs, p.width, kNormBwdBlocks)), block(kNormThreads<L>);
+  const dim3 grid(norm_bwd_blocks(p.vecs, p.width)), block(kNormThreads<L>);
   if (p.dres && p.gate)
     hipLaunchKernelGGL((rmsnorm_bwd_kernel<L, N, true, true>), grid, block, 0, stream, p);
   else if (p.dres)
@@ -537,7 +551,9 @@ extern "C" kda_status kda_rmsnorm(int64_t rows, int32_t heads, int32_t width, co
 extern "C" size_t kda_rmsnorm_backward_workspace_size(int64_t rows, int32_t heads,
                                                       int32_t width) {
   if (kda::check_sizes(rows, heads, width, 1.0f)) return 0;
-  return size_t(kda::norm_blocks(rows * heads, width, kda::kNormBwdBlocks)) * size_t(width) * 4;
+  const int64_t vecs = rows * heads;  // (never less for more rows, so that one buffer serves all)
+  const int64_t most = kda::most_bwd_blocks(width);
+  return size_t(vecs < most ? vecs : most) * size_t(width) * 4;
 }
 
 extern "C" kda_status kda_rmsnorm_backward(
@@ -559,7 +575,7 @@ extern "C" kda_status kda_rmsnorm_backward(
         (gate && !kda::rows_apart(rows, dgate_row_stride, W)))
       return KDA_ERR_BAD_STRIDE;
   }
-  const int blocks = int(kda::norm_blocks(rows * heads, width, kda::kNormBwdBlocks));
+  const int blocks = int(kda::norm_bwd_blocks(rows * heads, width));
   if (dweight && rows > 0) {
     if (workspace_bytes < size_t(blocks) * size_t(width) * 4) return KDA_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace) return KDA_ERR_NULL_POINTER;

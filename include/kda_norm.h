@@ -76,7 +76,7 @@ kda_status kda_rmsnorm(int64_t rows, int32_t heads, int32_t width,
 
 /*
  * kda_rmsnorm_backward_workspace_size -- bytes kda_rmsnorm_backward needs for
- * these sizes (0 for invalid ones). Pure host arithmetic.
+ * these sizes (0 for invalid ones), never less for more rows. Pure host arithmetic.
  */
 size_t kda_rmsnorm_backward_workspace_size(int64_t rows, int32_t heads, int32_t width);
 

@@ -97,6 +97,17 @@ def test_workspace_size(lib):
     assert size(1 << 40, 1, 8192) == size(1 << 20, 1, 8192)  # bounded by the grid
 
 
+@pytest.mark.parametrize("width", [1, 128, 200, 1024, 1536, 2560, 2561, 8192, 16384])
+def test_workspace_grows_with_rows(lib, width):
+    """One buffer made for the most rows serves every call with fewer: the shapes that hold
+    a vector change with the row count."""
+    size = kda.kda_rmsnorm_backward_workspace_size
+    rows = [1, 2, 255, 256, 257, 511, 512, 513, 1000, 1024, 1025, 2100, 5000, 16384, 10 ** 6]
+    for heads in (1, 3):
+        got = [size(r, heads, width) for r in rows]
+        assert got == sorted(got)
+
+
 def test_binding_refuses(lib):
     x = torch.zeros(4, 128, dtype=BF)
     w = torch.ones(128)
