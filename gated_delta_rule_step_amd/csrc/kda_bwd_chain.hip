@@ -96,6 +96,16 @@ struct Right {
   }
 };
 
+// Lanes 4 q + j hold element i of column j; afterwards lane 4 q + j holds column i's element
+// j. With it a row's 16 values leave as four 16-byte stores instead of 16 of 4 bytes.
+__device__ __forceinline__ f32x4 quad_transpose(f32x4 a, int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const float r0 = dpp<0xB1>(b0 ? a[0] : a[1]), r2 = dpp<0xB1>(b0 ? a[2] : a[3]);
+  const f32x4 c = {b0 ? r0 : a[0], b0 ? a[1] : r0, b0 ? r2 : a[2], b0 ? a[3] : r2};
+  const float s0 = dpp<0x4E>(b1 ? c[0] : c[2]), s1 = dpp<0x4E>(b1 ? c[1] : c[3]);
+  return f32x4{b1 ? s0 : c[0], b1 ? s1 : c[1], b1 ? c[2] : s0, b1 ? c[3] : s1};
+}
+
 // Workgroups of TW value tiles, KS waves each.
 template <int KS, int TW>
 struct ChainShape {
@@ -131,6 +141,7 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   const int kh = wave % KS;
   const int g4 = lane >> 4, n16 = lane & 15;
   const int v = 16 * (part * TW + wave / KS) + n16;  // this lane's value channel
+  const int at_row = (4 * g4 + (lane & 3)) * D + (v & ~3);  // after quad_transpose, in a 16-row tile
   const int k0 = 16 * NM * kh + 4 * g4;                   // its first key channel
   const int32_t t0 = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc]);
   const int32_t len = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc + 1]) - t0;
@@ -225,16 +236,13 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
       if constexpr (KS == 4)  // (pairs first: the same sum in all four)
         x[r] += lds4(xch + (((wave ^ 2) * NB + r) * 64 + lane) * 4) +
                 lds4(xch + (((wave ^ 3) * NB + r) * 64 + lane) * 4);
-      if (r / NX == kh)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rows[(16 * r + 4 * g4 + i) * D + v] = x[r][i];
+      if (r / NX == kh) *reinterpret_cast<f32x4*>(rows + 16 * r * D + at_row) = quad_transpose(x[r], lane);
     }
   };
   auto store_state = [&](float* rows) {
 #pragma unroll
     for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) rows[(k0 + 16 * m + i) * D + v] = s[m][i];
+      *reinterpret_cast<f32x4*>(rows + 16 * (NM * kh + m) * D + at_row) = quad_transpose(s[m], lane);
   };
   // the start of x of chunk n, this wave's token blocks
   auto load_x0 = [&](f32x4 (&x0)[NX], int n, int op) {
