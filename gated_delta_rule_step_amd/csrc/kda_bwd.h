@@ -65,7 +65,8 @@ struct DocOrder {
 //               32 kt + 4 (lane / 16) + 0..3 and 16 further
 //   KE, KG, QG  [m 8][t 2][hi, lo][lane]    key channel 16 m + lane % 16, tokens
 //               32 t + 4 (lane / 16) + 0..3 and 16 further
-//   O           [vt 8][t 2][lane]           value channel 16 vt + lane % 16, tokens as in KE
+//   O           [vt 8][t 2][lane]           value channel 16 vt + lane % 16, tokens as in KE,
+//               scaled per value channel
 // X0 and DV0 are accumulator tiles [vt 8][rt 4][lane][4 tokens], X and DV rows
 // [token][value], S and dS rows [key][value], all fp32.
 constexpr int kOpTail = 0;               // e^Gl [128], beta [64], scales (below)
@@ -76,8 +77,9 @@ constexpr int kOpKG = kOpZ + 32768;      // e^G k
 constexpr int kOpQG = kOpKG + 32768;     // e^G q_hat
 constexpr int kOpX0 = kOpQG + 32768;     // T V
 constexpr int kOpDV0 = kOpX0 + 32768;    // T^T P^T dO
-constexpr int kOpO = kOpDV0 + 32768;     // dO (bf16)
-constexpr int kOpX = kOpO + 16384;       // x
+constexpr int kOpO = kOpDV0 + 32768;     // dO, as QG's right side (fp16)
+constexpr int kOpUnO = kOpO + 16384;     // what undoes O's scales [128]
+constexpr int kOpX = kOpUnO + 512;       // x
 constexpr int kOpDV = kOpX + 32768;      // dV
 constexpr int kOpS = kOpDV + 32768;      // S entering the chunk
 constexpr int kOpDS = kOpS + 65536;      // dS leaving it

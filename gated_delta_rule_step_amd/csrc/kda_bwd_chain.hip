@@ -353,11 +353,13 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   if (active && chunks > 0) {
     Stage<2 * NA, T> sb;
     f32x4 x0[NX];
-    u32x4 ow[2];  // dO: 64 tokens of this lane's value, in the order of a right fragment
+    f16x8 ow[2];  // dO: 64 tokens of this lane's value, a right fragment
+    float uow;
     auto load_o = [&](int n) {
       const uint8_t* src = ops0 + n * step + kOpO + ((v >> 4) * 2 * 64 + lane) * 16;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) ow[t] = *reinterpret_cast<const u32x4*>(src + t * 1024);
+      for (int t = 0; t < 2; ++t) ow[t] = frag(src, t);
+      uow = reinterpret_cast<const float*>(ops0 + n * step + kOpUnO)[v];
     };
     load_a(ops0 + (chunks - 1) * step + kOpZ);
     load_tail(chunks - 1);
@@ -405,28 +407,10 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
 #pragma unroll
       for (int r = 0; r < NB; ++r) x[r] *= dn[r];
       b.set(x);
-      f16x8 o[2];
-      float y[2][8], top = 0.f;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        unpack8_bf16(ow[t], y[t]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[t][i] *= dn[2 * t + i / 4];
-          top = fmaxf(top, fabsf(y[t][i]));
-        }
-      }
-      const Scale sc = scale_for(column_max(top));
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(y[t][2 * i] * sc.up, y[t][2 * i + 1] * sc.up);
-        o[t] = __builtin_bit_cast(f16x8, w);
-      }
+      const f16x8 o[2] = {ow[0], ow[1]};
+      const float un = -b.un * kFixedUn, uno = uow * (p.scale * kFixedUn);
       load_x0(x0, n > 0 ? n - 1 : 0, kOpDV0);
       load_o(n > 0 ? n - 1 : 0);
-      const float un = -b.un * kFixedUn, uno = sc.un * (p.scale * kFixedUn);
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         f32x4 acc = zero4(), acc2 = zero4();

@@ -81,14 +81,19 @@ __device__ __forceinline__ void block_of(int n, int& I, int& J) {
   while (J > I) J -= ++I;
 }
 
-// 64 tokens of a bf16 column as right fragments, scaled by the column's largest magnitude.
-__device__ __forceinline__ void bf16_fragments(const u32x4 (&w)[2], f16x8 (&f)[2], float& un) {
+// 64 tokens of a bf16 column, times a power of two per token block, as right fragments,
+// scaled by the column's largest magnitude.
+__device__ __forceinline__ void bf16_fragments(const u32x4 (&w)[2], f16x8 (&f)[2], float& un,
+                                               f32x4 by = f32x4{1.f, 1.f, 1.f, 1.f}) {
   float x[2][8], top = 0.f;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     unpack8_bf16(w[t], x[t]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[t][i]));
+    for (int i = 0; i < 8; ++i) {
+      x[t][i] *= by[2 * t + i / 4];
+      top = fmaxf(top, fabsf(x[t][i]));
+    }
   }
   const Scale sc = scale_for(column_max(top));
   un = sc.un;
@@ -322,11 +327,19 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
         vb[t][i] = uint32_t(s.b.v[at]) | uint32_t(s.b.v[at + D]) << 16;
         ob[t][i] = uint32_t(s.b.o[at]) | uint32_t(s.b.o[at + D]) << 16;
       }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      *reinterpret_cast<u32x4*>(ops + kOpO + ((w * 2 + t) * 64 + lane) * 16) = ob[t];
     bf16_fragments(vb, vf, unv);
     bf16_fragments(ob, of, uno);
+    // dO once more for the chain, with what undoes QG's scales
+    f32x4 dn;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) dn[b] = unit_scale(uniform_bits(s.top[kTopPre + b])).un;
+    f16x8 og[2];
+    float ung;
+    bf16_fragments(ob, og, ung, dn);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      *reinterpret_cast<f16x8*>(ops + kOpO + ((w * 2 + t) * 64 + lane) * 16) = og[t];
+    if (g4 == 0) reinterpret_cast<float*>(ops + kOpUnO)[kc] = ung;
   }
   __syncthreads();
   // T_IJ = -T_II sum_K A_IK T_KJ, one wave per block column

@@ -30,7 +30,7 @@ extern "C" {
 /*
  * kda_prefill_backward_workspace_size -- bytes of device workspace
  * kda_prefill_varlen_backward needs for these sizes (0 when K or V is not 128 or
- * a size is invalid). Pure host arithmetic: about 6.9 KB per token and head (per
+ * a size is invalid). Pure host arithmetic: about 7.0 KB per token and head (per
  * 64-token chunk and head: the state that enters it, the state gradient that
  * leaves it, and the chunk's operands, fp32).
  */
