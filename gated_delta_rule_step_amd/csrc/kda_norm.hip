@@ -22,9 +22,7 @@
 // reaches 5.2 TB/s.) The partial rows' sum adds 4 to 5 us.
 //
 // Rows of odd strides or widths use the same 16-byte accesses: gfx950 takes
-// unaligned vector loads and stores from global memory, and only the last,
-// partial group of 8 of a vector goes element by element. (16384 rows of 8191: 263 us
-// against 197 of 8192, both as calls; rows then share lines.)
+// unaligned vector loads and stores from global memory.
 
 #include <stdint.h>
 
@@ -36,6 +34,8 @@ namespace {
 
 typedef u32x4 u32x4_u __attribute__((aligned(1)));
 typedef u32x2 u32x2_u __attribute__((aligned(1)));
+typedef uint32_t u32_u __attribute__((aligned(1)));
+typedef uint16_t u16_u __attribute__((aligned(1)));
 
 constexpr int kOutBf16 = 0;
 constexpr int kOutFp8 = 1;       // one scale per vector
@@ -70,32 +70,59 @@ struct NormBwdParams {
   int64_t z_stride, dy_stride, gate_stride, dres_stride, dz_stride, dgate_stride;
 };
 
-// 8 channels from c on; channels past the width read as zeros.
+// 8 channels from c on, to be put right by `own8` once they are used: no lane waits behind a
+// branch, those at the end take the vector's last 8 channels. (Against a partial group read
+// channel by channel, us: 16384 rows of 2500 100.6 and 63.2, of 8191 262 and 236, their
+// gradient 259 and 179.) In place, another lane may have stored some of them by then: those
+// are the ones that are shifted out.
 __device__ __forceinline__ u32x4 load_ch8(const uint16_t* row, int c, int width) {
-  if (c + 8 <= width) return *reinterpret_cast<const u32x4_u*>(row + c);
+  if (width >= 8) return *reinterpret_cast<const u32x4_u*>(row + min(c, width - 8));
   u32x4 w = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 7; ++i)
     if (c + i < width) w[i >> 1] |= uint32_t(row[c + i]) << (16 * (i & 1));
   return w;
 }
+// Shifts out the channels of other groups; channels past the width become zeros. CAP: what
+// the lanes hold in all.
+template <int CAP>
+__device__ __forceinline__ u32x4 own8(u32x4 w, int c, int width) {
+  if (width == CAP || width < 8) return w;
+  uint64_t lo = uint64_t(w[1]) << 32 | w[0], hi = uint64_t(w[3]) << 32 | w[2];
+  const int over = -width & 7;  // channels that the last group lacks
+  if (over != 0) {
+    const bool last = c == (width & ~7);
+    const uint64_t l =
+        over < 4 ? lo >> (16 * over) | hi << (64 - 16 * over) : hi >> (16 * over - 64);
+    const uint64_t h = over < 4 ? hi >> (16 * over) : 0;
+    lo = last ? l : lo;
+    hi = last ? h : hi;
+  }
+  if (c >= width) lo = hi = 0;
+  return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+}
+// The last, partial group leaves in pieces of 4, 2 and 1.
 __device__ __forceinline__ void store_ch8(uint16_t* row, int c, int width, u32x4 w) {
   if (c + 8 <= width) {
     *reinterpret_cast<u32x4_u*>(row + c) = w;
-    return;
+  } else if (c < width) {
+    const int four = width & 4, two = width & 2;
+    if (four) *reinterpret_cast<u32x2_u*>(row + c) = u32x2{w[0], w[1]};
+    const uint32_t a = four ? w[2] : w[0], b = four ? w[3] : w[1];
+    if (two) *reinterpret_cast<u32_u*>(row + c + four) = a;
+    if (width & 1) row[c + four + two] = uint16_t(two ? b : a);
   }
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (c + i < width) row[c + i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
 }
 __device__ __forceinline__ void store_ch8(uint8_t* row, int c, int width, u32x2 w) {
   if (c + 8 <= width) {
     *reinterpret_cast<u32x2_u*>(row + c) = w;
-    return;
+  } else if (c < width) {
+    const int four = width & 4, two = width & 2;
+    if (four) *reinterpret_cast<u32_u*>(row + c) = w[0];
+    const uint32_t a = four ? w[1] : w[0];
+    if (two) *reinterpret_cast<u16_u*>(row + c + four) = uint16_t(a);
+    if (width & 1) row[c + four + two] = uint8_t(two ? a >> 16 : a);
   }
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (c + i < width) row[c + i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
 }
 // 8 weights from c on, zeros past the width.
 __device__ __forceinline__ void load_w8(const float* w, int c, int width, float (&x)[8]) {
@@ -166,6 +193,7 @@ template <int LPR, int NV, bool RES, bool GATE, int OUT>
 __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p) {
   constexpr int T = kNormThreads<LPR>;
   constexpr int VPB = T / LPR;  // vectors of a workgroup at a time
+  constexpr int CAP = LPR * NV * 8;
   __shared__ float buf[4][T / 64];
   const int lane = threadIdx.x % LPR;
   const float inv_n = 1.0f / float(p.width);
@@ -191,10 +219,10 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      unpack8_bf16(xw[j], z[j]);
+      unpack8_bf16(own8<CAP>(xw[j], (j * LPR + lane) * 8, p.width), z[j]);
       if constexpr (RES) {
         float t[8];
-        unpack8_bf16(rw[j], t);
+        unpack8_bf16(own8<CAP>(rw[j], (j * LPR + lane) * 8, p.width), t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[j][i] += t[i];
         if (p.res_out)
@@ -210,7 +238,7 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_kernel(NormParams p
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float t[8];
-      if constexpr (GATE) unpack8_bf16(gw[j], t);
+      if constexpr (GATE) unpack8_bf16(own8<CAP>(gw[j], (j * LPR + lane) * 8, p.width), t);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float y = z[j][i] * s * w[j][i];
@@ -291,6 +319,11 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_bwd_kernel(NormBwdP
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float z[8], a[8], g[8];
+      const int c = (j * LPR + lane) * 8;
+      zw[j] = own8<CAP>(zw[j], c, p.width);
+      yw[j] = own8<CAP>(yw[j], c, p.width);
+      if constexpr (GATE) gw[j] = own8<CAP>(gw[j], c, p.width);
+      if constexpr (RES) rw[j] = own8<CAP>(rw[j], c, p.width);
       unpack8_bf16(zw[j], z);
       unpack8_bf16(yw[j], a);
       if constexpr (GATE) unpack8_bf16(gw[j], g);
@@ -429,7 +462,7 @@ constexpr int64_t kNormBlocks = 2048;
 // with two per CU (8208 rows: 1024 workgroups 94.0, 512 86.5), and so do workgroups of several vectors
 // (525,312 gated heads of 128: 127 and 120); one narrow row per workgroup takes four
 // where each still walks 16 (16384 rows, with two and with four: of 1536 38.5 and 32.8, of 2500
-// 91.4 and 65.3, of 4096 78.0 and 87.1).
+// 91.4 and 65.3, of 4096 78.0 and 87.1; a partial last group was slower then).
 int64_t most_bwd_blocks(int width) { return width > 1024 && width <= 2560 ? 1024 : 512; }
 unsigned norm_bwd_blocks(int64_t vecs, int width) {
   const int64_t walk = vecs / 16;
