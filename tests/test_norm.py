@@ -293,6 +293,49 @@ def test_backward(shape, res, gated, pad, off):
     assert torch.equal(again, dwo)
 
 
+# the last group of 8 holds 1 to 7 channels, next to another head's; below 8 it is the only one
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [2, 3, 5, 6] + list(range(9, 16)) + list(range(2049, 2056)) +
+                         [8190, 16383])
+def test_partial_groups(width):
+    """Out of place, in place (the same bits) and fp8; gradients too."""
+    shape = (5, 3, width)
+    x, r, g, dy = (_rand(shape, 30 + i) for i in range(4))
+    w = 1 + 0.1 * _rand((width,), 34).float()
+    z, y = _ref(x, w, r, g, 1e-6)
+    top = y.abs().amax(-1, keepdim=True)
+    out, zo = torch.empty(shape, dtype=BF, device="cuda"), torch.empty(shape, dtype=BF, device="cuda")
+    kda.kda_rmsnorm(x.cuda(), w.cuda(), out, residual=r.cuda(), residual_out=zo, gate=g.cuda())
+    assert ((out.double().cpu() - y).abs() <= (2.0 ** -8 + 2e-5) * y.abs() + 1e-6 * top).all()
+    assert torch.equal(zo.cpu(), z.to(BF))
+    xi, ri = x.cuda(), r.cuda()
+    kda.kda_rmsnorm(xi, w.cuda(), xi, residual=ri, residual_out=ri, gate=g.cuda())
+    assert torch.equal(xi, out) and torch.equal(ri, zo)
+    o8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(5, 3, device="cuda")
+    kda.kda_rmsnorm(x.cuda(), w.cuda(), o8, residual=r.cuda(), gate=g.cuda(), scales=sc)
+    scd = sc.double().cpu()[..., None]
+    assert ((scd * 448 - top).abs() <= 2e-5 * top).all()
+    # half an e4m3 step: 2^-4 of the value, 2^-10 where the format is at its smallest
+    assert ((o8.double().cpu() * scd - y).abs() <=
+            (2.0 ** -4 + 1e-4) * y.abs() + (2.0 ** -10 + 1e-6) * scd).all()
+    dz, dw, dg = _ref_bwd(x, w, dy, g, r, 1e-6)
+    dzo, dgo = torch.empty_like(out), torch.empty_like(out)
+    dwo = torch.empty(width, device="cuda")
+    kda.kda_rmsnorm_backward(x.cuda(), w.cuda(), dy.cuda(), dzo, dwo, gate=g.cuda(), dgate=dgo,
+                             d_residual=r.cuda())
+    for got, ref in ((dzo, dz), (dgo, dg)):
+        # half a bf16 step; what cancels in dz is as large as the row's largest
+        big = (ref.abs() + r.double().abs()).amax(-1, keepdim=True)
+        assert ((got.double().cpu() - ref).abs() <= (2.0 ** -8 + 2e-5) * ref.abs() + 2e-5 * big).all()
+    mags = (dy.double().abs() * (x.double() / torch.sqrt(
+        x.double().pow(2).mean(-1, keepdim=True) + 1e-6)).abs()).sum((0, 1))
+    assert ((dwo.double().cpu() - dw).abs() <= 2e-5 * mags + 1e-12).all()
+    di, gi = dy.cuda(), g.cuda()
+    kda.kda_rmsnorm_backward(x.cuda(), w.cuda(), di, di, gate=gi, dgate=gi, d_residual=r.cuda())
+    assert torch.equal(di, dzo) and torch.equal(gi, dgo)
+
+
 @pytest.mark.gpu
 def test_backward_against_differences():
     """dz, dgate and dweight against central differences of the forward formula."""
