@@ -23,7 +23,9 @@ namespace {
 //   the same, operands to registers (few)  722 | 1199 | 2963
 //   two waves, two tiles                   884 | 1162 | 2895
 //   two waves, one tile                    844 | 1470 | 3806
-// so the first, second and fourth are taken where each is best, see launch_chains.
+// so the first, second and fourth are taken where each is best, see launch_chains. (Since
+// then dO is prepared once per chunk and rows leave in 16-byte stores: 685 | 1027 | 2553, of
+// which this kernel takes 373, 374 and 872, the last at 4.3 TB/s of operands and states.)
 //
 // The products run on fp16 MFMA, both sides split into high and low parts (three terms,
 // fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides, the state and x in
