@@ -96,7 +96,8 @@ extern "C" size_t kda_prefill_backward_workspace_size(int32_t n_docs, int64_t to
   if (n_docs < 0 || total_tokens < 0 || total_tokens > INT32_MAX || H < 1 || H > 65535 ||
       K != kda::D || V != kda::D)
     return 0;
-  return size_t(kda::bwd::slots_of(n_docs, total_tokens)) * size_t(H) * (kda::bwd::kOps + 2 * kda::D * 4);
+  return size_t(kda::bwd::slots_of(n_docs, total_tokens)) * size_t(H) *
+         (kda::bwd::kOps + 2 * kda::D * 4);
 }
 
 extern "C" kda_status kda_prefill_varlen_backward(

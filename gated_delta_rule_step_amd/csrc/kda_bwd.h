@@ -399,7 +399,8 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
 // there. The device's entry in `done` is only ever set, so calls from several threads at
 // worst allow it twice.
 constexpr int kMaxDevices = 64;
-inline hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<bool> (&done)[kMaxDevices]) {
+inline hipError_t allow_lds(const void* kernel, size_t bytes,
+                            std::atomic<bool> (&done)[kMaxDevices]) {
   int dev = -1;
   if (const hipError_t e = hipGetDevice(&dev)) return e;
   if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;

@@ -143,7 +143,8 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   const int kh = wave % KS;
   const int g4 = lane >> 4, n16 = lane & 15;
   const int v = 16 * (part * TW + wave / KS) + n16;  // this lane's value channel
-  const int at_row = (4 * g4 + (lane & 3)) * D + (v & ~3);  // after quad_transpose, in a 16-row tile
+  // where a lane's values go after quad_transpose, in a tile of 16 rows
+  const int at_row = (4 * g4 + (lane & 3)) * D + (v & ~3);
   const int k0 = 16 * NM * kh + 4 * g4;                   // its first key channel
   const int32_t t0 = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc]);
   const int32_t len = __builtin_amdgcn_readfirstlane(p.cu_seqlens[doc + 1]) - t0;
@@ -191,7 +192,7 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
   u32x4 st = {0u, 0u, 0u, 0u};
   auto tail_of = [&](int n) { return tails + (OWN ? n % 3 : n & 1) * 256; };
   auto xch_of = [&](int n) { return xch0 + (OWN ? (n & 1) * (Shape::kXch / 4) : 0); };
-  // tile A of chunk n, and of the next one a share per token block
+  // the first tile A (later ones come in shares, a token block at a time)
   auto load_a = [&](const uint8_t* src) {
     if constexpr (OWN) {
 #pragma unroll
@@ -220,7 +221,7 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
       }
     }
   };
-  // x = x0 + un * (what `product` left), rows written: the two waves of a tile add up their
+  // x = x0 + un * (what `product` left), rows written: the waves of a tile add up their
   // parts (x0 and the rows are shared between them, a part of the blocks each).
   auto exchange_out = [&](f32x4 (&x)[NB], const f32x4 (&acc)[NB], float un, f32x4 unr,
                           const f32x4 (&x0)[NX], float* xch) {
@@ -238,13 +239,15 @@ __device__ __forceinline__ void chain(const BwdParams& p, int doc, int h, bool d
       if constexpr (KS == 4)  // (pairs first: the same sum in all four)
         x[r] += lds4(xch + (((wave ^ 2) * NB + r) * 64 + lane) * 4) +
                 lds4(xch + (((wave ^ 3) * NB + r) * 64 + lane) * 4);
-      if (r / NX == kh) *reinterpret_cast<f32x4*>(rows + 16 * r * D + at_row) = quad_transpose(x[r], lane);
+      if (r / NX == kh)
+        *reinterpret_cast<f32x4*>(rows + 16 * r * D + at_row) = quad_transpose(x[r], lane);
     }
   };
   auto store_state = [&](float* rows) {
 #pragma unroll
     for (int m = 0; m < NM; ++m)
-      *reinterpret_cast<f32x4*>(rows + 16 * (NM * kh + m) * D + at_row) = quad_transpose(s[m], lane);
+      *reinterpret_cast<f32x4*>(rows + 16 * (NM * kh + m) * D + at_row) =
+          quad_transpose(s[m], lane);
   };
   // the start of x of chunk n, this wave's token blocks
   auto load_x0 = [&](f32x4 (&x0)[NX], int n, int op) {
@@ -496,14 +499,16 @@ __global__ __launch_bounds__(Wide::kThreads) void chain_kernel(BwdParams p, DocO
 hipError_t launch_chains(const BwdParams& p, const DocOrder& ord, hipStream_t stream) {
   if (blocks_of<4, 1>(p.n_docs, p.H) <= kCus) {
     static std::atomic<bool> allowed[kMaxDevices];
-    if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(chain_few_kernel), Few::kLds, allowed))
+    const void* kernel = reinterpret_cast<const void*>(chain_few_kernel);
+    if (const hipError_t e = allow_lds(kernel, Few::kLds, allowed))
       return e;
     hipLaunchKernelGGL(chain_few_kernel, dim3(unsigned(blocks_of<4, 1>(p.n_docs, p.H))),
                        dim3(Few::kThreads), Few::kLds, stream, p, ord);
     return hipGetLastError();
   }
   static std::atomic<bool> allowed[kMaxDevices];
-  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(chain_kernel), Wide::kLds, allowed))
+  const void* kernel = reinterpret_cast<const void*>(chain_kernel);
+  if (const hipError_t e = allow_lds(kernel, Wide::kLds, allowed))
     return e;
   const int64_t blocks = blocks_of<4, 2>(ord.deep, p.H) + blocks_of<2, 4>(p.n_docs - ord.deep, p.H);
   hipLaunchKernelGGL(chain_kernel, dim3(unsigned(blocks)), dim3(Wide::kThreads), Wide::kLds, stream,

@@ -59,7 +59,8 @@ __device__ __forceinline__ int perm32(int t) {
   return (t & ~31) + 8 * ((t & 15) >> 2) + 4 * ((t >> 4) & 1) + (t & 3);
 }
 
-__device__ __forceinline__ void zero_row(uint16_t* p, int64_t t, int64_t stride, int64_t at, int n) {
+__device__ __forceinline__ void zero_row(uint16_t* p, int64_t t, int64_t stride, int64_t at,
+                                         int n) {
   for (int e = threadIdx.x; e < n; e += kThreads) p[t * stride + at + e] = 0;
 }
 
@@ -588,7 +589,8 @@ template <bool PRE>
 static hipError_t launch_grad(const BwdParams& p, hipStream_t stream) {
   static_assert(sizeof(GradSmem) <= 160 * 1024, "LDS of a CU");
   static std::atomic<bool> allowed[kMaxDevices];
-  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(grad_kernel<PRE>), sizeof(GradSmem), allowed))
+  const void* kernel = reinterpret_cast<const void*>(grad_kernel<PRE>);
+  if (const hipError_t e = allow_lds(kernel, sizeof(GradSmem), allowed))
     return e;
   hipLaunchKernelGGL(grad_kernel<PRE>, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
                      sizeof(GradSmem), stream, p);

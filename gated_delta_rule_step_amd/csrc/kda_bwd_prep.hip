@@ -509,7 +509,8 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 template <bool PRE>
 static hipError_t launch_prep(const BwdParams& p, hipStream_t stream) {
   static std::atomic<bool> allowed[kMaxDevices];
-  if (const hipError_t e = allow_lds(reinterpret_cast<const void*>(prep_kernel<PRE>), sizeof(PrepSmem), allowed))
+  const void* kernel = reinterpret_cast<const void*>(prep_kernel<PRE>);
+  if (const hipError_t e = allow_lds(kernel, sizeof(PrepSmem), allowed))
     return e;
   hipLaunchKernelGGL(prep_kernel<PRE>, dim3(unsigned(p.slots), unsigned(p.H)), dim3(kThreads),
                      sizeof(PrepSmem), stream, p);

@@ -463,9 +463,9 @@ constexpr int64_t kNormBlocks = 2048;
 // A workgroup of the gradient leaves a partial row, as much traffic as a vector, so it walks
 // at least eight vectors as long as every CU has one (8192 channels, us, 512 workgroups
 // against this rule: 512 rows 22.2 and 16.2, 2048 rows 31.0 and 28.4). Wide rows fill the chip
-// with two per CU (8208 rows: 1024 workgroups 94.0, 512 86.5), and so do workgroups of several vectors
-// (525,312 gated heads of 128: 127 and 120); one narrow row per workgroup takes four
-// where each still walks 16 (16384 rows, with two and with four: of 1536 38.5 and 32.8, of 2500
+// with two per CU (8208 rows: 1024 workgroups 94.0, 512 86.5), and so do workgroups of
+// several vectors (525,312 gated heads of 128: 127 and 120); one narrow row per workgroup
+// takes four where each still walks 16 (16384 rows, with two and with four: of 1536 38.5 and 32.8, of 2500
 // 91.4 and 65.3, of 4096 78.0 and 87.1; a partial last group was slower then).
 int64_t most_bwd_blocks(int width) { return width > 1024 && width <= 2560 ? 1024 : 512; }
 unsigned norm_bwd_blocks(int64_t vecs, int width) {
