@@ -353,6 +353,27 @@ def test_no_tokens():
     assert (o["dA"] == 0).all() and (o["ddt"] == 0).all()
 
 
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """On two streams, with workspaces of their own: each gives what it gives alone."""
+    cs = [make((300, 40), H=3, seed=61, state=BF, dfinal=True), make((500,), H=20, seed=62)]
+    alone = [run(c) for c in cs]
+    ws = [torch.empty(kda.kda_prefill_backward_workspace_size(len(c["lens"]), sum(c["lens"]),
+                                                              c["H"]),
+                      dtype=torch.uint8, device="cuda") for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(3):
+        got = []
+        for c, st, w in zip(cs, streams, ws):
+            with torch.cuda.stream(st):
+                got.append(run(c, workspace=w, stream=st))
+        torch.cuda.synchronize()
+        for o, one in zip(got, alone):
+            for n, t in one.items():
+                assert t is None or torch.equal(o[n], t), n
+
+
 # the chains' forms: four long documents in the one of least latency and the rest in the
 # wide one; all in the first; all in the second; a document count that leaves blocks over
 @pytest.mark.gpu
