@@ -121,6 +121,24 @@ def _ptr(t):
     return _P(t.data_ptr()) if t is not None else _P(0)
 
 
+def _workspace(need, dev, stream):
+    """A workspace for one call on `stream` (None: dev's current one), from that
+    stream's memory pool: it is ordered behind the stream's earlier work, and whatever
+    gets the block after the call behind the call's kernels. A block of the current
+    stream's pool could be handed out again while another stream's kernels use it."""
+    import torch
+    if need == 0:
+        return None
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
 def _bf16(name, t, last_contig=True):
     import torch
     if t.dtype != torch.bfloat16:
@@ -268,15 +286,13 @@ def kda_prefill_varlen(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, beta_raw, A_
     [N, H, R, 128]) with cache_base int32 [n_docs] and ring_tail in 1..16: each
     document hands its last prefill_handoff_hist(...)[d] tokens to the ring at
     rows cache_base[d] onwards, and its slot receives the state before them."""
-    import torch
     args = _prefill_args(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, beta_raw, A_log, dt_bias,
                          state_pool, state_indices, out, use_initial_state, lower_bound, scale,
                          gate_mode, checkpoints, checkpoint_cu_starts, checkpoint_interval, ring,
                          cache_base, ring_tail)
     if workspace is None:
         need = kda_prefill_workspace_size(args[0], args[1], args[2])
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().kda_prefill_varlen(*args, _ptr(workspace), ws_bytes, _stream(stream))
     _check("kda_prefill_varlen", st)
@@ -464,9 +480,7 @@ def kda_prefill_varlen_backward(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, bet
                            ("d_final_state", d_final_state),
                            ("d_initial_state", d_initial_state), ("workspace", workspace)))
     if workspace is None:
-        need = kda_prefill_backward_workspace_size(n_docs, T, H)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _workspace(kda_prefill_backward_workspace_size(n_docs, T, H), dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch("kda_prefill_varlen_backward", dev, stream,
             n_docs, T, H, HEAD_DIM, HEAD_DIM, cu_seqlens_host.data_ptr(), _adr(cu_seqlens),
@@ -564,7 +578,6 @@ def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None,
     d_residual, the gradient that reaches z past the norm. workspace: uint8 GPU
     tensor of >= kda_rmsnorm_backward_workspace_size(...) bytes, or None to have
     one allocated here for this call."""
-    import torch
     rows, heads, width = _norm_sizes("z", z)
     zs = _vectors("z", z, rows, heads, width)
     ys = _vectors("dy", dy, rows, heads, width)
@@ -579,8 +592,8 @@ def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None,
                            ("gate", gate), ("dgate", dgate), ("d_residual", d_residual),
                            ("workspace", workspace)))
     if workspace is None and dweight is not None and rows > 0:
-        need = kda_rmsnorm_backward_workspace_size(rows, heads, width)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _workspace(kda_rmsnorm_backward_workspace_size(rows, heads, width), dev,
+                               stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch("kda_rmsnorm_backward", dev, stream, rows, heads, width, _adr(z), zs, _adr(dy), ys,
             _adr(gate), gs, _adr(d_residual), rs, _adr(weight), float(eps), _adr(dz), ds,
