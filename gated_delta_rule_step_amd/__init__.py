@@ -139,6 +139,16 @@ def _workspace(need, dev, stream):
         return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
+def _workspace_bytes(t, dev):
+    """The size of a workspace (None: 0): contiguous, so that it holds as many bytes as it
+    has elements, and where the kernels run."""
+    if t is None:
+        return 0
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous GPU tensor on {dev}")
+    return t.numel() * t.element_size()
+
+
 def _bf16(name, t, last_contig=True):
     import torch
     if t.dtype != torch.bfloat16:
@@ -293,7 +303,7 @@ def kda_prefill_varlen(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, beta_raw, A_
     if workspace is None:
         need = kda_prefill_workspace_size(args[0], args[1], args[2])
         workspace = _workspace(need, q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, q.device)
     st = lib().kda_prefill_varlen(*args, _ptr(workspace), ws_bytes, _stream(stream))
     _check("kda_prefill_varlen", st)
 
@@ -481,7 +491,7 @@ def kda_prefill_varlen_backward(cu_seqlens_host, cu_seqlens, q, k, v, g_raw, bet
                            ("d_initial_state", d_initial_state), ("workspace", workspace)))
     if workspace is None:
         workspace = _workspace(kda_prefill_backward_workspace_size(n_docs, T, H), dev, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     _launch("kda_prefill_varlen_backward", dev, stream,
             n_docs, T, H, HEAD_DIM, HEAD_DIM, cu_seqlens_host.data_ptr(), _adr(cu_seqlens),
             _adr(q), q.stride(0), _adr(k), k.stride(0), _adr(v), v.stride(0),
@@ -594,7 +604,7 @@ def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None,
     if workspace is None and dweight is not None and rows > 0:
         workspace = _workspace(kda_rmsnorm_backward_workspace_size(rows, heads, width), dev,
                                stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(workspace, dev)
     _launch("kda_rmsnorm_backward", dev, stream, rows, heads, width, _adr(z), zs, _adr(dy), ys,
             _adr(gate), gs, _adr(d_residual), rs, _adr(weight), float(eps), _adr(dz), ds,
             _adr(dgate), dgs, _adr(dweight), _adr(workspace), ws_bytes)

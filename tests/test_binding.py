@@ -1,4 +1,5 @@
-"""The Python binding's own work around the C calls: where a workspace comes from.
+"""The Python binding's own work around the C calls: where a workspace comes from, and
+which one it takes.
 
 On the CPU the library, the allocator and the streams are stand-ins that note what they
 are asked for; the GPU tests run the real ones.
@@ -139,6 +140,28 @@ def test_workspace_of_another_device_stream(fake, name):
     with pytest.raises(ValueError, match="stream"):
         call(name, Gpu, stream=Stream(0x200, torch.device("cuda", 1)))
     assert not lib.seen and not made
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("bad", [
+    Gpu(torch.zeros(1, dtype=torch.uint8).expand(1 << 20)),       # one byte
+    Gpu(torch.zeros(1 << 12, dtype=torch.uint8)[::2]),
+    torch.zeros(1 << 12, dtype=torch.uint8)], ids=["expanded", "every other byte", "on the CPU"])
+def test_workspace_refused(fake, name, bad):
+    """Memory that holds fewer bytes than its elements would take, or that the kernels
+    cannot reach."""
+    lib, _ = fake
+    with pytest.raises(ValueError, match="workspace"):
+        call(name, Gpu, workspace=bad)
+    assert not lib.seen
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_workspace_of_the_caller(fake, name):
+    lib, made = fake
+    ws = Gpu(torch.zeros(8, 512, dtype=torch.float32))
+    call(name, Gpu, workspace=ws)
+    assert lib.seen == [(name, CURRENT, ws.data_ptr())] and not made
 
 
 # ---------------------------------------------------------------------------
