@@ -332,6 +332,15 @@ __device__ __forceinline__ void load_lane(const BwdParams& p, const Chunk& ch, i
 // block's two halves.
 __device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
 
+// log(1 + e) for e >= 0. The sum 1 + e is rounded by up to 2^-24, which is half of e itself
+// where the gates of a slowly decaying head lie (e of 1e-7), so small e take four terms of the
+// series: below 1/32 they leave out 2e-7 of the result, and above it the rounding is at most
+// 2e-6 of it. dA_log, a sum of gates, needs that, and so do decays over many like tokens.
+__device__ __forceinline__ float log1p_of(float e) {
+  const float series = e * fmaf(-e, fmaf(-e, fmaf(-e, 0.25f, 1.f / 3.f), 0.5f), 1.f);
+  return e < 1.f / 32.f ? series : LN2 * __builtin_amdgcn_logf(1.0f + e);
+}
+
 struct Lane {
   float k[NB][4], q[NB][4];  // k_hat, q_hat
   float up[NB][4];
@@ -366,7 +375,7 @@ __device__ __forceinline__ void make_lane(const BwdParams& p, const Chunk& ch, i
         // kept finite: log(1 + e^y) is y long before
         const float y = x + dtb;
         const float e = fexp(fminf(y, 80.f));
-        const float gu = -ea * fmaxf(y, LN2 * __builtin_amdgcn_logf(1.0f + e));
+        const float gu = -ea * fmaxf(y, log1p_of(e));
         g = fmaxf(gu, p.lower_bound);
         if (SLOPE) s = gu >= p.lower_bound ? -ea * (e * __builtin_amdgcn_rcpf(1.0f + e)) : 0.f;
       }

@@ -588,3 +588,47 @@ def test_binding_refuses():
     c = make((10,), H=2, seed=1)
     with pytest.raises(kda.KdaError):
         run(c, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+# gate logits plus bias of a trained or freshly initialised layer: decays of 1e-1 to 1e-8
+@pytest.mark.gpu
+@pytest.mark.parametrize("bias,A", [(-2.0, 2.7), (-4.0, 0.0), (-7.0, 0.0), (-9.0, 2.7), (-12.0, 0.0),
+                                    (-15.0, 2.7), (-18.0, 0.0), (-40.0, 0.0)])
+@pytest.mark.parametrize("gate,alike", [(0, False), (0, True), (HEAD, False)],
+                         ids=["spread", "alike", "per head"])
+def test_slow_decay(bias, A, gate, alike):
+    """Raw gates whose softplus is small: dA_log is the sum of dg g, so the log-decay itself has
+    to be right relative to its size. `alike`: one logit for all tokens, whose rounding errors
+    add up.
+
+    Tolerances: those of the other cases, and what 300 tokens add to a decay that is nearly 1:
+    each a_t = e^g_t is off by 2^-24 (one step below 1), the product of the decays by half of
+    that again, in the same direction where the tokens are alike, so a weight is off by
+    300 * 1.5 * 2^-24 = 2.7e-5. The softplus adds nothing to speak of: the exponential's
+    argument is rounded twice, 2 * 2^-24 |y| < 5e-6 of it at y = -40."""
+    c = make((300, 65), H=2, gate=gate, seed=70, state=BF, dfinal=True)
+    c["dt"] += bias
+    c["A"] += A
+    if alike:
+        c["g"][:] = c["g"][0]
+    o = run(c)
+    torch.cuda.synchronize()
+    (*rows, dA, ddt), dS = reference(c)
+    far, H = 300 * 1.5 * 2.0 ** -24, c["H"]
+    t = 0
+    for n in c["lens"]:
+        for name, r in zip(("dq", "dk", "dv", "dg", "db"), rows):
+            got = o[name][t:t + n].double().cpu().reshape(n, H, -1)
+            ref = r[t:t + n].reshape(n, H, -1)
+            top = ref.abs().amax((0, 2), keepdim=True)
+            assert ((got - ref).abs() <= 2.0 ** -8 * ref.abs() + (1e-4 + far) * top).all(), name
+        t += n
+    x = c["g"].double() + c["dt"].double()
+    terms = rows[3].reshape(-1, H, x.shape[1] // H)
+    mag = terms.abs().sum(0).reshape(-1)
+    assert ((o["ddt"].double().cpu() - ddt).abs() <= (2e-5 + far) * mag).all()
+    ratio = (torch.log1p(torch.exp(x)) / torch.sigmoid(x)).reshape(terms.shape)
+    mag = (terms * ratio).abs().sum((0, 2))
+    assert ((o["dA"].double().cpu() - dA).abs() <= (2e-5 + far) * mag).all()
+    top = dS.abs().amax((2, 3), keepdim=True)
+    assert ((o["dS"].double().cpu() - dS).abs() <= (1e-5 + far) * top).all()
