@@ -24,6 +24,7 @@
 // Rows of odd strides or widths use the same 16-byte accesses: gfx950 takes
 // unaligned vector loads and stores from global memory.
 
+#include <float.h>
 #include <stdint.h>
 
 #include "../../include/kda_norm.h"
@@ -152,6 +153,13 @@ __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d)
 // as much as by HBM, and a division takes ten of them.
 __device__ __forceinline__ float sigmoid_rcp(float x) {
   return __builtin_amdgcn_rcpf(1.0f + fexp(-x));
+}
+// The sigmoid and what it lacks of 1, e^-x times it: 1 - sig would leave nothing of it where
+// x is large. (e^-x is kept finite: where it would overflow, the sigmoid is 0.)
+__device__ __forceinline__ void sigmoid_both(float x, float& sig, float& rest) {
+  const float e = fexp(-x);
+  sig = __builtin_amdgcn_rcpf(1.0f + e);
+  rest = fminf(e, FLT_MAX) * sig;
 }
 
 __device__ __forceinline__ float row16_max(float x) {
@@ -354,9 +362,10 @@ __global__ __launch_bounds__(kNormThreads<LPR>) void rmsnorm_bwd_kernel(NormBwdP
         const float n = z[i] * s;
         float d = y[i];
         if constexpr (GATE) {
-          const float sig = sigmoid_rcp(g[i]);
+          float sig, rest;
+          sigmoid_both(g[i], sig, rest);
           d *= sig;
-          g[i] = d * (1.0f - sig) * n * w[j][i];
+          g[i] = d * rest * n * w[j][i];
         }
         dw[j][i] = fmaf(d, n, dw[j][i]);
         y[i] = s * fmaf(-m, z[i], d * w[j][i]);

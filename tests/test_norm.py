@@ -409,3 +409,52 @@ def test_captured_and_on_another_stream():
         for a, b in zip(captured, eager):
             assert np.array_equal(a.view(torch.uint8).cpu().numpy(),
                                   b.view(torch.uint8).cpu().numpy())
+
+
+# gate logits from where the sigmoid is 1e-13 to where 1 - sigmoid is; each vector holds one
+# size of them, so that no other element sets its scale
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,width", [(3, 128), (1, 1001), (1, 2048)])
+def test_backward_of_saturated_gates(heads, width):
+    """dgate = dy n w sig (1 - sig), each element to half a bf16 step and the fp32 arithmetic:
+    the exponential's argument is rounded to 2^-24 of itself, twice, so sig and 1 - sig are off
+    by 2 * 2^-24 * 30 = 4e-6 at a logit of 30, and the other factors by a few roundings and
+    the norm's 4e-6: 2e-5 covers it."""
+    logits = torch.arange(-30.0, 31.0)
+    shape = (len(logits), heads, width)
+    z, dy, w = _rand(shape, 70), _rand(shape, 71), 1 + 0.1 * _rand((width,), 72).float()
+    g = (logits[:, None, None] + 0.5 * _rand(shape, 73).float().clamp(-1, 1)).to(BF)
+    dz, dw, _ = _ref_bwd(z, w, dy, g, None, 1e-6)
+    x = g.double()
+    n = z.double() / torch.sqrt(z.double().pow(2).mean(-1, keepdim=True) + 1e-6)
+    dg = dy.double() * n * w.double() * torch.sigmoid(x) * torch.sigmoid(-x)
+    dzo, dgo = (torch.empty(shape, dtype=BF, device="cuda") for _ in range(2))
+    kda.kda_rmsnorm_backward(z.cuda(), w.cuda(), dy.cuda(), dzo, gate=g.cuda(), dgate=dgo)
+    assert ((dgo.double().cpu() - dg).abs() <= (2.0 ** -8 + 2e-5) * dg.abs()).all()
+    s = 1 / torch.sqrt(z.double().pow(2).mean(-1, keepdim=True) + 1e-6)
+    big = (s * (dy.double() * w.double() * torch.sigmoid(g.double())).abs()).amax(-1, keepdim=True)
+    assert ((dzo.double().cpu() - dz).abs() <= 2.0 ** -8 * dz.abs() + 2e-5 * big).all()
+
+
+@pytest.mark.gpu
+def test_backward_of_infinite_gates():
+    """A gate of -inf or +inf, or one whose exponential overflows: sigmoid 0 or 1, no gradient
+    at the gate, and nothing else disturbed."""
+    shape = (4, 1, 256)
+    z, dy, w = _rand(shape, 74), _rand(shape, 75), torch.ones(256)
+    g = _rand(shape, 76)
+    for i, x in enumerate((float("-inf"), float("inf"), -200.0, 200.0)):
+        g[i, 0, ::3] = x
+    dzo, dgo = (torch.empty(shape, dtype=BF, device="cuda") for _ in range(2))
+    kda.kda_rmsnorm_backward(z.cuda(), w.cuda(), dy.cuda(), dzo, gate=g.cuda(), dgate=dgo)
+    sig = torch.sigmoid(g.double())
+    s = 1 / torch.sqrt(z.double().pow(2).mean(-1, keepdim=True) + 1e-6)
+    n, a = z.double() * s, dy.double() * sig
+    dz = s * (a - n * (a * n).mean(-1, keepdim=True))
+    dg = dy.double() * n * sig * (1 - sig)
+    dg[:, 0, ::3] = 0  # (e^-200 is 1e-87, below every bf16)
+    got = dgo.double().cpu()
+    assert (got[:, 0, ::3] == 0).all()
+    assert ((got - dg).abs() <= (2.0 ** -8 + 2e-5) * dg.abs()).all()
+    big = (s * a.abs()).amax(-1, keepdim=True)
+    assert ((dzo.double().cpu() - dz).abs() <= 2.0 ** -8 * dz.abs() + 2e-5 * big).all()
