@@ -2,6 +2,7 @@
 // kernels (gfx950). The method is described in kda_backward.hip.
 #pragma once
 
+#include <float.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -259,9 +260,12 @@ __device__ __forceinline__ Rows rows_of(const uint16_t* x, const Chunk& ch, int6
 // load behind a branch would be waited for one at a time.
 
 // 1 / |q|, 1 / |k| (with the epsilon) and beta of the chunk's tokens, to LDS: 16
-// lanes per token. Padding rows get zeros.
+// lanes per token. Padding rows get zeros. With SLOPE, beta's derivative by its input too: of a
+// logit, beta (1 - beta) with 1 - beta as e^-x beta, which does not cancel near 1 (e^-x kept
+// finite: where it would overflow, beta is 0).
+template <bool SLOPE>
 __device__ __forceinline__ void token_scalars(const BwdParams& p, const Chunk& ch, int h,
-                                              float* rq, float* rk, float* beta) {
+                                              float* rq, float* rk, float* beta, float* slope) {
   constexpr int N = C / (kThreads / 16);
   const int c0 = (threadIdx.x & 15) * 8;
   const Rows qr = rows_of(p.q, ch, p.q_stride, int64_t(h) * D);
@@ -289,8 +293,13 @@ __device__ __forceinline__ void token_scalars(const BwdParams& p, const Chunk& c
     sq = row16_sum(sq);
     sk = row16_sum(sk);
     if ((threadIdx.x & 15) == 0) {
-      float b = bf1(bw[j]);
-      if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) b = sigmoidf(b);
+      float b = bf1(bw[j]), by = 1.0f;
+      if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) {
+        const float e = expf(-b);
+        b = 1.0f / (1.0f + e);
+        by = fminf(e, FLT_MAX) * b * b;
+      }
+      if constexpr (SLOPE) slope[t] = by;
       rq[t] = t < ch.c ? 1.0f / sqrtf(sq + kL2Eps) : 0.f;
       rk[t] = t < ch.c ? 1.0f / sqrtf(sk + kL2Eps) : 0.f;
       beta[t] = t < ch.c ? b : 0.f;

@@ -44,6 +44,7 @@ struct GradSmem {
   float top[3][8];
   alignas(16) float beta[C];
   alignas(16) float rq[C], rk[C];
+  float slope[C];  // beta's derivative by its input
 };
 // In the place of dO, dV and x once they are read out: sums over a wave's 16 channels per
 // token, and every lane's log-decays and gate slopes.
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
     xv[j] = lds4(reinterpret_cast<const float*>(ops + kOpX) + t * D + c0);
     dv[j] = lds4(reinterpret_cast<const float*>(ops + kOpDV) + t * D + c0);
   }
-  token_scalars(p, ch, h, s.rq, s.rk, s.beta);
+  token_scalars<true>(p, ch, h, s.rq, s.rk, s.beta, s.slope);
   // rows of S and dS: a key's values by the four lanes that share it, in perm32 order
   f32x4 Sv[8], dSv[8];
   {
@@ -502,10 +503,8 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(BwdParams p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x += sr.red[which][i][t];
       sr.red[which][0][t] = x;
-      if (which == 2 && t < ch.c) {
-        if (!(p.gate_mode & KDA_BETA_PRESIGMOID)) x *= s.beta[t] * (1.f - s.beta[t]);
-        p.dbeta[(ch.t0 + t) * p.dbeta_stride + h] = to_bf16(x);
-      }
+      if (which == 2 && t < ch.c)
+        p.dbeta[(ch.t0 + t) * p.dbeta_stride + h] = to_bf16(x * s.slope[t]);
     }
   }
   __syncthreads();

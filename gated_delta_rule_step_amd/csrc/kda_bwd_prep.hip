@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kThreads, 4) void prep_kernel(BwdParams p) {
 
   RawLane raw;
   load_lane(p, ch, h, kc, g4, raw);
-  token_scalars(p, ch, h, s.rq, s.rk, s.beta);
+  token_scalars<false>(p, ch, h, s.rq, s.rk, s.beta, nullptr);
   if (threadIdx.x < 4 * NB + 1 + kBlocks) s.top[threadIdx.x] = 0;
   __syncthreads();
   if (threadIdx.x < C) tail[kTailBeta + threadIdx.x] = s.beta[threadIdx.x];

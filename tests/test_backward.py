@@ -632,3 +632,22 @@ def test_slow_decay(bias, A, gate, alike):
     assert ((o["dA"].double().cpu() - dA).abs() <= (2e-5 + far) * mag).all()
     top = dS.abs().amax((2, 3), keepdim=True)
     assert ((o["dS"].double().cpu() - dS).abs() <= (1e-5 + far) * top).all()
+
+
+@pytest.mark.gpu
+def test_saturated_beta():
+    """Beta logits of -30 .. 30, dbeta to half a bf16 step of each element and 1e-4 of the
+    largest derivative by beta itself times the sigmoid's slope: beta (1 - beta) does not
+    cancel, its exponential is off by 2 * 2^-24 * 30 = 4e-6 of it."""
+    c = make((61, 61), H=2, seed=71, scale=D ** -0.5)
+    c["b"] = (torch.arange(-30.0, 31.0).repeat(2)[:, None] + torch.tensor([0.0, 0.3])).to(BF)
+    o = run(c)
+    torch.cuda.synchronize()
+    got = o["db"].double().cpu()
+    # the derivative by beta, with beta as given (to 64 bits), times the slope
+    x = c["b"].double()
+    p = dict(c, gate=PRESIG, b=torch.sigmoid(x))
+    by_beta = reference(p)[0][4].reshape(x.shape)
+    slope = torch.sigmoid(x) * torch.sigmoid(-x)
+    top = torch.cat([t.abs().amax(0).expand(61, 2) for t in by_beta.split(61)])
+    assert ((got - by_beta * slope).abs() <= (2.0 ** -8 * by_beta.abs() + 1e-4 * top) * slope).all()
