@@ -75,7 +75,7 @@ hipError_t launch_backward(const BwdParams& p, int64_t total_tokens, const int32
   }
   if (total_tokens > 0)
     if (const hipError_t e = launch_prep(p, stream)) return e;
-  if (total_tokens > 0 || p.d_initial)
+  if (p.n_docs > 0 && (total_tokens > 0 || p.d_initial))
     if (const hipError_t e = launch_chains(p, ord, stream)) return e;
   if (total_tokens > 0)
     if (const hipError_t e = launch_grads(p, stream)) return e;

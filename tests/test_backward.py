@@ -651,3 +651,22 @@ def test_saturated_beta():
     slope = torch.sigmoid(x) * torch.sigmoid(-x)
     top = torch.cat([t.abs().amax(0).expand(61, 2) for t in by_beta.split(61)])
     assert ((got - by_beta * slope).abs() <= (2.0 ** -8 * by_beta.abs() + 1e-4 * top) * slope).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [1, 40])
+def test_no_documents(H):
+    """No documents at all: dA_log and ddt_bias become zeros, whatever else is given."""
+    lib = kda.lib()
+    dA, ddt = torch.full((H,), 7.0, device="cuda"), torch.full((H * D,), 7.0, device="cuda")
+    di = torch.full((4,), 7.0, device="cuda")
+    assert di.data_ptr() % 16 == 0
+    args = dict(n=0, T=0, H=H, cu=(0,), da=dA.data_ptr(), dd=ddt.data_ptr(), ss=H * 16384,
+                s=(H * D,) * 4 + (H,), os=(H * D,) * 4 + (H,), dos=H * D)
+    for d_initial in (di.data_ptr(), 0):
+        dA.fill_(7.0)
+        ddt.fill_(7.0)
+        assert _call(lib, di=d_initial, **args) == OK
+        torch.cuda.synchronize()
+        assert (dA == 0).all() and (ddt == 0).all() and (di == 7.0).all()
+    assert _call(lib, **dict(args, da=0, dd=0, di=di.data_ptr())) == OK
