@@ -670,3 +670,21 @@ def test_no_documents(H):
         torch.cuda.synchronize()
         assert (dA == 0).all() and (ddt == 0).all() and (di == 7.0).all()
     assert _call(lib, **dict(args, da=0, dd=0, di=di.data_ptr())) == OK
+
+
+@pytest.mark.gpu
+def test_state_gradients_in_one_tensor():
+    """d_initial_state may be d_final_state itself: documents of no tokens, one, several
+    chunks, an inactive one, in each of the chains' forms."""
+    for lens, H in (((70, 0, 1, 33), 2), ((130, 66, 1, 0), 20)):
+        c = make(lens, H=H, seed=72, state=BF, dfinal=True, idx=(1, 0, 3, -1))
+        apart = run(c)["dS"]
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+        x = {n: c[n].cuda() for n in ("q", "k", "v", "g", "b", "do", "A", "dt", "pool", "idx")}
+        o = [torch.empty_like(x[n]) for n in ("q", "k", "v", "g", "b")]
+        both = c["df"].cuda()
+        kda.kda_prefill_varlen_backward(
+            cu, cu.cuda(), x["q"], x["k"], x["v"], x["g"], x["b"], x["A"], x["dt"], x["pool"],
+            x["idx"], x["do"], *o, d_final_state=both, d_initial_state=both, scale=c["scale"])
+        torch.cuda.synchronize()
+        assert torch.equal(both, apart)

@@ -458,3 +458,92 @@ def test_backward_of_infinite_gates():
     assert ((got - dg).abs() <= (2.0 ** -8 + 2e-5) * dg.abs()).all()
     big = (s * a.abs()).amax(-1, keepdim=True)
     assert ((dzo.double().cpu() - dz).abs() <= 2.0 ** -8 * dz.abs() + 2e-5 * big).all()
+
+
+# more than 512 vectors, where fewer lanes hold each: on both sides of every shape's border, with
+# whole and partial last groups, and enough rows that workgroups walk (the gradient's from 513
+# vectors on; the forward's from 2049 on where one vector fills a workgroup, so that with 4200
+# some take a third)
+MANY = [(512, 1, 1024), (513, 1, 513), (513, 1, 1001), (4200, 1, 1024), (700, 3, 640),
+        (513, 1, 1025), (4200, 1, 2048), (513, 1, 2049), (4200, 1, 3000), (700, 2, 4096),
+        (512, 1, 8192), (513, 1, 4097), (4200, 1, 8192), (600, 1, 8191), (513, 1, 8193),
+        (2100, 1, 16384), (520, 1, 16383), (515, 1, 12160)]
+
+
+def _gpu(shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(BF)
+
+
+def _padded(t, pad):
+    """A copy with `pad` more elements between the rows (and so off 16 bytes)."""
+    rows, n = t.shape[0], t[0].numel()
+    buf = torch.full((rows, n + pad), -7.0, dtype=t.dtype, device="cuda")
+    v = buf.as_strided(t.shape, (n + pad,) + tuple(t.stride()[1:]))
+    v.copy_(t)
+    return v, buf[:, n:]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", MANY, ids=str)
+@pytest.mark.parametrize("gated,pad", [(False, 0), (True, 3)])
+def test_forward_of_many_rows(shape, gated, pad):
+    """bf16 out of place and in place (the same bits), fp8 with a scale per vector and per
+    group; the tolerances of the other tests."""
+    rows, heads, width = shape
+    x, r, w = _gpu(shape, 80), _gpu(shape, 81, 2.0), 1 + 0.1 * _gpu((width,), 82).float()
+    g = _gpu(shape, 83) if gated else None
+    z, y = _ref(x, w, r, g, 1e-6)
+    top = y.abs().amax(-1, keepdim=True)
+    (xp, _), (rp, _), (out, gap), (zo, zgap) = (_padded(t, pad) for t in (x, r, x * 0, x * 0))
+    gp = _padded(g, pad)[0] if gated else None
+    kda.kda_rmsnorm(xp, w, out, residual=rp, residual_out=zo, gate=gp)
+    assert ((out.double() - y).abs() <= (2.0 ** -8 + 2e-5) * y.abs() + 1e-6 * top).all()
+    assert torch.equal(zo, z.to(BF))
+    assert (gap == -7.0).all() and (zgap == -7.0).all()
+    kda.kda_rmsnorm(xp, w, xp, residual=rp, residual_out=rp, gate=gp)
+    assert torch.equal(xp, out) and torch.equal(rp, zo)
+    for group in (width, 128):
+        if width % group:
+            continue
+        o8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device="cuda")
+        sc = torch.empty(rows, heads * width // group, device="cuda")
+        kda.kda_rmsnorm(x, w, o8, residual=r, gate=g, scales=sc)
+        yg = y.reshape(rows, -1, group)
+        scd, most = sc.double()[..., None], yg.abs().amax(-1, keepdim=True)
+        assert ((scd * 448 - most).abs() <= 2e-5 * most).all()
+        assert ((o8.double().reshape(yg.shape) * scd - yg).abs() <=
+                (2.0 ** -4 + 1e-4) * yg.abs() + (2.0 ** -10 + 1e-6) * scd).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", MANY, ids=str)
+@pytest.mark.parametrize("res,gated,pad", [(True, False, 0), (False, True, 3)])
+def test_backward_of_many_rows(shape, res, gated, pad):
+    rows, heads, width = shape
+    z, dy, w = _gpu(shape, 84), _gpu(shape, 85), 1 + 0.1 * _gpu((width,), 86).float()
+    r = _gpu(shape, 87) if res else None
+    g = _gpu(shape, 88) if gated else None
+    dz, dw, dg = _ref_bwd(z, w, dy, g, r, 1e-6)
+    (zp, _), (dp, _), (out, gap) = (_padded(t, pad) for t in (z, dy, z * 0))
+    kw = dict(gate=_padded(g, pad)[0] if gated else None, d_residual=r)
+    dgo = _padded(z, pad)[0] if gated else None
+    dwo = torch.empty(width, device="cuda")
+    kda.kda_rmsnorm_backward(zp, w, dp, out, dwo, dgate=dgo, **kw)
+    assert (gap == -7.0).all()
+    s = 1 / torch.sqrt(z.double().pow(2).mean(-1, keepdim=True) + 1e-6)
+    big = (s * (dy.double() * w.double()).abs()).amax(-1, keepdim=True)
+    if res:
+        big = big + r.double().abs().amax(-1, keepdim=True)
+    assert ((out.double() - dz).abs() <= 2.0 ** -8 * dz.abs() + 2e-5 * big).all()
+    if gated:
+        assert ((dgo.double() - dg).abs() <= (2.0 ** -8 + 2e-5) * dg.abs()).all()
+    mags = (dy.double() * z.double() * s).abs().sum((0, 1))
+    assert ((dwo.double() - dw).abs() <= 2e-5 * mags + 1e-12).all()
+    again, ws = torch.empty_like(dwo), torch.full(
+        (kda.kda_rmsnorm_backward_workspace_size(rows, heads, width),), 255, dtype=torch.uint8,
+        device="cuda")
+    gi = kw.pop("gate")
+    kda.kda_rmsnorm_backward(zp, w, dp, dp, again, gate=gi, dgate=gi, workspace=ws, **kw)
+    assert torch.equal(again, dwo) and torch.equal(dp, out)  # in place
+    assert gi is None or torch.equal(gi, dgo)
