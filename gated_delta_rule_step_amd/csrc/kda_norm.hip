@@ -435,9 +435,11 @@ __global__ __launch_bounds__(1024) void reduce_partials(const float* partial, in
 
 // The lanes and groups of 8 that hold a vector: the narrowest shape that covers its
 // width, or, where there are too few vectors to fill the chip (up to two per CU), the one
-// with the most lanes, so that a vector's loads are all in flight at once. (8192 channels, us,
-// most lanes against fewer; 1 row 3.1 and 3.6, 512 rows 6.1 and 6.5, their gradient 22.3 and
-// 24.5; 1024 rows 12.3 and 12.0, their gradient 27.6 and 24.3.)
+// with the most lanes, so that a vector's loads are all in flight at once. One border for the
+// norm and its gradient (8192 channels, residual, operands in cache, us, most lanes against fewer:
+// 16 rows 3.6 and 3.9, 256 rows 4.7 and 4.9, 512 rows 6.9 and 6.6, 1024 rows 13.2 and 11.9; their
+// gradient 9.1 and 9.6, 15.0 and 15.3, 16.5 and 17.6, 21.7 and 22.9; 512 rows of 1000 channels 3.5
+// and 3.7, 7.6 and 6.4).
 constexpr int64_t kFewVecs = 512;
 #define KDA_NORM_SHAPES(F)                        \
   if (width == 128) return F(16, 1, 128);         \
@@ -470,13 +472,17 @@ unsigned norm_blocks(int64_t vecs, int width, int64_t most) {
 }
 constexpr int64_t kNormBlocks = 2048;
 // A workgroup of the gradient leaves a partial row, as much traffic as a vector, so it walks
-// at least eight vectors as long as every CU has one (8192 channels, us, 512 workgroups
-// against this rule: 512 rows 22.2 and 16.2, 2048 rows 31.0 and 28.4). Wide rows fill the chip
-// with two per CU (8208 rows: 1024 workgroups 94.0, 512 86.5), and so do workgroups of
-// several vectors (525,312 gated heads of 128: 127 and 120); one narrow row per workgroup
-// takes four where each still walks 16 (16384 rows, with two and with four: of 1536 38.5 and 32.8, of 2500
-// 91.4 and 65.3, of 4096 78.0 and 87.1; a partial last group was slower then).
-int64_t most_bwd_blocks(int width) { return width > 1024 && width <= 2560 ? 1024 : 512; }
+// at least eight vectors as long as every CU has one (8192 channels with d_residual and the
+// weights' sums, us, 512 workgroups against this rule: 512 rows 23.9 and 16.9, 1024 rows 26.3 and
+// 23.6, 2048 rows equal; 256 against it: 4096 rows 59.3 and 53.5). Wide rows fill the chip with
+// two per CU (8208 rows: 1024 workgroups 122.6, 512 112.0), and so do workgroups of several
+// vectors (525,312 gated heads of 128: 133.4 and 124.8). One narrow row per workgroup takes
+// four where each still walks 16, up to the width where they meet (without d_residual, two and
+// four per CU, 16384 rows | 65536 rows: 1536 channels 41.2 and 33.4 | 183 and 119, 2048 41.3 and
+// 38.6 | 187 and 153, 2816 66.3 and 58.2 | 242 and 220, 3000 70.5 and 61.2 | 248 and 238, 3200 69.9
+// and 65.7 | 249 and 248, 3328 70.7 and 72.3 | 252 and 259, 4096 76.1 and 88.2 | 281 and 323). With
+// 9000 rows, a few more workgroups than two per CU, four take 1 to 5 % more.
+int64_t most_bwd_blocks(int width) { return width > 1024 && width <= 3200 ? 1024 : 512; }
 unsigned norm_bwd_blocks(int64_t vecs, int width) {
   const int64_t walk = vecs / 16;
   int64_t most = vecs / 8 < 256 ? 256 : vecs / 8 > 512 ? 512 : vecs / 8;

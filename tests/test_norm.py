@@ -467,7 +467,9 @@ def test_backward_of_infinite_gates():
 MANY = [(512, 1, 1024), (513, 1, 513), (513, 1, 1001), (4200, 1, 1024), (700, 3, 640),
         (513, 1, 1025), (4200, 1, 2048), (513, 1, 2049), (4200, 1, 3000), (700, 2, 4096),
         (512, 1, 8192), (513, 1, 4097), (4200, 1, 8192), (600, 1, 8191), (513, 1, 8193),
-        (2100, 1, 16384), (520, 1, 16383), (515, 1, 12160)]
+        (2100, 1, 16384), (520, 1, 16383), (515, 1, 12160),
+        # where the gradient takes more than two workgroups per CU, and its borders
+        (16391, 1, 1536), (9001, 1, 2816), (16400, 1, 3200), (8500, 1, 3201)]
 
 
 def _gpu(shape, seed, scale=1.0):
@@ -482,6 +484,13 @@ def _padded(t, pad):
     v = buf.as_strided(t.shape, (n + pad,) + tuple(t.stride()[1:]))
     v.copy_(t)
     return v, buf[:, n:]
+
+
+def test_workspace_of_narrow_and_wide_rows(lib):
+    """A partial row for each of four workgroups per CU up to 3200 channels, of two above."""
+    size = kda.kda_rmsnorm_backward_workspace_size
+    assert size(10 ** 6, 1, 1024) == 512 * 1024 * 4 and size(10 ** 6, 1, 1025) == 1024 * 1025 * 4
+    assert size(10 ** 6, 1, 3200) == 1024 * 3200 * 4 and size(10 ** 6, 1, 3201) == 512 * 3201 * 4
 
 
 @pytest.mark.gpu
