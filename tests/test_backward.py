@@ -688,3 +688,100 @@ def test_state_gradients_in_one_tensor():
             x["idx"], x["do"], *o, d_final_state=both, d_initial_state=both, scale=c["scale"])
         torch.cuda.synchronize()
         assert torch.equal(both, apart)
+
+
+@pytest.mark.gpu
+def test_long_document_of_slow_decay():
+    """20,000 tokens in one document, decays of 1e-4 a token, against the recurrence in 64 bits
+    token by token on the GPU (one head, states kept every 100 tokens).
+
+    Tolerances: as in test_slow_decay, with the tokens that a state remembers: a write takes
+    beta (2 - beta) of the state along its key, 0.75 / 128 of its square on average, so after
+    2000 tokens less than e^-5 is left, and 2000 * 1.5 * 2^-24 = 1.8e-4 covers the decays."""
+    T, far = 20000, 2000 * 1.5 * 2.0 ** -24
+    c = make((T,), H=1, seed=73, dfinal=True, state=BF, scale=D ** -0.5)
+    c["dt"] -= 9.0
+    o = run(c)
+    f64 = {n: c[n].double().cuda() for n in ("q", "k", "v", "do", "g", "b", "A", "dt")}
+    nq, nk = (torch.sqrt(f64[n].pow(2).sum(-1, keepdim=True) + 1e-6) for n in ("q", "k"))
+    q, k, v, do = f64["q"] / nq, f64["k"] / nk, f64["v"], f64["do"]
+    x = f64["g"] + f64["dt"]
+    ea, beta = torch.exp(f64["A"]), torch.sigmoid(f64["b"])
+    g = -ea * torch.log1p(torch.exp(x))
+    a, sc = torch.exp(g), c["scale"]
+    S = c["pool"][int(c["idx"][0])][0].double().cuda()
+
+    def step(S, t):  # decayed state, x, u, state
+        Sd = S * a[t]
+        r = v[t] - Sd @ k[t]
+        return Sd, r, beta[t] * r, torch.addr(Sd, beta[t] * r, k[t])
+
+    kept = []
+    for t in range(T):
+        if t % 100 == 0:
+            kept.append(S)
+        S = step(S, t)[3]
+    dS = c["df"][0, 0].double().cuda()
+    dq, dk, dv, dg = (torch.empty_like(q) for _ in range(4))
+    db = torch.empty_like(beta)
+    for s in reversed(range(len(kept))):
+        S, seg = kept[s], []
+        for t in range(100 * s, 100 * s + 100):
+            seg.append(step(S, t))
+            S = seg[-1][3]
+        for t in reversed(range(100 * s, 100 * s + 100)):
+            Sd, r, u, S1 = seg[t - 100 * s]
+            dq[t] = sc * (do[t] @ S1)
+            dS = torch.addr(dS, do[t], sc * q[t])
+            du = dS @ k[t]
+            db[t, 0] = du @ r
+            dv[t] = beta[t] * du
+            dk[t] = u @ dS - dv[t] @ Sd
+            dS = torch.addr(dS, -dv[t], k[t])
+            dg[t] = (dS * Sd).sum(0)
+            dS = dS * a[t]
+    dq = (dq - q * (q * dq).sum(-1, keepdim=True)) / nq
+    dk = (dk - k * (k * dk).sum(-1, keepdim=True)) / nk
+    db = db * beta * torch.sigmoid(-f64["b"])
+    slope = -ea * torch.sigmoid(x)
+    for name, ref in (("dq", dq), ("dk", dk), ("dv", dv), ("dg", dg * slope), ("db", db)):
+        err = (o[name].double() - ref).abs()
+        assert (err <= 2.0 ** -8 * ref.abs() + (1e-4 + far) * ref.abs().max()).all(), name
+    assert ((o["ddt"].double() - (dg * slope).sum(0)).abs() <=
+            (2e-5 + far) * (dg * slope).abs().sum(0)).all()
+    assert abs(o["dA"].double() - (dg * g).sum()) <= (2e-5 + far) * (dg * g).abs().sum()
+    assert ((o["dS"][0, 0].double() - dS).abs() <= (1e-5 + far) * dS.abs().max()).all()
+
+
+@pytest.mark.gpu
+def test_strides_past_32_bits():
+    """Tokens 2^21 elements apart: 1100 of them span 2.3e9 elements (4.6 GB). The same bits as
+    from packed rows."""
+    lens, H, stride = (1000, 0, 100), 1, 1 << 21
+    c = make(lens, H=H, seed=74, state=BF, dfinal=True)
+    want = run(c)
+    T = sum(lens)
+    ins = torch.empty(T * stride, dtype=BF, device="cuda")
+    outs = torch.empty(T * stride, dtype=BF, device="cuda")
+
+    def at(buf, col, t):
+        return buf[col:].as_strided(tuple(t.shape), (stride, 1))
+
+    x = {}
+    for i, n in enumerate(("q", "k", "v", "g", "do", "b")):
+        x[n] = at(ins, stride - 1000 + 129 * i, c[n])
+        x[n].copy_(c[n])
+    o = {n: at(outs, 131 * i + 5, c[m])
+         for i, (n, m) in enumerate((("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"), ("db", "b")))}
+    dA, ddt = torch.empty(H, device="cuda"), torch.empty(H * D, device="cuda")
+    dS = torch.empty(3, H, D, D, device="cuda")
+    cu = torch.tensor([0, 1000, 1000, 1100], dtype=torch.int32)
+    kda.kda_prefill_varlen_backward(
+        cu, cu.cuda(), x["q"], x["k"], x["v"], x["g"], x["b"], c["A"].cuda(), c["dt"].cuda(),
+        c["pool"].cuda(), c["idx"].cuda(), x["do"], *o.values(), dA_log=dA, ddt_bias=ddt,
+        d_final_state=c["df"].cuda(), d_initial_state=dS, scale=c["scale"])
+    torch.cuda.synchronize()
+    for n, t in o.items():
+        assert torch.equal(t, want[n]), n
+    assert torch.equal(dA, want["dA"]) and torch.equal(ddt, want["ddt"])
+    assert torch.equal(dS, want["dS"])

@@ -224,3 +224,43 @@ def test_own_workspace_on_the_default_stream_handle():
     torch.cuda.synchronize()
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_own_workspace_in_a_captured_call():
+    """The capturing stream given by name: the workspace comes from the graph's memory, and the
+    replays give the bits of the calls alone, with other work between them."""
+    want = [t.clone() for t in _training_step(None)()]
+    g = torch.Generator().manual_seed(1)
+    T, H = 700, 4
+    W = H * D
+
+    def rnd(*shape, dtype=BF):
+        return torch.randn(*shape, generator=g).to(dtype).cuda()
+
+    cu = torch.tensor([0, 300, T], dtype=torch.int32)
+    cud, idx = cu.cuda(), torch.tensor([1, 0], dtype=torch.int32).cuda()
+    q, k, v, gate, do = (rnd(T, W) for _ in range(5))
+    b, A, dt = rnd(T, H), rnd(H, dtype=torch.float32), 0.1 * rnd(W, dtype=torch.float32)
+    pool, wt = 0.1 * rnd(2, H, D, D), rnd(W, dtype=torch.float32)
+    out, dz, dw = torch.empty_like(q), torch.empty_like(q), torch.empty_like(wt)
+    grads = [torch.empty_like(t) for t in (q, k, v, gate, b, A, dt)]
+    state = pool.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = torch.cuda.current_stream()
+        kda.kda_prefill_varlen(cu, cud, q, k, v, gate, b, A, dt, state, idx, out, stream=s)
+        kda.kda_prefill_varlen_backward(cu, cud, q, k, v, gate, b, A, dt, pool, idx, do,
+                                        *grads[:5], dA_log=grads[5], ddt_bias=grads[6],
+                                        stream=s.cuda_stream)
+        kda.kda_rmsnorm_backward(out, wt, do, dz, dw, stream=s)
+    for _ in range(3):
+        state.copy_(pool)
+        for t in (out, dz, dw, *grads):
+            t.fill_(-1.0)
+        graph.replay()
+        torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        for x, y in zip([out, state, *grads, dz, dw], want):
+            assert torch.equal(x, y)

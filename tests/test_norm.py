@@ -556,3 +556,39 @@ def test_backward_of_many_rows(shape, res, gated, pad):
     kda.kda_rmsnorm_backward(zp, w, dp, dp, again, gate=gi, dgate=gi, workspace=ws, **kw)
     assert torch.equal(again, dwo) and torch.equal(dp, out)  # in place
     assert gi is None or torch.equal(gi, dgo)
+
+
+@pytest.mark.gpu
+def test_strides_past_32_bits():
+    """Rows 2^21 elements apart: 1100 of them span 2.3e9 elements. The same bits as from packed
+    rows, forward (bf16 and fp8, with its scales) and gradient."""
+    shape, stride = (1100, 2, 200), 1 << 21
+    rows, n = shape[0], shape[1] * shape[2]
+    x, r, g, dy = (_gpu(shape, 90 + i) for i in range(4))
+    w = 1 + 0.1 * _gpu((200,), 94).float()
+
+    def calls(place, o8, sc):
+        xs, rs, gs, ys = (place(t, i) for i, t in enumerate((x, r, g, dy)))
+        outs = [place(torch.zeros_like(x), 4 + i) for i in range(4)]
+        dw = torch.empty(200, device="cuda")
+        kda.kda_rmsnorm(xs, w, outs[0], residual=rs, residual_out=outs[1], gate=gs)
+        kda.kda_rmsnorm(xs, w, o8, residual=rs, gate=gs, scales=sc)
+        kda.kda_rmsnorm_backward(xs, w, ys, outs[2], dw, gate=gs, dgate=outs[3], d_residual=rs)
+        torch.cuda.synchronize()
+        return outs + [o8.view(torch.uint8), sc, dw]
+
+    e4m3 = torch.float8_e4m3fn
+    want = calls(lambda t, i: t, torch.empty(shape, dtype=e4m3, device="cuda"),
+                 torch.empty(rows, 2, device="cuda"))
+    buf = torch.empty(rows * stride, dtype=BF, device="cuda")
+    far = torch.empty(rows * stride, dtype=torch.uint8, device="cuda")
+
+    def place(t, i):
+        v = buf[stride - 1 - (i + 1) * n:].as_strided(shape, (stride, 200, 1))
+        v.copy_(t)
+        return v
+
+    got = calls(place, far.view(e4m3).as_strided(shape, (stride, 200, 1), 3),
+                torch.empty(rows * stride, device="cuda").as_strided((rows, 2), (stride, 1)))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
