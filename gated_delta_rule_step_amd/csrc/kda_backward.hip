@@ -37,10 +37,10 @@
 //
 // Precision. States, sums and decays are fp32. Products run either on fp32 MFMA or on
 // fp16 MFMA with both sides split into high and low parts (22 bits and a sign each, three
-// terms), which loses nothing against fp32 and takes 3/16 of its time; fp16's range is
-// met by power-of-two scales. Operand tiles are read as consecutive contraction indices
-// per lane, in an order that lets an accumulator tile (rows 4 (lane / 16) + i) serve as the
-// next product's right operand as it is.
+// terms), which leaves out 2^-22 of a term, two bits more than fp32 rounds, in 3/16 of its
+// time; fp16's range is met by power-of-two scales. Operand tiles are read as consecutive
+// contraction indices per lane, in an order that lets an accumulator tile (rows
+// 4 (lane / 16) + i) serve as the next product's right operand as it is.
 
 #include <math.h>
 #include <stdint.h>

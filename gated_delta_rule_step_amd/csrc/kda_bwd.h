@@ -107,7 +107,7 @@ typedef u32x4 u32x4_u __attribute__((aligned(2)));  // any bf16 address
 typedef __fp16 f16x8 __attribute__((__vector_size__(8 * sizeof(__fp16))));  // MFMA operand
 
 // fp32 as fp16 high + low parts: 22 bits and a sign. Three products (high high,
-// high low, low high) then leave out 2^-22 of a term, less than the fp32 additions.
+// high low, low high) then leave out 2^-22 of a term, what four fp32 additions may round.
 __device__ __forceinline__ void split4h(f32x4 x, u32x2& hi, u32x2& lo) {
   hi = u32x2{pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3])};
   lo = u32x2{pack_f16x2(x[0] - f16_lo(hi[0]), x[1] - f16_hi(hi[0])),

@@ -24,11 +24,11 @@ namespace {
 //   two waves, two tiles                   884 | 1162 | 2895
 //   two waves, one tile                    844 | 1470 | 3806
 // so the first, second and fourth are taken where each is best, see launch_chains. (Since
-// then dO is prepared once per chunk and rows leave in 16-byte stores: 685 | 1027 | 2553, of
-// which this kernel takes 373, 374 and 872, the last at 4.3 TB/s of operands and states.)
+// then dO is prepared once per chunk and rows leave in 16-byte stores: 687 | 1033 | 2562, of
+// which this kernel takes 377, 377 and 873, the last at 4.3 TB/s of operands and states.)
 //
 // The products run on fp16 MFMA, both sides split into high and low parts (three terms,
-// fp32 accuracy at 3/16 of fp32 MFMA's time). The right sides, the state and x in
+// 22 bits a side, at 3/16 of fp32 MFMA's time). The right sides, the state and x in
 // accumulator layout, are scaled per value channel.
 //
 // A chunk's left operands come in two tiles (W, then KE; or Z, then KG and QG). With several

@@ -24,7 +24,7 @@ namespace {
 //
 // S and dS rows, decays and sums take 247 registers and the token tiles 152 KB, so one
 // workgroup fills a CU and nothing hides its loads: of a workgroup's 65,000 cycles 28 % pass
-// before the first product. 64 heads of 8208 tokens: 1169 us, 2.49 GB read and 0.56 GB
+// before the first product. 64 heads of 8208 tokens: 1199 us, 2.50 GB read and 0.56 GB
 // written (2.6 TB/s), the vector units busy for 43 % and the matrix units for 16 % of the
 // cycles. One chunk alone: 26 us. (Non-temporal loads of what the chains left made the whole
 // call 6 % slower.)

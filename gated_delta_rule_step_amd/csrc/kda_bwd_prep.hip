@@ -13,8 +13,8 @@ namespace {
 // bound by different things (loads and gates, fp32 MFMA, latency, stores), so LDS and
 // registers are kept to half a CU and two workgroups overlap theirs.
 //
-// 64 heads of 8208 tokens: 775 us, 1.35 GB read and 2.07 GB written (4.4 TB/s), the vector
-// units busy for 48 % and the matrix units for 24 % of the cycles. One chunk alone: 25 us.
+// 64 heads of 8208 tokens: 769 us, 1.33 GB read and 2.07 GB written (4.4 TB/s), the vector
+// units busy for 50 % and the matrix units for 24 % of the cycles. One chunk alone: 25 us.
 constexpr int HC = D / 2;   // channels whose rows are in LDS at a time
 constexpr int RS = HC + 4;  // padded row (fp32) of [token][channel]
 constexpr int GS = 20;      // row (fp32) of a 16 x 16 block

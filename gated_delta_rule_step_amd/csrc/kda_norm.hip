@@ -16,9 +16,9 @@
 // wave, no LDS) and a wide row one workgroup. A workgroup walks over several
 // vectors and keeps its weights in registers meanwhile.
 //
-// 16384 rows of 8192 with a residual: 193 us, 5.6 TB/s; 13889 rows of 12 heads of 128 with
-// a gate, fp8: 21 us, 5.0 TB/s; one row of 1536: 2.7 us. Gradients: 8208 rows of 8192
-// 108 us, 5.0 TB/s; 8208 rows of 64 gated heads of 128 122 us, 5.5 TB/s. (A large copy
+// 16384 rows of 8192 with a residual: 192 us, 5.6 TB/s; 13889 rows of 12 heads of 128 with
+// a gate, fp8: 21 us, 5.1 TB/s; one row of 1536: 2.5 us. Gradients: 8208 rows of 8192
+// 111 us, 4.9 TB/s; 8208 rows of 64 gated heads of 128 122 us, 5.5 TB/s. (A large copy
 // reaches 5.2 TB/s.) The partial rows' sum adds 4 to 5 us.
 //
 // Rows of odd strides or widths use the same 16-byte accesses: gfx950 takes

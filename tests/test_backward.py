@@ -2,9 +2,10 @@
 differentiation of the token recurrence in 64 bits (GPU).
 
 Tolerances. The kernels compute in fp32: every product sums at most 128 terms, and a
-decay weight is an exponential of a sum of at most 16 gates within +-88, so its
-relative error stays under 100 * 2^-24 = 6e-6; a gradient passes through fewer than
-ten such factors. dq, dk and dg then subtract parts of similar size, so the error is
+decay weight inside a block is a product of at most 16 exponentials of gates within 5.5,
+each off by its argument's rounding, a step of its own and the product's, (5.5 + 2 + 1)
+2^-24, so its relative error stays under 136 * 2^-24 = 8.1e-6; a gradient passes through
+fewer than ten such factors. dq, dk and dg then subtract parts of similar size, so the error is
 relative to the largest gradient of the document and head, not to the element:
 1e-4 of it. bf16 outputs add half a step, 2^-8 of the element. fp32 outputs:
 the state gradient 1e-5 of the largest element; dA_log and ddt_bias 2e-5 of
