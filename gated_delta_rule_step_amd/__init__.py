@@ -131,10 +131,11 @@ def _workspace(need, dev, stream):
         return None
     if stream is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream.device != dev:
+    if getattr(stream, "device", dev) != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    if not isinstance(stream, torch.cuda.Stream):  # a handle, or anything that holds one
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(need, dtype=torch.uint8, device=dev)
 

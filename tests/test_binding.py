@@ -56,6 +56,11 @@ class Calls:
         return call
 
 
+class Holder:
+    """Another library's stream object."""
+    cuda_stream = 0x400
+
+
 CURRENT = 0x100
 
 
@@ -123,8 +128,8 @@ NAMES = ["kda_prefill_varlen", "kda_prefill_varlen_backward", "kda_rmsnorm_backw
 
 @pytest.mark.parametrize("name", NAMES)
 @pytest.mark.parametrize("stream,want", [(None, CURRENT), (Stream(0x200), 0x200), (0x300, 0x300),
-                                         (Stream(CURRENT), CURRENT)],
-                         ids=["current", "stream", "handle", "same"])
+                                         (Stream(CURRENT), CURRENT), (Holder(), 0x400)],
+                         ids=["current", "stream", "handle", "same", "holder"])
 def test_workspace_belongs_to_the_launch_stream(fake, name, stream, want):
     """A workspace that the binding makes comes from the pool of the stream that the
     kernels run on: from another one it could be handed out again while they use it."""
@@ -198,14 +203,16 @@ def _training_step(stream, T=700, H=4):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("form", ["stream", "handle"])
+@pytest.mark.parametrize("form", ["stream", "handle", "holder"])
 def test_own_workspace_on_a_side_stream(form):
     """Calls on a side stream next to allocations and fills of the current stream: the bits
     of the calls alone."""
     want = [t.clone() for t in _training_step(None)()]
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    step = _training_step(side if form == "stream" else side.cuda_stream)
+    holder = Holder()
+    holder.cuda_stream = side.cuda_stream
+    step = _training_step(dict(stream=side, handle=side.cuda_stream, holder=holder)[form])
     need = kda.kda_prefill_backward_workspace_size(2, 700, 4)
     for _ in range(5):
         got = step()
