@@ -4,8 +4,9 @@ Argument marshalling only: every function takes torch tensors that already
 live on the GPU, checks dtype/device/contiguity of the innermost dimension,
 and passes raw pointers, element strides and the current HIP stream to the C
 ABI declared in include/kda.h (the recurrence: decode, verify, prefill),
-kda_backward.h (the prefill's gradients) and kda_norm.h (the layer's RMS norms
-and their gradients). All arithmetic runs in the library's kernels;
+kda_backward.h (the prefill's gradients), kda_norm.h (the layer's RMS norms
+and their gradients) and kda_cache.h (the paged 8-bit key/value cache of the
+attention layers beside it). All arithmetic runs in the library's kernels;
 there is no fallback. If libkda.so is missing the first call raises.
 
 bf16 tensors are torch.bfloat16; A_log and dt_bias are float32; indices and
@@ -62,6 +63,14 @@ _SIGS = {
     "kda_rmsnorm_backward_workspace_size": (_c.c_size_t, [_I64, _I32, _I32]),
     "kda_rmsnorm_backward": (_c.c_int, [_I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
                                         _P, _F, _P, _I64, _P, _I64, _P, _P, _c.c_size_t, _P]),
+    "kda_cache_write": (_c.c_int, [_I32, _I64, _I32, _I32, _P, _P, _I64, _P, _I64, _I32, _I32,
+                                   _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I64, _P, _P]),
+    "kda_cache_read": (_c.c_int, [_I32, _I64, _I32, _I32, _P, _P, _I64, _P, _I64, _I32, _I32,
+                                  _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I64, _P, _P]),
+    "kda_cache_attention_workspace_size": (_c.c_size_t, [_I32, _I64, _I32, _I32]),
+    "kda_cache_attention": (_c.c_int, [_I32, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _I32, _I32,
+                                       _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _I64, _P, _F,
+                                       _P, _I64, _P, _I64, _P, _c.c_size_t, _P]),
 }
 
 # Scratch held by the library per device for kda_prefill_varlen_noalloc
@@ -609,3 +618,140 @@ def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None,
     _launch("kda_rmsnorm_backward", dev, stream, rows, heads, width, _adr(z), zs, _adr(dy), ys,
             _adr(gate), gs, _adr(d_residual), rs, _adr(weight), float(eps), _adr(dz), ds,
             _adr(dgate), dgs, _adr(dweight), _adr(workspace), ws_bytes)
+
+
+def _cache_geometry(k_cache, v_cache, k_scale, v_scale, page_table, kv_lens):
+    """Checks of a paged cache and its tables; the C arguments between the dtype and the
+    tables, those of the tables, the head count, and the tensors by name."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape[3] != HEAD_DIM:
+        raise ValueError(f"k_cache must be [pages, H, page_size, 128], got {list(k_cache.shape)}")
+    if k_cache.dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise TypeError(f"k_cache must be float8_e4m3fn or int8, got {k_cache.dtype}")
+    pages, H, size = k_cache.shape[:3]
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != k_cache.dtype or t.shape != k_cache.shape:
+            raise ValueError(f"{name} must be {k_cache.dtype} {list(k_cache.shape)}, got "
+                             f"{t.dtype} {list(t.shape)}")
+        if not t.is_cuda or (pages > 0 and not t[0].is_contiguous()):
+            raise ValueError(f"{name} must be a GPU tensor whose pages are contiguous")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _f32(name, t)
+        if tuple(t.shape) != (pages, H):
+            raise ValueError(f"{name} must be [{pages}, {H}], got {list(t.shape)}")
+    _i32("kv_lens", kv_lens)
+    if kv_lens.dim() != 1:
+        raise ValueError(f"kv_lens must be [sequences], got {list(kv_lens.shape)}")
+    n = kv_lens.shape[0]
+    if page_table.dtype != torch.int32 or not page_table.is_cuda:
+        raise ValueError("page_table must be an int32 GPU tensor")
+    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.shape[1] < 1 or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be [{n}, pages of a sequence] with contiguous rows, "
+                         f"got {list(page_table.shape)}")
+    width = page_table.shape[1]
+    cache = (1 if k_cache.dtype == torch.int8 else 0, size, pages, _adr(k_cache),
+             k_cache.stride(0), _adr(v_cache), v_cache.stride(0), _adr(k_scale), _adr(v_scale))
+    tables = (_adr(page_table), width, page_table.stride(0) if n > 1 else width, _adr(kv_lens))
+    return cache + tables, n, H, (("k_cache", k_cache), ("v_cache", v_cache),
+                                  ("k_scale", k_scale), ("v_scale", v_scale),
+                                  ("page_table", page_table), ("kv_lens", kv_lens))
+
+
+def _cache_rows(name, t, tokens, width):
+    """bf16 [tokens, width] with contiguous rows: the row stride."""
+    _bf16(name, t)
+    if tuple(t.shape) != (tokens, width):
+        raise ValueError(f"{name} must be [{tokens}, {width}], got {list(t.shape)}")
+    return t.stride(0)
+
+
+def _cache_seqlens(cu_seqlens, n, tokens):
+    if cu_seqlens is not None:
+        _i32("cu_seqlens", cu_seqlens)
+        if tuple(cu_seqlens.shape) != (n + 1,):
+            raise ValueError(f"cu_seqlens must be [{n + 1}], got {list(cu_seqlens.shape)}")
+    elif n == 0 and tokens > 0 or n > 0 and tokens % n != 0:
+        raise ValueError(f"{tokens} tokens of {n} sequences need cu_seqlens")
+
+
+def _cache_rows_call(fn, k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
+                     cu_seqlens, stream):
+    cache, n, H, named = _cache_geometry(k_cache, v_cache, k_scale, v_scale, page_table, kv_lens)
+    T = k.shape[0]
+    ks = _cache_rows("k", k, T, H * HEAD_DIM)
+    vs = _cache_rows("v", v, T, H * HEAD_DIM)
+    _cache_seqlens(cu_seqlens, n, T)
+    dev = _same_device(k, (("v", v), ("cu_seqlens", cu_seqlens)) + named)
+    _launch(fn, dev, stream, n, T, H, HEAD_DIM, _adr(cu_seqlens), _adr(k), ks, _adr(v), vs,
+            *cache)
+
+
+def kda_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
+                    cu_seqlens=None, stream=None) -> None:
+    """Quantise new tokens into their sequences' pages. k, v: bf16 [T, H*128]
+    (row-strided); k_cache, v_cache: float8_e4m3fn or int8 [pages, H, page_size, 128]
+    (page_size 16, 32, 64, 128 or 256; page-strided); k_scale, v_scale: fp32 [pages, H];
+    page_table: int32 [n, pages of a sequence] (row-strided); kv_lens: int32 [n], lengths
+    with the new tokens, which are the last ones of each sequence. cu_seqlens: int32
+    [n + 1], or None where every sequence has T / n new tokens. Caches and scales are
+    updated in place."""
+    _cache_rows_call("kda_cache_write", k, v, k_cache, v_cache, k_scale, v_scale, page_table,
+                     kv_lens, cu_seqlens, stream)
+
+
+def kda_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
+                   cu_seqlens=None, stream=None) -> None:
+    """The last tokens of each sequence, code * scale, into k and v (bf16 [T, H*128],
+    row-strided). Other arguments as for kda_cache_write: sequence b's rows receive its
+    positions kv_lens[b] - n_b .. kv_lens[b] - 1."""
+    _cache_rows_call("kda_cache_read", k, v, k_cache, v_cache, k_scale, v_scale, page_table,
+                     kv_lens, cu_seqlens, stream)
+
+
+def kda_cache_attention_workspace_size(n_seqs: int, total_tokens: int, H_q: int,
+                                       H_kv: int) -> int:
+    return int(lib().kda_cache_attention_workspace_size(n_seqs, total_tokens, H_q, H_kv))
+
+
+def kda_cache_attention(q, out, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
+                        cu_seqlens_host=None, cu_seqlens=None, lse=None,
+                        scale: float = HEAD_DIM ** -0.5, workspace=None, stream=None) -> None:
+    """Causal softmax attention of each sequence's last tokens over its cache, which
+    holds them already. q, out: bf16 [T, H_q*128] (row-strided), H_q a multiple of the
+    cache's H; lse: fp32 [T, H_q] (row-strided) or None. cu_seqlens_host (CPU int32
+    [n + 1]) and cu_seqlens (the same on the GPU), or None where every sequence has T / n
+    new tokens. Cache arguments as for kda_cache_write. workspace: uint8 GPU tensor of >=
+    kda_cache_attention_workspace_size(...) bytes, or None to have one allocated here for
+    this call."""
+    import torch
+    cache, n, H, named = _cache_geometry(k_cache, v_cache, k_scale, v_scale, page_table, kv_lens)
+    if q.dim() != 2:
+        raise ValueError(f"q must be [T, H_q*128], got {list(q.shape)}")
+    T, W = q.shape
+    Hq = W // HEAD_DIM
+    if W != Hq * HEAD_DIM or Hq < 1 or Hq % H != 0:
+        raise ValueError(f"q must be [T, H_q*128] with H_q a multiple of {H}, got {list(q.shape)}")
+    qs = _cache_rows("q", q, T, W)
+    os_ = _cache_rows("out", out, T, W)
+    ls = 0
+    if lse is not None:
+        if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (T, Hq) or \
+                (Hq > 1 and lse.stride(1) != 1):
+            raise ValueError(f"lse must be a float32 GPU tensor [{T}, {Hq}] with contiguous rows")
+        ls = lse.stride(0)
+    _cache_seqlens(cu_seqlens, n, T)
+    if (cu_seqlens is None) != (cu_seqlens_host is None):
+        raise ValueError("cu_seqlens and cu_seqlens_host go together")
+    if cu_seqlens_host is not None and (
+            cu_seqlens_host.dtype != torch.int32 or cu_seqlens_host.is_cuda or
+            not cu_seqlens_host.is_contiguous() or tuple(cu_seqlens_host.shape) != (n + 1,)):
+        raise ValueError(f"cu_seqlens_host must be a contiguous int32 CPU tensor [{n + 1}]")
+    dev = _same_device(q, (("out", out), ("cu_seqlens", cu_seqlens), ("lse", lse),
+                           ("workspace", workspace)) + named)
+    if workspace is None and T > 0:
+        workspace = _workspace(kda_cache_attention_workspace_size(n, T, Hq, H), dev, stream)
+    ws_bytes = _workspace_bytes(workspace, dev)
+    _launch("kda_cache_attention", dev, stream, n, T, Hq, H, HEAD_DIM, _adr(cu_seqlens_host),
+            _adr(cu_seqlens), _adr(q), qs, *cache, float(scale), _adr(out), os_, _adr(lse), ls,
+            _adr(workspace), ws_bytes)

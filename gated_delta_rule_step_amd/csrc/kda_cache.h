@@ -1,0 +1,110 @@
+// The paged 8-bit cache: parameter block and helpers that its calls share.
+#pragma once
+
+#include "../../include/kda_cache.h"
+#include "kda_common.h"
+
+namespace kda {
+namespace cache {
+
+constexpr int kFp8 = KDA_CACHE_FP8;
+constexpr int kInt8 = KDA_CACHE_INT8;
+
+typedef u32x4 u32x4_u __attribute__((aligned(2)));  // bf16 rows need no alignment of their own
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct CacheView {
+  int32_t n_seqs, H;    // H: key/value heads
+  int64_t total;        // packed tokens
+  const int32_t* cu;    // NULL: per_seq tokens of every sequence
+  int32_t per_seq;
+  int32_t page_shift;   // page size: 1 << page_shift tokens
+  int64_t num_pages;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t k_page, v_page;  // page strides
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  int32_t width;
+  int64_t table_stride;
+  const int32_t* lens;
+};
+
+// A sequence's tokens of this call, packed rows first .. first + n - 1, and its length with
+// them (-1: inactive).
+struct Seq {
+  int64_t first;
+  int32_t n, len;
+};
+__device__ __forceinline__ int32_t clamp_row(const CacheView& p, int32_t x) {
+  return min(max(x, 0), int32_t(p.total));
+}
+__device__ __forceinline__ Seq sequence(const CacheView& p, int32_t b) {
+  Seq s;
+  const int32_t len = p.lens[b];
+  if (p.cu) {
+    const int32_t c0 = clamp_row(p, p.cu[b]), c1 = clamp_row(p, p.cu[b + 1]);
+    s.first = c0;
+    s.n = max(c1 - c0, 0);
+  } else {
+    s.first = int64_t(b) * p.per_seq;
+    s.n = p.per_seq;
+  }
+  s.len = len < s.n || len > (int64_t(p.width) << p.page_shift) ? -1 : len;
+  return s;
+}
+// The page that holds position `at` >> page_shift == i of sequence b; -1: none.
+__device__ __forceinline__ int32_t page_of(const CacheView& p, int32_t b, int32_t i) {
+  const int32_t id = p.table[b * p.table_stride + i];
+  return uint32_t(id) < uint64_t(p.num_pages) ? id : -1;
+}
+
+// Four codes as two bf16 pairs, exact: e4m3 has 4 significant bits, int8 7.
+template <int KIND>
+__device__ __forceinline__ u32x2 widen4(uint32_t w) {
+  if constexpr (KIND == kFp8) {
+    return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
+  } else {
+    return u32x2{pack_bf16x2_exact(float(int8_t(w)), float(int8_t(w >> 8))),
+                 pack_bf16x2_exact(float(int8_t(w >> 16)), float(int8_t(w >> 24)))};
+  }
+}
+template <int KIND>
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
+  const u32x2 a = widen4<KIND>(lo), b = widen4<KIND>(hi);
+  return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
+}
+
+__device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Host: the checks that the calls share, and the view. `empty`: nothing to do.
+struct CacheArgs {
+  int32_t n_seqs;
+  int64_t total_tokens;
+  int32_t H, D;
+  const int32_t* cu_seqlens;
+  int32_t cache_dtype, page_size;
+  int64_t num_pages;
+  const void* k_cache;
+  int64_t k_page_stride;
+  const void* v_cache;
+  int64_t v_page_stride;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* page_table;
+  int32_t table_width;
+  int64_t table_row_stride;
+  const int32_t* kv_lens;
+};
+kda_status check(const CacheArgs& a, CacheView* view);
+// Rows of `len` elements do not overlap.
+inline bool rows_apart(int64_t rows, int64_t stride, int64_t len) {
+  return rows <= 1 || stride >= len;
+}
+
+}  // namespace cache
+}  // namespace kda

@@ -1,0 +1,378 @@
+// Writing and reading the paged 8-bit key/value cache (gfx950).
+//
+// Both are bound by HBM (2 bytes per value on one side, 1 on the other) and, for a decode
+// step's few tokens, by the latency of the chain sequence -> page -> scale -> bytes.
+//
+// Write: a page's scale needs the largest magnitude of all its new tokens before any can be
+// rounded, so the tokens of one (page, head, side) stay in the registers of one workgroup
+// (or one wave, where a page gets at most 16) between the two: read once, written once.
+
+#include <stdint.h>
+
+#include "kda_cache.h"
+
+namespace kda {
+namespace cache {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMinExp = -100;  // smallest exponent of a scale
+
+struct WriteParams {
+  CacheView c;
+  const uint16_t* src[2];  // k, v
+  int64_t src_stride[2];
+  uint8_t* dst[2];
+  float* scale[2];
+  int32_t per_seq_items;  // without cu: pages that a sequence's tokens may touch
+};
+
+struct ReadParams {
+  CacheView c;
+  uint16_t* dst[2];
+  int64_t dst_stride[2];
+  int32_t per_seq_items;
+};
+
+// Work items are (sequence, page that gets tokens). n tokens touch at most
+// (n + P - 2) / P + 1 pages, so items of sequence b start at cu[b] / P + 2 b: no prefix sum.
+// The last b with a start <= item, found by 64 lanes at a time.
+__device__ __forceinline__ int32_t find_seq(const CacheView& p, int32_t item, int32_t lane) {
+  int32_t lo = 0, span = p.n_seqs;  // the answer lies in [lo, lo + span)
+  while (span > 1) {
+    const int32_t step = (span + 63) >> 6;
+    const int32_t b = lo + lane * step;
+    const bool is = lane * step < span &&
+                    (clamp_row(p, p.cu[b]) >> p.page_shift) + 2 * int64_t(b) <= item;
+    const int32_t hits = __popcll(__ballot(is));
+    lo += max(hits - 1, 0) * step;
+    span = min(step, p.n_seqs - lo);
+  }
+  return lo;
+}
+
+// The item's page (-1: none), its slots [a, z) that get the packed rows from `row` on.
+struct Item {
+  int32_t b, page, a, z;
+  int64_t row;
+};
+__device__ __forceinline__ Item find_item(const CacheView& p, int32_t item, int32_t per_seq_items,
+                                          int32_t lane) {
+  Item it;
+  int32_t j;
+  if (p.cu) {
+    it.b = __builtin_amdgcn_readfirstlane(find_seq(p, item, lane));
+    j = item - ((clamp_row(p, p.cu[it.b]) >> p.page_shift) + 2 * it.b);
+  } else {
+    it.b = item / per_seq_items;
+    j = item - it.b * per_seq_items;
+  }
+  const Seq s = sequence(p, it.b);
+  const int32_t P = 1 << p.page_shift;
+  it.page = -1;
+  it.a = it.z = 0;
+  it.row = s.first;
+  if (j < 0 || s.n == 0) return it;
+  // an inactive sequence's rows are walked as if it began on a page's border
+  const int32_t start = s.len < 0 ? 0 : s.len - s.n;
+  const int32_t first = start & (P - 1);
+  const int64_t from = (int64_t(j) << p.page_shift) - first;  // token in the page's slot 0
+  if (from >= s.n) return it;
+  it.a = from < 0 ? first : 0;
+  it.z = int32_t(min(int64_t(P), int64_t(s.n) - from));
+  it.row = s.first + (from < 0 ? 0 : from);
+  if (s.len >= 0) it.page = page_of(p, it.b, (start >> p.page_shift) + j);
+  return it;
+}
+
+// Magnitude bits of finite bf16 values, 0 for others.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
+}
+// need = 2^e from the bits of amax: 1.m 2^(E - 127) <= 1.75 2^8 2^e (e4m3),
+// <= 1.984375 2^6 2^e (int8).
+template <int KIND>
+__device__ __forceinline__ float need_scale(uint32_t amax) {
+  const int32_t E = int32_t(amax >> 7), m = int32_t(amax & 127u);
+  const int32_t e = KIND == kFp8 ? E - 135 + (m > 96) : E - 133 + (m > 126);
+  return __uint_as_float(uint32_t(max(e, kMinExp) + 127) << 23);
+}
+
+// Four values, already divided by the scale, to codes.
+template <int KIND>
+__device__ __forceinline__ float saturate(float x) {
+  if constexpr (KIND == kFp8)
+    return x != x ? x : f8_sat(x);  // a NaN stays one
+  else
+    return x != x ? 0.0f : rintf(__builtin_amdgcn_fmed3f(x, -127.0f, 127.0f));
+}
+template <int KIND>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  a = saturate<KIND>(a), b = saturate<KIND>(b), c = saturate<KIND>(c), d = saturate<KIND>(d);
+  if constexpr (KIND == kFp8) {
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true));
+  } else {
+    return (uint32_t(int32_t(a)) & 255u) | (uint32_t(int32_t(b)) & 255u) << 8 |
+           (uint32_t(int32_t(c)) & 255u) << 16 | uint32_t(int32_t(d)) << 24;
+  }
+}
+template <int KIND>
+__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+  if constexpr (KIND == kFp8) {
+    const f32x2 a = f8x2_lo(w), b = f8x2_hi(w);
+    x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
+  } else {
+    x[0] = float(int8_t(w)), x[1] = float(int8_t(w >> 8));
+    x[2] = float(int8_t(w >> 16)), x[3] = float(int8_t(w >> 24));
+  }
+}
+
+// One (page, head, side) by WAVES waves, 4 WAVES PASSES >= the page's new tokens. A row is 16
+// lanes of 8 channels.
+template <int KIND, int WAVES, int PASSES>
+__global__ __launch_bounds__(kThreads) void write_kernel(WriteParams p) {
+  __shared__ uint32_t tops[4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int kPer = 4 / WAVES;  // (head, side) pairs of a workgroup
+  const int pair = blockIdx.y * kPer + (WAVES == 4 ? 0 : wave);
+  if (WAVES == 1 && pair >= 2 * p.c.H) return;
+  const int side = pair & 1, h = pair >> 1;
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
+  if (it.page < 0) return;  // the same for all waves
+  const int t = WAVES == 4 ? threadIdx.x : lane;
+  const int r0 = t >> 4, ch = (t & 15) * 8;
+  const int rows = it.z - it.a;
+  float* const scale_at = p.scale[side] + int64_t(it.page) * p.c.H + h;
+  const float old = it.a > 0 ? *scale_at : 0.0f;
+  const uint16_t* const src = p.src[side] + it.row * p.src_stride[side] + h * D + ch;
+  u32x4 x[PASSES];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int r = r0 + i * 4 * WAVES;
+    x[i] = u32x4{0u, 0u, 0u, 0u};
+    if (r < rows) x[i] = *reinterpret_cast<const u32x4_u*>(src + r * p.src_stride[side]);
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, finite2(x[i][j]));
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) top = max(top, uint32_t(__shfl_xor(int(top), s)));
+  if (WAVES == 4) {
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  }
+  const float scale = fmaxf(need_scale<KIND>(top), old);
+  const float inv = 1.0f / scale;  // exact for powers of two
+  const int64_t page_stride = side ? p.c.v_page : p.c.k_page;
+  uint8_t* const page =
+      p.dst[side] + it.page * page_stride + ((int64_t(h) << p.c.page_shift) * D);
+  if (old > 0.0f && old != scale) {  // earlier tokens of a page whose scale grew
+    const float ratio = old * inv;
+    for (int i = t; i < it.a * (D / 4); i += 64 * WAVES) {
+      uint32_t* const w = reinterpret_cast<uint32_t*>(page) + i;
+      float y[4];
+      decode4<KIND>(*w, y);
+      *w = encode4<KIND>(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
+    }
+  }
+  if (t == 0) *scale_at = scale;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int r = r0 + i * 4 * WAVES;
+    if (r < rows) {
+      float y[8];
+      unpack8_bf16(x[i], y);
+      *reinterpret_cast<u32x2*>(page + (it.a + r) * D + ch) =
+          u32x2{encode4<KIND>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                encode4<KIND>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)};
+    }
+  }
+}
+
+// Rows (head, slot) of a page are one run of bytes; a workgroup takes kReadRows of them, a
+// row by 8 lanes of 16 codes.
+constexpr int kReadRows = 256;
+template <int KIND>
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadParams p) {
+  const int lane = threadIdx.x & 63, side = blockIdx.z;
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
+  if (it.z == it.a) return;
+  const int P = 1 << p.c.page_shift;
+  const int most = p.c.H << p.c.page_shift;
+  const uint8_t* const page = (side ? p.c.v + max(it.page, 0) * p.c.v_page
+                                    : p.c.k + max(it.page, 0) * p.c.k_page);
+  const float* const scales = (side ? p.c.v_scale : p.c.k_scale) + int64_t(max(it.page, 0)) * p.c.H;
+  const int ch = (threadIdx.x & 7) * 16;
+#pragma unroll
+  for (int i = 0; i < kReadRows / 32; ++i) {
+    const int r = blockIdx.y * kReadRows + i * 32 + (threadIdx.x >> 3);
+    const int h = r >> p.c.page_shift, slot = r & (P - 1);
+    if (r >= most || slot < it.a || slot >= it.z) continue;
+    u32x4 w = {0u, 0u, 0u, 0u};
+    float scale = 0.0f;
+    if (it.page >= 0) {
+      w = *reinterpret_cast<const u32x4*>(page + int64_t(r) * D + ch);
+      scale = scales[h];
+    }
+    u32x4 o[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[4];
+      decode4<KIND>(w[j], x);
+      o[j >> 1][2 * (j & 1)] = pack_bf16x2(x[0] * scale, x[1] * scale);
+      o[j >> 1][2 * (j & 1) + 1] = pack_bf16x2(x[2] * scale, x[3] * scale);
+    }
+    u32x4_u* const dst = reinterpret_cast<u32x4_u*>(
+        p.dst[side] + (it.row + slot - it.a) * p.dst_stride[side] + h * D + ch);
+    dst[0] = o[0];
+    dst[1] = o[1];
+  }
+}
+
+// Work items (see find_seq), 0: more than a launch takes.
+int64_t count_items(const CacheView& c, int32_t* per_seq) {
+  const int64_t P = int64_t(1) << c.page_shift;
+  *per_seq = int32_t((c.per_seq + P - 2) / P + 1);
+  const int64_t n = c.cu ? c.total / P + 2 * int64_t(c.n_seqs) : int64_t(c.n_seqs) * *per_seq;
+  return n < (int64_t(1) << 31) ? n : 0;
+}
+
+template <int KIND, int WAVES, int PASSES>
+hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream) {
+  const unsigned pairs = 2u * unsigned(p.c.H), per = 4 / WAVES;
+  hipLaunchKernelGGL((write_kernel<KIND, WAVES, PASSES>), dim3(items, (pairs + per - 1) / per),
+                     dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+template <int KIND>
+hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream) {
+  const int P = 1 << p.c.page_shift;
+  const int most = p.c.cu ? P : (p.c.per_seq < P ? p.c.per_seq : P);
+  if (most <= 4) return launch_write<KIND, 1, 1>(p, items, stream);
+  if (most <= 16) return launch_write<KIND, 1, 4>(p, items, stream);
+  if (most <= 64) return launch_write<KIND, 4, 4>(p, items, stream);
+  return launch_write<KIND, 4, 16>(p, items, stream);
+}
+
+}  // namespace
+
+kda_status check(const CacheArgs& a, CacheView* c) {
+  if (a.n_seqs < 0 || a.total_tokens < 0 || a.H < 1 || a.num_pages < 0 || a.table_width < 1)
+    return KDA_ERR_BAD_SHAPE;
+  if (a.D != D || (a.cache_dtype != KDA_CACHE_FP8 && a.cache_dtype != KDA_CACHE_INT8))
+    return KDA_ERR_UNSUPPORTED;
+  int32_t shift = 4;
+  while (shift < 8 && (1 << shift) < a.page_size) ++shift;
+  if ((1 << shift) != a.page_size) return KDA_ERR_UNSUPPORTED;
+  if (a.total_tokens > (int64_t(1) << 30) || a.H > (1 << 14) || a.num_pages > INT32_MAX ||
+      int64_t(a.n_seqs) * a.table_width > (int64_t(1) << 37) / a.page_size)
+    return KDA_ERR_UNSUPPORTED;
+  if (a.total_tokens > 0 && a.n_seqs == 0) return KDA_ERR_BAD_SHAPE;
+  if (!a.cu_seqlens && a.n_seqs > 0 && a.total_tokens % a.n_seqs != 0) return KDA_ERR_BAD_SHAPE;
+  if (a.table_row_stride < 0 || a.k_page_stride < 0 || a.v_page_stride < 0)
+    return KDA_ERR_BAD_STRIDE;
+  if (a.total_tokens == 0) return KDA_OK;
+  if (!a.page_table || !a.kv_lens) return KDA_ERR_NULL_POINTER;
+  if (a.num_pages > 0 && (!a.k_cache || !a.v_cache || !a.k_scale || !a.v_scale))
+    return KDA_ERR_NULL_POINTER;
+  const int64_t page = int64_t(a.H) * a.page_size * D;
+  if (!rows_apart(a.num_pages, a.k_page_stride, page) ||
+      !rows_apart(a.num_pages, a.v_page_stride, page) ||
+      !rows_apart(a.n_seqs, a.table_row_stride, a.table_width))
+    return KDA_ERR_BAD_STRIDE;
+  if (((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache) |
+        uint64_t(a.k_page_stride) | uint64_t(a.v_page_stride)) & 15u) != 0)
+    return KDA_ERR_UNSUPPORTED;
+  c->n_seqs = a.n_seqs;
+  c->H = a.H;
+  c->total = a.total_tokens;
+  c->cu = a.cu_seqlens;
+  c->per_seq = a.cu_seqlens ? 0 : int32_t(a.total_tokens / a.n_seqs);
+  c->page_shift = shift;
+  c->num_pages = a.num_pages;
+  c->k = static_cast<const uint8_t*>(a.k_cache);
+  c->v = static_cast<const uint8_t*>(a.v_cache);
+  c->k_page = a.k_page_stride;
+  c->v_page = a.v_page_stride;
+  c->k_scale = a.k_scale;
+  c->v_scale = a.v_scale;
+  c->table = a.page_table;
+  c->width = a.table_width;
+  c->table_stride = a.table_row_stride;
+  c->lens = a.kv_lens;
+  return KDA_OK;
+}
+
+}  // namespace cache
+}  // namespace kda
+
+extern "C" kda_status kda_cache_write(
+    int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t D, const int32_t* cu_seqlens,
+    const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride, int32_t cache_dtype,
+    int32_t page_size, int64_t num_pages, void* k_cache, int64_t k_page_stride, void* v_cache,
+    int64_t v_page_stride, float* k_scale, float* v_scale, const int32_t* page_table,
+    int32_t table_width, int64_t table_row_stride, const int32_t* kv_lens, hipStream_t stream) {
+  namespace kc = kda::cache;
+  kc::WriteParams p;
+  const kc::CacheArgs a = {n_seqs,  total_tokens, H, D, cu_seqlens, cache_dtype, page_size,
+                           num_pages, k_cache, k_page_stride, v_cache, v_page_stride, k_scale,
+                           v_scale, page_table, table_width, table_row_stride, kv_lens};
+  if (const kda_status st = kc::check(a, &p.c)) return st;
+  if (k_row_stride < 0 || v_row_stride < 0) return KDA_ERR_BAD_STRIDE;
+  if (total_tokens == 0) return KDA_OK;
+  if (!k || !v) return KDA_ERR_NULL_POINTER;
+  const int64_t items = kc::count_items(p.c, &p.per_seq_items);
+  if (items == 0) return KDA_ERR_UNSUPPORTED;
+  if (num_pages == 0) return KDA_OK;  // no page to write to
+  p.src[0] = static_cast<const uint16_t*>(k);
+  p.src[1] = static_cast<const uint16_t*>(v);
+  p.src_stride[0] = k_row_stride;
+  p.src_stride[1] = v_row_stride;
+  p.dst[0] = static_cast<uint8_t*>(k_cache);
+  p.dst[1] = static_cast<uint8_t*>(v_cache);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  const hipError_t e = cache_dtype == KDA_CACHE_FP8
+                           ? kc::launch_write<kc::kFp8>(p, unsigned(items), stream)
+                           : kc::launch_write<kc::kInt8>(p, unsigned(items), stream);
+  return e == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" kda_status kda_cache_read(
+    int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t D, const int32_t* cu_seqlens, void* k,
+    int64_t k_row_stride, void* v, int64_t v_row_stride, int32_t cache_dtype, int32_t page_size,
+    int64_t num_pages, const void* k_cache, int64_t k_page_stride, const void* v_cache,
+    int64_t v_page_stride, const float* k_scale, const float* v_scale, const int32_t* page_table,
+    int32_t table_width, int64_t table_row_stride, const int32_t* kv_lens, hipStream_t stream) {
+  namespace kc = kda::cache;
+  kc::ReadParams p;
+  const kc::CacheArgs a = {n_seqs,  total_tokens, H, D, cu_seqlens, cache_dtype, page_size,
+                           num_pages, k_cache, k_page_stride, v_cache, v_page_stride, k_scale,
+                           v_scale, page_table, table_width, table_row_stride, kv_lens};
+  if (const kda_status st = kc::check(a, &p.c)) return st;
+  const int64_t row = int64_t(H) * D;
+  if (k_row_stride < 0 || v_row_stride < 0 || !kc::rows_apart(total_tokens, k_row_stride, row) ||
+      !kc::rows_apart(total_tokens, v_row_stride, row))
+    return KDA_ERR_BAD_STRIDE;
+  if (total_tokens == 0) return KDA_OK;
+  if (!k || !v) return KDA_ERR_NULL_POINTER;
+  const int64_t items = kc::count_items(p.c, &p.per_seq_items);
+  if (items == 0) return KDA_ERR_UNSUPPORTED;
+  p.dst[0] = static_cast<uint16_t*>(k);
+  p.dst[1] = static_cast<uint16_t*>(v);
+  p.dst_stride[0] = k_row_stride;
+  p.dst_stride[1] = v_row_stride;
+  const unsigned rows = unsigned(H) << p.c.page_shift;
+  const dim3 grid(unsigned(items), (rows + kc::kReadRows - 1) / kc::kReadRows, 2);
+  if (cache_dtype == KDA_CACHE_FP8)
+    hipLaunchKernelGGL(kc::read_kernel<kc::kFp8>, grid, dim3(kc::kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL(kc::read_kernel<kc::kInt8>, grid, dim3(kc::kThreads), 0, stream, p);
+  return hipGetLastError() == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}

@@ -1,0 +1,659 @@
+"""kda_cache_write, kda_cache_read and kda_cache_attention: host validation (CPU) and parity
+with the definitions in 64 bits (GPU).
+
+Tolerances. Bytes, scales and values read back are exact: scales are powers of two, so every
+division and product is, and the one rounding is to the nearest code (even on a tie).
+
+Attention. Products of bf16 and widened codes are exact in fp32; a score sums 128 of them and
+takes two more roundings, so it is off by at most d = 131 * 2^-24 * |scale| sum |q k|, and its
+weight by that relatively, plus 2^-22 for the exponential. A sum of n weights adds n * 2^-24
+at most, and so does each output sum. The weights enter the second product with a relative
+error of `weight` (2^-16 as two bf16 parts, 2^-8 as one). So out is off by at most
+half a step of bf16, 2^-8 |out|, and (weight + 2 d + 2 n 2^-24 + 2^-20) times the mean of |v|
+under the weights; lse by d + n 2^-24 + 2^-21 (1 + |lse|). A weight under 2^-126 of the largest one's
+range may be flushed to zero, fp32's smallest normal number (the reference exponent is at most
+the largest score's, so the sum that divides it is at least 1), and a part of one bf16 pair under
+2^-126 too: n 2^-125 max |v| more.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import gated_delta_rule_step_amd as kda
+
+OK, NULLP, SHAPE, STRIDE, UNSUP, SEQ, WS = range(7)
+BF, F8, I8, I32 = torch.bfloat16, torch.float8_e4m3fn, torch.int8, torch.int32
+KINDS = [F8, I8]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.LIB_PATH):
+        from gated_delta_rule_step_amd import build
+        build.build()
+    return kda.lib()
+
+
+# ---------------------------------------------------------------------------
+# refusals: every call returns before anything is launched (made-up pointers)
+
+def _args(**kw):
+    a = dict(n=2, T=6, H=3, D=128, cu=0, k=4096, ks=384, v=4096, vs=384, dt=0, P=16, N=5, kc=4096,
+             kp=6144, vc=4096, vp=6144, ksc=4096, vsc=4096, tab=4096, w=4, ts=4, lens=4096)
+    a.update(kw)
+    return a
+
+
+def _rows_call(lib, fn, **kw):
+    a, P = _args(**kw), ctypes.c_void_p
+    return getattr(lib, fn)(a["n"], a["T"], a["H"], a["D"], P(a["cu"]), P(a["k"]), a["ks"],
+                            P(a["v"]), a["vs"], a["dt"], a["P"], a["N"], P(a["kc"]), a["kp"],
+                            P(a["vc"]), a["vp"], P(a["ksc"]), P(a["vsc"]), P(a["tab"]), a["w"],
+                            a["ts"], P(a["lens"]), P(0))
+
+
+COMMON = [
+    (SHAPE, dict(n=-1)), (SHAPE, dict(T=-1)), (SHAPE, dict(H=0)), (SHAPE, dict(N=-1)),
+    (SHAPE, dict(w=0)), (SHAPE, dict(T=7)), (SHAPE, dict(n=0)), (UNSUP, dict(D=64)),
+    (UNSUP, dict(dt=2)), (UNSUP, dict(dt=-1)), (UNSUP, dict(P=8)), (UNSUP, dict(P=24)),
+    (UNSUP, dict(P=512)), (UNSUP, dict(P=0)), (UNSUP, dict(H=1 << 15)),
+    (UNSUP, dict(N=1 << 31)), (UNSUP, dict(n=1 << 20, T=1 << 20, w=1 << 14, ts=1 << 14)),
+    (UNSUP, dict(T=(1 << 30) + 2)), (UNSUP, dict(kc=4100)), (UNSUP, dict(vp=6148)),
+    (STRIDE, dict(ts=-1)), (STRIDE, dict(ts=3)), (STRIDE, dict(kp=6128)), (STRIDE, dict(vp=-16)),
+    (NULLP, dict(tab=0)), (NULLP, dict(lens=0)), (NULLP, dict(kc=0)), (NULLP, dict(vc=0)),
+    (NULLP, dict(ksc=0)), (NULLP, dict(vsc=0)),
+]
+
+
+@pytest.mark.parametrize("want,kw", COMMON + [
+    (STRIDE, dict(ks=-1)), (STRIDE, dict(vs=-384)), (NULLP, dict(k=0)), (NULLP, dict(v=0)),
+    (OK, dict(T=0, k=0, v=0, tab=0, lens=0, kc=0)), (OK, dict(n=0, T=0)),
+    (OK, dict(N=0, kc=0, vc=0, ksc=0, vsc=0)),
+])
+def test_write_refusals(lib, want, kw):
+    assert _rows_call(lib, "kda_cache_write", **kw) == want
+
+
+@pytest.mark.parametrize("want,kw", COMMON + [
+    (STRIDE, dict(ks=383)), (STRIDE, dict(vs=100)), (STRIDE, dict(ks=-1)), (NULLP, dict(k=0)),
+    (NULLP, dict(v=0)), (OK, dict(T=0, k=0, v=0, tab=0, lens=0)),
+])
+def test_read_refusals(lib, want, kw):
+    assert _rows_call(lib, "kda_cache_read", **kw) == want
+
+
+def _attend(lib, host=None, **kw):
+    a, P = _args(Hq=6, q=4096, qs=768, o=4096, os=768, lse=0, ls=6, sc=0.1, ws=4096, wb=1 << 40,
+                 cuh=0), ctypes.c_void_p
+    a.update(kw)
+    if host is not None:
+        host = (ctypes.c_int32 * len(host))(*host)
+        a["cuh"], a["cu"] = ctypes.addressof(host), a["cu"] or 4096
+    return lib.kda_cache_attention(
+        a["n"], a["T"], a["Hq"], a["H"], a["D"], P(a["cuh"]), P(a["cu"]), P(a["q"]), a["qs"],
+        a["dt"], a["P"], a["N"], P(a["kc"]), a["kp"], P(a["vc"]), a["vp"], P(a["ksc"]),
+        P(a["vsc"]), P(a["tab"]), a["w"], a["ts"], P(a["lens"]), a["sc"], P(a["o"]), a["os"],
+        P(a["lse"]), a["ls"], P(a["ws"]), a["wb"], P(0))
+
+
+@pytest.mark.parametrize("want,kw", [x for x in COMMON if "H" not in x[1]] + [
+    (SHAPE, dict(Hq=0)), (SHAPE, dict(Hq=7)), (SHAPE, dict(H=0)), (SHAPE, dict(H=-3)),
+    (UNSUP, dict(Hq=771)), (UNSUP, dict(sc=float("nan"))), (UNSUP, dict(sc=float("inf"))),
+    (UNSUP, dict(ws=4100)), (WS, dict(wb=3)), (NULLP, dict(ws=0)), (NULLP, dict(q=0)),
+    (NULLP, dict(o=0)), (NULLP, dict(cu=4096)), (STRIDE, dict(qs=-1)), (STRIDE, dict(os=767)),
+    (STRIDE, dict(lse=4096, ls=5)), (STRIDE, dict(lse=4096, ls=-6)),
+    (SEQ, dict(host=[1, 2, 3])), (SEQ, dict(host=[0, 3, 2])), (SEQ, dict(host=[0, 3, 7])),
+    (OK, dict(host=[0, 0, 0])), (OK, dict(T=0, q=0, o=0, ws=0, wb=0)),
+])
+def test_attention_refusals(lib, want, kw):
+    assert _attend(lib, **kw) == want
+
+
+def test_workspace_size(lib):
+    size = kda.kda_cache_attention_workspace_size
+    assert size(0, 4, 8, 8) == 0 and size(1, 0, 8, 8) == 0
+    assert size(1, 1, 7, 2) == 0 and size(1, 1, 0, 0) == 0 and size(1, 1, 514, 2) == 0
+    for heads in ((12, 12), (64, 8), (6, 2), (40, 1)):
+        got = [size(n, n, *heads) for n in (1, 2, 63, 512, 5000)]
+        assert got == sorted(got) and got[0] > 0
+        got = [size(3, n, *heads) for n in (1, 2, 8, 17, 64, 1000, 1 << 20)]
+        assert got == sorted(got)  # one buffer serves every smaller call
+
+
+def test_binding_refuses(lib):
+    c = torch.zeros(3, 2, 16, 128, dtype=I8)
+    s, tab, lens = torch.ones(3, 2), torch.zeros(1, 3, dtype=I32), torch.ones(1, dtype=I32)
+    k = torch.zeros(1, 256, dtype=BF)
+    with pytest.raises(ValueError):  # not on a GPU
+        kda.kda_cache_write(k, k, c, c, s, s, tab, lens)
+    with pytest.raises(TypeError):
+        kda.kda_cache_write(k, k, c.float(), c.float(), s, s, tab, lens)
+    with pytest.raises(ValueError):
+        kda.kda_cache_read(k, k, c[0], c[0], s, s, tab, lens)
+
+
+# ---------------------------------------------------------------------------
+# definitions in 64 bits (CPU)
+
+def _value(codes, kind):
+    if kind == I8:
+        return codes.double()
+    b = codes.view(torch.uint8).long()
+    e, m = (b >> 3) & 15, (b & 7).double()
+    x = torch.where(e > 0, (1 + m / 8) * torch.exp2((e - 7).double()), m / 512)
+    x = torch.where((b & 127) == 127, torch.nan, x)
+    return torch.where(b >= 128, -x, x)
+
+
+def _nearest(x, kind):
+    if kind == I8:
+        return torch.nan_to_num(x.round().clamp(-127, 127), nan=0.0)
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(2.0 ** -6, 512))) - 3)
+    return ((x / step).round() * step).clamp(-448, 448)
+
+
+def _need(x, kind):
+    """The scale for rows x [H, tokens, 128], by trial: no logarithm rounds here."""
+    a = torch.where(x.isfinite(), x.abs(), 0.0).amax((1, 2))
+    out = []
+    for top in a.tolist():
+        e = -100
+        while top > (448.0 if kind == F8 else 127.0) * 2.0 ** e:
+            e += 1
+        out.append(2.0 ** e)
+    return torch.tensor(out, dtype=torch.float64)
+
+
+class Pool:
+    """A cache with everything that no sequence owns poisoned, and its mirror in 64 bits:
+    `code` [2][N, H, P, 128] and `scale` [2][N, H]."""
+
+    def __init__(self, kind, H, P, totals, seed=0, spare=3, pad=0, width=None):
+        g = torch.Generator().manual_seed(seed)
+        self.kind, self.H, self.P, self.g = kind, H, P, g
+        used = [-(-max(x, 0) // P) for x in totals]
+        self.N = N = sum(used) + spare
+        self.width = width or max(used + [1])
+        order = torch.randperm(N, generator=g).tolist()
+        self.table = torch.full((len(totals), self.width), 2 ** 31 - 1, dtype=torch.int64)
+        for b, n in enumerate(used):
+            for j in range(min(n, self.width)):
+                self.table[b, j] = order.pop()
+        poison = 0x7f if kind == F8 else 77
+        size = H * P * 128 + pad
+        self.raw = [torch.full((N * size + 16,), poison, dtype=torch.uint8) for _ in range(2)]
+        self.shape, self.strides = (N, H, P, 128), (size, P * 128, 128, 1)
+        self.scale = [torch.full((N, H), torch.nan) for _ in range(2)]
+        self.lens = torch.tensor(totals, dtype=torch.int64)
+
+    def fill(self, tokens=None):
+        """Random codes and scales for each sequence's first tokens (all: None)."""
+        for side in range(2):
+            c = self.codes(self.raw)[side]
+            for b, n in enumerate(self.lens.tolist() if tokens is None else tokens):
+                for j in range(-(-max(n, 0) // self.P)):
+                    page = self.table[b, j].item()
+                    if not 0 <= page < self.N:
+                        continue
+                    z = min(self.P, n - j * self.P)
+                    x = torch.randn(self.H, z, 128, generator=self.g) * \
+                        (40.0 if self.kind == F8 else 35.0)
+                    y = x.clamp(-448, 448).to(F8) if self.kind == F8 else \
+                        x.round().clamp(-127, 127).to(I8)
+                    c[page, :, :z] = y.view(torch.uint8)
+                    self.scale[side][page] = torch.exp2(
+                        torch.randint(-7, -4, (self.H,), generator=self.g).float())
+        return self
+
+    def codes(self, raw):
+        return [r.as_strided(self.shape, self.strides) for r in raw]
+
+    def gpu(self):
+        """k_cache, v_cache, k_scale, v_scale, page_table, kv_lens for a call."""
+        self.dev = [r.cuda() for r in self.raw]
+        caches = [c.view(self.kind) for c in self.codes(self.dev)]
+        self.dev_scale = [s.cuda() for s in self.scale]
+        return (*caches, *self.dev_scale, self.table.to(I32).cuda(), self.lens.to(I32).cuda())
+
+    def tokens(self, side, b, n):
+        """Values of positions 0 .. n - 1 [n, H, 128], and whether they exist."""
+        x = torch.zeros(max(n, 0), self.H, 128, dtype=torch.float64)
+        real = torch.zeros(max(n, 0), dtype=torch.bool)
+        c = self.codes(self.raw)[side]
+        for j in range(-(-max(n, 0) // self.P)):
+            page, z = self.table[b, j].item(), min(self.P, n - j * self.P)
+            if 0 <= page < self.N:
+                y = _value(c[page, :, :z].contiguous().view(self.kind), self.kind)
+                x[j * self.P:j * self.P + z] = \
+                    (y * self.scale[side][page].double()[:, None, None]).transpose(0, 1)
+                real[j * self.P:j * self.P + z] = True
+        return x, real
+
+    def cap(self):
+        return self.width * self.P
+
+
+def _ref_attention(pool, q, counts, G, scale, weight):
+    """out, lse and their tolerances [T, Hq, ..]; q fp64 [T, Hq, 128]."""
+    T, Hq = q.shape[:2]
+    out, tol = torch.zeros(T, Hq, 128, dtype=torch.float64), torch.zeros(T, Hq, 128).double()
+    lse, lt = torch.full((T, Hq), -torch.inf).double(), torch.zeros(T, Hq).double()
+    at = 0
+    for b, n in enumerate(counts):
+        total = pool.lens[b].item()
+        active = n > 0 and n <= total <= pool.cap()
+        if active:
+            keys, there = pool.tokens(0, b, total)
+            values, _ = pool.tokens(1, b, total)
+        for i in range(n):
+            row, see = at + i, total - n + i + 1
+            if not active or not there[:see].any():
+                continue
+            k, v, real = keys[:see], values[:see], there[:see]
+            for h in range(Hq):
+                kh, vh = k[real][:, h // G], v[real][:, h // G]
+                s = scale * (kh @ q[row, h])
+                d = 131 * 2.0 ** -24 * abs(scale) * (kh.abs() @ q[row, h].abs()).max()
+                lse[row, h] = torch.logsumexp(s, 0)
+                p = torch.exp(s - lse[row, h])
+                out[row, h] = p @ vh
+                m = len(s)
+                tol[row, h] = 2.0 ** -8 * out[row, h].abs() + \
+                    (weight + 2 * d + m * 2.0 ** -23 + 2.0 ** -20) * (p @ vh.nan_to_num(0.0).abs()) + \
+                    m * 2.0 ** -125 * vh.abs().nan_to_num(0.0).max()
+                lt[row, h] = d + m * 2.0 ** -24 + 2.0 ** -21 * (1 + lse[row, h].abs())
+        at += n
+    return out, lse, tol, lt
+
+
+def _close(got, want, tol):
+    got, want = got.double().cpu(), want
+    fine = (got - want).abs() <= tol
+    same = (got == want) | (got.isnan() & want.isnan())  # infinities, NaN
+    off = int((~(fine | same)).sum())
+    assert off == 0, f"{off} of {got.numel()} off, worst {(got - want).abs().max()}"
+
+
+def _cu(counts):
+    cu = [0]
+    for n in counts:
+        cu.append(cu[-1] + n)
+    return torch.tensor(cu, dtype=I32)
+
+
+def _strided(t, pad, offset):
+    """The same values on the GPU, rows `pad` elements further apart, from `offset` on."""
+    n = t.shape[1]
+    buf = torch.full((offset + max(t.shape[0], 1) * (n + pad),), -7.0, dtype=t.dtype,
+                     device="cuda")
+    view = buf[offset:].as_strided(tuple(t.shape), (n + pad, 1))
+    view.copy_(t)
+    return view, buf
+
+
+# ---------------------------------------------------------------------------
+# writing and reading
+
+def _ref_write(pool, x, counts):
+    """The definition, page by page, into pool.raw and pool.scale. x: [2][T, H, 128] fp64."""
+    for side in range(2):
+        c, at = pool.codes(pool.raw)[side], 0
+        for b, n in enumerate(counts):
+            end = pool.lens[b].item()
+            first, at = at, at + n
+            if end < n or end > pool.cap():
+                continue
+            pos = end - n
+            while pos < end:
+                page, a = pool.table[b, pos // pool.P].item(), pos % pool.P
+                z = min(pool.P, a + end - pos)
+                rows = x[side][first:first + z - a].transpose(0, 1)
+                first, pos = first + z - a, pos + z - a
+                if not 0 <= page < pool.N:
+                    continue
+                s = _need(rows, pool.kind)
+                if a:
+                    old = pool.scale[side][page].double()
+                    s = torch.maximum(s, old)
+                    y = _value(c[page, :, :a].contiguous().view(pool.kind), pool.kind)
+                    y = torch.where((s > old)[:, None, None],
+                                    _nearest(y * (old / s)[:, None, None], pool.kind), y)
+                    c[page, :, :a] = y.float().to(pool.kind).view(torch.uint8)
+                y = _nearest(rows / s[:, None, None], pool.kind).float()
+                c[page, :, a:z] = y.to(pool.kind).view(torch.uint8)
+                pool.scale[side][page] = s.float()
+
+
+def _tokens(T, H, g, spread=3):
+    """Keys or values whose size changes from token to token and head to head."""
+    x = torch.randn(T, H, 128, generator=g)
+    return (x * torch.exp2(torch.randint(-spread, spread + 1, (T, H, 1), generator=g).float())).to(BF)
+
+
+def _check_write(pool, k, v, counts, uniform, pad=0, offset=0):
+    H, T = pool.H, k.shape[0]
+    cache = pool.gpu()
+    kd, _ = _strided(k.reshape(T, -1), pad, offset)
+    vd, _ = _strided(v.reshape(T, -1), 2 * pad, offset)
+    kda.kda_cache_write(kd, vd, *cache, cu_seqlens=None if uniform else _cu(counts).cuda())
+    _ref_write(pool, [k.double(), v.double()], counts)
+    for side in range(2):
+        got = pool.dev[side].cpu()
+        if pool.kind == F8:  # a NaN has two codes
+            nan = ((got & 127) == 127) & ((pool.raw[side] & 127) == 127)
+            assert torch.equal(torch.where(nan, 0, got), torch.where(nan, 0, pool.raw[side]))
+        else:
+            assert torch.equal(got, pool.raw[side])
+        assert torch.equal(pool.dev_scale[side].cpu().nan_to_num(-1), pool.scale[side].nan_to_num(-1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("T", [1, 4, 5, 17, 70, 300])
+def test_write_uniform(lib, kind, P, T):
+    totals = [T, T + 1, T + P - 1, T + P, T + 2 * P + 3]
+    pool = Pool(kind, 3, P, totals, seed=T, pad=16).fill([x - T for x in totals])
+    g = torch.Generator().manual_seed(P)
+    _check_write(pool, _tokens(T * 5, 3, g), _tokens(T * 5, 3, g), [T] * 5, True, pad=6, offset=3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 64, 256])
+@pytest.mark.parametrize("H", [1, 5])
+def test_write_ragged(lib, kind, P, H):
+    counts = [0, 1, 300, 0, 16, 15, 33, 0, 129, 2]
+    past = [5, 0, 9, 0, 64, 17, 0, 3, 255, 31]
+    totals = [a + b for a, b in zip(counts, past)]
+    pool = Pool(kind, H, P, totals, seed=1).fill(past)
+    g = torch.Generator().manual_seed(P + H)
+    T = sum(counts) + 3  # rows behind the last sequence
+    _check_write(pool, _tokens(T, H, g), _tokens(T, H, g), counts, False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [63, 64, 65, 130, 4100])
+def test_write_many_sequences(lib, n):
+    g = torch.Generator().manual_seed(n)
+    counts = torch.randint(0, 4, (n,), generator=g).tolist()
+    past = torch.randint(0, 40, (n,), generator=g).tolist()
+    pool = Pool(F8, 1, 16, [a + b for a, b in zip(counts, past)], seed=2).fill(past)
+    T = sum(counts)
+    _check_write(pool, _tokens(T, 1, g), _tokens(T, 1, g), counts, False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_write_bad_values_and_sequences(lib, kind):
+    """Infinities, NaN, zeros, the smallest and largest values; inactive sequences; pages
+    that do not exist."""
+    totals = [40, 0, 7, 5000, -3, 20, 33]
+    counts = [33, 2, 8, 4, 1, 20, 3]
+    pool = Pool(kind, 2, 16, [40, 0, 16, 48, 0, 20, 33], seed=3, width=3).fill()
+    pool.lens = torch.tensor(totals)
+    pool.table[0, 1] = -1
+    pool.table[5, 0] = pool.N
+    g = torch.Generator().manual_seed(4)
+    T = sum(counts)
+    k, v = _tokens(T, 2, g), _tokens(T, 2, g)
+    k[0] = 0.0
+    k[5, 0, 3], k[6, 1, 0], v[30, 0, 127] = torch.inf, -torch.inf, torch.nan
+    v[31, 1, 0], k[-1], v[-1, 0] = 3.3e38, 1e-40, 2.0 ** -133
+    k[-2], v[-2], k[-3], v[-3] = 0.0, 0.0, 0.0, -0.0
+    _check_write(pool, k, v, counts, False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 128])
+def test_write_token_by_token(lib, kind, P):
+    """A decode loop: scales grow, earlier codes follow, as the definition says call by call."""
+    g = torch.Generator().manual_seed(5)
+    pool = Pool(kind, 2, P, [40, 23], seed=6)
+    pool.lens = torch.zeros(2, dtype=torch.int64)
+    cache = pool.gpu()
+    for t in range(23):
+        pool.lens = torch.tensor([t + 1, t + 1])
+        k, v = _tokens(2, 2, g, spread=6), _tokens(2, 2, g, spread=6)
+        kda.kda_cache_write(k.reshape(2, -1).cuda(), v.reshape(2, -1).cuda(), *cache[:5],
+                            pool.lens.to(I32).cuda())
+        _ref_write(pool, [k.double(), v.double()], [1, 1])
+    for side in range(2):
+        assert torch.equal(pool.dev[side].cpu(), pool.raw[side])
+        assert torch.equal(pool.dev_scale[side].cpu().nan_to_num(-1), pool.scale[side].nan_to_num(-1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("H", [1, 3])
+def test_read(lib, kind, P, H):
+    """Ragged ranges, inactive sequences, pages that do not exist, odd strides; rows behind the
+    last sequence and the space between rows stay as they were."""
+    counts = [0, 1, 300, 16, 15, 33, 4, 129, 2]
+    totals = [5, 1, 309, 80, 32, 33, 3, 400, 70]
+    pool = Pool(kind, H, P, totals, seed=7, pad=32).fill()
+    pool.table[2, 0] = -5
+    pool.table[7, min(1, pool.width - 1)] = pool.N + 1
+    pool.lens[6], pool.lens[8] = 3, 100000  # shorter than its tokens; longer than its table
+    T = sum(counts) + 2
+    seen, bufs = [], []
+    for off in (1, 4):
+        t, buf = _strided(torch.full((T, H * 128), -7.0, dtype=BF), 5, off)
+        seen.append(t)
+        bufs.append(buf)
+    kda.kda_cache_read(*seen, *pool.gpu(), cu_seqlens=_cu(counts).cuda())
+    for side, off in ((0, 1), (1, 4)):
+        want = torch.full((T, H * 128), -7.0).double()
+        at = 0
+        for b, n in enumerate(counts):
+            total = pool.lens[b].item()
+            want[at:at + n] = 0.0
+            if n <= total <= pool.cap():
+                want[at:at + n] = pool.tokens(side, b, total)[0][total - n:].reshape(n, H * 128)
+            at += n
+        assert torch.equal(seen[side].double().cpu(), want)
+        whole = bufs[side][off:].cpu().reshape(T, -1)
+        assert (whole[:, H * 128:] == -7).all() and (bufs[side][:off] == -7).all()
+
+
+@pytest.mark.gpu
+def test_write_then_read_returns_the_rounded_tokens(lib):
+    """e4m3: within half a step, 2^-4 of the value, or half of the smallest step under the
+    page's scale; int8 within half its step."""
+    for kind in KINDS:
+        pool = Pool(kind, 4, 64, [200, 77], seed=8)
+        cache = pool.gpu()
+        g = torch.Generator().manual_seed(9)
+        k, v = _tokens(277, 4, g, spread=0), _tokens(277, 4, g, spread=0)
+        cu = _cu([200, 77]).cuda()
+        kda.kda_cache_write(k.reshape(277, -1).cuda(), v.reshape(277, -1).cuda(), *cache,
+                            cu_seqlens=cu)
+        got = [torch.empty(277, 512, dtype=BF, device="cuda") for _ in range(2)]
+        kda.kda_cache_read(*got, *cache, cu_seqlens=cu)
+        for x, y in zip((k, v), got):
+            x, y = x.double().reshape(277, -1), y.double().cpu()
+            top = x.abs().max()
+            tol = 2.0 ** -4 * x.abs() + 2.0 ** -10 * top / 224 if kind == F8 else top / 63
+            assert ((x - y).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------------------
+# attention
+
+def _check_attention(pool, counts, G, uniform, scale=128 ** -0.5, weight=2.0 ** -16, pad=0,
+                     offset=0, seed=0, size=1.0, extra=0, q=None):
+    T, Hq = sum(counts) + extra, pool.H * G
+    g = torch.Generator().manual_seed(seed)
+    if q is None:
+        q = (torch.randn(T, Hq, 128, generator=g) * size).to(BF)
+    qd, _ = _strided(q.reshape(T, -1), pad, offset)
+    out, buf = _strided(torch.full((T, Hq * 128), -7.0, dtype=BF), 2 * pad, offset)
+    lse, lbuf = _strided(torch.full((T, Hq), -7.0), pad, 0)
+    cu = None if uniform else _cu(counts)
+    kda.kda_cache_attention(qd, out, *pool.gpu(), cu_seqlens_host=cu,
+                            cu_seqlens=None if uniform else cu.cuda(), lse=lse, scale=scale)
+    want, wl, tol, lt = _ref_attention(pool, q.double(), counts, G, scale, weight)
+    n = T - extra
+    _close(out[:n].reshape(n, Hq, 128), want[:n], tol[:n])
+    _close(lse[:n], wl[:n], lt[:n])
+    assert (out[n:] == -7).all() and (lse[n:] == -7).all()
+    assert (buf[:offset] == -7).all()
+    assert (buf[offset:].reshape(T, -1)[:, Hq * 128:] == -7).all()
+    assert (lbuf.reshape(T, -1)[:, Hq:] == -7).all()
+    return out, lse
+
+
+EDGES = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 400]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("H,G", [(3, 1), (2, 3), (1, 8), (1, 16)])
+def test_attention_one_token(lib, kind, P, H, G):
+    pool = Pool(kind, H, P, EDGES, seed=P + G, pad=48).fill()
+    _check_attention(pool, [1] * len(EDGES), G, True, pad=3, offset=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [2, 3, 5, 8])
+@pytest.mark.parametrize("H,G", [(2, 1), (1, 3), (1, 8)])
+def test_attention_draft_tokens(lib, kind, T, H, G):
+    totals = [T + x for x in (0, 1, 13, 16, 27, 32, 120, 128, 250)]
+    for P in (16, 64):
+        pool = Pool(kind, H, P, totals, seed=T + G).fill()
+        _check_attention(pool, [T] * len(totals), G, True, seed=T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_parts(lib, kind):
+    """Long caches are cut into parts: one long sequence, and one beside short and empty ones."""
+    for totals, H, G, P in (([5003], 1, 2, 64), ([3000, 1, 40, 0, 900], 2, 1, 16),
+                            ([2049], 2, 8, 256)):
+        pool = Pool(kind, H, P, totals, seed=11).fill()
+        _check_attention(pool, [1] * len(totals), G, True, seed=12, size=2.0)
+
+
+@pytest.mark.gpu
+def test_attention_parts_of_draft_tokens(lib):
+    """The last parts are seen by some of the rows only."""
+    for total in (1025, 1030, 1281):
+        pool = Pool(F8, 1, 64, [total, 600], seed=13).fill()
+        _check_attention(pool, [8, 8], 2, True, seed=14)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [63, 64, 65, 200])
+def test_attention_many_sequences(lib, n):
+    g = torch.Generator().manual_seed(n)
+    totals = torch.randint(1, 90, (n,), generator=g).tolist()
+    totals[n // 2] = 700
+    pool = Pool(I8, 1, 16, totals, seed=15).fill()
+    _check_attention(pool, [1] * n, 2, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [1, 4])
+def test_attention_inactive_and_missing(lib, kind, T):
+    """Inactive sequences and tokens without any key give zeros and -infinity; pages that do
+    not exist are left out."""
+    totals = [40, 0, T - 1, 5000, -3, 20, 48, 33]
+    pool = Pool(kind, 2, 16, [40, 0, 16, 48, 0, 20, 48, 33], seed=16, width=3).fill()
+    pool.lens = torch.tensor(totals)
+    pool.table[0, 1] = -1
+    pool.table[5] = pool.N
+    pool.table[6, 2] = 1 << 30
+    pool.table[7, 0] = -(1 << 31)
+    out, lse = _check_attention(pool, [T] * 8, 3, True)
+    for b in (1, 2, 3, 4, 5):
+        assert (out[b * T:(b + 1) * T] == 0).all()
+        assert (lse[b * T:(b + 1) * T] == -torch.inf).all()
+
+
+@pytest.mark.gpu
+def test_attention_of_an_empty_pool(lib):
+    pool = Pool(F8, 2, 16, [0, 0], spare=0)
+    pool.lens = torch.tensor([5, 16])
+    _check_attention(pool, [1, 1], 2, True)
+    _check_attention(pool, [3, 40], 2, False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 4, 8])
+def test_attention_nan_of_hidden_tokens(lib, T):
+    """A NaN key or value reaches exactly the rows that see it."""
+    for total in (9, 40, 300):
+        for what in range(2):
+            pool = Pool(F8, 1, 64, [total], seed=17).fill()
+            at = total - 1 - T // 3
+            page, slot = pool.table[0, at // 64].item(), at % 64
+            pool.codes(pool.raw)[what][page, 0, slot, 5] = 0xff
+            out, _ = _check_attention(pool, [T], 2, True, seed=18)
+            sees = torch.arange(total - T, total) >= at
+            assert torch.equal(out.isnan().any(1).cpu(), sees)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_attention_scales(lib, scale):
+    """No weight but equal ones, keys of least product first, and weights that all but vanish."""
+    pool = Pool(F8, 2, 32, [70, 333], seed=19).fill()
+    _check_attention(pool, [1, 1], 3, True, scale=scale, size=3.0)
+
+
+@pytest.mark.gpu
+def test_attention_scores_that_rise(lib):
+    """The reference exponent has to follow: keys that grow along the sequence, and fall."""
+    for rise in (1, -1):
+        pool = Pool(I8, 1, 16, [600], seed=20).fill()
+        order = pool.table[0] if rise > 0 else pool.table[0].flip(0)
+        for j, page in enumerate(order.tolist()):
+            pool.scale[0][page] = 2.0 ** (j // 3 - 8)
+        _check_attention(pool, [1], 8, True, seed=21)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 64, 256])
+@pytest.mark.parametrize("H,G", [(2, 1), (1, 5), (1, 16)])
+def test_attention_documents(lib, kind, P, H, G):
+    """Packed documents of odd lengths, from their start and over earlier tokens, beside single
+    tokens and empty ones; rows behind the last are left as they were."""
+    counts = [1, 130, 0, 33, 64, 5, 200, 1]
+    past = [0, 0, 7, 100, 64, 31, 57, 150]
+    totals = [a + b for a, b in zip(counts, past)]
+    pool = Pool(kind, H, P, totals, seed=22, pad=16).fill()
+    _check_attention(pool, counts, G, False, weight=2.0 ** -8, pad=5, offset=3, seed=23, extra=2)
+
+
+@pytest.mark.gpu
+def test_attention_document_inactive_and_missing(lib):
+    counts, totals = [70, 90, 40, 65], [69, 5000, 100, 200]
+    pool = Pool(F8, 1, 16, [69, 100, 100, 200], seed=24, width=13).fill()
+    pool.lens = torch.tensor(totals)
+    pool.table[2, 2], pool.table[2, 6], pool.table[3] = -1, pool.N, -7
+    out, lse = _check_attention(pool, counts, 2, False, weight=2.0 ** -8)
+    assert (out[:160] == 0).all() and (lse[:160] == -torch.inf).all()
+    assert (out[200:] == 0).all() and (lse[200:] == -torch.inf).all()
+
+
+@pytest.mark.gpu
+def test_attention_document_nan(lib):
+    """A NaN key or value in a document reaches exactly the rows that see it."""
+    for n, total in ((150, 150), (100, 237)):
+        for what in range(2):
+            pool = Pool(F8, 1, 64, [total], seed=25).fill()
+            at = total - 40
+            page, slot = pool.table[0, at // 64].item(), at % 64
+            pool.codes(pool.raw)[what][page, 0, slot, 5] = 0x7f
+            out, _ = _check_attention(pool, [n], 3, False, weight=2.0 ** -8, seed=26)
+            assert torch.equal(out.isnan().any(1).cpu(), torch.arange(total - n, total) >= at)
