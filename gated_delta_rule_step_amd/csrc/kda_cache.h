@@ -77,6 +77,19 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
 }
 
+// Bytes of four tokens' words to one word of four tokens per channel.
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                           uint32_t (&o)[4]) {
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u);  // a0 b0 a1 b1
+  const uint32_t AB = __builtin_amdgcn_perm(b, a, 0x07030602u);  // a2 b2 a3 b3
+  const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x05010400u);
+  const uint32_t CD = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
+}
+
 __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }

@@ -42,7 +42,7 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, int
   int32_t chunk = kWhole;
   if (p.targets > 0) {
     int32_t sum = 0;
-    for (int32_t b = lane; b < B; b += 64) sum += units_of(p.c, b);
+    for (int32_t b = lane; b < B; b += 64) sum += is_few(p, b) ? units_of(p.c, b) : 0;
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s);
     chunk = max(kMinUnits, (sum + p.targets - 1) / p.targets);
@@ -50,8 +50,9 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, int
   int32_t items = 0, slots = 0;
   for (int32_t b0 = 0; b0 < B; b0 += 64) {
     const int32_t b = b0 + lane;
-    const int32_t units = b < B ? units_of(p.c, b) : 0;
-    const int32_t n = b < B ? max((units + chunk - 1) / chunk, 1) : 0;
+    const bool few = b < B && is_few(p, b);
+    const int32_t units = few ? units_of(p.c, b) : 0;
+    const int32_t n = few ? max((units + chunk - 1) / chunk, 1) : 0;
     const int32_t s = n > 1 ? n : 0;
     int32_t ni = n, si = s;  // inclusive prefix sums
 #pragma unroll
@@ -116,19 +117,6 @@ __device__ __forceinline__ void load_step(const AttnParams& p, int32_t b, int32_
   }
 }
 
-// Bytes of four tokens' words to one word of four tokens per channel.
-__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
-                                           uint32_t (&o)[4]) {
-  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u);  // a0 b0 a1 b1
-  const uint32_t AB = __builtin_amdgcn_perm(b, a, 0x07030602u);  // a2 b2 a3 b3
-  const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x05010400u);
-  const uint32_t CD = __builtin_amdgcn_perm(d, c, 0x07030602u);
-  o[0] = __builtin_amdgcn_perm(cd, ab, 0x05040100u);
-  o[1] = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
-  o[2] = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
-  o[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
-}
-
 __device__ __forceinline__ float over_groups_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16));
   return fmaxf(x, __shfl_xor(x, 32));
@@ -184,9 +172,9 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
   Part part;
   if (!find_part(p, item, lane, part)) return;
   const Seq seq = sequence(p.c, part.b);
-  if (p.plan && hb == 0 && part.index == 0 && threadIdx.x == 0)
+  if (hb == 0 && part.index == 0 && threadIdx.x == 0)
     p.plan[part.b] = make_int2(part.slot, part.parts);
-  const int rows = int(min(int64_t(p.G) * seq.n, int64_t(p.most_rows))), row0 = rb * 16 * NT;
+  const int rows = rows_of(p, part.b), row0 = rb * 16 * NT;
   if (row0 >= rows) return;
   const int32_t len = p.c.num_pages > 0 ? max(seq.len, 0) : 0;
   const int32_t to = min(part.to, len);
@@ -368,11 +356,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = (p.most_rows * p.c.H + 3) / 4;
   const int b = blockIdx.x / per, i = (blockIdx.x - b * per) * 4 + wave;
+  if (i >= p.most_rows * p.c.H || !is_few(p, b)) return;
   const int2 plan = p.plan[b];
-  if (plan.y <= 1 || i >= p.most_rows * p.c.H) return;
   const Seq seq = sequence(p.c, b);
   const int r = i / p.c.H, h = i - r * p.c.H;
-  if (r >= p.G * seq.n) return;
+  if (plan.y <= 1 || r >= p.G * seq.n) return;
   const int64_t first = (int64_t(plan.x) * p.c.H + h) * p.most_rows + r;
   const int64_t step = int64_t(p.c.H) * p.most_rows;
   float top = -INFINITY;
@@ -405,25 +393,23 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
 
 // Host: the plan of a call.
 constexpr int64_t kGroups = 1024;  // workgroups that the cut aims at
-constexpr int32_t kCutRows = 64;   // sequences with more rows are not cut
+constexpr int32_t kFewRows = 64;   // sequences with more rows are documents
 
 struct Plan {
-  int32_t n_most, tiles, row_blocks, targets;
-  int64_t plan_bytes, slots, bytes;
+  int32_t tiles, row_blocks, targets;
+  int64_t plan_bytes, stat_bytes, bytes;
 };
-Plan make_plan(int32_t n_seqs, int64_t n_most, int32_t G, int32_t H) {
+// Sequences of at most `rows` <= kFewRows rows for each of H key/value heads.
+Plan make_plan(int32_t n_seqs, int32_t rows, int32_t H) {
   Plan r;
-  r.n_most = int32_t(n_most);
-  const int64_t rows = G * n_most;
   r.tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  r.row_blocks = int32_t((rows + 16 * r.tiles - 1) / (16 * r.tiles));
-  r.targets = rows > kCutRows ? 0
-                              : int32_t(std::max<int64_t>(1, kGroups / (int64_t(H) * r.row_blocks)));
-  // a cut sequence has at most twice its share of the parts
-  r.slots = r.targets > 0 ? 2 * int64_t(r.targets) : 0;
+  r.row_blocks = (rows + 16 * r.tiles - 1) / (16 * r.tiles);
+  r.targets = int32_t(std::max<int64_t>(1, kGroups / (int64_t(H) * r.row_blocks)));
+  // a cut sequence has less than twice its share of the parts
+  const int64_t vecs = 2 * int64_t(r.targets) * H * rows;
   r.plan_bytes = (int64_t(n_seqs) * 8 + 255) / 256 * 256;
-  const int64_t vec = r.slots * H * rows;
-  r.bytes = r.targets > 0 ? r.plan_bytes + (vec * 8 + 255) / 256 * 256 + vec * D * 4 : 0;
+  r.stat_bytes = (vecs * 8 + 255) / 256 * 256;
+  r.bytes = r.plan_bytes + r.stat_bytes + vecs * D * 4;
   return r;
 }
 
@@ -453,8 +439,8 @@ extern "C" size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t tot
   // the largest that any split of the tokens over the sequences needs
   const int32_t G = H_q / H_kv;
   int64_t most = 0;
-  for (int64_t n = 1; n <= total_tokens && n * G <= kc::kCutRows; ++n)
-    most = std::max(most, kc::make_plan(n_seqs, n, G, H_kv).bytes);
+  for (int64_t n = 1; n <= total_tokens && n * G <= kc::kFewRows; ++n)
+    most = std::max(most, kc::make_plan(n_seqs, int32_t(n * G), H_kv).bytes);
   return size_t(most);
 }
 
@@ -482,27 +468,41 @@ extern "C" kda_status kda_cache_attention(
   if (total_tokens == 0) return KDA_OK;
   if (!q || !out) return KDA_ERR_NULL_POINTER;
   if ((cu_seqlens != nullptr) != (cu_seqlens_host != nullptr)) return KDA_ERR_NULL_POINTER;
-  int64_t n_most = p.c.per_seq;
+  p.G = H_q / H_kv;
+  // the most rows of few-token sequences, of documents, and the documents' blocks
+  int64_t few = 0, most = 0, blocks = 0;
+  const auto note = [&](int64_t n, int64_t times) {
+    const int64_t rows = n * p.G;
+    if (rows <= kc::kFewRows) {
+      few = std::max(few, rows);
+    } else {
+      most = std::max(most, rows);
+      blocks += (rows + kc::kDocRows - 1) / kc::kDocRows * times;
+    }
+  };
   if (cu_seqlens_host) {
     if (cu_seqlens_host[0] != 0 || cu_seqlens_host[n_seqs] > total_tokens) return KDA_ERR_BAD_SEQLENS;
     for (int32_t b = 0; b < n_seqs; ++b) {
       const int64_t n = int64_t(cu_seqlens_host[b + 1]) - cu_seqlens_host[b];
       if (n < 0) return KDA_ERR_BAD_SEQLENS;
-      n_most = std::max(n_most, n);
+      note(n, 1);
     }
-    if (n_most == 0) return KDA_OK;
+  } else {
+    note(p.c.per_seq, n_seqs);
   }
-  p.G = H_q / H_kv;
-  const kc::Plan plan = kc::make_plan(n_seqs, n_most, p.G, H_kv);
-  if (p.G * n_most > INT32_MAX) return KDA_ERR_UNSUPPORTED;
-  const int64_t grid = (int64_t(plan.targets) + n_seqs) * H_kv * plan.row_blocks;
-  const int64_t joins = (int64_t(p.G) * n_most * H_kv + 3) / 4 * n_seqs;
-  if (grid > INT32_MAX || (plan.targets > 0 && joins > INT32_MAX)) return KDA_ERR_UNSUPPORTED;
-  if (plan.bytes > 0) {
+  kc::Plan plan = {};
+  int64_t grid = 0, joins = 0;
+  if (few > 0) {
+    plan = kc::make_plan(n_seqs, int32_t(few), H_kv);
+    grid = (int64_t(plan.targets) + n_seqs) * H_kv * plan.row_blocks;
+    joins = (few * H_kv + 3) / 4 * n_seqs;
     if (workspace_bytes < size_t(plan.bytes)) return KDA_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace) return KDA_ERR_NULL_POINTER;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KDA_ERR_UNSUPPORTED;
   }
+  if (grid > INT32_MAX || joins > INT32_MAX || most > INT32_MAX - kc::kDocRows ||
+      blocks * H_kv > INT32_MAX)
+    return KDA_ERR_UNSUPPORTED;
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_row_stride;
   p.scale2 = scale * kda::LOG2E;
@@ -510,27 +510,29 @@ extern "C" kda_status kda_cache_attention(
   p.out_stride = out_row_stride;
   p.lse = lse;
   p.lse_stride = lse_row_stride;
+  p.few_rows = kc::kFewRows;
   p.row_blocks = plan.row_blocks;
-  p.most_rows = int32_t(p.G * n_most);
   p.targets = plan.targets;
-  p.plan = nullptr;
-  p.stat = nullptr;
-  p.part = nullptr;
-  if (plan.bytes > 0) {
-    uint8_t* const ws = static_cast<uint8_t*>(workspace);
-    const int64_t vec = plan.slots * H_kv * p.most_rows;
-    p.plan = reinterpret_cast<int2*>(ws);
-    p.stat = reinterpret_cast<float2*>(ws + plan.plan_bytes);
-    p.part = reinterpret_cast<float*>(ws + plan.plan_bytes + (vec * 8 + 255) / 256 * 256);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  p.plan = reinterpret_cast<int2*>(ws);
+  p.stat = reinterpret_cast<float2*>(ws + plan.plan_bytes);
+  p.part = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.stat_bytes);
+  const bool int8 = cache_dtype == KDA_CACHE_INT8;
+  if (few > 0) {
+    p.most_rows = int32_t(few);
+    if ((int8 ? kc::launch_attend<kc::kInt8>(p, plan, unsigned(grid), stream)
+              : kc::launch_attend<kc::kFp8>(p, plan, unsigned(grid), stream)) != hipSuccess)
+      return KDA_ERR_LAUNCH;
+    // no part is cut where the table is too short for two
+    if (int64_t(table_width) * page_size > kc::kMinUnits * kc::kUnit) {
+      hipLaunchKernelGGL(kc::join_kernel, dim3(unsigned(joins)), dim3(kc::kThreads), 0, stream, p);
+      if (hipGetLastError() != hipSuccess) return KDA_ERR_LAUNCH;
+    }
   }
-  hipError_t e = cache_dtype == KDA_CACHE_FP8
-                     ? kc::launch_attend<kc::kFp8>(p, plan, unsigned(grid), stream)
-                     : kc::launch_attend<kc::kInt8>(p, plan, unsigned(grid), stream);
-  if (e != hipSuccess) return KDA_ERR_LAUNCH;
-  // no part is cut where the table is too short for two
-  if (plan.targets > 0 && int64_t(table_width) * page_size > kc::kMinUnits * kc::kUnit) {
-    hipLaunchKernelGGL(kc::join_kernel, dim3(unsigned(joins)), dim3(kc::kThreads), 0, stream, p);
-    if (hipGetLastError() != hipSuccess) return KDA_ERR_LAUNCH;
+  if (blocks > 0) {
+    p.most_rows = int32_t(most);
+    if (kc::launch_documents(p, int8, unsigned(blocks * H_kv), stream) != hipSuccess)
+      return KDA_ERR_LAUNCH;
   }
   return KDA_OK;
 }
