@@ -620,71 +620,90 @@ def kda_rmsnorm_backward(z, weight, dy, dz, dweight=None, gate=None, dgate=None,
             _adr(dgate), dgs, _adr(dweight), _adr(workspace), ws_bytes)
 
 
-def _cache_geometry(k_cache, v_cache, k_scale, v_scale, page_table, kv_lens):
-    """Checks of a paged cache and its tables; the C arguments between the dtype and the
-    tables, those of the tables, the head count, and the tensors by name."""
-    import torch
-    if k_cache.dim() != 4 or k_cache.shape[3] != HEAD_DIM:
-        raise ValueError(f"k_cache must be [pages, H, page_size, 128], got {list(k_cache.shape)}")
-    if k_cache.dtype not in (torch.float8_e4m3fn, torch.int8):
-        raise TypeError(f"k_cache must be float8_e4m3fn or int8, got {k_cache.dtype}")
-    pages, H, size = k_cache.shape[:3]
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != k_cache.dtype or t.shape != k_cache.shape:
-            raise ValueError(f"{name} must be {k_cache.dtype} {list(k_cache.shape)}, got "
-                             f"{t.dtype} {list(t.shape)}")
-        if not t.is_cuda or (pages > 0 and not t[0].is_contiguous()):
-            raise ValueError(f"{name} must be a GPU tensor whose pages are contiguous")
+def _paged(name, t, dtype, shape):
+    """A cache tensor of that dtype and shape whose pages are contiguous: its page stride."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    st = t.stride()
+    if st[1:] != (shape[2] * HEAD_DIM, HEAD_DIM, 1) and shape[0] > 0 and not t[0].is_contiguous():
+        raise ValueError(f"{name}: each page must be contiguous")
+    return st[0]
+
+
+def _cache_args(torch, first, tokens, cache, cu_seqlens):
+    """Checks of a paged cache, its tables and cu_seqlens, all on the GPU of `first` (a
+    (name, tensor)): the C arguments from the dtype to kv_lens, the sequences, the heads."""
+    k_cache, v_cache, k_scale, v_scale, page_table, kv_lens = cache
+    dtype, shape = k_cache.dtype, k_cache.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM:
+        raise ValueError(f"k_cache must be [pages, H, page_size, 128], got {list(shape)}")
+    if dtype is not torch.float8_e4m3fn and dtype is not torch.int8:
+        raise TypeError(f"k_cache must be float8_e4m3fn or int8, got {dtype}")
+    kp = _paged("k_cache", k_cache, dtype, shape)
+    vp = _paged("v_cache", v_cache, dtype, shape)
+    pages, H, size, _ = shape
+    f32, i32 = torch.float32, torch.int32
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _f32(name, t)
-        if tuple(t.shape) != (pages, H):
-            raise ValueError(f"{name} must be [{pages}, {H}], got {list(t.shape)}")
-    _i32("kv_lens", kv_lens)
-    if kv_lens.dim() != 1:
-        raise ValueError(f"kv_lens must be [sequences], got {list(kv_lens.shape)}")
-    n = kv_lens.shape[0]
-    if page_table.dtype != torch.int32 or not page_table.is_cuda:
-        raise ValueError("page_table must be an int32 GPU tensor")
-    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.shape[1] < 1 or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be [{n}, pages of a sequence] with contiguous rows, "
-                         f"got {list(page_table.shape)}")
-    width = page_table.shape[1]
-    cache = (1 if k_cache.dtype == torch.int8 else 0, size, pages, _adr(k_cache),
-             k_cache.stride(0), _adr(v_cache), v_cache.stride(0), _adr(k_scale), _adr(v_scale))
-    tables = (_adr(page_table), width, page_table.stride(0) if n > 1 else width, _adr(kv_lens))
-    return cache + tables, n, H, (("k_cache", k_cache), ("v_cache", v_cache),
-                                  ("k_scale", k_scale), ("v_scale", v_scale),
-                                  ("page_table", page_table), ("kv_lens", kv_lens))
+        if t.dtype is not f32 or t.shape != (pages, H) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor [{pages}, {H}], got "
+                             f"{t.dtype} {list(t.shape)}")
+    at = kv_lens.shape
+    if kv_lens.dtype is not i32 or len(at) != 1 or not kv_lens.is_contiguous():
+        raise ValueError(f"kv_lens must be a contiguous int32 tensor [sequences], got "
+                         f"{kv_lens.dtype} {list(at)}")
+    n = at[0]
+    at, st = page_table.shape, page_table.stride()
+    if page_table.dtype is not i32 or len(at) != 2 or at[0] != n or at[1] < 1 or \
+            (st[1] != 1 and at[1] > 1):
+        raise ValueError(f"page_table must be an int32 tensor [{n}, pages of a sequence] with "
+                         f"contiguous rows, got {page_table.dtype} {list(at)}")
+    if cu_seqlens is None:
+        if tokens > 0 and (n == 0 or tokens % n != 0):
+            raise ValueError(f"{tokens} tokens of {n} sequences need cu_seqlens")
+        cu = None
+    else:
+        if cu_seqlens.dtype is not i32 or cu_seqlens.shape != (n + 1,) or \
+                not cu_seqlens.is_contiguous():
+            raise ValueError(f"cu_seqlens must be a contiguous int32 tensor [{n + 1}], got "
+                             f"{cu_seqlens.dtype} {list(cu_seqlens.shape)}")
+        cu = cu_seqlens.data_ptr()
+    if not first[1].is_cuda:
+        raise ValueError(f"{first[0]} must be a GPU tensor")
+    gpu = first[1].get_device()
+    for t in cache:
+        if t.get_device() != gpu:
+            raise ValueError(f"the cache and its tables must be on {first[1].device}, got a "
+                             f"tensor on {t.device}")
+    if cu is not None and cu_seqlens.get_device() != gpu:
+        raise ValueError(f"cu_seqlens must be on {first[1].device}, got {cu_seqlens.device}")
+    return (1 if dtype is torch.int8 else 0, size, pages, k_cache.data_ptr(), kp,
+            v_cache.data_ptr(), vp, k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr(), at[1], st[0] if n > 1 else at[1],
+            kv_lens.data_ptr()), n, H, cu
 
 
-def _cache_rows(name, t, tokens, width):
+def _token_rows(name, t, bf16, tokens, width):
     """bf16 [tokens, width] with contiguous rows: the row stride."""
-    _bf16(name, t)
-    if tuple(t.shape) != (tokens, width):
-        raise ValueError(f"{name} must be [{tokens}, {width}], got {list(t.shape)}")
-    return t.stride(0)
+    if t.dtype is not bf16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    st = t.stride()
+    if t.shape != (tokens, width) or st[1] != 1:
+        raise ValueError(f"{name} must be [{tokens}, {width}] with contiguous rows, got "
+                         f"{list(t.shape)}")
+    return st[0]
 
 
-def _cache_seqlens(cu_seqlens, n, tokens):
-    if cu_seqlens is not None:
-        _i32("cu_seqlens", cu_seqlens)
-        if tuple(cu_seqlens.shape) != (n + 1,):
-            raise ValueError(f"cu_seqlens must be [{n + 1}], got {list(cu_seqlens.shape)}")
-    elif n == 0 and tokens > 0 or n > 0 and tokens % n != 0:
-        raise ValueError(f"{tokens} tokens of {n} sequences need cu_seqlens")
-
-
-def _cache_rows_call(fn, k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
-                     cu_seqlens, stream):
-    cache, n, H, named = _cache_geometry(k_cache, v_cache, k_scale, v_scale, page_table, kv_lens)
+def _cache_rows(fn, k, v, cache, cu_seqlens, stream):
+    """kda_cache_write and kda_cache_read."""
+    import torch
+    if k.dim() != 2:
+        raise ValueError(f"k must be [T, H*128], got {list(k.shape)}")
     T = k.shape[0]
-    ks = _cache_rows("k", k, T, H * HEAD_DIM)
-    vs = _cache_rows("v", v, T, H * HEAD_DIM)
-    _cache_seqlens(cu_seqlens, n, T)
-    dev = _same_device(k, (("v", v), ("cu_seqlens", cu_seqlens)) + named)
-    _launch(fn, dev, stream, n, T, H, HEAD_DIM, _adr(cu_seqlens), _adr(k), ks, _adr(v), vs,
-            *cache)
+    args, n, H, cu = _cache_args(torch, ("k", k), T, cache, cu_seqlens)
+    W, bf16 = H * HEAD_DIM, torch.bfloat16
+    ks, vs = _token_rows("k", k, bf16, T, W), _token_rows("v", v, bf16, T, W)
+    dev = _same_device(k, (("v", v),))
+    _launch(fn, dev, stream, n, T, H, HEAD_DIM, cu, k.data_ptr(), ks, v.data_ptr(), vs, *args)
 
 
 def kda_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
@@ -696,8 +715,8 @@ def kda_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_len
     with the new tokens, which are the last ones of each sequence. cu_seqlens: int32
     [n + 1], or None where every sequence has T / n new tokens. Caches and scales are
     updated in place."""
-    _cache_rows_call("kda_cache_write", k, v, k_cache, v_cache, k_scale, v_scale, page_table,
-                     kv_lens, cu_seqlens, stream)
+    _cache_rows("kda_cache_write", k, v, (k_cache, v_cache, k_scale, v_scale, page_table, kv_lens),
+                cu_seqlens, stream)
 
 
 def kda_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens,
@@ -705,8 +724,8 @@ def kda_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens
     """The last tokens of each sequence, code * scale, into k and v (bf16 [T, H*128],
     row-strided). Other arguments as for kda_cache_write: sequence b's rows receive its
     positions kv_lens[b] - n_b .. kv_lens[b] - 1."""
-    _cache_rows_call("kda_cache_read", k, v, k_cache, v_cache, k_scale, v_scale, page_table,
-                     kv_lens, cu_seqlens, stream)
+    _cache_rows("kda_cache_read", k, v, (k_cache, v_cache, k_scale, v_scale, page_table, kv_lens),
+                cu_seqlens, stream)
 
 
 def kda_cache_attention_workspace_size(n_seqs: int, total_tokens: int, H_q: int,
@@ -725,33 +744,33 @@ def kda_cache_attention(q, out, k_cache, v_cache, k_scale, v_scale, page_table, 
     kda_cache_attention_workspace_size(...) bytes, or None to have one allocated here for
     this call."""
     import torch
-    cache, n, H, named = _cache_geometry(k_cache, v_cache, k_scale, v_scale, page_table, kv_lens)
     if q.dim() != 2:
         raise ValueError(f"q must be [T, H_q*128], got {list(q.shape)}")
     T, W = q.shape
+    args, n, H, cu = _cache_args(torch, ("q", q), T, (k_cache, v_cache, k_scale, v_scale,
+                                                      page_table, kv_lens), cu_seqlens)
     Hq = W // HEAD_DIM
-    if W != Hq * HEAD_DIM or Hq < 1 or Hq % H != 0:
+    if W != Hq * HEAD_DIM or Hq < 1 or H < 1 or Hq % H != 0:
         raise ValueError(f"q must be [T, H_q*128] with H_q a multiple of {H}, got {list(q.shape)}")
-    qs = _cache_rows("q", q, T, W)
-    os_ = _cache_rows("out", out, T, W)
+    bf16 = torch.bfloat16
+    qs, os_ = _token_rows("q", q, bf16, T, W), _token_rows("out", out, bf16, T, W)
     ls = 0
     if lse is not None:
-        if lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (T, Hq) or \
-                (Hq > 1 and lse.stride(1) != 1):
+        ls = lse.stride()
+        if lse.dtype is not torch.float32 or lse.shape != (T, Hq) or (Hq > 1 and ls[1] != 1):
             raise ValueError(f"lse must be a float32 GPU tensor [{T}, {Hq}] with contiguous rows")
-        ls = lse.stride(0)
-    _cache_seqlens(cu_seqlens, n, T)
-    if (cu_seqlens is None) != (cu_seqlens_host is None):
+        ls = ls[0]
+    if (cu is None) != (cu_seqlens_host is None):
         raise ValueError("cu_seqlens and cu_seqlens_host go together")
-    if cu_seqlens_host is not None and (
-            cu_seqlens_host.dtype != torch.int32 or cu_seqlens_host.is_cuda or
-            not cu_seqlens_host.is_contiguous() or tuple(cu_seqlens_host.shape) != (n + 1,)):
-        raise ValueError(f"cu_seqlens_host must be a contiguous int32 CPU tensor [{n + 1}]")
-    dev = _same_device(q, (("out", out), ("cu_seqlens", cu_seqlens), ("lse", lse),
-                           ("workspace", workspace)) + named)
+    host = None
+    if cu is not None:
+        if cu_seqlens_host.dtype is not torch.int32 or cu_seqlens_host.is_cuda or \
+                not cu_seqlens_host.is_contiguous() or cu_seqlens_host.shape != (n + 1,):
+            raise ValueError(f"cu_seqlens_host must be a contiguous int32 CPU tensor [{n + 1}]")
+        host = cu_seqlens_host.data_ptr()
+    dev = _same_device(q, (("out", out), ("lse", lse), ("workspace", workspace)))
     if workspace is None and T > 0:
         workspace = _workspace(kda_cache_attention_workspace_size(n, T, Hq, H), dev, stream)
     ws_bytes = _workspace_bytes(workspace, dev)
-    _launch("kda_cache_attention", dev, stream, n, T, Hq, H, HEAD_DIM, _adr(cu_seqlens_host),
-            _adr(cu_seqlens), _adr(q), qs, *cache, float(scale), _adr(out), os_, _adr(lse), ls,
-            _adr(workspace), ws_bytes)
+    _launch("kda_cache_attention", dev, stream, n, T, Hq, H, HEAD_DIM, host, cu, q.data_ptr(), qs,
+            *args, float(scale), out.data_ptr(), os_, _adr(lse), ls, _adr(workspace), ws_bytes)
