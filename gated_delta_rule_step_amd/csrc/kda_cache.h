@@ -94,6 +94,22 @@ __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Inclusive sums over the wave's lanes: prefixes within rows of 16 lanes, then the rows' last
+// lanes added to the rows behind them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t dpp_add(int32_t x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int32_t wave_prefix(int32_t x) {
+  x = dpp_add<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8
+  x = dpp_add<0x112, 0xf>(x);
+  x = dpp_add<0x114, 0xf>(x);
+  x = dpp_add<0x118, 0xf>(x);
+  x = dpp_add<0x142, 0xa>(x);  // row_bcast 15 into rows 1 and 3
+  x = dpp_add<0x143, 0xc>(x);  // row_bcast 31 into rows 2 and 3
+  return x;
+}
+
 // Host: the checks that the calls share, and the view. `empty`: nothing to do.
 struct CacheArgs {
   int32_t n_seqs;

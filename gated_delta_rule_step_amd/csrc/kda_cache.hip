@@ -271,6 +271,7 @@ kda_status check(const CacheArgs& a, CacheView* c) {
   while (shift < 8 && (1 << shift) < a.page_size) ++shift;
   if ((1 << shift) != a.page_size) return KDA_ERR_UNSUPPORTED;
   if (a.total_tokens > (int64_t(1) << 30) || a.H > (1 << 14) || a.num_pages > INT32_MAX ||
+      int64_t(a.table_width) * a.page_size > (int64_t(1) << 28) ||
       int64_t(a.n_seqs) * a.table_width > (int64_t(1) << 37) / a.page_size)
     return KDA_ERR_UNSUPPORTED;
   if (a.total_tokens > 0 && a.n_seqs == 0) return KDA_ERR_BAD_SHAPE;

@@ -1,5 +1,11 @@
 // Attention over the paged 8-bit cache: what its kernels share.
+//
+// Three kernels share the sequences of a call by their rows, G * tokens for each key/value head:
+// few rows (one token, or a few with few heads to a key), a handful of tokens, and documents. Each
+// cuts the keys into parts where its rows alone would not fill the chip.
 #pragma once
+
+#include <limits.h>
 
 #include "kda_cache.h"
 
@@ -16,39 +22,150 @@ struct AttnParams {
   int64_t out_stride;
   float* lse;           // NULL: not wanted
   int64_t lse_stride;
-  // the plan
-  int32_t few_rows;     // sequences of at most so many rows (G * tokens) have few, the others are
-                        // documents
-  int32_t most_rows;    // of a sequence of the kernel's kind
-  int32_t row_blocks;   // few rows: row blocks of a sequence and key/value head
-  int32_t targets;      // parts that all the keys are cut into
+  // this kernel's sequences and its plan
+  int32_t over, most;   // those with over < rows <= most
+  int32_t block_rows;   // rows of a block (of a part's results, too)
+  int32_t targets;      // parts that all the blocks' keys are cut into, 0: none is cut
+  int32_t min_units;    // units of a part at least
   int2* plan;           // [n_seqs]: first slot, parts
-  float2* stat;         // [slot][H][row]: reference exponent, sum
-  float* part;          // [slot][H][row][128]: sums of p v
+  float2* stat;         // [slot][H][block_rows]: reference exponent, sum
+  float* part;          // [slot][H][block_rows][128]: sums of p v
 };
-
-__device__ __forceinline__ int32_t rows_of(const AttnParams& p, int32_t b) {
-  int32_t n = p.c.per_seq;
-  if (p.c.cu) n = max(clamp_row(p.c, p.c.cu[b + 1]) - clamp_row(p.c, p.c.cu[b]), 0);
-  const int64_t rows = int64_t(n) * p.G;
-  return int32_t(min(rows, int64_t(INT32_MAX)));
-}
-__device__ __forceinline__ bool is_few(const AttnParams& p, int32_t b) {
-  const int32_t rows = rows_of(p, b);
-  return rows > 0 && rows <= min(p.few_rows, p.most_rows);
-}
 
 // Keys are split in units of 128 tokens.
 constexpr int kUnit = 128;
-constexpr int kMinUnits = 2;  // a part has at least so many
 __device__ __forceinline__ int32_t units_of(const CacheView& p, int32_t b) {
   const int32_t len = p.lens[b];
   return len < 0 || len > (int64_t(p.width) << p.page_shift) ? 0 : (len + kUnit - 1) / kUnit;
 }
 
-// Rows of a documents' workgroup, and the launch of `grid` of them.
-constexpr int kDocRows = 128;
-hipError_t launch_documents(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream);
+__device__ __forceinline__ int32_t rows_of(const AttnParams& p, int32_t b) {
+  int32_t n = p.c.per_seq;
+  if (p.c.cu) n = max(clamp_row(p.c, p.c.cu[b + 1]) - clamp_row(p.c, p.c.cu[b]), 0);
+  return int32_t(min(int64_t(n) * p.G, int64_t(INT_MAX)));
+}
+// Blocks of a sequence, 0 for another kernel's.
+__device__ __forceinline__ int32_t blocks_of(const AttnParams& p, int32_t b) {
+  const int32_t rows = rows_of(p, b);
+  return rows <= p.over || rows > p.most ? 0 : (rows + p.block_rows - 1) / p.block_rows;
+}
+
+// Part `index` of `parts` of the keys of block `rb` of sequence b: tokens from .. to - 1; its
+// results go to slot `slot` where there is more than one.
+struct Part {
+  int32_t b, rb, index, parts, slot, first_slot, from, to;
+};
+struct FindSmem {
+  int32_t work[4], items[4], slots[4];  // a wave's sums
+  Part part;
+};
+// Work item `item`: the sequences one after the other, a sequence's last block (with the most
+// keys to see) first. Every workgroup of T threads finds it for itself from the lengths on the
+// device, K sequences a thread; SPLIT: the keys may be cut. Each sequence's keys are cut into equal
+// parts of a length that is the same for all, however ragged the batch, except for what rounding
+// to units leaves. (By single waves, 64 sequences at a time, 512 sequences took 10 us to walk.)
+template <bool SPLIT, int T>
+__device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, FindSmem& lds,
+                                          Part& out) {
+  constexpr int kHeld = 4;  // sequences of a thread that stay in registers
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t B = p.c.n_seqs, K = (B + T - 1) / T, b0 = int32_t(threadIdx.x) * K;
+  const auto sizes = [&](int k, int32_t& blocks, int32_t& units) {
+    const bool is = k < K && b0 + k < B;
+    blocks = is ? blocks_of(p, b0 + k) : 0;
+    units = SPLIT && is ? units_of(p.c, b0 + k) : 0;
+  };
+  int32_t blocks[kHeld], units[kHeld], chunk = 1 << 28;  // whole sequences
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) sizes(k, blocks[k], units[k]);
+  if (threadIdx.x == 0) lds.part.b = -1;
+  if (SPLIT) {
+    int32_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) sum += blocks[k] * units[k];
+    for (int k = kHeld; k < K; ++k) {
+      int32_t n, u;
+      sizes(k, n, u);
+      sum += n * u;
+    }
+    sum = wave_prefix(sum);
+    if (lane == 63) lds.work[wave] = sum;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w) sum += lds.work[w];
+    chunk = max(p.min_units, (sum + p.targets - 1) / p.targets);
+  }
+  const auto parts_of = [&](int32_t u) { return SPLIT ? max((u + chunk - 1) / chunk, 1) : 1; };
+  int32_t items = 0, slots = 0;
+  const auto count = [&](int32_t n, int32_t u) {
+    const int32_t parts = parts_of(u);
+    items += n * parts;
+    slots += parts > 1 ? n * parts : 0;
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) count(blocks[k], units[k]);
+  for (int k = kHeld; k < K; ++k) {
+    int32_t n, u;
+    sizes(k, n, u);
+    count(n, u);
+  }
+  int32_t first = wave_prefix(items), slot = SPLIT ? wave_prefix(slots) : 0;
+  if (lane == 63) {
+    lds.items[wave] = first;
+    lds.slots[wave] = slot;
+  }
+  first -= items;
+  slot -= slots;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < T / 64 - 1; ++w)
+    if (w < wave) {
+      first += lds.items[w];
+      slot += lds.slots[w];
+    }
+  if (item >= first && item < first + items) {
+    for (int k = 0; k < K; ++k) {
+      int32_t n, u;
+      sizes(k, n, u);
+      const int32_t parts = parts_of(u);
+      if (item < first + n * parts) {
+        const int32_t rb = SPLIT ? (item - first) / parts : item - first;
+        Part x;
+        x.b = b0 + k;
+        x.parts = parts;
+        x.index = item - first - rb * parts;
+        x.rb = n - 1 - rb;
+        x.first_slot = slot;
+        x.slot = slot + x.rb * parts + x.index;
+        x.from = parts == 1 ? 0 : x.index * chunk * kUnit;
+        x.to = x.index + 1 == parts ? INT_MAX : x.from + chunk * kUnit;
+        // (more slots than there are: cu_seqlens is not what the host's copy says)
+        if (parts > 1 && (slot < 0 || x.slot >= 2 * p.targets)) x.b = -1;
+        lds.part = x;
+        break;
+      }
+      first += n * parts;
+      slot += parts > 1 ? n * parts : 0;
+    }
+  }
+  __syncthreads();
+  out.b = __builtin_amdgcn_readfirstlane(lds.part.b);
+  if (out.b < 0) return false;
+  out.rb = __builtin_amdgcn_readfirstlane(lds.part.rb);
+  out.index = __builtin_amdgcn_readfirstlane(lds.part.index);
+  out.parts = __builtin_amdgcn_readfirstlane(lds.part.parts);
+  out.slot = __builtin_amdgcn_readfirstlane(lds.part.slot);
+  out.first_slot = __builtin_amdgcn_readfirstlane(lds.part.first_slot);
+  out.from = __builtin_amdgcn_readfirstlane(lds.part.from);
+  out.to = __builtin_amdgcn_readfirstlane(lds.part.to);
+  return true;
+}
+
+// Documents' and handfuls' kernel: workgroups of 32 * waves rows (waves 2 or 4).
+hipError_t launch_documents(const AttnParams& p, int waves, bool int8, unsigned grid,
+                            hipStream_t stream);
 
 }  // namespace cache
 }  // namespace kda

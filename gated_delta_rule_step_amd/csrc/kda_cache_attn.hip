@@ -1,4 +1,4 @@
-// Attention of a few tokens of each sequence over the paged 8-bit cache (gfx950).
+// Attention of a few tokens of each sequence over the paged 8-bit cache (gfx950), and the call.
 //
 // Row r of a sequence and key/value head is query head r mod G of token r / G. With keys
 // as the rows of the matrix products (S^T = K Q^T, O^T = V^T P^T), a lane's scores, sums and
@@ -6,13 +6,11 @@
 // exchange between lanes, and P^T leaves the first product where the second one reads it.
 //
 // Bound by HBM: every key and value byte passes once. The keys of all sequences are cut into
-// parts of about equal length, however ragged the batch (every wave finds its part from
-// kv_lens; no host copy is needed), and a part's four waves walk 32 tokens at a time each.
+// parts of about equal length, and a part's four waves walk 32 tokens at a time each.
 // The codes are widened to bf16 in registers, exactly; the scales of a page multiply scores
 // and weights. The weights p enter the second product as high and low bf16 parts: the
 // matrix units idle otherwise, and the output keeps fp32's accuracy.
 
-#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -24,96 +22,59 @@ namespace cache {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStep = 32;     // tokens of a wave's step
-constexpr int32_t kWhole = 1 << 28;  // units of a part where nothing is cut
-constexpr int kRow = D + 4;   // fp32 row in LDS
+constexpr int kStep = 32;            // tokens of a wave's step
+constexpr int kStride = 4 * kStep;   // and of the workgroup's
+constexpr int kRow = D + 4;          // fp32 row in LDS
 // The reference exponent of a row moves only when a score passes it by this much (base 2):
 // weights stay below 2^8, far inside bf16 and fp32.
 constexpr float kSlack = 8.0f;
 
-struct Part {
-  int32_t b, index, parts, slot;
-  int32_t from, to;  // tokens
+// A wave's 32 tokens are two tiles of 16, each inside one page.
+struct Ids {
+  int32_t id[2];  // -1: no page
+};
+struct Keys {
+  u32x4 w[2][2];  // lane (m, g): token m, channels 64 i + 16 g ..
+  float scale[2];
+};
+struct Values {
+  u32x2 w[2][4];  // lane (m, g): token 4 g + r, channels 8 m ..
+  float scale[2];
 };
 
-// Part `item` of all sequences' parts, by each wave for itself.
-__device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, int lane, Part& out) {
-  const int32_t B = p.c.n_seqs;
-  int32_t chunk = kWhole;
-  if (p.targets > 0) {
-    int32_t sum = 0;
-    for (int32_t b = lane; b < B; b += 64) sum += is_few(p, b) ? units_of(p.c, b) : 0;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s);
-    chunk = max(kMinUnits, (sum + p.targets - 1) / p.targets);
-  }
-  int32_t items = 0, slots = 0;
-  for (int32_t b0 = 0; b0 < B; b0 += 64) {
-    const int32_t b = b0 + lane;
-    const bool few = b < B && is_few(p, b);
-    const int32_t units = few ? units_of(p.c, b) : 0;
-    const int32_t n = few ? max((units + chunk - 1) / chunk, 1) : 0;
-    const int32_t s = n > 1 ? n : 0;
-    int32_t ni = n, si = s;  // inclusive prefix sums
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int32_t x = __shfl_up(ni, d), y = __shfl_up(si, d);
-      if (lane >= d) ni += x, si += y;
-    }
-    const uint64_t hit = __ballot(item < items + ni);
-    if (hit) {
-      const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      out.b = b0 + at;
-      out.parts = __shfl(n, at);
-      out.index = item - (items + __shfl(ni - n, at));
-      out.slot = slots + __shfl(si - s, at);
-      out.from = out.parts == 1 ? 0 : out.index * chunk * kUnit;
-      out.to = out.index + 1 == out.parts ? INT_MAX : out.from + chunk * kUnit;
-      out.b = __builtin_amdgcn_readfirstlane(out.b);
-      out.parts = __builtin_amdgcn_readfirstlane(out.parts);
-      out.index = __builtin_amdgcn_readfirstlane(out.index);
-      out.slot = __builtin_amdgcn_readfirstlane(out.slot);
-      out.from = __builtin_amdgcn_readfirstlane(out.from);
-      out.to = __builtin_amdgcn_readfirstlane(out.to);
-      return true;
-    }
-    items += __shfl(ni, 63);
-    slots += __shfl(si, 63);
-  }
-  return false;
-}
-
-// 32 tokens of a wave: two tiles of 16, each inside one page.
-struct Step {
-  u32x4 k[2][2];  // lane (m, g): token m, channels 64 i + 16 g ..
-  u32x2 v[2][4];  // lane (m, g): token 4 g + r, channels 8 m ..
-  float ks[2], vs[2];
-  int32_t live[2];  // tokens that exist
-};
-
-__device__ __forceinline__ void load_step(const AttnParams& p, int32_t b, int32_t h, int32_t at,
-                                          int32_t end, int lane, Step& s) {
-  const int m = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void load_ids(const AttnParams& p, int32_t b, int32_t at, int32_t end,
+                                         Ids& s) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int32_t tok = at + 16 * u;
-    int32_t id = -1;
-    if (tok < end) id = page_of(p.c, b, tok >> p.c.page_shift);
-    s.live[u] = id < 0 ? 0 : min(16, end - tok);
-    id = max(id, 0);  // page 0's bytes in the place of none's
-    const int64_t in_page =
-        ((int64_t(h) << p.c.page_shift) + (tok & ((1 << p.c.page_shift) - 1))) * D;
-    const uint8_t* const k = p.c.k + id * p.c.k_page + in_page;
-    const uint8_t* const v = p.c.v + id * p.c.v_page + in_page;
+    s.id[u] = tok < end ? page_of(p.c, b, tok >> p.c.page_shift) : -1;
+  }
+}
+// Page 0's bytes in the place of none's.
+__device__ __forceinline__ int64_t tile_at(const CacheView& c, int32_t id, int64_t page, int32_t h,
+                                           int32_t tok) {
+  return max(id, 0) * page + ((int64_t(h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D;
+}
+__device__ __forceinline__ void load_keys(const AttnParams& p, int32_t h, int32_t at, const Ids& ids,
+                                          int m, int g, Keys& s) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* const k = p.c.k + tile_at(p.c, ids.id[u], p.c.k_page, h, at + 16 * u);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      s.k[u][i] = *reinterpret_cast<const u32x4*>(k + m * D + i * 64 + g * 16);
+      s.w[u][i] = *reinterpret_cast<const u32x4*>(k + (m * D + i * 64 + g * 16));
+    s.scale[u] = p.c.k_scale[int64_t(max(ids.id[u], 0)) * p.c.H + h];
+  }
+}
+__device__ __forceinline__ void load_values(const AttnParams& p, int32_t h, int32_t at,
+                                            const Ids& ids, int m, int g, Values& s) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* const v = p.c.v + tile_at(p.c, ids.id[u], p.c.v_page, h, at + 16 * u);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      s.v[u][r] = *reinterpret_cast<const u32x2*>(v + (4 * g + r) * D + m * 8);
-    const int64_t sc = int64_t(id) * p.c.H + h;
-    s.ks[u] = p.c.k_scale[sc];
-    s.vs[u] = p.c.v_scale[sc];
+      s.w[u][r] = *reinterpret_cast<const u32x2*>(v + (4 * g * D + m * 8) + r * D);
+    s.scale[u] = p.c.v_scale[int64_t(max(ids.id[u], 0)) * p.c.H + h];
   }
 }
 
@@ -126,77 +87,81 @@ __device__ __forceinline__ float over_groups_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// O^T += V^T P^T over the step's 32 tokens.
-template <int KIND, int NT>
-__device__ __forceinline__ void weigh(const Step& s, const bf16x8 (&ph)[NT], const bf16x8 (&pl)[NT],
-                                      f32x4 (&o)[NT][8]) {
-#pragma unroll
-  for (int c4 = 0; c4 < 2; ++c4) {  // channels 8 m + 4 c4 ..
-    uint32_t t0[4], t1[4];
-    transpose4(s.v[0][0][c4], s.v[0][1][c4], s.v[0][2][c4], s.v[0][3][c4], t0);
-    transpose4(s.v[1][0][c4], s.v[1][1][c4], s.v[1][2][c4], s.v[1][3][c4], t1);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const bf16x8 v = widen8<KIND>(t0[c], t1[c]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][4 * c4 + c] = mfma32(v, ph[n], o[n][4 * c4 + c]);
-        o[n][4 * c4 + c] = mfma32(v, pl[n], o[n][4 * c4 + c]);
-      }
-    }
-  }
-}
-// Whether a value code of a token behind `all_see` is e4m3's NaN.
-__device__ __forceinline__ bool nan_beyond(const Step& s, int32_t at, int32_t all_see, int g) {
-  uint32_t any = 0;
+// Values that a row of the block does not see: bytes of tokens that are not there become zeros, and so
+// do NaN codes behind `all_see`, which leave the first position that holds one in
+// nan_at[channel]: rows that see it become NaN in the end, and the others stay clear of 0 NaN.
+template <int KIND>
+__device__ __forceinline__ void clear_values(Values& v, const int32_t (&live)[2], int32_t at,
+                                             int32_t all_see, int m, int g, int32_t* nan_at) {
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (at + 16 * u + 4 * g + r > all_see)
-        any |= ((s.v[u][r][0] & 0x7f7f7f7fu) + 0x01010101u) |
-               ((s.v[u][r][1] & 0x7f7f7f7fu) + 0x01010101u);
-  return __any((any & 0x80808080u) != 0);
+    for (int r = 0; r < 4; ++r) {
+      const int in = 4 * g + r;
+      if (in >= live[u]) v.w[u][r] = u32x2{0u, 0u};
+      if (KIND == kFp8 && at + 16 * u + in > all_see) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t hit = ((v.w[u][r][j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+          if (hit)
+            for (int c = 0; c < 4; ++c)
+              if (hit >> (8 * c + 7) & 1) {
+                atomicMin(nan_at + m * 8 + 4 * j + c, at + 16 * u + in);
+                v.w[u][r][j] &= ~(0xffu << (8 * c));
+              }
+        }
+      }
+    }
 }
 
-// One workgroup: (part, key/value head, block of 16 NT rows).
+// One workgroup: (part of a sequence's keys, key/value head) for up to 16 NT rows.
 template <int KIND, int NT>
-__global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
+__global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void attend_kernel(AttnParams p) {
   __shared__ float sums[4][16 * kRow];
   __shared__ float refs[4][16], tots[4][16];
+  __shared__ int32_t nan_at[D];
+  __shared__ FindSmem find;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = p.c.H * p.row_blocks;
-  const int item = blockIdx.x / per, hb = blockIdx.x - item * per;
-  const int rb = hb / p.c.H, h = hb - rb * p.c.H;
+  const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
   Part part;
-  if (!find_part(p, item, lane, part)) return;
+  if (!find_part<true, kThreads>(p, item, find, part)) return;
   const Seq seq = sequence(p.c, part.b);
-  if (hb == 0 && part.index == 0 && threadIdx.x == 0)
-    p.plan[part.b] = make_int2(part.slot, part.parts);
-  const int rows = rows_of(p, part.b), row0 = rb * 16 * NT;
-  if (row0 >= rows) return;
+  const int rows = rows_of(p, part.b);
   const int32_t len = p.c.num_pages > 0 ? max(seq.len, 0) : 0;
   const int32_t to = min(part.to, len);
+  const int32_t base = len - seq.n;  // position of the first token, which every row sees
+
+  int32_t at = part.from + wave * kStep;
+  Ids ids, ids_next;
+  Keys k;
+  Values v;
+  load_ids(p, part.b, at, to, ids);
+  load_ids(p, part.b, at + kStride, to, ids_next);
+  if (at < to) {
+    load_keys(p, h, at, ids, m, g, k);
+    load_values(p, h, at, ids, m, g, v);
+  }
+  if (threadIdx.x < D) nan_at[threadIdx.x] = INT_MAX;
+  __syncthreads();
 
   // queries: lane (m, g) holds row m's channels of group g, eight per product
   bf16x8 q[NT][4];
   int32_t last[NT];  // the last position that the lane's row sees
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = row0 + 16 * n + m, t = r / p.G;
-    last[n] = len - seq.n + t;
-    const uint16_t* const at =
+    const int r = 16 * n + m, t = r / p.G;
+    last[n] = base + t;
+    const uint16_t* const src =
         p.q + (seq.first + t) * p.q_stride + (int64_t(h) * p.G + (r - t * p.G)) * D;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       u32x4 w = {0u, 0u, 0u, 0u};
       if (r < rows)
-        w = *reinterpret_cast<const u32x4_u*>(at + (j >> 1) * 64 + g * 16 + (j & 1) * 8);
+        w = *reinterpret_cast<const u32x4_u*>(src + (j >> 1) * 64 + g * 16 + (j & 1) * 8);
       q[n][j] = __builtin_bit_cast(bf16x8, w);
     }
   }
-  const int32_t all_see = len - seq.n + row0 / p.G;  // every row of the block sees up to here
 
   f32x4 o[NT][8];
   float ref[NT], tot[NT];
@@ -208,48 +173,48 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
     for (int c = 0; c < 8; ++c) o[n][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  Step next;
-  int32_t at = part.from + wave * kStep;
-  if (at < to) load_step(p, part.b, h, at, to, lane, next);
-  for (; at < to; at += 4 * kStep) {
-    Step cur = next;
-    if (at + 4 * kStep < to) load_step(p, part.b, h, at + 4 * kStep, to, lane, next);
-    const bool masked = cur.live[0] < 16 || cur.live[1] < 16 || at + kStep - 1 > all_see;
-    if (cur.live[0] < 16 || cur.live[1] < 16) {  // bytes of tokens that are not there
+  for (; at < to; at += kStride) {
+    const bool more = at + kStride < to;
+    int32_t live[2];  // tokens that exist
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) live[u] = ids.id[u] < 0 ? 0 : min(16, to - (at + 16 * u));
+    const bool masked = live[0] < 16 || live[1] < 16 || at + kStep - 1 > base;
+    f32x4 acc[NT][2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (4 * g + r >= cur.live[u]) cur.v[u][r] = u32x2{0u, 0u};
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) acc[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 a = widen8<KIND>(k.w[u][j >> 1][2 * (j & 1)], k.w[u][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][u] = mfma32(a, q[n][j], acc[n][u]);
+      }
+    const float f[2] = {p.scale2 * k.scale[0], p.scale2 * k.scale[1]};
+    if (more) load_keys(p, h, at + kStride, ids_next, m, g, k);
     bf16x8 ph[NT], pl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float s[2][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc = mfma32(widen8<KIND>(cur.k[u][j >> 1][2 * (j & 1)], cur.k[u][j >> 1][2 * (j & 1) + 1]),
-                       q[n][j], acc);
-        const float f = p.scale2 * cur.ks[u];
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          s[u][r] = acc[r] * f;
-          if (masked && (4 * g + r >= cur.live[u] || at + 16 * u + 4 * g + r > last[n]))
+          s[u][r] = acc[n][u][r] * f[u];
+          if (masked && (4 * g + r >= live[u] || at + 16 * u + 4 * g + r > last[n]))
             s[u][r] = -INFINITY;
         }
-      }
-      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                        fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                              fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
       if (__any(top > ref[n] + kSlack)) {
         const float to_ref = fmaxf(ref[n], over_groups_max(top));
-        const float f = to_ref == ref[n] ? 1.0f : __builtin_amdgcn_exp2f(ref[n] - to_ref);
+        const float down = to_ref == ref[n] ? 1.0f : __builtin_amdgcn_exp2f(ref[n] - to_ref);
         ref[n] = to_ref;
-        tot[n] *= f;
+        tot[n] *= down;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) o[n][c] *= f;
+        for (int c = 0; c < 8; ++c) o[n][c] *= down;
       }
       const float r0 = ref[n] == -INFINITY ? 0.0f : ref[n];
       uint32_t hi[4], lo[4];
@@ -260,8 +225,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
         for (int r = 0; r < 4; ++r) {
           w[r] = __builtin_amdgcn_exp2f(s[u][r] - r0);
           tot[n] += w[r];
-          w[r] *= cur.vs[u];
-          if (masked && 4 * g + r >= cur.live[u]) w[r] = 0.0f;  // whatever that scale was
+          w[r] *= v.scale[u];
+          if (masked && 4 * g + r >= live[u]) w[r] = 0.0f;  // whatever that scale was
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -273,32 +238,25 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
       ph[n] = __builtin_bit_cast(bf16x8, u32x4{hi[0], hi[1], hi[2], hi[3]});
       pl[n] = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], lo[2], lo[3]});
     }
-    if (KIND == kFp8 && masked && nan_beyond(cur, at, all_see, g)) {
-      // a NaN value that some rows see and others do not: token by token, since 0 NaN = NaN
-      for (int32_t t = row0 / p.G; t <= (row0 + 16 * NT - 1) / p.G; ++t) {
-        const int32_t end = len - seq.n + t;
-        Step seen = cur;
+    if (masked) clear_values<KIND>(v, live, at, base, m, g, nan_at);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int c4 = 0; c4 < 2; ++c4) {  // channels 8 m + 4 c4 ..
+      uint32_t t0[4], t1[4];
+      transpose4(v.w[0][0][c4], v.w[0][1][c4], v.w[0][2][c4], v.w[0][3][c4], t0);
+      transpose4(v.w[1][0][c4], v.w[1][1][c4], v.w[1][2][c4], v.w[1][3][c4], t1);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (at + 16 * u + 4 * g + r > end) seen.v[u][r] = u32x2{0u, 0u};
-        f32x4 part_o[NT][8];
+      for (int c = 0; c < 4; ++c) {
+        const bf16x8 a = widen8<KIND>(t0[c], t1[c]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) part_o[n][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        weigh<KIND, NT>(seen, ph, pl, part_o);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (last[n] == end) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) o[n][c] += part_o[n][c];
-          }
+        for (int n = 0; n < NT; ++n) {
+          o[n][4 * c4 + c] = mfma32(a, ph[n], o[n][4 * c4 + c]);
+          o[n][4 * c4 + c] = mfma32(a, pl[n], o[n][4 * c4 + c]);
+        }
       }
-    } else {
-      weigh<KIND, NT>(cur, ph, pl, o);
     }
+    if (more) load_values(p, h, at + kStride, ids_next, m, g, v);
+    ids = ids_next;
+    load_ids(p, part.b, at + 2 * kStride, to, ids_next);
   }
 
   // the four waves' sums, 16 rows at a time; thread (row, 8 channels)
@@ -318,20 +276,25 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
       *reinterpret_cast<f32x4*>(to_lds + 4) = f32x4{o[n][4][r], o[n][5][r], o[n][6][r], o[n][7][r]};
     }
     __syncthreads();
+    const int r = 16 * n + row;
+    if (r >= rows) continue;
+    const int t = r / p.G;
     const float top = fmaxf(fmaxf(refs[0][row], refs[1][row]), fmaxf(refs[2][row], refs[3][row]));
-    const float base = top == -INFINITY ? 0.0f : top;
+    const float r0 = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float f = __builtin_amdgcn_exp2f(refs[w][row] - base);
+      const float f = __builtin_amdgcn_exp2f(refs[w][row] - r0);
       sum += tots[w][row] * f;
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] += sums[w][row * kRow + ch + c] * f;
     }
-    const int r = row0 + 16 * n + row;
-    if (r >= rows) continue;
+    if (KIND == kFp8) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (nan_at[ch + c] <= base + t) acc[c] = NAN;
+    }
     if (part.parts == 1) {
-      const int t = r / p.G;
       const int64_t head = int64_t(h) * p.G + (r - t * p.G);
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       *reinterpret_cast<u32x4_u*>(p.out + (seq.first + t) * p.out_stride + head * D + ch) =
@@ -339,46 +302,83 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttnParams p) {
                 pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv)};
       if (p.lse && ch == 0)
         p.lse[(seq.first + t) * p.lse_stride + head] =
-            sum == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * LN2;
+            sum == 0.0f ? -INFINITY : (r0 + __builtin_amdgcn_logf(sum)) * LN2;
     } else {
-      const int64_t slot = (int64_t(part.slot + part.index) * p.c.H + h) * p.most_rows + r;
+      const int64_t slot = (int64_t(part.slot) * p.c.H + h) * p.block_rows + r;
       float* const dst = p.part + slot * D + ch;
       *reinterpret_cast<f32x4*>(dst) = f32x4{acc[0], acc[1], acc[2], acc[3]};
       *reinterpret_cast<f32x4*>(dst + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
       if (ch == 0) p.stat[slot] = make_float2(top, sum);
     }
   }
+  if (h == 0 && part.rb == 0 && part.index == 0 && threadIdx.x == 0)
+    p.plan[part.b] = make_int2(part.first_slot, part.parts);
 }
 
-// Joins the parts of a row: a wave per row, 32 lanes of 4 channels, every other part each.
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
+// Joins the parts of a row: a wave (or, WAVES = 4, where there are few rows, a workgroup) per row,
+// 32 lanes of 4 channels, four parts at a time.
+template <int WAVES>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p, int32_t most_rows) {
+  __shared__ f32x4 accs[WAVES == 1 ? 1 : WAVES][32];
+  __shared__ float tots[WAVES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = (p.most_rows * p.c.H + 3) / 4;
-  const int b = blockIdx.x / per, i = (blockIdx.x - b * per) * 4 + wave;
-  if (i >= p.most_rows * p.c.H || !is_few(p, b)) return;
+  const int pairs = most_rows * p.c.H;
+  const int per = WAVES == 1 ? (pairs + 3) / 4 : pairs;
+  const int b = blockIdx.x / per;
+  const int i = WAVES == 1 ? (blockIdx.x - b * per) * 4 + wave : blockIdx.x - b * per;
+  if (i >= pairs || blocks_of(p, b) == 0) return;
   const int2 plan = p.plan[b];
   const Seq seq = sequence(p.c, b);
   const int r = i / p.c.H, h = i - r * p.c.H;
-  if (plan.y <= 1 || r >= p.G * seq.n) return;
-  const int64_t first = (int64_t(plan.x) * p.c.H + h) * p.most_rows + r;
-  const int64_t step = int64_t(p.c.H) * p.most_rows;
+  if (plan.y <= 1 || r >= rows_of(p, b)) return;
+  const int rb = r / p.block_rows;
+  if (plan.x < 0 || plan.x + (int64_t(rb) + 1) * plan.y > 2 * p.targets) return;  // see find_part
+  const int64_t first = ((int64_t(plan.x) + int64_t(rb) * plan.y) * p.c.H + h) * p.block_rows +
+                        (r - rb * p.block_rows);
+  const int64_t step = int64_t(p.c.H) * p.block_rows;
   float top = -INFINITY;
   for (int s = lane; s < plan.y; s += 64) top = fmaxf(top, p.stat[first + s * step].x);
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
-  const float base = top == -INFINITY ? 0.0f : top;
+  const float r0 = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = lane >> 5; s < plan.y; s += 2) {
-    const float2 st = p.stat[first + s * step];
-    const float f = __builtin_amdgcn_exp2f(st.x - base);
-    sum += st.y * f;
-    acc += *reinterpret_cast<const f32x4*>(p.part + (first + s * step) * D + (lane & 31) * 4) * f;
+  const int mine = (WAVES == 1 ? 0 : wave * 2) + (lane >> 5);
+  for (int s0 = mine; s0 < plan.y; s0 += 8 * WAVES) {
+    float2 st[4];
+    f32x4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = s0 + 2 * WAVES * j;
+      st[j] = make_float2(-INFINITY, 0.0f);
+      x[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (s < plan.y) {
+        st[j] = p.stat[first + s * step];
+        x[j] = *reinterpret_cast<const f32x4*>(p.part + (first + s * step) * D + (lane & 31) * 4);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = __builtin_amdgcn_exp2f(st[j].x - r0);
+      sum += st[j].y * f;
+      acc += x[j] * f;
+    }
   }
   sum += __shfl_xor(sum, 32);
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], 32);
+  if (WAVES > 1) {
+    if (lane < 32) accs[wave][lane] = acc;
+    if (lane == 0) tots[wave] = sum;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      acc += accs[w][lane & 31];
+      sum += tots[w];
+    }
+  }
   if (lane >= 32) return;
   const int t = r / p.G;
   const int64_t head = int64_t(h) * p.G + (r - t * p.G);
@@ -388,39 +388,60 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
       u32x2{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
   if (p.lse && lane == 0)
     p.lse[(seq.first + t) * p.lse_stride + head] =
-        sum == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * LN2;
+        sum == 0.0f ? -INFINITY : (r0 + __builtin_amdgcn_logf(sum)) * LN2;
 }
 
-// Host: the plan of a call.
-constexpr int64_t kGroups = 1024;  // workgroups that the cut aims at
-constexpr int32_t kFewRows = 64;   // sequences with more rows are documents
+// Host: the three kernels' shares of a call.
+struct Share {
+  int32_t over, most;         // its sequences have over < rows <= most
+  int32_t waves;              // documents' kernel: waves; 0: few rows
+  int32_t block_rows, groups, min_units;
+};
+constexpr Share kShares[] = {
+    {0, 32, 0, 32, 1024, 8},
+    {32, 64, 2, 64, 1024, 4},
+    {64, INT_MAX, 4, 128, 512, 4},
+};
+constexpr int kShareCount = 3;
 
 struct Plan {
-  int32_t tiles, row_blocks, targets;
-  int64_t plan_bytes, stat_bytes, bytes;
+  int32_t block_rows, targets;
+  int64_t plan_bytes, stat_bytes, bytes, grid;
 };
-// Sequences of at most `rows` <= kFewRows rows for each of H key/value heads.
-Plan make_plan(int32_t n_seqs, int32_t rows, int32_t H) {
-  Plan r;
-  r.tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  r.row_blocks = (rows + 16 * r.tiles - 1) / (16 * r.tiles);
-  r.targets = int32_t(std::max<int64_t>(1, kGroups / (int64_t(H) * r.row_blocks)));
-  // a cut sequence has less than twice its share of the parts
-  const int64_t vecs = 2 * int64_t(r.targets) * H * rows;
-  r.plan_bytes = (int64_t(n_seqs) * 8 + 255) / 256 * 256;
-  r.stat_bytes = (vecs * 8 + 255) / 256 * 256;
-  r.bytes = r.plan_bytes + r.stat_bytes + vecs * D * 4;
+// `rows`: the most of a sequence; `blocks`: in all.
+Plan make_plan(const Share& s, int32_t n_seqs, int64_t rows, int64_t blocks, int32_t H) {
+  Plan r = {};
+  r.block_rows = s.waves ? s.block_rows : int32_t(std::min<int64_t>(rows, s.block_rows));
+  const int64_t targets = std::max<int64_t>(1, s.groups / H);
+  // few rows are cut however many sequences there are, since those may differ in length
+  if (s.waves == 0 || blocks < targets) {
+    r.targets = int32_t(targets);
+    // what is cut has less than twice its share of the parts
+    const int64_t vecs = 2 * targets * H * r.block_rows;
+    r.plan_bytes = (int64_t(n_seqs) * 8 + 255) / 256 * 256;
+    r.stat_bytes = (vecs * 8 + 255) / 256 * 256;
+    r.bytes = r.plan_bytes + r.stat_bytes + vecs * D * 4;
+  }
+  r.grid = (r.targets + blocks) * H;
   return r;
 }
 
 template <int KIND>
-hipError_t launch_attend(const AttnParams& p, const Plan& plan, unsigned grid, hipStream_t stream) {
-  if (plan.tiles == 1)
+hipError_t launch_attend(const AttnParams& p, unsigned grid, hipStream_t stream) {
+  if (p.block_rows <= 16)
     hipLaunchKernelGGL((attend_kernel<KIND, 1>), dim3(grid), dim3(kThreads), 0, stream, p);
-  else if (plan.tiles == 2)
-    hipLaunchKernelGGL((attend_kernel<KIND, 2>), dim3(grid), dim3(kThreads), 0, stream, p);
   else
-    hipLaunchKernelGGL((attend_kernel<KIND, 4>), dim3(grid), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attend_kernel<KIND, 2>), dim3(grid), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_join(const AttnParams& p, int32_t rows, int64_t pairs, hipStream_t stream) {
+  if (pairs <= 1024)
+    hipLaunchKernelGGL(join_kernel<4>, dim3(unsigned(pairs)), dim3(kThreads), 0, stream, p, rows);
+  else
+    hipLaunchKernelGGL(join_kernel<1>,
+                       dim3(unsigned((int64_t(rows) * p.c.H + 3) / 4 * p.c.n_seqs)),
+                       dim3(kThreads), 0, stream, p, rows);
   return hipGetLastError();
 }
 
@@ -435,13 +456,16 @@ bool bad_heads(int32_t H_q, int32_t H_kv) {
 extern "C" size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t total_tokens,
                                                      int32_t H_q, int32_t H_kv) {
   namespace kc = kda::cache;
-  if (n_seqs < 1 || total_tokens < 1 || kc::bad_heads(H_q, H_kv) || H_q / H_kv > 256) return 0;
-  // the largest that any split of the tokens over the sequences needs
-  const int32_t G = H_q / H_kv;
-  int64_t most = 0;
-  for (int64_t n = 1; n <= total_tokens && n * G <= kc::kFewRows; ++n)
-    most = std::max(most, kc::make_plan(n_seqs, int32_t(n * G), H_kv).bytes);
-  return size_t(most);
+  if (n_seqs < 1 || total_tokens < 1 || total_tokens > (int64_t(1) << 30) ||
+      kc::bad_heads(H_q, H_kv) || H_q / H_kv > 256)
+    return 0;
+  // whatever the sequences' shares of the tokens
+  const int64_t rows = total_tokens * (H_q / H_kv);
+  int64_t bytes = 0;
+  for (const kc::Share& s : kc::kShares)
+    if (rows > s.over)
+      bytes += kc::make_plan(s, n_seqs, std::min<int64_t>(rows, s.most), 0, H_kv).bytes;
+  return size_t(bytes);
 }
 
 extern "C" kda_status kda_cache_attention(
@@ -469,16 +493,14 @@ extern "C" kda_status kda_cache_attention(
   if (!q || !out) return KDA_ERR_NULL_POINTER;
   if ((cu_seqlens != nullptr) != (cu_seqlens_host != nullptr)) return KDA_ERR_NULL_POINTER;
   p.G = H_q / H_kv;
-  // the most rows of few-token sequences, of documents, and the documents' blocks
-  int64_t few = 0, most = 0, blocks = 0;
+  int64_t most[kc::kShareCount] = {}, blocks[kc::kShareCount] = {};
   const auto note = [&](int64_t n, int64_t times) {
     const int64_t rows = n * p.G;
-    if (rows <= kc::kFewRows) {
-      few = std::max(few, rows);
-    } else {
-      most = std::max(most, rows);
-      blocks += (rows + kc::kDocRows - 1) / kc::kDocRows * times;
-    }
+    for (int i = 0; i < kc::kShareCount; ++i)
+      if (rows > kc::kShares[i].over && (rows <= kc::kShares[i].most || i + 1 == kc::kShareCount)) {
+        most[i] = std::max(most[i], rows);
+        blocks[i] += (rows + kc::kShares[i].block_rows - 1) / kc::kShares[i].block_rows * times;
+      }
   };
   if (cu_seqlens_host) {
     if (cu_seqlens_host[0] != 0 || cu_seqlens_host[n_seqs] > total_tokens) return KDA_ERR_BAD_SEQLENS;
@@ -490,19 +512,22 @@ extern "C" kda_status kda_cache_attention(
   } else {
     note(p.c.per_seq, n_seqs);
   }
-  kc::Plan plan = {};
-  int64_t grid = 0, joins = 0;
-  if (few > 0) {
-    plan = kc::make_plan(n_seqs, int32_t(few), H_kv);
-    grid = (int64_t(plan.targets) + n_seqs) * H_kv * plan.row_blocks;
-    joins = (few * H_kv + 3) / 4 * n_seqs;
-    if (workspace_bytes < size_t(plan.bytes)) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  kc::Plan plan[kc::kShareCount];
+  int64_t bytes = 0;
+  for (int i = 0; i < kc::kShareCount; ++i) {
+    plan[i] = {};
+    if (blocks[i] == 0) continue;
+    plan[i] = kc::make_plan(kc::kShares[i], n_seqs, most[i], blocks[i], H_kv);
+    bytes += plan[i].bytes;
+    if (most[i] > INT32_MAX - 128 || plan[i].grid > INT32_MAX ||
+        (plan[i].bytes > 0 && (most[i] * H_kv + 3) / 4 * n_seqs > INT32_MAX))
+      return KDA_ERR_UNSUPPORTED;
+  }
+  if (bytes > 0) {
+    if (workspace_bytes < size_t(bytes)) return KDA_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace) return KDA_ERR_NULL_POINTER;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KDA_ERR_UNSUPPORTED;
   }
-  if (grid > INT32_MAX || joins > INT32_MAX || most > INT32_MAX - kc::kDocRows ||
-      blocks * H_kv > INT32_MAX)
-    return KDA_ERR_UNSUPPORTED;
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_row_stride;
   p.scale2 = scale * kda::LOG2E;
@@ -510,28 +535,28 @@ extern "C" kda_status kda_cache_attention(
   p.out_stride = out_row_stride;
   p.lse = lse;
   p.lse_stride = lse_row_stride;
-  p.few_rows = kc::kFewRows;
-  p.row_blocks = plan.row_blocks;
-  p.targets = plan.targets;
-  uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  p.plan = reinterpret_cast<int2*>(ws);
-  p.stat = reinterpret_cast<float2*>(ws + plan.plan_bytes);
-  p.part = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.stat_bytes);
   const bool int8 = cache_dtype == KDA_CACHE_INT8;
-  if (few > 0) {
-    p.most_rows = int32_t(few);
-    if ((int8 ? kc::launch_attend<kc::kInt8>(p, plan, unsigned(grid), stream)
-              : kc::launch_attend<kc::kFp8>(p, plan, unsigned(grid), stream)) != hipSuccess)
-      return KDA_ERR_LAUNCH;
-    // no part is cut where the table is too short for two
-    if (int64_t(table_width) * page_size > kc::kMinUnits * kc::kUnit) {
-      hipLaunchKernelGGL(kc::join_kernel, dim3(unsigned(joins)), dim3(kc::kThreads), 0, stream, p);
-      if (hipGetLastError() != hipSuccess) return KDA_ERR_LAUNCH;
-    }
-  }
-  if (blocks > 0) {
-    p.most_rows = int32_t(most);
-    if (kc::launch_documents(p, int8, unsigned(blocks * H_kv), stream) != hipSuccess)
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  for (int i = 0; i < kc::kShareCount; ++i) {
+    if (blocks[i] == 0) continue;
+    const kc::Share& s = kc::kShares[i];
+    p.over = s.over;
+    p.most = s.most;
+    p.block_rows = plan[i].block_rows;
+    p.targets = plan[i].targets;
+    p.min_units = s.min_units;
+    p.plan = reinterpret_cast<int2*>(ws);
+    p.stat = reinterpret_cast<float2*>(ws + plan[i].plan_bytes);
+    p.part = reinterpret_cast<float*>(ws + plan[i].plan_bytes + plan[i].stat_bytes);
+    ws += plan[i].bytes;
+    const unsigned grid = unsigned(plan[i].grid);
+    const hipError_t e = s.waves ? kc::launch_documents(p, s.waves, int8, grid, stream)
+                         : int8  ? kc::launch_attend<kc::kInt8>(p, grid, stream)
+                                 : kc::launch_attend<kc::kFp8>(p, grid, stream);
+    if (e != hipSuccess) return KDA_ERR_LAUNCH;
+    // nothing is cut where the table is too short for two parts
+    if (plan[i].targets > 0 && int64_t(table_width) * page_size > s.min_units * kc::kUnit &&
+        kc::launch_join(p, int32_t(most[i]), most[i] * H_kv * n_seqs, stream) != hipSuccess)
       return KDA_ERR_LAUNCH;
   }
   return KDA_OK;

@@ -14,7 +14,7 @@
 // not): errors of half a step, independent of one another, that leave the output about as far off
 // as its own rounding does; a second part would cost a quarter more products.
 
-#include <limits.h>
+#include <math.h>
 
 #include "kda_cache_attn.h"
 
@@ -41,40 +41,6 @@ __device__ __forceinline__ int swizzle(int channel) { return (channel ^ (channel
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
-// Block `item` of all documents' blocks of ROWS rows, a document's last rows (with the most keys)
-// first.
-struct Block {
-  int32_t b, rb, slot;
-};
-__device__ __forceinline__ int32_t blocks_of(const AttnParams& p, int32_t b, int rows_per) {
-  const int32_t rows = min(rows_of(p, b), p.most_rows);
-  return rows <= p.few_rows ? 0 : (rows + rows_per - 1) / rows_per;
-}
-__device__ __forceinline__ bool find_block(const AttnParams& p, int32_t item, int lane, int rows_per,
-                                           Block& out) {
-  int32_t before = 0;
-  for (int32_t b0 = 0; b0 < p.c.n_seqs; b0 += 64) {
-    const int32_t b = b0 + lane;
-    const int32_t n = b < p.c.n_seqs ? blocks_of(p, b, rows_per) : 0;
-    int32_t sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int32_t x = __shfl_up(sum, d);
-      if (lane >= d) sum += x;
-    }
-    const uint64_t hit = __ballot(item < before + sum);
-    if (hit) {
-      const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      const int32_t first = before + __shfl(sum - n, at);
-      out.b = __builtin_amdgcn_readfirstlane(b0 + at);
-      out.rb = __builtin_amdgcn_readfirstlane(__shfl(n, at) - 1 - (item - first));
-      return true;
-    }
-    before += __shfl(sum, 63);
-  }
-  return false;
 }
 
 // A thread's share of a tile's codes. T threads.
@@ -214,29 +180,35 @@ __device__ __forceinline__ void store_share(Share<T>& s, int32_t at, bool diagon
   }
 }
 
+// Four waves have two tiles in LDS, and two such workgroups fill a CU; two waves one, and there are
+// four of them.
+constexpr int tiles_of(int waves) { return waves == 4 ? 2 : 1; }
+
 // One workgroup: (32 WAVES rows of a document, key/value head, part of its keys).
-template <int KIND, int WAVES>
+template <int KIND, int WAVES, bool SPLIT>
 __global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
-  constexpr int T = 64 * WAVES, ROWS = 32 * WAVES;
+  constexpr int T = 64 * WAVES, ROWS = 32 * WAVES, kTiles = tiles_of(WAVES);
   extern __shared__ __align__(16) uint8_t smem[];
   Tile* const tiles = reinterpret_cast<Tile*>(smem);
-  int32_t* const nan_at = reinterpret_cast<int32_t*>(tiles + 2);
+  int32_t* const nan_at = reinterpret_cast<int32_t*>(tiles + kTiles);
   const int lane = threadIdx.x & 63, m = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
-  Block blk;
-  if (!find_block(p, item, lane, ROWS, blk)) return;
-  const Seq seq = sequence(p.c, blk.b);
-  const int32_t rows = min(rows_of(p, blk.b), p.most_rows);
-  const int32_t row0 = blk.rb * ROWS + wave * 32;
+  Part part;
+  if (!find_part<SPLIT, T>(p, item, *reinterpret_cast<FindSmem*>(smem), part)) return;
+  __syncthreads();
+  const Seq seq = sequence(p.c, part.b);
+  const int32_t rows = rows_of(p, part.b);
+  const int32_t row0 = part.rb * ROWS + wave * 32;
   const int32_t len = p.c.num_pages > 0 ? max(seq.len, 0) : 0;
   const int32_t base = len - seq.n;  // position of the first token
-  // positions up to here are seen by the wave's first, the workgroup's first and last rows
+  // positions up to here are seen by the workgroup's first and last rows, the wave's first and last
+  const int32_t all_see = base + part.rb * ROWS / p.G;
+  const int32_t most = base + min(part.rb * ROWS + ROWS - 1, rows - 1) / p.G;
   const int32_t wave_all = base + row0 / p.G;
-  const int32_t all_see = base + blk.rb * ROWS / p.G;
-  const int32_t wave_most = base + min(row0 + 31, rows - 1) / p.G;
-  const int32_t most = base + min(blk.rb * ROWS + ROWS - 1, rows - 1) / p.G;
-  const int32_t end = min(len, most + 1);
+  const int32_t wave_most = row0 < rows ? base + min(row0 + 31, rows - 1) / p.G : -1;
+  const int32_t begin = SPLIT ? part.from : 0;
+  const int32_t end = min(SPLIT ? min(part.to, len) : len, most + 1);
 
   for (int i = threadIdx.x; i < D; i += T) nan_at[i] = INT_MAX;
 
@@ -266,20 +238,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
 
   Share<T> next;
   Pages<T> pages;
-  if (end > 0) {
-    load_pages<T>(p, blk.b, 0, end, pages);
-    load_share<T>(p, h, 0, end, pages, next);
-    load_pages<T>(p, blk.b, kTile, end, pages);
+  if (begin < end) {
+    load_pages<T>(p, part.b, begin, end, pages);
+    load_share<T>(p, h, begin, end, pages, next);
+    load_pages<T>(p, part.b, begin + kTile, end, pages);
   }
   __syncthreads();
-  if (end > 0) store_share<KIND, T>(next, 0, kTile - 1 > all_see, tiles[0], nan_at);
+  if (begin < end)
+    store_share<KIND, T>(next, begin, begin + kTile - 1 > all_see, tiles[0], nan_at);
   __syncthreads();
   int which = 0;
-  for (int32_t at = 0; at < end; at += kTile, which ^= 1) {
+  for (int32_t at = begin; at < end; at += kTile, which ^= kTiles - 1) {
     const bool more = at + kTile < end;
     if (more) {
       load_share<T>(p, h, at + kTile, end, pages, next);
-      load_pages<T>(p, blk.b, at + 2 * kTile, end, pages);
+      load_pages<T>(p, part.b, at + 2 * kTile, end, pages);
     }
     const Tile& tile = tiles[which];
     if (at <= wave_most) {
@@ -366,50 +339,71 @@ __global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
         }
       }
     }
+    if (kTiles == 1) __syncthreads();
     if (more)
-      store_share<KIND, T>(next, at + kTile, at + 2 * kTile - 1 > all_see, tiles[which ^ 1], nan_at);
+      store_share<KIND, T>(next, at + kTile, at + 2 * kTile - 1 > all_see,
+                           tiles[which ^ (kTiles - 1)], nan_at);
     __syncthreads();
   }
 
+  if (SPLIT && h == 0 && part.rb == 0 && part.index == 0 && threadIdx.x == 0)
+    p.plan[part.b] = make_int2(part.first_slot, part.parts);
   tot += __shfl_xor(tot, 32);
   if (r >= rows) return;
-  const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+  const bool whole = !SPLIT || part.parts == 1;
+  const float inv = !whole ? 1.0f : tot == 0.0f ? 0.0f : 1.0f / tot;
   uint16_t* const dst = p.out + (seq.first + tok) * p.out_stride + head * D;
+  const int64_t slot = (int64_t(part.slot) * p.c.H + h) * ROWS + wave * 32 + m;
   typedef u32x2 u32x2_u __attribute__((aligned(2)));
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ch = c * 32 + 8 * i + 4 * hi;
-      float y[4];
+      f32x4 y;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         y[j] = o[c][4 * i + j] * inv;
         if (KIND == kFp8 && nan_at[ch + j] <= last) y[j] = NAN;
       }
-      *reinterpret_cast<u32x2_u*>(dst + ch) =
-          u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+      if (whole)
+        *reinterpret_cast<u32x2_u*>(dst + ch) =
+            u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+      else
+        *reinterpret_cast<f32x4*>(p.part + slot * D + ch) = y;
     }
-  if (p.lse && hi == 0)
+  if (hi != 0) return;
+  if (!whole)
+    p.stat[slot] = make_float2(tot == 0.0f ? -INFINITY : ref, tot);
+  else if (p.lse)
     p.lse[(seq.first + tok) * p.lse_stride + head] =
         tot == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(tot)) * LN2;
 }
 
-template <int KIND, int WAVES>
+template <int KIND, int WAVES, bool SPLIT>
 hipError_t launch(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  constexpr int kSmem = 2 * sizeof(Tile) + D * 4;
+  constexpr int kSmem = tiles_of(WAVES) * sizeof(Tile) + D * 4;
   static const hipError_t ready = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&document_kernel<KIND, WAVES>),
+      reinterpret_cast<const void*>(&document_kernel<KIND, WAVES, SPLIT>),
       hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (ready != hipSuccess) return ready;
-  hipLaunchKernelGGL((document_kernel<KIND, WAVES>), dim3(grid), dim3(64 * WAVES), kSmem, stream, p);
+  hipLaunchKernelGGL((document_kernel<KIND, WAVES, SPLIT>), dim3(grid), dim3(64 * WAVES), kSmem,
+                     stream, p);
   return hipGetLastError();
+}
+template <int KIND>
+hipError_t launch(const AttnParams& p, int waves, unsigned grid, hipStream_t stream) {
+  if (p.targets > 0)
+    return waves == 2 ? launch<KIND, 2, true>(p, grid, stream) : launch<KIND, 4, true>(p, grid, stream);
+  return waves == 2 ? launch<KIND, 2, false>(p, grid, stream)
+                    : launch<KIND, 4, false>(p, grid, stream);
 }
 
 }  // namespace
 
-hipError_t launch_documents(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream) {
-  return int8 ? launch<kInt8, 4>(p, grid, stream) : launch<kFp8, 4>(p, grid, stream);
+hipError_t launch_documents(const AttnParams& p, int waves, bool int8, unsigned grid,
+                            hipStream_t stream) {
+  return int8 ? launch<kInt8>(p, waves, grid, stream) : launch<kFp8>(p, waves, grid, stream);
 }
 
 }  // namespace cache

@@ -44,9 +44,9 @@
  *
  * Errors common to the calls. KDA_ERR_BAD_SHAPE: negative sizes, H < 1,
  * num_pages < 0, table_width < 1, total_tokens no multiple of n_seqs without
- * cu_seqlens, tokens without sequences. KDA_ERR_UNSUPPORTED: D other than 128, cache_dtype, page_size, more
- * than 2^30 tokens, or n_seqs * table_width * page_size over 2^37, or more work items
- * than a launch takes (2^31 - 1 workgroups). KDA_ERR_BAD_STRIDE: a negative
+ * cu_seqlens, tokens without sequences. KDA_ERR_UNSUPPORTED: D other than 128, cache_dtype, page_size,
+ * H over 2^14, more than 2^30 tokens, table_width * page_size over 2^28 or n_seqs times
+ * that over 2^37, or more work items than a launch takes (2^31 - 1 workgroups). KDA_ERR_BAD_STRIDE: a negative
  * stride, a page stride below H * page_size * 128, output rows or the pages' rows
  * that overlap, a table_row_stride below table_width. num_pages = 0 needs no cache
  * pointers; total_tokens = 0 is a no-op that needs no pointers.
