@@ -67,6 +67,7 @@ __device__ __forceinline__ u32x2 widen4(uint32_t w) {
     return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
   } else {
+    asm("" : "+v"(w));  // one register up to here, not one for each byte
     return u32x2{pack_bf16x2_exact(float(int8_t(w)), float(int8_t(w >> 8))),
                  pack_bf16x2_exact(float(int8_t(w >> 16)), float(int8_t(w >> 24)))};
   }

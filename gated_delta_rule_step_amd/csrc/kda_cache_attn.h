@@ -59,8 +59,8 @@ struct FindSmem {
   int32_t work[4], items[4], slots[4];  // a wave's sums
   Part part;
 };
-// Work item `item`: the sequences one after the other, a sequence's last block (with the most
-// keys to see) first. Every workgroup of T threads finds it for itself from the lengths on the
+// Work item `item`: the sequences one after the other, a sequence's parts in turn, the blocks that
+// share a part's keys next to each other, the last one (with the most keys to see) first. Every workgroup of T threads finds it for itself from the lengths on the
 // device, K sequences a thread; SPLIT: the keys may be cut. Each sequence's keys are cut into equal
 // parts of a length that is the same for all, however ragged the batch, except for what rounding
 // to units leaves. (By single waves, 64 sequences at a time, 512 sequences took 10 us to walk.)
@@ -131,12 +131,11 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
       sizes(k, n, u);
       const int32_t parts = parts_of(u);
       if (item < first + n * parts) {
-        const int32_t rb = SPLIT ? (item - first) / parts : item - first;
         Part x;
         x.b = b0 + k;
         x.parts = parts;
-        x.index = item - first - rb * parts;
-        x.rb = n - 1 - rb;
+        x.index = SPLIT ? (item - first) / n : 0;
+        x.rb = n - 1 - (item - first - x.index * n);
         x.first_slot = slot;
         x.slot = slot + x.rb * parts + x.index;
         x.from = parts == 1 ? 0 : x.index * chunk * kUnit;

@@ -116,7 +116,7 @@ __device__ __forceinline__ void clear_values(Values& v, const int32_t (&live)[2]
 
 // One workgroup: (part of a sequence's keys, key/value head) for up to 16 NT rows.
 template <int KIND, int NT>
-__global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void attend_kernel(AttnParams p) {
+__global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnParams p) {
   __shared__ float sums[4][16 * kRow];
   __shared__ float refs[4][16], tots[4][16];
   __shared__ int32_t nan_at[D];
@@ -127,10 +127,11 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void 
   Part part;
   if (!find_part<true, kThreads>(p, item, find, part)) return;
   const Seq seq = sequence(p.c, part.b);
-  const int rows = rows_of(p, part.b);
+  const int rows = rows_of(p, part.b), row0 = part.rb * 16 * NT;
   const int32_t len = p.c.num_pages > 0 ? max(seq.len, 0) : 0;
   const int32_t to = min(part.to, len);
-  const int32_t base = len - seq.n;  // position of the first token, which every row sees
+  const int32_t base = len - seq.n;              // position of the first token
+  const int32_t all_see = base + row0 / p.G;     // every row sees up to here
 
   int32_t at = part.from + wave * kStep;
   Ids ids, ids_next;
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void 
   int32_t last[NT];  // the last position that the lane's row sees
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = 16 * n + m, t = r / p.G;
+    const int r = row0 + 16 * n + m, t = r / p.G;
     last[n] = base + t;
     const uint16_t* const src =
         p.q + (seq.first + t) * p.q_stride + (int64_t(h) * p.G + (r - t * p.G)) * D;
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void 
     int32_t live[2];  // tokens that exist
 #pragma unroll
     for (int u = 0; u < 2; ++u) live[u] = ids.id[u] < 0 ? 0 : min(16, to - (at + 16 * u));
-    const bool masked = live[0] < 16 || live[1] < 16 || at + kStep - 1 > base;
+    const bool masked = live[0] < 16 || live[1] < 16 || at + kStep - 1 > all_see;
     f32x4 acc[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void 
       ph[n] = __builtin_bit_cast(bf16x8, u32x4{hi[0], hi[1], hi[2], hi[3]});
       pl[n] = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], lo[2], lo[3]});
     }
-    if (masked) clear_values<KIND>(v, live, at, base, m, g, nan_at);
+    if (masked) clear_values<KIND>(v, live, at, all_see, m, g, nan_at);
 #pragma unroll
     for (int c4 = 0; c4 < 2; ++c4) {  // channels 8 m + 4 c4 ..
       uint32_t t0[4], t1[4];
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void 
       *reinterpret_cast<f32x4*>(to_lds + 4) = f32x4{o[n][4][r], o[n][5][r], o[n][6][r], o[n][7][r]};
     }
     __syncthreads();
-    const int r = 16 * n + row;
+    const int r = row0 + 16 * n + row;
     if (r >= rows) continue;
     const int t = r / p.G;
     const float top = fmaxf(fmaxf(refs[0][row], refs[1][row]), fmaxf(refs[2][row], refs[3][row]));
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? 2 : KIND == kFp8 ? 4 : 3) void 
         p.lse[(seq.first + t) * p.lse_stride + head] =
             sum == 0.0f ? -INFINITY : (r0 + __builtin_amdgcn_logf(sum)) * LN2;
     } else {
-      const int64_t slot = (int64_t(part.slot) * p.c.H + h) * p.block_rows + r;
+      const int64_t slot = (int64_t(part.slot) * p.c.H + h) * p.block_rows + (r - row0);
       float* const dst = p.part + slot * D + ch;
       *reinterpret_cast<f32x4*>(dst) = f32x4{acc[0], acc[1], acc[2], acc[3]};
       *reinterpret_cast<f32x4*>(dst + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
@@ -398,8 +399,8 @@ struct Share {
   int32_t block_rows, groups, min_units;
 };
 constexpr Share kShares[] = {
-    {0, 32, 0, 32, 1024, 8},
-    {32, 64, 2, 64, 1024, 4},
+    {0, 64, 0, 32, 1024, 8},
+    {64, 64, 2, 64, 1024, 4},
     {64, INT_MAX, 4, 128, 512, 4},
 };
 constexpr int kShareCount = 3;
