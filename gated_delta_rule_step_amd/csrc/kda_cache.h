@@ -1,6 +1,8 @@
 // The paged 8-bit cache: parameter block and helpers that its calls share.
 #pragma once
 
+#include <limits.h>
+
 #include "../../include/kda_cache.h"
 #include "kda_common.h"
 
@@ -63,11 +65,11 @@ __device__ __forceinline__ int32_t page_of(const CacheView& p, int32_t b, int32_
 // Four codes as two bf16 pairs, exact: e4m3 has 4 significant bits, int8 7.
 template <int KIND>
 __device__ __forceinline__ u32x2 widen4(uint32_t w) {
+  asm("" : "+v"(w));  // one register up to here, not one for each byte
   if constexpr (KIND == kFp8) {
     return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
   } else {
-    asm("" : "+v"(w));  // one register up to here, not one for each byte
     return u32x2{pack_bf16x2_exact(float(int8_t(w)), float(int8_t(w >> 8))),
                  pack_bf16x2_exact(float(int8_t(w >> 16)), float(int8_t(w >> 24)))};
   }
@@ -89,6 +91,17 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
   o[1] = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
   o[2] = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
   o[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
+}
+
+// e4m3's NaN codes among four, as the bytes' top bits.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// Leaves the position of these in first[0 .. 3] where none stands before it; the bytes' mask.
+__device__ __forceinline__ uint32_t note_nans(uint32_t codes, int32_t* first, int32_t at) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) atomicMin(first + c, codes >> (8 * c + 7) & 1 ? at : INT_MAX);
+  return (codes >> 7) * 0xffu;
 }
 
 __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {

@@ -1,8 +1,8 @@
 // Attention over the paged 8-bit cache: what its kernels share.
 //
-// Three kernels share the sequences of a call by their rows, G * tokens for each key/value head:
-// few rows (one token, or a few with few heads to a key), a handful of tokens, and documents. Each
-// cuts the keys into parts where its rows alone would not fill the chip.
+// Two kernels share the sequences of a call by their rows, G * tokens for each key/value head: few
+// rows (one token, or a handful) and documents. Each cuts the keys into parts where its rows alone
+// would not fill the chip.
 #pragma once
 
 #include <limits.h>
@@ -162,9 +162,9 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
   return true;
 }
 
-// Documents' and handfuls' kernel: workgroups of 32 * waves rows (waves 2 or 4).
-hipError_t launch_documents(const AttnParams& p, int waves, bool int8, unsigned grid,
-                            hipStream_t stream);
+// Documents: workgroups of kDocRows rows.
+constexpr int kDocRows = 128;
+hipError_t launch_documents(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream);
 
 }  // namespace cache
 }  // namespace kda

@@ -102,13 +102,8 @@ __device__ __forceinline__ void clear_values(Values& v, const int32_t (&live)[2]
       if (KIND == kFp8 && at + 16 * u + in > all_see) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t hit = ((v.w[u][r][j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-          if (hit)
-            for (int c = 0; c < 4; ++c)
-              if (hit >> (8 * c + 7) & 1) {
-                atomicMin(nan_at + m * 8 + 4 * j + c, at + 16 * u + in);
-                v.w[u][r][j] &= ~(0xffu << (8 * c));
-              }
+          const uint32_t hit = nan_codes(v.w[u][r][j]);
+          if (hit) v.w[u][r][j] &= ~note_nans(hit, nan_at + m * 8 + 4 * j, at + 16 * u + in);
         }
       }
     }
@@ -116,11 +111,13 @@ __device__ __forceinline__ void clear_values(Values& v, const int32_t (&live)[2]
 
 // One workgroup: (part of a sequence's keys, key/value head) for up to 16 NT rows.
 template <int KIND, int NT>
-__global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnParams p) {
+__global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnParams p) {
   __shared__ float sums[4][16 * kRow];
   __shared__ float refs[4][16], tots[4][16];
   __shared__ int32_t nan_at[D];
   __shared__ FindSmem find;
+  constexpr bool kInLds = NT > 1;
+  __shared__ bf16x8 queries[kInLds ? NT * 4 * 64 : 1];
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
@@ -144,15 +141,15 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnP
     load_values(p, h, at, ids, m, g, v);
   }
   if (threadIdx.x < D) nan_at[threadIdx.x] = INT_MAX;
-  __syncthreads();
 
   // queries: lane (m, g) holds row m's channels of group g, eight per product
-  bf16x8 q[NT][4];
+  bf16x8 q[4];
   int32_t last[NT];  // the last position that the lane's row sees
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = row0 + 16 * n + m, t = r / p.G;
     last[n] = base + t;
+    if (kInLds && n != wave) continue;
     const uint16_t* const src =
         p.q + (seq.first + t) * p.q_stride + (int64_t(h) * p.G + (r - t * p.G)) * D;
 #pragma unroll
@@ -160,9 +157,11 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnP
       u32x4 w = {0u, 0u, 0u, 0u};
       if (r < rows)
         w = *reinterpret_cast<const u32x4_u*>(src + (j >> 1) * 64 + g * 16 + (j & 1) * 8);
-      q[n][j] = __builtin_bit_cast(bf16x8, w);
+      q[j] = __builtin_bit_cast(bf16x8, w);
+      if (kInLds) queries[(n * 4 + j) * 64 + lane] = q[j];
     }
   }
+  __syncthreads();
 
   f32x4 o[NT][8];
   float ref[NT], tot[NT];
@@ -186,12 +185,13 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnP
 #pragma unroll
       for (int u = 0; u < 2; ++u) acc[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int u = 0; u < 2; ++u) {
         const bf16x8 a = widen8<KIND>(k.w[u][j >> 1][2 * (j & 1)], k.w[u][j >> 1][2 * (j & 1) + 1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n][u] = mfma32(a, q[n][j], acc[n][u]);
+        for (int n = 0; n < NT; ++n)
+          acc[n][u] = mfma32(a, kInLds ? queries[(n * 4 + j) * 64 + lane] : q[j], acc[n][u]);
       }
     const float f[2] = {p.scale2 * k.scale[0], p.scale2 * k.scale[1]};
     if (more) load_keys(p, h, at + kStride, ids_next, m, g, k);
@@ -245,14 +245,25 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnP
       uint32_t t0[4], t1[4];
       transpose4(v.w[0][0][c4], v.w[0][1][c4], v.w[0][2][c4], v.w[0][3][c4], t0);
       transpose4(v.w[1][0][c4], v.w[1][1][c4], v.w[1][2][c4], v.w[1][3][c4], t1);
+      if constexpr (NT == 1) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bf16x8 a = widen8<KIND>(t0[c], t1[c]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          o[n][4 * c4 + c] = mfma32(a, ph[n], o[n][4 * c4 + c]);
-          o[n][4 * c4 + c] = mfma32(a, pl[n], o[n][4 * c4 + c]);
+        for (int c = 0; c < 4; ++c) {
+          const bf16x8 a = widen8<KIND>(t0[c], t1[c]);
+          o[0][4 * c4 + c] = mfma32(a, ph[0], o[0][4 * c4 + c]);
+          o[0][4 * c4 + c] = mfma32(a, pl[0], o[0][4 * c4 + c]);
         }
+      } else {  // (a sum's two products apart: 95 -> 92 us; with one row block it costs registers)
+        bf16x8 a[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = widen8<KIND>(t0[c], t1[c]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[n][4 * c4 + c] = mfma32(a[c], ph[n], o[n][4 * c4 + c]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[n][4 * c4 + c] = mfma32(a[c], pl[n], o[n][4 * c4 + c]);
       }
     }
     if (more) load_values(p, h, at + kStride, ids_next, m, g, v);
@@ -316,106 +327,118 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 2) void attend_kernel(AttnP
     p.plan[part.b] = make_int2(part.first_slot, part.parts);
 }
 
-// Joins the parts of a row: a wave (or, WAVES = 4, where there are few rows, a workgroup) per row,
-// 32 lanes of 4 channels, four parts at a time.
-template <int WAVES>
+// Joins the parts of a row: 16 lanes of 8 channels, four parts at a time. WIDE: a workgroup's 16
+// groups share one row's parts (few rows, many parts), else each has a row of its own.
+template <bool WIDE>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p, int32_t most_rows) {
-  __shared__ f32x4 accs[WAVES == 1 ? 1 : WAVES][32];
-  __shared__ float tots[WAVES];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pairs = most_rows * p.c.H;
-  const int per = WAVES == 1 ? (pairs + 3) / 4 : pairs;
+  __shared__ float accs[WIDE ? 16 : 1][D];
+  __shared__ float2 stats[WIDE ? 16 : 1];
+  const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
+  const int pairs = most_rows * p.c.H, per = WIDE ? pairs : (pairs + 15) / 16;
   const int b = blockIdx.x / per;
-  const int i = WAVES == 1 ? (blockIdx.x - b * per) * 4 + wave : blockIdx.x - b * per;
-  if (i >= pairs || blocks_of(p, b) == 0) return;
+  if (blocks_of(p, b) == 0) return;
   const int2 plan = p.plan[b];
-  const Seq seq = sequence(p.c, b);
-  const int r = i / p.c.H, h = i - r * p.c.H;
-  if (plan.y <= 1 || r >= rows_of(p, b)) return;
-  const int rb = r / p.block_rows;
-  if (plan.x < 0 || plan.x + (int64_t(rb) + 1) * plan.y > 2 * p.targets) return;  // see find_part
+  const int rows = rows_of(p, b);
+  const int i = WIDE ? blockIdx.x - b * per : (blockIdx.x - b * per) * 16 + group;
+  const int h = i / most_rows, r = i - h * most_rows, rb = r / p.block_rows;
+  // (more slots than there are: see find_part)
+  const bool mine = plan.y > 1 && i < pairs && r < rows && plan.x >= 0 &&
+                    plan.x + (int64_t(rb) + 1) * plan.y <= 2 * p.targets;
+  if (WIDE ? !mine : __ballot(mine) == 0) return;
   const int64_t first = ((int64_t(plan.x) + int64_t(rb) * plan.y) * p.c.H + h) * p.block_rows +
                         (r - rb * p.block_rows);
   const int64_t step = int64_t(p.c.H) * p.block_rows;
-  float top = -INFINITY;
-  for (int s = lane; s < plan.y; s += 64) top = fmaxf(top, p.stat[first + s * step].x);
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
-  const float r0 = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int mine = (WAVES == 1 ? 0 : wave * 2) + (lane >> 5);
-  for (int s0 = mine; s0 < plan.y; s0 += 8 * WAVES) {
+  const int parts = mine ? plan.y : 0, stride = WIDE ? 16 : 1;
+  float top = -INFINITY, sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s0 = WIDE ? group : 0; s0 < parts; s0 += 4 * stride) {
     float2 st[4];
-    f32x4 x[4];
+    f32x4 x[4][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int s = s0 + 2 * WAVES * j;
+      const int s = s0 + j * stride;
       st[j] = make_float2(-INFINITY, 0.0f);
-      x[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (s < plan.y) {
-        st[j] = p.stat[first + s * step];
-        x[j] = *reinterpret_cast<const f32x4*>(p.part + (first + s * step) * D + (lane & 31) * 4);
+      x[j][0] = x[j][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (s < parts) {
+        const int64_t at = first + s * step;
+        st[j] = p.stat[at];
+        x[j][0] = *reinterpret_cast<const f32x4*>(p.part + at * D + ch);
+        x[j][1] = *reinterpret_cast<const f32x4*>(p.part + at * D + ch + 4);
       }
     }
+    const float now = fmaxf(fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x)), top);
+    const float r0 = now == -INFINITY ? 0.0f : now;
+    const float down = __builtin_amdgcn_exp2f(top - r0);
+    top = now;
+    sum *= down;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= down;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float f = __builtin_amdgcn_exp2f(st[j].x - r0);
       sum += st[j].y * f;
-      acc += x[j] * f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += x[j][c >> 2][c & 3] * f;
     }
   }
-  sum += __shfl_xor(sum, 32);
+  if (WIDE) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], 32);
-  if (WAVES > 1) {
-    if (lane < 32) accs[wave][lane] = acc;
-    if (lane == 0) tots[wave] = sum;
+    for (int c = 0; c < 8; ++c) accs[group][ch + c] = acc[c];
+    if (ch == 0) stats[group] = make_float2(top, sum);
     __syncthreads();
-    if (wave > 0) return;
+    if (group > 0) return;
+    top = stats[0].x;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) {
-      acc += accs[w][lane & 31];
-      sum += tots[w];
+    for (int w = 1; w < 16; ++w) top = fmaxf(top, stats[w].x);
+    const float r0 = top == -INFINITY ? 0.0f : top;
+    sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+    for (int w = 0; w < 16; ++w) {
+      const float f = __builtin_amdgcn_exp2f(stats[w].x - r0);
+      sum += stats[w].y * f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += accs[w][ch + c] * f;
     }
   }
-  if (lane >= 32) return;
+  if (!mine) return;
+  const Seq seq = sequence(p.c, b);
   const int t = r / p.G;
   const int64_t head = int64_t(h) * p.G + (r - t * p.G);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  typedef u32x2 u32x2_u __attribute__((aligned(2)));
-  *reinterpret_cast<u32x2_u*>(p.out + (seq.first + t) * p.out_stride + head * D + lane * 4) =
-      u32x2{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv)};
-  if (p.lse && lane == 0)
+  *reinterpret_cast<u32x4_u*>(p.out + (seq.first + t) * p.out_stride + head * D + ch) =
+      u32x4{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+            pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv)};
+  if (p.lse && ch == 0)
     p.lse[(seq.first + t) * p.lse_stride + head] =
-        sum == 0.0f ? -INFINITY : (r0 + __builtin_amdgcn_logf(sum)) * LN2;
+        sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + __builtin_amdgcn_logf(sum)) * LN2;
 }
 
-// Host: the three kernels' shares of a call.
+// Host: the two kernels' shares of a call.
 struct Share {
-  int32_t over, most;         // its sequences have over < rows <= most
-  int32_t waves;              // documents' kernel: waves; 0: few rows
-  int32_t block_rows, groups, min_units;
+  int32_t over, most;  // its sequences have over < rows <= most
+  int32_t block_rows;
+  int32_t groups;      // workgroups that the cut aims at
+  int32_t min_units;   // of a part
 };
-constexpr Share kShares[] = {
-    {0, 64, 0, 32, 1024, 8},
-    {64, 64, 2, 64, 1024, 4},
-    {64, INT_MAX, 4, 128, 512, 4},
-};
-constexpr int kShareCount = 3;
+constexpr int kFew = 0, kDocuments = 1;
+// Up to 128 rows stay with blocks of 32 in registers, whose keys the second to fourth block find in
+// the L2 (64 sequences of up to 4000 tokens, 8 heads, as few rows | as documents, us: 72 rows 113 |
+// 196, 128 rows 143 | 200; 8 sequences: 128 rows 31 | 35, 160 rows 38 | 39; one of 30000: 54 | 52).
+// The cut's sizes matter little: 512 to 4096 workgroups, 4 or 8 units are within 5 %.
+constexpr Share kShares[] = {{0, 128, 32, 1024, 8}, {128, INT_MAX, kDocRows, 512, 4}};
 
 struct Plan {
   int32_t block_rows, targets;
   int64_t plan_bytes, stat_bytes, bytes, grid;
 };
 // `rows`: the most of a sequence; `blocks`: in all.
-Plan make_plan(const Share& s, int32_t n_seqs, int64_t rows, int64_t blocks, int32_t H) {
+Plan make_plan(int kind, int32_t n_seqs, int64_t rows, int64_t blocks, int32_t H) {
+  const Share& s = kShares[kind];
   Plan r = {};
-  r.block_rows = s.waves ? s.block_rows : int32_t(std::min<int64_t>(rows, s.block_rows));
+  r.block_rows = kind == kFew ? int32_t(std::min<int64_t>(rows, s.block_rows)) : s.block_rows;
   const int64_t targets = std::max<int64_t>(1, s.groups / H);
   // few rows are cut however many sequences there are, since those may differ in length
-  if (s.waves == 0 || blocks < targets) {
+  if (kind == kFew || blocks < targets) {
     r.targets = int32_t(targets);
     // what is cut has less than twice its share of the parts
     const int64_t vecs = 2 * targets * H * r.block_rows;
@@ -438,10 +461,10 @@ hipError_t launch_attend(const AttnParams& p, unsigned grid, hipStream_t stream)
 
 hipError_t launch_join(const AttnParams& p, int32_t rows, int64_t pairs, hipStream_t stream) {
   if (pairs <= 1024)
-    hipLaunchKernelGGL(join_kernel<4>, dim3(unsigned(pairs)), dim3(kThreads), 0, stream, p, rows);
+    hipLaunchKernelGGL(join_kernel<true>, dim3(unsigned(pairs)), dim3(kThreads), 0, stream, p, rows);
   else
-    hipLaunchKernelGGL(join_kernel<1>,
-                       dim3(unsigned((int64_t(rows) * p.c.H + 3) / 4 * p.c.n_seqs)),
+    hipLaunchKernelGGL(join_kernel<false>,
+                       dim3(unsigned((int64_t(rows) * p.c.H + 15) / 16 * p.c.n_seqs)),
                        dim3(kThreads), 0, stream, p, rows);
   return hipGetLastError();
 }
@@ -463,9 +486,9 @@ extern "C" size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t tot
   // whatever the sequences' shares of the tokens
   const int64_t rows = total_tokens * (H_q / H_kv);
   int64_t bytes = 0;
-  for (const kc::Share& s : kc::kShares)
-    if (rows > s.over)
-      bytes += kc::make_plan(s, n_seqs, std::min<int64_t>(rows, s.most), 0, H_kv).bytes;
+  for (int i = 0; i < 2; ++i)
+    if (rows > kc::kShares[i].over)
+      bytes += kc::make_plan(i, n_seqs, std::min<int64_t>(rows, kc::kShares[i].most), 0, H_kv).bytes;
   return size_t(bytes);
 }
 
@@ -494,11 +517,11 @@ extern "C" kda_status kda_cache_attention(
   if (!q || !out) return KDA_ERR_NULL_POINTER;
   if ((cu_seqlens != nullptr) != (cu_seqlens_host != nullptr)) return KDA_ERR_NULL_POINTER;
   p.G = H_q / H_kv;
-  int64_t most[kc::kShareCount] = {}, blocks[kc::kShareCount] = {};
+  int64_t most[2] = {}, blocks[2] = {};
   const auto note = [&](int64_t n, int64_t times) {
     const int64_t rows = n * p.G;
-    for (int i = 0; i < kc::kShareCount; ++i)
-      if (rows > kc::kShares[i].over && (rows <= kc::kShares[i].most || i + 1 == kc::kShareCount)) {
+    for (int i = 0; i < 2; ++i)
+      if (rows > kc::kShares[i].over && (rows <= kc::kShares[i].most || i == kc::kDocuments)) {
         most[i] = std::max(most[i], rows);
         blocks[i] += (rows + kc::kShares[i].block_rows - 1) / kc::kShares[i].block_rows * times;
       }
@@ -513,15 +536,15 @@ extern "C" kda_status kda_cache_attention(
   } else {
     note(p.c.per_seq, n_seqs);
   }
-  kc::Plan plan[kc::kShareCount];
+  kc::Plan plan[2];
   int64_t bytes = 0;
-  for (int i = 0; i < kc::kShareCount; ++i) {
+  for (int i = 0; i < 2; ++i) {
     plan[i] = {};
     if (blocks[i] == 0) continue;
-    plan[i] = kc::make_plan(kc::kShares[i], n_seqs, most[i], blocks[i], H_kv);
+    plan[i] = kc::make_plan(i, n_seqs, most[i], blocks[i], H_kv);
     bytes += plan[i].bytes;
     if (most[i] > INT32_MAX - 128 || plan[i].grid > INT32_MAX ||
-        (plan[i].bytes > 0 && (most[i] * H_kv + 3) / 4 * n_seqs > INT32_MAX))
+        (plan[i].bytes > 0 && (most[i] * H_kv + 15) / 16 * n_seqs > INT32_MAX))
       return KDA_ERR_UNSUPPORTED;
   }
   if (bytes > 0) {
@@ -538,7 +561,7 @@ extern "C" kda_status kda_cache_attention(
   p.lse_stride = lse_row_stride;
   const bool int8 = cache_dtype == KDA_CACHE_INT8;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  for (int i = 0; i < kc::kShareCount; ++i) {
+  for (int i = 0; i < 2; ++i) {
     if (blocks[i] == 0) continue;
     const kc::Share& s = kc::kShares[i];
     p.over = s.over;
@@ -551,9 +574,9 @@ extern "C" kda_status kda_cache_attention(
     p.part = reinterpret_cast<float*>(ws + plan[i].plan_bytes + plan[i].stat_bytes);
     ws += plan[i].bytes;
     const unsigned grid = unsigned(plan[i].grid);
-    const hipError_t e = s.waves ? kc::launch_documents(p, s.waves, int8, grid, stream)
-                         : int8  ? kc::launch_attend<kc::kInt8>(p, grid, stream)
-                                 : kc::launch_attend<kc::kFp8>(p, grid, stream);
+    const hipError_t e = i == kc::kDocuments ? kc::launch_documents(p, int8, grid, stream)
+                         : int8            ? kc::launch_attend<kc::kInt8>(p, grid, stream)
+                                           : kc::launch_attend<kc::kFp8>(p, grid, stream);
     if (e != hipSuccess) return KDA_ERR_LAUNCH;
     // nothing is cut where the table is too short for two parts
     if (plan[i].targets > 0 && int64_t(table_width) * page_size > s.min_units * kc::kUnit &&

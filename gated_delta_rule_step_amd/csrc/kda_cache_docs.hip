@@ -22,6 +22,7 @@ namespace kda {
 namespace cache {
 namespace {
 
+constexpr int kThreads = 256;
 constexpr int kTile = 64;  // keys
 constexpr float kSlack = 8.0f;
 constexpr float kNoRef = -3.0e38f;
@@ -149,14 +150,8 @@ __device__ __forceinline__ void store_share(Share<T>& s, int32_t at, bool diagon
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t hit = ((s.v[i][r][j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-          if (hit) {
-            for (int c = 0; c < 4; ++c)
-              if (hit >> (8 * c + 7) & 1) {
-                atomicMin(nan_at + ch + 4 * j + c, at + tok + r);
-                s.v[i][r][j] &= ~(0xffu << (8 * c));
-              }
-          }
+          const uint32_t hit = nan_codes(s.v[i][r][j]);
+          if (hit) s.v[i][r][j] &= ~note_nans(hit, nan_at + ch + 4 * j, at + tok + r);
         }
     }
     const bool power = !__any((__float_as_uint(s.vs[i]) & 0x007fffffu) != 0 || s.vs[i] <= 0.0f);
@@ -180,17 +175,13 @@ __device__ __forceinline__ void store_share(Share<T>& s, int32_t at, bool diagon
   }
 }
 
-// Four waves have two tiles in LDS, and two such workgroups fill a CU; two waves one, and there are
-// four of them.
-constexpr int tiles_of(int waves) { return waves == 4 ? 2 : 1; }
-
-// One workgroup: (32 WAVES rows of a document, key/value head, part of its keys).
-template <int KIND, int WAVES, bool SPLIT>
-__global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
-  constexpr int T = 64 * WAVES, ROWS = 32 * WAVES, kTiles = tiles_of(WAVES);
+// One workgroup: (128 rows of a document, key/value head, part of its keys).
+template <int KIND, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
+  constexpr int T = kThreads, ROWS = kDocRows;
   extern __shared__ __align__(16) uint8_t smem[];
   Tile* const tiles = reinterpret_cast<Tile*>(smem);
-  int32_t* const nan_at = reinterpret_cast<int32_t*>(tiles + kTiles);
+  int32_t* const nan_at = reinterpret_cast<int32_t*>(tiles + 2);
   const int lane = threadIdx.x & 63, m = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
@@ -248,7 +239,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
     store_share<KIND, T>(next, begin, begin + kTile - 1 > all_see, tiles[0], nan_at);
   __syncthreads();
   int which = 0;
-  for (int32_t at = begin; at < end; at += kTile, which ^= kTiles - 1) {
+  for (int32_t at = begin; at < end; at += kTile, which ^= 1) {
     const bool more = at + kTile < end;
     if (more) {
       load_share<T>(p, h, at + kTile, end, pages, next);
@@ -339,10 +330,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
         }
       }
     }
-    if (kTiles == 1) __syncthreads();
     if (more)
-      store_share<KIND, T>(next, at + kTile, at + 2 * kTile - 1 > all_see,
-                           tiles[which ^ (kTiles - 1)], nan_at);
+      store_share<KIND, T>(next, at + kTile, at + 2 * kTile - 1 > all_see, tiles[which ^ 1], nan_at);
     __syncthreads();
   }
 
@@ -380,30 +369,23 @@ __global__ __launch_bounds__(64 * WAVES, 2) void document_kernel(AttnParams p) {
         tot == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(tot)) * LN2;
 }
 
-template <int KIND, int WAVES, bool SPLIT>
+template <int KIND, bool SPLIT>
 hipError_t launch(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  constexpr int kSmem = tiles_of(WAVES) * sizeof(Tile) + D * 4;
+  constexpr int kSmem = 2 * sizeof(Tile) + D * 4;
   static const hipError_t ready = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&document_kernel<KIND, WAVES, SPLIT>),
+      reinterpret_cast<const void*>(&document_kernel<KIND, SPLIT>),
       hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (ready != hipSuccess) return ready;
-  hipLaunchKernelGGL((document_kernel<KIND, WAVES, SPLIT>), dim3(grid), dim3(64 * WAVES), kSmem,
-                     stream, p);
+  hipLaunchKernelGGL((document_kernel<KIND, SPLIT>), dim3(grid), dim3(kThreads), kSmem, stream, p);
   return hipGetLastError();
-}
-template <int KIND>
-hipError_t launch(const AttnParams& p, int waves, unsigned grid, hipStream_t stream) {
-  if (p.targets > 0)
-    return waves == 2 ? launch<KIND, 2, true>(p, grid, stream) : launch<KIND, 4, true>(p, grid, stream);
-  return waves == 2 ? launch<KIND, 2, false>(p, grid, stream)
-                    : launch<KIND, 4, false>(p, grid, stream);
 }
 
 }  // namespace
 
-hipError_t launch_documents(const AttnParams& p, int waves, bool int8, unsigned grid,
-                            hipStream_t stream) {
-  return int8 ? launch<kInt8>(p, waves, grid, stream) : launch<kFp8>(p, waves, grid, stream);
+hipError_t launch_documents(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream) {
+  if (p.targets > 0)
+    return int8 ? launch<kInt8, true>(p, grid, stream) : launch<kFp8, true>(p, grid, stream);
+  return int8 ? launch<kInt8, false>(p, grid, stream) : launch<kFp8, false>(p, grid, stream);
 }
 
 }  // namespace cache

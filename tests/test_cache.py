@@ -8,7 +8,7 @@ Attention. Products of bf16 and widened codes are exact in fp32; a score sums 12
 takes two more roundings, so it is off by at most d = 131 * 2^-24 * |scale| sum |q k|, and its
 weight by that relatively, plus 2^-22 for the exponential. A sum of n weights adds n * 2^-24
 at most, and so does each output sum. The weights enter the second product with a relative
-error of `weight`: 2^-16 as two bf16 parts (up to 32 rows, tokens times query heads of a
+error of `weight`: 2^-16 as two bf16 parts (up to 128 rows, tokens times query heads of a
 key/value head), half a step of bf16, 2^-8, as one (more rows). So out is off by at most
 half a step of bf16, 2^-8 |out|, and (weight + 2 d + 2 n 2^-24 + 2^-20) times the mean of |v|
 under the weights; lse by d + n 2^-24 + 2^-21 (1 + |lse|). A weight under 2^-126 of the largest one's
@@ -531,7 +531,7 @@ def test_attention_draft_tokens(lib, kind, T, H, G):
     for P in (16, 64):
         pool = Pool(kind, H, P, totals, seed=T + G).fill()
         _check_attention(pool, [T] * len(totals), G, True, seed=T,
-                         weight=2.0 ** (-16 if T * G <= 32 else -8))
+                         weight=2.0 ** (-16 if T * G <= 128 else -8))
 
 
 @pytest.mark.gpu
