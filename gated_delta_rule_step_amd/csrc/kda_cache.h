@@ -93,6 +93,17 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
   o[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
 }
 
+template <int KIND>
+__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+  if constexpr (KIND == kFp8) {
+    const f32x2 a = f8x2_lo(w), b = f8x2_hi(w);
+    x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
+  } else {
+    x[0] = float(int8_t(w)), x[1] = float(int8_t(w >> 8));
+    x[2] = float(int8_t(w >> 16)), x[3] = float(int8_t(w >> 24));
+  }
+}
+
 // e4m3's NaN codes among four, as the bytes' top bits.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;

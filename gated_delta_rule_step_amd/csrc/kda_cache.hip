@@ -118,17 +118,6 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
            (uint32_t(int32_t(c)) & 255u) << 16 | uint32_t(int32_t(d)) << 24;
   }
 }
-template <int KIND>
-__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
-  if constexpr (KIND == kFp8) {
-    const f32x2 a = f8x2_lo(w), b = f8x2_hi(w);
-    x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
-  } else {
-    x[0] = float(int8_t(w)), x[1] = float(int8_t(w >> 8));
-    x[2] = float(int8_t(w >> 16)), x[3] = float(int8_t(w >> 24));
-  }
-}
-
 // One (page, head, side) by WAVES waves, 4 WAVES PASSES >= the page's new tokens. A row is 16
 // lanes of 8 channels.
 template <int KIND, int WAVES, int PASSES>

@@ -31,7 +31,7 @@ constexpr float kSlack = 8.0f;
 
 // A wave's 32 tokens are two tiles of 16, each inside one page.
 struct Ids {
-  int32_t id[2];  // -1: no page
+  int32_t raw[2];  // as the table has them: looked at only where they are used, a step later
 };
 struct Keys {
   u32x4 w[2][2];  // lane (m, g): token m, channels 64 i + 16 g ..
@@ -45,36 +45,41 @@ struct Values {
 __device__ __forceinline__ void load_ids(const AttnParams& p, int32_t b, int32_t at, int32_t end,
                                          Ids& s) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int32_t tok = at + 16 * u;
-    s.id[u] = tok < end ? page_of(p.c, b, tok >> p.c.page_shift) : -1;
-  }
+  for (int u = 0; u < 2; ++u)
+    s.raw[u] = p.c.table[b * p.c.table_stride +
+                         (max(min(at + 16 * u, end - 1), 0) >> p.c.page_shift)];
+}
+__device__ __forceinline__ int32_t known_page(const AttnParams& p, const Ids& s, int u, int32_t at,
+                                              int32_t end) {
+  return at + 16 * u < end && uint32_t(s.raw[u]) < uint64_t(p.c.num_pages) ? s.raw[u] : -1;
 }
 // Page 0's bytes in the place of none's.
 __device__ __forceinline__ int64_t tile_at(const CacheView& c, int32_t id, int64_t page, int32_t h,
                                            int32_t tok) {
   return max(id, 0) * page + ((int64_t(h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D;
 }
-__device__ __forceinline__ void load_keys(const AttnParams& p, int32_t h, int32_t at, const Ids& ids,
-                                          int m, int g, Keys& s) {
+__device__ __forceinline__ void load_keys(const AttnParams& p, int32_t h, int32_t at, int32_t end,
+                                          const Ids& ids, int m, int g, Keys& s) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const uint8_t* const k = p.c.k + tile_at(p.c, ids.id[u], p.c.k_page, h, at + 16 * u);
+    const int32_t id = known_page(p, ids, u, at, end);
+    const uint8_t* const k = p.c.k + tile_at(p.c, id, p.c.k_page, h, at + 16 * u);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       s.w[u][i] = *reinterpret_cast<const u32x4*>(k + (m * D + i * 64 + g * 16));
-    s.scale[u] = p.c.k_scale[int64_t(max(ids.id[u], 0)) * p.c.H + h];
+    s.scale[u] = p.c.k_scale[int64_t(max(id, 0)) * p.c.H + h];
   }
 }
 __device__ __forceinline__ void load_values(const AttnParams& p, int32_t h, int32_t at,
-                                            const Ids& ids, int m, int g, Values& s) {
+                                            int32_t end, const Ids& ids, int m, int g, Values& s) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const uint8_t* const v = p.c.v + tile_at(p.c, ids.id[u], p.c.v_page, h, at + 16 * u);
+    const int32_t id = known_page(p, ids, u, at, end);
+    const uint8_t* const v = p.c.v + tile_at(p.c, id, p.c.v_page, h, at + 16 * u);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       s.w[u][r] = *reinterpret_cast<const u32x2*>(v + (4 * g * D + m * 8) + r * D);
-    s.scale[u] = p.c.v_scale[int64_t(max(ids.id[u], 0)) * p.c.H + h];
+    s.scale[u] = p.c.v_scale[int64_t(max(id, 0)) * p.c.H + h];
   }
 }
 
@@ -134,11 +139,11 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
   Ids ids, ids_next;
   Keys k;
   Values v;
-  load_ids(p, part.b, at, to, ids);
-  load_ids(p, part.b, at + kStride, to, ids_next);
   if (at < to) {
-    load_keys(p, h, at, ids, m, g, k);
-    load_values(p, h, at, ids, m, g, v);
+    load_ids(p, part.b, at, to, ids);
+    load_ids(p, part.b, at + kStride, to, ids_next);
+    load_keys(p, h, at, to, ids, m, g, k);
+    load_values(p, h, at, to, ids, m, g, v);
   }
   if (threadIdx.x < D) nan_at[threadIdx.x] = INT_MAX;
 
@@ -177,7 +182,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
     const bool more = at + kStride < to;
     int32_t live[2];  // tokens that exist
 #pragma unroll
-    for (int u = 0; u < 2; ++u) live[u] = ids.id[u] < 0 ? 0 : min(16, to - (at + 16 * u));
+    for (int u = 0; u < 2; ++u)
+      live[u] = known_page(p, ids, u, at, to) < 0 ? 0 : min(16, to - (at + 16 * u));
     const bool masked = live[0] < 16 || live[1] < 16 || at + kStep - 1 > all_see;
     f32x4 acc[NT][2];
 #pragma unroll
@@ -194,7 +200,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
           acc[n][u] = mfma32(a, kInLds ? queries[(n * 4 + j) * 64 + lane] : q[j], acc[n][u]);
       }
     const float f[2] = {p.scale2 * k.scale[0], p.scale2 * k.scale[1]};
-    if (more) load_keys(p, h, at + kStride, ids_next, m, g, k);
+    if (more) load_keys(p, h, at + kStride, to, ids_next, m, g, k);
     bf16x8 ph[NT], pl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -266,7 +272,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
           for (int c = 0; c < 4; ++c) o[n][4 * c4 + c] = mfma32(a[c], pl[n], o[n][4 * c4 + c]);
       }
     }
-    if (more) load_values(p, h, at + kStride, ids_next, m, g, v);
+    if (more) load_values(p, h, at + kStride, to, ids_next, m, g, v);
     ids = ids_next;
     load_ids(p, part.b, at + 2 * kStride, to, ids_next);
   }
