@@ -56,7 +56,7 @@ struct Part {
   int32_t b, rb, index, parts, slot, first_slot, from, to;
 };
 struct FindSmem {
-  int32_t work[8], items[8], slots[8];  // a wave's sums
+  int32_t work[4], items[4], slots[4];  // a wave's sums
   Part part;
 };
 // Work item `item`: the sequences one after the other, a sequence's parts in turn, the blocks that
@@ -163,7 +163,7 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
 }
 
 // Documents: workgroups of kDocRows rows.
-constexpr int kDocRows = 256;
+constexpr int kDocRows = 128;
 hipError_t launch_documents(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream);
 
 }  // namespace cache

@@ -2,21 +2,17 @@
 //
 // Bound by the matrix units: 4 * 128 operations for every visible (query row, key) pair. Row r of
 // a document and key/value head is query head r mod G of token r / G, so that grouped heads
-// share what is loaded. A workgroup of eight waves takes 32 rows per wave and walks 64 keys at a time: their
+// share what is loaded. A workgroup takes 32 rows per wave and walks 64 keys at a time: their
 // codes are widened to bf16 once for all its waves, into LDS (exact for the values' scales that
-// kda_cache_write makes; the keys' scales multiply the scores), the values transposed on the way.
+// kda_cache_write makes; the keys' scales multiply the scores), the values transposed on the way. The
+// next tile's codes come in meanwhile, and two workgroups share a CU, so that one's exponentials
+// run beside the other's products.
 //
 // With keys as the rows of the products (S^T = K Q^T, O^T = V^T P^T) all of a lane's scores and
 // outputs belong to one query row, and the weights P^T leave the first product in the
 // layout that the second one reads. They are rounded to bf16 there (the sum that divides them is
 // not): errors of half a step, independent of one another, that leave the output about as far off
 // as its own rounding does; a second part would cost a quarter more products.
-//
-// A wave's products and its exponentials take about as long, and neither hides the other. So the
-// waves of a SIMD (one of the first four, one of the last four) take turns: in one phase the
-// first multiply (scores of tile t + 1, outputs of tile t) while the last do the arithmetic between, in the next the
-// other way round, with a barrier after each phase. The first four waves also bring in the keys, the last the
-// values.
 
 #include <math.h>
 
@@ -26,7 +22,7 @@ namespace kda {
 namespace cache {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kTile = 64;   // keys
 constexpr float kSlack = 8.0f;
 constexpr float kNoRef = -3.0e38f;
@@ -51,78 +47,39 @@ __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// A wave's share of a tile lies in groups of 16 tokens, each inside one page: its bytes are a
-// scalar base and a lane's offset. Page indices and scales come by vector loads all the same, whose
-// counter keeps their order, and are looked at only where they are used, a tile later.
+// A wave brings in 16 tokens of a tile, which lie in one page: their bytes are a scalar base and
+// a lane's offset. Page indices and scales come by vector loads all the same, whose counter keeps
+// their order, and are looked at only where they are used, a tile later.
 __device__ __forceinline__ int32_t load_page(const AttnParams& p, int32_t b, int32_t tok,
                                              int32_t end, int32_t zero) {
   return p.c.table[b * p.c.table_stride + (min(tok, end - 1) >> p.c.page_shift) + zero];
 }
-__device__ __forceinline__ int32_t known_page(const AttnParams& p, int32_t raw, int32_t tok,
-                                              int32_t end) {
-  const int32_t id = __builtin_amdgcn_readfirstlane(raw);
-  return tok < end && uint32_t(id) < uint64_t(p.c.num_pages) ? id : -1;
-}
-__device__ __forceinline__ const uint8_t* group_at(const CacheView& c, const uint8_t* cache,
-                                                   int64_t page, int32_t id, int32_t h, int32_t tok) {
-  const int32_t in = tok & ((1 << c.page_shift) - 1);
-  return cache + max(id, 0) * page + ((int64_t(h) << c.page_shift) + in) * D;
-}
-
-// Keys of a tile, by the first four waves: 16 codes of rows 8 wave + lane / 8 and 32 further on.
-struct KeyShare {
-  u32x4 w[2];
-  float scale[2];
-  int32_t live[2];
-};
-__device__ __forceinline__ void load_share(const AttnParams& p, int32_t h, int32_t tok, int32_t end,
-                                           int wave, int lane, int32_t zero,
-                                           const int32_t (&raw)[2], KeyShare& s) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int32_t id = known_page(p, raw[i], tok + 32 * i, end);
-    s.w[i] = *reinterpret_cast<const u32x4*>(
-        group_at(p.c, p.c.k, p.c.k_page, id, h, tok + 32 * i) + ((wave & 1) * 8 * D + lane * 16));
-    s.scale[i] = p.c.k_scale[int64_t(max(id, 0)) * p.c.H + h + zero];
-    s.live[i] = id < 0 ? 0 : min(16, end - (tok + 32 * i));
-  }
-}
-template <int KIND>
-__device__ __forceinline__ void store_share(const KeyShare& s, int wave, int lane, int slot,
-                                            Smem& lds) {
-  const int c = (lane & 7) ^ (lane >> 3);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = 8 * wave + (lane >> 3) + 32 * i;
-    const u32x2 a = widen4<KIND>(s.w[i][0]), b = widen4<KIND>(s.w[i][1]);
-    const u32x2 d = widen4<KIND>(s.w[i][2]), e = widen4<KIND>(s.w[i][3]);
-    lds.k[slot][row * 16 + c] = u32x4{a[0], a[1], b[0], b[1]};
-    lds.k[slot][row * 16 + 8 + c] = u32x4{d[0], d[1], e[0], e[1]};
-    if ((wave & 1) == 0 && lane == 0) {
-      lds.ks[slot][(wave >> 1) + 2 * i] = s.scale[i];
-      lds.live[slot][(wave >> 1) + 2 * i] = s.live[i];
-    }
-  }
-}
-
-// Values of a tile, by the last four waves: 16 tokens a wave, four of 8 channels a lane.
-// Neighbouring lanes hold quads 0 and 2, or 1 and 3.
-struct ValueShare {
-  u32x2 w[4];
-  float scale;
-  int32_t live;
+struct Share {
+  u32x4 k[2];  // codes 16 (lane mod 8) .. of token lane / 8 and of the one 8 further on
+  u32x2 v[4];  // four tokens of 8 channels; neighbouring lanes hold quads 0 and 2, or 1 and 3
+  float ks, vs;
+  int32_t live;  // tokens that exist
 };
 __device__ __forceinline__ int lane_token(int lane) { return (lane & 1) * 8 + (lane >> 5) * 4; }
 __device__ __forceinline__ int lane_channel(int lane) { return ((lane >> 1) & 15) * 8; }
-__device__ __forceinline__ void load_share(const AttnParams& p, int32_t h, int32_t tok, int32_t end,
-                                           int lane, int32_t zero, int32_t raw, ValueShare& s) {
-  const int32_t id = known_page(p, raw, tok, end);
-  const uint8_t* const v = group_at(p.c, p.c.v, p.c.v_page, id, h, tok);
+
+__device__ __forceinline__ void load_share(const AttnParams& p, int32_t raw, int32_t h, int32_t tok,
+                                           int32_t end, int lane, int32_t zero, Share& s) {
+  const int32_t id = __builtin_amdgcn_readfirstlane(raw);
+  const bool is = tok < end && uint32_t(id) < uint32_t(p.c.num_pages);
+  const int32_t use = is ? id : 0;  // page 0's bytes in the place of none's
+  const int32_t in = ((h << p.c.page_shift) + (tok & ((1 << p.c.page_shift) - 1))) * D;
+  const uint8_t* const k = p.c.k + (use * p.c.k_page + in);
+  const uint8_t* const v = p.c.v + (use * p.c.v_page + in);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s.k[i] = *reinterpret_cast<const u32x4*>(k + lane * 16 + i * 8 * D);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    s.w[r] = *reinterpret_cast<const u32x2*>(v + (lane_token(lane) * D + lane_channel(lane) + r * D));
-  s.scale = p.c.v_scale[int64_t(max(id, 0)) * p.c.H + h + zero];
-  s.live = id < 0 ? 0 : min(16, end - tok);
+    s.v[r] = *reinterpret_cast<const u32x2*>(v + (lane_token(lane) * D + lane_channel(lane)) + r * D);
+  const int64_t at = int64_t(use) * p.c.H + h + zero;
+  s.ks = p.c.k_scale[at];
+  s.vs = p.c.v_scale[at];
+  s.live = is ? min(16, end - tok) : 0;
 }
 
 // Widened values of four tokens of one channel, times their scale (EXACT: a power of two).
@@ -139,37 +96,50 @@ __device__ __forceinline__ u32x2 scaled4(uint32_t w, float scale) {
   }
 }
 
-// Tokens that do not exist become zeros. With `diagonal`, so do NaN codes, which leave their
-// position in nan_at: rows that see it become NaN in the end, and the others stay clear of 0 NaN.
+// To LDS. Tokens that do not exist become zeros. With `diagonal`, so do NaN codes, which leave
+// their position in nan_at: rows that see it become NaN in the end, and the others stay clear of 0 NaN.
 template <int KIND>
-__device__ __forceinline__ void store_share(ValueShare& s, int lane, int32_t tok, bool diagonal,
-                                            int slot, int group, Smem& lds) {
+__device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_t tok, bool diagonal,
+                                            int slot, Smem& lds) {
+  const int c0 = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 16 * wave + (lane >> 3) + 8 * i;
+    const u32x2 a = widen4<KIND>(s.k[i][0]), b = widen4<KIND>(s.k[i][1]);
+    const u32x2 d = widen4<KIND>(s.k[i][2]), e = widen4<KIND>(s.k[i][3]);
+    lds.k[slot][row * 16 + c0] = u32x4{a[0], a[1], b[0], b[1]};
+    lds.k[slot][row * 16 + 8 + c0] = u32x4{d[0], d[1], e[0], e[1]};
+  }
+  if (lane == 0) {
+    lds.ks[slot][wave] = s.ks;
+    lds.live[slot][wave] = s.live;
+  }
   const int ch = lane_channel(lane);
   if (s.live < 16) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (lane_token(lane) + r >= s.live) s.w[r] = u32x2{0u, 0u};
+      if (lane_token(lane) + r >= s.live) s.v[r] = u32x2{0u, 0u};
   }
   if (KIND == kFp8 && diagonal) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t hit = nan_codes(s.w[r][j]);
+        const uint32_t hit = nan_codes(s.v[r][j]);
         if (hit)
-          s.w[r][j] &= ~note_nans(hit, lds.nan_at + ch + 4 * j, tok + lane_token(lane) + r);
+          s.v[r][j] &= ~note_nans(hit, lds.nan_at + ch + 4 * j, tok + lane_token(lane) + r);
       }
   }
-  const float scale = s.live > 0 ? __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(
-                                                               __builtin_bit_cast(int, s.scale)))
-                               : 1.0f;
+  float scale =
+      __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, s.vs)));
+  if (s.live == 0) scale = 1.0f;
   // quad q of 16 tokens goes to place 0, 2, 1, 3
-  const int place = group * 4 + ((lane >> 5) << 1 | (lane & 1));
+  const int place = wave * 4 + ((lane >> 5) << 1 | (lane & 1));
   const auto put = [&](auto exact) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t w[4];
-      transpose4(s.w[0][j], s.w[1][j], s.w[2][j], s.w[3][j], w);
+      transpose4(s.v[0][j], s.v[1][j], s.v[2][j], s.v[3][j], w);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int channel = ch + 4 * j + c;
@@ -178,14 +148,15 @@ __device__ __forceinline__ void store_share(ValueShare& s, int lane, int32_t tok
       }
     }
   };
-  // the hardware's scale is a power of two
+  // the conversion's own scale is a power of two
   if (KIND == kFp8 && (__float_as_uint(scale) & 0x007fffffu) == 0 && scale > 0.0f)
     put(std::true_type());
   else
     put(std::false_type());
 }
 
-// Order of 16 products and their 16 operands from LDS: six operands ahead.
+// Order of 16 products and their 16 operands from LDS: six operands ahead. (The compiler waits for
+// each operand in front of its product.)
 __device__ __forceinline__ void reads_ahead() {
   constexpr int kRead = 0x100, kProduct = 0x8, kAhead = 6;
   __builtin_amdgcn_sched_group_barrier(kRead, kAhead, 0);
@@ -197,15 +168,13 @@ __device__ __forceinline__ void reads_ahead() {
   __builtin_amdgcn_sched_group_barrier(kProduct, kAhead, 0);
 }
 
-// One workgroup: (256 rows of a document, key/value head, part of its keys).
+// One workgroup: (128 rows of a document, key/value head, part of its keys).
 template <int KIND, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
   constexpr int ROWS = kDocRows;
-  extern __shared__ __align__(16) uint8_t smem[];
-  Smem& lds = *reinterpret_cast<Smem*>(smem);
+  __shared__ Smem lds;
   const int lane = threadIdx.x & 63, m = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool first = wave < 4;  // the half that begins
   const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
   Part part;
   if (!find_part<SPLIT, kThreads>(p, item, lds.find, part)) return;
@@ -254,71 +223,39 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(q[j]));
 
-  f32x16 o[4], s[2];
-  bf16x8 w[4];
+  f32x16 o[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[c][i] = 0.0f;
   float ref = kNoRef, tot = 0.0f;
 
-  __syncthreads();  // nan_at
-  int32_t zero = 0;
+  // the wave's tokens of a tile; what is stored next, and the page of what is loaded after it
+  const int32_t mine = begin + 16 * wave;
+  Share share;
+  int32_t page = 0, zero = 0;
   asm volatile("" : "+v"(zero));
-  // One half's walk, in code of its own, so that what it loads stays in the registers where it arrives.
-  // Keys of tile 0 are there before the first phase, keys of tile 1 and values of tile 0 come
-  // during the first two, keys and values of tile t + 2 behind the products of step t.
-  const auto walk = [&](auto half) {
-    constexpr bool kFirst = decltype(half)::value;
-    const int32_t mine = 16 * (kFirst ? wave >> 1 : wave - 4);  // the wave's tokens of a tile
-    KeyShare keys;
-    ValueShare values;
-    int32_t pages[2];
-    const auto load_ahead = [&](int32_t t) {
+  if (tiles > 0) {
+    page = load_page(p, part.b, mine, end, zero);
+    load_share(p, page, h, mine, end, lane, zero, share);
+    page = load_page(p, part.b, mine + kTile, end, zero);
+  }
+  __syncthreads();  // nan_at
+  if (tiles > 0) store_share<KIND>(share, wave, lane, mine, begin + kTile - 1 > all_see, 0, lds);
+  __syncthreads();
+  for (int32_t t = 0; t < tiles; ++t) {
+    const int32_t at = begin + t * kTile, tok_next = mine + (t + 1) * kTile;
+    const int slot = t & 1;
+    // (behind the last tile: bytes of page 0, which nothing reads)
+    load_share(p, page, h, tok_next, end, lane, zero, share);
+    page = load_page(p, part.b, tok_next + kTile, end, zero);
+    if (at <= wave_most) {
+      f32x16 s[2];
+      bf16x8 w[4];
 #pragma unroll
-      for (int i = 0; i < (kFirst ? 2 : 1); ++i)
-        pages[i] = load_page(p, part.b, begin + t * kTile + mine + 32 * i, end, zero);
-    };
-    // (behind the last tile: bytes of page 0, never stored)
-    const auto load = [&](int32_t t) {
-      const int32_t tok = begin + t * kTile + mine;
-      if constexpr (kFirst)
-        load_share(p, h, tok, end, wave, lane, zero, pages, keys);
-      else
-        load_share(p, h, tok, end, lane, zero, pages[0], values);
-      load_ahead(t + 1);
-    };
-    const auto store = [&](int32_t t) {
-      if (t >= tiles) return;
-      const int32_t at = begin + t * kTile;
-      if constexpr (kFirst)
-        store_share<KIND>(keys, wave, lane, t & 1, lds);
-      else
-        store_share<KIND>(values, lane, at + mine, at + kTile - 1 > all_see, t & 1, wave - 4, lds);
-    };
-    load_ahead(0);
-    load(0);
-    if (kFirst) {
-      store(0);
-      load(1);
-    }
-    __syncthreads();
-    if (!kFirst) {
-      store(0);
-      load(1);
-      __syncthreads();
-    }
-    for (int32_t t = -1; t < tiles; ++t) {
-    const int32_t at = begin + (t + 1) * kTile;
-    const bool scores = t + 1 < tiles && at <= wave_most;
-    const int slot = (t + 1) & 1;
-    __builtin_amdgcn_s_setprio(1);
-    if (scores) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
-      }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -327,21 +264,6 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
           s[u] = mfma(__builtin_bit_cast(bf16x8, k), q[j], s[u]);
         }
       reads_ahead();
-    }
-    if (t >= 0 && at - kTile <= wave_most) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const u32x4 v =
-              values_at[g ^ 2 * (c & 1)][(slot ^ 1) * (D * kTile / 8) + c * (32 * kTile / 8)];
-          o[c] = mfma(__builtin_bit_cast(bf16x8, v), w[g], o[c]);
-        }
-      reads_ahead();
-    }
-    __builtin_amdgcn_s_setprio(0);
-    __syncthreads();
-    if (scores) {
       float f[4];
       int32_t live = INT_MAX;
 #pragma unroll
@@ -400,18 +322,18 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
         }
         w[g] = __builtin_bit_cast(bf16x8, u32x4{pk[0], pk[1], pk[2], pk[3]});
       }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const u32x4 v = values_at[g ^ 2 * (c & 1)][slot * (D * kTile / 8) + c * (32 * kTile / 8)];
+          o[c] = mfma(__builtin_bit_cast(bf16x8, v), w[g], o[c]);
+        }
+      reads_ahead();
     }
-      store(t + 2);
-      load(t + 3);
-      __syncthreads();
-    }
-    if (kFirst) __syncthreads();
-  };
-  if (tiles > 0) {
-    if (first)
-      walk(std::true_type());
-    else
-      walk(std::false_type());
+    if (t + 1 < tiles)
+      store_share<KIND>(share, wave, lane, tok_next, at + 2 * kTile - 1 > all_see, slot ^ 1, lds);
+    __syncthreads();
   }
 
   if (SPLIT && h == 0 && part.rb == 0 && part.index == 0 && threadIdx.x == 0)
@@ -450,12 +372,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
 
 template <int KIND, bool SPLIT>
 hipError_t launch(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  constexpr int kSmem = sizeof(Smem);
-  static const hipError_t ready = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&document_kernel<KIND, SPLIT>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (ready != hipSuccess) return ready;
-  hipLaunchKernelGGL((document_kernel<KIND, SPLIT>), dim3(grid), dim3(kThreads), kSmem, stream, p);
+  hipLaunchKernelGGL((document_kernel<KIND, SPLIT>), dim3(grid), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
