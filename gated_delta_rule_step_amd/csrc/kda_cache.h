@@ -95,6 +95,7 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
 
 template <int KIND>
 __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+  asm("" : "+v"(w));  // (see widen4)
   if constexpr (KIND == kFp8) {
     const f32x2 a = f8x2_lo(w), b = f8x2_hi(w);
     x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];

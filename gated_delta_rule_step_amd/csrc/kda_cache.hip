@@ -99,89 +99,147 @@ __device__ __forceinline__ float need_scale(uint32_t amax) {
   return __uint_as_float(uint32_t(max(e, kMinExp) + 127) << 23);
 }
 
-// Four values, already divided by the scale, to codes.
+// Four values, already divided by the scale, to codes; whatever they are.
 template <int KIND>
 __device__ __forceinline__ float saturate(float x) {
   if constexpr (KIND == kFp8)
     return x != x ? x : f8_sat(x);  // a NaN stays one
   else
-    return x != x ? 0.0f : rintf(__builtin_amdgcn_fmed3f(x, -127.0f, 127.0f));
+    return x != x ? 0.0f : __builtin_amdgcn_fmed3f(x, -127.0f, 127.0f);
+}
+// Values within the codes' range. int8: the low byte of x + 1.5 2^23, whose last place is 1, is x
+// rounded to nearest even.
+template <int KIND>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+  if constexpr (KIND == kFp8) {
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true));
+  } else {
+    const auto code = [&](float x) { return __float_as_uint(fmaf(x, inv, 12582912.0f)); };
+    const uint32_t lo = __builtin_amdgcn_perm(code(b), code(a), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code(d), code(c), 0x04000c0cu);
+    return lo | hi;
+  }
 }
 template <int KIND>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-  a = saturate<KIND>(a), b = saturate<KIND>(b), c = saturate<KIND>(c), d = saturate<KIND>(d);
-  if constexpr (KIND == kFp8) {
-    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true));
-  } else {
-    return (uint32_t(int32_t(a)) & 255u) | (uint32_t(int32_t(b)) & 255u) << 8 |
-           (uint32_t(int32_t(c)) & 255u) << 16 | uint32_t(int32_t(d)) << 24;
-  }
+__device__ __forceinline__ uint32_t encode4_any(float a, float b, float c, float d, float inv) {
+  return encode4<KIND>(saturate<KIND>(a * inv), saturate<KIND>(b * inv), saturate<KIND>(c * inv),
+                       saturate<KIND>(d * inv), 1.0f);
 }
-// One (page, head, side) by WAVES waves, 4 WAVES PASSES >= the page's new tokens. A row is 16
-// lanes of 8 channels.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  const auto step = [&](auto ctrl, auto rows) {
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), decltype(ctrl)::value,
+                                                    decltype(rows)::value, 0xf, false)));
+  };
+  step(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());
+  step(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());
+  step(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());
+  step(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());
+  step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());
+  step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());
+  return uint32_t(__builtin_amdgcn_readlane(int(x), 63));
+}
+
+// A side's new rows of one (page, head): loaded, their largest magnitude, stored. By WAVES waves,
+// 4 WAVES PASSES >= the page's new tokens; a row is 16 lanes of 8 channels.
 template <int KIND, int WAVES, int PASSES>
+struct Rows {
+  u32x4 x[PASSES];
+  float old;
+  bool any;
+
+  __device__ __forceinline__ void load(const WriteParams& p, int side, const Item& it, int h, int t) {
+    old = it.a > 0 ? p.scale[side][int64_t(it.page) * p.c.H + h] : 0.0f;
+    const uint16_t* const src =
+        p.src[side] + it.row * p.src_stride[side] + h * D + (t & 15) * 8;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = (t >> 4) + i * 4 * WAVES;
+      x[i] = u32x4{0u, 0u, 0u, 0u};
+      if (r < it.z - it.a) x[i] = *reinterpret_cast<const u32x4_u*>(src + r * p.src_stride[side]);
+    }
+  }
+  // Magnitude bits of the wave's largest finite value; `any`: it has others, too.
+  __device__ __forceinline__ uint32_t top() {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x[i][j] & 0x7fff7fffu));
+    uint32_t all = wave_max(max(uint32_t(m[0]), uint32_t(m[1])));
+    any = all >= 0x7f80u;
+    if (any) {
+      all = 0;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) all = max(all, finite2(x[i][j]));
+      all = wave_max(all);
+    }
+    return all;
+  }
+  __device__ __forceinline__ void store(const WriteParams& p, int side, const Item& it, int h, int t,
+                                        uint32_t top) {
+    const float scale = fmaxf(need_scale<KIND>(top), old);
+    const float inv = 1.0f / scale;  // exact for powers of two
+    uint8_t* const page = p.dst[side] + it.page * (side ? p.c.v_page : p.c.k_page) +
+                          ((int64_t(h) << p.c.page_shift) * D);
+    if (old > 0.0f && old != scale) {  // earlier tokens of a page whose scale grew
+      const float ratio = old * inv;
+      for (int i = t; i < it.a * (D / 4); i += 64 * WAVES) {
+        uint32_t* const w = reinterpret_cast<uint32_t*>(page) + i;
+        float y[4];
+        decode4<KIND>(*w, y);
+        *w = encode4_any<KIND>(y[0], y[1], y[2], y[3], ratio);
+      }
+    }
+    if (t == 0) p.scale[side][int64_t(it.page) * p.c.H + h] = scale;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int r = (t >> 4) + i * 4 * WAVES;
+      if (r < it.z - it.a) {
+        float y[8];
+        unpack8_bf16(x[i], y);
+        *reinterpret_cast<u32x2*>(page + (it.a + r) * D + (t & 15) * 8) =
+            any ? u32x2{encode4_any<KIND>(y[0], y[1], y[2], y[3], inv),
+                        encode4_any<KIND>(y[4], y[5], y[6], y[7], inv)}
+                : u32x2{encode4<KIND>(y[0], y[1], y[2], y[3], inv),
+                        encode4<KIND>(y[4], y[5], y[6], y[7], inv)};
+      }
+    }
+  }
+};
+
+// A workgroup per (page, head, side).
+template <int KIND, int PASSES>
 __global__ __launch_bounds__(kThreads) void write_kernel(WriteParams p) {
   __shared__ uint32_t tops[4];
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, side = blockIdx.y & 1, h = blockIdx.y >> 1;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr int kPer = 4 / WAVES;  // (head, side) pairs of a workgroup
-  const int pair = blockIdx.y * kPer + (WAVES == 4 ? 0 : wave);
-  if (WAVES == 1 && pair >= 2 * p.c.H) return;
-  const int side = pair & 1, h = pair >> 1;
   const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
   if (it.page < 0) return;  // the same for all waves
-  const int t = WAVES == 4 ? threadIdx.x : lane;
-  const int r0 = t >> 4, ch = (t & 15) * 8;
-  const int rows = it.z - it.a;
-  float* const scale_at = p.scale[side] + int64_t(it.page) * p.c.H + h;
-  const float old = it.a > 0 ? *scale_at : 0.0f;
-  const uint16_t* const src = p.src[side] + it.row * p.src_stride[side] + h * D + ch;
-  u32x4 x[PASSES];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = r0 + i * 4 * WAVES;
-    x[i] = u32x4{0u, 0u, 0u, 0u};
-    if (r < rows) x[i] = *reinterpret_cast<const u32x4_u*>(src + r * p.src_stride[side]);
-  }
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, finite2(x[i][j]));
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) top = max(top, uint32_t(__shfl_xor(int(top), s)));
-  if (WAVES == 4) {
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-  }
-  const float scale = fmaxf(need_scale<KIND>(top), old);
-  const float inv = 1.0f / scale;  // exact for powers of two
-  const int64_t page_stride = side ? p.c.v_page : p.c.k_page;
-  uint8_t* const page =
-      p.dst[side] + it.page * page_stride + ((int64_t(h) << p.c.page_shift) * D);
-  if (old > 0.0f && old != scale) {  // earlier tokens of a page whose scale grew
-    const float ratio = old * inv;
-    for (int i = t; i < it.a * (D / 4); i += 64 * WAVES) {
-      uint32_t* const w = reinterpret_cast<uint32_t*>(page) + i;
-      float y[4];
-      decode4<KIND>(*w, y);
-      *w = encode4<KIND>(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
-    }
-  }
-  if (t == 0) *scale_at = scale;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = r0 + i * 4 * WAVES;
-    if (r < rows) {
-      float y[8];
-      unpack8_bf16(x[i], y);
-      *reinterpret_cast<u32x2*>(page + (it.a + r) * D + ch) =
-          u32x2{encode4<KIND>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                encode4<KIND>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)};
-    }
-  }
+  Rows<KIND, 4, PASSES> rows;
+  rows.load(p, side, it, h, threadIdx.x);
+  const uint32_t top = rows.top();
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  rows.store(p, side, it, h, threadIdx.x, max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+}
+// Few tokens: a wave per (page, head), both sides.
+template <int KIND, int PASSES>
+__global__ __launch_bounds__(kThreads) void write_few_kernel(WriteParams p) {
+  const int lane = threadIdx.x & 63;
+  const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (h >= p.c.H) return;
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
+  if (it.page < 0) return;
+  Rows<KIND, 1, PASSES> k, v;
+  k.load(p, 0, it, h, lane);
+  v.load(p, 1, it, h, lane);
+  k.store(p, 0, it, h, lane, k.top());
+  v.store(p, 1, it, h, lane, v.top());
 }
 
 // Rows (head, slot) of a page are one run of bytes; a workgroup takes kReadRows of them, a
@@ -198,27 +256,32 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadParams p) {
                                     : p.c.k + max(it.page, 0) * p.c.k_page);
   const float* const scales = (side ? p.c.v_scale : p.c.k_scale) + int64_t(max(it.page, 0)) * p.c.H;
   const int ch = (threadIdx.x & 7) * 16;
+  u32x4 w[kReadRows / 32];
+  float scale[kReadRows / 32];
 #pragma unroll
   for (int i = 0; i < kReadRows / 32; ++i) {
-    const int r = blockIdx.y * kReadRows + i * 32 + (threadIdx.x >> 3);
-    const int h = r >> p.c.page_shift, slot = r & (P - 1);
-    if (r >= most || slot < it.a || slot >= it.z) continue;
-    u32x4 w = {0u, 0u, 0u, 0u};
-    float scale = 0.0f;
-    if (it.page >= 0) {
-      w = *reinterpret_cast<const u32x4*>(page + int64_t(r) * D + ch);
-      scale = scales[h];
+    const int r = blockIdx.y * kReadRows + i * 32 + (threadIdx.x >> 3), slot = r & (P - 1);
+    w[i] = u32x4{0u, 0u, 0u, 0u};
+    scale[i] = 0.0f;
+    if (it.page >= 0 && r < most && slot >= it.a && slot < it.z) {
+      w[i] = *reinterpret_cast<const u32x4*>(page + int64_t(r) * D + ch);
+      scale[i] = scales[r >> p.c.page_shift];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < kReadRows / 32; ++i) {
+    const int r = blockIdx.y * kReadRows + i * 32 + (threadIdx.x >> 3), slot = r & (P - 1);
+    if (r >= most || slot < it.a || slot >= it.z) continue;
     u32x4 o[2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float x[4];
-      decode4<KIND>(w[j], x);
-      o[j >> 1][2 * (j & 1)] = pack_bf16x2(x[0] * scale, x[1] * scale);
-      o[j >> 1][2 * (j & 1) + 1] = pack_bf16x2(x[2] * scale, x[3] * scale);
+      decode4<KIND>(w[i][j], x);
+      o[j >> 1][2 * (j & 1)] = pack_bf16x2(x[0] * scale[i], x[1] * scale[i]);
+      o[j >> 1][2 * (j & 1) + 1] = pack_bf16x2(x[2] * scale[i], x[3] * scale[i]);
     }
-    u32x4_u* const dst = reinterpret_cast<u32x4_u*>(
-        p.dst[side] + (it.row + slot - it.a) * p.dst_stride[side] + h * D + ch);
+    u32x4_u* const dst = reinterpret_cast<u32x4_u*>(p.dst[side] + (it.row + slot - it.a) * p.dst_stride[side] +
+                                                    (r >> p.c.page_shift) * D + ch);
     dst[0] = o[0];
     dst[1] = o[1];
   }
@@ -232,21 +295,20 @@ int64_t count_items(const CacheView& c, int32_t* per_seq) {
   return n < (int64_t(1) << 31) ? n : 0;
 }
 
-template <int KIND, int WAVES, int PASSES>
-hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream) {
-  const unsigned pairs = 2u * unsigned(p.c.H), per = 4 / WAVES;
-  hipLaunchKernelGGL((write_kernel<KIND, WAVES, PASSES>), dim3(items, (pairs + per - 1) / per),
-                     dim3(kThreads), 0, stream, p);
-  return hipGetLastError();
-}
 template <int KIND>
 hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream) {
   const int P = 1 << p.c.page_shift;
   const int most = p.c.cu ? P : (p.c.per_seq < P ? p.c.per_seq : P);
-  if (most <= 4) return launch_write<KIND, 1, 1>(p, items, stream);
-  if (most <= 16) return launch_write<KIND, 1, 4>(p, items, stream);
-  if (most <= 64) return launch_write<KIND, 4, 4>(p, items, stream);
-  return launch_write<KIND, 4, 16>(p, items, stream);
+  const dim3 few(items, (p.c.H + 3) / 4), grid(items, 2 * p.c.H), block(kThreads);
+  if (most <= 4)
+    hipLaunchKernelGGL((write_few_kernel<KIND, 1>), few, block, 0, stream, p);
+  else if (most <= 16)
+    hipLaunchKernelGGL((write_few_kernel<KIND, 4>), few, block, 0, stream, p);
+  else if (most <= 64)
+    hipLaunchKernelGGL((write_kernel<KIND, 4>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((write_kernel<KIND, 16>), grid, block, 0, stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace

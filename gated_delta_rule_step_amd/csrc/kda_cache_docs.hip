@@ -155,10 +155,10 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
     put(std::false_type());
 }
 
-// Order of 16 products and their 16 operands from LDS: six operands ahead. (The compiler waits for
+// Order of 16 products and their 16 operands from LDS: four operands ahead. (The compiler waits for
 // each operand in front of its product.)
 __device__ __forceinline__ void reads_ahead() {
-  constexpr int kRead = 0x100, kProduct = 0x8, kAhead = 6;
+  constexpr int kRead = 0x100, kProduct = 0x8, kAhead = 4;
   __builtin_amdgcn_sched_group_barrier(kRead, kAhead, 0);
 #pragma unroll
   for (int i = 0; i < 16 - kAhead; ++i) {
