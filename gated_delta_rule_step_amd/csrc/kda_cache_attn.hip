@@ -295,7 +295,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
     }
     __syncthreads();
     const int r = row0 + 16 * n + row;
-    if (r >= rows) continue;
+    if (r >= rows || r - row0 >= p.block_rows) continue;
     const int t = r / p.G;
     const float top = fmaxf(fmaxf(refs[0][row], refs[1][row]), fmaxf(refs[2][row], refs[3][row]));
     const float r0 = top == -INFINITY ? 0.0f : top;

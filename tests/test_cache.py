@@ -659,3 +659,302 @@ def test_attention_document_nan(lib):
             pool.codes(pool.raw)[what][page, 0, slot, 5] = 0x7f
             out, _ = _check_attention(pool, [n], 3, False, weight=2.0 ** -8, seed=26)
             assert torch.equal(out.isnan().any(1).cpu(), torch.arange(total - n, total) >= at)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [256, 257, 1100, 2100])
+def test_attention_more_sequences_than_threads(lib, n):
+    """The parts are found by workgroups whose threads take several sequences each."""
+    g = torch.Generator().manual_seed(n)
+    totals = torch.randint(1, 20, (n,), generator=g).tolist()
+    totals[5], totals[n - 1] = 2500, 1030
+    pool = Pool(F8, 1, 16, totals, seed=27).fill()
+    _check_attention(pool, [1] * n, 1, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_document_parts(lib, kind):
+    """A few tokens more than a handful over a long cache: documents whose keys are cut, the last
+    parts seen by some rows only, beside single tokens and one that is not cut."""
+    counts = [140, 1, 3, 130]
+    totals = [5003, 2900, 3, 131]
+    pool = Pool(kind, 1, 64, totals, seed=28).fill()
+    _check_attention(pool, counts, 1, False, weight=2.0 ** -8, seed=29)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,G", [(9, 8), (16, 8), (40, 3), (17, 8)])
+def test_attention_rows_between_the_kernels(lib, T, G):
+    """Up to 128 rows and more."""
+    pool = Pool(I8, 1, 32, [T + 300, T, 1700], seed=30).fill()
+    _check_attention(pool, [T] * 3, G, True, seed=31, weight=2.0 ** (-16 if T * G <= 128 else -8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 160])
+def test_attention_arbitrary_scales(lib, T):
+    """Scales that are no powers of two, negative and zero ones. Documents round a value times
+    such a scale to bf16: half a step of every value more."""
+    pool = Pool(F8, 2, 32, [T + 211], seed=32).fill()
+    g = torch.Generator().manual_seed(33)
+    for side in range(2):
+        pool.scale[side] = torch.where(pool.scale[side].isnan(), pool.scale[side],
+                                       torch.randn(pool.scale[side].shape, generator=g) * 0.03)
+        pool.scale[side][pool.table[0, 1]] = 0.0
+    _check_attention(pool, [T], 1, True, weight=2.0 ** -16 if T == 1 else 2.0 ** -7, seed=34)
+
+
+@pytest.mark.gpu
+def test_attention_is_the_same_every_time_and_fits_its_workspace(lib):
+    pool = Pool(F8, 2, 64, [4000, 700, 3, 160], seed=35).fill()
+    counts = [1, 5, 3, 150]
+    T, cu = sum(counts), _cu(counts)
+    q = torch.randn(T, 4 * 128).to(BF).cuda()
+    cache, size = pool.gpu(), kda.kda_cache_attention_workspace_size(4, T, 4, 2)
+    got = []
+    for fill in (0, 0xff, 0x5a):
+        buf = torch.full((size + 4096,), fill, dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty_like(q), torch.empty(T, 4, device="cuda")
+        kda.kda_cache_attention(q, out, *cache, cu_seqlens_host=cu, cu_seqlens=cu.cuda(), lse=lse,
+                                workspace=buf[:size])
+        assert (buf[size:] == fill).all()
+        got.append((out, lse))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_cache_attention(q, out, *cache, cu_seqlens_host=cu, cu_seqlens=cu.cuda(),
+                                workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == WS
+
+
+@pytest.mark.gpu
+def test_pages_past_32_bits(lib):
+    """A pool of which most lies more than 2^32 bytes into its allocation."""
+    H, P, stride = 2, 16, 1 << 29
+    totals = [150, 40]
+    pool = Pool(F8, H, P, totals, seed=36).fill()
+    small, N = pool.gpu(), pool.N
+    big = []
+    for side in range(2):
+        buf = torch.empty((N - 1) * stride + H * P * 128, dtype=torch.uint8, device="cuda")
+        view = buf.as_strided(pool.shape, (stride,) + pool.strides[1:])
+        view.copy_(small[side].view(torch.uint8))
+        big.append(view.view(F8))
+    assert (N - 1) * stride > 1 << 32
+    rest = small[2:]
+    q = torch.randn(2, H * 128).to(BF).cuda()
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    kda.kda_cache_attention(q, a, *small)
+    kda.kda_cache_attention(q, b, *big, *rest)
+    assert torch.equal(a, b)
+    cu = _cu(totals).cuda()
+    k = [torch.empty(190, H * 128, dtype=BF, device="cuda") for _ in range(4)]
+    kda.kda_cache_read(k[0], k[1], *small, cu_seqlens=cu)
+    kda.kda_cache_read(k[2], k[3], *big, *rest, cu_seqlens=cu)
+    assert torch.equal(k[0], k[2]) and torch.equal(k[1], k[3])
+    qd = torch.randn(190, H * 128).to(BF).cuda()
+    out = [torch.empty_like(qd) for _ in range(2)]
+    for o, cache in zip(out, (small, (*big, *rest))):
+        kda.kda_cache_attention(qd, o, *cache, cu_seqlens_host=cu.cpu(), cu_seqlens=cu)
+    assert torch.equal(*out)
+    new = torch.randn(2, H * 128).to(BF).cuda()
+    kda.kda_cache_write(new, new, *small)
+    kda.kda_cache_write(new, new, *big, *rest)
+    for side in range(2):
+        assert torch.equal(small[side].view(torch.uint8), big[side].view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(lib):
+    """Calls that overlap in time, each with a workspace of its own, on streams that are not the
+    current one."""
+    pools = [Pool(F8, 2, 32, [3000 + 64 * i, 200], seed=37 + i).fill() for i in range(2)]
+    caches = [p.gpu() for p in pools]
+    q = torch.randn(2, 4 * 128).to(BF).cuda()
+    want = [torch.empty_like(q) for _ in range(2)]
+    for o, c in zip(want, caches):
+        kda.kda_cache_attention(q, o, *c)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.zeros_like(q) for _ in range(20)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, o, c in zip(streams, got, caches):
+            kda.kda_cache_attention(q, o[i], *c, stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(w, x) for x in o)
+
+
+@pytest.mark.gpu
+def test_captured_steps_share_a_workspace(lib):
+    """Decode steps (write, attend) of two batches in two graphs that share one workspace: replayed
+    in turn with lengths that grow on the device, against eager calls on a copy."""
+    dev, g = "cuda", torch.Generator().manual_seed(39)
+    H, G, P = 2, 4, 16
+
+    def batch(totals, T):
+        pool = Pool(F8, H, P, [x + 64 for x in totals], seed=sum(totals)).fill()
+        for side in range(2):
+            pool.scale[side].nan_to_num_(1.0)
+        pool.lens = torch.tensor(totals)
+        n = len(totals) * T
+        return dict(cache=pool.gpu(), T=T, k=torch.zeros(n, H * 128, dtype=BF, device=dev),
+                    v=torch.zeros(n, H * 128, dtype=BF, device=dev),
+                    q=torch.zeros(n, H * G * 128, dtype=BF, device=dev),
+                    out=torch.zeros(n, H * G * 128, dtype=BF, device=dev),
+                    lse=torch.zeros(n, H * G, device=dev))
+
+    def step(b, ws):
+        b["cache"][5].add_(b["T"])
+        kda.kda_cache_write(b["k"], b["v"], *b["cache"])
+        kda.kda_cache_attention(b["q"], b["out"], *b["cache"], lse=b["lse"], workspace=ws)
+
+    batches = [batch([2100, 37, 1500], 1), batch([1300, 40], 4)]
+    copies = [{k: v.clone() if torch.is_tensor(v) else
+               [x.clone() for x in v] if k == "cache" else v for k, v in b.items()} for b in batches]
+    size = max(kda.kda_cache_attention_workspace_size(len(b["cache"][5]), b["q"].shape[0], H * G, H)
+               for b in batches)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    graphs = []
+    for b in batches:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(b, ws)
+        graphs.append(graph)
+    for i in range(6):
+        for b, c, graph in zip(batches, copies, graphs):
+            for name in ("k", "v", "q"):
+                x = torch.randn(b[name].shape, generator=g).to(BF)
+                b[name].copy_(x)
+                c[name].copy_(x)
+            graph.replay()
+            step(c, None)
+            if i % 2:
+                torch.cuda.synchronize()
+        for b, c in zip(batches, copies):
+            assert torch.equal(b["out"], c["out"]) and torch.equal(b["lse"], c["lse"])
+            for x, y in zip(b["cache"], c["cache"]):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_layer_served(lib, kind):
+    """An attention layer as a server runs it next to the recurrent ones: two documents in chunks, then
+    verification of three draft tokens, then single tokens; norm in front, residual norm behind. The
+    quantised cache is taken as it is written; the rest is compared in 64 bits."""
+    g = torch.Generator().manual_seed(41)
+    H, G, P, W = 2, 3, 32, 256
+    pool = Pool(kind, H, P, [200, 150], seed=42)
+    cache = list(pool.gpu())
+    for side in range(2):
+        cache[2 + side].nan_to_num_(1.0)
+    proj = (torch.randn(W, (G + 2) * H * 128, generator=g) * W ** -0.5).to(BF).cuda()
+    back = (torch.randn(G * H * 128, W, generator=g) * (G * H * 128) ** -0.5).to(BF).cuda()
+    weight = torch.ones(W).cuda()
+    done = [0, 0]
+    for counts in ([90, 61], [75, 0], [3, 3], [1, 1], [1, 1]):
+        T = sum(counts)
+        x = torch.randn(T, W, generator=g).to(BF).cuda()
+        y = torch.empty_like(x)
+        kda.kda_rmsnorm(x, weight, y)
+        qkv = y @ proj
+        q, k, v = qkv.split([G * H * 128, H * 128, H * 128], 1)  # rows further apart than wide
+        done = [a + b for a, b in zip(done, counts)]
+        cache[5] = torch.tensor(done, dtype=I32).cuda()
+        ragged = counts[0] != counts[1]
+        cu = _cu(counts)
+        kda.kda_cache_write(k, v, *cache, cu_seqlens=cu.cuda() if ragged else None)
+        out, lse = torch.empty(T, G * H * 128, dtype=BF, device="cuda"), \
+            torch.empty(T, G * H, device="cuda")
+        kda.kda_cache_attention(q, out, *cache, cu_seqlens_host=cu if ragged else None,
+                                cu_seqlens=cu.cuda() if ragged else None, lse=lse)
+        z = out @ back
+        r, s = torch.empty_like(x), torch.empty_like(x)
+        kda.kda_rmsnorm(z, weight, s, residual=x, residual_out=r)
+        # what the layer has now, in 64 bits
+        pool.lens = torch.tensor(done)
+        pool.raw = [t.cpu() for t in pool.dev]
+        pool.scale = [t.cpu() for t in cache[2:4]]
+        want, wl, tol, lt = _ref_attention(pool, q.double().cpu().reshape(T, G * H, 128), counts, G,
+                                           128 ** -0.5, 2.0 ** -8)
+        _close(out.reshape(T, G * H, 128), want, tol)
+        _close(lse, wl, lt)
+        assert torch.equal(r, (z.float() + x.float()).to(BF))
+        # and the cache holds this call's tokens within half a step
+        got = [torch.empty(T, H * 128, dtype=BF, device="cuda") for _ in range(2)]
+        kda.kda_cache_read(*got, *cache, cu_seqlens=cu.cuda())
+        for a, b in zip((k, v), got):
+            a, b = a.double(), b.double()
+            top = a.abs().max()
+            step = 2.0 ** -4 * a.abs() + 2.0 ** -10 * top / 224 if kind == F8 else top / 63
+            assert ((a - b).abs() <= step).all()
+
+
+def test_workspace_comes_from_the_stream(lib, monkeypatch):
+    """Without one given, the workspace is made in the launch stream's pool (stand-ins for the
+    library and the GPU)."""
+    import contextlib
+    seen, at = [], [0x100]
+
+    class Gpu:
+        is_cuda, device = True, torch.device("cuda", 0)
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 0
+
+    class Lib:
+        def kda_cache_attention_workspace_size(self, *a):
+            return 512
+
+        def kda_cache_attention(self, *a):
+            seen.append(("call", a[-3], a[-2], a[-1]))
+            return 0
+
+    class Stream:
+        cuda_stream, device = 0x200, torch.device("cuda", 0)
+
+    @contextlib.contextmanager
+    def use(stream):
+        at.append(stream.cuda_stream)
+        yield
+        at.pop()
+
+    empty = torch.empty
+    keep = []
+
+    def alloc(n, dtype, device):
+        keep.append(Gpu(empty(n, dtype=dtype)))
+        seen.append(("made", keep[-1].data_ptr(), n, at[-1]))
+        return keep[-1]
+
+    monkeypatch.setattr(kda, "lib", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: Stream())
+    monkeypatch.setattr(torch, "empty", alloc)
+    c = Gpu(torch.zeros(3, 2, 16, 128, dtype=I8))
+    s, tab, lens = Gpu(torch.ones(3, 2)), Gpu(torch.zeros(1, 3, dtype=I32)), \
+        Gpu(torch.ones(1, dtype=I32))
+    q, o = Gpu(torch.zeros(1, 512, dtype=BF)), Gpu(torch.zeros(1, 512, dtype=BF))
+    kda.kda_cache_attention(q, o, c, c, s, s, tab, lens, stream=Stream())
+    (_, adr, n, stream), (_, ws, size, raw) = seen
+    assert stream == 0x200 and raw == 0x200 and ws == adr and size == n == 512
+    with pytest.raises(ValueError):  # the host's copy alone
+        kda.kda_cache_attention(q, o, c, c, s, s, tab, lens,
+                                cu_seqlens_host=torch.zeros(2, dtype=I32))
+    with pytest.raises(ValueError):  # heads that do not divide
+        kda.kda_cache_attention(Gpu(torch.zeros(1, 384, dtype=BF)),
+                                Gpu(torch.zeros(1, 384, dtype=BF)), c, c, s, s, tab, lens)
+    with pytest.raises(ValueError):  # scales of another shape
+        kda.kda_cache_attention(q, o, c, c, Gpu(torch.ones(3, 1)), s, tab, lens)
+    with pytest.raises(TypeError):
+        kda.kda_cache_attention(q, o, Gpu(c.t.float()), c, s, s, tab, lens)
