@@ -21,7 +21,7 @@ struct CacheView {
   const int32_t* cu;    // NULL: per_seq tokens of every sequence
   int32_t per_seq;
   int32_t page_shift;   // page size: 1 << page_shift tokens
-  int64_t num_pages;
+  int32_t num_pages;
   const uint8_t* k;
   const uint8_t* v;
   int64_t k_page, v_page;  // page strides
@@ -59,13 +59,17 @@ __device__ __forceinline__ Seq sequence(const CacheView& p, int32_t b) {
 // The page that holds position `at` >> page_shift == i of sequence b; -1: none.
 __device__ __forceinline__ int32_t page_of(const CacheView& p, int32_t b, int32_t i) {
   const int32_t id = p.table[b * p.table_stride + i];
-  return uint32_t(id) < uint64_t(p.num_pages) ? id : -1;
+  return uint32_t(id) < uint32_t(p.num_pages) ? id : -1;
 }
 
+// Loaded words stay whole up to here. (The compiler else may keep a register for each byte of them.)
+template <typename T>
+__device__ __forceinline__ void whole(T& words) {
+  asm("" : "+v"(words));
+}
 // Four codes as two bf16 pairs, exact: e4m3 has 4 significant bits, int8 7.
 template <int KIND>
 __device__ __forceinline__ u32x2 widen4(uint32_t w) {
-  asm("" : "+v"(w));  // one register up to here, not one for each byte
   if constexpr (KIND == kFp8) {
     return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
@@ -95,7 +99,6 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
 
 template <int KIND>
 __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
-  asm("" : "+v"(w));  // (see widen4)
   if constexpr (KIND == kFp8) {
     const f32x2 a = f8x2_lo(w), b = f8x2_hi(w);
     x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];

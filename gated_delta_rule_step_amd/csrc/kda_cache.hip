@@ -276,6 +276,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadParams p) {
     const int r = r0 + i * 16, slot = r & (P - 1);
     if (r >= most || slot < it.a || slot >= it.z) continue;
     float x[4], y[4];
+    whole(w[i]);
     decode4<KIND>(w[i][0], x);
     decode4<KIND>(w[i][1], y);
     const float f = scale[i];
@@ -347,7 +348,7 @@ kda_status check(const CacheArgs& a, CacheView* c) {
   c->cu = a.cu_seqlens;
   c->per_seq = a.cu_seqlens ? 0 : int32_t(a.total_tokens / a.n_seqs);
   c->page_shift = shift;
-  c->num_pages = a.num_pages;
+  c->num_pages = int32_t(a.num_pages);
   c->k = static_cast<const uint8_t*>(a.k_cache);
   c->v = static_cast<const uint8_t*>(a.v_cache);
   c->k_page = a.k_page_stride;

@@ -25,8 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kStep = 32;            // tokens of a wave's step
 constexpr int kStride = 4 * kStep;   // and of the workgroup's
 constexpr int kRow = D + 4;          // fp32 row in LDS
-// The reference exponent of a row moves only when a score passes it by this much (base 2):
-// weights stay below 2^8, far inside bf16 and fp32.
+// Weights stay below 2^8 (see `slack`), far inside bf16 and fp32.
 constexpr float kSlack = 8.0f;
 
 // A wave's 32 tokens are two tiles of 16, each inside one page.
@@ -51,7 +50,7 @@ __device__ __forceinline__ void load_ids(const AttnParams& p, int32_t b, int32_t
 }
 __device__ __forceinline__ int32_t known_page(const AttnParams& p, const Ids& s, int u, int32_t at,
                                               int32_t end) {
-  return at + 16 * u < end && uint32_t(s.raw[u]) < uint64_t(p.c.num_pages) ? s.raw[u] : -1;
+  return at + 16 * u < end && uint32_t(s.raw[u]) < uint32_t(p.c.num_pages) ? s.raw[u] : -1;
 }
 // Page 0's bytes in the place of none's.
 __device__ __forceinline__ int64_t tile_at(const CacheView& c, int32_t id, int64_t page, int32_t h,
@@ -169,10 +168,12 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
   __syncthreads();
 
   f32x4 o[NT][8];
-  float ref[NT], tot[NT];
+  // A row's reference exponent moves when a score passes it by more than `slack`: by anything at first.
+  float ref[NT], slack[NT], tot[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    ref[n] = -INFINITY;
+    ref[n] = 0.0f;
+    slack[n] = -INFINITY;
     tot[n] = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) o[n][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -191,6 +192,11 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
 #pragma unroll
       for (int u = 0; u < 2; ++u) acc[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      whole(k.w[u][0]);
+      whole(k.w[u][1]);
+    }
+#pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -201,6 +207,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
       }
     const float f[2] = {p.scale2 * k.scale[0], p.scale2 * k.scale[1]};
     if (more) load_keys(p, h, at + kStride, to, ids_next, m, g, k);
+    // (whatever the scale of a page that does not exist is)
+    const float vs[2] = {live[0] > 0 ? v.scale[0] : 0.0f, live[1] > 0 ? v.scale[1] : 0.0f};
     bf16x8 ph[NT], pl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -208,32 +216,42 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          s[u][r] = acc[n][u][r] * f[u];
-          if (masked && (4 * g + r >= live[u] || at + 16 * u + 4 * g + r > last[n]))
-            s[u][r] = -INFINITY;
-        }
+        for (int r = 0; r < 4; ++r) s[u][r] = fmaf(acc[n][u][r], f[u], -ref[n]);
+      if (masked) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int in = 4 * g + r;
+            if (in >= live[u] || at + 16 * u + in > last[n]) s[u][r] = -INFINITY;
+          }
+      }
       const float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                               fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      if (__any(top > ref[n] + kSlack)) {
-        const float to_ref = fmaxf(ref[n], over_groups_max(top));
-        const float down = to_ref == ref[n] ? 1.0f : __builtin_amdgcn_exp2f(ref[n] - to_ref);
-        ref[n] = to_ref;
-        tot[n] *= down;
+      if (__any(top > slack[n])) {
+        const float over = over_groups_max(top);
+        if (over > slack[n]) {
+          const float down = slack[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(-over);
+          ref[n] += over;
+          slack[n] = kSlack;
+          tot[n] *= down;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) o[n][c] *= down;
+          for (int c = 0; c < 8; ++c) o[n][c] *= down;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[u][r] -= over;
+        }
       }
-      const float r0 = ref[n] == -INFINITY ? 0.0f : ref[n];
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float w[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          w[r] = __builtin_amdgcn_exp2f(s[u][r] - r0);
+          w[r] = __builtin_amdgcn_exp2f(s[u][r]);
           tot[n] += w[r];
-          w[r] *= v.scale[u];
-          if (masked && 4 * g + r >= live[u]) w[r] = 0.0f;  // whatever that scale was
+          w[r] *= vs[u];
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -245,6 +263,10 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
       ph[n] = __builtin_bit_cast(bf16x8, u32x4{hi[0], hi[1], hi[2], hi[3]});
       pl[n] = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], lo[2], lo[3]});
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) whole(v.w[u][r]);
     if (masked) clear_values<KIND>(v, live, at, all_see, m, g, nan_at);
 #pragma unroll
     for (int c4 = 0; c4 < 2; ++c4) {  // channels 8 m + 4 c4 ..
@@ -284,7 +306,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
     const float total = over_groups_sum(tot[n]);
     if (n > 0) __syncthreads();
     if (g == 0) {
-      refs[wave][m] = ref[n];
+      refs[wave][m] = slack[n] == -INFINITY ? -INFINITY : ref[n];
       tots[wave][m] = total;
     }
 #pragma unroll

@@ -105,6 +105,7 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int row = 16 * wave + (lane >> 3) + 8 * i;
+    whole(s.k[i]);
     const u32x2 a = widen4<KIND>(s.k[i][0]), b = widen4<KIND>(s.k[i][1]);
     const u32x2 d = widen4<KIND>(s.k[i][2]), e = widen4<KIND>(s.k[i][3]);
     lds.k[slot][row * 16 + c0] = u32x4{a[0], a[1], b[0], b[1]};
@@ -115,6 +116,8 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
     lds.live[slot][wave] = s.live;
   }
   const int ch = lane_channel(lane);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) whole(s.v[r]);
   if (s.live < 16) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
