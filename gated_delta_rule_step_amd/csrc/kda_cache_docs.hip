@@ -30,7 +30,7 @@ constexpr float kNoRef = -3.0e38f;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct Smem {
-  // chunk c < 8 of a key's row: channels 16 c .., c >= 8: channels 16 (c - 8) + 8 ..; at c ^ (key & 7)
+  // chunk c < 8 of a key's row: channels 16 c .., c >= 8: channels 16 (c - 8) + 8 ..; at c ^ (key & 15)
   u32x4 k[2][kTile * 16];
   // a channel's row: tokens of each run of 16 in the order 0-3, 8-11, 4-7, 12-15, chunks of 8 at
   // c ^ swizzle(channel)
@@ -108,8 +108,8 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
     whole(s.k[i]);
     const u32x2 a = widen4<KIND>(s.k[i][0]), b = widen4<KIND>(s.k[i][1]);
     const u32x2 d = widen4<KIND>(s.k[i][2]), e = widen4<KIND>(s.k[i][3]);
-    lds.k[slot][row * 16 + c0] = u32x4{a[0], a[1], b[0], b[1]};
-    lds.k[slot][row * 16 + 8 + c0] = u32x4{d[0], d[1], e[0], e[1]};
+    lds.k[slot][row * 16 + (c0 ^ 8 * i)] = u32x4{a[0], a[1], b[0], b[1]};
+    lds.k[slot][row * 16 + (c0 ^ 8 * (1 - i))] = u32x4{d[0], d[1], e[0], e[1]};
   }
   if (lane == 0) {
     lds.ks[slot][wave] = s.ks;
@@ -214,12 +214,13 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
     }
   }
 
-  // a lane's operands: row m of 32 keys, chunks 2 (j & 3) + hi; channel m of 32, chunks 2 g + hi
-  const u32x4* keys_at[4];
+  // a lane's operands: row m of 32 keys, chunks 2 j + hi; channel m of 32, chunks 2 g + hi
+  const u32x4* keys_at[8];
   const u32x4* values_at[4];
 #pragma unroll
+  for (int i = 0; i < 8; ++i) keys_at[i] = &lds.k[0][m * 16 + ((2 * i + hi) ^ (m & 15))];
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    keys_at[i] = &lds.k[0][m * 16 + ((2 * i + hi) ^ (m & 7))];
     values_at[i] = reinterpret_cast<const u32x4*>(lds.v[0]) + m * 8 + ((2 * i + hi) ^ swizzle(m));
   }
   // the queries are there before the loop, whose waits are for what it loads itself
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const u32x4 k = keys_at[j & 3][slot * (kTile * 16) + u * (32 * 16) + (j & 4) * 2];
+          const u32x4 k = keys_at[j][slot * (kTile * 16) + u * (32 * 16)];
           s[u] = mfma(__builtin_bit_cast(bf16x8, k), q[j], s[u]);
         }
       reads_ahead();
