@@ -11,6 +11,9 @@ namespace cache {
 
 constexpr int kFp8 = KDA_CACHE_FP8;
 constexpr int kInt8 = KDA_CACHE_INT8;
+constexpr int32_t kMaxHeads = 1 << 13;
+// Workgroups along x: a launch has less than 2^32 threads there, at 256 a workgroup.
+constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
 
 typedef u32x4 u32x4_u __attribute__((aligned(2)));  // bf16 rows need no alignment of their own
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -139,7 +142,7 @@ __device__ __forceinline__ int32_t wave_prefix(int32_t x) {
   return x;
 }
 
-// Host: the checks that the calls share, and the view. `empty`: nothing to do.
+// Host: the checks that the calls share, and the view (left alone where there are no tokens).
 struct CacheArgs {
   int32_t n_seqs;
   int64_t total_tokens;

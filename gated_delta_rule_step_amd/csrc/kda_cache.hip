@@ -186,7 +186,7 @@ struct Rows {
     const float inv = 1.0f / scale;  // exact for powers of two
     uint8_t* const page = p.dst[side] + it.page * (side ? p.c.v_page : p.c.k_page) +
                           ((int64_t(h) << p.c.page_shift) * D);
-    if (old > 0.0f && old != scale) {  // earlier tokens of a page whose scale grew
+    if (old != scale) {  // earlier tokens of a page whose scale grew
       const float ratio = old * inv;
       for (int i = t; i < it.a * (D / 4); i += 64 * WAVES) {
         uint32_t* const w = reinterpret_cast<uint32_t*>(page) + i;
@@ -293,7 +293,7 @@ int64_t count_items(const CacheView& c, int32_t* per_seq) {
   const int64_t P = int64_t(1) << c.page_shift;
   *per_seq = int32_t((c.per_seq + P - 2) / P + 1);
   const int64_t n = c.cu ? c.total / P + 2 * int64_t(c.n_seqs) : int64_t(c.n_seqs) * *per_seq;
-  return n < (int64_t(1) << 31) ? n : 0;
+  return n <= kMaxGrid ? n : 0;
 }
 
 template <int KIND>
@@ -322,9 +322,9 @@ kda_status check(const CacheArgs& a, CacheView* c) {
   int32_t shift = 4;
   while (shift < 8 && (1 << shift) < a.page_size) ++shift;
   if ((1 << shift) != a.page_size) return KDA_ERR_UNSUPPORTED;
-  if (a.total_tokens > (int64_t(1) << 30) || a.H > (1 << 14) || a.num_pages > INT32_MAX ||
+  if (a.total_tokens > (int64_t(1) << 30) || a.H > kMaxHeads || a.num_pages > INT32_MAX ||
       int64_t(a.table_width) * a.page_size > (int64_t(1) << 28) ||
-      int64_t(a.n_seqs) * a.table_width > (int64_t(1) << 37) / a.page_size)
+      int64_t(a.n_seqs) * a.table_width > (int64_t(1) << 35) / a.page_size)
     return KDA_ERR_UNSUPPORTED;
   if (a.total_tokens > 0 && a.n_seqs == 0) return KDA_ERR_BAD_SHAPE;
   if (!a.cu_seqlens && a.n_seqs > 0 && a.total_tokens % a.n_seqs != 0) return KDA_ERR_BAD_SHAPE;

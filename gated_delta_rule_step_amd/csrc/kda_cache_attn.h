@@ -27,7 +27,7 @@ struct AttnParams {
   int32_t block_rows;   // rows of a block (of a part's results, too)
   int32_t targets;      // parts that all the blocks' keys are cut into, 0: none is cut
   int32_t min_units;    // units of a part at least
-  int2* plan;           // [n_seqs]: first slot, parts
+  int4* cuts;           // [0].x: blocks whose keys are cut; then their sequence, block, slot, parts
   float2* stat;         // [slot][H][block_rows]: reference exponent, sum
   float* part;          // [slot][H][block_rows][128]: sums of p v
 };
@@ -53,17 +53,24 @@ __device__ __forceinline__ int32_t blocks_of(const AttnParams& p, int32_t b) {
 // Part `index` of `parts` of the keys of block `rb` of sequence b: tokens from .. to - 1; its
 // results go to slot `slot` where there is more than one.
 struct Part {
-  int32_t b, rb, index, parts, slot, first_slot, from, to;
+  int32_t b, rb, index, parts, slot, from, to;
+  int32_t cut;  // the block among those that are cut, -1: whole
 };
 struct FindSmem {
-  int32_t work[4], items[4], slots[4];  // a wave's sums
+  int32_t work[4], items[4];  // a wave's sums
+  uint32_t cuts[4];
+  int32_t all_cuts;  // blocks that are cut
   Part part;
 };
 // Work item `item`: the sequences one after the other, a sequence's parts in turn, the blocks that
-// share a part's keys next to each other, the last one (with the most keys to see) first. Every workgroup of T threads finds it for itself from the lengths on the
-// device, K sequences a thread; SPLIT: the keys may be cut. Each sequence's keys are cut into equal
-// parts of a length that is the same for all, however ragged the batch, except for what rounding
-// to units leaves. (By single waves, 64 sequences at a time, 512 sequences took 10 us to walk.)
+// share a part's keys next to each other, the last one (with the most keys to see) first. Every
+// workgroup of T threads finds it for itself from the lengths on the device, K sequences a thread;
+// SPLIT: the keys may be cut. Each sequence's keys are cut into equal parts of a length that is the
+// same for all, however ragged the batch, except for what rounding to units leaves. What is cut has
+// less than twice its share of the parts: 2 * targets slots. The blocks that are cut are listed for
+// the join, which has workgroups for as many as there may be (with workgroups for every row that a
+// sequence may have, 1024 decoded tokens beside a document of 7680 rows took 1740 us, now 377).
+// (By single waves, 64 sequences at a time, 512 sequences took 10 us to walk.)
 template <bool SPLIT, int T>
 __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, FindSmem& lds,
                                           Part& out) {
@@ -98,11 +105,16 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
     chunk = max(p.min_units, (sum + p.targets - 1) / p.targets);
   }
   const auto parts_of = [&](int32_t u) { return SPLIT ? max((u + chunk - 1) / chunk, 1) : 1; };
-  int32_t items = 0, slots = 0;
+  // blocks that are cut << 16 | their slots (both far below 2^16)
+  const auto cut = [](int32_t n, int32_t parts) {
+    return parts > 1 ? uint32_t(n) << 16 | uint32_t(n * parts) : 0u;
+  };
+  int32_t items = 0;
+  uint32_t cuts = 0;
   const auto count = [&](int32_t n, int32_t u) {
     const int32_t parts = parts_of(u);
     items += n * parts;
-    slots += parts > 1 ? n * parts : 0;
+    cuts += cut(n, parts);
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) count(blocks[k], units[k]);
@@ -111,20 +123,22 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
     sizes(k, n, u);
     count(n, u);
   }
-  int32_t first = wave_prefix(items), slot = SPLIT ? wave_prefix(slots) : 0;
+  int32_t first = wave_prefix(items);
+  uint32_t before = SPLIT ? uint32_t(wave_prefix(int32_t(cuts))) : 0;
   if (lane == 63) {
     lds.items[wave] = first;
-    lds.slots[wave] = slot;
+    lds.cuts[wave] = before;
   }
   first -= items;
-  slot -= slots;
+  before -= cuts;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < T / 64 - 1; ++w)
     if (w < wave) {
       first += lds.items[w];
-      slot += lds.slots[w];
+      before += lds.cuts[w];
     }
+  if (SPLIT && threadIdx.x == T - 1) lds.all_cuts = int32_t((before + cuts) >> 16);
   if (item >= first && item < first + items) {
     for (int k = 0; k < K; ++k) {
       int32_t n, u;
@@ -136,17 +150,17 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
         x.parts = parts;
         x.index = SPLIT ? (item - first) / n : 0;
         x.rb = n - 1 - (item - first - x.index * n);
-        x.first_slot = slot;
-        x.slot = slot + x.rb * parts + x.index;
+        x.slot = int32_t(before & 0xffffu) + x.rb * parts + x.index;
         x.from = parts == 1 ? 0 : x.index * chunk * kUnit;
         x.to = x.index + 1 == parts ? INT_MAX : x.from + chunk * kUnit;
-        // (more slots than there are: cu_seqlens is not what the host's copy says)
-        if (parts > 1 && (slot < 0 || x.slot >= 2 * p.targets)) x.b = -1;
+        x.cut = parts > 1 ? int32_t(before >> 16) + x.rb : -1;
+        // (more than there are: cu_seqlens is not what the host's copy says)
+        if (x.cut >= p.targets || (parts > 1 && x.slot >= 2 * p.targets)) x.b = -1;
         lds.part = x;
         break;
       }
       first += n * parts;
-      slot += parts > 1 ? n * parts : 0;
+      before += cut(n, parts);
     }
   }
   __syncthreads();
@@ -156,10 +170,18 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
   out.index = __builtin_amdgcn_readfirstlane(lds.part.index);
   out.parts = __builtin_amdgcn_readfirstlane(lds.part.parts);
   out.slot = __builtin_amdgcn_readfirstlane(lds.part.slot);
-  out.first_slot = __builtin_amdgcn_readfirstlane(lds.part.first_slot);
   out.from = __builtin_amdgcn_readfirstlane(lds.part.from);
   out.to = __builtin_amdgcn_readfirstlane(lds.part.to);
   return true;
+}
+
+// For the join, by the kernel's end (a store in front of its loop has the loop wait for it).
+__device__ __forceinline__ void list_cuts(const AttnParams& p, int32_t h, const FindSmem& lds) {
+  if (h != 0 || threadIdx.x != 0) return;
+  if (blockIdx.x == 0) p.cuts[0].x = min(lds.all_cuts, p.targets);
+  const Part& x = lds.part;
+  if (x.b >= 0 && x.cut >= 0 && x.index == 0)
+    p.cuts[1 + x.cut] = make_int4(x.b, x.rb, x.slot, x.parts);
 }
 
 // Documents: workgroups of kDocRows rows.

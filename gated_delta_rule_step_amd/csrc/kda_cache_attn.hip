@@ -299,6 +299,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
     load_ids(p, part.b, at + 2 * kStride, to, ids_next);
   }
 
+  list_cuts(p, h, find);
   // the four waves' sums, 16 rows at a time; thread (row, 8 channels)
   const int row = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
 #pragma unroll
@@ -351,32 +352,32 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
       if (ch == 0) p.stat[slot] = make_float2(top, sum);
     }
   }
-  if (h == 0 && part.rb == 0 && part.index == 0 && threadIdx.x == 0)
-    p.plan[part.b] = make_int2(part.first_slot, part.parts);
 }
 
-// Joins the parts of a row: 16 lanes of 8 channels, four parts at a time. WIDE: a workgroup's 16
-// groups share one row's parts (few rows, many parts), else each has a row of its own.
+// Joins the parts of the blocks that are cut, a row by 16 lanes of 8 channels, four parts at a time.
+// WIDE: a workgroup's 16 groups share one row's parts (few rows, many parts), else each has a row
+// of its own.
 template <bool WIDE>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p, int32_t most_rows) {
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
   __shared__ float accs[WIDE ? 16 : 1][D];
   __shared__ float2 stats[WIDE ? 16 : 1];
   const int group = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
-  const int pairs = most_rows * p.c.H, per = WIDE ? pairs : (pairs + 15) / 16;
-  const int b = blockIdx.x / per;
-  if (blocks_of(p, b) == 0) return;
-  const int2 plan = p.plan[b];
-  const int rows = rows_of(p, b);
-  const int i = WIDE ? blockIdx.x - b * per : (blockIdx.x - b * per) * 16 + group;
-  const int h = i / most_rows, r = i - h * most_rows, rb = r / p.block_rows;
-  // (more slots than there are: see find_part)
-  const bool mine = plan.y > 1 && i < pairs && r < rows && plan.x >= 0 &&
-                    plan.x + (int64_t(rb) + 1) * plan.y <= 2 * p.targets;
+  const int pairs = p.block_rows * p.c.H, per = WIDE ? pairs : (pairs + 15) / 16;
+  const int n = blockIdx.x / per;
+  const int4 cut = p.cuts[1 + n];
+  if (n >= p.cuts[0].x) return;
+  const int b = cut.x;
+  // (an entry that this call did not write: cu_seqlens is not what the host's copy says)
+  if (uint32_t(b) >= uint32_t(p.c.n_seqs) || uint32_t(cut.y) >= uint32_t(blocks_of(p, b)) ||
+      cut.z < 0 || cut.w < 2 || int64_t(cut.z) + cut.w > 2 * p.targets)
+    return;
+  const int i = WIDE ? blockIdx.x - n * per : (blockIdx.x - n * per) * 16 + group;
+  const int h = i / p.block_rows, in = i - h * p.block_rows, r = cut.y * p.block_rows + in;
+  const bool mine = i < pairs && r < rows_of(p, b);
   if (WIDE ? !mine : __ballot(mine) == 0) return;
-  const int64_t first = ((int64_t(plan.x) + int64_t(rb) * plan.y) * p.c.H + h) * p.block_rows +
-                        (r - rb * p.block_rows);
+  const int64_t first = (int64_t(cut.z) * p.c.H + h) * p.block_rows + in;
   const int64_t step = int64_t(p.c.H) * p.block_rows;
-  const int parts = mine ? plan.y : 0, stride = WIDE ? 16 : 1;
+  const int parts = mine ? cut.w : 0, stride = WIDE ? 16 : 1;
   float top = -INFINITY, sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int s0 = WIDE ? group : 0; s0 < parts; s0 += 4 * stride) {
     float2 st[4];
@@ -457,10 +458,11 @@ constexpr Share kShares[] = {{0, 128, 32, 1024, 8}, {128, INT_MAX, kDocRows, 512
 
 struct Plan {
   int32_t block_rows, targets;
-  int64_t plan_bytes, stat_bytes, bytes, grid;
+  int64_t cuts_bytes, stat_bytes, bytes, grid;
+  int64_t join_blocks;  // blocks that may be cut
 };
 // `rows`: the most of a sequence; `blocks`: in all.
-Plan make_plan(int kind, int32_t n_seqs, int64_t rows, int64_t blocks, int32_t H) {
+Plan make_plan(int kind, int64_t rows, int64_t blocks, int32_t H) {
   const Share& s = kShares[kind];
   Plan r = {};
   r.block_rows = kind == kFew ? int32_t(std::min<int64_t>(rows, s.block_rows)) : s.block_rows;
@@ -468,11 +470,11 @@ Plan make_plan(int kind, int32_t n_seqs, int64_t rows, int64_t blocks, int32_t H
   // few rows are cut however many sequences there are, since those may differ in length
   if (kind == kFew || blocks < targets) {
     r.targets = int32_t(targets);
-    // what is cut has less than twice its share of the parts
+    r.join_blocks = std::min(blocks, targets);
     const int64_t vecs = 2 * targets * H * r.block_rows;
-    r.plan_bytes = (int64_t(n_seqs) * 8 + 255) / 256 * 256;
+    r.cuts_bytes = ((targets + 1) * 16 + 255) / 256 * 256;
     r.stat_bytes = (vecs * 8 + 255) / 256 * 256;
-    r.bytes = r.plan_bytes + r.stat_bytes + vecs * D * 4;
+    r.bytes = r.cuts_bytes + r.stat_bytes + vecs * D * 4;
   }
   r.grid = (r.targets + blocks) * H;
   return r;
@@ -487,13 +489,13 @@ hipError_t launch_attend(const AttnParams& p, unsigned grid, hipStream_t stream)
   return hipGetLastError();
 }
 
-hipError_t launch_join(const AttnParams& p, int32_t rows, int64_t pairs, hipStream_t stream) {
-  if (pairs <= 1024)
-    hipLaunchKernelGGL(join_kernel<true>, dim3(unsigned(pairs)), dim3(kThreads), 0, stream, p, rows);
+hipError_t launch_join(const AttnParams& p, int64_t blocks, hipStream_t stream) {
+  const int64_t pairs = int64_t(p.block_rows) * p.c.H;
+  if (blocks * pairs <= 1024)
+    hipLaunchKernelGGL(join_kernel<true>, dim3(unsigned(blocks * pairs)), dim3(kThreads), 0, stream, p);
   else
-    hipLaunchKernelGGL(join_kernel<false>,
-                       dim3(unsigned((int64_t(rows) * p.c.H + 15) / 16 * p.c.n_seqs)),
-                       dim3(kThreads), 0, stream, p, rows);
+    hipLaunchKernelGGL(join_kernel<false>, dim3(unsigned(blocks * ((pairs + 15) / 16))),
+                       dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -509,14 +511,14 @@ extern "C" size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t tot
                                                      int32_t H_q, int32_t H_kv) {
   namespace kc = kda::cache;
   if (n_seqs < 1 || total_tokens < 1 || total_tokens > (int64_t(1) << 30) ||
-      kc::bad_heads(H_q, H_kv) || H_q / H_kv > 256)
+      kc::bad_heads(H_q, H_kv) || H_q / H_kv > 256 || H_kv > kc::kMaxHeads)
     return 0;
   // whatever the sequences' shares of the tokens
   const int64_t rows = total_tokens * (H_q / H_kv);
   int64_t bytes = 0;
   for (int i = 0; i < 2; ++i)
     if (rows > kc::kShares[i].over)
-      bytes += kc::make_plan(i, n_seqs, std::min<int64_t>(rows, kc::kShares[i].most), 0, H_kv).bytes;
+      bytes += kc::make_plan(i, std::min<int64_t>(rows, kc::kShares[i].most), 0, H_kv).bytes;
   return size_t(bytes);
 }
 
@@ -535,7 +537,7 @@ extern "C" kda_status kda_cache_attention(
                            num_pages, k_cache, k_page_stride, v_cache, v_page_stride, k_scale,
                            v_scale, page_table, table_width, table_row_stride, kv_lens};
   if (const kda_status st = kc::check(a, &p.c)) return st;
-  if (H_q / H_kv > 256 || !isfinite(scale)) return KDA_ERR_UNSUPPORTED;
+  if (H_q / H_kv > 256 || !isfinite(scale * kda::LOG2E)) return KDA_ERR_UNSUPPORTED;
   const int64_t row = int64_t(H_q) * D;
   if (q_row_stride < 0 || out_row_stride < 0 || (lse && lse_row_stride < 0) ||
       !kc::rows_apart(total_tokens, out_row_stride, row) ||
@@ -569,11 +571,9 @@ extern "C" kda_status kda_cache_attention(
   for (int i = 0; i < 2; ++i) {
     plan[i] = {};
     if (blocks[i] == 0) continue;
-    plan[i] = kc::make_plan(i, n_seqs, most[i], blocks[i], H_kv);
+    plan[i] = kc::make_plan(i, most[i], blocks[i], H_kv);
     bytes += plan[i].bytes;
-    if (most[i] > INT32_MAX - 128 || plan[i].grid > INT32_MAX ||
-        (plan[i].bytes > 0 && (most[i] * H_kv + 15) / 16 * n_seqs > INT32_MAX))
-      return KDA_ERR_UNSUPPORTED;
+    if (most[i] > INT32_MAX - 128 || plan[i].grid > kc::kMaxGrid) return KDA_ERR_UNSUPPORTED;
   }
   if (bytes > 0) {
     if (workspace_bytes < size_t(bytes)) return KDA_ERR_WORKSPACE_TOO_SMALL;
@@ -597,9 +597,9 @@ extern "C" kda_status kda_cache_attention(
     p.block_rows = plan[i].block_rows;
     p.targets = plan[i].targets;
     p.min_units = s.min_units;
-    p.plan = reinterpret_cast<int2*>(ws);
-    p.stat = reinterpret_cast<float2*>(ws + plan[i].plan_bytes);
-    p.part = reinterpret_cast<float*>(ws + plan[i].plan_bytes + plan[i].stat_bytes);
+    p.cuts = reinterpret_cast<int4*>(ws);
+    p.stat = reinterpret_cast<float2*>(ws + plan[i].cuts_bytes);
+    p.part = reinterpret_cast<float*>(ws + plan[i].cuts_bytes + plan[i].stat_bytes);
     ws += plan[i].bytes;
     const unsigned grid = unsigned(plan[i].grid);
     const hipError_t e = i == kc::kDocuments ? kc::launch_documents(p, int8, grid, stream)
@@ -608,7 +608,7 @@ extern "C" kda_status kda_cache_attention(
     if (e != hipSuccess) return KDA_ERR_LAUNCH;
     // nothing is cut where the table is too short for two parts
     if (plan[i].targets > 0 && int64_t(table_width) * page_size > s.min_units * kc::kUnit &&
-        kc::launch_join(p, int32_t(most[i]), most[i] * H_kv * n_seqs, stream) != hipSuccess)
+        kc::launch_join(p, plan[i].join_blocks, stream) != hipSuccess)
       return KDA_ERR_LAUNCH;
   }
   return KDA_OK;

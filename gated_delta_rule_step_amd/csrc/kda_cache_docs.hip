@@ -340,8 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
     __syncthreads();
   }
 
-  if (SPLIT && h == 0 && part.rb == 0 && part.index == 0 && threadIdx.x == 0)
-    p.plan[part.b] = make_int2(part.first_slot, part.parts);
+  if (SPLIT) list_cuts(p, h, lds.find);
   tot += __shfl_xor(tot, 32);
   if (r >= rows) return;
   const bool whole = !SPLIT || part.parts == 1;

@@ -44,12 +44,14 @@
  *
  * Errors common to the calls. KDA_ERR_BAD_SHAPE: negative sizes, H < 1,
  * num_pages < 0, table_width < 1, total_tokens no multiple of n_seqs without
- * cu_seqlens, tokens without sequences. KDA_ERR_UNSUPPORTED: D other than 128, cache_dtype, page_size,
- * H over 2^14, more than 2^30 tokens, table_width * page_size over 2^28 or n_seqs times
- * that over 2^37, or more work items than a launch takes (2^31 - 1 workgroups). KDA_ERR_BAD_STRIDE: a negative
- * stride, a page stride below H * page_size * 128, output rows or the pages' rows
- * that overlap, a table_row_stride below table_width. num_pages = 0 needs no cache
- * pointers; total_tokens = 0 is a no-op that needs no pointers.
+ * cu_seqlens, tokens without sequences. KDA_ERR_UNSUPPORTED: D other than 128,
+ * cache_dtype, page_size, H over 2^13, more than 2^30 tokens, table_width * page_size
+ * over 2^28 or n_seqs times that over 2^35, or more than the 2^24 - 1 workgroups of a
+ * launch (a page that gets or gives tokens, or 32 or 128 query rows of a key/value
+ * head). KDA_ERR_BAD_STRIDE: a negative stride, a page stride below H * page_size *
+ * 128, output rows or the pages' rows that overlap, a table_row_stride below
+ * table_width. num_pages = 0 needs no cache pointers; total_tokens = 0 is a no-op that
+ * needs no pointers. No output may overlap an input or another output.
  */
 #ifndef KDA_CACHE_H_
 #define KDA_CACHE_H_
@@ -75,7 +77,8 @@ enum {
  *   need  = 2^e, e the smallest integer >= -100 with amax <= M 2^e
  *   scale = need where the call writes slot 0 of the page, else max(need, old scale)
  *   code  = value / scale, rounded to nearest even; beyond +-M (infinities) +-M;
- *           NaN: the e4m3 NaN, or 0 in int8
+ *           NaN: the e4m3 NaN, or 0 in int8. (Behind an old scale that is no power of
+ *           two and stays: value * (1 / scale), both in fp32.)
  * Where the scale grows, the codes of the sequence's earlier tokens in that page
  * become code * (old scale / scale), rounded the same way: with powers of two an
  * e4m3 value changes only where it falls below 2^-6 of the new scale. Other slots
@@ -127,7 +130,7 @@ size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t total_tokens, 
  *                     query head h reads key/value head h / (H_q / H_kv)
  *  cu_seqlens_host    HOST copy of cu_seqlens (the plan of the launch); both or neither
  *  q                  bf16 [total_tokens, H_q * 128]
- *  scale              finite; multiplies q . k
+ *  scale              multiplies q . k; finite, also times log2(e)
  *  out                bf16 [total_tokens, H_q * 128]
  *  lse                fp32 [total_tokens, H_q] with lse_row_stride, or NULL
  *  workspace          >= kda_cache_attention_workspace_size(...) bytes, 256-byte
@@ -135,7 +138,10 @@ size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t total_tokens, 
  *                     that do not overlap in time may share one
  * Token i of sequence b sees the keys at positions 0 .. kv_lens[b] - n_b + i:
  *   s_j = scale q . k_j,  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
- * with fp32 sums, maxima and products; a token that sees no key has out = 0 and
+ * with fp32 sums and maxima. The products take q, the codes and the weights exp(s_j - ref)
+ * of a sequence's call with at most 128 query rows per key/value head (n_b * H_q / H_kv)
+ * to at least 16 bits; with more rows weights are rounded to bf16, as are values whose
+ * page has a scale that is no power of two. A token that sees no key has out = 0 and
  * lse = -infinity. The cache has to hold the call's own tokens (kda_cache_write).
  * The result does not depend on other sequences' contents, and is the same in every
  * call with the same lengths.

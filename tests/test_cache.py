@@ -63,6 +63,8 @@ COMMON = [
     (UNSUP, dict(dt=2)), (UNSUP, dict(dt=-1)), (UNSUP, dict(P=8)), (UNSUP, dict(P=24)),
     (UNSUP, dict(P=512)), (UNSUP, dict(P=0)), (UNSUP, dict(H=1 << 15)),
     (UNSUP, dict(N=1 << 31)), (UNSUP, dict(n=1 << 20, T=1 << 20, w=1 << 14, ts=1 << 14)),
+    (UNSUP, dict(n=1 << 19, T=1 << 19, w=1 << 13, ts=1 << 13)),
+    (UNSUP, dict(n=1 << 24, T=1 << 24, w=1, ts=1)), (UNSUP, dict(H=8193, kp=8193 * 2048, vp=8193 * 2048)),
     (UNSUP, dict(T=(1 << 30) + 2)), (UNSUP, dict(kc=4100)), (UNSUP, dict(vp=6148)),
     (STRIDE, dict(ts=-1)), (STRIDE, dict(ts=3)), (STRIDE, dict(kp=6128)), (STRIDE, dict(vp=-16)),
     (NULLP, dict(tab=0)), (NULLP, dict(lens=0)), (NULLP, dict(kc=0)), (NULLP, dict(vc=0)),
@@ -104,7 +106,8 @@ def _attend(lib, host=None, **kw):
 @pytest.mark.parametrize("want,kw", [x for x in COMMON if "H" not in x[1]] + [
     (SHAPE, dict(Hq=0)), (SHAPE, dict(Hq=7)), (SHAPE, dict(H=0)), (SHAPE, dict(H=-3)),
     (UNSUP, dict(Hq=771)), (UNSUP, dict(sc=float("nan"))), (UNSUP, dict(sc=float("inf"))),
-    (UNSUP, dict(ws=4100)), (WS, dict(wb=3)), (NULLP, dict(ws=0)), (NULLP, dict(q=0)),
+    (UNSUP, dict(sc=3e38)), (UNSUP, dict(H=8193, Hq=8193)),
+    (UNSUP, dict(n=1 << 23, T=1 << 23, w=1, ts=1)), (UNSUP, dict(ws=4100)), (WS, dict(wb=3)), (NULLP, dict(ws=0)), (NULLP, dict(q=0)),
     (NULLP, dict(o=0)), (NULLP, dict(cu=4096)), (STRIDE, dict(qs=-1)), (STRIDE, dict(os=767)),
     (STRIDE, dict(lse=4096, ls=5)), (STRIDE, dict(lse=4096, ls=-6)),
     (SEQ, dict(host=[1, 2, 3])), (SEQ, dict(host=[0, 3, 2])), (SEQ, dict(host=[0, 3, 7])),
@@ -117,6 +120,7 @@ def test_attention_refusals(lib, want, kw):
 def test_workspace_size(lib):
     size = kda.kda_cache_attention_workspace_size
     assert size(0, 4, 8, 8) == 0 and size(1, 0, 8, 8) == 0
+    assert size(1, 1, 8193, 8193) == 0 < size(1, 1, 8192, 8192)
     assert size(1, 1, 7, 2) == 0 and size(1, 1, 0, 0) == 0 and size(1, 1, 514, 2) == 0
     for heads in ((12, 12), (64, 8), (6, 2), (40, 1)):
         got = [size(n, n, *heads) for n in (1, 2, 63, 512, 5000)]
@@ -411,6 +415,21 @@ def test_write_bad_values_and_sequences(lib, kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [1, 30])
+def test_write_behind_scales_of_other_makers(lib, kind, n):
+    """Earlier tokens under zero, negative and odd scales, below what the new tokens need."""
+    pool = Pool(kind, 3, 64, [13 + n, 64 + 5 + n], seed=7).fill([13, 69])
+    for side in range(2):
+        for page in (pool.table[0, 0], pool.table[1, 1]):
+            pool.scale[side][page] = torch.tensor([0.0, -2.0 ** -6, 1.5 * 2.0 ** -9])
+    g = torch.Generator().manual_seed(8)
+    k, v = _tokens(2 * n, 3, g), _tokens(2 * n, 3, g)
+    k[0], k[n], v[0], v[n] = 9.0, -5.0, 7.0, 30.0
+    _check_write(pool, k, v, [n, n], True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("P", [16, 128])
 def test_write_token_by_token(lib, kind, P):
     """A decode loop: scales grow, earlier codes follow, as the definition says call by call."""
@@ -681,6 +700,20 @@ def test_attention_document_parts(lib, kind):
     totals = [5003, 2900, 3, 131]
     pool = Pool(kind, 1, 64, totals, seed=28).fill()
     _check_attention(pool, counts, 1, False, weight=2.0 ** -8, seed=29)
+
+
+@pytest.mark.gpu
+def test_attention_parts_of_a_mixed_batch(lib):
+    """Decoded tokens, a few of them with long caches, drafts of several blocks and documents, cut
+    and whole: every block that is cut is joined, and no other."""
+    g = torch.Generator().manual_seed(45)
+    counts = [1] * 290
+    totals = torch.randint(1, 30, (290,), generator=g).tolist()
+    for b, n, total in ((3, 45, 2200), (70, 1, 2600), (71, 150, 1700), (140, 0, 1500),
+                        (200, 100, 1300), (255, 260, 2000), (256, 129, 129), (289, 1, 1100)):
+        counts[b], totals[b] = n, total
+    pool = Pool(F8, 2, 32, totals, seed=46).fill()
+    _check_attention(pool, counts, 1, False, weight=2.0 ** -8, seed=47, extra=2)
 
 
 @pytest.mark.gpu
