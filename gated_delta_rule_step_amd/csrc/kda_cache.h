@@ -65,7 +65,7 @@ __device__ __forceinline__ int32_t page_of(const CacheView& p, int32_t b, int32_
   return uint32_t(id) < uint32_t(p.num_pages) ? id : -1;
 }
 
-// Loaded words stay whole up to here. (The compiler else may keep a register for each byte of them.)
+// Loaded words stay whole up to here. (The compiler else may keep a register for each byte.)
 template <typename T>
 __device__ __forceinline__ void whole(T& words) {
   asm("" : "+v"(words));
@@ -74,8 +74,9 @@ __device__ __forceinline__ void whole(T& words) {
 template <int KIND>
 __device__ __forceinline__ u32x2 widen4(uint32_t w) {
   if constexpr (KIND == kFp8) {
-    return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
+    return u32x2{
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
   } else {
     return u32x2{pack_bf16x2_exact(float(int8_t(w)), float(int8_t(w >> 8))),
                  pack_bf16x2_exact(float(int8_t(w >> 16)), float(int8_t(w >> 24)))};

@@ -4,15 +4,19 @@
 // a document and key/value head is query head r mod G of token r / G, so that grouped heads
 // share what is loaded. A workgroup takes 32 rows per wave and walks 64 keys at a time: their
 // codes are widened to bf16 once for all its waves, into LDS (exact for the values' scales that
-// kda_cache_write makes; the keys' scales multiply the scores), the values transposed on the way. The
-// next tile's codes come in meanwhile, and two workgroups share a CU, so that one's exponentials
+// kda_cache_write makes; the keys' scales multiply the scores), the values transposed on the way.
+// The next tile's codes come in meanwhile, and two workgroups share a CU, so that one's exponentials
 // run beside the other's products.
 //
 // With keys as the rows of the products (S^T = K Q^T, O^T = V^T P^T) all of a lane's scores and
 // outputs belong to one query row, and the weights P^T leave the first product in the
 // layout that the second one reads. They are rounded to bf16 there (the sum that divides them is
 // not): errors of half a step, independent of one another, that leave the output about as far off
-// as its own rounding does; a second part would cost a quarter more products.
+// as its own rounding does; a second part would cost half as many products again.
+//
+// Documents of 4096 and 1777 tokens behind 2000 to 12000, 64 query heads on 8: 1.38 ms, 965 TFLOP/s
+// of the 1605 that a large library product reaches; 14 documents of 16384 tokens, 12 heads on 4:
+// 161 us, 707. Matrix instructions take 45 % of a SIMD's cycles, vector instructions 41 %.
 
 #include <math.h>
 
@@ -30,7 +34,8 @@ constexpr float kNoRef = -3.0e38f;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct Smem {
-  // chunk c < 8 of a key's row: channels 16 c .., c >= 8: channels 16 (c - 8) + 8 ..; at c ^ (key & 15)
+  // chunk c < 8 of a key's row: channels 16 c .., c >= 8: channels 16 (c - 8) + 8 ..; at
+  // c ^ (key & 15): no bank conflicts
   u32x4 k[2][kTile * 16];
   // a channel's row: tokens of each run of 16 in the order 0-3, 8-11, 4-7, 12-15, chunks of 8 at
   // c ^ swizzle(channel)
@@ -97,7 +102,8 @@ __device__ __forceinline__ u32x2 scaled4(uint32_t w, float scale) {
 }
 
 // To LDS. Tokens that do not exist become zeros. With `diagonal`, so do NaN codes, which leave
-// their position in nan_at: rows that see it become NaN in the end, and the others stay clear of 0 NaN.
+// their position in nan_at: rows that see it become NaN in the end, and the others stay clear of
+// 0 NaN.
 template <int KIND>
 __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_t tok, bool diagonal,
                                             int slot, Smem& lds) {

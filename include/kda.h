@@ -1,6 +1,7 @@
 /*
  * kda.h -- C ABI of the MI355X (gfx950) KDA gated delta-rule step library.
- * (kda_backward.h: the prefill's gradients; kda_norm.h: a KDA layer's norms.)
+ * (kda_backward.h: the prefill's gradients; kda_norm.h: a KDA layer's norms;
+ * kda_cache.h: the paged cache of attention layers beside KDA layers.)
  *
  * The method (Kimi Delta Attention): per head h, a state S that maps 128 key
  * channels to 128 value channels is updated for every token by

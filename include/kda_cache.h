@@ -138,9 +138,9 @@ size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t total_tokens, 
  *                     that do not overlap in time may share one
  * Token i of sequence b sees the keys at positions 0 .. kv_lens[b] - n_b + i:
  *   s_j = scale q . k_j,  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
- * with fp32 sums and maxima. The products take q, the codes and the weights exp(s_j - ref)
- * of a sequence's call with at most 128 query rows per key/value head (n_b * H_q / H_kv)
- * to at least 16 bits; with more rows weights are rounded to bf16, as are values whose
+ * with fp32 sums and maxima, and products of exact q and codes. The weights exp(s_j - ref)
+ * keep 16 significant bits where a sequence has at most 128 query rows per key/value
+ * head (n_b * H_q / H_kv); with more rows they are rounded to bf16, as are values whose
  * page has a scale that is no power of two. A token that sees no key has out = 0 and
  * lse = -infinity. The cache has to hold the call's own tokens (kda_cache_write).
  * The result does not depend on other sequences' contents, and is the same in every

@@ -792,10 +792,13 @@ def test_pages_past_32_bits(lib):
         kda.kda_cache_attention(qd, o, *cache, cu_seqlens_host=cu.cpu(), cu_seqlens=cu)
     assert torch.equal(*out)
     new = torch.randn(2, H * 128).to(BF).cuda()
+    new[0, 5] = 100.0  # its page's scale grows
+    scales = [s.clone() for s in rest[:2]]  # each write has the scales as they were
     kda.kda_cache_write(new, new, *small)
-    kda.kda_cache_write(new, new, *big, *rest)
+    kda.kda_cache_write(new, new, *big, *scales, *rest[2:])
     for side in range(2):
         assert torch.equal(small[side].view(torch.uint8), big[side].view(torch.uint8))
+        assert torch.equal(rest[side].nan_to_num(-1), scales[side].nan_to_num(-1))
 
 
 @pytest.mark.gpu
