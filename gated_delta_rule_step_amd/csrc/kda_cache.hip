@@ -33,19 +33,21 @@ struct ReadParams {
   CacheView c;
   uint16_t* dst[2];
   int64_t dst_stride[2];
-  int32_t per_seq_items;
+  int32_t per_seq_items, shift;  // units of 1 << shift tokens
 };
 
-// Work items are (sequence, page that gets tokens). n tokens touch at most
-// (n + P - 2) / P + 1 pages, so items of sequence b start at cu[b] / P + 2 b: no prefix sum.
-// The last b with a start <= item, found by 64 lanes at a time.
-__device__ __forceinline__ int32_t find_seq(const CacheView& p, int32_t item, int32_t lane) {
+// Work items are (sequence, unit with tokens of the call): a unit is a page or, for reads, an equal
+// share of one. n tokens touch at most (n + U - 2) / U + 1 units of U tokens, so items of sequence b
+// start at cu[b] / U + 2 b: no prefix sum. The last b with a start <= item, found by 64 lanes at a
+// time.
+__device__ __forceinline__ int32_t find_seq(const CacheView& p, int32_t item, int32_t shift,
+                                            int32_t lane) {
   int32_t lo = 0, span = p.n_seqs;  // the answer lies in [lo, lo + span)
   while (span > 1) {
     const int32_t step = (span + 63) >> 6;
     const int32_t b = lo + lane * step;
     const bool is = lane * step < span &&
-                    (clamp_row(p, p.cu[b]) >> p.page_shift) + 2 * int64_t(b) <= item;
+                    (clamp_row(p, p.cu[b]) >> shift) + 2 * int64_t(b) <= item;
     const int32_t hits = __popcll(__ballot(is));
     lo += max(hits - 1, 0) * step;
     span = min(step, p.n_seqs - lo);
@@ -53,37 +55,40 @@ __device__ __forceinline__ int32_t find_seq(const CacheView& p, int32_t item, in
   return lo;
 }
 
-// The item's page (-1: none), its slots [a, z) that get the packed rows from `row` on.
+// The item's page (-1: none), the unit's first slot there, and the slots [a, z) that belong to the
+// packed rows from `row` on.
 struct Item {
-  int32_t b, page, a, z;
+  int32_t b, page, at, a, z;
   int64_t row;
 };
 __device__ __forceinline__ Item find_item(const CacheView& p, int32_t item, int32_t per_seq_items,
-                                          int32_t lane) {
+                                          int32_t shift, int32_t lane) {
   Item it;
   int32_t j;
   if (p.cu) {
-    it.b = __builtin_amdgcn_readfirstlane(find_seq(p, item, lane));
-    j = item - ((clamp_row(p, p.cu[it.b]) >> p.page_shift) + 2 * it.b);
+    it.b = __builtin_amdgcn_readfirstlane(find_seq(p, item, shift, lane));
+    j = item - ((clamp_row(p, p.cu[it.b]) >> shift) + 2 * it.b);
   } else {
     it.b = item / per_seq_items;
     j = item - it.b * per_seq_items;
   }
   const Seq s = sequence(p, it.b);
-  const int32_t P = 1 << p.page_shift;
+  const int32_t U = 1 << shift;
   it.page = -1;
-  it.a = it.z = 0;
+  it.at = it.a = it.z = 0;
   it.row = s.first;
   if (j < 0 || s.n == 0) return it;
   // an inactive sequence's rows are walked as if it began on a page's border
   const int32_t start = s.len < 0 ? 0 : s.len - s.n;
-  const int32_t first = start & (P - 1);
-  const int64_t from = (int64_t(j) << p.page_shift) - first;  // token in the page's slot 0
+  const int32_t first = start & (U - 1);
+  const int64_t from = (int64_t(j) << shift) - first;  // token in the unit's first slot
   if (from >= s.n) return it;
-  it.a = from < 0 ? first : 0;
-  it.z = int32_t(min(int64_t(P), int64_t(s.n) - from));
+  const int32_t unit = int32_t(start + from);
+  it.at = unit & ((1 << p.page_shift) - 1);
+  it.a = it.at + (from < 0 ? first : 0);
+  it.z = it.at + int32_t(min(int64_t(U), int64_t(s.n) - from));
   it.row = s.first + (from < 0 ? 0 : from);
-  if (s.len >= 0) it.page = page_of(p, it.b, (start >> p.page_shift) + j);
+  if (s.len >= 0) it.page = page_of(p, it.b, unit >> p.page_shift);
   return it;
 }
 
@@ -215,29 +220,19 @@ struct Rows {
   }
 };
 
-// A workgroup per (page, head, side).
+// A side of a (page, head) by a workgroup, both sides by a wave.
 template <int KIND, int PASSES>
-__global__ __launch_bounds__(kThreads) void write_kernel(WriteParams p) {
-  __shared__ uint32_t tops[4];
-  const int lane = threadIdx.x & 63, side = blockIdx.y & 1, h = blockIdx.y >> 1;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
-  if (it.page < 0) return;  // the same for all waves
+__device__ __forceinline__ void write_page(const WriteParams& p, int side, const Item& it, int h,
+                                           uint32_t (&tops)[4]) {
   Rows<KIND, 4, PASSES> rows;
   rows.load(p, side, it, h, threadIdx.x);
   const uint32_t top = rows.top();
-  if (lane == 0) tops[wave] = top;
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
   __syncthreads();
   rows.store(p, side, it, h, threadIdx.x, max(max(tops[0], tops[1]), max(tops[2], tops[3])));
 }
-// Few tokens: a wave per (page, head), both sides.
 template <int KIND, int PASSES>
-__global__ __launch_bounds__(kThreads) void write_few_kernel(WriteParams p) {
-  const int lane = threadIdx.x & 63;
-  const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (h >= p.c.H) return;
-  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
-  if (it.page < 0) return;
+__device__ __forceinline__ void write_few(const WriteParams& p, const Item& it, int h, int lane) {
   Rows<KIND, 1, PASSES> k, v;
   k.load(p, 0, it, h, lane);
   v.load(p, 1, it, h, lane);
@@ -245,7 +240,42 @@ __global__ __launch_bounds__(kThreads) void write_few_kernel(WriteParams p) {
   v.store(p, 1, it, h, lane, v.top());
 }
 
-// Rows (head, slot) of a page are one run of bytes; a workgroup takes kReadRows of them, a
+// A workgroup per (page, head, side).
+template <int KIND, int PASSES>
+__global__ __launch_bounds__(kThreads) void write_kernel(WriteParams p) {
+  __shared__ uint32_t tops[4];
+  const int lane = threadIdx.x & 63, side = blockIdx.y & 1, h = blockIdx.y >> 1;
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, p.c.page_shift, lane);
+  if (it.page < 0) return;  // the same for all waves
+  write_page<KIND, PASSES>(p, side, it, h, tops);
+}
+// Few tokens: a wave per (page, head), both sides.
+template <int KIND, int PASSES>
+__global__ __launch_bounds__(kThreads) void write_few_kernel(WriteParams p) {
+  const int lane = threadIdx.x & 63;
+  const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (h >= p.c.H) return;
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, p.c.page_shift, lane);
+  if (it.page < 0) return;
+  write_few<KIND, PASSES>(p, it, h, lane);
+}
+// Single tokens and drafts beside documents: four heads by a workgroup, in either way.
+template <int KIND, int PASSES>
+__global__ __launch_bounds__(kThreads) void write_mixed_kernel(WriteParams p) {
+  __shared__ uint32_t tops[2][4];
+  const int lane = threadIdx.x & 63, h0 = blockIdx.y * 4, heads = min(p.c.H - h0, 4);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, p.c.page_shift, lane);
+  if (it.page < 0) return;  // the same for all waves, as is what follows
+  if (it.z - it.a <= 16) {
+    if (wave < heads) write_few<KIND, 4>(p, it, h0 + wave, lane);
+    return;
+  }
+  for (int i = 0; i < 2 * heads; ++i)
+    write_page<KIND, PASSES>(p, i & 1, it, h0 + (i >> 1), tops[i & 1]);
+}
+
+// Rows (head, slot) of a unit; a workgroup takes kReadRows of them, a
 // row by 16 lanes of 8 codes, so that a wave's loads and stores are whole lines. Non-temporal
 // stores of few rows per workgroup: 16384 tokens of 8 heads 17.6 us, 5.7 TB/s (with 8 lanes to a row
 // 29.6 us, ordinary stores of 256 rows 27.5, non-temporal ones 21.7, of 128 rows 19.1).
@@ -254,10 +284,9 @@ constexpr int kReadPasses = kReadRows / 16;
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadParams p) {
   const int lane = threadIdx.x & 63, side = blockIdx.z;
-  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, lane);
+  const Item it = find_item(p.c, blockIdx.x, p.per_seq_items, p.shift, lane);
   if (it.z == it.a) return;
-  const int P = 1 << p.c.page_shift;
-  const int most = p.c.H << p.c.page_shift;
+  const int most = p.c.H << p.shift;
   const uint8_t* const page = (side ? p.c.v + max(it.page, 0) * p.c.v_page
                                     : p.c.k + max(it.page, 0) * p.c.k_page);
   const float* const scales = (side ? p.c.v_scale : p.c.k_scale) + int64_t(max(it.page, 0)) * p.c.H;
@@ -266,17 +295,18 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadParams p) {
   float scale[kReadPasses];
 #pragma unroll
   for (int i = 0; i < kReadPasses; ++i) {
-    const int r = r0 + i * 16, slot = r & (P - 1);
+    const int r = r0 + i * 16, h = r >> p.shift, slot = it.at + (r & ((1 << p.shift) - 1));
     w[i] = u32x2{0u, 0u};
     scale[i] = 0.0f;
     if (it.page >= 0 && r < most && slot >= it.a && slot < it.z) {
-      w[i] = *reinterpret_cast<const u32x2*>(page + int64_t(r) * D + ch);
-      scale[i] = scales[r >> p.c.page_shift];
+      w[i] = *reinterpret_cast<const u32x2*>(
+          page + ((int64_t(h) << p.c.page_shift) + slot) * D + ch);
+      scale[i] = scales[h];
     }
   }
 #pragma unroll
   for (int i = 0; i < kReadPasses; ++i) {
-    const int r = r0 + i * 16, slot = r & (P - 1);
+    const int r = r0 + i * 16, h = r >> p.shift, slot = it.at + (r & ((1 << p.shift) - 1));
     if (r >= most || slot < it.a || slot >= it.z) continue;
     float x[4], y[4];
     whole(w[i]);
@@ -285,17 +315,16 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadParams p) {
     const float f = scale[i];
     const u32x4_u o = u32x4{pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
                             pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f)};
-    uint16_t* const dst = p.dst[side] + (it.row + slot - it.a) * p.dst_stride[side] +
-                          (r >> p.c.page_shift) * D + ch;
+    uint16_t* const dst = p.dst[side] + (it.row + slot - it.a) * p.dst_stride[side] + h * D + ch;
     __builtin_nontemporal_store(o, reinterpret_cast<u32x4_u*>(dst));
   }
 }
 
-// Work items (see find_seq), 0: more than a launch takes.
-int64_t count_items(const CacheView& c, int32_t* per_seq) {
-  const int64_t P = int64_t(1) << c.page_shift;
-  *per_seq = int32_t((c.per_seq + P - 2) / P + 1);
-  const int64_t n = c.cu ? c.total / P + 2 * int64_t(c.n_seqs) : int64_t(c.n_seqs) * *per_seq;
+// Work items (see find_seq) of units of 1 << shift tokens, 0: more than a launch takes.
+int64_t count_items(const CacheView& c, int32_t shift, int32_t* per_seq) {
+  const int64_t U = int64_t(1) << shift;
+  *per_seq = int32_t((c.per_seq + U - 2) / U + 1);
+  const int64_t n = c.cu ? c.total / U + 2 * int64_t(c.n_seqs) : int64_t(c.n_seqs) * *per_seq;
   return n <= kMaxGrid ? n : 0;
 }
 
@@ -304,7 +333,15 @@ hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream
   const int P = 1 << p.c.page_shift;
   const int most = p.c.cu ? P : (p.c.per_seq < P ? p.c.per_seq : P);
   const dim3 few(items, (p.c.H + 3) / 4), grid(items, 2 * p.c.H), block(kThreads);
-  if (most <= 4)
+  // Sequences of at most 16 tokens on the average: most pages get a few. (8 heads, pages of 64 | 256,
+  // against a workgroup per side: 1024 single tokens 12 us against 41 | 14.5 against 57, beside a
+  // document of 960 tokens 19 against 42 | 35 against 58; 64 of them beside it 12.4 against 11.1.)
+  if (p.c.cu && most > 16 && p.c.total <= 16 * int64_t(p.c.n_seqs)) {
+    if (most <= 64)
+      hipLaunchKernelGGL((write_mixed_kernel<KIND, 4>), few, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((write_mixed_kernel<KIND, 16>), few, block, 0, stream, p);
+  } else if (most <= 4)
     hipLaunchKernelGGL((write_few_kernel<KIND, 1>), few, block, 0, stream, p);
   else if (most <= 16)
     hipLaunchKernelGGL((write_few_kernel<KIND, 4>), few, block, 0, stream, p);
@@ -383,7 +420,7 @@ extern "C" kda_status kda_cache_write(
   if (k_row_stride < 0 || v_row_stride < 0) return KDA_ERR_BAD_STRIDE;
   if (total_tokens == 0) return KDA_OK;
   if (!k || !v) return KDA_ERR_NULL_POINTER;
-  const int64_t items = kc::count_items(p.c, &p.per_seq_items);
+  const int64_t items = kc::count_items(p.c, p.c.page_shift, &p.per_seq_items);
   if (items == 0) return KDA_ERR_UNSUPPORTED;
   if (num_pages == 0) return KDA_OK;  // no page to write to
   p.src[0] = static_cast<const uint16_t*>(k);
@@ -418,13 +455,18 @@ extern "C" kda_status kda_cache_read(
     return KDA_ERR_BAD_STRIDE;
   if (total_tokens == 0) return KDA_OK;
   if (!k || !v) return KDA_ERR_NULL_POINTER;
-  const int64_t items = kc::count_items(p.c, &p.per_seq_items);
+  // Units about as long as a sequence's tokens (1024 single tokens, 8 heads, pages of 64 | 256: 14 |
+  // 15 us, by whole pages 39 | 134).
+  const int64_t mean = (total_tokens + n_seqs - 1) / n_seqs;
+  p.shift = 4;
+  while (p.shift < p.c.page_shift && (1 << p.shift) < mean) ++p.shift;
+  const int64_t items = kc::count_items(p.c, p.shift, &p.per_seq_items);
   if (items == 0) return KDA_ERR_UNSUPPORTED;
   p.dst[0] = static_cast<uint16_t*>(k);
   p.dst[1] = static_cast<uint16_t*>(v);
   p.dst_stride[0] = k_row_stride;
   p.dst_stride[1] = v_row_stride;
-  const unsigned rows = unsigned(H) << p.c.page_shift;
+  const unsigned rows = unsigned(H) << p.shift;
   const dim3 grid(unsigned(items), (rows + kc::kReadRows - 1) / kc::kReadRows, 2);
   if (cache_dtype == KDA_CACHE_FP8)
     hipLaunchKernelGGL(kc::read_kernel<kc::kFp8>, grid, dim3(kc::kThreads), 0, stream, p);

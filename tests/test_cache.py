@@ -382,6 +382,34 @@ def test_write_ragged(lib, kind, P, H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [32, 64, 128, 256])
+@pytest.mark.parametrize("H", [1, 5, 8])
+def test_mixed_batch_written_and_read(lib, kind, P, H):
+    """Single tokens and drafts beside documents, some behind earlier tokens, some inactive."""
+    counts = [1] * 40
+    past = torch.randint(0, 2 * P, (40,), generator=torch.Generator().manual_seed(P)).tolist()
+    for b, n in ((0, 0), (3, 17), (4, 8), (9, 300), (10, 16), (21, 0), (22, 70), (39, 33)):
+        counts[b] = n
+    pool = Pool(kind, H, P, [a + b for a, b in zip(counts, past)], seed=9).fill(past)
+    pool.lens[5], pool.lens[12] = 0, pool.cap() + 1
+    g = torch.Generator().manual_seed(H)
+    T = sum(counts)
+    _check_write(pool, _tokens(T, H, g), _tokens(T, H, g), counts, False, pad=6, offset=3)
+    got = [torch.full((T + 2, H * 128), -7.0, dtype=BF, device="cuda") for _ in range(2)]
+    kda.kda_cache_read(*got, *pool.gpu(), cu_seqlens=_cu(counts).cuda())
+    for side in range(2):
+        want, at = torch.zeros(T, H, 128, dtype=torch.float64), 0
+        for b, n in enumerate(counts):
+            total = pool.lens[b].item()
+            if n <= total <= pool.cap():
+                want[at:at + n] = pool.tokens(side, b, total)[0][total - n:]
+            at += n
+        assert torch.equal(got[side][:T].double().cpu().reshape(T, H, 128), want)
+        assert (got[side][T:] == -7).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [63, 64, 65, 130, 4100])
 def test_write_many_sequences(lib, n):
     g = torch.Generator().manual_seed(n)
