@@ -27,7 +27,8 @@ struct AttnParams {
   int32_t block_rows;   // rows of a block (of a part's results, too)
   int32_t targets;      // parts that all the blocks' keys are cut into, 0: none is cut
   int32_t min_units;    // units of a part at least
-  int4* cuts;           // [0].x: blocks whose keys are cut; then their sequence, block, slot, parts
+  int4* starts;         // [n_seqs], if listed: first item, cuts before, parts, blocks
+  int4* cuts;           // [0].x: blocks whose keys are cut (y: units of a part, if listed); then their sequence, block, slot, parts
   float2* stat;         // [slot][H][block_rows]: reference exponent, sum
   float* part;          // [slot][H][block_rows][128]: sums of p v
 };
@@ -62,22 +63,74 @@ struct FindSmem {
   int32_t all_cuts;  // blocks that are cut
   Part part;
 };
+// Up to so many sequences each workgroup finds its work by itself, from kHeld of them a thread;
+// more are walked once, by list_sequences, and searched (single tokens, 8 heads, us, walked |
+// listed: 300 of 500 keys 68 | 70, 512 of them 111 | 116, 512 of 100 keys 58 | 48, 1024 of 60 keys
+// 78 | 56, 4096 of 250 keys 885 | 399, 16384 of 60 keys 11056 | 777).
+constexpr int32_t kHeld = 2, kWalked = 512;
+
+// Blocks that are cut << 16 | their slots (both far below 2^16)
+__device__ __forceinline__ uint32_t cut_of(int32_t blocks, int32_t parts) {
+  return parts > 1 ? uint32_t(blocks) << 16 | uint32_t(blocks * parts) : 0u;
+}
+// Part of the sequence b, `in` items behind its first one.
+__device__ __forceinline__ Part part_at(const AttnParams& p, int32_t b, int32_t in, int32_t blocks,
+                                        int32_t parts, uint32_t before, int32_t chunk) {
+  Part x;
+  x.b = b;
+  x.parts = parts;
+  x.index = parts > 1 ? in / blocks : 0;
+  x.rb = blocks - 1 - (in - x.index * blocks);
+  x.slot = int32_t(before & 0xffffu) + x.rb * parts + x.index;
+  x.from = parts == 1 ? 0 : x.index * chunk * kUnit;
+  x.to = x.index + 1 == parts ? INT_MAX : x.from + chunk * kUnit;
+  x.cut = parts > 1 ? int32_t(before >> 16) + x.rb : -1;
+  // (more than there are: cu_seqlens is not what the host's copy says)
+  if (x.cut >= p.targets || (parts > 1 && x.slot >= 2 * p.targets)) x.b = -1;
+  return x;
+}
 // Work item `item`: the sequences one after the other, a sequence's parts in turn, the blocks that
-// share a part's keys next to each other, the last one (with the most keys to see) first. Every
-// workgroup of T threads finds it for itself from the lengths on the device, K sequences a thread;
-// SPLIT: the keys may be cut. Each sequence's keys are cut into equal parts of a length that is the
+// share a part's keys next to each other, the last one (with the most keys to see) first. A
+// workgroup of T threads finds it for itself from the lengths on the device, K sequences a thread, or
+// (LISTED) from what list_sequences left. SPLIT: the keys may be cut. Each sequence's keys are cut into equal parts of a length that is the
 // same for all, however ragged the batch, except for what rounding to units leaves. What is cut has
 // less than twice its share of the parts: 2 * targets slots. The blocks that are cut are listed for
 // the join, which has workgroups for as many as there may be (with workgroups for every row that a
 // sequence may have, 1024 decoded tokens beside a document of 7680 rows took 1740 us, now 377).
 // (By single waves, 64 sequences at a time, 512 sequences took 10 us to walk.)
-template <bool SPLIT, int T>
+template <bool SPLIT, int T, bool LISTED>
 __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, FindSmem& lds,
                                           Part& out) {
-  constexpr int kHeld = 4;  // sequences of a thread that stay in registers
+  static_assert(LISTED || kWalked <= kHeld * T, "a thread holds kHeld sequences");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t B = p.c.n_seqs, K = (B + T - 1) / T, b0 = int32_t(threadIdx.x) * K;
+  if constexpr (LISTED) {
+    int32_t b = 0, span = B;  // the last sequence with a first item <= item is in [b, b + span)
+    while (span > 1) {
+      const int32_t step = (span + 63) >> 6;
+      const bool is = lane * step < span && p.starts[b + lane * step].x <= item;
+      b += max(int32_t(__popcll(__ballot(is))) - 1, 0) * step;
+      span = min(step, B - b);
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    const int4 s = p.starts[b];
+    const int32_t in = item - s.x;
+    if (in < 0 || in >= s.z * s.w) return false;
+    out = part_at(p, b, in, s.w, s.z, uint32_t(s.y), p.cuts[0].y);
+    if (threadIdx.x == 0) {
+      lds.part = out;
+      lds.all_cuts = p.cuts[0].x;
+    }
+    out.b = __builtin_amdgcn_readfirstlane(out.b);
+    out.rb = __builtin_amdgcn_readfirstlane(out.rb);
+    out.index = __builtin_amdgcn_readfirstlane(out.index);
+    out.parts = __builtin_amdgcn_readfirstlane(out.parts);
+    out.slot = __builtin_amdgcn_readfirstlane(out.slot);
+    out.from = __builtin_amdgcn_readfirstlane(out.from);
+    out.to = __builtin_amdgcn_readfirstlane(out.to);
+    return out.b >= 0;
+  }
   const auto sizes = [&](int k, int32_t& blocks, int32_t& units) {
     const bool is = k < K && b0 + k < B;
     blocks = is ? blocks_of(p, b0 + k) : 0;
@@ -91,11 +144,6 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
     int32_t sum = 0;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) sum += blocks[k] * units[k];
-    for (int k = kHeld; k < K; ++k) {
-      int32_t n, u;
-      sizes(k, n, u);
-      sum += n * u;
-    }
     sum = wave_prefix(sum);
     if (lane == 63) lds.work[wave] = sum;
     __syncthreads();
@@ -105,24 +153,15 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
     chunk = max(p.min_units, (sum + p.targets - 1) / p.targets);
   }
   const auto parts_of = [&](int32_t u) { return SPLIT ? max((u + chunk - 1) / chunk, 1) : 1; };
-  // blocks that are cut << 16 | their slots (both far below 2^16)
-  const auto cut = [](int32_t n, int32_t parts) {
-    return parts > 1 ? uint32_t(n) << 16 | uint32_t(n * parts) : 0u;
-  };
   int32_t items = 0;
   uint32_t cuts = 0;
   const auto count = [&](int32_t n, int32_t u) {
     const int32_t parts = parts_of(u);
     items += n * parts;
-    cuts += cut(n, parts);
+    cuts += cut_of(n, parts);
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) count(blocks[k], units[k]);
-  for (int k = kHeld; k < K; ++k) {
-    int32_t n, u;
-    sizes(k, n, u);
-    count(n, u);
-  }
   int32_t first = wave_prefix(items);
   uint32_t before = SPLIT ? uint32_t(wave_prefix(int32_t(cuts))) : 0;
   if (lane == 63) {
@@ -145,22 +184,11 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
       sizes(k, n, u);
       const int32_t parts = parts_of(u);
       if (item < first + n * parts) {
-        Part x;
-        x.b = b0 + k;
-        x.parts = parts;
-        x.index = SPLIT ? (item - first) / n : 0;
-        x.rb = n - 1 - (item - first - x.index * n);
-        x.slot = int32_t(before & 0xffffu) + x.rb * parts + x.index;
-        x.from = parts == 1 ? 0 : x.index * chunk * kUnit;
-        x.to = x.index + 1 == parts ? INT_MAX : x.from + chunk * kUnit;
-        x.cut = parts > 1 ? int32_t(before >> 16) + x.rb : -1;
-        // (more than there are: cu_seqlens is not what the host's copy says)
-        if (x.cut >= p.targets || (parts > 1 && x.slot >= 2 * p.targets)) x.b = -1;
-        lds.part = x;
+        lds.part = part_at(p, b0 + k, item - first, n, parts, before, chunk);
         break;
       }
       first += n * parts;
-      before += cut(n, parts);
+      before += cut_of(n, parts);
     }
   }
   __syncthreads();

@@ -118,7 +118,7 @@ __device__ __forceinline__ void clear_values(Values& v, const int32_t (&live)[2]
 }
 
 // One workgroup: (part of a sequence's keys, key/value head) for up to 16 NT rows.
-template <int KIND, int NT>
+template <int KIND, int NT, bool LISTED>
 __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnParams p) {
   __shared__ float sums[4][16 * kRow];
   __shared__ float refs[4][16], tots[4][16];
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
   Part part;
-  if (!find_part<true, kThreads>(p, item, find, part)) return;
+  if (!find_part<true, kThreads, LISTED>(p, item, find, part)) return;
   const Seq seq = sequence(p.c, part.b);
   const int rows = rows_of(p, part.b), row0 = part.rb * 16 * NT;
   const int32_t len = p.c.num_pages > 0 ? max(seq.len, 0) : 0;
@@ -448,6 +448,57 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
                     : ((top == -INFINITY ? 0.0f : top) + __builtin_amdgcn_logf(sum)) * LN2;
 }
 
+// What find_part finds by walking all sequences, for its searches: by one workgroup.
+constexpr int kListThreads = 1024;
+__global__ __launch_bounds__(kListThreads) void list_sequences(AttnParams p) {
+  constexpr int T = kListThreads;
+  __shared__ int32_t work[T / 64], all_items[T / 64];
+  __shared__ uint32_t all_cuts[T / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t K = (p.c.n_seqs + T - 1) / T, b0 = int32_t(threadIdx.x) * K;
+  const int32_t b1 = min(b0 + K, p.c.n_seqs);
+  int32_t chunk = 1 << 28;  // whole sequences
+  if (p.targets > 0) {
+    int32_t sum = 0;
+    for (int32_t b = b0; b < b1; ++b) sum += blocks_of(p, b) * units_of(p.c, b);
+    sum = wave_prefix(sum);
+    if (lane == 63) work[wave] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < T / 64; ++w) sum += work[w];
+    chunk = max(p.min_units, (sum + p.targets - 1) / p.targets);
+  }
+  const auto parts_of = [&](int32_t b) { return max((units_of(p.c, b) + chunk - 1) / chunk, 1); };
+  int32_t items = 0;
+  uint32_t cuts = 0;
+  for (int32_t b = b0; b < b1; ++b) {
+    const int32_t n = blocks_of(p, b), parts = parts_of(b);
+    items += n * parts;
+    cuts += cut_of(n, parts);
+  }
+  int32_t first = wave_prefix(items);
+  uint32_t before = uint32_t(wave_prefix(int32_t(cuts)));
+  if (lane == 63) {
+    all_items[wave] = first;
+    all_cuts[wave] = before;
+  }
+  first -= items;
+  before -= cuts;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    first += all_items[w];
+    before += all_cuts[w];
+  }
+  for (int32_t b = b0; b < b1; ++b) {
+    const int32_t n = blocks_of(p, b), parts = parts_of(b);
+    p.starts[b] = make_int4(first, int32_t(before), parts, n);
+    first += n * parts;
+    before += cut_of(n, parts);
+  }
+  if (threadIdx.x == T - 1)
+    p.cuts[0] = make_int4(min(int32_t(before >> 16), p.targets), chunk, 0, 0);
+}
+
 // Host: the two kernels' shares of a call.
 struct Share {
   int32_t over, most;  // its sequences have over < rows <= most
@@ -464,15 +515,19 @@ constexpr Share kShares[] = {{0, 128, 32, 1024, 8}, {128, INT_MAX, kDocRows, 512
 
 struct Plan {
   int32_t block_rows, targets;
-  int64_t cuts_bytes, stat_bytes, bytes, grid;
+  int64_t starts_bytes, cuts_bytes, stat_bytes, bytes, grid;
   int64_t join_blocks;  // blocks that may be cut
 };
 // `rows`: the most of a sequence; `blocks`: in all.
-Plan make_plan(int kind, int64_t rows, int64_t blocks, int32_t H) {
+Plan make_plan(int kind, int32_t n_seqs, int64_t rows, int64_t blocks, int32_t H) {
   const Share& s = kShares[kind];
   Plan r = {};
   r.block_rows = kind == kFew ? int32_t(std::min<int64_t>(rows, s.block_rows)) : s.block_rows;
   const int64_t targets = std::max<int64_t>(1, s.groups / H);
+  if (n_seqs > kWalked) {
+    r.starts_bytes = (int64_t(n_seqs) * 16 + 255) / 256 * 256;
+    r.cuts_bytes = 256;
+  }
   // few rows are cut however many sequences there are, since those may differ in length
   if (kind == kFew || blocks < targets) {
     r.targets = int32_t(targets);
@@ -480,19 +535,27 @@ Plan make_plan(int kind, int64_t rows, int64_t blocks, int32_t H) {
     const int64_t vecs = 2 * targets * H * r.block_rows;
     r.cuts_bytes = ((targets + 1) * 16 + 255) / 256 * 256;
     r.stat_bytes = (vecs * 8 + 255) / 256 * 256;
-    r.bytes = r.cuts_bytes + r.stat_bytes + vecs * D * 4;
+    r.bytes = r.stat_bytes + vecs * D * 4;
   }
+  r.bytes += r.starts_bytes + r.cuts_bytes;
   r.grid = (r.targets + blocks) * H;
   return r;
 }
 
-template <int KIND>
+template <int KIND, bool LISTED>
 hipError_t launch_attend(const AttnParams& p, unsigned grid, hipStream_t stream) {
   if (p.block_rows <= 16)
-    hipLaunchKernelGGL((attend_kernel<KIND, 1>), dim3(grid), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attend_kernel<KIND, 1, LISTED>), dim3(grid), dim3(kThreads), 0, stream, p);
   else
-    hipLaunchKernelGGL((attend_kernel<KIND, 2>), dim3(grid), dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attend_kernel<KIND, 2, LISTED>), dim3(grid), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
+}
+hipError_t launch_few(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream) {
+  if (p.starts)
+    return int8 ? launch_attend<kInt8, true>(p, grid, stream)
+                : launch_attend<kFp8, true>(p, grid, stream);
+  return int8 ? launch_attend<kInt8, false>(p, grid, stream)
+              : launch_attend<kFp8, false>(p, grid, stream);
 }
 
 hipError_t launch_join(const AttnParams& p, int64_t blocks, hipStream_t stream) {
@@ -525,7 +588,7 @@ extern "C" size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t tot
   int64_t bytes = 0;
   for (int i = 0; i < 2; ++i)
     if (rows > kc::kShares[i].over)
-      bytes += kc::make_plan(i, std::min<int64_t>(rows, kc::kShares[i].most), 0, H_kv).bytes;
+      bytes += kc::make_plan(i, n_seqs, std::min<int64_t>(rows, kc::kShares[i].most), 0, H_kv).bytes;
   return size_t(bytes);
 }
 
@@ -579,7 +642,7 @@ extern "C" kda_status kda_cache_attention(
   for (int i = 0; i < 2; ++i) {
     plan[i] = {};
     if (blocks[i] == 0) continue;
-    plan[i] = kc::make_plan(i, most[i], blocks[i], H_kv);
+    plan[i] = kc::make_plan(i, n_seqs, most[i], blocks[i], H_kv);
     bytes += plan[i].bytes;
     if (most[i] > INT32_MAX - 128 || plan[i].grid > kc::kMaxGrid) return KDA_ERR_UNSUPPORTED;
   }
@@ -605,15 +668,20 @@ extern "C" kda_status kda_cache_attention(
     p.block_rows = plan[i].block_rows;
     p.targets = plan[i].targets;
     p.min_units = s.min_units;
-    p.cuts = reinterpret_cast<int4*>(ws);
-    p.stat = reinterpret_cast<float2*>(ws + plan[i].cuts_bytes);
-    p.part = reinterpret_cast<float*>(ws + plan[i].cuts_bytes + plan[i].stat_bytes);
+    p.starts = plan[i].starts_bytes > 0 ? reinterpret_cast<int4*>(ws) : nullptr;
+    p.cuts = reinterpret_cast<int4*>(ws + plan[i].starts_bytes);
+    uint8_t* const results = ws + plan[i].starts_bytes + plan[i].cuts_bytes;
+    p.stat = reinterpret_cast<float2*>(results);
+    p.part = reinterpret_cast<float*>(results + plan[i].stat_bytes);
     ws += plan[i].bytes;
     const unsigned grid = unsigned(plan[i].grid);
-    const hipError_t e = i == kc::kDocuments ? kc::launch_documents(p, int8, grid, stream)
-                         : int8            ? kc::launch_attend<kc::kInt8>(p, grid, stream)
-                                           : kc::launch_attend<kc::kFp8>(p, grid, stream);
-    if (e != hipSuccess) return KDA_ERR_LAUNCH;
+    if (p.starts) {
+      hipLaunchKernelGGL(kc::list_sequences, dim3(1), dim3(kc::kListThreads), 0, stream, p);
+      if (hipGetLastError() != hipSuccess) return KDA_ERR_LAUNCH;
+    }
+    if ((i == kc::kDocuments ? kc::launch_documents(p, int8, grid, stream)
+                             : kc::launch_few(p, int8, grid, stream)) != hipSuccess)
+      return KDA_ERR_LAUNCH;
     // nothing is cut where the table is too short for two parts
     if (plan[i].targets > 0 && int64_t(table_width) * page_size > s.min_units * kc::kUnit &&
         kc::launch_join(p, plan[i].join_blocks, stream) != hipSuccess)

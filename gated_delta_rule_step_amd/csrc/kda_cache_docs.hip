@@ -178,7 +178,7 @@ __device__ __forceinline__ void reads_ahead() {
 }
 
 // One workgroup: (128 rows of a document, key/value head, part of its keys).
-template <int KIND, bool SPLIT>
+template <int KIND, bool SPLIT, bool LISTED>
 __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
   constexpr int ROWS = kDocRows;
   __shared__ Smem lds;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = blockIdx.x / p.c.H, h = blockIdx.x - item * p.c.H;
   Part part;
-  if (!find_part<SPLIT, kThreads>(p, item, lds.find, part)) return;
+  if (!find_part<SPLIT, kThreads, LISTED>(p, item, lds.find, part)) return;
   const Seq seq = sequence(p.c, part.b);
   const int32_t rows = rows_of(p, part.b);
   const int32_t row0 = part.rb * ROWS + wave * 32;
@@ -379,18 +379,23 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
         tot == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(tot)) * LN2;
 }
 
-template <int KIND, bool SPLIT>
+template <int KIND, bool SPLIT, bool LISTED>
 hipError_t launch(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  hipLaunchKernelGGL((document_kernel<KIND, SPLIT>), dim3(grid), dim3(kThreads), 0, stream, p);
+  hipLaunchKernelGGL((document_kernel<KIND, SPLIT, LISTED>), dim3(grid), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_documents(const AttnParams& p, bool int8, unsigned grid, hipStream_t stream) {
+  if (p.starts)
+    return int8 ? launch<kInt8, true, true>(p, grid, stream)
+                : launch<kFp8, true, true>(p, grid, stream);
   if (p.targets > 0)
-    return int8 ? launch<kInt8, true>(p, grid, stream) : launch<kFp8, true>(p, grid, stream);
-  return int8 ? launch<kInt8, false>(p, grid, stream) : launch<kFp8, false>(p, grid, stream);
+    return int8 ? launch<kInt8, true, false>(p, grid, stream)
+                : launch<kFp8, true, false>(p, grid, stream);
+  return int8 ? launch<kInt8, false, false>(p, grid, stream)
+              : launch<kFp8, false, false>(p, grid, stream);
 }
 
 }  // namespace cache

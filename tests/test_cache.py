@@ -731,17 +731,44 @@ def test_attention_document_parts(lib, kind):
 
 
 @pytest.mark.gpu
-def test_attention_parts_of_a_mixed_batch(lib):
+@pytest.mark.parametrize("n", [290, 1300])
+def test_attention_parts_of_a_mixed_batch(lib, n):
     """Decoded tokens, a few of them with long caches, drafts of several blocks and documents, cut
     and whole: every block that is cut is joined, and no other."""
     g = torch.Generator().manual_seed(45)
-    counts = [1] * 290
-    totals = torch.randint(1, 30, (290,), generator=g).tolist()
-    for b, n, total in ((3, 45, 2200), (70, 1, 2600), (71, 150, 1700), (140, 0, 1500),
-                        (200, 100, 1300), (255, 260, 2000), (256, 129, 129), (289, 1, 1100)):
-        counts[b], totals[b] = n, total
+    counts = [1] * n
+    totals = torch.randint(1, 30, (n,), generator=g).tolist()
+    for b, m, total in ((3, 45, 2200), (70, 1, 2600), (71, 150, 1700), (140, 0, 1500),
+                        (200, 100, 1300), (255, 260, 2000), (256, 129, 129), (n - 1, 1, 1100)):
+        counts[b], totals[b] = m, total
     pool = Pool(F8, 2, 32, totals, seed=46).fill()
     _check_attention(pool, counts, 1, False, weight=2.0 ** -8, seed=47, extra=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [512, 513, 1025, 5000])
+@pytest.mark.parametrize("H", [2, 128])
+def test_attention_few_of_many_sequences(lib, n, H):
+    """A few sequences among many without tokens: the bits of the few alone. Documents that are
+    cut (2 heads) and whole."""
+    at = [7, 400, n - 20, n - 1]
+    counts, totals = [1, 3, 200, 330], [300, 40, 1200, 333]
+    pool = Pool(F8, H, 32, totals, seed=48).fill()
+    T = sum(counts)
+    q = torch.randn(T, H * 128, generator=torch.Generator().manual_seed(49)).to(BF).cuda()
+    cache = pool.gpu()
+    table = torch.full((n, pool.width), -1, dtype=I32, device="cuda")
+    lens, many = torch.zeros(n, dtype=I32, device="cuda"), [0] * n
+    for i, b in enumerate(at):
+        table[b], lens[b], many[b] = cache[4][i], cache[5][i], counts[i]
+    got = []
+    for c, cu in (((*cache[:4], table, lens), _cu(many)), (cache, _cu(counts))):
+        out = torch.full((T, H * 128), -7.0, dtype=BF, device="cuda")
+        lse = torch.full((T, H), -7.0, device="cuda")
+        kda.kda_cache_attention(q, out, *c, cu_seqlens_host=cu, cu_seqlens=cu.cuda(), lse=lse)
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert got[0][0].isfinite().all()
 
 
 @pytest.mark.gpu
