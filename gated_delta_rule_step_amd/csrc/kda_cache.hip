@@ -333,8 +333,8 @@ hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream
   const int P = 1 << p.c.page_shift;
   const int most = p.c.cu ? P : (p.c.per_seq < P ? p.c.per_seq : P);
   const dim3 few(items, (p.c.H + 3) / 4), grid(items, 2 * p.c.H), block(kThreads);
-  // Sequences of at most 16 tokens on the average: most pages get a few. (8 heads, pages of 64 | 256,
-  // against a workgroup per side: 1024 single tokens 12 us against 41 | 14.5 against 57, beside a
+  // Sequences of at most 16 tokens on the average: most pages get a few. (8 heads, pages of 64 |
+  // 256, against a workgroup per side: 1024 single tokens 12 us against 41 | 14.5 against 57, beside a
   // document of 960 tokens 19 against 42 | 35 against 58; 64 of them beside it 12.4 against 11.1.)
   if (p.c.cu && most > 16 && p.c.total <= 16 * int64_t(p.c.n_seqs)) {
     if (most <= 64)

@@ -28,7 +28,9 @@ struct AttnParams {
   int32_t targets;      // parts that all the blocks' keys are cut into, 0: none is cut
   int32_t min_units;    // units of a part at least
   int4* starts;         // [n_seqs], if listed: first item, cuts before, parts, blocks
-  int4* cuts;           // [0].x: blocks whose keys are cut (y: units of a part, if listed); then their sequence, block, slot, parts
+  // [0].x: blocks whose keys are cut (y: units of a part, if listed); then their sequence, block,
+  // slot, parts
+  int4* cuts;
   float2* stat;         // [slot][H][block_rows]: reference exponent, sum
   float* part;          // [slot][H][block_rows][128]: sums of p v
 };
@@ -91,13 +93,13 @@ __device__ __forceinline__ Part part_at(const AttnParams& p, int32_t b, int32_t 
 }
 // Work item `item`: the sequences one after the other, a sequence's parts in turn, the blocks that
 // share a part's keys next to each other, the last one (with the most keys to see) first. A
-// workgroup of T threads finds it for itself from the lengths on the device, K sequences a thread, or
-// (LISTED) from what list_sequences left. SPLIT: the keys may be cut. Each sequence's keys are cut into equal parts of a length that is the
-// same for all, however ragged the batch, except for what rounding to units leaves. What is cut has
-// less than twice its share of the parts: 2 * targets slots. The blocks that are cut are listed for
-// the join, which has workgroups for as many as there may be (with workgroups for every row that a
-// sequence may have, 1024 decoded tokens beside a document of 7680 rows took 1740 us, now 377).
-// (By single waves, 64 sequences at a time, 512 sequences took 10 us to walk.)
+// workgroup of T threads finds it for itself from the lengths on the device, K sequences a thread,
+// or (LISTED) from what list_sequences left. SPLIT: the keys may be cut, each sequence's into equal
+// parts of a length that is the same for all, however ragged the batch, except for what rounding to
+// units leaves. What is cut has less than twice its share of the parts: 2 * targets slots. The blocks
+// that are cut are listed for the join, which has workgroups for as many as there may be (with
+// workgroups for every row that a sequence may have, 1024 decoded tokens beside a document of 7680
+// rows took 1740 us, now 377). (By single waves, 64 sequences at a time, 512 took 10 us to walk.)
 template <bool SPLIT, int T, bool LISTED>
 __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, FindSmem& lds,
                                           Part& out) {

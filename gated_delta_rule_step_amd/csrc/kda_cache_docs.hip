@@ -80,7 +80,8 @@ __device__ __forceinline__ void load_share(const AttnParams& p, int32_t raw, int
   for (int i = 0; i < 2; ++i) s.k[i] = *reinterpret_cast<const u32x4*>(k + lane * 16 + i * 8 * D);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    s.v[r] = *reinterpret_cast<const u32x2*>(v + (lane_token(lane) * D + lane_channel(lane)) + r * D);
+    s.v[r] =
+        *reinterpret_cast<const u32x2*>(v + (lane_token(lane) * D + lane_channel(lane)) + r * D);
   const int64_t at = int64_t(use) * p.c.H + h + zero;
   s.ks = p.c.k_scale[at];
   s.vs = p.c.v_scale[at];
@@ -381,7 +382,8 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
 
 template <int KIND, bool SPLIT, bool LISTED>
 hipError_t launch(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  hipLaunchKernelGGL((document_kernel<KIND, SPLIT, LISTED>), dim3(grid), dim3(kThreads), 0, stream, p);
+  hipLaunchKernelGGL((document_kernel<KIND, SPLIT, LISTED>), dim3(grid), dim3(kThreads), 0, stream,
+                     p);
   return hipGetLastError();
 }
 
