@@ -45,7 +45,8 @@ __device__ __forceinline__ int32_t units_of(const CacheView& p, int32_t b) {
 __device__ __forceinline__ int32_t rows_of(const AttnParams& p, int32_t b) {
   int32_t n = p.c.per_seq;
   if (p.c.cu) n = max(clamp_row(p.c, p.c.cu[b + 1]) - clamp_row(p.c, p.c.cu[b]), 0);
-  return int32_t(min(int64_t(n) * p.G, int64_t(INT_MAX)));
+  // (a call of more rows is refused: only a cu_seqlens that is not the host's copy reaches this)
+  return int32_t(min(int64_t(n) * p.G, int64_t(INT_MAX - 255)));
 }
 // Blocks of a sequence, 0 for another kernel's.
 __device__ __forceinline__ int32_t blocks_of(const AttnParams& p, int32_t b) {
@@ -75,20 +76,22 @@ constexpr int32_t kHeld = 2, kWalked = 512;
 __device__ __forceinline__ uint32_t cut_of(int32_t blocks, int32_t parts) {
   return parts > 1 ? uint32_t(blocks) << 16 | uint32_t(blocks * parts) : 0u;
 }
-// Part of the sequence b, `in` items behind its first one.
+// Part of the sequence b, `in` items behind its first one; b = -1 where there is no such part or
+// no room for its results: cu_seqlens is not what the host's copy says, so that any of the 32-bit
+// sums and counts before this may have wrapped round. What passes is in range, whatever they are.
 __device__ __forceinline__ Part part_at(const AttnParams& p, int32_t b, int32_t in, int32_t blocks,
                                         int32_t parts, uint32_t before, int32_t chunk) {
   Part x;
-  x.b = b;
+  x.b = in < 0 || in >= int64_t(blocks) * parts ? -1 : b;
   x.parts = parts;
   x.index = parts > 1 ? in / blocks : 0;
   x.rb = blocks - 1 - (in - x.index * blocks);
-  x.slot = int32_t(before & 0xffffu) + x.rb * parts + x.index;
+  const int64_t slot = int64_t(before & 0xffffu) + int64_t(x.rb) * parts + x.index;
+  x.slot = int32_t(slot);
   x.from = parts == 1 ? 0 : x.index * chunk * kUnit;
   x.to = x.index + 1 == parts ? INT_MAX : x.from + chunk * kUnit;
   x.cut = parts > 1 ? int32_t(before >> 16) + x.rb : -1;
-  // (more than there are: cu_seqlens is not what the host's copy says)
-  if (x.cut >= p.targets || (parts > 1 && x.slot >= 2 * p.targets)) x.b = -1;
+  if (parts > 1 && (x.cut >= p.targets || slot >= 2 * p.targets)) x.b = -1;
   return x;
 }
 // Work item `item`: the sequences one after the other, a sequence's parts in turn, the blocks that
@@ -117,9 +120,8 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
     }
     b = __builtin_amdgcn_readfirstlane(b);
     const int4 s = p.starts[b];
-    const int32_t in = item - s.x;
-    if (in < 0 || in >= s.z * s.w) return false;
-    out = part_at(p, b, in, s.w, s.z, uint32_t(s.y), p.cuts[0].y);
+    if (s.w == 0) return false;  // behind the last item
+    out = part_at(p, b, item - s.x, s.w, s.z, uint32_t(s.y), p.cuts[0].y);
     if (threadIdx.x == 0) {
       lds.part = out;
       lds.all_cuts = p.cuts[0].x;
@@ -195,7 +197,11 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
   }
   __syncthreads();
   out.b = __builtin_amdgcn_readfirstlane(lds.part.b);
-  if (out.b < 0) return false;
+  if (out.b < 0) {
+    // the list of an earlier call in this workspace is not this one's
+    if (SPLIT && blockIdx.x == 0 && threadIdx.x == 0) p.cuts[0].x = 0;
+    return false;
+  }
   out.rb = __builtin_amdgcn_readfirstlane(lds.part.rb);
   out.index = __builtin_amdgcn_readfirstlane(lds.part.index);
   out.parts = __builtin_amdgcn_readfirstlane(lds.part.parts);

@@ -1049,3 +1049,112 @@ def test_workspace_comes_from_the_stream(lib, monkeypatch):
         kda.kda_cache_attention(q, o, c, c, Gpu(torch.ones(3, 1)), s, tab, lens)
     with pytest.raises(TypeError):
         kda.kda_cache_attention(q, o, Gpu(c.t.float()), c, s, s, tab, lens)
+
+
+# ---------------------------------------------------------------------------
+# cu_seqlens on the device that is not what the call was planned for: nothing outside of the
+# call's rows, pages and workspace is touched
+
+BAD_CU = [
+    [-5, 1, 61, 64, 64, 104], [-(1 << 31)] * 6, [0, 1, 61, 1 << 30, 64, (1 << 31) - 1],
+    [0, 90, 13, 64, 2, 104], [104, 64, 64, 61, 1, 0], [104] * 6, [0] * 6, [0, 104, 0, 104, 0, 104],
+    [0, 104, 104, 104, 104, 104], [50, 51, 52, 52, 60, 104],
+]
+
+
+def _rows_named(cu, T):
+    """The rows that some sequence of a clamped cu_seqlens has."""
+    named = torch.zeros(T, dtype=torch.bool)
+    for a, b in zip(cu, cu[1:]):
+        named[min(max(a, 0), T):max(min(max(b, 0), T), 0)] = True
+    return named
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", BAD_CU)
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_cu_seqlens_written_and_read(lib, cu, kind):
+    H, P, T = 3, 32, 104
+    pool = Pool(kind, H, P, [130, 200, 111, 104, 333], seed=60, pad=16).fill()
+    cache = pool.gpu()
+    k, v = (torch.full((T, H * 128), x, dtype=BF, device="cuda") for x in (3.0, -0.5))
+    bad = torch.tensor(cu, dtype=I32).cuda()
+    kda.kda_cache_write(k, v, *cache, cu_seqlens=bad)
+    owned = pool.table[(pool.table >= 0) & (pool.table < pool.N)]
+    free = torch.ones(pool.N, dtype=torch.bool)
+    free[owned] = False
+    for side in range(2):
+        got, size = pool.dev[side].cpu(), pool.strides[0]
+        assert torch.equal(got[pool.N * size:], pool.raw[side][pool.N * size:])
+        got, was = (x[:pool.N * size].reshape(pool.N, size) for x in (got, pool.raw[side]))
+        assert torch.equal(got[free], was[free]) and torch.equal(got[:, -16:], was[:, -16:])
+        assert pool.dev_scale[side].cpu()[free].isnan().all()
+    seen, bufs = [], []
+    for off in (16, 32):
+        buf = torch.full((T * H * 128 + 2 * off,), -7.0, dtype=BF, device="cuda")
+        seen.append(buf[off:-off].reshape(T, H * 128))
+        bufs.append((buf, off))
+    kda.kda_cache_read(*seen, *cache, cu_seqlens=bad)
+    for x, (buf, off) in zip(seen, bufs):
+        assert (x[~_rows_named(cu, T).cuda()] == -7).all()
+        assert (buf[:off] == -7).all() and (buf[-off:] == -7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", BAD_CU)
+@pytest.mark.parametrize("n", [5, 600])
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_cu_seqlens_attention(lib, cu, n, kind):
+    """Planned for a single token, a document, a draft and another document; 5 sequences, or these
+    among 600."""
+    H, G, T, counts = 2, 4, 104, [1, 60, 3, 0, 40]
+    pool = Pool(kind, H, 32, [1300, 2000, 111, 104, 1500], seed=61).fill()
+    cache = list(pool.gpu())
+    host, bad = _cu(counts), torch.tensor(cu, dtype=I32)
+    if n > 5:
+        more = n - 5
+        cache[4] = torch.cat([cache[4], cache[4][:1].expand(more, -1)])
+        cache[5] = torch.cat([cache[5], torch.full((more,), 300, dtype=I32, device="cuda")])
+        host = torch.cat([host, host[-1:].expand(more)])
+        bad = torch.cat([bad, bad[torch.arange(more) % 6]])
+    q = torch.randn(T, H * G * 128, generator=torch.Generator().manual_seed(62)).to(BF).cuda()
+    size = kda.kda_cache_attention_workspace_size(n, T, H * G, H)
+    ws = torch.full((size + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    obuf = torch.full((T + 2, H * G * 128), -7.0, dtype=BF, device="cuda")
+    lbuf = torch.full((T + 2, H * G), -7.0, device="cuda")
+    for device in (bad, host, bad):  # the bad ones find what a call before them left, too
+        obuf.fill_(-7.0)
+        lbuf.fill_(-7.0)
+        kda.kda_cache_attention(q, obuf[1:-1], *cache, cu_seqlens_host=host,
+                                cu_seqlens=device.cuda(), lse=lbuf[1:-1],
+                                workspace=ws[4096:-4096])
+        named = _rows_named(device.tolist(), T).cuda()
+        for x in (obuf, lbuf):
+            assert (x[0] == -7).all() and (x[-1] == -7).all()
+            assert (x[1:-1][~named] == -7).all()
+        assert (ws[:4096] == 0x5a).all() and (ws[-4096:] == 0x5a).all()
+
+
+@pytest.mark.gpu
+def test_bad_cu_seqlens_of_more_parts_than_32_bits_count(lib):
+    """Planned for one token, with 262194 of 256 query heads on the device: 2^19 + 100 blocks of 128
+    rows, and 32761 units of 128 keys. The blocks' units, added up in 32 bits, are negative, so that
+    parts are the shortest ones, 8191 of them, and the last blocks' numbers times the parts pass 2^32:
+    there is no room for any of their results."""
+    T, units = 262194, 32761
+    assert (T * 2 * units + (1 << 31)) % (1 << 32) < 1 << 31  # negative
+    assert 0 < T * 2 * 8191 - (1 << 32) < 36 * 8191
+    c = torch.zeros(1, 1, 256, 128, dtype=I8, device="cuda")
+    s = torch.ones(1, 1, device="cuda")
+    table = torch.zeros(1, units // 2 + 1, dtype=I32, device="cuda")
+    lens = torch.tensor([units * 128], dtype=I32, device="cuda")
+    q = torch.ones(1, 256 * 128, dtype=BF, device="cuda").expand(T, -1)
+    out = torch.full((T, 256 * 128), -7.0, dtype=BF, device="cuda")
+    size = kda.kda_cache_attention_workspace_size(1, T, 256, 1)
+    ws = torch.full((size + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    kda.kda_cache_attention(q, out, c, c, s, s, table, lens,
+                            cu_seqlens_host=torch.tensor([0, 1], dtype=I32),
+                            cu_seqlens=torch.tensor([0, T], dtype=I32).cuda(),
+                            workspace=ws[4096:-4096])
+    assert (ws[:4096] == 0x5a).all() and (ws[-4096:] == 0x5a).all()
+    assert (out == -7).all()  # no part of these fits
