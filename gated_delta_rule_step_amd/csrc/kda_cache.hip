@@ -114,8 +114,9 @@ __device__ __forceinline__ float saturate(float x) {
   else
     return x != x ? 0.0f : __builtin_amdgcn_fmed3f(x, -127.0f, 127.0f);
 }
-// Values within the codes' range. int8: the low byte of x + 1.5 2^23, whose last place is 1, is x
-// rounded to nearest even.
+// Values within the codes' range, inv a power of two. int8: the low byte of x + 1.5 2^23, whose last
+// place is 1, is x rounded to nearest even. (One fused operation, since a inv is exact; it would
+// pass over the rounding of any other product.)
 template <int KIND>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
   if constexpr (KIND == kFp8) {
@@ -128,6 +129,7 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
     return lo | hi;
   }
 }
+// Any values and any scale: a inv is rounded to fp32 first.
 template <int KIND>
 __device__ __forceinline__ uint32_t encode4_any(float a, float b, float c, float d, float inv) {
   return encode4<KIND>(saturate<KIND>(a * inv), saturate<KIND>(b * inv), saturate<KIND>(c * inv),
@@ -167,7 +169,8 @@ struct Rows {
       if (r < it.z - it.a) x[i] = *reinterpret_cast<const u32x4_u*>(src + r * p.src_stride[side]);
     }
   }
-  // Magnitude bits of the wave's largest finite value; `any`: it has others, too.
+  // Magnitude bits of the wave's largest finite value; `any`: it has others, too. (An old scale that
+  // stays and is no power of two adds to it, in store.)
   __device__ __forceinline__ uint32_t top() {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     u16x2 m = {0, 0};
@@ -204,6 +207,7 @@ struct Rows {
       }
     }
     if (t == 0) p.scale[side][int64_t(it.page) * p.c.H + h] = scale;
+    any |= (__float_as_uint(scale) & 0x007fffffu) != 0;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int r = (t >> 4) + i * 4 * WAVES;

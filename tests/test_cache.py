@@ -1158,3 +1158,38 @@ def test_bad_cu_seqlens_of_more_parts_than_32_bits_count(lib):
                             workspace=ws[4096:-4096])
     assert (ws[:4096] == 0x5a).all() and (ws[-4096:] == 0x5a).all()
     assert (out == -7).all()  # no part of these fits
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("n", [1, 3, 13, 40])
+@pytest.mark.parametrize("bad", [None, torch.nan, -torch.inf])
+def test_write_behind_an_odd_scale_that_stays(lib, kind, P, n, bad):
+    """Earlier tokens under a scale that is no power of two and more than the new ones need: codes
+    are value * (1 / scale), each step rounded to fp32, then to the nearest code. Odd multiples of
+    half the scale are ties in exact arithmetic and in fp32, though not of the unrounded product; an
+    infinity or a NaN changes its own code only."""
+    odd = torch.tensor([1.5, 0.7, 3.1])
+    pool = Pool(kind, 3, P, [5 + n], seed=70, width=5).fill([5])
+    for side in range(2):
+        pool.scale[side][pool.table[0, 0]] = odd
+    g = torch.Generator().manual_seed(71)
+    x = [(torch.randint(-30, 30, (n, 3, 128), generator=g) + 0.5).float() * odd[:, None]
+         for _ in range(2)]
+    x[0][:, :, ::3] = torch.randn(n, 3, 43, generator=g) * 9
+    k, v = (t.to(BF) for t in x)
+    if bad is not None:
+        k[0, 0, 1], v[n - 1, 2, 127] = bad, bad
+    cache = pool.gpu()
+    kda.kda_cache_write(k.reshape(n, -1).cuda(), v.reshape(n, -1).cuda(), *cache)
+    here = min(n, P - 5)  # the new tokens in the earlier ones' page
+    for side, t in enumerate((k, v)):
+        want = _nearest((t[:here].float() * (1 / odd)[:, None]).double(), kind)
+        if kind == F8:
+            want = torch.where(t[:here].isnan(), torch.nan, want)
+        page = pool.table[0, 0]
+        got = pool.codes([r.cpu() for r in pool.dev])[side][page].contiguous().view(kind)
+        got = _value(got, kind)[:, 5:5 + here].transpose(0, 1)
+        assert torch.equal(got.nan_to_num(1000.0), want.nan_to_num(1000.0))
+        assert torch.equal(pool.dev_scale[side][page].cpu(), odd)
