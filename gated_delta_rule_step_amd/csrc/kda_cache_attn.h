@@ -197,11 +197,7 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
   }
   __syncthreads();
   out.b = __builtin_amdgcn_readfirstlane(lds.part.b);
-  if (out.b < 0) {
-    // the list of an earlier call in this workspace is not this one's
-    if (SPLIT && blockIdx.x == 0 && threadIdx.x == 0) p.cuts[0].x = 0;
-    return false;
-  }
+  if (out.b < 0) return false;
   out.rb = __builtin_amdgcn_readfirstlane(lds.part.rb);
   out.index = __builtin_amdgcn_readfirstlane(lds.part.index);
   out.parts = __builtin_amdgcn_readfirstlane(lds.part.parts);
