@@ -31,8 +31,8 @@ struct AttnParams {
   // [0].x: blocks whose keys are cut (y: units of a part, if listed); then their sequence, block,
   // slot, parts
   int4* cuts;
-  float2* stat;         // [slot][H][block_rows]: reference exponent, sum
-  float* part;          // [slot][H][block_rows][128]: sums of p v
+  float2* stat;         // [slot][H][block_rows]: reference exponent, sum of the weights
+  float* part;          // [slot][H][block_rows][128]: sums of p v, divided by that sum
 };
 
 // Keys are split in units of 128 tokens.
@@ -205,6 +205,13 @@ __device__ __forceinline__ bool find_part(const AttnParams& p, int32_t item, Fin
   out.from = __builtin_amdgcn_readfirstlane(lds.part.from);
   out.to = __builtin_amdgcn_readfirstlane(lds.part.to);
   return true;
+}
+
+// Natural logarithm of sum 2^ref; the sum's exponent is added where the reference's is.
+__device__ __forceinline__ float log_sum(float ref, float sum) {
+  if (sum == 0.0f) return -INFINITY;
+  return (ref + float(__builtin_amdgcn_frexp_expf(sum)) +
+          __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(sum))) * LN2;
 }
 
 // For the join, by the kernel's end (a store in front of its loop has the loop wait for it).

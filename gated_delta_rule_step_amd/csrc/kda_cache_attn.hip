@@ -29,8 +29,12 @@ constexpr int kThreads = 256;
 constexpr int kStep = 32;            // tokens of a wave's step
 constexpr int kStride = 4 * kStep;   // and of the workgroup's
 constexpr int kRow = D + 4;          // fp32 row in LDS
-// Weights stay below 2^8 (see `slack`), far inside bf16 and fp32.
+// Weights stay below 2^kSlack (see `slack`), 2^kLarge times that with the values' scales.
 constexpr float kSlack = 8.0f;
+// Scales beyond 2^60 bring values whose sums, or products with a weight, may pass fp32's range. From the
+// first one on a wave's weights and sums are 2^-64 of what they were, so that sums of 2^28 tokens stay
+// below 2^128 whatever the scale; what that flushes to zero is less than 2^-120 of such a value.
+constexpr float kLarge = 0x1p60f, kSmaller = 0x1p-64f;
 
 // A wave's 32 tokens are two tiles of 16, each inside one page.
 struct Ids {
@@ -121,7 +125,7 @@ __device__ __forceinline__ void clear_values(Values& v, const int32_t (&live)[2]
 template <int KIND, int NT, bool LISTED>
 __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnParams p) {
   __shared__ float sums[4][16 * kRow];
-  __shared__ float refs[4][16], tots[4][16];
+  __shared__ float refs[4][16], tots[4][16], units[4];
   __shared__ int32_t nan_at[D];
   __shared__ FindSmem find;
   constexpr bool kInLds = NT > 1;
@@ -172,6 +176,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
   __syncthreads();
 
   f32x4 o[NT][8];
+  bool smaller = false;  // see kLarge
   // A row's reference exponent moves when a score passes it by more than `slack`: by anything at
   // first.
   float ref[NT], slack[NT], tot[NT];
@@ -213,7 +218,17 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
     const float f[2] = {p.scale2 * k.scale[0], p.scale2 * k.scale[1]};
     if (more) load_keys(p, h, at + kStride, to, ids_next, m, g, k);
     // (whatever the scale of a page that does not exist is)
-    const float vs[2] = {live[0] > 0 ? v.scale[0] : 0.0f, live[1] > 0 ? v.scale[1] : 0.0f};
+    float vs[2] = {live[0] > 0 ? v.scale[0] : 0.0f, live[1] > 0 ? v.scale[1] : 0.0f};
+    if (smaller || __any(fmaxf(fabsf(vs[0]), fabsf(vs[1])) > kLarge)) {
+      const float down = smaller ? 1.0f : kSmaller;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[n][c] *= down;
+      vs[0] *= kSmaller;
+      vs[1] *= kSmaller;
+      smaller = true;
+    }
     bf16x8 ph[NT], pl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -305,6 +320,7 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
   }
 
   list_cuts(p, h, find);
+  if (lane == 0) units[wave] = smaller ? kSmaller : 1.0f;
   // the four waves' sums, 16 rows at a time; thread (row, 8 channels)
   const int row = threadIdx.x >> 4, ch = (threadIdx.x & 15) * 8;
 #pragma unroll
@@ -327,11 +343,13 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
     const int t = r / p.G;
     const float top = fmaxf(fmaxf(refs[0][row], refs[1][row]), fmaxf(refs[2][row], refs[3][row]));
     const float r0 = top == -INFINITY ? 0.0f : top;
+    const float unit = fminf(fminf(units[0], units[1]), fminf(units[2], units[3]));
     float sum = 0.0f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float f = __builtin_amdgcn_exp2f(refs[w][row] - r0);
+      float f = __builtin_amdgcn_exp2f(refs[w][row] - r0);
       sum += tots[w][row] * f;
+      if (units[w] != unit) f *= unit;
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] += sums[w][row * kRow + ch + c] * f;
     }
@@ -340,15 +358,19 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
       for (int c = 0; c < 8; ++c)
         if (nan_at[ch + c] <= base + t) acc[c] = NAN;
     }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = acc[c] * inv;
+    if (unit != 1.0f) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] *= 1.0f / kSmaller;
+    }
     if (part.parts == 1) {
       const int64_t head = int64_t(h) * p.G + (r - t * p.G);
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       *reinterpret_cast<u32x4_u*>(p.out + (seq.first + t) * p.out_stride + head * D + ch) =
-          u32x4{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv)};
-      if (p.lse && ch == 0)
-        p.lse[(seq.first + t) * p.lse_stride + head] =
-            sum == 0.0f ? -INFINITY : (r0 + __builtin_amdgcn_logf(sum)) * LN2;
+          u32x4{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7])};
+      if (p.lse && ch == 0) p.lse[(seq.first + t) * p.lse_stride + head] = log_sum(r0, sum);
     } else {
       const int64_t slot = (int64_t(part.slot) * p.c.H + h) * p.block_rows + (r - row0);
       float* const dst = p.part + slot * D + ch;
@@ -359,7 +381,8 @@ __global__ __launch_bounds__(kThreads, NT == 1 ? 4 : 3) void attend_kernel(AttnP
   }
 }
 
-// Joins the parts of the blocks that are cut, a row by 16 lanes of 8 channels, four parts at a time.
+// Joins the parts of the blocks that are cut, a row by 16 lanes of 8 channels, four parts at a time:
+// an average, so that no value is beyond the largest of them.
 // WIDE: a workgroup's 16 groups share one row's parts (few rows, many parts), else each has a row
 // of its own.
 template <bool WIDE>
@@ -401,15 +424,21 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
     }
     const float now = fmaxf(fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x)), top);
     const float r0 = now == -INFINITY ? 0.0f : now;
-    const float down = __builtin_amdgcn_exp2f(top - r0);
-    top = now;
-    sum *= down;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] *= down;
+    float f = sum * __builtin_amdgcn_exp2f(top - r0), all = f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float f = __builtin_amdgcn_exp2f(st[j].x - r0);
-      sum += st[j].y * f;
+      st[j].y *= __builtin_amdgcn_exp2f(st[j].x - r0);
+      all += st[j].y;
+    }
+    top = now;
+    sum = all;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    f *= inv;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f = st[j].y * inv;
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] += x[j][c >> 2][c & 3] * f;
     }
@@ -427,9 +456,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
     sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+    for (int w = 0; w < 16; ++w) sum += stats[w].y * __builtin_amdgcn_exp2f(stats[w].x - r0);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     for (int w = 0; w < 16; ++w) {
-      const float f = __builtin_amdgcn_exp2f(stats[w].x - r0);
-      sum += stats[w].y * f;
+      const float f = stats[w].y * __builtin_amdgcn_exp2f(stats[w].x - r0) * inv;
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] += accs[w][ch + c] * f;
     }
@@ -438,14 +468,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnParams p) {
   const Seq seq = sequence(p.c, b);
   const int t = r / p.G;
   const int64_t head = int64_t(h) * p.G + (r - t * p.G);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   *reinterpret_cast<u32x4_u*>(p.out + (seq.first + t) * p.out_stride + head * D + ch) =
-      u32x4{pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-            pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv)};
+      u32x4{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+            pack_bf16x2(acc[6], acc[7])};
   if (p.lse && ch == 0)
-    p.lse[(seq.first + t) * p.lse_stride + head] =
-        sum == 0.0f ? -INFINITY
-                    : ((top == -INFINITY ? 0.0f : top) + __builtin_amdgcn_logf(sum)) * LN2;
+    p.lse[(seq.first + t) * p.lse_stride + head] = log_sum(top == -INFINITY ? 0.0f : top, sum);
 }
 
 // What find_part finds by walking all sequences, for its searches: by one workgroup.

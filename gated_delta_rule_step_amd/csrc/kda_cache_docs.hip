@@ -351,7 +351,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
   tot += __shfl_xor(tot, 32);
   if (r >= rows) return;
   const bool whole = !SPLIT || part.parts == 1;
-  const float inv = !whole ? 1.0f : tot == 0.0f ? 0.0f : 1.0f / tot;
+  const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
   uint16_t* const dst = p.out + (seq.first + tok) * p.out_stride + head * D;
   const int64_t slot = (int64_t(part.slot) * p.c.H + h) * ROWS + wave * 32 + m;
   typedef u32x2 u32x2_u __attribute__((aligned(2)));
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
     p.stat[slot] = make_float2(tot == 0.0f ? -INFINITY : ref, tot);
   else if (p.lse)
     p.lse[(seq.first + tok) * p.lse_stride + head] =
-        tot == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(tot)) * LN2;
+        log_sum(ref, tot);
 }
 
 template <int KIND, bool SPLIT, bool LISTED>

@@ -1193,3 +1193,101 @@ def test_write_behind_an_odd_scale_that_stays(lib, kind, P, n, bad):
         got = _value(got, kind)[:, 5:5 + here].transpose(0, 1)
         assert torch.equal(got.nan_to_num(1000.0), want.nan_to_num(1000.0))
         assert torch.equal(pool.dev_scale[side][page].cpu(), odd)
+
+
+# ---------------------------------------------------------------------------
+# attention by whole sequences, the tolerance by each sequence's rows
+#
+# As above, with these weights' relative errors: 2^-16 up to 128 rows, and half a step of fp16,
+# 2^-11, beyond. fp16's smallest step is 2^-24 where the largest (weight * |scale|) of a row so far is
+# 2^6 at least: half of it for each of n tokens, times a code of up to 448 and over a sum that is at
+# least as large, n 2^-31 * 448 max (p |scale|). Few rows flush what is below 2^-126, or below 2^-62
+# where a scale passes 2^60: n times that, times 448. bf16's smallest step adds 2^-134. log2 of a
+# scale that is no power of two, up to 2^7 and a step of 2^-17, is off by 2^-18 + 2^-23, and its
+# reciprocal by 2^-23: 2^-18 covers both in a weight, 2^-18 in lse.
+
+def _ref_sequences(pool, q, counts, G, scale):
+    """out, lse, tol, lt, and sum (p v)^2; q fp64 [T, Hq, 128]."""
+    T, Hq = q.shape[:2]
+    out, tol, sq = (torch.zeros(T, Hq, 128, dtype=torch.float64) for _ in range(3))
+    lse, lt = torch.full((T, Hq), -torch.inf).double(), torch.zeros(T, Hq).double()
+    at = 0
+    for b, n in enumerate(counts):
+        total = pool.lens[b].item()
+        rows, at = slice(at, at + n), at + n
+        if n == 0 or not n <= total <= pool.cap():
+            continue
+        doc = n * G > 128
+        (keys, there), (values, _) = pool.tokens(0, b, total), pool.tokens(1, b, total)
+        size = torch.zeros(total, pool.H, dtype=torch.float64)
+        for j in range(-(-total // pool.P)):
+            if 0 <= pool.table[b, j] < pool.N:
+                size[j * pool.P:(j + 1) * pool.P] = \
+                    pool.scale[1][pool.table[b, j]].abs().double()
+        hidden = ~there | (torch.arange(total) > torch.arange(total - n, total)[:, None])
+        for h in range(pool.H):
+            x = q[rows, h * G:(h + 1) * G].transpose(0, 1)  # [G, n, 128]
+            s = (scale * (x @ keys[:, h].T)).masked_fill(hidden, -torch.inf)
+            d = (abs(scale) * 131 * 2.0 ** -24 * (x.abs() @ keys[:, h].abs().T)) \
+                .masked_fill(hidden, 0.0).amax(-1)
+            l = torch.logsumexp(s, -1)
+            p = torch.exp(s - torch.where(l.isfinite(), l, 0.0)[..., None])
+            v, m = values[:, h], (~hidden).sum(-1).double()[:, None]
+            o = p @ v
+            big = (p * size[:, h]).amax(-1, keepdim=True)
+            rel = (2.0 ** -11 + 2.0 ** -18 if doc else 2.0 ** -16) + m * 2.0 ** -23 + 2.0 ** -20 + \
+                2 * d[..., None]
+            lost = 2.0 ** -31 * big if doc else 2.0 ** (-62 if size.max() > 2.0 ** 60 else -126)
+            t = 2.0 ** -8 * o.abs() + rel * (p @ v.abs()) + m * 448 * lost + 2.0 ** -134
+            where = (rows, slice(h * G, (h + 1) * G))
+            out[where], tol[where] = o.transpose(0, 1), t.transpose(0, 1)
+            sq[where] = ((p * p) @ (v * v)).transpose(0, 1)
+            lse[where] = l.T
+            lt[where] = (d + m[:, 0] * 2.0 ** -24 + (2.0 ** -18 if doc else 0) +
+                         2.0 ** -21 * (1 + l.abs())).T
+    # what bf16 rounds to infinity
+    out = torch.where(out.abs() >= 2.0 ** 128 * (1 - 2.0 ** -9), out.sign() * torch.inf, out)
+    return out, lse, tol, lt, sq
+
+
+def _check_sequences(pool, counts, G, scale=128 ** -0.5, seed=0, size=1.0, q=None):
+    T, Hq = sum(counts), pool.H * G
+    if q is None:
+        q = (torch.randn(T, Hq, 128, generator=torch.Generator().manual_seed(seed)) * size).to(BF)
+    out = torch.full((T, Hq * 128), -7.0, dtype=BF, device="cuda")
+    lse, cu = torch.full((T, Hq), -7.0, device="cuda"), _cu(counts)
+    kda.kda_cache_attention(q.reshape(T, -1).cuda(), out, *pool.gpu(), cu_seqlens_host=cu,
+                            cu_seqlens=cu.cuda(), lse=lse, scale=scale)
+    want, wl, tol, lt, sq = _ref_sequences(pool, q.double(), counts, G, scale)
+    out = out.reshape(T, Hq, 128)
+    _close(out, want, tol)
+    _close(lse, wl, lt)
+    return out, want, sq
+
+
+def _scale_values(pool, choices, seed):
+    """Each page and head's values under one of these scales."""
+    g = torch.Generator().manual_seed(seed)
+    which = torch.randint(0, len(choices), (pool.N, pool.H), generator=g)
+    pool.scale[1] = torch.tensor(choices)[which]
+    return pool
+
+
+def _positive_values(pool):
+    c = pool.raw[1]
+    pool.raw[1] = c & 127 if pool.kind == F8 else c.view(I8).abs().view(torch.uint8)
+    return pool
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("totals", [[90, 700, 6], [3000, 40, 900, 2500]])
+def test_attention_of_few_rows_large_values(lib, kind, T, totals):
+    """Values up to 2^126, whose sums pass fp32's range though their averages do not, alone and
+    beside ordinary ones, whole and in parts."""
+    big = 2.0 ** (118 if kind == F8 else 119)
+    for i, choices in enumerate(([big], [big, 2.0 ** -7], [big, 2.0 ** 61, 2.0 ** 60, 2.0 ** 59])):
+        pool = _positive_values(Pool(kind, 2, 16, totals, seed=80).fill())
+        _scale_values(pool, choices, 81 + i)
+        _check_sequences(pool, [T] * len(totals), 2, seed=82)
