@@ -3,20 +3,22 @@
 // Bound by the matrix units: 4 * 128 operations for every visible (query row, key) pair. Row r of
 // a document and key/value head is query head r mod G of token r / G, so that grouped heads
 // share what is loaded. A workgroup takes 32 rows per wave and walks 64 keys at a time: their
-// codes are widened to bf16 once for all its waves, into LDS (exact for the values' scales that
-// kda_cache_write makes; the keys' scales multiply the scores), the values transposed on the way.
-// The next tile's codes come in meanwhile, and two workgroups share a CU, so that one's exponentials
-// run beside the other's products.
+// codes are widened once for all its waves, into LDS, exactly (keys to bf16, values to fp16), the
+// values transposed on the way. The next tile's codes come in meanwhile, and two workgroups share a
+// CU, so that one's exponentials run beside the other's products.
 //
 // With keys as the rows of the products (S^T = K Q^T, O^T = V^T P^T) all of a lane's scores and
 // outputs belong to one query row, and the weights P^T leave the first product in the
-// layout that the second one reads. They are rounded to bf16 there (the sum that divides them is
-// not): errors of half a step, independent of one another, that leave the output about as far off
-// as its own rounding does; a second part would cost half as many products again.
+// layout that the second one reads. A page's scales go to the scores and to the weights, there as
+// log2 before the exponential, so that weight times scale is what the running maximum bounds: it
+// fits fp16 whatever the scales, and the codes of the values do, too. fp16 rounds a weight by 2^-11
+// at most, independently of others, which adds about 1 % to what rounding the output to bf16 leaves (root
+// of the mean square; one bf16 part, at the same rate of products, added 41 % and took 1.37 ms
+// instead of 1.40 in the first case below). The sum that divides is not rounded.
 //
-// Documents of 4096 and 1777 tokens behind 2000 to 12000, 64 query heads on 8: 1.38 ms, 965 TFLOP/s
-// of the 1605 that a large library product reaches; 14 documents of 16384 tokens, 12 heads on 4:
-// 161 us, 707. Matrix instructions take 45 % of a SIMD's cycles, vector instructions 41 %.
+// Documents of 4096 and 1777 tokens behind 2000 to 12000, 64 query heads on 8: 1.40 to 1.46 ms on
+// different cards, 917 to 951 TFLOP/s of the 1605 that a large library product reaches; 14 documents of
+// 16384 tokens, 12 heads on 4, int8: 161 to 165 us, 706 to 689.
 
 #include <math.h>
 
@@ -28,28 +30,40 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;   // keys
-constexpr float kSlack = 8.0f;
+// Weights of the second product lie below 2^kSlack, the largest that a row has seen at 2^(kTop - 1)
+// at least: fp16 rounds them by 2^-11 down to 2^-20 of that one, and by 2^-31 of it below.
+constexpr float kTop = 7.0f, kSlack = 15.0f;
 constexpr float kNoRef = -3.0e38f;
+constexpr int32_t kWide = 40, kWideTile = 64;  // see `apart`
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __fp16 f16x8 __attribute__((__vector_size__(8 * sizeof(__fp16))));  // MFMA operand
+
+// What a tile's groups of 16 tokens have in LDS: the keys' scale times the scores', log2 of the
+// values' (of its magnitude), the reciprocal of that magnitude, and, as an integer, how many of the
+// tokens exist (kWideTile less: see `apart`).
+constexpr int kKeyScale = 0, kValueLog = 1, kValueInv = 2, kLive = 3, kGroupKinds = 4;
 
 struct Smem {
+  alignas(16) float group[2][kGroupKinds][4];  // of 16 tokens each
   // chunk c < 8 of a key's row: channels 16 c .., c >= 8: channels 16 (c - 8) + 8 ..; at
   // c ^ (key & 15): no bank conflicts
   u32x4 k[2][kTile * 16];
   // a channel's row: tokens of each run of 16 in the order 0-3, 8-11, 4-7, 12-15, chunks of 8 at
   // c ^ swizzle(channel)
   u32x2 v[2][D * kTile / 4];
-  float ks[2][4];      // the keys' scales, 16 tokens each
-  int32_t live[2][4];  // tokens of each 16 that exist
   // the first position behind what every row sees that holds a NaN value
   int32_t nan_at[D];
+  float ref_apart[kDocRows], tot_apart[kDocRows][2];  // see `apart`
   FindSmem find;
 };
 __device__ __forceinline__ int swizzle(int channel) { return (channel ^ (channel >> 3)) & 7; }
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
 // A wave brings in 16 tokens of a tile, which lie in one page: their bytes are a scalar base and
@@ -88,18 +102,25 @@ __device__ __forceinline__ void load_share(const AttnParams& p, int32_t raw, int
   s.live = is ? min(16, end - tok) : 0;
 }
 
-// Widened values of four tokens of one channel, times their scale (EXACT: a power of two).
-template <int KIND, bool EXACT>
-__device__ __forceinline__ u32x2 scaled4(uint32_t w, float scale) {
-  if constexpr (EXACT) {
+// Four codes as two fp16 pairs, exact. int8: 0x6400 | b is 1024 + b.
+template <int KIND>
+__device__ __forceinline__ u32x2 widen4_f16(uint32_t w) {
+  if constexpr (KIND == kFp8) {
     return u32x2{
-        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false)),
-        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true))};
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))};
   } else {
-    float x[4];
-    decode4<KIND>(w, x);
-    return u32x2{pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale)};
+    const f16x2 off = {_Float16(1152), _Float16(1152)};
+    w ^= 0x80808080u;
+    const f16x2 a = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u));
+    const f16x2 b = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u));
+    return u32x2{__builtin_bit_cast(uint32_t, a - off), __builtin_bit_cast(uint32_t, b - off)};
   }
+}
+// log2 of a scale: a whole number for a power of two, -infinity for zero.
+__device__ __forceinline__ float log2_of(float x) {
+  return float(__builtin_amdgcn_frexp_expf(x)) +
+         __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(x));
 }
 
 // To LDS. Tokens that do not exist become zeros. With `diagonal`, so do NaN codes, which leave
@@ -107,7 +128,7 @@ __device__ __forceinline__ u32x2 scaled4(uint32_t w, float scale) {
 // 0 NaN.
 template <int KIND>
 __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_t tok, bool diagonal,
-                                            int slot, Smem& lds) {
+                                            int slot, float scale2, Smem& lds) {
   const int c0 = (lane & 7) ^ (lane >> 3);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -117,10 +138,6 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
     const u32x2 d = widen4<KIND>(s.k[i][2]), e = widen4<KIND>(s.k[i][3]);
     lds.k[slot][row * 16 + (c0 ^ 8 * i)] = u32x4{a[0], a[1], b[0], b[1]};
     lds.k[slot][row * 16 + (c0 ^ 8 * (1 - i))] = u32x4{d[0], d[1], e[0], e[1]};
-  }
-  if (lane == 0) {
-    lds.ks[slot][wave] = s.ks;
-    lds.live[slot][wave] = s.live;
   }
   const int ch = lane_channel(lane);
 #pragma unroll
@@ -140,12 +157,27 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
           s.v[r][j] &= ~note_nans(hit, lds.nan_at + ch + 4 * j, tok + lane_token(lane) + r);
       }
   }
-  float scale =
-      __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, s.vs)));
-  if (s.live == 0) scale = 1.0f;
+  // the scale's magnitude goes to the weights, its sign to the codes
+  const uint32_t all = __builtin_amdgcn_readfirstlane(__float_as_int(s.vs));
+  const uint32_t bits = s.live == 0 ? 0x3f800000u : all & 0x7fffffffu;
+  const int32_t exponent = int32_t(bits >> 23) - 127;
+  float lg = float(exponent), inv = __uint_as_float(0x7f000000u - bits);
+  if ((bits & 0x007fffffu) != 0 || bits == 0) {  // no power of two
+    asm volatile("");                            // (a branch, not a choice)
+    lg = log2_of(__uint_as_float(bits));
+    inv = __builtin_amdgcn_rcpf(__uint_as_float(bits));
+  }
+  if (lane == 0) {
+    float* const to = &lds.group[slot][0][wave];
+    to[4 * kKeyScale] = scale2 * s.ks;
+    to[4 * kValueLog] = lg;
+    to[4 * kValueInv] = inv;
+    to[4 * kLive] = __int_as_float(abs(exponent) > kWide ? s.live - kWideTile : s.live);
+  }
   // quad q of 16 tokens goes to place 0, 2, 1, 3
   const int place = wave * 4 + ((lane >> 5) << 1 | (lane & 1));
-  const auto put = [&](auto exact) {
+  const auto put = [&](auto negative) {
+    constexpr uint32_t kSigns = decltype(negative)::value ? 0x80008000u : 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t w[4];
@@ -154,12 +186,11 @@ __device__ __forceinline__ void store_share(Share& s, int wave, int lane, int32_
       for (int c = 0; c < 4; ++c) {
         const int channel = ch + 4 * j + c;
         lds.v[slot][channel * 16 + ((((place >> 1) ^ swizzle(channel)) << 1) | (place & 1))] =
-            scaled4<KIND, decltype(exact)::value>(w[c], scale);
+            widen4_f16<KIND>(w[c]) ^ kSigns;
       }
     }
   };
-  // the conversion's own scale is a power of two
-  if (KIND == kFp8 && (__float_as_uint(scale) & 0x007fffffu) == 0 && scale > 0.0f)
+  if (int32_t(all) < 0 && s.live > 0)
     put(std::true_type());
   else
     put(std::false_type());
@@ -239,7 +270,17 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[c][i] = 0.0f;
-  float ref = kNoRef, tot = 0.0f;
+  // Weights of the second product are 2^(score + vlog - ref), whatever the pages' scales; `tot`, the
+  // weights' sum without the scales, is counted in 2^ref too, by vinv. References are whole numbers
+  // that move when a weight passes 2^slack (by anything at first).
+  float ref = 0.0f, slack = -INFINITY, tot = 0.0f;
+  // Where a scale is zero or beyond 2^+-kWide (a page of zeros has 2^-100), the weights with and without
+  // the scales may be too far apart for one reference in fp32 (up to there, what is flushed to zero is
+  // less than 2^-50 of `tot`): from that tile on, which goes the way of masked ones, the wave counts
+  // `tot` in a reference of its own, in LDS.
+  int32_t apart = 16;  // < 0: so it is
+  float& ref_apart = lds.ref_apart[wave * 32 + m];
+  float& tot_apart = lds.tot_apart[wave * 32 + m][hi];
 
   // the wave's tokens of a tile; what is stored next, and the page of what is loaded after it
   const int32_t mine = begin + 16 * wave;
@@ -252,7 +293,8 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
     page = load_page(p, part.b, mine + kTile, end, zero);
   }
   __syncthreads();  // nan_at
-  if (tiles > 0) store_share<KIND>(share, wave, lane, mine, begin + kTile - 1 > all_see, 0, lds);
+  if (tiles > 0)
+    store_share<KIND>(share, wave, lane, mine, begin + kTile - 1 > all_see, 0, p.scale2, lds);
   __syncthreads();
   for (int32_t t = 0; t < tiles; ++t) {
     const int32_t at = begin + t * kTile, tok_next = mine + (t + 1) * kTile;
@@ -262,7 +304,7 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
     page = load_page(p, part.b, tok_next + kTile, end, zero);
     if (at <= wave_most) {
       f32x16 s[2];
-      bf16x8 w[4];
+      f16x8 w[4];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -276,11 +318,12 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
         }
       reads_ahead();
       float f[4];
-      int32_t live = INT_MAX;
+      f32x4 c = *reinterpret_cast<const f32x4*>(lds.group[slot][kValueLog]);
+      int32_t live = apart;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[i] = p.scale2 * lds.ks[slot][i];
-        live = min(live, lds.live[slot][i]);
+        f[i] = lds.group[slot][kKeyScale][i];
+        live = min(live, __float_as_int(lds.group[slot][kLive][i]));
       }
       if (live < 16 || at + kTile - 1 > wave_all) {
 #pragma unroll
@@ -289,69 +332,101 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
           for (int i = 0; i < 16; ++i) {
             const int in = 8 * (i >> 2) + 4 * hi + (i & 3);  // key of 32
             const int group = 2 * u + (i >> 3);
-            const bool hidden = (in & 15) >= lds.live[slot][group] || at + 32 * u + in > last;
+            const bool hidden =
+                (in & 15) >= (__float_as_int(lds.group[slot][kLive][group]) & 31) ||
+                at + 32 * u + in > last;
             s[u][i] = hidden ? -INFINITY : s[u][i] * f[group];
           }
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = 1.0f;
+        if (__builtin_amdgcn_readfirstlane(live) < 0) {
+          const float was = apart < 0 ? ref_apart : slack == -INFINITY ? kNoRef : ref;
+          float now = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) now = fmaxf(now, s[u][i]);
+          now = fmaxf(was, ceilf(fmaxf(now, __shfl_xor(now, 32))) - kTop);
+          float sum = apart < 0 ? tot_apart : tot;
+          if (now != was) sum *= __builtin_amdgcn_exp2f(was - now);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum += __builtin_amdgcn_exp2f(s[u][i] - now);
+          tot_apart = sum;
+          ref_apart = now;
+          apart = -1;
+        }
       }
-      float x[2][16], top = -INFINITY;
+      const f32x4 by = *reinterpret_cast<const f32x4*>(lds.group[slot][kValueInv]);
+      c -= ref;
+      float top = -INFINITY;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          x[u][i] = fmaf(s[u][i], f[2 * u + (i >> 3)], -ref);
-          top = fmaxf(top, x[u][i]);
+          s[u][i] = fmaf(s[u][i], f[2 * u + (i >> 3)], c[2 * u + (i >> 3)]);
+          top = fmaxf(top, s[u][i]);
         }
-      if (__any(top > kSlack)) {
-        float now = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) now = fmaxf(now, s[u][i] * f[2 * u + (i >> 3)]);
-        now = fmaxf(ref, fmaxf(now, __shfl_xor(now, 32)));
-        const float down = now == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - now);
-        ref = now;
+      if (__any(top > slack)) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float over = top > slack ? ceilf(top) - kTop : 0.0f;
+        const float down = slack == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(-over);
+        ref += over;
+        if (top > slack) slack = kSlack;
         tot *= down;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] *= down;
+        for (int i = 0; i < 4; ++i) o[i] *= down;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[u][i] = fmaf(s[u][i], f[2 * u + (i >> 3)], -ref);
+          for (int i = 0; i < 16; ++i) s[u][i] -= over;
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         uint32_t pk[4];
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int at8 = 8 * (g & 1) + 2 * i;
-          const float a = __builtin_amdgcn_exp2f(x[g >> 1][at8]);
-          const float b = __builtin_amdgcn_exp2f(x[g >> 1][at8 + 1]);
-          tot += a + b;
-          pk[i] = pack_bf16x2(a, b);
+          const float a = __builtin_amdgcn_exp2f(s[g >> 1][at8]);
+          const float b = __builtin_amdgcn_exp2f(s[g >> 1][at8 + 1]);
+          sum = i == 0 ? a + b : sum + (a + b);
+          pk[i] = pack_f16x2(a, b);
         }
-        w[g] = __builtin_bit_cast(bf16x8, u32x4{pk[0], pk[1], pk[2], pk[3]});
+        tot = fmaf(sum, by[g], tot);
+        w[g] = __builtin_bit_cast(f16x8, u32x4{pk[0], pk[1], pk[2], pk[3]});
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const u32x4 v = values_at[g ^ 2 * (c & 1)][slot * (D * kTile / 8) + c * (32 * kTile / 8)];
-          o[c] = mfma(__builtin_bit_cast(bf16x8, v), w[g], o[c]);
+          o[c] = mfma(__builtin_bit_cast(f16x8, v), w[g], o[c]);
         }
       reads_ahead();
     }
     if (t + 1 < tiles)
-      store_share<KIND>(share, wave, lane, tok_next, at + 2 * kTile - 1 > all_see, slot ^ 1, lds);
+      store_share<KIND>(share, wave, lane, tok_next, at + 2 * kTile - 1 > all_see, slot ^ 1,
+                        p.scale2, lds);
     __syncthreads();
   }
 
   if (SPLIT) list_cuts(p, h, lds.find);
+  if (apart < 0) tot = tot_apart;
   tot += __shfl_xor(tot, 32);
   if (r >= rows) return;
   const bool whole = !SPLIT || part.parts == 1;
-  const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+  float inv = tot == 0.0f ? 0.0f : 1.0f / tot, ref_sum = ref;
+  if (apart < 0) {
+    ref_sum = ref_apart;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        o[c][i] = __builtin_amdgcn_ldexpf(o[c][i] * inv, int(ref - ref_sum));
+    inv = 1.0f;
+  }
   uint16_t* const dst = p.out + (seq.first + tok) * p.out_stride + head * D;
   const int64_t slot = (int64_t(part.slot) * p.c.H + h) * ROWS + wave * 32 + m;
   typedef u32x2 u32x2_u __attribute__((aligned(2)));
@@ -374,10 +449,10 @@ __global__ __launch_bounds__(kThreads, 2) void document_kernel(AttnParams p) {
     }
   if (hi != 0) return;
   if (!whole)
-    p.stat[slot] = make_float2(tot == 0.0f ? -INFINITY : ref, tot);
+    p.stat[slot] = make_float2(tot == 0.0f ? -INFINITY : ref_sum, tot);
   else if (p.lse)
     p.lse[(seq.first + tok) * p.lse_stride + head] =
-        log_sum(ref, tot);
+        log_sum(ref_sum, tot);
 }
 
 template <int KIND, bool SPLIT, bool LISTED>

@@ -139,10 +139,10 @@ size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t total_tokens, 
  * Token i of sequence b sees the keys at positions 0 .. kv_lens[b] - n_b + i:
  *   s_j = scale q . k_j,  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j
  * with fp32 sums and maxima, and products of exact q and codes. The weights exp(s_j - ref)
- * keep 16 significant bits where a sequence has at most 128 query rows per key/value
- * head (n_b * H_q / H_kv); with more rows they are rounded to bf16, as are values whose
- * page has a scale that is no power of two. A token that sees no key has out = 0 and
- * lse = -infinity. The cache has to hold the call's own tokens (kda_cache_write).
+ * are off by 2^-16 of themselves at most where a sequence has at most 128 query rows per
+ * key/value head (n_b * H_q / H_kv); with more rows, multiplied by the values' scale, they are
+ * rounded to fp16: by 2^-11 of themselves, or 2^-31 of the largest such product that a row has
+ * seen. A token that sees no key has out = 0 and lse = -infinity. The cache has to hold the call's own tokens (kda_cache_write).
  * Values may be of any size with code * scale below 2^128: no sum leaves fp32's range, and
  * out is infinite only where the definition's value rounds to infinity in bf16. Scores have to
  * stay inside fp32's range, as sums of |q| |code| and multiplied by scale * log2(e) and the

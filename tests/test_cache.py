@@ -1291,3 +1291,88 @@ def test_attention_of_few_rows_large_values(lib, kind, T, totals):
         pool = _positive_values(Pool(kind, 2, 16, totals, seed=80).fill())
         _scale_values(pool, choices, 81 + i)
         _check_sequences(pool, [T] * len(totals), 2, seed=82)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("H,counts,past", [(2, [150, 260], [37, 900]), (64, [130, 259, 190], [0, 70, 12])])
+def test_attention_document_weights_keep_11_bits(lib, kind, H, counts, past):
+    """Half a step of fp16 is all that a weight is off, in each output and on the average, cut (2 heads)
+    and whole. The mean square of an output's rounding to bf16 is a third of its half step's square; the
+    weights' errors, independent of one another, add a third of 2^-22 sum (p v)^2 at most, less than
+    3 % where values are independent of one another. (Half a step of bf16, 2^-8, would make it about
+    twice as large.) Rows' weights are shared by their 128 channels: a few hundred of them leave the mean
+    within 10 %."""
+    for P in (16, 64):
+        pool = Pool(kind, H, P, [a + b for a, b in zip(counts, past)], seed=83).fill()
+        G = 2 if H == 2 else 1
+        got, want, sq = _check_sequences(pool, counts, G, seed=84)
+        got = got.double().cpu()
+        step = torch.exp2(torch.floor(torch.log2(want.abs())) - 8)
+        expected = ((step * step + 2.0 ** -22 * sq) / 3).sum()
+        assert ((got - want) ** 2).sum() <= 1.1 * expected
+
+
+WIDE = [0.0, 2.0 ** -100, 2.0 ** -41, 2.0 ** -40, 1.37 * 2.0 ** -3, -2.0 ** -5, 2.0 ** 40, 2.0 ** 41,
+        1.9 * 2.0 ** 40, 2.0 ** 60, 2.0 ** 61, 2.0 ** 90, 2.0 ** -140]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("counts,past", [([150, 300], [37, 900]), ([1, 8, 1], [3000, 90, 10]),
+                                         ([140], [5000])])
+@pytest.mark.parametrize("choices", [WIDE, WIDE[:3], WIDE[4:6], [2.0 ** -100], [2.0 ** 116],
+                                     [2.0 ** -100, 2.0 ** -7], [2.0 ** -100, 2.0 ** 100],
+                                     [2.0 ** -40, 2.0 ** 40]])
+def test_attention_scales_far_apart(lib, kind, P, counts, past, choices):
+    """Pages whose values are far larger or smaller than others', for documents, cut and whole, and few
+    rows; scores that are even, and scores that pick the keys of a few pages."""
+    for i, size in enumerate((1.0, 8.0)):
+        pool = Pool(kind, 2, P, [a + b for a, b in zip(counts, past)], seed=85).fill()
+        _scale_values(pool, choices, 86 + i)
+        _check_sequences(pool, counts, 2, seed=87, size=size)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("H,counts,past", [(2, [150], [37]), (64, [130, 259, 190], [0, 70, 12]),
+                                           (1, [140], [3000])])
+def test_attention_documents_large_values(lib, kind, H, counts, past):
+    """Values up to 2^126, whose sums pass fp32's range though their averages do not; and the code
+    that stands for 2^128, which the largest bf16 values are written as: rows that do not see it are as
+    if it were not there."""
+    big = 2.0 ** (118 if kind == F8 else 119)
+    pool = _positive_values(Pool(kind, H, 16, [a + b for a, b in zip(counts, past)], seed=88).fill())
+    _scale_values(pool, [big, 2.0 ** -7], 89)
+    _check_sequences(pool, counts, 1, seed=90)
+    for b, n in enumerate(counts):
+        at = past[b] + n // 2
+        page = pool.table[b, at // 16]
+        c = pool.codes(pool.raw)[1]
+        c[page, :, at % 16, 7] = 0x78 if kind == F8 else 64
+        pool.scale[1][page] = 2.0 ** (120 if kind == F8 else 122)
+        c[page, :, at % 16 + 1:] = 0
+        c[page, :, :at % 16] = 0
+    _check_sequences(pool, counts, 1, seed=91)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("down", [18, 24, 28])
+@pytest.mark.parametrize("H", [1, 300])
+def test_attention_documents_small_weights(lib, kind, down, H):
+    """One key of weight 1 whose values are zeros, before 4000 of 2^-down with the largest values: fp16's
+    subnormal numbers, whose sum is all there is. Cut (one head) and whole."""
+    n, total = (140, 4000) if H == 1 else (129, 700)
+    pool = Pool(kind, H, 64, [total], seed=92).fill()
+    for side in range(2):
+        pool.codes(pool.raw)[side][:] = 0
+        pool.scale[side][:] = 2.0 ** -6
+    page = pool.table[0, 0]
+    pool.codes(pool.raw)[0][page, :, 0, 0] = torch.tensor([64.0]).to(kind).view(torch.uint8)
+    pool.codes(pool.raw)[1][:] = 0x7e if kind == F8 else 127
+    pool.codes(pool.raw)[1][page, :, 0] = 0
+    q = torch.zeros(n, H, 128)
+    q[:, :, 0] = down * 0.6931471805599453
+    _check_sequences(pool, [n], 1, scale=1.0, q=q.to(BF))
