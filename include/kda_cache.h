@@ -16,8 +16,9 @@
  *  - KDA_CACHE_INT8: signed integers from -127 to 127.
  * The scales that kda_cache_write makes are powers of two, so that dividing by one
  * is exact, the values read back are exact in bf16, and an e4m3 value keeps its
- * relative step whatever the scale. kda_cache_read and kda_cache_attention take any
- * finite scale.
+ * relative step whatever the scale. (The largest bf16 values, from 3.3e38 on, round to
+ * a code that stands for 2^128: it reads back as infinity.) kda_cache_read and
+ * kda_cache_attention take any finite scale.
  *
  * Sequences. Sequence b has kv_lens[b] tokens, those of this call included; token
  * position i lies in slot i mod page_size of page page_table[b * table_row_stride +
@@ -103,7 +104,8 @@ kda_status kda_cache_write(int32_t n_seqs, int64_t total_tokens, int32_t H, int3
  * kda_cache_read -- the last n_b tokens of each sequence in bf16 (with cu_seqlens
  * and kv_lens of its first m tokens, any range of them).
  *
- *  k, v               bf16 [total_tokens, H * 128] out: code * scale, rounded once
+ *  k, v               bf16 [total_tokens, H * 128] out: code * scale in fp32, rounded to
+ *                     bf16 (the product is exact where the scale is a power of two)
  */
 kda_status kda_cache_read(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t D,
                           const int32_t* cu_seqlens,

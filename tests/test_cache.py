@@ -1376,3 +1376,38 @@ def test_attention_documents_small_weights(lib, kind, down, H):
     q = torch.zeros(n, H, 128)
     q[:, :, 0] = down * 0.6931471805599453
     _check_sequences(pool, [n], 1, scale=1.0, q=q.to(BF))
+
+
+# ---------------------------------------------------------------------------
+# reading under any scale
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_read_behind_odd_scales(lib, kind):
+    """The product is rounded to fp32, then to bf16: 15 * 9542042 lies between two fp32 numbers, the
+    lower of which is a tie in bf16. Negative, zero, tiny and huge scales; a code that stands for 2^128
+    is infinity."""
+    choices = [9542042.0, 0.1, -3.7, 0.0, 1e-38, 3e-42, 7.3e36, 2.0 ** 120, -1.0 / 3.0]
+    pool = Pool(kind, 3, 16, [150, 33], seed=95).fill()
+    g = torch.Generator().manual_seed(96)
+    for side in range(2):
+        which = torch.randint(0, len(choices), (pool.N, 3), generator=g)
+        which[pool.table[0, :3]] = 0
+        which[pool.table[0, 3:5]] = 7
+        pool.scale[side] = torch.tensor(choices)[which]
+        c = pool.codes(pool.raw)[side]
+        c[pool.table[0, 0], :, 3, 5] = torch.tensor([15.0]).to(kind).view(torch.uint8)
+        c[pool.table[0, 3], :, 3, 5] = 0x78 if kind == F8 else 127
+    got = [torch.full((183, 3 * 128), -7.0, dtype=BF, device="cuda") for _ in range(2)]
+    kda.kda_cache_read(*got, *pool.gpu(), cu_seqlens=_cu([150, 33]).cuda())
+    for side in range(2):
+        at, c = 0, pool.codes(pool.raw)[side]
+        for b, n in ((0, 150), (1, 33)):
+            for i in range(n):
+                page = pool.table[b, i // 16]
+                code = _value(c[page, :, i % 16].contiguous().view(kind), kind).float()
+                want = (code * pool.scale[side][page][:, None]).to(BF).reshape(-1)
+                assert torch.equal(got[side][at].cpu(), want)
+                at += 1
+        if kind == F8:
+            assert got[side].float()[3 * 16 + 3, 5] == torch.inf
