@@ -337,10 +337,15 @@ hipError_t launch_write(const WriteParams& p, unsigned items, hipStream_t stream
   const int P = 1 << p.c.page_shift;
   const int most = p.c.cu ? P : (p.c.per_seq < P ? p.c.per_seq : P);
   const dim3 few(items, (p.c.H + 3) / 4), grid(items, 2 * p.c.H), block(kThreads);
-  // Sequences of at most 16 tokens on the average: most pages get a few. (8 heads, pages of 64 |
-  // 256, against a workgroup per side: 1024 single tokens 12 us against 41 | 14.5 against 57, beside a
-  // document of 960 tokens 19 against 42 | 35 against 58; 64 of them beside it 12.4 against 11.1.)
-  if (p.c.cu && most > 16 && p.c.total <= 16 * int64_t(p.c.n_seqs)) {
+  // Sequences of at most 16 tokens on the average: most pages get a few. A workgroup for each side of
+  // these has little to do, but one that walks a long page of four heads takes 12 us (24 of 256
+  // tokens), so that there have to be many (kernels alone, pages of 64 | 256, 8 heads, us, a workgroup
+  // per side against this: 64 sequences, a document of 960 tokens among them, 6.4 against 11.9 | 8.0
+  // against 24.3; 256 of them 13.7 against 12.8 | 21.5 against 24.7; 512: 23.8 against 14.5 | 31.6
+  // against 27.8; 1024 sequences, of which one has 16384 tokens and the others none, 36.6 against
+  // 23.3 | 36.0 against 37.8).
+  if (p.c.cu && most > 16 && p.c.total <= 16 * int64_t(p.c.n_seqs) &&
+      int64_t(p.c.n_seqs) * p.c.H >= (P > 128 ? 4096 : 2048)) {
     if (most <= 64)
       hipLaunchKernelGGL((write_mixed_kernel<KIND, 4>), few, block, 0, stream, p);
     else

@@ -1411,3 +1411,25 @@ def test_read_behind_odd_scales(lib, kind):
                 at += 1
         if kind == F8:
             assert got[side].float()[3 * 16 + 3, 5] == torch.inf
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [32, 64, 128, 256])
+def test_many_single_tokens_beside_documents_written(lib, kind, P):
+    """520 sequences of 8 heads: single tokens, drafts, empty ones and documents, behind earlier tokens
+    and not; NaN and infinities among them."""
+    g = torch.Generator().manual_seed(P)
+    n, H = 520, 8
+    counts = [1] * n
+    past = torch.randint(0, 40, (n,), generator=g).tolist()
+    for b, c in ((0, 0), (3, 17), (64, 8), (65, 300), (130, 16), (200, 0), (255, 70), (256, 33),
+                 (400, 600), (519, 90)):
+        counts[b] = c
+    past[65], past[400] = 2 * P - 3, P
+    pool = Pool(kind, H, P, [a + b for a, b in zip(counts, past)], seed=97, pad=16).fill(past)
+    pool.lens[5], pool.lens[130] = 0, pool.cap() + 1
+    T = sum(counts)
+    k, v = _tokens(T, H, g), _tokens(T, H, g)
+    k[40, 3, 7], v[100, 5, 0], v[300, 1, 1] = torch.nan, torch.inf, -torch.inf
+    _check_write(pool, k, v, counts, False, pad=6, offset=3)
