@@ -1433,3 +1433,115 @@ def test_many_single_tokens_beside_documents_written(lib, kind, P):
     k, v = _tokens(T, H, g), _tokens(T, H, g)
     k[40, 3, 7], v[100, 5, 0], v[300, 1, 1] = torch.nan, torch.inf, -torch.inf
     _check_write(pool, k, v, counts, False, pad=6, offset=3)
+
+
+# ---------------------------------------------------------------------------
+# every instance of the attention kernels, each sequence to its own tolerance
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [513, 1100])
+@pytest.mark.parametrize("H,G,T", [(1, 1, 1), (2, 3, 1), (1, 8, 3)])
+def test_attention_of_more_than_512_sequences(lib, kind, n, H, G, T):
+    """Single tokens and drafts, one and two blocks of rows, most caches short and a few cut."""
+    g = torch.Generator().manual_seed(n + H)
+    totals = torch.randint(T, 40, (n,), generator=g).tolist()
+    totals[5], totals[n - 1], totals[n // 2] = 2500, 1030, 700
+    pool = Pool(kind, H, 16, totals, seed=100).fill()
+    _check_sequences(pool, [T] * n, G, seed=101)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [290, 1300])
+@pytest.mark.parametrize("H", [2, 96])
+def test_attention_of_mixed_batches_by_sequences(lib, kind, n, H):
+    """Single tokens, drafts of several blocks and documents, cut (2 heads) and whole."""
+    g = torch.Generator().manual_seed(102)
+    counts = [1] * n
+    totals = torch.randint(1, 30, (n,), generator=g).tolist()
+    for b, m, total in ((3, 45, 2200), (70, 1, 2600), (71, 150, 1700), (140, 0, 1500),
+                        (200, 100, 1300), (255, 260, 1400), (256, 129, 129), (n - 1, 1, 1100)):
+        counts[b], totals[b] = m, total if H == 2 else min(total, m + 300)
+    pool = Pool(kind, H, 32, totals, seed=103).fill()
+    _check_sequences(pool, counts, 1, seed=104)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G", [17, 32, 33, 64, 128, 129, 256])
+@pytest.mark.parametrize("T", [1, 2])
+def test_attention_of_large_groups(lib, kind, G, T):
+    """Up to 256 query heads of a key/value head: single tokens are several blocks, and documents."""
+    totals = [T, 40, 333, 2600, 5]
+    pool = Pool(kind, 2, 32, totals, seed=105).fill()
+    _check_sequences(pool, [T] * 5, G, seed=106)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [513, 5000])
+@pytest.mark.parametrize("H", [2, 128])
+def test_attention_few_int8_of_many_sequences(lib, n, H):
+    """The bits of a few sequences do not depend on a thousand without tokens beside them."""
+    at, counts, totals = [7, 400, n - 20, n - 1], [1, 3, 200, 330], [300, 40, 1200, 333]
+    pool = Pool(I8, H, 32, totals, seed=107).fill()
+    T = sum(counts)
+    q = torch.randn(T, H * 128, generator=torch.Generator().manual_seed(108)).to(BF).cuda()
+    cache = pool.gpu()
+    table = torch.full((n, pool.width), -1, dtype=I32, device="cuda")
+    lens, many = torch.zeros(n, dtype=I32, device="cuda"), [0] * n
+    for i, b in enumerate(at):
+        table[b], lens[b], many[b] = cache[4][i], cache[5][i], counts[i]
+    got = []
+    for c, cu in (((*cache[:4], table, lens), _cu(many)), (cache, _cu(counts))):
+        out = torch.full((T, H * 128), -7.0, dtype=BF, device="cuda")
+        lse = torch.full((T, H), -7.0, device="cuda")
+        kda.kda_cache_attention(q, out, *c, cu_seqlens_host=cu, cu_seqlens=cu.cuda(), lse=lse)
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert got[0][0].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,total", [(1, 5000), (8, 3000), (150, 200), (150, 4000)])
+@pytest.mark.parametrize("what", [0, 1])
+def test_attention_nan_through_parts(lib, T, total, what):
+    """A NaN key or value, early, in the middle and among the call's own tokens, in whole and in joined
+    blocks: NaN in exactly the rows that see it (and, for a value, its channel)."""
+    for at in (3, total // 2, total - 1 - T // 2):
+        pool = Pool(F8, 1, 64, [total, 40], seed=109).fill()
+        pool.codes(pool.raw)[what][pool.table[0, at // 64], 0, at % 64, 5] = 0xff
+        q = torch.randn(T + 1, 256, generator=torch.Generator().manual_seed(110)).to(BF).cuda()
+        out, lse = torch.empty_like(q), torch.empty(T + 1, 2, device="cuda")
+        cu = _cu([T, 1])
+        kda.kda_cache_attention(q, out, *pool.gpu(), cu_seqlens_host=cu, cu_seqlens=cu.cuda(), lse=lse)
+        sees = torch.zeros(T + 1, 2, 128, dtype=torch.bool)
+        sees[:T][torch.arange(total - T, total) >= at] = True
+        if what:
+            sees[:, :, :5] = False
+            sees[:, :, 6:] = False
+        assert torch.equal(out.isnan().cpu().reshape(T + 1, 2, 128), sees)
+        assert torch.equal(lse.isnan().cpu(), sees.all(-1) if not what else torch.zeros(T + 1, 2).bool())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,total", [(1, 300), (1, 5000), (8, 3000), (150, 200), (150, 4000)])
+@pytest.mark.parametrize("bad", [torch.inf, -torch.inf, torch.nan, 3e38])
+def test_attention_of_queries_beyond_range(lib, kind, T, total, bad):
+    """A query that is not finite, or whose products are not, spoils its own row and head: NaN there, and
+    the bits of all others as they are without it."""
+    pool = Pool(kind, 1, 64, [total, 40], seed=111).fill()
+    q = torch.randn(T + 1, 256, generator=torch.Generator().manual_seed(112)).to(BF).cuda()
+    cu, cache, got = _cu([T, 1]), pool.gpu(), []
+    for i in range(2):
+        if i:
+            q[T // 2, 128:] = bad
+        out, lse = torch.empty_like(q), torch.empty(T + 1, 2, device="cuda")
+        kda.kda_cache_attention(q, out, *cache, cu_seqlens_host=cu, cu_seqlens=cu.cuda(), lse=lse)
+        got.append((out.reshape(T + 1, 2, 128), lse))
+    others = torch.ones(T + 1, 2, dtype=torch.bool)
+    others[T // 2, 1] = False
+    for a, b in zip(*got):
+        assert torch.equal(a[others], b[others]) and a.isfinite().all()
+        assert b[T // 2, 1].isnan().all()
