@@ -6,8 +6,8 @@
 // Write: a page's scale needs the largest magnitude of all its new tokens before any can be
 // rounded, so the tokens of one (page, head, side) stay in the registers of one workgroup
 // (or one wave, where a page gets at most 16) between the two: read once, written once. 16384
-// tokens of 8 heads 20.6 us, 4.9 TB/s; 8 tokens of 512 sequences of 12 heads, int8, 10.8 us; 32
-// tokens of 8 heads 3.8 us.
+// tokens of 8 heads 20.7 us, 4.9 TB/s; 8 tokens of 512 sequences of 12 heads, int8, 11.0 us; 32
+// tokens of 8 heads 3.9 us.
 
 #include <stdint.h>
 
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kThreads) void write_mixed_kernel(WriteParams p) {
 
 // Rows (head, slot) of a unit; a workgroup takes kReadRows of them, a
 // row by 16 lanes of 8 codes, so that a wave's loads and stores are whole lines. Non-temporal
-// stores of few rows per workgroup: 16384 tokens of 8 heads 17.6 us, 5.7 TB/s (with 8 lanes to a row
+// stores of few rows per workgroup: 16384 tokens of 8 heads 17.5 us, 5.8 TB/s (with 8 lanes to a row
 // 29.6 us, ordinary stores of 256 rows 27.5, non-temporal ones 21.7, of 128 rows 19.1).
 constexpr int kReadRows = 64;
 constexpr int kReadPasses = kReadRows / 16;

@@ -11,9 +11,9 @@
 // and weights. The weights p enter the second product as high and low bf16 parts: the
 // matrix units idle otherwise, and the output keeps fp32's accuracy.
 //
-// 128 sequences of 500 to 8190 tokens, 64 query heads on 8: 141 us, 4.7 TB/s of the cache's bytes;
-// 512 of 71 to 1500, 12 heads in int8: 157 us, 4.9 TB/s; one of 131070: 59 us, 5 of them the join's.
-// 8 tokens of 64 sequences, 64 rows: 83 us, bound by vector instructions (45 % of a SIMD's cycles).
+// 128 sequences of 500 to 8190 tokens, 64 query heads on 8: 142 us, 4.6 TB/s of the cache's bytes;
+// 512 of 71 to 1500, 12 heads in int8: 158 us, 4.9 TB/s; one of 131070: 60 us, 5 of them the join's.
+// 8 tokens of 64 sequences, 64 rows: 79 us, bound by vector instructions (50 % of a SIMD's cycles).
 
 #include <math.h>
 
