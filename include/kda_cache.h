@@ -144,12 +144,13 @@ size_t kda_cache_attention_workspace_size(int32_t n_seqs, int64_t total_tokens, 
  * are off by 2^-16 of themselves at most where a sequence has at most 128 query rows per
  * key/value head (n_b * H_q / H_kv); with more rows, multiplied by the values' scale, they are
  * rounded to fp16: by 2^-11 of themselves, or 2^-31 of the largest such product that a row has
- * seen. A token that sees no key has out = 0 and lse = -infinity. The cache has to hold the call's own tokens (kda_cache_write).
+ * seen. A token that sees no key has out = 0 and lse = -infinity. The cache has to hold
+ * the call's own tokens (kda_cache_write).
  * Values may be of any size with code * scale below 2^128: no sum leaves fp32's range, and
- * out is infinite only where the definition's value rounds to infinity in bf16. Scores have to
- * stay inside fp32's range, as sums of |q| |code| and multiplied by scale * log2(e) and the
- * keys' scale. Beyond, and where a query is not finite, a row (a token's head) is NaN or what
- * infinite scores give; no other row is touched by it.
+ * out is infinite only where the definition's value rounds to infinity in bf16. Scores have
+ * to stay inside fp32's range, as sums of |q| |code| and multiplied by scale * log2(e) and
+ * the keys' scale. Beyond, and where a query is not finite, a row (a token's head) is NaN or
+ * what infinite scores give; no other row is touched by it.
  * The result does not depend on other sequences' contents, and is the same in every
  * call with the same lengths.
  * KDA_ERR_BAD_SEQLENS: cu_seqlens_host does not run from 0 upwards to at most

@@ -1545,3 +1545,39 @@ def test_attention_of_queries_beyond_range(lib, kind, T, total, bad):
     for a, b in zip(*got):
         assert torch.equal(a[others], b[others]) and a.isfinite().all()
         assert b[T // 2, 1].isnan().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+@pytest.mark.parametrize("H", [1, 300])
+def test_attention_document_scales(lib, kind, scale, H):
+    """No weight but equal ones, keys of least product first, and weights that all but vanish, cut
+    (one head) and whole."""
+    pool = Pool(kind, H, 32, [1300 if H == 1 else 333], seed=113).fill()
+    _check_sequences(pool, [135], 1, scale=scale, seed=114, size=3.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("counts,past", [([150, 300], [37, 900]), ([140], [5000])])
+def test_attention_documents_over_zeros(lib, kind, P, counts, past):
+    """Pages of zeros, which a write leaves under 2^-100 (some by negative zeros, some under a scale of
+    zero), that take most of the weight or none, beside ordinary pages and some beyond 2^40."""
+    g = torch.Generator().manual_seed(115)
+    for keys in (2.0 ** -9, 2.0 ** -4):
+        pool = Pool(kind, 2, P, [a + b for a, b in zip(counts, past)], seed=116).fill()
+        pool.scale[0][:] = 2.0 ** -8
+        zero = torch.rand(pool.N, 2, generator=g) < 0.3
+        c = pool.codes(pool.raw)[1]
+        c[zero] = 0
+        pool.scale[0][zero] = keys
+        pool.scale[1][zero] = torch.where(torch.rand(int(zero.sum()), generator=g) < 0.8,
+                                          2.0 ** -100, 0.0)
+        if kind == F8:
+            minus = zero & (torch.rand(pool.N, 2, generator=g) < 0.3)
+            c[minus] = 0x80
+        _check_sequences(pool, counts, 2, seed=117)
+        pool.scale[1][pool.table[0, 2]] = 2.0 ** 41
+        _check_sequences(pool, counts, 2, seed=118)
